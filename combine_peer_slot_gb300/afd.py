@@ -32,6 +32,8 @@ AFD_MAX_PEERS = 64
 AFD_MAX_RING = 64
 AFD_FORM_TOKENS, AFD_FORM_GROUPED = 0, 1
 AFD_MAX_FFN_RANKS = 16
+AFD_SCORE_SOFTMAX, AFD_SCORE_SIGMOID = 0, 1
+AFD_MX4_SCALE_FLOOR, AFD_MX4_SCALE_CEIL = 0, 1
 
 
 class afd_config(C.Structure):
@@ -117,6 +119,15 @@ SIGNATURES = [
     ("afd_attn_rows", _I, [_P, _I, C.POINTER(C.c_int)]),
     ("afd_attn_poll_status", _I, [_P]),
     ("afd_attn_launch_count", _I64, [_P]),
+    ("afd_route_select", _I, [_P, _I64, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    ("afd_mx4_quantize", _I, [_P, _I64, _I64, _I, _I, _P, _I, _I64, _I, _P, _P, _P]),
+    ("afd_mx4_dequantize", _I, [_P, _P, _I64, _I, _I, _P, _I64, _P]),
+    ("afd_mx4_weight_bytes", _I64, [_I, _I, _I, _I]),
+    ("afd_mx4_pack_weight", _I, [_P, _P, _I, _I, _I, _I, _P, _I64, _P]),
+    ("afd_mx4_gemm", _I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _P, _I64, _P]),
+    ("afd_mx4_ffn_workspace", _I64, [_I64, _I]),
+    ("afd_mx4_ffn", _I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _I64, _P]),
+    ("afd_mx4_poll_status", _I, [_P]),
 ]
 AFD_NUM_STAGES = 8
 STAGE_NAMES = ("header_check", "router", "plan", "gather", "gemm_swiglu", "gemm_down",
@@ -407,3 +418,54 @@ def afd_attn_poll_status(a):
 
 def afd_attn_launch_count(a):
     return int(lib().afd_attn_launch_count(a))
+
+
+# ---- routing choice and MXFP4 (no context; pointers as ints) -------------------
+def afd_route_select(logits, ld, n_tokens, logits_dtype, bias, num_experts, topk, score, n_groups,
+                     topk_groups, group_top, renorm, routed_scaling, ids, weights, stream=0):
+    return lib().afd_route_select(logits or None, ld, n_tokens, logits_dtype, bias or None,
+                                  num_experts, topk, score, n_groups, topk_groups, group_top,
+                                  int(bool(renorm)), routed_scaling, ids or None, weights or None,
+                                  stream or None)
+
+
+def afd_mx4_quantize(x, ldx, x_rows, cols, dtype, src_rows, topk, n_rows, scale_rule, codes, scales,
+                     stream=0):
+    return lib().afd_mx4_quantize(x or None, ldx, x_rows, cols, dtype, src_rows or None, topk,
+                                  n_rows, scale_rule, codes or None, scales or None, stream or None)
+
+
+def afd_mx4_dequantize(codes, scales, n_rows, cols, dtype, out, ldo, stream=0):
+    return lib().afd_mx4_dequantize(codes or None, scales or None, n_rows, cols, dtype, out or None,
+                                    ldo, stream or None)
+
+
+def afd_mx4_weight_bytes(num_experts, M, K, swiglu):
+    return int(lib().afd_mx4_weight_bytes(num_experts, M, K, int(bool(swiglu))))
+
+
+def afd_mx4_pack_weight(codes, scales, num_experts, M, K, swiglu, packed, packed_bytes, stream=0):
+    return lib().afd_mx4_pack_weight(codes or None, scales or None, num_experts, M, K,
+                                     int(bool(swiglu)), packed or None, packed_bytes, stream or None)
+
+
+def afd_mx4_gemm(codes, scales, n_rows, offsets, num_experts, weight, M, K, swiglu, out_dtype, out,
+                 ldo, stream=0):
+    return lib().afd_mx4_gemm(codes or None, scales or None, n_rows, offsets or None, num_experts,
+                              weight or None, M, K, int(bool(swiglu)), out_dtype, out or None, ldo,
+                              stream or None)
+
+
+def afd_mx4_ffn_workspace(n_rows, inter):
+    return int(lib().afd_mx4_ffn_workspace(n_rows, inter))
+
+
+def afd_mx4_ffn(codes, scales, n_rows, offsets, num_experts, w13, wd, hidden, inter, out_dtype, out,
+                ldo, workspace, workspace_bytes, stream=0):
+    return lib().afd_mx4_ffn(codes or None, scales or None, n_rows, offsets or None, num_experts,
+                             w13 or None, wd or None, hidden, inter, out_dtype, out or None, ldo,
+                             workspace or None, workspace_bytes, stream or None)
+
+
+def afd_mx4_poll_status(stream=0):
+    return lib().afd_mx4_poll_status(stream or None)

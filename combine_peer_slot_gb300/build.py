@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 SOURCES = ["afd_api.cu", "afd_kernels.cu", "afd_gemm_tc.cu", "afd_gemm_tc2.cu", "afd_noalloc.cu",
-           "afd_attn.cu"]
+           "afd_attn.cu", "afd_select.cu", "afd_mx4.cu", "afd_mx4_gemm.cu"]
 
 
 def _compile(src, verbose, debug=False):

@@ -13,6 +13,29 @@
 #include "../../include/afd.h"
 
 #include <atomic>
+#include <initializer_list>
+
+// The pointers of a call without a context (NULL ones are skipped): memory
+// that kernels on the current device can use.  AFD_ERR_NOT_DEVICE for host
+// memory, AFD_ERR_ARG for another device's.
+inline int check_device_ptrs(std::initializer_list<const void*> ptrs) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return AFD_ERR_CUDA;
+  }
+  for (const void* p : ptrs) {
+    if (!p) continue;
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+      cudaGetLastError();
+      return AFD_ERR_NOT_DEVICE;
+    }
+    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return AFD_ERR_NOT_DEVICE;
+    if (a.type == cudaMemoryTypeDevice && a.device != dev) return AFD_ERR_ARG;
+  }
+  return AFD_OK;
+}
 
 // Launch settings the launchers cache (a kernel's shared-memory attribute,
 // occupancy figures) are per device: a process may hold contexts on several.

@@ -1,0 +1,103 @@
+// afd_mx4.cuh -- what the MXFP4 translation units share: the format's
+// arithmetic, the packed weight's layout and the launchers.
+//
+// MXFP4 (OCP Microscaling Formats 1.0): 32 consecutive values share one
+// e8m0 scale 2^(s - 127) (byte s, 255 = NaN); each value is an e2m1 number,
+// one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign (bit 3 of its nibble).  A
+// row of K values is K / 2 bytes of codes (value 2 i in the low nibble of
+// byte i) and K / 32 scale bytes.
+#pragma once
+
+#include "afd_internal.cuh"
+
+constexpr int kMx4Block = 32;
+// Packed weights: [expert][128-row tile][128-column block] of
+//   8192 bytes of codes: row r's 64 bytes at r * 64, its 16-byte chunk c at
+//        chunk c ^ ((r >> 1) & 3) (the 64-byte swizzle tcgen05.mma reads)
+//    512 bytes of scales: row r's four at (r % 32) * 16 + (r / 32) * 4 (the
+//        image tcgen05.cp.32x128b spreads over the TMEM lanes)
+// contiguous, so one bulk copy moves any run of column blocks with its
+// scales; rows and columns past the weight's edge are zero.  128 columns a
+// block and not 256: inter sizes such as 1408 are whole blocks, where 256
+// would read 9 % more than the weight holds.
+constexpr int kMx4BlkCols = 128;
+constexpr int kMx4BlkCodes = 128 * kMx4BlkCols / 2;
+constexpr int kMx4BlkBytes = kMx4BlkCodes + 512;
+
+// tiles and bytes of a packed weight [E][M][K]; with swiglu, tile t holds
+// the gate and up rows of features [64 t, 64 t + 64): each 32 rows are 16
+// gate rows, then the 16 matching up rows
+__host__ __device__ inline int mx4_tiles(int64_t M, int swiglu) {
+  return (int)(swiglu ? (M / 2 + 63) / 64 : (M + 127) / 128);
+}
+__host__ __device__ inline int mx4_kblocks(int K) { return (K + kMx4BlkCols - 1) / kMx4BlkCols; }
+inline int64_t mx4_weight_bytes(int64_t E, int64_t M, int K, int swiglu) {
+  return E * mx4_tiles(M, swiglu) * mx4_kblocks(K) * kMx4BlkBytes;
+}
+
+// Arguments of one grouped product.  Group g < n_groups is rows
+// [offsets[g], offsets[g + 1]) of the rows of kind 0 times weight g; with
+// shared rows, one more group: all of kind 1's rows times its weight.
+struct Mx4GemmArgs {
+  CUtensorMap tmX[2];        // codes of the rows [x_rows][K / 2], box 128 bytes x token tile
+  const uint8_t* xs[2];      // their scales [x_rows][K / 32]
+  int64_t x_rows[2];
+  const uint8_t* w[2];       // packed weights
+  void* out[2];
+  uint8_t* out_lo[2];        // OUT_Y24
+  int64_t ldo[2];            // output row pitch in elements
+  int fmt[2];                // OUT_*
+  int M[2], K[2];
+  const int32_t* offsets;    // [n_groups + 1], device
+  int n_groups;
+  int has_shared;
+  int swiglu;
+  int32_t* status;           // NULL: the file-scope status word
+};
+// bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
+// output tiles, which sizes the grid
+int mx4_token_tile(int64_t rows, int groups);
+cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units);
+int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn);
+
+cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx, int64_t x_rows, int f32,
+                                const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,
+                                uint8_t* codes, uint8_t* scales);
+cudaError_t launch_mx4_pack(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int E, int64_t M,
+                            int K, int swiglu, uint8_t* packed);
+
+#ifdef __CUDACC__
+// e8m0 byte -> fp32 2^(s - 127); 0 is fp32's subnormal 2^-127, 255 NaN
+__device__ __forceinline__ float mx4_scale(uint32_t s) {
+  return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
+}
+// The scale byte of a block whose largest magnitude has these fp32 bits.
+// floor rule (the OCP format's): 2^(floor(log2 amax) - 2), under which a
+// block's largest values up to 8 scales saturate to 6; ceil rule: the
+// smallest power of two whose 6 reaches amax (mantissa over 1.5 takes the
+// next one), up to 2^125: the 4 and 6 of a larger scale are no finite fp32.
+// 255 for a block with a NaN or an infinity.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax_bits, int ceil_rule) {
+  if (amax_bits >= 0x7f800000u) return 255u;
+  const int e = (int)(amax_bits >> 23) - 2 + (ceil_rule && (amax_bits & 0x7fffffu) > 0x400000u);
+  return (uint32_t)min(max(e, 0), 252);
+}
+// eight values, already divided by the scale, to eight nibbles: round to
+// nearest, ties to an even code, saturating at 6
+__device__ __forceinline__ uint32_t mx4_encode8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{ .reg .b8 b0, b1, b2, b3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      "mov.b32 %0, {b0, b1, b2, b3}; }"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+// 1 / scale as fp32: exact, scale bytes 0 .. 253 (255: 0, every code 0)
+__device__ __forceinline__ float mx4_inv_scale(uint32_t s) {
+  return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
+}
+#endif

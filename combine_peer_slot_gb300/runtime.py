@@ -308,3 +308,160 @@ class RankSet:
         for c in self.ranks:
             A.afd_destroy(c)
         self.ranks = []
+
+
+# ---- routing choice and MXFP4 on torch tensors ----------------------------------
+def _act_code(dtype):
+    import torch
+    if dtype is torch.bfloat16:
+        return A.AFD_DTYPE_BF16
+    if dtype is torch.float32:
+        return A.AFD_DTYPE_F32
+    raise A.AfdError(A.AFD_ERR_ARG, f"dtype {dtype}: bfloat16 or float32 wanted")
+
+
+def _stream(t):
+    """The current stream of t's device; t must live on the current device
+    (the library launches there)."""
+    import torch
+    if t.device.type != "cuda":
+        raise A.AfdError(A.AFD_ERR_NOT_DEVICE, "a CUDA tensor is wanted")
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _want(ok, what):
+    if not ok:
+        raise A.AfdError(A.AFD_ERR_ARG, what)
+
+
+def _int32_vector(t, what):
+    import torch
+    _want(t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous(), f"{what}: int32 vector wanted")
+    return t
+
+
+def route_select(logits, topk, bias=None, score="softmax", n_groups=1, topk_groups=1, group_top=1,
+                 renorm=False, routed_scaling=1.0):
+    """afd_route_select of logits [T, E] (bf16 or fp32, any row pitch):
+    (ids int32 [T, topk], weights fp32 [T, topk])."""
+    import torch
+    _want(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), "logits: rows [T, E] wanted")
+    T, E = logits.shape
+    if bias is not None:
+        _want(bias.dtype is torch.float32 and bias.shape == (E,) and bias.is_contiguous(),
+              "bias: fp32 [E] wanted")
+    _want(score in ("softmax", "sigmoid"), f"score {score!r}")
+    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    A._check(A.afd_route_select(logits.data_ptr(), logits.stride(0) if T > 1 else E, T, _act_code(logits.dtype),
+                                0 if bias is None else bias.data_ptr(), E, topk,
+                                A.AFD_SCORE_SIGMOID if score == "sigmoid" else A.AFD_SCORE_SOFTMAX,
+                                n_groups, topk_groups, group_top, renorm, routed_scaling,
+                                ids.data_ptr(), weights.data_ptr(), _stream(logits)),
+             "afd_route_select")
+    return ids, weights
+
+
+class Mx4:
+    """MXFP4 rows: codes uint8 [rows, cols / 2], scales uint8 [rows, cols / 32]."""
+
+    def __init__(self, codes, scales):
+        import torch
+        _want(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.dim() == 2
+              and codes.is_contiguous() and scales.is_contiguous()
+              and codes.shape[1] % 16 == 0 and scales.shape == (codes.shape[0], codes.shape[1] // 16),
+              "MXFP4: contiguous uint8 codes [rows, cols / 2] and scales [rows, cols / 32] wanted")
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols = codes.shape[0], 2 * codes.shape[1]
+
+
+def mx4_quantize(x, src_rows=None, topk=1, rule="floor"):
+    """afd_mx4_quantize of x [rows, cols] (bf16 or fp32, any 16-byte row
+    pitch); src_rows int32 [n]: row r codes x[src_rows[r] // topk]."""
+    import torch
+    _want(x.dim() == 2 and x.shape[1] % 32 == 0 and x.stride(1) == 1, "x: rows [n, 32 m] wanted")
+    _want(rule in ("floor", "ceil"), f"rule {rule!r}")
+    n = x.shape[0] if src_rows is None else _int32_vector(src_rows, "src_rows").numel()
+    q = Mx4(torch.empty((n, x.shape[1] // 2), dtype=torch.uint8, device=x.device),
+            torch.empty((n, x.shape[1] // 32), dtype=torch.uint8, device=x.device))
+    A._check(A.afd_mx4_quantize(x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1], x.shape[0],
+                                x.shape[1], _act_code(x.dtype),
+                                0 if src_rows is None else src_rows.data_ptr(), topk, n,
+                                A.AFD_MX4_SCALE_CEIL if rule == "ceil" else A.AFD_MX4_SCALE_FLOOR,
+                                q.codes.data_ptr(), q.scales.data_ptr(), _stream(x)),
+             "afd_mx4_quantize")
+    return q
+
+
+def mx4_dequantize(q, dtype):
+    """The values of q as a tensor [rows, cols] of dtype (bf16 or fp32)."""
+    import torch
+    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    A._check(A.afd_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+                                  _act_code(dtype), out.data_ptr(), q.cols, _stream(q.codes)),
+             "afd_mx4_dequantize")
+    return out
+
+
+class Mx4Weight:
+    """Expert weights [E, M, K] in MXFP4 (codes uint8 [E, M, K / 2], scales
+    uint8 [E, M, K / 32]) packed for the product; the inputs are not kept."""
+
+    def __init__(self, codes, scales, swiglu=False):
+        import torch
+        _want(codes.dim() == 3 and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+              and codes.is_contiguous() and scales.is_contiguous()
+              and scales.shape == (*codes.shape[:2], codes.shape[2] // 16),
+              "weight: contiguous uint8 codes [E, M, K / 2] and scales [E, M, K / 32] wanted")
+        self.experts, self.M, self.K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        self.swiglu = bool(swiglu)
+        nbytes = A.afd_mx4_weight_bytes(self.experts, self.M, self.K, self.swiglu)
+        _want(nbytes > 0, f"weight dimensions {(self.experts, self.M, self.K)}")
+        self.packed = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        A._check(A.afd_mx4_pack_weight(codes.data_ptr(), scales.data_ptr(), self.experts, self.M, self.K,
+                                       self.swiglu, self.packed.data_ptr(), nbytes, _stream(codes)),
+                 "afd_mx4_pack_weight")
+
+
+def mx4_gemm(x, offsets, weight, out_dtype=None, out=None):
+    """afd_mx4_gemm of the rows x (Mx4) grouped by offsets int32 [E + 1] with
+    weight (Mx4Weight): [rows, M], or [rows, M / 2] = silu(gate) * up for a
+    swiglu weight.  Rows in no group are not written (out: the caller's)."""
+    import torch
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    _want(_int32_vector(offsets, "offsets").numel() == weight.experts + 1, "offsets: int32 [E + 1] wanted")
+    _want(x.cols == weight.K, f"rows of {x.cols} columns, weight of {weight.K}")
+    cols = weight.M // 2 if weight.swiglu else weight.M
+    if out is None:
+        out = torch.empty((x.rows, cols), dtype=out_dtype, device=x.codes.device)
+    _want(out.shape == (x.rows, cols) and out.stride(1) == 1 and out.dtype is out_dtype, "out")
+    A._check(A.afd_mx4_gemm(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(),
+                            weight.experts, weight.packed.data_ptr(), weight.M, weight.K, weight.swiglu,
+                            _act_code(out_dtype), out.data_ptr(), out.stride(0) if x.rows > 1 else cols,
+                            _stream(x.codes)),
+             "afd_mx4_gemm")
+    return out
+
+
+def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
+    """afd_mx4_ffn: the expert FFN of the grouped rows x (Mx4) with w13 (a
+    swiglu Mx4Weight [E, 2 inter, hidden]) and wd ([E, hidden, inter])."""
+    import torch
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    hidden, inter = wd.M, wd.K
+    _want(w13.swiglu and not wd.swiglu and w13.experts == wd.experts and w13.K == hidden
+          and w13.M == 2 * inter and x.cols == hidden, "w13 / wd / x dimensions do not match")
+    _want(_int32_vector(offsets, "offsets").numel() == wd.experts + 1, "offsets: int32 [E + 1] wanted")
+    if out is None:
+        out = torch.empty((x.rows, hidden), dtype=out_dtype, device=x.codes.device)
+    _want(out.shape == (x.rows, hidden) and out.stride(1) == 1 and out.dtype is out_dtype, "out")
+    if workspace is None:
+        workspace = torch.empty(max(A.afd_mx4_ffn_workspace(x.rows, inter), 1), dtype=torch.uint8,
+                                device=x.codes.device)
+    A._check(A.afd_mx4_ffn(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), wd.experts,
+                           w13.packed.data_ptr(), wd.packed.data_ptr(), hidden, inter,
+                           _act_code(out_dtype), out.data_ptr(), out.stride(0) if x.rows > 1 else hidden,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           _stream(x.codes)),
+             "afd_mx4_ffn")
+    return out

@@ -625,6 +625,119 @@ int afd_route_noalloc(const void* x, int n_tokens, int hidden, int act_dtype, co
                       const float* bias, int num_experts, int topk, int renorm,
                       float routed_scaling, int32_t* ids, float* weights, void* cuda_stream);
 
+/* ---- routing choice on given logits ----------------------------------------
+ * The choice step of a gate whose logits the caller has: softmax or sigmoid
+ * scores, a balance bias that takes part in the choice only, expert groups
+ * and masked experts.  afd_route_noalloc is the plain softmax form with the
+ * logits computed from the activations.
+ *   logits   device, [n_tokens, num_experts] of logits_dtype, row pitch ld
+ *            elements (>= num_experts); -inf: the expert is masked for the row
+ *   bias     device fp32 [num_experts] or NULL (-inf masks the expert)
+ *   s = softmax(logits) over the row or 1 / (1 + exp(-logits))
+ *   c = s + bias, or without a bias the logits themselves (s rises with them)
+ *   n_groups > 1: the experts are n_groups (<= 32) blocks of consecutive
+ *            experts; a block ranks by the sum of its group_top (1 or 2)
+ *            largest c (without a bias and group_top 2: largest s), and only
+ *            the experts of the topk_groups first blocks may be chosen
+ *   ids      device int32 [n_tokens, topk]: the topk largest c among the
+ *            experts that may be chosen, in descending order
+ *   weights  device fp32 [n_tokens, topk]: their s, divided by their sum when
+ *            renorm, times routed_scaling
+ * Equal values go to the lower index (blocks and experts).  The choice is
+ * that of the exact scores: values that fp32 cannot tell apart are compared
+ * in fp64.  Where fewer than topk experts may be chosen, the entries left
+ * get id -1 and weight 0.  A row with a NaN (or, under softmax, +inf) in
+ * its logits, or a NaN in the bias, gets id -1 and weight NaN throughout.
+ * num_experts <= 256, topk <= 16, topk <= topk_groups * (num_experts /
+ * n_groups), num_experts % n_groups == 0.  Asynchronous on cuda_stream,
+ * allocates nothing, keeps nothing; may be captured.  Errors: AFD_ERR_ARG
+ * (also a pointer of another device), AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA. */
+#define AFD_SCORE_SOFTMAX 0
+#define AFD_SCORE_SIGMOID 1
+int afd_route_select(const void* logits, int64_t ld, int n_tokens, int logits_dtype,
+                     const float* bias, int num_experts, int topk, int score, int n_groups,
+                     int topk_groups, int group_top, int renorm, float routed_scaling,
+                     int32_t* ids, float* weights, void* cuda_stream);
+
+/* ---- MXFP4: coding, grouped product, expert FFN -----------------------------
+ * OCP Microscaling Formats 1.0, MXFP4: 32 consecutive values of a row share
+ * one e8m0 scale 2^(s - 127) (byte s; 255 = NaN), each value is an e2m1
+ * number (0, 0.5, 1, 1.5, 2, 3, 4, 6, with a sign in bit 3 of its nibble).
+ * A matrix [rows, cols] (cols % 32 == 0) is codes uint8 [rows, cols / 2]
+ * (value 2 i in the low nibble of byte i) and scales uint8 [rows, cols / 32],
+ * both without row padding.  All calls are asynchronous on cuda_stream,
+ * allocate nothing, keep nothing between calls, and may be captured.
+ * Errors of all: AFD_ERR_ARG (ranges, alignment, a pointer of another
+ * device), AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA; n_rows == 0 does nothing.
+ *
+ * afd_mx4_quantize -- row r of the result codes row src_rows[r] / topk of x
+ * (src_rows device int32 [n_rows]: positions t * topk + j as AFD_WS_PERM
+ * holds them; an entry whose row is outside [0, x_rows) gives a row of
+ * zeros), or row r of x when src_rows is NULL (then n_rows == x_rows and
+ * topk == 1).  x: device, dtype [x_rows, cols], row pitch ldx elements, rows
+ * and codes 16-byte aligned.  The scale of a block with largest magnitude m:
+ *   AFD_MX4_SCALE_FLOOR  2^(floor(log2 m) - 2), the OCP rule; magnitudes
+ *                        over 6 scales become 6
+ *   AFD_MX4_SCALE_CEIL   the smallest power of two with 6 scales >= m
+ * but at least 2^-127 and at most 2^125 (the 6 of a larger one is no finite
+ * fp32); a value becomes the nearest e2m1 multiple of the
+ * scale, ties to the even code.  A block with a NaN or an infinity gets
+ * scale byte 255 and codes 0: all of it reads as NaN. */
+#define AFD_MX4_SCALE_FLOOR 0
+#define AFD_MX4_SCALE_CEIL 1
+int afd_mx4_quantize(const void* x, int64_t ldx, int64_t x_rows, int cols, int dtype,
+                     const int32_t* src_rows, int topk, int64_t n_rows, int scale_rule,
+                     uint8_t* codes, uint8_t* scales, void* cuda_stream);
+
+/* The values of codes and scales into out (dtype [n_rows, cols], row pitch
+ * ldo elements, rows and codes 16-byte aligned): exact in either type
+ * (infinity where a foreign scale over 2^125 takes a value past its range). */
+int afd_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, int cols,
+                       int dtype, void* out, int64_t ldo, void* cuda_stream);
+
+/* Weights of the product, laid out once per layer: codes and scales of
+ * [num_experts, M, K] (as above) into the blocks the tensor cores read.
+ * swiglu: rows 0..M/2-1 of an expert are its gate, M/2..M-1 its up
+ * projection (afd_set_layer's W13), interleaved for the SwiGLU epilogue;
+ * M % 16 == 0 then, else M % 8 == 0.  num_experts <= 256, M and K <= 65536.
+ * packed: device, 128-byte aligned, packed_bytes >= afd_mx4_weight_bytes
+ * (host only; 0 for dimensions outside these limits), else AFD_ERR_CAPACITY. */
+int64_t afd_mx4_weight_bytes(int num_experts, int M, int K, int swiglu);
+int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_experts, int M, int K,
+                        int swiglu, void* packed, int64_t packed_bytes, void* cuda_stream);
+
+/* Grouped product: out[r] = W[g] x[r] for the rows r in [offsets[g],
+ * offsets[g + 1]), fp32 accumulation, one rounding to out_dtype.
+ *   codes, scales  the rows x, MXFP4 [n_rows, K]; codes 16-byte, scales
+ *                  4-byte aligned
+ *   offsets        device int32 [num_experts + 1], ascending (AFD_WS_OFFSETS);
+ *                  clamped to [0, n_rows]; rows in no group are left as they were
+ *   weight         afd_mx4_pack_weight of [num_experts, M, K] with this swiglu
+ *   out            device [n_rows, M], row pitch ldo (ldo % 8 == 0), 16-byte
+ *                  aligned; swiglu: bf16 [n_rows, M / 2], silu(gate) * up
+ * swiglu with AFD_DTYPE_F32: AFD_ERR_UNSUPPORTED. */
+int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
+                 const int32_t* offsets, int num_experts, const void* weight, int M, int K,
+                 int swiglu, int out_dtype, void* out, int64_t ldo, void* cuda_stream);
+
+/* The expert FFN: the SwiGLU product with w13 (packed [num_experts, 2 inter,
+ * hidden], swiglu), its bf16 rows coded again (AFD_MX4_SCALE_FLOOR), the
+ * product with wd (packed [num_experts, hidden, inter]).  inter % 32 == 0.
+ * The same bits as afd_mx4_gemm, afd_mx4_quantize and afd_mx4_gemm in turn.
+ * workspace: device, 256-byte aligned, at least afd_mx4_ffn_workspace bytes
+ * (host only; -1 for dimensions outside the limits), else AFD_ERR_CAPACITY;
+ * one call at a time may use it. */
+int64_t afd_mx4_ffn_workspace(int64_t n_rows, int inter);
+int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
+                const int32_t* offsets, int num_experts, const void* w13, const void* wd,
+                int hidden, int inter, int out_dtype, void* out, int64_t ldo, void* workspace,
+                int64_t workspace_bytes, void* cuda_stream);
+
+/* Synchronise the stream; return and clear the first device error of the
+ * products above on the current device (AFD_ERR_TIMEOUT: a bounded wait gave
+ * up and the outputs are incomplete), AFD_OK if none. */
+int afd_mx4_poll_status(void* cuda_stream);
+
 /* Static string for a status code. */
 const char* afd_strerror(int code);
 
