@@ -274,7 +274,7 @@ int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_exp
 // One product over the grouped rows.
 static int product(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
                    const int32_t* offsets, int E, const void* w, int M, int K, int swiglu, int fmt, void* out,
-                   int64_t ldo) {
+                   int64_t ldo, uint8_t* out_scales = nullptr) {
   Mx4GemmArgs a;
   memset(&a, 0, sizeof a);
   const int bn = mx4_token_tile(n_rows, E);
@@ -284,6 +284,7 @@ static int product(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* sca
   a.x_rows[0] = n_rows;
   a.w[0] = static_cast<const uint8_t*>(w);
   a.out[0] = out;
+  a.out_lo[0] = out_scales;
   a.ldo[0] = ldo;
   a.fmt[0] = fmt;
   a.M[0] = M;
@@ -316,11 +317,11 @@ int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, co
                  out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo);
 }
 
-// workspace: h as bf16 rows, then its codes and scales
+// workspace: the codes and scales of h
 int64_t afd_mx4_ffn_workspace(int64_t n_rows, int inter) {
   if (n_rows < 0 || n_rows > kMaxRows || inter < kMx4Block || inter > kMaxDim || inter % kMx4Block) return -1;
   const int64_t n = n_rows * inter;
-  return (n * 2 + 255) / 256 * 256 + (n / 2 + 255) / 256 * 256 + (n / 32 + 255) / 256 * 256;
+  return (n / 2 + 255) / 256 * 256 + (n / 32 + 255) / 256 * 256;
 }
 
 int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* offsets,
@@ -342,12 +343,10 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, con
   if (!rc) rc = make_lc(cuda_stream, &lc);
   if (rc) return rc;
   const int64_t n = n_rows * inter;
-  uint8_t* h = static_cast<uint8_t*>(workspace);
-  uint8_t* hc = h + (n * 2 + 255) / 256 * 256;
+  uint8_t* hc = static_cast<uint8_t*>(workspace);
   uint8_t* hs = hc + (n / 2 + 255) / 256 * 256;
-  rc = product(lc, codes, scales, n_rows, offsets, num_experts, w13, 2 * inter, hidden, 1, OUT_ACT, h, inter);
-  if (!rc)
-    rc = launched(launch_mx4_quantize(lc, h, inter, n_rows, 0, nullptr, 1, n_rows, inter, 0, hc, hs), "mx4 ffn");
+  rc = product(lc, codes, scales, n_rows, offsets, num_experts, w13, 2 * inter, hidden, 1, OUT_MX4, hc, inter, hs);
+  lc.pdl = 1;  // the second launch's set-up runs while the first drains
   if (!rc)
     rc = product(lc, hc, hs, n_rows, offsets, num_experts, wd, hidden, inter, 0,
                  out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo);

@@ -38,13 +38,14 @@ inline int64_t mx4_weight_bytes(int64_t E, int64_t M, int K, int swiglu) {
 // Arguments of one grouped product.  Group g < n_groups is rows
 // [offsets[g], offsets[g + 1]) of the rows of kind 0 times weight g; with
 // shared rows, one more group: all of kind 1's rows times its weight.
+#define OUT_MX4 3  // SwiGLU only: codes in out, scales in out_lo (ldo % 32 == 0)
 struct Mx4GemmArgs {
   CUtensorMap tmX[2];        // codes of the rows [x_rows][K / 2], box 128 bytes x token tile
   const uint8_t* xs[2];      // their scales [x_rows][K / 32]
   int64_t x_rows[2];
   const uint8_t* w[2];       // packed weights
   void* out[2];
-  uint8_t* out_lo[2];        // OUT_Y24
+  uint8_t* out_lo[2];        // OUT_Y24: the low plane; OUT_MX4: the scales
   int64_t ldo[2];            // output row pitch in elements
   int fmt[2];                // OUT_*
   int M[2], K[2];

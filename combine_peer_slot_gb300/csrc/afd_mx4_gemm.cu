@@ -30,9 +30,11 @@ constexpr int BK = 256;               // columns per stage
 constexpr int A_BYTES = 2 * kMx4BlkBytes;
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 128 + EPI_WARPS * 32;
-constexpr int EPI_PITCH_SWIGLU = 48;
-constexpr int EPI_PITCH_BF16 = 80;
-constexpr int EPI_BUF_BYTES = 32 * EPI_PITCH_BF16;
+// epilogue staging, one buffer per four warps: 32 tokens x 128 output rows
+// (SwiGLU: 64) of bf16, the rows 16 bytes apart in the banks
+constexpr int EPI_PITCH = 272;
+constexpr int EPI_PITCH_SWIGLU = 144;
+constexpr int EPI_BUF_BYTES = 32 * EPI_PITCH;
 constexpr int MAX_GROUPS = 257;       // 256 experts and the shared rows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -64,7 +66,7 @@ struct Ring {
     int wsum[NUM_THREADS / 32];
   };
   static constexpr size_t kEpiOffset = ((size_t)STAGES * STAGE_BYTES + sizeof(Tail) + 127) / 128 * 128;
-  static constexpr size_t kSmemBytes = 1024 + kEpiOffset + (size_t)EPI_WARPS * EPI_BUF_BYTES;
+  static constexpr size_t kSmemBytes = 1024 + kEpiOffset + (size_t)(EPI_WARPS / 4) * EPI_BUF_BYTES;
   static_assert(kSmemBytes <= 232448, "over the per-CTA shared memory limit");
 };
 
@@ -117,6 +119,43 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// TMEM lanes [l, l + 16) x 32 columns in the fragment layout: register 4 i
+// + 2 h + j holds row lane / 4 + 8 h, column 8 i + 2 (lane % 4) + j
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// four 8 x 8 matrices of 16-bit values, transposed: lane 8 m + j gives the
+// address of column j (16 bytes) of matrix m
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// the four warps of one staging buffer
+__device__ __forceinline__ void group_sync(int half) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+}
+
+// the same, and whether all of them pass ok: they leave together, so none
+// waits at a later barrier for one that gave up
+__device__ __forceinline__ bool group_all(int half, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %2, 0; bar.red.and.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(1 + half), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 
 struct Unit {
   int group, kind, mt, rows, n_mma;
@@ -361,98 +400,145 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     }
   } else {
     // ------------------------------ epilogue (warps 4..11)
+    // Two groups of four warps take 32 token columns at a time in turn; a
+    // warp reads its 32 TMEM lanes in the fragment layout, so that stmatrix
+    // writes tokens as rows (a 32 x 32 piece in 4 instructions, where 2-byte
+    // stores from the lane-per-row layout took 32) and, with SwiGLU, a
+    // thread holds the gate and the up value of one output: the group's
+    // rows then leave shared memory as whole 256-byte (SwiGLU: 128) runs.
     const int q = warp & 3;
     const int half = (warp - 4) >> 2;
-    uint8_t* ebuf = smem + R::kEpiOffset + (size_t)(warp - 4) * EPI_BUF_BYTES;
-    const bool lo = lane < 16;
+    const int gt = threadIdx.x & 127;  // thread of the group
+    uint8_t* ebuf = smem + R::kEpiOffset + (size_t)half * EPI_BUF_BYTES;
+    const uint32_t ebuf_s = smem_u32(ebuf);
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
       const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
       bool ok = wait_bar(smem_u32(&tail->tfull[acc]), acc_ph, abort_flag, deadline, status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!group_all(half, ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       const int kind = t.kind;
       const int64_t ldo = a.ldo[kind];
-      if (a.swiglu) {
-        const int col0 = t.mt * 64 + q * 16, I = a.M[kind] / 2;
-        for (int c0 = half * 32; c0 < t.rows; c0 += 64) {
+      const int fmt = a.fmt[kind];
+      bool released = false;
+      auto release = [&]() {  // this warp has read the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail->tempty[acc]));
+        released = true;
+      };
+      for (int c0 = half * 32; c0 < t.rows; c0 += 64) {
+        const bool last = c0 + 64 >= t.rows;
+        const int nrows = min(32, t.rows - c0);
+        if (!a.swiglu && fmt != OUT_ACT) {  // lane = output row: 32 neighbours per token already
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + (uint32_t)c0, v);
           tmem_ld_wait();
-          uint16_t* sb = reinterpret_cast<uint16_t*>(ebuf);
-#pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const float x = __uint_as_float(v[j]), y = __uint_as_float(v[16 + j]);
-            const float recv = __shfl_xor_sync(0xffffffffu, lo ? y : x, 16);
-            const float g = lo ? x : recv;
-            const float u = lo ? recv : y;
-            const __nv_bfloat16 hv = __float2bfloat16_rn(silu_f(g) * u);
-            const int tok = lo ? j : 16 + j;
-            sb[(tok * EPI_PITCH_SWIGLU + (lo ? 0 : 32)) / 2 + (lane & 15)] = *reinterpret_cast<const uint16_t*>(&hv);
-          }
-          __syncwarp();
-          const int r = c0 + lane;
-          if (r < t.rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(ebuf + lane * EPI_PITCH_SWIGLU + (lo ? 0 : 32));
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + r) * ldo + col0);
-            if (col0 + 8 <= I) dst[0] = src[0];
-            if (col0 + 16 <= I) dst[1] = src[1];
-          }
-          __syncwarp();
-        }
-      } else {
-        const int col0 = t.mt * 128 + q * 32, M = a.M[kind];
-        const int fmt = a.fmt[kind];
-        for (int c0 = half * 32; c0 < t.rows; c0 += 64) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(taddr + (uint32_t)c0, v);
-          tmem_ld_wait();
-          if (fmt == OUT_F32) {
-            if (col0 + lane < M) {
-              float* dst = reinterpret_cast<float*>(a.out[kind]) + (t.row + c0) * ldo + col0 + lane;
+          if (last) release();
+          const int col = t.mt * 128 + q * 32 + lane;
+          if (col < a.M[kind]) {
+            const int64_t at = (t.row + c0) * ldo + col;
+            if (fmt == OUT_F32) {
+              float* dst = reinterpret_cast<float*>(a.out[kind]) + at;
 #pragma unroll
               for (int c = 0; c < 32; c++)
-                if (c0 + c < t.rows) dst[(int64_t)c * ldo] = __uint_as_float(v[c]);
-            }
-          } else if (fmt == OUT_Y24) {
-            if (col0 + lane < M) {
-              uint16_t* dh = reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0) * ldo + col0 + lane;
-              uint8_t* dl = a.out_lo[kind] + (t.row + c0) * ldo + col0 + lane;
+                if (c < nrows) dst[(int64_t)c * ldo] = __uint_as_float(v[c]);
+            } else {
+              uint16_t* dh = reinterpret_cast<uint16_t*>(a.out[kind]) + at;
+              uint8_t* dl = a.out_lo[kind] + at;
 #pragma unroll
               for (int c = 0; c < 32; c++)
-                if (c0 + c < t.rows) {
+                if (c < nrows) {
                   const uint32_t b24 = y24_encode(__uint_as_float(v[c]));
                   dh[(int64_t)c * ldo] = (uint16_t)(b24 >> 8);
                   dl[(int64_t)c * ldo] = (uint8_t)(b24 & 0xffu);
                 }
             }
-          } else {
+          }
+          continue;
+        }
+        uint32_t x[16], y[16];  // output rows 0..15 and 16..31 (SwiGLU: gate, up)
+        tmem_ld_16x256b_x4(taddr + (uint32_t)c0, x);
+        tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)c0, y);
+        tmem_ld_wait();
+        if (last) release();
+        if (a.swiglu) {
+          uint32_t h[8];
 #pragma unroll
-            for (int c = 0; c < 32; c++) {
-              const __nv_bfloat16 yv = __float2bfloat16_rn(__uint_as_float(v[c]));
-              *reinterpret_cast<uint16_t*>(ebuf + c * EPI_PITCH_BF16 + lane * 2) =
-                  *reinterpret_cast<const uint16_t*>(&yv);
+          for (int i = 0; i < 8; i++) {
+            const float g0 = __uint_as_float(x[2 * i]), g1 = __uint_as_float(x[2 * i + 1]);
+            h[i] = pack_bf16(silu_f(g0) * __uint_as_float(y[2 * i]), silu_f(g1) * __uint_as_float(y[2 * i + 1]));
+          }
+          group_sync(half);  // the buffer's last rows have been read
+          const uint32_t at =
+              ebuf_s + (8 * (lane >> 4) + (lane & 7)) * EPI_PITCH_SWIGLU + (q * 16 + ((lane >> 3) & 1) * 8) * 2;
+          stmatrix_x4_trans(at, h[0], h[1], h[2], h[3]);
+          stmatrix_x4_trans(at + 16 * EPI_PITCH_SWIGLU, h[4], h[5], h[6], h[7]);
+          group_sync(half);
+          const int I = a.M[kind] / 2;
+          if (fmt == OUT_MX4) {
+            // a thread codes 16 of a token's 64 features, two threads a block
+            const int r = gt >> 2, f = t.mt * 64 + (gt & 3) * 16;
+            const uint4* src = reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH_SWIGLU + (gt & 3) * 32);
+            const uint4 lo = src[0], hi = src[1];
+            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            const uint32_t sc = mx4_scale_byte(m, 0);
+            const float inv = mx4_inv_scale(sc);
+            uint32_t code[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              float v[8];
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                v[2 * j] = __uint_as_float(w[4 * i + j] << 16) * inv;
+                v[2 * j + 1] = __uint_as_float(w[4 * i + j] & 0xffff0000u) * inv;
+              }
+              code[i] = sc == 255u ? 0u : mx4_encode8(v);
             }
-            __syncwarp();
-            const int r = c0 + lane;
-            if (r < t.rows) {
-              const uint4* src = reinterpret_cast<const uint4*>(ebuf + lane * EPI_PITCH_BF16);
-              uint4* dst =
-                  reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + r) * ldo + col0);
+            if (r < nrows && f < I) {
+              const int64_t at = (t.row + c0 + r) * ldo + f;
+              *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out[kind]) + at / 2) =
+                  make_uint2(code[0], code[1]);
+              if ((gt & 1) == 0) a.out_lo[kind][at / 32] = (uint8_t)sc;
+            }
+          } else {
+            const int r0 = gt >> 3, f = t.mt * 64 + (gt & 7) * 8;
 #pragma unroll
-              for (int x = 0; x < 4; x++)
-                if (col0 + 8 * x + 8 <= M) dst[x] = src[x];
+            for (int p = 0; p < 2; p++) {
+              const int r = r0 + 16 * p;
+              if (r < nrows && f + 8 <= I)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + f) =
+                    *reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH_SWIGLU + (gt & 7) * 16);
             }
           }
-          __syncwarp();
+        } else {
+          group_sync(half);
+          const uint32_t at = ebuf_s + (lane & 7) * EPI_PITCH + (q * 32 + (lane >> 3) * 8) * 2;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            stmatrix_x4_trans(at + 8 * i * EPI_PITCH,
+                              pack_bf16(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
+                              pack_bf16(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])),
+                              pack_bf16(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])),
+                              pack_bf16(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])));
+          group_sync(half);
+          const int r0 = gt >> 4, col = t.mt * 128 + (gt & 15) * 8;
+#pragma unroll
+          for (int p = 0; p < 4; p++) {
+            const int r = r0 + 8 * p;
+            if (r < nrows && col + 8 <= a.M[kind])
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + col) =
+                  *reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH + (gt & 15) * 16);
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->tempty[acc]));
+      if (!released) release();  // no columns of this unit were this group's
       if (++acc == 2) { acc = 0; acc_ph ^= 1; }
     }
   }
