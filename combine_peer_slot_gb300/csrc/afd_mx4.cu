@@ -307,7 +307,7 @@ int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, co
   if (swiglu && out_dtype != AFD_DTYPE_BF16) return AFD_ERR_UNSUPPORTED;
   if (n_rows == 0) return AFD_OK;
   if (!codes || !scales || !offsets || !weight || !out || !aligned(codes, 16) || !aligned(weight, 128) ||
-      !aligned(scales, 4) || !aligned(out, 16) || !aligned(offsets, 4) || ldo % 8)
+      !aligned(scales, 8) || !aligned(out, 16) || !aligned(offsets, 4) || ldo % 8)
     return AFD_ERR_ARG;
   int rc = check_device_ptrs({codes, scales, offsets, weight, out});
   LaunchCtx lc;
@@ -335,7 +335,7 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, con
   if (n_rows == 0) return AFD_OK;
   if (workspace_bytes < need) return AFD_ERR_CAPACITY;
   if (!codes || !scales || !offsets || !w13 || !wd || !out || !workspace || !aligned(codes, 16) ||
-      !aligned(scales, 4) || !aligned(w13, 128) || !aligned(wd, 128) || !aligned(out, 16) || !aligned(offsets, 4) ||
+      !aligned(scales, 8) || !aligned(w13, 128) || !aligned(wd, 128) || !aligned(out, 16) || !aligned(offsets, 4) ||
       !aligned(workspace, 256) || ldo % 8)
     return AFD_ERR_ARG;
   int rc = check_device_ptrs({codes, scales, offsets, w13, wd, out, workspace});

@@ -9,11 +9,11 @@
 // takes a narrow instruction and not a mostly empty 128-row one.  Per stage
 // of 256 columns a CTA takes 17 KB of weight (codes and scales in one bulk
 // copy), the tokens' codes by TMA (128-byte swizzle) and their scales, which
-// two warps gather from the plain rows into the image tcgen05.cp spreads
+// several warps gather from the plain rows into the image tcgen05.cp spreads
 // over the lanes: a group's rows start anywhere, so the tiled image could
 // not be laid out before the groups are known.
 //
-// Warps: 0 copies, 1 MMA, 2-3 token scales, 4-11 epilogue.  All waits are
+// Warps: 0 copies, 1 MMA, from 2 token scales, 8-15 epilogue.  All waits are
 // bounded.
 #include "afd_mx4.cuh"
 
@@ -29,7 +29,8 @@ __device__ int32_t g_mx4_status;  // calls without a context
 constexpr int BK = 256;               // columns per stage
 constexpr int A_BYTES = 2 * kMx4BlkBytes;
 constexpr int EPI_WARPS = 8;
-constexpr int NUM_THREADS = 128 + EPI_WARPS * 32;
+constexpr int EPI_WARP0 = 8;          // a multiple of 4: a warp reads the TMEM lanes of its number mod 4
+constexpr int NUM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 // epilogue staging, one buffer per four warps: 32 tokens x 128 output rows
 // (SwiGLU: 64) of bf16, the rows 16 bytes apart in the banks
 constexpr int EPI_PITCH = 272;
@@ -41,6 +42,12 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 template <int BN>
 struct Ring {
   static constexpr int STAGES = BN > 64 ? 4 : 7;
+  // Warps that fill the token scales, a stage each in turn.  No more than
+  // stages: a warp that has filled stage i waits next for the release of
+  // i + SF_WARPS - STAGES, and a parity wait tells a phase from the one
+  // before it only; with more warps than stages it could pass one round early.
+  static constexpr int SF_WARPS = BN > 64 ? 4 : 6;
+  static_assert(SF_WARPS <= STAGES && 2 + SF_WARPS <= EPI_WARP0, "scale warps");
   static constexpr int NB = (BN + 127) / 128;            // 128-row scale images per 128 columns
   static constexpr int B_BYTES = BN * (BK / 2);
   static constexpr int S_BYTES = 2 * NB * 512;
@@ -202,7 +209,11 @@ __device__ __forceinline__ void load_scales(const uint8_t* xs, int64_t x_rows, i
     const int64_t row = row0 + lane + 32 * i;
     if (row >= x_rows) continue;
     const uint8_t* p = xs + row * pitch + b0;
-    if ((pitch & 3) == 0) {  // rows start on 4 bytes
+    if ((pitch & 7) == 0) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v[i][0] = w.x;
+      v[i][1] = w.y;
+    } else if ((pitch & 3) == 0) {  // rows start on 4 bytes
       v[i][0] = *reinterpret_cast<const uint32_t*>(p);
       if (b0 + 4 < pitch) v[i][1] = *reinterpret_cast<const uint32_t*>(p + 4);
     } else {
@@ -353,8 +364,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       const uint64_t dl = globaltimer_ns() + 100000000ull;
       while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
     }
-  } else if (warp < 4) {
-    // ------------------------------ token scales: the two warps take stages in turn
+  } else if (warp < 2 + R::SF_WARPS) {
+    // ------------------------------ token scales: the warps take stages in turn
     int unit = blockIdx.x, kb = 0;
     Unit t;
     int nkb = 0;
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       t = decode_unit<BN>(a, tail, ngroups, unit);
       nkb = (a.K[t.kind] + BK - 1) / BK;
     };
-    if (warp == 3 && unit < total) advance();
+    for (int i = 2; i < warp && unit < total; i++) advance();
     uint32_t v[BN / 32][2];
     if (unit < total) load_scales<BN>(a.xs[t.kind], a.x_rows[t.kind], a.K[t.kind] / 32, t.row, kb, lane, v);
     int it = warp - 2;
@@ -393,13 +404,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail->full[s]));
-      advance();
-      if (unit < total) advance();
+      for (int i = 0; i < R::SF_WARPS && unit < total; i++) advance();
       if (unit < total) load_scales<BN>(a.xs[t.kind], a.x_rows[t.kind], a.K[t.kind] / 32, t.row, kb, lane, v);
-      it += 2;
+      it += R::SF_WARPS;
     }
-  } else {
-    // ------------------------------ epilogue (warps 4..11)
+  } else if (warp >= EPI_WARP0) {
+    // ------------------------------ epilogue
     // Two groups of four warps take 32 token columns at a time in turn; a
     // warp reads its 32 TMEM lanes in the fragment layout, so that stmatrix
     // writes tokens as rows (a 32 x 32 piece in 4 instructions, where 2-byte
@@ -407,7 +417,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     // thread holds the gate and the up value of one output: the group's
     // rows then leave shared memory as whole 256-byte (SwiGLU: 128) runs.
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int half = (warp - EPI_WARP0) >> 2;
     const int gt = threadIdx.x & 127;  // thread of the group
     uint8_t* ebuf = smem + R::kEpiOffset + (size_t)half * EPI_BUF_BYTES;
     const uint32_t ebuf_s = smem_u32(ebuf);

@@ -709,7 +709,7 @@ int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_exp
 /* Grouped product: out[r] = W[g] x[r] for the rows r in [offsets[g],
  * offsets[g + 1]), fp32 accumulation, one rounding to out_dtype.
  *   codes, scales  the rows x, MXFP4 [n_rows, K]; codes 16-byte, scales
- *                  4-byte aligned
+ *                  8-byte aligned
  *   offsets        device int32 [num_experts + 1], ascending (AFD_WS_OFFSETS);
  *                  clamped to [0, n_rows]; rows in no group are left as they were
  *   weight         afd_mx4_pack_weight of [num_experts, M, K] with this swiglu

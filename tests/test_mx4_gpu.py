@@ -177,6 +177,13 @@ def test_product_swiglu(counts, M, K):
     check_product(counts, M, K, torch.bfloat16, swiglu=True, seed=M + K)
 
 
+@pytest.mark.parametrize("counts,M,K", [([2500, 3000], 2048, 1408), ([40] * 16, 2048, 1408), ([700, 1, 3300], 2816, 320)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_units_per_sm(counts, M, K, swiglu):
+    """More output tiles than the GPU has SMs: every ring goes round many times."""
+    check_product(counts, M, K, torch.bfloat16, swiglu=swiglu, seed=K)
+
+
 @pytest.mark.parametrize("counts", [[7, 0, 30], [250, 400]])
 def test_rows_outside_groups_keep_their_values(counts):
     for swiglu in (False, True):
