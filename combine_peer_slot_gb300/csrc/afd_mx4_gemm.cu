@@ -80,14 +80,19 @@ struct Ring {
 // matrix descriptors: K-major operand tiles with the 128-byte swizzle (rows
 // of 128 bytes, groups of 8 rows 1024 bytes apart) and the 64-byte one (rows
 // of 64 bytes, 512 apart); a scale image without swizzle (8 x 16-byte core
-// matrices 128 bytes apart)
-__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)layout << 61;
+// matrices 128 bytes apart).  The upper word is the layout's, the lower the
+// address in 16-byte units: one thread issues every MMA, so the loop only
+// adds to the lower words (with whole descriptors built at each use it was
+// the issuing thread that bounded the kernel: 1500 cycles a stage whatever
+// the tile's width).
+constexpr uint32_t kDescTokens = (1024u >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDescWeight = (512u >> 4) | 1u << 14 | 4u << 29;
+constexpr uint32_t kDescScales = (128u >> 4) | 1u << 14;
+__device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t addr16) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | 1u << 16), "r"(hi));
+  return d;
 }
-__device__ __forceinline__ uint64_t desc_tokens(uint32_t saddr) { return desc_of(saddr, 1024, 2); }
-__device__ __forceinline__ uint64_t desc_weight(uint32_t saddr) { return desc_of(saddr, 512, 4); }
-__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) { return desc_of(saddr, 128, 0); }
 
 // kind::mxf4: A and B e2m1 (format 1), e8m0 scales (bit 23), K = 64, M = 128;
 // sf: the first of the two scale bytes used of each lane's four (0 or 2)
@@ -95,18 +100,37 @@ __device__ __forceinline__ uint32_t idesc_mx4(int n, int sf) {
   return (uint32_t)sf << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(128 >> 4) << 24 |
          (uint32_t)sf << 29;
 }
-__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, uint32_t accumulate) {
+// The issuing warp runs its loop as a whole and each of the next three is
+// predicated on its elected lane: under a branch on the lane the operands
+// would leave the uniform registers these instructions take them from.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_mx4(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %7, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(elected)
       : "memory");
 }
 // 32 lanes x 16 bytes of shared memory into four TMEM columns, the same for
 // each quarter of the lanes
-__device__ __forceinline__ void cp_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void cp_scales(uint32_t elected, uint32_t tmem, uint64_t desc) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(tmem),
+      "l"(desc), "r"(elected)
+      : "memory");
 }
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
@@ -123,6 +147,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
   }
   return true;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
+                                          int32_t* status) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, deadline, status));
 }
 
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
@@ -320,50 +349,56 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         for (int i = 0; i < 10000; i++) __nanosleep(1000);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------ MMA issuer
-      int s = 0;
-      uint32_t ph = 0;
-      int acc = 0;
-      uint32_t acc_ph = 0;
-      bool ok = true;
-      for (int unit = blockIdx.x; unit < total && ok; unit += gridDim.x) {
-        const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
-        const int K = a.K[t.kind];
-        const uint32_t id0 = idesc_mx4(t.n_mma, 0), id2 = idesc_mx4(t.n_mma, 2);
-        if (!wait_bar(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * BN);
-        for (int kb = 0; kb * BK < K; kb++) {
-          if (!wait_bar(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_base + s * R::STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES, ss = sb + R::B_BYTES;
-          const uint32_t sf = tmem + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
-          const int steps = min(4, (K - kb * BK + 63) / 64);
-          for (int c = 0; c < (steps + 1) / 2; c++) {  // 128 columns: scales, then two MMAs
-            cp_scales(sf + 4 * c, desc_scales(sa + c * kMx4BlkBytes + kMx4BlkCodes));
-#pragma unroll
-            for (int b = 0; b < NB; b++)
-              cp_scales(sf + 8 + 4 * (c * NB + b), desc_scales(ss + (c * NB + b) * 512));
-          }
-          for (int kk = 0; kk < steps; kk++) {
-            const int c = kk >> 1, o = kk & 1;
-            mma_mx4(d, desc_weight(sa + c * kMx4BlkBytes + o * 32), desc_tokens(sb + kk * 32), o ? id2 : id0,
-                    sf + 4 * c, sf + 8 + 4 * c * NB, (kb | kk) != 0);
-          }
-          tc_commit(smem_u32(&tail->empty[s]));
-          if (++s == STAGES) { s = 0; ph ^= 1; }
-        }
+    // ------------------------------ MMA issuer
+    const uint32_t el = elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    bool ok = true;
+    for (int unit = blockIdx.x; unit < total && ok; unit += gridDim.x) {
+      const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
+      const int K = a.K[t.kind];
+      const uint32_t id0 = idesc_mx4(t.n_mma, 0), id2 = idesc_mx4(t.n_mma, 2);
+      ok = warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * BN);
+      for (int kb = 0; kb * BK < K; kb++) {
+        ok = warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status);
         if (!ok) break;
-        tc_commit(smem_u32(&tail->tfull[acc]));
-        if (++acc == 2) { acc = 0; acc_ph ^= 1; }
+        tc_fence_after();
+        const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
+        const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
+        const uint32_t sf = tmem + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
+        const int steps = min(4, (K - kb * BK + 63) / 64);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {  // 128 columns: their scales
+          if (2 * c >= steps) break;
+          cp_scales(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
+#pragma unroll
+          for (int b = 0; b < NB; b++)
+            cp_scales(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++) {
+          if (kk >= steps) break;
+          const int c = kk >> 1, o = kk & 1;
+          mma_mx4(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
+                  o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, (kb | kk) != 0);
+        }
+        commit(el, smem_u32(&tail->empty[s]));
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
-      // every issued MMA completes before TMEM is released
-      tc_commit(smem_u32(&tail->drain));
-      const uint64_t dl = globaltimer_ns() + 100000000ull;
-      while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
+      if (!ok) break;
+      commit(el, smem_u32(&tail->tfull[acc]));
+      if (++acc == 2) { acc = 0; acc_ph ^= 1; }
     }
+    // every issued MMA completes before TMEM is released
+    commit(el, smem_u32(&tail->drain));
+    const uint64_t dl = globaltimer_ns() + 100000000ull;
+    while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
+    __syncwarp();
   } else if (warp < 2 + R::SF_WARPS) {
     // ------------------------------ token scales: the warps take stages in turn
     int unit = blockIdx.x, kb = 0;
