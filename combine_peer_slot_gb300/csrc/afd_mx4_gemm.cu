@@ -198,33 +198,55 @@ struct Unit {
   int64_t row;  // first row of the token tile
 };
 
+// A role's walk over its units.  Consecutive units of a CTA lie gridDim.x
+// apart, so the group is found by stepping from the last one (a few shared
+// loads), and by a search only over a run of empty groups.
 template <int BN>
-__device__ __forceinline__ Unit decode_unit(const Mx4GemmArgs& a, const typename Ring<BN>::Tail* T, int ngroups,
-                                            int unit) {
-  int lo = 0, hi = ngroups - 1;
-  while (lo < hi) {  // last group whose first unit is <= unit (empty groups share it with the next)
-    const int mid = (lo + hi + 1) >> 1;
-    if (T->tile0[mid] <= unit) lo = mid; else hi = mid - 1;
-  }
+struct Walk {
+  const Mx4GemmArgs& a;
+  const typename Ring<BN>::Tail* T;
+  int ngroups, total;
+  int unit, g;
   Unit t;
-  t.group = lo;
-  t.kind = lo == a.n_groups;
-  const int u = unit - T->tile0[lo];
-  const int n_tiles = (T->rows[lo] + BN - 1) / BN;
-  const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
-  int nt;
-  if (BN == 64) {  // the weights stream from HBM: a weight tile's token tiles side by side, for L2
-    nt = u % n_tiles;
-    t.mt = u / n_tiles;
-  } else {         // the units running at once share token tiles
-    t.mt = u % m_tiles;
-    nt = u / m_tiles;
+  __device__ __forceinline__ Walk(const Mx4GemmArgs& args, const typename Ring<BN>::Tail* tail, int n, int tot)
+      : a(args), T(tail), ngroups(n), total(tot), unit((int)blockIdx.x), g(0) {
+    decode();
   }
-  t.row = (int64_t)T->row0[lo] + (int64_t)nt * BN;
-  t.rows = min(BN, T->rows[lo] - nt * BN);
-  t.n_mma = (t.rows + 15) & ~15;
-  return t;
-}
+  __device__ __forceinline__ bool more() const { return unit < total; }
+  __device__ __forceinline__ void next() {
+    unit += (int)gridDim.x;
+    decode();
+  }
+  __device__ __forceinline__ void decode() {
+    if (unit >= total) return;
+#pragma unroll 1
+    for (int i = 0; i < 4 && T->tile0[g + 1] <= unit; i++) g++;
+    if (T->tile0[g + 1] <= unit) {
+      int lo = g, hi = ngroups - 1;
+      while (lo < hi) {  // last group whose first unit is <= unit (empty groups share it with the next)
+        const int mid = (lo + hi + 1) >> 1;
+        if (T->tile0[mid] <= unit) lo = mid; else hi = mid - 1;
+      }
+      g = lo;
+    }
+    t.group = g;
+    t.kind = g == a.n_groups;
+    const int u = unit - T->tile0[g], rows = T->rows[g];
+    int nt;
+    if (BN == 64) {  // the weights stream from HBM: a weight tile's token tiles side by side, for L2
+      const int n_tiles = (rows + BN - 1) / BN;
+      t.mt = n_tiles == 1 ? u : u / n_tiles;
+      nt = u - t.mt * n_tiles;
+    } else {         // the units running at once share token tiles
+      const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
+      nt = u / m_tiles;
+      t.mt = u - nt * m_tiles;
+    }
+    t.row = (int64_t)T->row0[g] + (int64_t)nt * BN;
+    t.rows = min(BN, rows - nt * BN);
+    t.n_mma = (t.rows + 15) & ~15;
+  }
+};
 
 // A lane's scale bytes of one stage: rows lane + 32 i, eight bytes each
 // (columns kb * 256 ..), zero past the row's end or the last row.
@@ -312,7 +334,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     if (w < warp) before += tail->wsum[w];
     total += tail->wsum[w];
   }
-  if (threadIdx.x < ngroups) tail->tile0[threadIdx.x] = before + incl - mine;
+  if (threadIdx.x < ngroups) tail->tile0[threadIdx.x + 1] = before + incl;
+  if (threadIdx.x == 0) tail->tile0[0] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -327,11 +350,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int unit = blockIdx.x; unit < total && ok; unit += gridDim.x) {
-        const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
+      for (Walk<BN> w(a, tail, ngroups, total); w.more() && ok; w.next()) {
+        const Unit& t = w.t;
         const int nk = mx4_kblocks(a.K[t.kind]);
         const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
-        const uint8_t* w =
+        const uint8_t* wt =
             a.w[t.kind] + ((int64_t)(t.kind ? 0 : t.group) * m_tiles + t.mt) * nk * (int64_t)kMx4BlkBytes;
         for (int kb = 0; kb * 2 < nk; kb++) {
           if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
@@ -339,7 +362,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           const uint32_t a_bytes = min(2, nk - 2 * kb) * kMx4BlkBytes;
           mbar_expect_tx(full, a_bytes + R::B_BYTES);
           const uint32_t sa = smem_base + s * R::STAGE_BYTES;
-          bulk_load(sa, w + (int64_t)kb * 2 * kMx4BlkBytes, a_bytes, full);
+          bulk_load(sa, wt + (int64_t)kb * 2 * kMx4BlkBytes, a_bytes, full);
           tma_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2), (int)t.row, full);
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
@@ -356,10 +379,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     int acc = 0;
     uint32_t acc_ph = 0;
     bool ok = true;
-    for (int unit = blockIdx.x; unit < total && ok; unit += gridDim.x) {
-      const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
-      const int K = a.K[t.kind];
-      const uint32_t id0 = idesc_mx4(t.n_mma, 0), id2 = idesc_mx4(t.n_mma, 2);
+    Walk<BN> w(a, tail, ngroups, total);
+    while (w.more()) {
+      const int K = a.K[w.t.kind];
+      const uint32_t id0 = idesc_mx4(w.t.n_mma, 0), id2 = idesc_mx4(w.t.n_mma, 2);
       ok = warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status);
       if (!ok) break;
       tc_fence_after();
@@ -389,6 +412,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
         commit(el, smem_u32(&tail->empty[s]));
         if (++s == STAGES) { s = 0; ph ^= 1; }
+        if (kb == 0) w.next();  // found while this unit's MMAs run
       }
       if (!ok) break;
       commit(el, smem_u32(&tail->tfull[acc]));
@@ -401,26 +425,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     __syncwarp();
   } else if (warp < 2 + R::SF_WARPS) {
     // ------------------------------ token scales: the warps take stages in turn
-    int unit = blockIdx.x, kb = 0;
-    Unit t;
-    int nkb = 0;
-    if (unit < total) {
-      t = decode_unit<BN>(a, tail, ngroups, unit);
-      nkb = (a.K[t.kind] + BK - 1) / BK;
-    }
-    auto advance = [&]() {
-      if (++kb < nkb) return;
-      kb = 0;
-      unit += gridDim.x;
-      if (unit >= total) return;
-      t = decode_unit<BN>(a, tail, ngroups, unit);
-      nkb = (a.K[t.kind] + BK - 1) / BK;
+    Walk<BN> w(a, tail, ngroups, total);
+    int kb = 0;
+    auto advance = [&](int n) {  // n stages on
+      kb += n;
+      while (w.more()) {
+        const int nkb = (a.K[w.t.kind] + BK - 1) / BK;
+        if (kb < nkb) break;
+        kb -= nkb;
+        w.next();
+      }
     };
-    for (int i = 2; i < warp && unit < total; i++) advance();
+    auto load = [&](uint32_t (&v)[BN / 32][2]) {
+      if (w.more())
+        load_scales<BN>(a.xs[w.t.kind], a.x_rows[w.t.kind], a.K[w.t.kind] / 32, w.t.row, kb, lane, v);
+    };
+    advance(warp - 2);
     uint32_t v[BN / 32][2];
-    if (unit < total) load_scales<BN>(a.xs[t.kind], a.x_rows[t.kind], a.K[t.kind] / 32, t.row, kb, lane, v);
+    load(v);
     int it = warp - 2;
-    while (unit < total) {
+    while (w.more()) {
       const int s = it % STAGES;
       const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
       bool ok = wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status);
@@ -439,8 +463,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail->full[s]));
-      for (int i = 0; i < R::SF_WARPS && unit < total; i++) advance();
-      if (unit < total) load_scales<BN>(a.xs[t.kind], a.x_rows[t.kind], a.K[t.kind] / 32, t.row, kb, lane, v);
+      advance(R::SF_WARPS);
+      load(v);
       it += R::SF_WARPS;
     }
   } else if (warp >= EPI_WARP0) {
@@ -458,8 +482,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     const uint32_t ebuf_s = smem_u32(ebuf);
     int acc = 0;
     uint32_t acc_ph = 0;
-    for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
-      const Unit t = decode_unit<BN>(a, tail, ngroups, unit);
+    for (Walk<BN> w(a, tail, ngroups, total); w.more(); w.next()) {
+      const Unit& t = w.t;
       bool ok = wait_bar(smem_u32(&tail->tfull[acc]), acc_ph, abort_flag, deadline, status);
       if (!group_all(half, ok)) break;
       tc_fence_after();
@@ -528,10 +552,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             const int r = gt >> 2, f = t.mt * 64 + (gt & 3) * 16;
             const uint4* src = reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH_SWIGLU + (gt & 3) * 32);
             const uint4 lo = src[0], hi = src[1];
-            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const uint32_t hw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+            for (int i = 0; i < 8; i++) m = max(m, max((hw[i] << 16) & 0x7fffffffu, hw[i] & 0x7fff0000u));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             const uint32_t sc = mx4_scale_byte(m, 0);
             const float inv = mx4_inv_scale(sc);
@@ -541,8 +565,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
               float v[8];
 #pragma unroll
               for (int j = 0; j < 4; j++) {
-                v[2 * j] = __uint_as_float(w[4 * i + j] << 16) * inv;
-                v[2 * j + 1] = __uint_as_float(w[4 * i + j] & 0xffff0000u) * inv;
+                v[2 * j] = __uint_as_float(hw[4 * i + j] << 16) * inv;
+                v[2 * j + 1] = __uint_as_float(hw[4 * i + j] & 0xffff0000u) * inv;
               }
               code[i] = sc == 255u ? 0u : mx4_encode8(v);
             }
