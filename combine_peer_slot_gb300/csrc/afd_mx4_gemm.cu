@@ -39,6 +39,13 @@ constexpr int EPI_BUF_BYTES = 32 * EPI_PITCH;
 constexpr int MAX_GROUPS = 257;       // 256 experts and the shared rows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
+// A stage's word for the MMA issuer, written by the copies' producer: bits
+// 0-8 the instruction's N, 9-11 the 64-column steps, then first / last stage
+// of its unit, and no more stages.  The issuer follows these words alone: it
+// is the one thread of control on the tensor pipe's critical path, and
+// finding its own units there cost 280 cycles a stage.
+constexpr uint32_t INFO_FIRST = 1u << 12, INFO_LAST = 1u << 13, INFO_STOP = 1u << 14;
+
 template <int BN>
 struct Ring {
   static constexpr int STAGES = BN > 64 ? 4 : 7;
@@ -67,6 +74,9 @@ struct Ring {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t info[STAGES];      // what the stage holds (INFO_*)
+    int m_tiles[2];             // weight tiles per kind, and (2^32 - 1) / m_tiles
+    uint32_t m_magic[2];
     int tile0[MAX_GROUPS + 1];  // first unit of each group
     int row0[MAX_GROUPS];
     int rows[MAX_GROUPS];
@@ -238,8 +248,9 @@ struct Walk {
       t.mt = n_tiles == 1 ? u : u / n_tiles;
       nt = u - t.mt * n_tiles;
     } else {         // the units running at once share token tiles
-      const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
-      nt = u / m_tiles;
+      const int m_tiles = T->m_tiles[t.kind];
+      nt = (int)__umulhi((uint32_t)u, T->m_magic[t.kind]);  // u / m_tiles, or one less
+      if ((nt + 1) * m_tiles <= u) nt++;
       t.mt = u - nt * m_tiles;
     }
     t.row = (int64_t)T->row0[g] + (int64_t)nt * BN;
@@ -335,7 +346,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     total += tail->wsum[w];
   }
   if (threadIdx.x < ngroups) tail->tile0[threadIdx.x + 1] = before + incl;
-  if (threadIdx.x == 0) tail->tile0[0] = 0;
+  if (threadIdx.x == 0) {
+    tail->tile0[0] = 0;
+    for (int k = 0; k < 2; k++) {
+      const int m = max(mx4_tiles(a.M[k], a.swiglu), 1);
+      tail->m_tiles[k] = m;
+      tail->m_magic[k] = 0xffffffffu / (uint32_t)m;  // under 2^32 / m by at most 1: u m_magic / 2^32 > u / m - 1
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -360,12 +378,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
           const uint32_t full = smem_u32(&tail->full[s]);
           const uint32_t a_bytes = min(2, nk - 2 * kb) * kMx4BlkBytes;
+          const int left = (a.K[t.kind] - kb * BK + 63) / 64;
+          tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, 4) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
+                          (left <= 4 ? INFO_LAST : 0u);
           mbar_expect_tx(full, a_bytes + R::B_BYTES);
           const uint32_t sa = smem_base + s * R::STAGE_BYTES;
           bulk_load(sa, wt + (int64_t)kb * 2 * kMx4BlkBytes, a_bytes, full);
           tma_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2), (int)t.row, full);
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
+      }
+      if (ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
+        tail->info[s] = INFO_STOP;
+        mbar_arrive(smem_u32(&tail->full[s]));
+        mbar_arrive(smem_u32(&tail->full[s]));  // for the scale warp, which has no such stage
       }
       // a wait gave up: the copies in flight land before the CTA leaves
       if (!ok)
@@ -374,49 +400,45 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   } else if (warp == 1) {
     // ------------------------------ MMA issuer
     const uint32_t el = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     int s = 0;
     uint32_t ph = 0;
     int acc = 0;
     uint32_t acc_ph = 0;
-    bool ok = true;
-    Walk<BN> w(a, tail, ngroups, total);
-    while (w.more()) {
-      const int K = a.K[w.t.kind];
-      const uint32_t id0 = idesc_mx4(w.t.n_mma, 0), id2 = idesc_mx4(w.t.n_mma, 2);
-      ok = warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status);
-      if (!ok) break;
+    for (;;) {
+      if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
+      const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
+      if (info & INFO_STOP) break;
+      if (info & INFO_FIRST)
+        if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
       tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(acc * BN);
-      for (int kb = 0; kb * BK < K; kb++) {
-        ok = warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
-        const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
-        const uint32_t sf = tmem + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
-        const int steps = min(4, (K - kb * BK + 63) / 64);
+      const uint32_t id0 = idesc_mx4((int)(info & 511u), 0), id2 = id0 | idesc_mx4(0, 2);
+      const uint32_t d = tm + (uint32_t)(acc * BN);
+      const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
+      const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
+      const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
+      const int steps = (int)(info >> 9) & 7;
 #pragma unroll
-        for (int c = 0; c < 2; c++) {  // 128 columns: their scales
-          if (2 * c >= steps) break;
-          cp_scales(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
+      for (int c = 0; c < 2; c++) {  // 128 columns: their scales
+        if (2 * c >= steps) break;
+        cp_scales(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
 #pragma unroll
-          for (int b = 0; b < NB; b++)
-            cp_scales(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; kk++) {
-          if (kk >= steps) break;
-          const int c = kk >> 1, o = kk & 1;
-          mma_mx4(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
-                  o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, (kb | kk) != 0);
-        }
-        commit(el, smem_u32(&tail->empty[s]));
-        if (++s == STAGES) { s = 0; ph ^= 1; }
-        if (kb == 0) w.next();  // found while this unit's MMAs run
+        for (int b = 0; b < NB; b++)
+          cp_scales(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
       }
-      if (!ok) break;
-      commit(el, smem_u32(&tail->tfull[acc]));
-      if (++acc == 2) { acc = 0; acc_ph ^= 1; }
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        if (kk >= steps) break;
+        const int c = kk >> 1, o = kk & 1;
+        mma_mx4(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
+                o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 || !(info & INFO_FIRST));
+      }
+      commit(el, smem_u32(&tail->empty[s]));
+      if (++s == STAGES) { s = 0; ph ^= 1; }
+      if (info & INFO_LAST) {
+        commit(el, smem_u32(&tail->tfull[acc]));
+        if (++acc == 2) { acc = 0; acc_ph ^= 1; }
+      }
     }
     // every issued MMA completes before TMEM is released
     commit(el, smem_u32(&tail->drain));
