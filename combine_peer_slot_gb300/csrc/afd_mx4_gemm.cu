@@ -159,6 +159,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+__device__ __forceinline__ uint32_t mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
                                           int32_t* status) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, deadline, status));
@@ -401,40 +410,68 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     // ------------------------------ MMA issuer
     const uint32_t el = elect_one();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // Each stage's barrier is tested, and its word read, while the stage
+    // before it is being issued: the two round trips to shared memory would
+    // otherwise stand between the stages (about 330 of 860 cycles a stage).
     int s = 0;
     uint32_t ph = 0;
     int acc = 0;
     uint32_t acc_ph = 0;
+    bool ready = false;
+    uint32_t word = 0;
     for (;;) {
-      if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
-      const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
-      if (info & INFO_STOP) break;
-      if (info & INFO_FIRST)
+      if (!ready) {
+        if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
+        word = *(volatile uint32_t*)&tail->info[s];
+      }
+      const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
+      if (info & (INFO_STOP | INFO_FIRST)) {
+        if (info & INFO_STOP) break;
         if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
+      }
       tc_fence_after();
+      const int s1 = s + 1 == STAGES ? 0 : s + 1;
+      const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
+      const uint32_t test = mbar_test_wait(smem_u32(&tail->full[s1]), ph1);
       const uint32_t id0 = idesc_mx4((int)(info & 511u), 0), id2 = id0 | idesc_mx4(0, 2);
       const uint32_t d = tm + (uint32_t)(acc * BN);
       const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
       const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
       const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
       const int steps = (int)(info >> 9) & 7;
-#pragma unroll
-      for (int c = 0; c < 2; c++) {  // 128 columns: their scales
-        if (2 * c >= steps) break;
+      const uint32_t more = (info & INFO_FIRST) ? 0u : 1u;
+      auto scales = [&](int c) {  // of 128 columns
         cp_scales(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
 #pragma unroll
         for (int b = 0; b < NB; b++)
           cp_scales(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
-      }
-#pragma unroll
-      for (int kk = 0; kk < 4; kk++) {
-        if (kk >= steps) break;
+      };
+      auto mma = [&](int kk) {    // of 64 columns
         const int c = kk >> 1, o = kk & 1;
         mma_mx4(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
-                o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 || !(info & INFO_FIRST));
+                o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 ? 1u : more);
+      };
+      if (steps == 4) {  // no branch between the instructions of a whole stage
+        scales(0);
+        scales(1);
+        ready = __all_sync(0xffffffffu, test != 0);
+        mma(0);
+        mma(1);
+        word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
+        mma(2);
+        mma(3);
+      } else {           // the unit's last columns
+        scales(0);
+        if (steps > 2) scales(1);
+        ready = __all_sync(0xffffffffu, test != 0);
+        word = *(volatile uint32_t*)&tail->info[s1];
+        mma(0);
+        if (steps > 1) mma(1);
+        if (steps > 2) mma(2);
       }
       commit(el, smem_u32(&tail->empty[s]));
-      if (++s == STAGES) { s = 0; ph ^= 1; }
+      s = s1;
+      ph = ph1;
       if (info & INFO_LAST) {
         commit(el, smem_u32(&tail->tfull[acc]));
         if (++acc == 2) { acc = 0; acc_ph ^= 1; }
