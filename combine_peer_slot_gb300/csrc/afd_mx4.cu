@@ -1,6 +1,8 @@
 // afd_mx4.cu -- MXFP4 coding on sm_103a (quantise, with the gather of routed
 // rows; dequantise; packing of weights for the product) and the host side
 // of the MXFP4 entry points.
+#include <cuda_fp16.h>
+
 #include <cstdio>
 #include <cstring>
 
@@ -11,13 +13,35 @@ namespace {
 constexpr int kThreads = 256;
 int64_t g_mx4_launches = 0;
 
+// Both coding kernels walk the matrix in chunks of eight values, a CTA
+// kChunks * 256 consecutive ones, a thread every 256th of them: a warp's
+// loads and stores are contiguous whatever the row length, and each thread
+// has kChunks independent loads in flight.  The row of the CTA's first chunk
+// takes one 64-bit division, the rest 32-bit ones by multiplication.
+constexpr int kChunks = 4;
+struct ChunkPos {
+  int64_t row0;
+  uint32_t c0, chunks, magic;
+  __device__ __forceinline__ ChunkPos(int64_t first, int n, uint32_t m) : chunks((uint32_t)n), magic(m) {
+    row0 = first / n;
+    c0 = (uint32_t)(first - row0 * n);
+  }
+  // row and chunk of the CTA's i-th chunk
+  __device__ __forceinline__ void at(int i, int64_t& row, int& c) const {
+    const uint32_t v = c0 + (uint32_t)i;
+    uint32_t q = __umulhi(v, magic);  // v / chunks, or one less (magic = (2^32 - 1) / chunks)
+    if ((q + 1) * chunks <= v) q++;
+    row = row0 + q;
+    c = (int)(v - q * chunks);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // quantise: four lanes hold one block of 32, eight values each (one 16-byte
-// load of bf16, two of fp32), so loads and the 4-byte code stores of a warp
-// are contiguous.  The block's largest magnitude is an integer maximum of
-// the sign-less bits (NaN and infinity sort above every number), the scale
-// is a power of two and the division by it exact: every code is the nearest
-// e2m1 value of the exact quotient.
+// load of bf16, two of fp32).  The block's largest magnitude is an integer
+// maximum of the sign-less bits (NaN and infinity sort above every number),
+// the scale is a power of two and the division by it exact: every code is
+// the nearest e2m1 value of the exact quotient.  Bound by memory.
 // ---------------------------------------------------------------------------
 struct QuantArgs {
   const uint8_t* x;
@@ -27,91 +51,128 @@ struct QuantArgs {
   int topk;
   int64_t n_rows;
   int chunks;  // eight-value chunks per row
+  uint32_t magic;
   int ceil_rule;
   uint32_t* codes;
   uint8_t* scales;
 };
 
 template <bool F32>
-__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
-  if (F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <bool F32>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const __grid_constant__ QuantArgs a) {
-  const int64_t total = a.n_rows * a.chunks;  // a multiple of 4
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / a.chunks;
-    const int c = (int)(i - r * a.chunks);
-    int64_t src = r;
+  const int64_t total = a.n_rows * a.chunks;  // a multiple of 4: a block's lanes are all in or all out
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kChunks);
+  const ChunkPos pos(first, a.chunks, a.magic);
+  uint4 lo[kChunks], hi[kChunks];
+#pragma unroll
+  for (int u = 0; u < kChunks; u++) {
+    const int i = u * kThreads + threadIdx.x;
+    lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+    if (first + i >= total) continue;
+    int64_t r;
+    int c;
+    pos.at(i, r, c);
     if (a.src) {
       const int32_t s = a.src[r];
-      src = s < 0 ? -1 : s / a.topk;
+      r = s < 0 ? -1 : (int64_t)((uint32_t)s / (uint32_t)a.topk);
+      if (r >= a.x_rows) r = -1;
     }
-    float v[8] = {};
-    if (src >= 0 && src < a.x_rows) load8<F32>(a.x + src * a.ld_bytes + (int64_t)c * (F32 ? 32 : 16), v);
-    uint32_t m = 0;
+    if (r < 0) continue;
+    const uint4* p = reinterpret_cast<const uint4*>(a.x + r * a.ld_bytes + (int64_t)c * (F32 ? 32 : 16));
+    lo[u] = p[0];
+    if (F32) hi[u] = p[1];
+  }
 #pragma unroll
-    for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    const uint32_t quad = 0xfu << (threadIdx.x & 28);  // the block's four lanes are all here
-    m = max(m, __shfl_xor_sync(quad, m, 1));
-    m = max(m, __shfl_xor_sync(quad, m, 2));
+  for (int u = 0; u < kChunks; u++) {
+    const int64_t i = first + u * kThreads + threadIdx.x;
+    const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+    float v[8];
+    uint32_t m = 0;
+    if (F32) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        v[j] = __uint_as_float(w[j]);
+        m = max(m, w[j] & 0x7fffffffu);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+      }
+      m = max(m << 16, m & 0x7fff0000u);
+    }
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (i >= total) continue;
     const uint32_t s = mx4_scale_byte(m, a.ceil_rule);
     const float inv = mx4_inv_scale(s);
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = s == 255u ? 0.0f : v[j] * inv;
-    a.codes[i] = mx4_encode8(v);
+    for (int j = 0; j < 8; j++) v[j] *= inv;
+    a.codes[i] = s == 255u ? 0u : mx4_encode8(v);
     if ((threadIdx.x & 3) == 0) a.scales[i >> 2] = (uint8_t)s;
   }
 }
 
 // ---------------------------------------------------------------------------
-// dequantise: eight values per thread.  Every value fits bf16 and fp32
-// exactly (three significant bits, exponents within both types').
+// dequantise: every value fits bf16 and fp32 exactly (three significant
+// bits, exponents within both types').  Bound by memory.
 // ---------------------------------------------------------------------------
+struct DequantArgs {
+  const uint32_t* codes;
+  const uint8_t* scales;
+  int64_t n_rows;
+  int chunks;
+  uint32_t magic;
+  uint8_t* out;
+  int64_t ld_bytes;
+};
+
 template <bool F32>
-__global__ void __launch_bounds__(kThreads)
-k_mx4_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total, int chunks,
-                 uint8_t* out, int64_t ld_bytes) {
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / chunks;
-    const int c = (int)(i - r * chunks);
-    const uint32_t w = codes[i];
-    const float s = mx4_scale(scales[i >> 2]);
-    float v[8];
+__global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const __grid_constant__ DequantArgs a) {
+  const int64_t total = a.n_rows * a.chunks;
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kChunks);
+  const ChunkPos pos(first, a.chunks, a.magic);
+  uint32_t code[kChunks];
+  float scale[kChunks];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const uint32_t n = (w >> (4 * j)) & 15u, e = (n >> 1) & 3u;
-      // e2m1: (1 + f / 2) 2^(e - 1), or f / 2 for e = 0
-      const float mag = e ? __uint_as_float((126u + e) << 23 | (n & 1u) << 22) : 0.5f * (float)(n & 1u);
-      v[j] = (n & 8u ? -mag : mag) * s;
+  for (int u = 0; u < kChunks; u++) {
+    const int64_t i = first + u * kThreads + threadIdx.x;
+    code[u] = i < total ? a.codes[i] : 0u;
+    scale[u] = i < total ? mx4_scale(a.scales[i >> 2]) : 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < kChunks; u++) {
+    const int i = u * kThreads + threadIdx.x;
+    if (first + i >= total) continue;
+    int64_t r;
+    int c;
+    pos.at(i, r, c);
+    uint32_t h[4];  // pairs of fp16, which holds every e2m1 value
+    asm("{ .reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3; }"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(code[u]));
+    float2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      v[j] = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      v[j].x *= scale[u];
+      v[j].y *= scale[u];
     }
-    uint8_t* p = out + r * ld_bytes + (int64_t)c * (F32 ? 32 : 16);
+    uint4* p = reinterpret_cast<uint4*>(a.out + r * a.ld_bytes + (int64_t)c * (F32 ? 32 : 16));
     if (F32) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
-      uint32_t h[4];
+      uint32_t b[4];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        h[j] = *reinterpret_cast<const uint32_t*>(&b);
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[j].x, v[j].y);
+        b[j] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+      p[0] = make_uint4(b[0], b[1], b[2], b[3]);
     }
   }
 }
@@ -155,10 +216,7 @@ k_mx4_pack(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales
   }
 }
 
-unsigned stride_grid(int64_t items, int num_sms) {
-  const int64_t g = (items + kThreads - 1) / kThreads;
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(g, (int64_t)num_sms * 16));
-}
+int64_t chunk_grid(int64_t chunks) { return (chunks + kThreads * kChunks - 1) / (kThreads * kChunks); }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -191,10 +249,11 @@ cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx,
                                 const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,
                                 uint8_t* codes, uint8_t* scales) {
   const QuantArgs a{static_cast<const uint8_t*>(x), ldx * (f32 ? 4 : 2), x_rows, src_rows, topk, n_rows, cols / 8,
-                    ceil_rule, reinterpret_cast<uint32_t*>(codes), scales};
-  const unsigned grid = stride_grid(n_rows * (cols / 8), lc.num_sms);
-  return f32 ? launch_k(lc, k_mx4_quantize<true>, grid, kThreads, 0, a)
-             : launch_k(lc, k_mx4_quantize<false>, grid, kThreads, 0, a);
+                    0xffffffffu / (uint32_t)(cols / 8), ceil_rule, reinterpret_cast<uint32_t*>(codes), scales};
+  const int64_t grid = chunk_grid(n_rows * (cols / 8));
+  if (grid >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+  return f32 ? launch_k(lc, k_mx4_quantize<true>, (unsigned)grid, kThreads, 0, a)
+             : launch_k(lc, k_mx4_quantize<false>, (unsigned)grid, kThreads, 0, a);
 }
 
 cudaError_t launch_mx4_pack(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int E, int64_t M,
@@ -219,6 +278,7 @@ int afd_mx4_quantize(const void* x, int64_t ldx, int64_t x_rows, int cols, int d
   if ((!x && x_rows > 0) || !codes || !scales || !aligned(x, 16) || (ldx * es) % 16 || !aligned(codes, 16) ||
       !aligned(src_rows, 4))
     return AFD_ERR_ARG;
+  if (chunk_grid(n_rows * (cols / 8)) >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
   int rc = check_device_ptrs({x, src_rows, codes, scales});
   LaunchCtx lc;
   if (!rc) rc = make_lc(cuda_stream, &lc);
@@ -242,13 +302,12 @@ int afd_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n_ro
   if (!rc) rc = make_lc(cuda_stream, &lc);
   if (rc) return rc;
   const int chunks = cols / 8;
-  const int64_t total = n_rows * chunks;
-  const uint32_t* c32 = reinterpret_cast<const uint32_t*>(codes);
-  uint8_t* o = static_cast<uint8_t*>(out);
-  return launched(es == 4 ? launch_k(lc, k_mx4_dequantize<true>, stride_grid(total, lc.num_sms), kThreads, 0, c32,
-                                     scales, total, chunks, o, ldo * 4)
-                          : launch_k(lc, k_mx4_dequantize<false>, stride_grid(total, lc.num_sms), kThreads, 0, c32,
-                                     scales, total, chunks, o, ldo * 2),
+  const int64_t grid = chunk_grid(n_rows * chunks);
+  if (grid >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
+  const DequantArgs a{reinterpret_cast<const uint32_t*>(codes), scales, n_rows, chunks, 0xffffffffu / (uint32_t)chunks,
+                      static_cast<uint8_t*>(out), ldo * es};
+  return launched(es == 4 ? launch_k(lc, k_mx4_dequantize<true>, (unsigned)grid, kThreads, 0, a)
+                          : launch_k(lc, k_mx4_dequantize<false>, (unsigned)grid, kThreads, 0, a),
                   "mx4 dequantize");
 }
 

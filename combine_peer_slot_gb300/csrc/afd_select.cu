@@ -30,6 +30,8 @@ struct SelArgs {
   float* w;
   int n, E, k, sigmoid, G, tg, gtop, renorm;
   float scale;
+  int vec, bvec;  // logits rows / bias: a lane's run of experts can be loaded whole
+  int whole;      // an expert group is a power of two of lanes
 };
 
 // order-preserving map of the fp32 values to unsigned (NaN excluded), with
@@ -146,51 +148,130 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
   }
 }
 
+// PER consecutive values, 16 bytes at a time where the row allows it
+template <typename LT, int PER>
+__device__ __forceinline__ void load_run(const void* base, int64_t i0, int have, bool vec, float (&v)[PER]) {
+  if (vec && have >= PER) {
+    if (sizeof(LT) == 4) {
+      if (PER % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < PER / 4; i++) {
+          const float4 q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i0)[i];
+          v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+        }
+      } else {
+        const float2 q = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(base) + i0);
+        v[0] = q.x; v[1] = q.y;
+      }
+    } else {
+      uint32_t w[PER / 2];
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + i0;
+      if (PER == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x; w[1 % (PER / 2)] = q.y; w[2 % (PER / 2)] = q.z; w[3 % (PER / 2)] = q.w;
+      } else if (PER == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        w[0] = q.x; w[1 % (PER / 2)] = q.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+#pragma unroll
+      for (int i = 0; i < PER / 2; i++) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; i++) v[i] = i < have ? load_logit<LT>(base, i0 + i) : -INFINITY;
+}
+
+// (v, slot) above (w, slot'): the larger key, the lower slot of two equal.
+// Packed as key << 32 | (31 - slot) one unsigned comparison says so.
+__device__ __forceinline__ void order(uint64_t& a, uint64_t& b) {
+  const uint64_t hi = a > b ? a : b, lo = a > b ? b : a;
+  a = hi;
+  b = lo;
+}
+template <int PER>
+__device__ __forceinline__ void sort_down(uint64_t (&k)[PER]) {
+  if (PER == 2) {
+    order(k[0], k[1 % PER]);
+  } else if (PER == 4) {
+    order(k[0], k[1 % PER]); order(k[2 % PER], k[3 % PER]);
+    order(k[0], k[2 % PER]); order(k[1 % PER], k[3 % PER]);
+    order(k[1 % PER], k[2 % PER]);
+  } else {  // Batcher's odd-even merge network for eight: 19 comparisons
+    order(k[0], k[1 % PER]); order(k[2 % PER], k[3 % PER]); order(k[4 % PER], k[5 % PER]); order(k[6 % PER], k[7 % PER]);
+    order(k[0], k[2 % PER]); order(k[1 % PER], k[3 % PER]); order(k[4 % PER], k[6 % PER]); order(k[5 % PER], k[7 % PER]);
+    order(k[1 % PER], k[2 % PER]); order(k[5 % PER], k[6 % PER]);
+    order(k[0], k[4 % PER]); order(k[1 % PER], k[5 % PER]); order(k[2 % PER], k[6 % PER]); order(k[3 % PER], k[7 % PER]);
+    order(k[2 % PER], k[4 % PER]); order(k[3 % PER], k[5 % PER]);
+    order(k[1 % PER], k[2 % PER]); order(k[3 % PER], k[4 % PER]); order(k[5 % PER], k[6 % PER]);
+  }
+}
+
+__device__ __forceinline__ void merge_two(float& m1, float& m2, int o) {
+  const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+  m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+  m1 = fmaxf(m1, o1);
+}
+
 // One warp per row; lane l holds experts [l * PER, (l + 1) * PER), so the
-// lowest lane of a tie holds the lowest index.
+// lowest lane of a tie holds the lowest index.  A lane sorts its own values
+// once; each choice is then one warp-wide integer maximum of the lanes'
+// heads, and the owner moves to its next value.
 template <typename LT, int PER>
 __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_constant__ SelArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kSelWarps + (threadIdx.x >> 5);
   if (row >= a.n) return;
-  const int e0 = lane * PER;
-  float l[PER], s[PER];
-  uint32_t key[PER];  // what is compared; 0: not to be chosen
+  const int e0 = lane * PER, have = a.E - e0;
+  float l[PER], s[PER], c[PER];
+  load_run<LT, PER>(a.logits, row * a.ld + e0, have, a.vec, l);
+  const bool scored = a.bias != nullptr;  // the choice is by score + bias, not by logit
+  const bool by_score = scored || (a.G > 1 && a.gtop == 2);
+  float b[PER];
+  if (scored) load_run<float, PER>(a.bias, e0, have, a.bvec, b);
   float top = -INFINITY;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    l[i] = e0 + i < a.E ? load_logit<LT>(a.logits, row * a.ld + e0 + i) : -INFINITY;
     bad |= l[i] != l[i] || (!a.sigmoid && l[i] == INFINITY);
     top = fmaxf(top, l[i]);
   }
+  // Scores: 2^x and 1 / x as the hardware approximates them (2 and 1 ulp).
+  // They rank; the chosen ones' weights are computed again in full.
+  float z = 0.0f;
   if (!a.sigmoid) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  float z = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; i++) {
-    s[i] = l[i] == -INFINITY ? 0.0f : a.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - top);
-    z += s[i];
-  }
-  if (!a.sigmoid) {
+    for (int i = 0; i < PER; i++) {
+      s[i] = l[i] == -INFINITY ? 0.0f : __expf(l[i] - top);
+      z += s[i];
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (by_score) {
+      const float r = z > 0.0f ? 1.0f / z : 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; i++) s[i] = z > 0.0f ? s[i] / z : 0.0f;
+      for (int i = 0; i < PER; i++) s[i] *= r;
+    }
+  } else if (by_score) {
+#pragma unroll
+    for (int i = 0; i < PER; i++) s[i] = l[i] == -INFINITY ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-l[i]));
   }
-  const bool scored = a.bias != nullptr;  // the choice is by score + bias, not by logit
-  float c[PER];
+  uint64_t key[PER];  // high word: what is compared, 0 = not to be chosen
 #pragma unroll
   for (int i = 0; i < PER; i++) {
     c[i] = l[i];
-    if (scored && e0 + i < a.E) {
-      const float b = a.bias[e0 + i];
-      bad |= b != b;
-      if (l[i] > -INFINITY) c[i] = s[i] + b;
+    if (scored) {
+      bad |= i < have && b[i] != b[i];
+      if (l[i] > -INFINITY) c[i] = s[i] + b[i];
     }
-    key[i] = c[i] > -INFINITY ? ordered(c[i]) : 0u;
+    key[i] = c[i] > -INFINITY ? (uint64_t)ordered(c[i]) << 32 | (uint32_t)(31 - i) : 0ull;
   }
   if (__any_sync(0xffffffffu, bad)) {
     if (lane < a.k) {
@@ -200,96 +281,113 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     return;
   }
   // What two fp32 values of c may be off together, in units of the largest
-  // score (1 for a sigmoid, 1 / z for a softmax) and of |c|.  u = 2^-24: a
-  // sigmoid's error is at most 6 u (expf 2 ulp, the sum, the division), a
-  // softmax score's 25 u of the largest score (the argument's rounding enters
-  // as d u exp(-d) <= 0.37 u, expf 4 u, the sum of 256 terms in 8 + 5 steps
-  // and the division under 20 u), adding b another u |c|.  Twice that stays
-  // under unit times the larger of the two.
+  // score (1 for a sigmoid, 1 / z for a softmax) and of |c|.  u = 2^-24.  A
+  // sigmoid: the exponential's argument is off by |l| u, which moves s by
+  // s (1 - s) |l| u <= 0.3 u, its 2 ulp by 4 u s (1 - s) <= u, the sum 1 + e
+  // and the reciprocal by 3 u: 4.3 u in all.  A softmax: the argument enters
+  // as d u exp(-d) <= 0.37 u twice (difference, product by log2 e), the
+  // exponential 4 u, z and the two roundings under 24 u: 29 u of the largest
+  // score.  Adding b: another u |c|.  Twice each stays under unit times the
+  // larger of the largest score and |c| (16 u and 64 u).
   const float smax = a.sigmoid ? 1.0f : (z > 0.0f ? 1.0f / z : 0.0f);
   const float unit = a.sigmoid ? 9.5367431640625e-07f : 3.814697265625e-06f;  // 2^-20, 2^-18
   bool close = false;
   if (a.G > 1) {
     const int per = a.E / a.G;
-    float gs = -INFINITY;  // lane g: group g
-    const bool by_score = scored || a.gtop == 2;
-    for (int g = 0; g < a.G; g++) {
+    float gs;     // this lane's group's rank (whole), or lane g: group g's
+    int ahead = 0;
+    bool kept;    // whole: this lane's group stays
+    uint32_t keep = 0u;
+    float in, out;
+    if (a.whole) {
+      // a group is 1, 2, 4 .. lanes: each lane's own two best, merged over
+      // the group's lanes (2 steps for 8 groups of 256, where going through
+      // the groups one by one with the whole warp took 8 x 5)
       float m1 = -INFINITY, m2 = -INFINITY;
-      const int lo = g * per, hi = lo + per;
 #pragma unroll
       for (int i = 0; i < PER; i++) {
-        const bool in = e0 + i >= lo && e0 + i < hi && key[i] != 0u;
-        const float v = in ? (scored || !by_score ? c[i] : s[i]) : -INFINITY;
+        const float v = key[i] != 0ull ? (scored || !by_score ? c[i] : s[i]) : -INFINITY;
         m2 = fmaxf(m2, fminf(m1, v));
         m1 = fmaxf(m1, v);
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
-        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-        m1 = fmaxf(m1, o1);
+      const int lanes = per / PER;
+      for (int o = 1; o < lanes; o <<= 1) merge_two(m1, m2, o);
+      gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+      const int mine = lane / lanes;
+      for (int g = 0; g < a.G; g++) {
+        const float v = __shfl_sync(0xffffffffu, gs, (g * lanes) & 31);
+        ahead += v > gs || (v == gs && g < mine);
       }
-      if (lane == g) gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+      kept = ahead < a.tg;
+      const bool real = mine < a.G;
+      in = real && ahead == a.tg - 1 ? gs : -INFINITY;
+      out = real && ahead == a.tg ? gs : -INFINITY;
+    } else {
+      gs = -INFINITY;
+      for (int g = 0; g < a.G; g++) {
+        float m1 = -INFINITY, m2 = -INFINITY;
+        const int lo = g * per, hi = lo + per;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+          const bool here = e0 + i >= lo && e0 + i < hi && key[i] != 0ull;
+          const float v = here ? (scored || !by_score ? c[i] : s[i]) : -INFINITY;
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) merge_two(m1, m2, o);
+        if (lane == g) gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+      }
+      for (int g = 0; g < a.G; g++) {
+        const float v = __shfl_sync(0xffffffffu, gs, g);
+        ahead += v > gs || (v == gs && g < lane);
+      }
+      keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
+      kept = false;
+      in = lane < a.G && ahead == a.tg - 1 ? gs : -INFINITY;
+      out = lane < a.G && ahead == a.tg ? gs : -INFINITY;
     }
-    int ahead = 0;
-    for (int g = 0; g < a.G; g++) {
-      const float v = __shfl_sync(0xffffffffu, gs, g);
-      ahead += v > gs || (v == gs && g < lane);
-    }
-    const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
     if (by_score && a.tg < a.G) {
       // the weakest group kept against the strongest left out; a sum of two
       // has twice the error and its own rounding, and |c| of each term counts
       uint32_t mag = 0u;
 #pragma unroll
       for (int i = 0; i < PER; i++)
-        if (scored && key[i] != 0u) mag = max(mag, __float_as_uint(fabsf(c[i])));
+        if (scored && key[i] != 0ull) mag = max(mag, __float_as_uint(fabsf(c[i])));
       const float cmax = __uint_as_float(__reduce_max_sync(0xffffffffu, mag));
-      const float in = lane < a.G && ahead == a.tg - 1 ? gs : -INFINITY;
-      const float out = lane < a.G && ahead == a.tg ? gs : -INFINITY;
       const float vin = unordered(__reduce_max_sync(0xffffffffu, ordered(in)));
       const float vout = unordered(__reduce_max_sync(0xffffffffu, ordered(out)));
       close = vout > -INFINITY && !(vin - vout > 2.0f * unit * (smax + cmax));
     }
 #pragma unroll
     for (int i = 0; i < PER; i++)
-      if (e0 + i < a.E && !((keep >> ((e0 + i) / per)) & 1u)) key[i] = 0u;
+      if (a.whole ? !kept : (i < have && !((keep >> ((e0 + i) / per)) & 1u))) key[i] = 0ull;
   }
   // the k best, and one more where fp32 may have erred
+  sort_down<PER>(key);
   int my_id = -1;
-  float my_s = 0.0f, my_l = 0.0f;
   uint32_t my_key = 0u;
   const int rounds = scored ? a.k + 1 : a.k;
   for (int j = 0; j < rounds; j++) {
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < PER; i++) best = max(best, key[i]);
-    const uint32_t v = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t head = (uint32_t)(key[0] >> 32);
+    const uint32_t v = __reduce_max_sync(0xffffffffu, head);
     if (v == 0u) break;
-    const int owner = __ffs((int)__ballot_sync(0xffffffffu, best == v)) - 1;
-    int id = 0;
-    float sv = 0.0f, lv = 0.0f;
-    bool done = false;
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, head == v)) - 1;
+    const int id = __shfl_sync(0xffffffffu, e0 + 31 - (int)(uint32_t)key[0], owner);
+    if (lane == owner) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-      const bool hit = !done && key[i] == v;
-      if (hit) {
-        id = e0 + i;
-        sv = s[i];
-        lv = l[i];
-        if (lane == owner) key[i] = 0u;
-      }
-      done |= hit;
+      for (int i = 0; i + 1 < PER; i++) key[i] = key[i + 1];
+      key[PER - 1] = 0ull;
     }
-    id = __shfl_sync(0xffffffffu, id, owner);
-    sv = __shfl_sync(0xffffffffu, sv, owner);
-    lv = __shfl_sync(0xffffffffu, lv, owner);
     if (lane == j) {
       my_id = id;
-      my_s = sv;
-      my_l = lv;
       my_key = v;
     }
+  }
+  float my_l = 0.0f, my_s = 0.0f;
+  if (my_id >= 0) {
+    my_l = load_logit<LT>(a.logits, row * a.ld + my_id);
+    my_s = a.sigmoid ? 1.0f / (1.0f + expf(-my_l)) : expf(my_l - top) / z;
   }
   if (scored) {
     const uint32_t nk = __shfl_down_sync(0xffffffffu, my_key, 1);
@@ -297,15 +395,15 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     const int ni = __shfl_down_sync(0xffffffffu, my_id, 1);
     if (lane < a.k && my_key != 0u && nk != 0u) {
       const float v0 = unordered(my_key), v1 = unordered(nk);
-      // equal logit and bias: equal values, rightly decided by index
-      const bool same = my_l == nl && a.bias[my_id] == a.bias[ni];
-      close |= !same && !(v0 - v1 > unit * fmaxf(smax, fmaxf(fabsf(v0), fabsf(v1))));
+      if (!(v0 - v1 > unit * fmaxf(smax, fmaxf(fabsf(v0), fabsf(v1)))))
+        // equal logit and bias: equal values, rightly decided by index
+        close |= !(my_l == nl && a.bias[my_id] == a.bias[ni]);
     }
   }
   float sum = lane < a.k ? my_s : 0.0f;
   if (a.renorm) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);  // k <= 16: lanes 0 .. 15
     // scores near fp32's smallest: their ratios need the wider exponent
     close |= sum < 1e-30f && lane < a.k && my_id >= 0;
   }
@@ -321,12 +419,19 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
 
 int64_t g_select_launches = 0;
 
+template <typename LT, int PER>
+cudaError_t launch_per(const LaunchCtx& lc, SelArgs a) {
+  const unsigned grid = (unsigned)((a.n + kSelWarps - 1) / kSelWarps);
+  const uintptr_t run = std::min<uintptr_t>(16, PER * sizeof(LT)), brun = std::min<uintptr_t>(16, PER * 4);
+  a.vec = reinterpret_cast<uintptr_t>(a.logits) % run == 0 && a.ld * (int64_t)sizeof(LT) % (int64_t)run == 0;
+  a.bvec = reinterpret_cast<uintptr_t>(a.bias) % brun == 0;
+  const int per = a.E / a.G, lanes = per / PER;
+  a.whole = per % PER == 0 && (lanes & (lanes - 1)) == 0;
+  return launch_k(lc, k_route_select<LT, PER>, grid, kSelWarps * 32, 0, a);
+}
 template <typename LT>
 cudaError_t launch_select(const LaunchCtx& lc, const SelArgs& a) {
-  const unsigned grid = (unsigned)((a.n + kSelWarps - 1) / kSelWarps);
-  if (a.E <= 64) return launch_k(lc, k_route_select<LT, 2>, grid, kSelWarps * 32, 0, a);
-  if (a.E <= 128) return launch_k(lc, k_route_select<LT, 4>, grid, kSelWarps * 32, 0, a);
-  return launch_k(lc, k_route_select<LT, 8>, grid, kSelWarps * 32, 0, a);
+  return a.E <= 64 ? launch_per<LT, 2>(lc, a) : a.E <= 128 ? launch_per<LT, 4>(lc, a) : launch_per<LT, 8>(lc, a);
 }
 
 }  // namespace
@@ -352,7 +457,7 @@ extern "C" int afd_route_select(const void* logits, int64_t ld, int n_tokens, in
   int rc = check_device_ptrs({logits, bias, ids, weights});
   if (rc) return rc;
   const SelArgs a{logits, ld, bias, ids, weights, n_tokens, num_experts, topk,
-                  score == AFD_SCORE_SIGMOID, n_groups, topk_groups, group_top, renorm != 0, routed_scaling};
+                  score == AFD_SCORE_SIGMOID, n_groups, topk_groups, group_top, renorm != 0, routed_scaling, 0, 0, 0};
   const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, &g_select_launches};
   const cudaError_t e = logits_dtype == AFD_DTYPE_F32 ? launch_select<float>(lc, a) : launch_select<uint16_t>(lc, a);
   if (e != cudaSuccess) {

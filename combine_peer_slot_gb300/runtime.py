@@ -311,95 +311,135 @@ class RankSet:
 
 
 # ---- routing choice and MXFP4 on torch tensors ----------------------------------
-def _act_code(dtype):
-    import torch
-    if dtype is torch.bfloat16:
-        return A.AFD_DTYPE_BF16
-    if dtype is torch.float32:
-        return A.AFD_DTYPE_F32
-    raise A.AfdError(A.AFD_ERR_ARG, f"dtype {dtype}: bfloat16 or float32 wanted")
+# These calls are short: at decode sizes the host's own work is most of their
+# time, so the checks are few and plain, and the library's functions, the
+# current stream's handle and the scratch come without intermediate layers.
+class _Host:
+    """torch, the dtypes' codes, the library's functions: looked up once."""
+
+    def __init__(self):
+        import torch
+        self.empty = torch.empty
+        self.int32, self.uint8, self.f32, self.bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+        self.code = {torch.bfloat16: A.AFD_DTYPE_BF16, torch.float32: A.AFD_DTYPE_F32}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        L = A.lib()
+        self.select, self.quantize, self.dequantize = L.afd_route_select, L.afd_mx4_quantize, L.afd_mx4_dequantize
+        self.gemm, self.ffn, self.ffn_workspace = L.afd_mx4_gemm, L.afd_mx4_ffn, L.afd_mx4_ffn_workspace
 
 
-def _stream(t):
-    """The current stream of t's device; t must live on the current device
-    (the library launches there)."""
-    import torch
-    if t.device.type != "cuda":
+_host = None
+
+
+def _get():
+    global _host
+    if _host is None:
+        _host = _Host()
+    return _host
+
+
+def _bad(what):
+    raise A.AfdError(A.AFD_ERR_ARG, what)
+
+
+def _device(t):
+    """t's device and the handle of its current stream.  t has to live on the
+    current device, where the library launches (it refuses other pointers)."""
+    if not t.is_cuda:
         raise A.AfdError(A.AFD_ERR_NOT_DEVICE, "a CUDA tensor is wanted")
-    return torch.cuda.current_stream(t.device).cuda_stream
+    d = t.device
+    return d, _host.raw_stream(d.index)
 
 
-def _want(ok, what):
-    if not ok:
-        raise A.AfdError(A.AFD_ERR_ARG, what)
+def _rows_int32(h, t, n, what):
+    if t.dtype is not h.int32 or t.dim() != 1 or not t.is_contiguous() or (n >= 0 and t.shape[0] != n):
+        _bad(f"{what}: contiguous int32 vector" + (f" of {n} wanted" if n >= 0 else " wanted"))
 
 
-def _int32_vector(t, what):
-    import torch
-    _want(t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous(), f"{what}: int32 vector wanted")
-    return t
+_SCORES = {"softmax": A.AFD_SCORE_SOFTMAX, "sigmoid": A.AFD_SCORE_SIGMOID}
+_RULES = {"floor": A.AFD_MX4_SCALE_FLOOR, "ceil": A.AFD_MX4_SCALE_CEIL}
 
 
 def route_select(logits, topk, bias=None, score="softmax", n_groups=1, topk_groups=1, group_top=1,
                  renorm=False, routed_scaling=1.0):
     """afd_route_select of logits [T, E] (bf16 or fp32, any row pitch):
     (ids int32 [T, topk], weights fp32 [T, topk])."""
-    import torch
-    _want(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), "logits: rows [T, E] wanted")
+    h = _host or _get()
+    code = h.code.get(logits.dtype)
+    if code is None or logits.dim() != 2 or score not in _SCORES:
+        _bad("logits: bf16 or fp32 rows [T, E] wanted, score softmax or sigmoid")
     T, E = logits.shape
+    ld, step = logits.stride()
+    if step != 1 and E > 1:
+        _bad("logits: rows of neighbouring elements wanted")
+    bias_ptr = 0
     if bias is not None:
-        _want(bias.dtype is torch.float32 and bias.shape == (E,) and bias.is_contiguous(),
-              "bias: fp32 [E] wanted")
-    _want(score in ("softmax", "sigmoid"), f"score {score!r}")
-    ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    A._check(A.afd_route_select(logits.data_ptr(), logits.stride(0) if T > 1 else E, T, _act_code(logits.dtype),
-                                0 if bias is None else bias.data_ptr(), E, topk,
-                                A.AFD_SCORE_SIGMOID if score == "sigmoid" else A.AFD_SCORE_SOFTMAX,
-                                n_groups, topk_groups, group_top, renorm, routed_scaling,
-                                ids.data_ptr(), weights.data_ptr(), _stream(logits)),
-             "afd_route_select")
+        if bias.dtype is not h.f32 or bias.shape != (E,) or not bias.is_contiguous():
+            _bad("bias: contiguous fp32 [E] wanted")
+        bias_ptr = bias.data_ptr()
+    dev, stream = _device(logits)
+    ids = h.empty((T, topk), dtype=h.int32, device=dev)
+    weights = h.empty((T, topk), dtype=h.f32, device=dev)
+    rc = h.select(logits.data_ptr(), ld if T > 1 else E, T, code, bias_ptr, E, topk, _SCORES[score], n_groups,
+                  topk_groups, group_top, 1 if renorm else 0, routed_scaling, ids.data_ptr(), weights.data_ptr(),
+                  stream)
+    if rc:
+        raise A.AfdError(rc, "afd_route_select")
     return ids, weights
 
 
 class Mx4:
     """MXFP4 rows: codes uint8 [rows, cols / 2], scales uint8 [rows, cols / 32]."""
+    __slots__ = ("codes", "scales", "rows", "cols")
 
     def __init__(self, codes, scales):
-        import torch
-        _want(codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.dim() == 2
-              and codes.is_contiguous() and scales.is_contiguous()
-              and codes.shape[1] % 16 == 0 and scales.shape == (codes.shape[0], codes.shape[1] // 16),
-              "MXFP4: contiguous uint8 codes [rows, cols / 2] and scales [rows, cols / 32] wanted")
-        self.codes, self.scales = codes, scales
-        self.rows, self.cols = codes.shape[0], 2 * codes.shape[1]
+        h = _host or _get()
+        rows, half = codes.shape if codes.dim() == 2 else _bad("codes: [rows, cols / 2] wanted")
+        if (codes.dtype is not h.uint8 or scales.dtype is not h.uint8 or half % 16
+                or scales.shape != (rows, half // 16) or not codes.is_contiguous() or not scales.is_contiguous()):
+            _bad("MXFP4: contiguous uint8 codes [rows, cols / 2] and scales [rows, cols / 32] wanted")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, 2 * half
 
 
 def mx4_quantize(x, src_rows=None, topk=1, rule="floor"):
     """afd_mx4_quantize of x [rows, cols] (bf16 or fp32, any 16-byte row
     pitch); src_rows int32 [n]: row r codes x[src_rows[r] // topk]."""
-    import torch
-    _want(x.dim() == 2 and x.shape[1] % 32 == 0 and x.stride(1) == 1, "x: rows [n, 32 m] wanted")
-    _want(rule in ("floor", "ceil"), f"rule {rule!r}")
-    n = x.shape[0] if src_rows is None else _int32_vector(src_rows, "src_rows").numel()
-    q = Mx4(torch.empty((n, x.shape[1] // 2), dtype=torch.uint8, device=x.device),
-            torch.empty((n, x.shape[1] // 32), dtype=torch.uint8, device=x.device))
-    A._check(A.afd_mx4_quantize(x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1], x.shape[0],
-                                x.shape[1], _act_code(x.dtype),
-                                0 if src_rows is None else src_rows.data_ptr(), topk, n,
-                                A.AFD_MX4_SCALE_CEIL if rule == "ceil" else A.AFD_MX4_SCALE_FLOOR,
-                                q.codes.data_ptr(), q.scales.data_ptr(), _stream(x)),
-             "afd_mx4_quantize")
+    h = _host or _get()
+    code = h.code.get(x.dtype)
+    if code is None or x.dim() != 2 or rule not in _RULES:
+        _bad("x: bf16 or fp32 rows wanted, rule floor or ceil")
+    n_x, cols = x.shape
+    ld, step = x.stride()
+    if cols % 32 or step != 1:
+        _bad("x: rows of 32 m neighbouring elements wanted")
+    n, src = n_x, 0
+    if src_rows is not None:
+        _rows_int32(h, src_rows, -1, "src_rows")
+        n, src = src_rows.shape[0], src_rows.data_ptr()
+    dev, stream = _device(x)
+    q = Mx4.__new__(Mx4)
+    q.codes = codes = h.empty((n, cols // 2), dtype=h.uint8, device=dev)
+    q.scales = scales = h.empty((n, cols // 32), dtype=h.uint8, device=dev)
+    q.rows, q.cols = n, cols
+    rc = h.quantize(x.data_ptr(), ld if n_x > 1 else cols, n_x, cols, code, src, topk, n, _RULES[rule],
+                    codes.data_ptr(), scales.data_ptr(), stream)
+    if rc:
+        raise A.AfdError(rc, "afd_mx4_quantize")
     return q
 
 
 def mx4_dequantize(q, dtype):
     """The values of q as a tensor [rows, cols] of dtype (bf16 or fp32)."""
-    import torch
-    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    A._check(A.afd_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
-                                  _act_code(dtype), out.data_ptr(), q.cols, _stream(q.codes)),
-             "afd_mx4_dequantize")
+    h = _host or _get()
+    code = h.code.get(dtype)
+    if code is None:
+        _bad(f"dtype {dtype}: bfloat16 or float32 wanted")
+    dev, stream = _device(q.codes)
+    out = h.empty((q.rows, q.cols), dtype=dtype, device=dev)
+    rc = h.dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, code, out.data_ptr(), q.cols, stream)
+    if rc:
+        raise A.AfdError(rc, "afd_mx4_dequantize")
     return out
 
 
@@ -408,60 +448,75 @@ class Mx4Weight:
     uint8 [E, M, K / 32]) packed for the product; the inputs are not kept."""
 
     def __init__(self, codes, scales, swiglu=False):
-        import torch
-        _want(codes.dim() == 3 and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
-              and codes.is_contiguous() and scales.is_contiguous()
-              and scales.shape == (*codes.shape[:2], codes.shape[2] // 16),
-              "weight: contiguous uint8 codes [E, M, K / 2] and scales [E, M, K / 32] wanted")
+        h = _host or _get()
+        if (codes.dim() != 3 or codes.dtype is not h.uint8 or scales.dtype is not h.uint8
+                or not codes.is_contiguous() or not scales.is_contiguous()
+                or scales.shape != (*codes.shape[:2], codes.shape[2] // 16)):
+            _bad("weight: contiguous uint8 codes [E, M, K / 2] and scales [E, M, K / 32] wanted")
         self.experts, self.M, self.K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
         self.swiglu = bool(swiglu)
         nbytes = A.afd_mx4_weight_bytes(self.experts, self.M, self.K, self.swiglu)
-        _want(nbytes > 0, f"weight dimensions {(self.experts, self.M, self.K)}")
-        self.packed = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        if nbytes <= 0:
+            _bad(f"weight dimensions {(self.experts, self.M, self.K)}")
+        dev, stream = _device(codes)
+        self.packed = h.empty(nbytes, dtype=h.uint8, device=dev)
         A._check(A.afd_mx4_pack_weight(codes.data_ptr(), scales.data_ptr(), self.experts, self.M, self.K,
-                                       self.swiglu, self.packed.data_ptr(), nbytes, _stream(codes)),
+                                       self.swiglu, self.packed.data_ptr(), nbytes, stream),
                  "afd_mx4_pack_weight")
+
+
+def _output(h, x, cols, out_dtype, out, dev):
+    """(out, its row pitch, the dtype's code)"""
+    if out is None:
+        out_dtype = h.bf16 if out_dtype is None else out_dtype
+        code = h.code.get(out_dtype)
+        if code is None:
+            _bad(f"out_dtype {out_dtype}: bfloat16 or float32 wanted")
+        return h.empty((x.rows, cols), dtype=out_dtype, device=dev), cols, code
+    code = h.code.get(out.dtype)
+    if code is None or out.shape != (x.rows, cols) or out.stride(1) != 1 or out_dtype not in (None, out.dtype):
+        _bad("out: bf16 or fp32 [rows, columns] wanted")
+    return out, out.stride(0) if x.rows > 1 else cols, code
 
 
 def mx4_gemm(x, offsets, weight, out_dtype=None, out=None):
     """afd_mx4_gemm of the rows x (Mx4) grouped by offsets int32 [E + 1] with
     weight (Mx4Weight): [rows, M], or [rows, M / 2] = silu(gate) * up for a
     swiglu weight.  Rows in no group are not written (out: the caller's)."""
-    import torch
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    _want(_int32_vector(offsets, "offsets").numel() == weight.experts + 1, "offsets: int32 [E + 1] wanted")
-    _want(x.cols == weight.K, f"rows of {x.cols} columns, weight of {weight.K}")
-    cols = weight.M // 2 if weight.swiglu else weight.M
-    if out is None:
-        out = torch.empty((x.rows, cols), dtype=out_dtype, device=x.codes.device)
-    _want(out.shape == (x.rows, cols) and out.stride(1) == 1 and out.dtype is out_dtype, "out")
-    A._check(A.afd_mx4_gemm(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(),
-                            weight.experts, weight.packed.data_ptr(), weight.M, weight.K, weight.swiglu,
-                            _act_code(out_dtype), out.data_ptr(), out.stride(0) if x.rows > 1 else cols,
-                            _stream(x.codes)),
-             "afd_mx4_gemm")
+    h = _host or _get()
+    _rows_int32(h, offsets, weight.experts + 1, "offsets")
+    if x.cols != weight.K:
+        _bad(f"rows of {x.cols} columns, weight of {weight.K}")
+    dev, stream = _device(x.codes)
+    out, ldo, code = _output(h, x, weight.M // 2 if weight.swiglu else weight.M, out_dtype, out, dev)
+    rc = h.gemm(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), weight.experts,
+                weight.packed.data_ptr(), weight.M, weight.K, 1 if weight.swiglu else 0, code, out.data_ptr(), ldo,
+                stream)
+    if rc:
+        raise A.AfdError(rc, "afd_mx4_gemm")
     return out
 
 
 def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
     """afd_mx4_ffn: the expert FFN of the grouped rows x (Mx4) with w13 (a
     swiglu Mx4Weight [E, 2 inter, hidden]) and wd ([E, hidden, inter])."""
-    import torch
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    h = _host or _get()
     hidden, inter = wd.M, wd.K
-    _want(w13.swiglu and not wd.swiglu and w13.experts == wd.experts and w13.K == hidden
-          and w13.M == 2 * inter and x.cols == hidden, "w13 / wd / x dimensions do not match")
-    _want(_int32_vector(offsets, "offsets").numel() == wd.experts + 1, "offsets: int32 [E + 1] wanted")
-    if out is None:
-        out = torch.empty((x.rows, hidden), dtype=out_dtype, device=x.codes.device)
-    _want(out.shape == (x.rows, hidden) and out.stride(1) == 1 and out.dtype is out_dtype, "out")
+    if (not w13.swiglu or wd.swiglu or w13.experts != wd.experts or w13.K != hidden or w13.M != 2 * inter
+            or x.cols != hidden):
+        _bad("w13 / wd / x dimensions do not match")
+    _rows_int32(h, offsets, wd.experts + 1, "offsets")
+    dev, stream = _device(x.codes)
+    out, ldo, code = _output(h, x, hidden, out_dtype, out, dev)
+    need = h.ffn_workspace(x.rows, inter)
     if workspace is None:
-        workspace = torch.empty(max(A.afd_mx4_ffn_workspace(x.rows, inter), 1), dtype=torch.uint8,
-                                device=x.codes.device)
-    A._check(A.afd_mx4_ffn(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), wd.experts,
-                           w13.packed.data_ptr(), wd.packed.data_ptr(), hidden, inter,
-                           _act_code(out_dtype), out.data_ptr(), out.stride(0) if x.rows > 1 else hidden,
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           _stream(x.codes)),
-             "afd_mx4_ffn")
+        workspace = h.empty(max(need, 1), dtype=h.uint8, device=dev)
+        have = need
+    else:
+        have = workspace.numel() * workspace.element_size()
+    rc = h.ffn(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), wd.experts,
+               w13.packed.data_ptr(), wd.packed.data_ptr(), hidden, inter, code, out.data_ptr(), ldo,
+               workspace.data_ptr(), have, stream)
+    if rc:
+        raise A.AfdError(rc, "afd_mx4_ffn")
     return out
