@@ -20,7 +20,6 @@
 namespace {
 
 constexpr int kSelWarps = 8;
-constexpr int kMaxPer = 8;  // experts per lane: 32 * 8 = 256
 
 struct SelArgs {
   const void* logits;
@@ -32,7 +31,12 @@ struct SelArgs {
   float scale;
   int vec, bvec;  // logits rows / bias: a lane's run of experts can be loaded whole
   int whole;      // an expert group is a power of two of lanes
+  uint32_t gmagic;  // 65536 / (experts per group) + 1
 };
+
+// expert group of expert e < 256: e / per by multiplication, exact for all
+// e, per <= 256 (e gmagic / 65536 is over e / per by at most e / 65536 < 1 / per)
+__device__ __forceinline__ int group_of(const SelArgs& a, int e) { return (int)((uint32_t)e * a.gmagic >> 16); }
 
 // order-preserving map of the fp32 values to unsigned (NaN excluded), with
 // -inf at 0x007fffff; 0 is below every value.  v + 0 turns -0 into +0.
@@ -53,99 +57,6 @@ __device__ __forceinline__ float load_logit<float>(const void* p, int64_t i) {
 template <>
 __device__ __forceinline__ float load_logit<uint16_t>(const void* p, int64_t i) {
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
-}
-
-// One row decided in fp64, by one warp; expert e = lane + 32 m.
-template <typename LT>
-__device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lane) {
-  const int64_t l0 = row * a.ld;
-  double top = -INFINITY;
-  for (int e = lane; e < a.E; e += 32) top = fmax(top, (double)load_logit<LT>(a.logits, l0 + e));
-  for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-  double z = 0.0, s[kMaxPer], c[kMaxPer];
-  for (int m = 0; m < kMaxPer; m++) {
-    const int e = lane + 32 * m;
-    s[m] = 0.0;
-    c[m] = -INFINITY;
-    if (e >= a.E) continue;
-    const double l = (double)load_logit<LT>(a.logits, l0 + e);
-    if (l == -INFINITY) continue;
-    s[m] = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top);
-    z += s[m];
-  }
-  for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  for (int m = 0; m < kMaxPer; m++) {
-    const int e = lane + 32 * m;
-    if (e >= a.E || load_logit<LT>(a.logits, l0 + e) == -INFINITY) continue;
-    if (!a.sigmoid) s[m] /= z;
-    c[m] = a.bias ? s[m] + (double)a.bias[e] : (double)load_logit<LT>(a.logits, l0 + e);
-  }
-  if (a.G > 1) {
-    const int per = a.E / a.G;
-    double gs = -INFINITY;  // lane g: group g
-    for (int g = 0; g < a.G; g++) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      for (int m = 0; m < kMaxPer; m++) {
-        const int e = lane + 32 * m;
-        if (e >= a.E || e / per != g) continue;
-        const double v = c[m] > -INFINITY && !a.bias && a.gtop == 2 ? s[m] : c[m];
-        m2 = fmax(m2, fmin(m1, v));
-        m1 = fmax(m1, v);
-      }
-      for (int o = 16; o; o >>= 1) {
-        const double o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
-        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-        m1 = fmax(m1, o1);
-      }
-      if (lane == g) gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
-    }
-    int ahead = 0;
-    for (int g = 0; g < a.G; g++) {
-      const double v = __shfl_sync(0xffffffffu, gs, g);
-      ahead += v > gs || (v == gs && g < lane);
-    }
-    const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
-    for (int m = 0; m < kMaxPer; m++) {
-      const int e = lane + 32 * m;
-      if (e < a.E && !((keep >> (e / per)) & 1u)) c[m] = -INFINITY;
-    }
-  }
-  int my_id = -1;
-  double my_s = 0.0;
-  for (int j = 0; j < a.k; j++) {
-    double best = -INFINITY, bs = 0.0;
-    int bi = 0x7fffffff;
-    for (int m = 0; m < kMaxPer; m++)
-      if (c[m] > best) {
-        best = c[m];
-        bs = s[m];
-        bi = lane + 32 * m;
-      }
-    for (int o = 16; o; o >>= 1) {
-      const double ov = __shfl_xor_sync(0xffffffffu, best, o), os = __shfl_xor_sync(0xffffffffu, bs, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (ov > best || (ov == best && oi < bi)) {
-        best = ov;
-        bs = os;
-        bi = oi;
-      }
-    }
-    if (best == -INFINITY) break;
-    if (lane == (bi & 31)) c[bi >> 5] = -INFINITY;
-    if (lane == j) {
-      my_id = bi;
-      my_s = bs;
-    }
-  }
-  if (a.renorm) {
-    double sum = my_s;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (sum > 0.0) my_s /= sum;
-  }
-  if (lane < a.k) {
-    a.ids[row * a.k + lane] = my_id;
-    a.w[row * a.k + lane] = (float)(my_s * (double)a.scale);
-  }
 }
 
 // PER consecutive values, 16 bytes at a time where the row allows it
@@ -218,12 +129,203 @@ __device__ __forceinline__ void merge_two(float& m1, float& m2, int o) {
   m1 = fmaxf(m1, o1);
 }
 
+// Contenders of one row: experts whose place fp32 cannot settle, with their
+// exact values.
+struct Contenders {
+  uint8_t id[256];
+  double v[256];
+};
+
+// Every lane's marked experts to the list, ascending; returns their number.
+template <int PER>
+__device__ __forceinline__ int gather_marked(Contenders& q, uint32_t marked, int e0, int lane) {
+  int before = __popc(marked);
+  const int mine = before;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const int n = __shfl_sync(0xffffffffu, before, 31);
+  int at = before - mine;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; i++)
+    if ((marked >> i) & 1u) q.id[at++] = (uint8_t)(e0 + i);
+  __syncwarp();
+  return n;
+}
+
+// One row decided by its exact scores, by one warp: fp32 picks the few
+// contenders (all within the fp32 errors of the border), one lane each
+// computes their fp64 values, and those are ranked.  fp64 for every expert
+// took 22 to 45 us for the one row in hundreds that needs it, which then
+// was the time of the launch.
+template <typename LT, int PER>
+__device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lane, Contenders& q) {
+  const int64_t l0 = row * a.ld;
+  const int e0 = lane * PER;
+  const bool scored = a.bias != nullptr, by_score = scored || (a.G > 1 && a.gtop == 2);
+  float l[PER], s[PER], c[PER];
+  uint32_t open = 0u;
+  float top = -INFINITY, cmax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    l[i] = e0 + i < a.E ? load_logit<LT>(a.logits, l0 + e0 + i) : -INFINITY;
+    top = fmaxf(top, l[i]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  double z = 1.0;
+  if (!a.sigmoid) {
+    z = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+      if (l[i] > -INFINITY) z += exp((double)l[i] - (double)top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  auto score64 = [&](int e) {
+    const double x = (double)load_logit<LT>(a.logits, l0 + e);
+    return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top) / z;
+  };
+  // exact value of expert e: what experts are chosen by, or (rank) what groups are ranked by
+  auto value64 = [&](int e, bool rank) {
+    if (scored) return score64(e) + (double)a.bias[e];
+    return rank && by_score ? score64(e) : (double)load_logit<LT>(a.logits, l0 + e);
+  };
+  const float rz = (float)(1.0 / z);
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    s[i] = 0.0f;
+    c[i] = l[i];
+    if (l[i] > -INFINITY) {
+      if (by_score) s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top) * rz;
+      if (scored) c[i] = s[i] + a.bias[e0 + i];
+      if (c[i] > -INFINITY) {
+        open |= 1u << i;
+        cmax = fmaxf(cmax, fabsf(c[i]));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+  // over what two fp32 values may be off together (see the kernel); without scores they are exact
+  const float tol = by_score ? (a.sigmoid ? 2.0f * 9.5367431640625e-07f : 2.0f * 3.814697265625e-06f) *
+                                   ((a.sigmoid ? 1.0f : rz) + (scored ? cmax : 0.0f))
+                             : 0.0f;
+  if (a.G > 1) {
+    uint32_t marked = 0u;
+    int grp[PER];
+    float rv[PER];  // what groups are ranked by
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      grp[i] = (open >> i) & 1u ? group_of(a, e0 + i) : -1;
+      rv[i] = scored || !by_score ? c[i] : s[i];
+    }
+    for (int g = 0; g < a.G; g++) {
+      float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; i++) {
+        const float v = grp[i] == g ? rv[i] : -INFINITY;
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) merge_two(m1, m2, o);
+      const float border = (a.gtop == 2 ? m2 : m1) - tol;
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (grp[i] == g && !(rv[i] < border)) marked |= 1u << i;
+    }
+    const int n = gather_marked<PER>(q, marked, e0, lane);
+    for (int i = lane; i < n; i += 32) q.v[i] = value64(q.id[i], true);
+    __syncwarp();
+    double gs = -INFINITY;  // lane g: group g
+    if (lane < a.G) {
+      double m1 = -INFINITY, m2 = -INFINITY;
+      for (int i = 0; i < n; i++)
+        if (group_of(a, q.id[i]) == lane) {
+          const double v = q.v[i];
+          if (v > m1) {
+            m2 = m1;
+            m1 = v;
+          } else if (v > m2) {
+            m2 = v;
+          }
+        }
+      gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+    }
+    int ahead = 0;
+    for (int g = 0; g < a.G; g++) {
+      const double v = __shfl_sync(0xffffffffu, gs, g);
+      ahead += v > gs || (v == gs && g < lane);
+    }
+    const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+      if (((open >> i) & 1u) && !((keep >> grp[i]) & 1u)) open &= ~(1u << i);
+  }
+  // the k-th largest fp32 value, and everything not clearly below it
+  uint32_t left = open, kth = 0u;
+  for (int j = 0; j < a.k; j++) {
+    uint32_t best = 0u;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      const uint32_t o = (left >> i) & 1u ? ordered(c[i]) : 0u;
+      if (o > best) {
+        best = o;
+        bi = i;
+      }
+    }
+    kth = __reduce_max_sync(0xffffffffu, best);
+    if (kth == 0u) break;
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, best == kth)) - 1;
+    if (lane == owner) left &= ~(1u << bi);
+  }
+  const float border = kth ? unordered(kth) - tol : -INFINITY;
+  uint32_t marked = 0u;
+#pragma unroll
+  for (int i = 0; i < PER; i++)
+    if (((open >> i) & 1u) && !(c[i] < border)) marked |= 1u << i;
+  const int n = gather_marked<PER>(q, marked, e0, lane);
+  for (int i = lane; i < n; i += 32) q.v[i] = value64(q.id[i], false);
+  __syncwarp();
+  int my_id = -1;  // lane j: the j-th choice
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    int place = 32;
+    if (i < n) {
+      const double v = q.v[i];
+      place = 0;
+      for (int j = 0; j < n; j++) place += q.v[j] > v || (q.v[j] == v && j < i);
+    }
+    for (int j = 0; j < a.k; j++) {
+      const uint32_t who = __ballot_sync(0xffffffffu, place == j);
+      if (who && lane == j) my_id = q.id[i0 + __ffs((int)who) - 1];
+    }
+  }
+  double my_s = my_id >= 0 ? score64(my_id) : 0.0;
+  if (a.renorm) {
+    double sum = my_s;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (sum > 0.0) my_s /= sum;
+  }
+  if (lane < a.k) {
+    a.ids[row * a.k + lane] = my_id;
+    a.w[row * a.k + lane] = (float)(my_s * (double)a.scale);
+  }
+}
+
 // One warp per row; lane l holds experts [l * PER, (l + 1) * PER), so the
 // lowest lane of a tie holds the lowest index.  A lane sorts its own values
 // once; each choice is then one warp-wide integer maximum of the lanes'
 // heads, and the owner moves to its next value.
 template <typename LT, int PER>
 __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_constant__ SelArgs a) {
+  __shared__ Contenders contenders[kSelWarps];
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kSelWarps + (threadIdx.x >> 5);
   if (row >= a.n) return;
@@ -361,7 +463,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < PER; i++)
-      if (a.whole ? !kept : (i < have && !((keep >> ((e0 + i) / per)) & 1u))) key[i] = 0ull;
+      if (a.whole ? !kept : (i < have && !((keep >> group_of(a, e0 + i)) & 1u))) key[i] = 0ull;
   }
   // the k best, and one more where fp32 may have erred
   sort_down<PER>(key);
@@ -408,7 +510,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     close |= sum < 1e-30f && lane < a.k && my_id >= 0;
   }
   if (__any_sync(0xffffffffu, close)) {
-    choose_exact<LT>(a, row, lane);
+    choose_exact<LT, PER>(a, row, lane, contenders[threadIdx.x >> 5]);
     return;
   }
   if (lane < a.k) {
@@ -426,6 +528,7 @@ cudaError_t launch_per(const LaunchCtx& lc, SelArgs a) {
   a.vec = reinterpret_cast<uintptr_t>(a.logits) % run == 0 && a.ld * (int64_t)sizeof(LT) % (int64_t)run == 0;
   a.bvec = reinterpret_cast<uintptr_t>(a.bias) % brun == 0;
   const int per = a.E / a.G, lanes = per / PER;
+  a.gmagic = 65536u / (uint32_t)per + 1u;
   a.whole = per % PER == 0 && (lanes & (lanes - 1)) == 0;
   return launch_k(lc, k_route_select<LT, PER>, grid, kSelWarps * 32, 0, a);
 }
@@ -457,7 +560,7 @@ extern "C" int afd_route_select(const void* logits, int64_t ld, int n_tokens, in
   int rc = check_device_ptrs({logits, bias, ids, weights});
   if (rc) return rc;
   const SelArgs a{logits, ld, bias, ids, weights, n_tokens, num_experts, topk,
-                  score == AFD_SCORE_SIGMOID, n_groups, topk_groups, group_top, renorm != 0, routed_scaling, 0, 0, 0};
+                  score == AFD_SCORE_SIGMOID, n_groups, topk_groups, group_top, renorm != 0, routed_scaling, 0, 0, 0, 0};
   const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, &g_select_launches};
   const cudaError_t e = logits_dtype == AFD_DTYPE_F32 ? launch_select<float>(lc, a) : launch_select<uint16_t>(lc, a);
   if (e != cudaSuccess) {
