@@ -133,8 +133,29 @@ __device__ __forceinline__ void merge_two(float& m1, float& m2, int o) {
 // exact values.
 struct Contenders {
   uint8_t id[256];
-  double v[256];
+  int64_t v[256];  // ordered64; first, for groups, the double's bits
 };
+
+// What two fp32 values of c may be off together, u = 2^-24: kScoreErr times
+// the largest score (1 for a sigmoid, 1 / z for a softmax) and 2 u |c| for
+// adding the bias.  __expf(x) is off by 2 + 1.173 |x| ulp, __fdividef by 2.
+//   sigmoid: s (1 - s) times the exponential's (4 + 2.35 |l|) u, at most
+//   1.6 u, the sum 1 + e and the division 5 u: 6.6 u, twice 13.2 u
+//   softmax: the exponential's (4 + 3.35 d) u, d = top - l with its rounding,
+//   on s = s_max exp(-d): 5.3 u; z over 256 terms 19 u, 1 / z and the product
+//   3 u: 27 u, twice 54 u
+// The sums of two that rank groups: twice as much, each |c| twice, and the
+// two sums' roundings: kGroupErr of the largest score and 8 u max |c|.
+constexpr float kU = 5.9604644775390625e-08f;
+__device__ __forceinline__ float score_err(int sigmoid) { return sigmoid ? 14.0f * kU : 56.0f * kU; }
+__device__ __forceinline__ float group_err(int sigmoid) { return sigmoid ? 28.0f * kU : 112.0f * kU; }
+
+// fp64 to integers of the same order (NaN excluded): compared in a few cycles
+// where the fp64 pipe takes tens
+__device__ __forceinline__ int64_t ordered64(double v) {
+  const int64_t b = __double_as_longlong(v + 0.0);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
 
 // Every lane's marked experts to the list, ascending; returns their number.
 template <int PER>
@@ -159,16 +180,18 @@ __device__ __forceinline__ int gather_marked(Contenders& q, uint32_t marked, int
 // One row decided by its exact scores, by one warp: fp32 picks the few
 // contenders (all within the fp32 errors of the border), one lane each
 // computes their fp64 values, and those are ranked.  fp64 for every expert
-// took 22 to 45 us for the one row in hundreds that needs it, which then
-// was the time of the launch.
+// took 22 to 45 us for the one row in hundreds that needs it, which then was
+// the time of the launch.  open: this lane's experts that may be chosen;
+// border: the k-th largest fp32 value among them; both only where the groups
+// are settled (or there are none), else the groups are ranked here first.
 template <typename LT, int PER>
-__device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lane, Contenders& q) {
+__device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lane, Contenders& q, bool settled,
+                                          uint32_t open, float border) {
   const int64_t l0 = row * a.ld;
   const int e0 = lane * PER;
   const bool scored = a.bias != nullptr, by_score = scored || (a.G > 1 && a.gtop == 2);
   float l[PER], s[PER], c[PER];
-  uint32_t open = 0u;
-  float top = -INFINITY, cmax = 0.0f;
+  float top = -INFINITY, cmax = 0.0f, zf = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
     l[i] = e0 + i < a.E ? load_logit<LT>(a.logits, l0 + e0 + i) : -INFINITY;
@@ -184,6 +207,7 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
       if (l[i] > -INFINITY) z += exp((double)l[i] - (double)top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    zf = (float)z;
   }
   auto score64 = [&](int e) {
     const double x = (double)load_logit<LT>(a.logits, l0 + e);
@@ -194,110 +218,113 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
     if (scored) return score64(e) + (double)a.bias[e];
     return rank && by_score ? score64(e) : (double)load_logit<LT>(a.logits, l0 + e);
   };
-  const float rz = (float)(1.0 / z);
+  const float smax = a.sigmoid ? 1.0f : 1.0f / zf;
+  uint32_t all = 0u;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
     s[i] = 0.0f;
     c[i] = l[i];
     if (l[i] > -INFINITY) {
-      if (by_score) s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top) * rz;
+      if (by_score) s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top) * smax;
       if (scored) c[i] = s[i] + a.bias[e0 + i];
       if (c[i] > -INFINITY) {
-        open |= 1u << i;
+        all |= 1u << i;
         cmax = fmaxf(cmax, fabsf(c[i]));
       }
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-  // over what two fp32 values may be off together (see the kernel); without scores they are exact
-  const float tol = by_score ? (a.sigmoid ? 2.0f * 9.5367431640625e-07f : 2.0f * 3.814697265625e-06f) *
-                                   ((a.sigmoid ? 1.0f : rz) + (scored ? cmax : 0.0f))
-                             : 0.0f;
-  if (a.G > 1) {
-    uint32_t marked = 0u;
-    int grp[PER];
-    float rv[PER];  // what groups are ranked by
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-      grp[i] = (open >> i) & 1u ? group_of(a, e0 + i) : -1;
-      rv[i] = scored || !by_score ? c[i] : s[i];
-    }
-    for (int g = 0; g < a.G; g++) {
-      float m1 = -INFINITY, m2 = -INFINITY;
+  const float tol = by_score ? score_err(a.sigmoid) * smax + (scored ? 2.0f * kU * cmax : 0.0f) : 0.0f;
+  if (!settled) {
+    open = all;
+    if (a.G > 1) {
+      uint32_t marked = 0u;
+      int grp[PER];
+      float rv[PER];  // what groups are ranked by
 #pragma unroll
       for (int i = 0; i < PER; i++) {
-        const float v = grp[i] == g ? rv[i] : -INFINITY;
-        m2 = fmaxf(m2, fminf(m1, v));
-        m1 = fmaxf(m1, v);
+        grp[i] = (open >> i) & 1u ? group_of(a, e0 + i) : -1;
+        rv[i] = scored || !by_score ? c[i] : s[i];
       }
+      for (int g = 0; g < a.G; g++) {
+        float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) merge_two(m1, m2, o);
-      const float border = (a.gtop == 2 ? m2 : m1) - tol;
+        for (int i = 0; i < PER; i++) {
+          const float v = grp[i] == g ? rv[i] : -INFINITY;
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) merge_two(m1, m2, o);
+        const float low = (a.gtop == 2 ? m2 : m1) - tol;
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+          if (grp[i] == g && !(rv[i] < low)) marked |= 1u << i;
+      }
+      const int n = gather_marked<PER>(q, marked, e0, lane);
+      for (int i = lane; i < n; i += 32) q.v[i] = __double_as_longlong(value64(q.id[i], true));
+      __syncwarp();
+      double gs = -INFINITY;  // lane g: group g
+      if (lane < a.G) {
+        double m1 = -INFINITY, m2 = -INFINITY;
+        for (int i = 0; i < n; i++)
+          if (group_of(a, q.id[i]) == lane) {
+            const double v = __longlong_as_double(q.v[i]);
+            if (v > m1) {
+              m2 = m1;
+              m1 = v;
+            } else if (v > m2) {
+              m2 = v;
+            }
+          }
+        gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+      }
+      const int64_t og = ordered64(gs);
+      int ahead = 0;
+      for (int g = 0; g < a.G; g++) {
+        const int64_t v = __shfl_sync(0xffffffffu, og, g);
+        ahead += v > og || (v == og && g < lane);
+      }
+      const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
 #pragma unroll
       for (int i = 0; i < PER; i++)
-        if (grp[i] == g && !(rv[i] < border)) marked |= 1u << i;
+        if (((open >> i) & 1u) && !((keep >> grp[i]) & 1u)) open &= ~(1u << i);
     }
-    const int n = gather_marked<PER>(q, marked, e0, lane);
-    for (int i = lane; i < n; i += 32) q.v[i] = value64(q.id[i], true);
-    __syncwarp();
-    double gs = -INFINITY;  // lane g: group g
-    if (lane < a.G) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      for (int i = 0; i < n; i++)
-        if (group_of(a, q.id[i]) == lane) {
-          const double v = q.v[i];
-          if (v > m1) {
-            m2 = m1;
-            m1 = v;
-          } else if (v > m2) {
-            m2 = v;
-          }
+    // the k-th largest fp32 value
+    uint32_t left = open, kth = 0u;
+    for (int j = 0; j < a.k; j++) {
+      uint32_t best = 0u;
+      int bi = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i++) {
+        const uint32_t o = (left >> i) & 1u ? ordered(c[i]) : 0u;
+        if (o > best) {
+          best = o;
+          bi = i;
         }
-      gs = a.gtop == 2 && m2 > -INFINITY ? m1 + m2 : m1;
-    }
-    int ahead = 0;
-    for (int g = 0; g < a.G; g++) {
-      const double v = __shfl_sync(0xffffffffu, gs, g);
-      ahead += v > gs || (v == gs && g < lane);
-    }
-    const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.G && ahead < a.tg);
-#pragma unroll
-    for (int i = 0; i < PER; i++)
-      if (((open >> i) & 1u) && !((keep >> grp[i]) & 1u)) open &= ~(1u << i);
-  }
-  // the k-th largest fp32 value, and everything not clearly below it
-  uint32_t left = open, kth = 0u;
-  for (int j = 0; j < a.k; j++) {
-    uint32_t best = 0u;
-    int bi = 0;
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-      const uint32_t o = (left >> i) & 1u ? ordered(c[i]) : 0u;
-      if (o > best) {
-        best = o;
-        bi = i;
       }
+      kth = __reduce_max_sync(0xffffffffu, best);
+      if (kth == 0u) break;
+      const int owner = __ffs((int)__ballot_sync(0xffffffffu, best == kth)) - 1;
+      if (lane == owner) left &= ~(1u << bi);
     }
-    kth = __reduce_max_sync(0xffffffffu, best);
-    if (kth == 0u) break;
-    const int owner = __ffs((int)__ballot_sync(0xffffffffu, best == kth)) - 1;
-    if (lane == owner) left &= ~(1u << bi);
+    border = kth ? unordered(kth) : -INFINITY;
   }
-  const float border = kth ? unordered(kth) - tol : -INFINITY;
+  border -= tol;
   uint32_t marked = 0u;
 #pragma unroll
   for (int i = 0; i < PER; i++)
     if (((open >> i) & 1u) && !(c[i] < border)) marked |= 1u << i;
   const int n = gather_marked<PER>(q, marked, e0, lane);
-  for (int i = lane; i < n; i += 32) q.v[i] = value64(q.id[i], false);
+  for (int i = lane; i < n; i += 32) q.v[i] = ordered64(value64(q.id[i], false));
   __syncwarp();
   int my_id = -1;  // lane j: the j-th choice
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
     int place = 32;
     if (i < n) {
-      const double v = q.v[i];
+      const int64_t v = q.v[i];
       place = 0;
       for (int j = 0; j < n; j++) place += q.v[j] > v || (q.v[j] == v && j < i);
     }
@@ -306,16 +333,30 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
       if (who && lane == j) my_id = q.id[i0 + __ffs((int)who) - 1];
     }
   }
-  double my_s = my_id >= 0 ? score64(my_id) : 0.0;
+  // weights in fp32, but where their sum nears fp32's smallest number
+  float my_l = 0.0f, my_s = 0.0f;
+  if (my_id >= 0) {
+    my_l = load_logit<LT>(a.logits, l0 + my_id);
+    my_s = a.sigmoid ? 1.0f / (1.0f + expf(-my_l)) : expf(my_l - top) / zf;
+  }
+  float w = my_s;
   if (a.renorm) {
-    double sum = my_s;
+    float sum = my_s;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (sum > 0.0) my_s /= sum;
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (__shfl_sync(0xffffffffu, sum, 0) < 1e-30f) {
+      const double m = my_id >= 0 ? score64(my_id) : 0.0;
+      double all64 = m;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) all64 += __shfl_xor_sync(0xffffffffu, all64, o);
+      w = all64 > 0.0 ? (float)(m / all64) : 0.0f;
+    } else {
+      w = my_s / sum;
+    }
   }
   if (lane < a.k) {
     a.ids[row * a.k + lane] = my_id;
-    a.w[row * a.k + lane] = (float)(my_s * (double)a.scale);
+    a.w[row * a.k + lane] = w * a.scale;
   }
 }
 
@@ -382,17 +423,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     }
     return;
   }
-  // What two fp32 values of c may be off together, in units of the largest
-  // score (1 for a sigmoid, 1 / z for a softmax) and of |c|.  u = 2^-24.  A
-  // sigmoid: the exponential's argument is off by |l| u, which moves s by
-  // s (1 - s) |l| u <= 0.3 u, its 2 ulp by 4 u s (1 - s) <= u, the sum 1 + e
-  // and the reciprocal by 3 u: 4.3 u in all.  A softmax: the argument enters
-  // as d u exp(-d) <= 0.37 u twice (difference, product by log2 e), the
-  // exponential 4 u, z and the two roundings under 24 u: 29 u of the largest
-  // score.  Adding b: another u |c|.  Twice each stays under unit times the
-  // larger of the largest score and |c| (16 u and 64 u).
   const float smax = a.sigmoid ? 1.0f : (z > 0.0f ? 1.0f / z : 0.0f);
-  const float unit = a.sigmoid ? 9.5367431640625e-07f : 3.814697265625e-06f;  // 2^-20, 2^-18
   bool close = false;
   if (a.G > 1) {
     const int per = a.E / a.G;
@@ -459,27 +490,44 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
       const float cmax = __uint_as_float(__reduce_max_sync(0xffffffffu, mag));
       const float vin = unordered(__reduce_max_sync(0xffffffffu, ordered(in)));
       const float vout = unordered(__reduce_max_sync(0xffffffffu, ordered(out)));
-      close = vout > -INFINITY && !(vin - vout > 2.0f * unit * (smax + cmax));
+      close = vout > -INFINITY && !(vin - vout > group_err(a.sigmoid) * smax + 8.0f * kU * cmax);
     }
 #pragma unroll
     for (int i = 0; i < PER; i++)
       if (a.whole ? !kept : (i < have && !((keep >> group_of(a, e0 + i)) & 1u))) key[i] = 0ull;
   }
-  // the k best, and one more where fp32 may have erred
+  const bool settled = !__any_sync(0xffffffffu, close);
+  uint32_t open = 0u;
+  if (scored) {
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+      if (key[i] != 0ull) open |= 1u << i;
+  }
+  // the k best, and one more where fp32 may have erred: the lanes' sorted
+  // values wait in shared memory, a lane's slots in the nibbles of one word
   sort_down<PER>(key);
+  uint32_t* heads = reinterpret_cast<uint32_t*>(contenders[threadIdx.x >> 5].v);  // [PER + 1][32]
+  uint32_t slots = 0u;
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    if (i) heads[i * 32 + lane] = (uint32_t)(key[i] >> 32);
+    slots |= (31u - (uint32_t)key[i]) << (4 * i);
+  }
+  heads[PER * 32 + lane] = 0u;
+  uint32_t head = (uint32_t)(key[0] >> 32);
+  int at = lane;
   int my_id = -1;
   uint32_t my_key = 0u;
   const int rounds = scored ? a.k + 1 : a.k;
   for (int j = 0; j < rounds; j++) {
-    const uint32_t head = (uint32_t)(key[0] >> 32);
     const uint32_t v = __reduce_max_sync(0xffffffffu, head);
     if (v == 0u) break;
     const int owner = __ffs((int)__ballot_sync(0xffffffffu, head == v)) - 1;
-    const int id = __shfl_sync(0xffffffffu, e0 + 31 - (int)(uint32_t)key[0], owner);
+    const int id = __shfl_sync(0xffffffffu, e0 + (int)(slots & 15u), owner);
     if (lane == owner) {
-#pragma unroll
-      for (int i = 0; i + 1 < PER; i++) key[i] = key[i + 1];
-      key[PER - 1] = 0ull;
+      at += 32;
+      head = heads[at];
+      slots >>= 4;
     }
     if (lane == j) {
       my_id = id;
@@ -497,7 +545,7 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     const int ni = __shfl_down_sync(0xffffffffu, my_id, 1);
     if (lane < a.k && my_key != 0u && nk != 0u) {
       const float v0 = unordered(my_key), v1 = unordered(nk);
-      if (!(v0 - v1 > unit * fmaxf(smax, fmaxf(fabsf(v0), fabsf(v1)))))
+      if (!(v0 - v1 > score_err(a.sigmoid) * smax + 2.0f * kU * fmaxf(fabsf(v0), fabsf(v1))))
         // equal logit and bias: equal values, rightly decided by index
         close |= !(my_l == nl && a.bias[my_id] == a.bias[ni]);
     }
@@ -510,7 +558,9 @@ __global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_co
     close |= sum < 1e-30f && lane < a.k && my_id >= 0;
   }
   if (__any_sync(0xffffffffu, close)) {
-    choose_exact<LT, PER>(a, row, lane, contenders[threadIdx.x >> 5]);
+    const uint32_t kth = __shfl_sync(0xffffffffu, my_key, a.k - 1);
+    choose_exact<LT, PER>(a, row, lane, contenders[threadIdx.x >> 5], scored && settled, open,
+                          kth ? unordered(kth) : -INFINITY);
     return;
   }
   if (lane < a.k) {
