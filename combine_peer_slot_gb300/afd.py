@@ -124,8 +124,9 @@ SIGNATURES = [
     ("afd_mx4_dequantize", _I, [_P, _P, _I64, _I, _I, _P, _I64, _P]),
     ("afd_mx4_weight_bytes", _I64, [_I, _I, _I, _I]),
     ("afd_mx4_pack_weight", _I, [_P, _P, _I, _I, _I, _I, _P, _I64, _P]),
-    ("afd_mx4_gemm", _I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _P, _I64, _P]),
-    ("afd_mx4_ffn_workspace", _I64, [_I64, _I]),
+    ("afd_mx4_gemm_workspace", _I64, [_I64, _I, _I]),
+    ("afd_mx4_gemm", _I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _P, _I64, _P, _I64, _P]),
+    ("afd_mx4_ffn_workspace", _I64, [_I64, _I, _I, _I]),
     ("afd_mx4_ffn", _I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _I64, _P]),
     ("afd_mx4_poll_status", _I, [_P]),
 ]
@@ -449,15 +450,19 @@ def afd_mx4_pack_weight(codes, scales, num_experts, M, K, swiglu, packed, packed
                                      int(bool(swiglu)), packed or None, packed_bytes, stream or None)
 
 
+def afd_mx4_gemm_workspace(n_rows, num_experts, K):
+    return int(lib().afd_mx4_gemm_workspace(n_rows, num_experts, K))
+
+
 def afd_mx4_gemm(codes, scales, n_rows, offsets, num_experts, weight, M, K, swiglu, out_dtype, out,
-                 ldo, stream=0):
+                 ldo, workspace=0, workspace_bytes=0, stream=0):
     return lib().afd_mx4_gemm(codes or None, scales or None, n_rows, offsets or None, num_experts,
                               weight or None, M, K, int(bool(swiglu)), out_dtype, out or None, ldo,
-                              stream or None)
+                              workspace or None, workspace_bytes, stream or None)
 
 
-def afd_mx4_ffn_workspace(n_rows, inter):
-    return int(lib().afd_mx4_ffn_workspace(n_rows, inter))
+def afd_mx4_ffn_workspace(n_rows, num_experts, hidden, inter):
+    return int(lib().afd_mx4_ffn_workspace(n_rows, num_experts, hidden, inter))
 
 
 def afd_mx4_ffn(codes, scales, n_rows, offsets, num_experts, w13, wd, hidden, inter, out_dtype, out,

@@ -330,15 +330,29 @@ int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_exp
                   "mx4 pack weight");
 }
 
-// One product over the grouped rows.
-static int product(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
+static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// One product over the grouped rows.  image: the rows' scale images (wide
+// form; written here from scales unless that is NULL).  out_scales: OUT_MX4's.
+static int product(LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, uint8_t* image, int64_t n_rows,
                    const int32_t* offsets, int E, const void* w, int M, int K, int swiglu, int fmt, void* out,
                    int64_t ldo, uint8_t* out_scales = nullptr) {
   Mx4GemmArgs a;
   memset(&a, 0, sizeof a);
   const int bn = mx4_token_tile(n_rows, E);
+  const int64_t img = mx4_image_bytes(n_rows, E, K);
+  const int64_t units = (int64_t)mx4_tiles(M, swiglu) * ((n_rows + bn - 1) / bn + std::min<int64_t>(E, n_rows));
+  if (units >= (int64_t)1 << 31 || img / 128 >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
   int rc = encode_mx4_rows(&a.tmX[0], codes, n_rows, K, bn);
+  if (!rc) rc = encode_mx4_weight(&a.tmW[0], w, mx4_weight_bytes(E, M, K, swiglu));
+  if (!rc && fmt == OUT_ACT) rc = encode_mx4_out(&a.tmO[0], out, n_rows, swiglu ? M / 2 : M, ldo);
+  if (!rc && img) rc = encode_mx4_images(&a.tmS[0], image, img);
   if (rc) return rc;
+  if (img && scales) {
+    rc = launched(launch_mx4_images(lc, scales, n_rows, offsets, E, K, image), "mx4 scale images");
+    if (rc) return rc;
+    lc.pdl = 1;  // the product's set-up runs while the images are written
+  }
   a.xs[0] = scales;
   a.x_rows[0] = n_rows;
   a.w[0] = static_cast<const uint8_t*>(w);
@@ -351,42 +365,52 @@ static int product(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* sca
   a.offsets = offsets;
   a.n_groups = E;
   a.swiglu = swiglu;
-  const int64_t units = (int64_t)mx4_tiles(M, swiglu) * ((n_rows + bn - 1) / bn + std::min<int64_t>(E, n_rows));
-  if (units >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
   return launched(launch_mx4_gemm(lc, a, bn, units), "mx4 gemm");
+}
+
+int64_t afd_mx4_gemm_workspace(int64_t n_rows, int num_experts, int K) {
+  if (n_rows < 0 || n_rows > kMaxRows || num_experts < 1 || num_experts > 256 || !dims_ok(1, K) || K % kMx4Block)
+    return -1;
+  return up256(mx4_image_bytes(n_rows, num_experts, K));
 }
 
 int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* offsets,
                  int num_experts, const void* weight, int M, int K, int swiglu, int out_dtype, void* out,
-                 int64_t ldo, void* cuda_stream) {
+                 int64_t ldo, void* workspace, int64_t workspace_bytes, void* cuda_stream) {
   const int cols = swiglu ? M / 2 : M;
   if (afd_mx4_weight_bytes(num_experts, M, K, swiglu) == 0 || n_rows < 0 || n_rows > kMaxRows || ldo < cols ||
       (out_dtype != AFD_DTYPE_F32 && out_dtype != AFD_DTYPE_BF16))
     return AFD_ERR_ARG;
   if (swiglu && out_dtype != AFD_DTYPE_BF16) return AFD_ERR_UNSUPPORTED;
   if (n_rows == 0) return AFD_OK;
+  const int64_t need = afd_mx4_gemm_workspace(n_rows, num_experts, K);
+  if (workspace_bytes < need) return AFD_ERR_CAPACITY;
+  if ((need && !workspace) || !aligned(workspace, 256)) return AFD_ERR_ARG;
   if (!codes || !scales || !offsets || !weight || !out || !aligned(codes, 16) || !aligned(weight, 128) ||
       !aligned(scales, 8) || !aligned(out, 16) || !aligned(offsets, 4) || ldo % 8)
     return AFD_ERR_ARG;
-  int rc = check_device_ptrs({codes, scales, offsets, weight, out});
+  int rc = check_device_ptrs({codes, scales, offsets, weight, out, need ? workspace : nullptr});
   LaunchCtx lc;
   if (!rc) rc = make_lc(cuda_stream, &lc);
   if (rc) return rc;
-  return product(lc, codes, scales, n_rows, offsets, num_experts, weight, M, K, swiglu != 0,
+  return product(lc, codes, scales, static_cast<uint8_t*>(workspace), n_rows, offsets, num_experts, weight, M, K, swiglu != 0,
                  out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo);
 }
 
-// workspace: the codes and scales of h
-int64_t afd_mx4_ffn_workspace(int64_t n_rows, int inter) {
-  if (n_rows < 0 || n_rows > kMaxRows || inter < kMx4Block || inter > kMaxDim || inter % kMx4Block) return -1;
-  const int64_t n = n_rows * inter;
-  return (n / 2 + 255) / 256 * 256 + (n / 32 + 255) / 256 * 256;
+// workspace: h's codes and its scales (or their images), x's scale images
+static int64_t ffn_scales_bytes(int64_t n_rows, int E, int inter) {
+  return up256(std::max(n_rows * inter / 32, mx4_image_bytes(n_rows, E, inter)));
+}
+int64_t afd_mx4_ffn_workspace(int64_t n_rows, int num_experts, int hidden, int inter) {
+  if (inter < kMx4Block || inter > kMaxDim || inter % kMx4Block) return -1;
+  const int64_t img = afd_mx4_gemm_workspace(n_rows, num_experts, hidden);
+  return img < 0 ? -1 : up256(n_rows * inter / 2) + ffn_scales_bytes(n_rows, num_experts, inter) + img;
 }
 
 int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, const int32_t* offsets,
                 int num_experts, const void* w13, const void* wd, int hidden, int inter, int out_dtype, void* out,
                 int64_t ldo, void* workspace, int64_t workspace_bytes, void* cuda_stream) {
-  const int64_t need = afd_mx4_ffn_workspace(n_rows, inter);
+  const int64_t need = afd_mx4_ffn_workspace(n_rows, num_experts, hidden, inter);
   if (need < 0 || afd_mx4_weight_bytes(num_experts, 2 * inter, hidden, 1) == 0 ||
       afd_mx4_weight_bytes(num_experts, hidden, inter, 0) == 0 || ldo < hidden ||
       (out_dtype != AFD_DTYPE_F32 && out_dtype != AFD_DTYPE_BF16))
@@ -401,13 +425,14 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, con
   LaunchCtx lc;
   if (!rc) rc = make_lc(cuda_stream, &lc);
   if (rc) return rc;
-  const int64_t n = n_rows * inter;
   uint8_t* hc = static_cast<uint8_t*>(workspace);
-  uint8_t* hs = hc + (n / 2 + 255) / 256 * 256;
-  rc = product(lc, codes, scales, n_rows, offsets, num_experts, w13, 2 * inter, hidden, 1, OUT_MX4, hc, inter, hs);
-  lc.pdl = 1;  // the second launch's set-up runs while the first drains
+  uint8_t* hs = hc + up256(n_rows * inter / 2);
+  uint8_t* xi = hs + ffn_scales_bytes(n_rows, num_experts, inter);
+  const bool wide = mx4_image_bytes(n_rows, num_experts, inter) > 0;
+  rc = product(lc, codes, scales, xi, n_rows, offsets, num_experts, w13, 2 * inter, hidden, 1, OUT_MX4, hc, inter, hs);
+  lc.pdl = 1;  // the second product's set-up runs while the first drains
   if (!rc)
-    rc = product(lc, hc, hs, n_rows, offsets, num_experts, wd, hidden, inter, 0,
+    rc = product(lc, hc, wide ? nullptr : hs, hs, n_rows, offsets, num_experts, wd, hidden, inter, 0,
                  out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo);
   return rc;
 }

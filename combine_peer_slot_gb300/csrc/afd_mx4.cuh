@@ -40,12 +40,15 @@ inline int64_t mx4_weight_bytes(int64_t E, int64_t M, int K, int swiglu) {
 // shared rows, one more group: all of kind 1's rows times its weight.
 #define OUT_MX4 3  // SwiGLU only: codes in out, scales in out_lo (ldo % 32 == 0)
 struct Mx4GemmArgs {
-  CUtensorMap tmX[2];        // codes of the rows [x_rows][K / 2], box 128 bytes x token tile
-  const uint8_t* xs[2];      // their scales [x_rows][K / 32]
+  CUtensorMap tmX[2];        // codes of the rows (encode_mx4_rows)
+  CUtensorMap tmW[2];        // packed weights (encode_mx4_weight); the wide form's
+  CUtensorMap tmS[2];        // their scale images (encode_mx4_images); the wide form's
+  const uint8_t* xs[2];      // their scales [x_rows][K / 32]; the narrow form's
   int64_t x_rows[2];
-  const uint8_t* w[2];       // packed weights
+  const uint8_t* w[2];       // packed weights; the narrow form's
+  CUtensorMap tmO[2];        // bf16 outputs (encode_mx4_out)
   void* out[2];
-  uint8_t* out_lo[2];        // OUT_Y24: the low plane; OUT_MX4: the scales
+  uint8_t* out_lo[2];        // OUT_Y24: the low plane; OUT_MX4: the scales (wide: their images)
   int64_t ldo[2];            // output row pitch in elements
   int fmt[2];                // OUT_*
   int M[2], K[2];
@@ -60,6 +63,13 @@ struct Mx4GemmArgs {
 int mx4_token_tile(int64_t rows, int groups);
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units);
 int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn);
+int64_t mx4_image_bytes(int64_t rows, int groups, int K);
+int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);
+// offsets NULL: one group of all rows
+cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
+                              int groups, int K, uint8_t* image);
+int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo);
+int encode_mx4_weight(CUtensorMap* m, const void* packed, int64_t bytes);
 
 cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx, int64_t x_rows, int f32,
                                 const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,

@@ -1,19 +1,28 @@
-// afd_mx4_gemm.cu -- the grouped MXFP4 product on one SM per tile:
+// afd_mx4_gemm.cu -- the grouped MXFP4 product on the tensor cores:
 // tcgen05.mma kind::mxf4 (e2m1 x e2m1, one e8m0 scale per 32 columns of each
 // operand, fp32 accumulate in TMEM).
 //
 //   y[r, m] = sum_k x[r, k] w[g(r), m, k]     x = code * 2^(scale - 127)
 //
-// A unit is 128 weight rows x one token tile of one group.  The weight rows
-// are the MMA's M side, the tokens its N side, so a group of few tokens
+// A unit is 128 weight rows per SM x one token tile of one group.  The weight
+// rows are the MMA's M side, the tokens its N side, so a group of few tokens
 // takes a narrow instruction and not a mostly empty 128-row one.  Per stage
-// of 256 columns a CTA takes 17 KB of weight (codes and scales in one bulk
-// copy), the tokens' codes by TMA (128-byte swizzle) and their scales, which
+// of 256 columns a CTA takes 17 KB of weight (codes and scales together),
+// the tokens' codes by TMA (128-byte swizzle) and their scales, which
 // several warps gather from the plain rows into the image tcgen05.cp spreads
-// over the lanes: a group's rows start anywhere, so the tiled image could
-// not be laid out before the groups are known.
+// over the lanes (wide: a small kernel beforehand, k_mx4_scale_image): a
+// group's rows start anywhere, so the tiled image could not be laid out
+// before the groups are known.
 //
-// Warps: 0 copies, 1 MMA, from 2 token scales, 8-15 epilogue.  All waits are
+// Two forms.  Narrow (64 tokens, one SM): groups of few tokens, bound by the
+// weights' bytes; the weight's stage is one bulk copy.  Wide (192 tokens, a
+// pair of SMs, cta_group::2): two weight tiles share the token tile, each SM
+// holds half of its codes and all of its scales, the leader issues for both.
+// One SM per tile moves 43 KB into shared memory and 40 KB out of it per
+// stage of 400 tensor cycles, over the 128 bytes a cycle shared memory has;
+// the pair 31 and 28 KB.
+//
+// Warps: 0 copies, 1 MMA, from 2 scales, 8-15 epilogue.  All waits are
 // bounded.
 #include "afd_mx4.cuh"
 
@@ -31,11 +40,13 @@ constexpr int A_BYTES = 2 * kMx4BlkBytes;
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 8;          // a multiple of 4: a warp reads the TMEM lanes of its number mod 4
 constexpr int NUM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
-// epilogue staging, one buffer per four warps: 32 tokens x 128 output rows
-// (SwiGLU: 64) of bf16, the rows 16 bytes apart in the banks
-constexpr int EPI_PITCH = 272;
-constexpr int EPI_PITCH_SWIGLU = 144;
-constexpr int EPI_BUF_BYTES = 32 * EPI_PITCH;
+// epilogue staging, two buffers per four warps, each 32 tokens x 128 output
+// rows (SwiGLU: 64) of bf16 as boxes of 64 (128 bytes a token, 128-byte swizzle)
+constexpr int EPI_BOX_BYTES = 32 * 128;
+constexpr int EPI_BUF_BYTES = 2 * EPI_BOX_BYTES;
+// lines of 8-byte words that the pair's copies take contiguous memory as: a
+// weight block is 8 of 1088 bytes, a 128-column scale image 1 of 1024
+constexpr int kBlkLines = 8, kImgLines = 1;
 constexpr int MAX_GROUPS = 257;       // 256 experts and the shared rows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -46,17 +57,18 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 // finding its own units there cost 280 cycles a stage.
 constexpr uint32_t INFO_FIRST = 1u << 12, INFO_LAST = 1u << 13, INFO_STOP = 1u << 14;
 
-template <int BN>
+template <int BN, int CTAS>
 struct Ring {
-  static constexpr int STAGES = BN > 64 ? 4 : 7;
-  // Warps that fill the token scales, a stage each in turn.  No more than
-  // stages: a warp that has filled stage i waits next for the release of
+  static constexpr int STAGES = CTAS == 2 ? 5 : 7;
+  // Narrow: warps that fill the token scales, a stage each in turn.  No more
+  // than stages: a warp that has filled stage i waits next for the release of
   // i + SF_WARPS - STAGES, and a parity wait tells a phase from the one
   // before it only; with more warps than stages it could pass one round early.
-  static constexpr int SF_WARPS = BN > 64 ? 4 : 6;
+  static constexpr int SF_WARPS = CTAS == 2 ? 0 : 6;
   static_assert(SF_WARPS <= STAGES && 2 + SF_WARPS <= EPI_WARP0, "scale warps");
   static constexpr int NB = (BN + 127) / 128;            // 128-row scale images per 128 columns
-  static constexpr int B_BYTES = BN * (BK / 2);
+  static constexpr int B_ROWS = BN / CTAS;               // token rows whose codes a CTA holds
+  static constexpr int B_BYTES = B_ROWS * (BK / 2);
   static constexpr int S_BYTES = 2 * NB * 512;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + S_BYTES;
   // TMEM columns: two accumulators, then per stage the weight scales (2 x 4)
@@ -69,21 +81,23 @@ struct Ring {
   struct Tail {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
+    uint64_t sfull[STAGES];     // wide: the stage's scales are in TMEM
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
     uint32_t info[STAGES];      // what the stage holds (INFO_*)
-    int m_tiles[2];             // weight tiles per kind, and (2^32 - 1) / m_tiles
+    int m_units[2];             // weight tiles (pairs of them) per kind, and (2^32 - 1) / m_units
     uint32_t m_magic[2];
     int tile0[MAX_GROUPS + 1];  // first unit of each group
     int row0[MAX_GROUPS];
     int rows[MAX_GROUPS];
-    int wsum[NUM_THREADS / 32];
+    int nt0[MAX_GROUPS];        // wide: first token tile of each group (scale images)
+    int wsum[NUM_THREADS / 32], nsum[NUM_THREADS / 32];
   };
-  static constexpr size_t kEpiOffset = ((size_t)STAGES * STAGE_BYTES + sizeof(Tail) + 127) / 128 * 128;
-  static constexpr size_t kSmemBytes = 1024 + kEpiOffset + (size_t)(EPI_WARPS / 4) * EPI_BUF_BYTES;
+  static constexpr size_t kEpiOffset = ((size_t)STAGES * STAGE_BYTES + sizeof(Tail) + 1023) / 1024 * 1024;
+  static constexpr size_t kSmemBytes = 1024 + kEpiOffset + (size_t)(EPI_WARPS / 4) * 2 * EPI_BUF_BYTES;
   static_assert(kSmemBytes <= 232448, "over the per-CTA shared memory limit");
 };
 
@@ -104,11 +118,12 @@ __device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t addr16) {
   return d;
 }
 
-// kind::mxf4: A and B e2m1 (format 1), e8m0 scales (bit 23), K = 64, M = 128;
-// sf: the first of the two scale bytes used of each lane's four (0 or 2)
+// kind::mxf4: A and B e2m1 (format 1), e8m0 scales (bit 23), K = 64, M = 128
+// per SM; sf: the first of the two scale bytes used of each lane's four (0 or 2)
+template <int CTAS>
 __device__ __forceinline__ uint32_t idesc_mx4(int n, int sf) {
-  return (uint32_t)sf << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(128 >> 4) << 24 |
-         (uint32_t)sf << 29;
+  return (uint32_t)sf << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 |
+         (uint32_t)(CTAS * 128 >> 4) << 24 | (uint32_t)sf << 29;
 }
 // The issuing warp runs its loop as a whole and each of the next three is
 // predicated on its elected lane: under a branch on the lane the operands
@@ -118,31 +133,118 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
   return e;
 }
+template <int CTAS>
 __device__ __forceinline__ void mma_mx4(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %7, 0;\n"
-      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
-      : "memory");
+  if (CTAS == 2)
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(elected)
+        : "memory");
 }
+// arrive on the barrier (of both CTAs of a pair) when the MMAs issued so far are done
+template <int CTAS>
 __device__ __forceinline__ void commit(uint32_t elected, uint32_t bar) {
-  asm volatile(
-      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
-      "r"(elected)
-      : "memory");
+  if (CTAS == 2)
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2; }"
+        ::"r"(bar), "r"(elected), "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+        "r"(elected)
+        : "memory");
 }
 // 32 lanes x 16 bytes of shared memory into four TMEM columns, the same for
-// each quarter of the lanes
+// each quarter of the lanes; in a pair, each CTA's shared memory at this
+// address into its own TMEM
+template <int CTAS>
 __device__ __forceinline__ void cp_scales(uint32_t elected, uint32_t tmem, uint64_t desc) {
+  if (CTAS == 2)
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1; }" ::"r"(tmem),
+        "l"(desc), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(tmem),
+        "l"(desc), "r"(elected)
+        : "memory");
+}
+
+// arrive on this CTA's barrier
+template <int CTAS>
+__device__ __forceinline__ void commit_local(uint32_t elected, uint32_t bar) {
+  if (CTAS == 2)
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(elected)
+        : "memory");
+  else
+    commit<1>(elected, bar);
+}
+// the scales of 128 columns: the weight's image, then the tokens'
+template <int CTAS, int NB>
+__device__ __forceinline__ void issue_scales(uint32_t el, int c, uint32_t sa, uint32_t ss, uint32_t sf) {
+  cp_scales<CTAS>(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
+#pragma unroll
+  for (int b = 0; b < NB; b++)
+    cp_scales<CTAS>(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm), "r"(src),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// the pair (rank 0 leads)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrive on the leader's barrier; one CTA: on its own.  Relaxed: it says that
+// TMEM has been read (tcgen05.wait::ld has returned, the tcgen05 fence stands
+// before it) and publishes no memory.
+template <int CTAS>
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  if (CTAS == 2)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+  else
+    mbar_arrive(bar);
+}
+// a box into this CTA's shared memory, its bytes counted on the leader's barrier
+__device__ __forceinline__ void tma_pair_load_2d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
+                                                 uint32_t bar_cluster) {
   asm volatile(
-      "{ .reg .pred q; setp.ne.b32 q, %2, 0;\n"
-      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1; }" ::"r"(tmem),
-      "l"(desc), "r"(elected)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(tm), "r"(c0), "r"(c1), "r"(bar_cluster)
       : "memory");
 }
 
+// (acquire at CTA scope: across the pair the barriers order copies, MMAs and
+// TMEM reads only, never the peer's plain stores)
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
                                          int32_t* status) {
   uint32_t spins = 0;
@@ -213,27 +315,28 @@ __device__ __forceinline__ bool group_all(int half, bool ok) {
 }
 
 struct Unit {
-  int group, kind, mt, rows, n_mma;
+  int group, kind, mt, rows, n_mma, tile;
   int64_t row;  // first row of the token tile
 };
 
-// A role's walk over its units.  Consecutive units of a CTA lie gridDim.x
-// apart, so the group is found by stepping from the last one (a few shared
+// A role's walk over its units.  Consecutive units of a CTA (pair) lie one
+// grid apart, so the group is found by stepping from the last one (a few shared
 // loads), and by a search only over a run of empty groups.
-template <int BN>
+template <int BN, int CTAS>
 struct Walk {
   const Mx4GemmArgs& a;
-  const typename Ring<BN>::Tail* T;
+  const typename Ring<BN, CTAS>::Tail* T;
   int ngroups, total;
   int unit, g;
   Unit t;
-  __device__ __forceinline__ Walk(const Mx4GemmArgs& args, const typename Ring<BN>::Tail* tail, int n, int tot)
-      : a(args), T(tail), ngroups(n), total(tot), unit((int)blockIdx.x), g(0) {
+  __device__ __forceinline__ Walk(const Mx4GemmArgs& args, const typename Ring<BN, CTAS>::Tail* tail, int n,
+                                  int tot)
+      : a(args), T(tail), ngroups(n), total(tot), unit((int)blockIdx.x / CTAS), g(0) {
     decode();
   }
   __device__ __forceinline__ bool more() const { return unit < total; }
   __device__ __forceinline__ void next() {
-    unit += (int)gridDim.x;
+    unit += (int)gridDim.x / CTAS;
     decode();
   }
   __device__ __forceinline__ void decode() {
@@ -257,14 +360,16 @@ struct Walk {
       t.mt = n_tiles == 1 ? u : u / n_tiles;
       nt = u - t.mt * n_tiles;
     } else {         // the units running at once share token tiles
-      const int m_tiles = T->m_tiles[t.kind];
-      nt = (int)__umulhi((uint32_t)u, T->m_magic[t.kind]);  // u / m_tiles, or one less
-      if ((nt + 1) * m_tiles <= u) nt++;
-      t.mt = u - nt * m_tiles;
+      const int m_units = T->m_units[t.kind];
+      nt = (int)__umulhi((uint32_t)u, T->m_magic[t.kind]);  // u / m_units, or one less
+      if ((nt + 1) * m_units <= u) nt++;
+      t.mt = u - nt * m_units;
+      t.tile = T->nt0[g] + nt;
     }
+    if (CTAS == 2) t.mt = 2 * t.mt + (int)cluster_rank();  // past an odd edge: computed, not stored
     t.row = (int64_t)T->row0[g] + (int64_t)nt * BN;
     t.rows = min(BN, rows - nt * BN);
-    t.n_mma = (t.rows + 15) & ~15;
+    t.n_mma = CTAS == 2 ? (t.rows + 31) & ~31 : (t.rows + 15) & ~15;  // 16 of each CTA's rows
   }
 };
 
@@ -295,40 +400,49 @@ __device__ __forceinline__ void load_scales(const uint8_t* xs, int64_t x_rows, i
   }
 }
 
-template <int BN>
+template <int BN, int CTAS>
 __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_constant__ Mx4GemmArgs a) {
-  using R = Ring<BN>;
+  using R = Ring<BN, CTAS>;
   constexpr int STAGES = R::STAGES;
   constexpr int NB = R::NB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   typename R::Tail* tail = reinterpret_cast<typename R::Tail*>(smem + (size_t)STAGES * R::STAGE_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool leader = CTAS == 1 || cluster_rank() == 0;
   int32_t* status = a.status ? a.status : &g_mx4_status;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; s++) {
-      mbar_init(smem_u32(&tail->full[s]), 2);  // the copies' producer, the scale warp
+      mbar_init(smem_u32(&tail->full[s]), CTAS == 2 ? 1 : 2);  // the producer (the leader's), the scale warp
+      mbar_init(smem_u32(&tail->sfull[s]), 1);
       mbar_init(smem_u32(&tail->empty[s]), 1);
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(smem_u32(&tail->tfull[b]), 1);
-      mbar_init(smem_u32(&tail->tempty[b]), EPI_WARPS);
+      mbar_init(smem_u32(&tail->tempty[b]), CTAS * EPI_WARPS);
     }
     mbar_init(smem_u32(&tail->drain), 1);
     tail->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&tail->tmem_base)),
-                 "r"(R::TMEM_COLS));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (CTAS == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tail->tmem_base)),
+                   "r"(R::TMEM_COLS));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&tail->tmem_base)),
+                   "r"(R::TMEM_COLS));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   grid_dep_wait();
   grid_dep_launch();
   // the groups: rows clamped to those there are, units counted
   const int ngroups = a.n_groups + a.has_shared;
-  int mine = 0;
+  int mine = 0, tiles = 0;
   if (threadIdx.x < ngroups) {
     const int g = threadIdx.x;
     const int kind = g == a.n_groups;
@@ -339,32 +453,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     }
     tail->row0[g] = lo;
     tail->rows[g] = hi - lo;
-    mine = (hi - lo + BN - 1) / BN * mx4_tiles(a.M[kind], a.swiglu);
+    tiles = (hi - lo + BN - 1) / BN;
+    mine = tiles * ((mx4_tiles(a.M[kind], a.swiglu) + CTAS - 1) / CTAS);
   }
-  int incl = mine;
+  int incl = mine, tincl = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, tincl, o);
+    if (lane >= o) {
+      incl += v;
+      tincl += w;
+    }
   }
-  if (lane == 31) tail->wsum[warp] = incl;
+  if (lane == 31) {
+    tail->wsum[warp] = incl;
+    tail->nsum[warp] = tincl;
+  }
   __syncthreads();
-  int before = 0, total = 0;
+  int before = 0, total = 0, tbefore = 0;
   for (int w = 0; w < NUM_THREADS / 32; w++) {
-    if (w < warp) before += tail->wsum[w];
+    if (w < warp) {
+      before += tail->wsum[w];
+      tbefore += tail->nsum[w];
+    }
     total += tail->wsum[w];
   }
-  if (threadIdx.x < ngroups) tail->tile0[threadIdx.x + 1] = before + incl;
+  if (threadIdx.x < ngroups) {
+    tail->tile0[threadIdx.x + 1] = before + incl;
+    tail->nt0[threadIdx.x] = (int)threadIdx.x == a.n_groups ? 0 : tbefore + tincl - tiles;  // per kind
+  }
   if (threadIdx.x == 0) {
     tail->tile0[0] = 0;
     for (int k = 0; k < 2; k++) {
-      const int m = max(mx4_tiles(a.M[k], a.swiglu), 1);
-      tail->m_tiles[k] = m;
+      const int m = max((mx4_tiles(a.M[k], a.swiglu) + CTAS - 1) / CTAS, 1);
+      tail->m_units[k] = m;
       tail->m_magic[k] = 0xffffffffu / (uint32_t)m;  // under 2^32 / m by at most 1: u m_magic / 2^32 > u / m - 1
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (CTAS == 2) cluster_sync();  // both CTAs' barriers and TMEM columns are in place
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
   const uint64_t deadline = globaltimer_ns() + kTimeoutNs;
@@ -377,30 +505,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (Walk<BN> w(a, tail, ngroups, total); w.more() && ok; w.next()) {
+      for (Walk<BN, CTAS> w(a, tail, ngroups, total); w.more() && ok; w.next()) {
         const Unit& t = w.t;
         const int nk = mx4_kblocks(a.K[t.kind]);
         const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
-        const uint8_t* wt =
-            a.w[t.kind] + ((int64_t)(t.kind ? 0 : t.group) * m_tiles + t.mt) * nk * (int64_t)kMx4BlkBytes;
+        const int64_t blk0 =  // the weight's blocks of this tile (past an odd edge: the last tile's again)
+            ((int64_t)(t.kind ? 0 : t.group) * m_tiles + min(t.mt, m_tiles - 1)) * nk;
         for (int kb = 0; kb * 2 < nk; kb++) {
           if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
           const uint32_t full = smem_u32(&tail->full[s]);
-          const uint32_t a_bytes = min(2, nk - 2 * kb) * kMx4BlkBytes;
-          const int left = (a.K[t.kind] - kb * BK + 63) / 64;
-          tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, 4) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
-                          (left <= 4 ? INFO_LAST : 0u);
-          mbar_expect_tx(full, a_bytes + R::B_BYTES);
+          const int blks = min(2, nk - 2 * kb);
+          if (leader) {
+            const int left = (a.K[t.kind] - kb * BK + 63) / 64;
+            tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, 4) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
+                            (left <= 4 ? INFO_LAST : 0u);
+            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + R::B_BYTES + (CTAS == 2 ? R::S_BYTES : 0)));
+          }
           const uint32_t sa = smem_base + s * R::STAGE_BYTES;
-          bulk_load(sa, wt + (int64_t)kb * 2 * kMx4BlkBytes, a_bytes, full);
-          tma_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2), (int)t.row, full);
+          if (CTAS == 2) {
+            const uint32_t full_leader = map_to_rank(full, 0);
+            for (int b = 0; b < blks; b++)
+              tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW[t.kind], 0,
+                               (int)(blk0 + 2 * kb + b) * kBlkLines, full_leader);
+            tma_pair_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2),
+                             (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
+            // (a lone last block: its second half is the next tile's, copied and not used)
+            tma_pair_load_2d(sa + A_BYTES + R::B_BYTES, &a.tmS[t.kind], 0, (t.tile * nk + 2 * kb) * kImgLines,
+                             full_leader);
+          } else {
+            bulk_load(sa, a.w[t.kind] + (blk0 + 2 * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
+            tma_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2), (int)t.row, full);
+          }
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
       }
-      if (ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
+      if (leader && ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
         tail->info[s] = INFO_STOP;
         mbar_arrive(smem_u32(&tail->full[s]));
-        mbar_arrive(smem_u32(&tail->full[s]));  // for the scale warp, which has no such stage
+        if (CTAS == 1) mbar_arrive(smem_u32(&tail->full[s]));  // for the scale warp, which has no such stage
       }
       // a wait gave up: the copies in flight land before the CTA leaves
       if (!ok)
@@ -408,83 +550,111 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer
-    const uint32_t el = elect_one();
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    // Each stage's barrier is tested, and its word read, while the stage
-    // before it is being issued: the two round trips to shared memory would
-    // otherwise stand between the stages (about 330 of 860 cycles a stage).
-    int s = 0;
-    uint32_t ph = 0;
-    int acc = 0;
-    uint32_t acc_ph = 0;
-    bool ready = false;
-    uint32_t word = 0;
-    for (;;) {
-      if (!ready) {
+    if (leader) {
+      const uint32_t el = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // Each stage's barrier is tested, and its word read, while the stage
+      // before it is being issued: the two round trips to shared memory would
+      // otherwise stand between the stages (about 330 of 860 cycles a stage).
+      int s = 0;
+      uint32_t ph = 0;
+      int acc = 0;
+      uint32_t acc_ph = 0;
+      bool ready = false;
+      uint32_t word = 0;
+      for (;;) {
+        if (!ready) {
+          if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
+          if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[s]), ph, abort_flag, deadline, status)) break;
+          word = *(volatile uint32_t*)&tail->info[s];
+        }
+        const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
+        if (info & (INFO_STOP | INFO_FIRST)) {
+          if (info & INFO_STOP) break;
+          if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
+        }
+        tc_fence_after();
+        const int s1 = s + 1 == STAGES ? 0 : s + 1;
+        const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
+        const uint32_t test = mbar_test_wait(smem_u32(&tail->full[s1]), ph1) &
+                              (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[s1]), ph1) : 1u);
+        const uint32_t id0 = idesc_mx4<CTAS>((int)(info & 511u), 0), id2 = id0 | idesc_mx4<CTAS>(0, 2);
+        const uint32_t d = tm + (uint32_t)(acc * BN);
+        const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
+        const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
+        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
+        const int steps = (int)(info >> 9) & 7;
+        const uint32_t more = (info & INFO_FIRST) ? 0u : 1u;
+        auto scales = [&](int c) {  // of 128 columns (wide: the scale warp's part)
+          if (CTAS == 1) issue_scales<CTAS, NB>(el, c, sa, ss, sf);
+        };
+        auto mma = [&](int kk) {    // of 64 columns
+          const int c = kk >> 1, o = kk & 1;
+          mma_mx4<CTAS>(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
+                  o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 ? 1u : more);
+        };
+        if (steps == 4) {  // no branch between the instructions of a whole stage
+          scales(0);
+          scales(1);
+          ready = __all_sync(0xffffffffu, test != 0);
+          mma(0);
+          mma(1);
+          word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
+          mma(2);
+          mma(3);
+        } else {           // the unit's last columns
+          scales(0);
+          if (steps > 2) scales(1);
+          ready = __all_sync(0xffffffffu, test != 0);
+          word = *(volatile uint32_t*)&tail->info[s1];
+          mma(0);
+          if (steps > 1) mma(1);
+          if (steps > 2) mma(2);
+        }
+        commit<CTAS>(el, smem_u32(&tail->empty[s]));
+        s = s1;
+        ph = ph1;
+        if (info & INFO_LAST) {
+          commit<CTAS>(el, smem_u32(&tail->tfull[acc]));
+          if (++acc == 2) { acc = 0; acc_ph ^= 1; }
+        }
+      }
+      // every issued MMA completes before TMEM is released
+      commit_local<CTAS>(el, smem_u32(&tail->drain));
+      const uint64_t dl = globaltimer_ns() + 100000000ull;
+      while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
+      __syncwarp();
+    }
+  } else if (CTAS == 2 && warp == 2) {
+    // ------------------------------ wide: scales into TMEM
+    // A warp of their own issues them: six copies and four MMAs a stage from
+    // one warp took longer to issue than the MMAs take to run.
+    if (leader) {
+      const uint32_t el = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      int s = 0;
+      uint32_t ph = 0;
+      for (;;) {
         if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
-        word = *(volatile uint32_t*)&tail->info[s];
-      }
-      const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
-      if (info & (INFO_STOP | INFO_FIRST)) {
-        if (info & INFO_STOP) break;
-        if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
-      }
-      tc_fence_after();
-      const int s1 = s + 1 == STAGES ? 0 : s + 1;
-      const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
-      const uint32_t test = mbar_test_wait(smem_u32(&tail->full[s1]), ph1);
-      const uint32_t id0 = idesc_mx4((int)(info & 511u), 0), id2 = id0 | idesc_mx4(0, 2);
-      const uint32_t d = tm + (uint32_t)(acc * BN);
-      const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
-      const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
-      const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
-      const int steps = (int)(info >> 9) & 7;
-      const uint32_t more = (info & INFO_FIRST) ? 0u : 1u;
-      auto scales = [&](int c) {  // of 128 columns
-        cp_scales(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
-#pragma unroll
-        for (int b = 0; b < NB; b++)
-          cp_scales(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
-      };
-      auto mma = [&](int kk) {    // of 64 columns
-        const int c = kk >> 1, o = kk & 1;
-        mma_mx4(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
-                o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 ? 1u : more);
-      };
-      if (steps == 4) {  // no branch between the instructions of a whole stage
-        scales(0);
-        scales(1);
-        ready = __all_sync(0xffffffffu, test != 0);
-        mma(0);
-        mma(1);
-        word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
-        mma(2);
-        mma(3);
-      } else {           // the unit's last columns
-        scales(0);
-        if (steps > 2) scales(1);
-        ready = __all_sync(0xffffffffu, test != 0);
-        word = *(volatile uint32_t*)&tail->info[s1];
-        mma(0);
-        if (steps > 1) mma(1);
-        if (steps > 2) mma(2);
-      }
-      commit(el, smem_u32(&tail->empty[s]));
-      s = s1;
-      ph = ph1;
-      if (info & INFO_LAST) {
-        commit(el, smem_u32(&tail->tfull[acc]));
-        if (++acc == 2) { acc = 0; acc_ph ^= 1; }
+        const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
+        if (info & INFO_STOP) {
+          if (lane == 0) mbar_arrive(smem_u32(&tail->sfull[s]));
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
+        const uint32_t ss = sa + ((A_BYTES + R::B_BYTES) >> 4);
+        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
+        issue_scales<CTAS, NB>(el, 0, sa, ss, sf);
+        if (((info >> 9) & 7u) > 2u) issue_scales<CTAS, NB>(el, 1, sa, ss, sf);
+        commit_local<CTAS>(el, smem_u32(&tail->sfull[s]));
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
-    // every issued MMA completes before TMEM is released
-    commit(el, smem_u32(&tail->drain));
-    const uint64_t dl = globaltimer_ns() + 100000000ull;
-    while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
     __syncwarp();
-  } else if (warp < 2 + R::SF_WARPS) {
-    // ------------------------------ token scales: the warps take stages in turn
-    Walk<BN> w(a, tail, ngroups, total);
+  } else if (CTAS == 1 && warp < 2 + R::SF_WARPS) {
+    // ------------------------------ narrow: token scales, the warps take stages in turn
+    Walk<BN, CTAS> w(a, tail, ngroups, total);
     int kb = 0;
     auto advance = [&](int n) {  // n stages on
       kb += n;
@@ -521,7 +691,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tail->full[s]));
+      if (lane == 0) arrive_leader<CTAS>(smem_u32(&tail->full[s]));
       advance(R::SF_WARPS);
       load(v);
       it += R::SF_WARPS;
@@ -532,16 +702,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     // warp reads its 32 TMEM lanes in the fragment layout, so that stmatrix
     // writes tokens as rows (a 32 x 32 piece in 4 instructions, where 2-byte
     // stores from the lane-per-row layout took 32) and, with SwiGLU, a
-    // thread holds the gate and the up value of one output: the group's
-    // rows then leave shared memory as whole 256-byte (SwiGLU: 128) runs.
+    // thread holds the gate and the up value of one output.  Whole pieces
+    // leave shared memory by TMA, the last rows of a group by plain stores
+    // (a box would run into the next group's rows).  Two buffers in turn, so
+    // one barrier a piece: it says that this buffer is full and the other
+    // one has been read.  Plain stores throughout made the epilogue, at 1750
+    // cycles a piece, what bounded the wide form.
     const int q = warp & 3;
     const int half = (warp - EPI_WARP0) >> 2;
     const int gt = threadIdx.x & 127;  // thread of the group
-    uint8_t* ebuf = smem + R::kEpiOffset + (size_t)half * EPI_BUF_BYTES;
-    const uint32_t ebuf_s = smem_u32(ebuf);
+    uint8_t* ebase = smem + R::kEpiOffset + (size_t)half * 2 * EPI_BUF_BYTES;
+    int buf = 0;
     int acc = 0;
     uint32_t acc_ph = 0;
-    for (Walk<BN> w(a, tail, ngroups, total); w.more(); w.next()) {
+    for (Walk<BN, CTAS> w(a, tail, ngroups, total); w.more(); w.next()) {
       const Unit& t = w.t;
       bool ok = wait_bar(smem_u32(&tail->tfull[acc]), acc_ph, abort_flag, deadline, status);
       if (!group_all(half, ok)) break;
@@ -551,10 +725,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       const int64_t ldo = a.ldo[kind];
       const int fmt = a.fmt[kind];
       bool released = false;
+      // the group's piece is in the buffer: whole ones go out by TMA
+      auto stored = [&](bool whole, int boxes, int kd, int col, int64_t row) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (gt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer has been read
+        group_sync(half);
+        if (whole && gt == 0) {
+          const uint32_t src = smem_u32(ebase + (buf ^ 1) * EPI_BUF_BYTES);
+          const int cols = a.swiglu ? a.M[kd] / 2 : a.M[kd];
+          for (int b = 0; b < boxes; b++)
+            if (col + 64 * b < cols) tma_store_2d(&a.tmO[kd], src + b * EPI_BOX_BYTES, col + 64 * b, (int)row);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      };
       auto release = [&]() {  // this warp has read the accumulator
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tail->tempty[acc]));
+        if (lane == 0) arrive_leader<CTAS>(smem_u32(&tail->tempty[acc]));
         released = true;
       };
       for (int c0 = half * 32; c0 < t.rows; c0 += 64) {
@@ -587,6 +774,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           }
           continue;
         }
+        uint8_t* ebuf = ebase + buf * EPI_BUF_BYTES;
+        buf ^= 1;
         uint32_t x[16], y[16];  // output rows 0..15 and 16..31 (SwiGLU: gate, up)
         tmem_ld_16x256b_x4(taddr + (uint32_t)c0, x);
         tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)c0, y);
@@ -599,18 +788,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             const float g0 = __uint_as_float(x[2 * i]), g1 = __uint_as_float(x[2 * i + 1]);
             h[i] = pack_bf16(silu_f(g0) * __uint_as_float(y[2 * i]), silu_f(g1) * __uint_as_float(y[2 * i + 1]));
           }
-          group_sync(half);  // the buffer's last rows have been read
-          const uint32_t at =
-              ebuf_s + (8 * (lane >> 4) + (lane & 7)) * EPI_PITCH_SWIGLU + (q * 16 + ((lane >> 3) & 1) * 8) * 2;
+          const uint32_t at = smem_u32(ebuf) + (8 * (lane >> 4) + (lane & 7)) * 128 +
+                              (((q * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
           stmatrix_x4_trans(at, h[0], h[1], h[2], h[3]);
-          stmatrix_x4_trans(at + 16 * EPI_PITCH_SWIGLU, h[4], h[5], h[6], h[7]);
-          group_sync(half);
+          stmatrix_x4_trans(at + 16 * 128, h[4], h[5], h[6], h[7]);
+          stored(nrows == 32 && fmt == OUT_ACT, 1, kind, t.mt * 64, t.row + c0);
           const int I = a.M[kind] / 2;
           if (fmt == OUT_MX4) {
             // a thread codes 16 of a token's 64 features, two threads a block
             const int r = gt >> 2, f = t.mt * 64 + (gt & 3) * 16;
-            const uint4* src = reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH_SWIGLU + (gt & 3) * 32);
-            const uint4 lo = src[0], hi = src[1];
+            const uint8_t* src = ebuf + r * 128;
+            const uint4 lo = *reinterpret_cast<const uint4*>(src + (((gt & 3) * 2 ^ (r & 7)) << 4));
+            const uint4 hi = *reinterpret_cast<const uint4*>(src + ((((gt & 3) * 2 + 1) ^ (r & 7)) << 4));
             const uint32_t hw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t m = 0;
 #pragma unroll
@@ -633,63 +822,163 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
               const int64_t at = (t.row + c0 + r) * ldo + f;
               *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out[kind]) + at / 2) =
                   make_uint2(code[0], code[1]);
-              if ((gt & 1) == 0) a.out_lo[kind][at / 32] = (uint8_t)sc;
+              if (CTAS == 1 && (gt & 1) == 0) a.out_lo[kind][at / 32] = (uint8_t)sc;
             }
-          } else {
+            if (CTAS == 2 && (gt & 1) == 0 && r < nrows) {
+              // into the next product's scale images; zeros past inter's
+              // end, so that no stray scale meets the zero columns there
+              const int blk = f / 32, nk2 = mx4_kblocks(I), rt = c0 + r;
+              uint8_t* img = a.out_lo[kind] + (int64_t)t.tile * nk2 * (R::S_BYTES / 2) + (rt >> 7) * 512 +
+                             (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
+              auto put = [&](int b, uint32_t v) {
+                if (b < nk2 * 4) img[(b >> 2) * (R::S_BYTES / 2) + (b & 3)] = (uint8_t)v;
+              };
+              put(blk, f < I ? sc : 0u);
+              if (t.mt == mx4_tiles(a.M[kind], 1) - 1) put(blk + 2, 0u);
+            }
+          } else if (nrows < 32) {
             const int r0 = gt >> 3, f = t.mt * 64 + (gt & 7) * 8;
 #pragma unroll
             for (int p = 0; p < 2; p++) {
               const int r = r0 + 16 * p;
               if (r < nrows && f + 8 <= I)
                 *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + f) =
-                    *reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH_SWIGLU + (gt & 7) * 16);
+                    *reinterpret_cast<const uint4*>(ebuf + r * 128 + (((gt & 7) ^ (r & 7)) << 4));
             }
           }
         } else {
-          group_sync(half);
-          const uint32_t at = ebuf_s + (lane & 7) * EPI_PITCH + (q * 32 + (lane >> 3) * 8) * 2;
+          const uint32_t at =
+              smem_u32(ebuf) + (q >> 1) * EPI_BOX_BYTES + (lane & 7) * 128 + ((((q & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll
           for (int i = 0; i < 4; i++)
-            stmatrix_x4_trans(at + 8 * i * EPI_PITCH,
+            stmatrix_x4_trans(at + 8 * i * 128,
                               pack_bf16(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
                               pack_bf16(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])),
                               pack_bf16(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])),
                               pack_bf16(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])));
-          group_sync(half);
-          const int r0 = gt >> 4, col = t.mt * 128 + (gt & 15) * 8;
+          stored(nrows == 32, 2, kind, t.mt * 128, t.row + c0);
+          if (nrows < 32) {
+            const int r0 = gt >> 4, col = t.mt * 128 + (gt & 15) * 8;
 #pragma unroll
-          for (int p = 0; p < 4; p++) {
-            const int r = r0 + 8 * p;
-            if (r < nrows && col + 8 <= a.M[kind])
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + col) =
-                  *reinterpret_cast<const uint4*>(ebuf + r * EPI_PITCH + (gt & 15) * 16);
+            for (int p = 0; p < 4; p++) {
+              const int r = r0 + 8 * p;
+              if (r < nrows && col + 8 <= a.M[kind])
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + col) =
+                    *reinterpret_cast<const uint4*>(ebuf + ((gt >> 3) & 1) * EPI_BOX_BYTES + r * 128 +
+                                                    (((gt & 7) ^ (r & 7)) << 4));
+            }
           }
         }
       }
       if (!released) release();  // no columns of this unit were this group's
       if (++acc == 2) { acc = 0; acc_ph ^= 1; }
     }
+    if (gt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // written before the CTA leaves
   }
 
   tc_fence_before();
   __syncthreads();
+  if (CTAS == 2) cluster_sync();  // no remote arrive, copy or MMA of the pair is outstanding past this point
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(R::TMEM_COLS));
+    if (CTAS == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(R::TMEM_COLS));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(R::TMEM_COLS));
   }
 }
 
-template <int BN>
-cudaError_t launch_variant(const LaunchCtx& lc, const Mx4GemmArgs& a, int64_t units) {
-  static std::atomic<int> attr_done[kMaxCachedDevices];
-  const cudaError_t e = smem_attr_once(k_mx4_gemm<BN>, (int)Ring<BN>::kSmemBytes, attr_done);
-  if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, lc.num_sms));
-  return launch_k(lc, k_mx4_gemm<BN>, grid, NUM_THREADS, Ring<BN>::kSmemBytes, a);
+constexpr int kWide = 192, kNarrow = 64;
+
+// ---------------------------------------------------------------------------
+// Token scales of the wide form: the plain rows' bytes into the images
+// tcgen05.cp takes, [token tile][128-column block][1024 bytes] (row r's four
+// bytes at (r / 128) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4), so that a
+// stage's are one copy.  Gathering them inside the product kept six warps
+// and a proxy fence a stage busy: 20 us of a 150 us product.  One CTA per
+// token tile.
+// ---------------------------------------------------------------------------
+constexpr int kImgThreads = 256;
+struct ImageArgs {
+  const uint8_t* xs;
+  int64_t x_rows;
+  const int32_t* offsets;  // NULL: one group of all rows
+  int n_groups, pitch, nk;
+  uint8_t* image;
+};
+__global__ void __launch_bounds__(kImgThreads) k_mx4_scale_image(const __grid_constant__ ImageArgs a) {
+  __shared__ int wsum[kImgThreads / 32];
+  __shared__ int64_t tile_row;
+  __shared__ int tile_rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile = (int)blockIdx.x;
+  if (threadIdx.x == 0) tile_rows = 0;
+  grid_dep_wait();
+  grid_dep_launch();
+  int64_t lo = 0, hi = 0;
+  if ((int)threadIdx.x < a.n_groups) {
+    if (a.offsets) {
+      lo = min(max((int64_t)a.offsets[threadIdx.x], (int64_t)0), a.x_rows);
+      hi = min(max((int64_t)a.offsets[threadIdx.x + 1], lo), a.x_rows);
+    } else {
+      hi = a.x_rows;
+    }
+  }
+  const int tiles = (int)((hi - lo + kWide - 1) / kWide);
+  int incl = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; w++) incl += wsum[w];
+  if (tile < incl && tile >= incl - tiles) {
+    const int nt = tile - (incl - tiles);
+    tile_row = lo + (int64_t)nt * kWide;
+    tile_rows = (int)min((int64_t)kWide, hi - lo - (int64_t)nt * kWide);
+  }
+  __syncthreads();
+  const int rows = tile_rows;
+  if (rows == 0) return;  // past the last tile
+  const uint8_t* src = a.xs + tile_row * a.pitch;
+  uint8_t* dst = a.image + (int64_t)tile * a.nk * 1024;
+  // a thread: the four rows l + 32 j of one half image, 16 bytes
+  for (int i = threadIdx.x; i < a.nk * 64; i += kImgThreads) {
+    const int l = i & 31, b = (i >> 5) & 1, c = i >> 6;
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int r = b * 128 + j * 32 + l;
+      q[j] = 0u;
+      if (r >= rows) continue;
+      const uint8_t* p = src + (int64_t)r * a.pitch + 4 * c;
+      if ((a.pitch & 3) == 0) {
+        q[j] = *reinterpret_cast<const uint32_t*>(p);
+      } else {
+        for (int k = 0; k < 4; k++)
+          if (4 * c + k < a.pitch) q[j] |= (uint32_t)p[k] << (8 * k);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + c * 1024 + b * 512 + l * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+  }
 }
 
-constexpr int kWide = 192, kNarrow = 64;
+template <int BN, int CTAS>
+cudaError_t launch_variant(const LaunchCtx& lc, const Mx4GemmArgs& a, int64_t units) {
+  constexpr size_t smem = Ring<BN, CTAS>::kSmemBytes;
+  static std::atomic<int> attr_done[kMaxCachedDevices];
+  const cudaError_t e = smem_attr_once(k_mx4_gemm<BN, CTAS>, (int)smem, attr_done);
+  if (e != cudaSuccess) return e;
+  if (CTAS == 2) {
+    const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>((units + 1) / 2, lc.num_sms / 2));
+    return launch_k_cluster(lc, k_mx4_gemm<BN, CTAS>, 2 * pairs, NUM_THREADS, smem, 2, a);
+  }
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, lc.num_sms));
+  return launch_k(lc, k_mx4_gemm<BN, CTAS>, grid, NUM_THREADS, smem, a);
+}
 
 }  // namespace
 
@@ -700,10 +989,11 @@ constexpr int kWide = 192, kNarrow = 64;
 int mx4_token_tile(int64_t rows, int groups) { return rows <= 48 * (int64_t)groups ? kNarrow : kWide; }
 
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units) {
-  return bn == kNarrow ? launch_variant<kNarrow>(lc, a, units) : launch_variant<kWide>(lc, a, units);
+  return bn == kNarrow ? launch_variant<kNarrow, 1>(lc, a, units) : launch_variant<kWide, 2>(lc, a, units);
 }
 
-int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn) {
+static int encode_box(CUtensorMap* m, CUtensorMapDataType type, int es, const void* base, int64_t row_bytes,
+                      int64_t pitch, int64_t rows, int box_bytes, int box_rows, CUtensorMapSwizzle swizzle) {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   std::call_once(once, [] {
@@ -715,18 +1005,51 @@ int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int 
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!encode) return AFD_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)std::max<int64_t>(rows, 1)};
-  const cuuint64_t str[1] = {(cuuint64_t)(K / 2)};
-  const cuuint32_t box[2] = {BK / 2, (cuuint32_t)bn};
+  const cuuint64_t dims[2] = {(cuuint64_t)(row_bytes / es), (cuuint64_t)std::max<int64_t>(rows, 1)};
+  const cuuint64_t str[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / es), (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, str, box, estr,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = encode(m, type, 2, const_cast<void*>(base), dims, str, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
-    fprintf(stderr, "afd: cuTensorMapEncodeTiled failed (%d) for MXFP4 rows\n", (int)r);
+    fprintf(stderr, "afd: cuTensorMapEncodeTiled failed (%d) for MXFP4 operands\n", (int)r);
     return AFD_ERR_CUDA;
   }
   return AFD_OK;
+}
+
+// token rows: boxes of one stage's columns x the rows one CTA holds
+int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn) {
+  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, K / 2, rows, BK / 2, bn == kNarrow ? Ring<kNarrow, 1>::B_ROWS : Ring<kWide, 2>::B_ROWS,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scale images of `rows` rows in `groups` groups over K columns (wide form;
+// 0 bytes for the narrow one)
+static int64_t image_tiles(int64_t rows, int groups) { return (rows + kWide - 1) / kWide + std::min<int64_t>(groups, rows); }
+int64_t mx4_image_bytes(int64_t rows, int groups, int K) {
+  return mx4_token_tile(rows, groups) == kWide ? image_tiles(rows, groups) * mx4_kblocks(K) * 1024 : 0;
+}
+int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
+  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
+                    Ring<kWide, 2>::S_BYTES / 1024, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
+                              int groups, int K, uint8_t* image) {
+  const ImageArgs a{scales, rows, offsets, groups, K / 32, mx4_kblocks(K), image};
+  return launch_k(lc, k_mx4_scale_image, (unsigned)image_tiles(rows, groups), kImgThreads, 0, a);
+}
+// bf16 output rows: boxes of 64 columns x 32 rows
+int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo) {
+  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, 2 * (int64_t)cols, 2 * ldo, rows, 128, 32,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// packed weight: boxes of one block (the pair's copies count on the leader's
+// barrier, which only tensor copies can)
+int encode_mx4_weight(CUtensorMap* m, const void* packed, int64_t bytes) {
+  constexpr int line = kMx4BlkBytes / kBlkLines;
+  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line, kBlkLines,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 extern "C" int afd_mx4_poll_status(void* cuda_stream) {

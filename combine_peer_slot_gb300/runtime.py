@@ -326,7 +326,8 @@ class _Host:
         self.raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         L = A.lib()
         self.select, self.quantize, self.dequantize = L.afd_route_select, L.afd_mx4_quantize, L.afd_mx4_dequantize
-        self.gemm, self.ffn, self.ffn_workspace = L.afd_mx4_gemm, L.afd_mx4_ffn, L.afd_mx4_ffn_workspace
+        self.gemm, self.gemm_workspace = L.afd_mx4_gemm, L.afd_mx4_gemm_workspace
+        self.ffn, self.ffn_workspace = L.afd_mx4_ffn, L.afd_mx4_ffn_workspace
 
 
 _host = None
@@ -479,7 +480,17 @@ def _output(h, x, cols, out_dtype, out, dev):
     return out, out.stride(0) if x.rows > 1 else cols, code
 
 
-def mx4_gemm(x, offsets, weight, out_dtype=None, out=None):
+def _scratch(h, workspace, need, dev):
+    """(pointer, bytes, what keeps it alive until the call is enqueued)"""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if need <= 0:
+        return 0, 0, None
+    t = h.empty(need, dtype=h.uint8, device=dev)
+    return t.data_ptr(), need, t
+
+
+def mx4_gemm(x, offsets, weight, out_dtype=None, out=None, workspace=None):
     """afd_mx4_gemm of the rows x (Mx4) grouped by offsets int32 [E + 1] with
     weight (Mx4Weight): [rows, M], or [rows, M / 2] = silu(gate) * up for a
     swiglu weight.  Rows in no group are not written (out: the caller's)."""
@@ -489,9 +500,10 @@ def mx4_gemm(x, offsets, weight, out_dtype=None, out=None):
         _bad(f"rows of {x.cols} columns, weight of {weight.K}")
     dev, stream = _device(x.codes)
     out, ldo, code = _output(h, x, weight.M // 2 if weight.swiglu else weight.M, out_dtype, out, dev)
+    ws, ws_bytes, keep = _scratch(h, workspace, h.gemm_workspace(x.rows, weight.experts, weight.K), dev)
     rc = h.gemm(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), weight.experts,
                 weight.packed.data_ptr(), weight.M, weight.K, 1 if weight.swiglu else 0, code, out.data_ptr(), ldo,
-                stream)
+                ws, ws_bytes, stream)
     if rc:
         raise A.AfdError(rc, "afd_mx4_gemm")
     return out
@@ -508,15 +520,10 @@ def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
     _rows_int32(h, offsets, wd.experts + 1, "offsets")
     dev, stream = _device(x.codes)
     out, ldo, code = _output(h, x, hidden, out_dtype, out, dev)
-    need = h.ffn_workspace(x.rows, inter)
-    if workspace is None:
-        workspace = h.empty(max(need, 1), dtype=h.uint8, device=dev)
-        have = need
-    else:
-        have = workspace.numel() * workspace.element_size()
+    ws, ws_bytes, keep = _scratch(h, workspace, h.ffn_workspace(x.rows, wd.experts, hidden, inter), dev)
     rc = h.ffn(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), wd.experts,
                w13.packed.data_ptr(), wd.packed.data_ptr(), hidden, inter, code, out.data_ptr(), ldo,
-               workspace.data_ptr(), have, stream)
+               ws, ws_bytes, stream)
     if rc:
         raise A.AfdError(rc, "afd_mx4_ffn")
     return out

@@ -715,10 +715,16 @@ int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_exp
  *   weight         afd_mx4_pack_weight of [num_experts, M, K] with this swiglu
  *   out            device [n_rows, M], row pitch ldo (ldo % 8 == 0), 16-byte
  *                  aligned; swiglu: bf16 [n_rows, M / 2], silu(gate) * up
+ *   workspace      device, 256-byte aligned, at least afd_mx4_gemm_workspace
+ *                  bytes (host only; 0 where the groups are small, -1 for
+ *                  dimensions outside the limits), else AFD_ERR_CAPACITY;
+ *                  one call at a time may use it
  * swiglu with AFD_DTYPE_F32: AFD_ERR_UNSUPPORTED. */
+int64_t afd_mx4_gemm_workspace(int64_t n_rows, int num_experts, int K);
 int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
                  const int32_t* offsets, int num_experts, const void* weight, int M, int K,
-                 int swiglu, int out_dtype, void* out, int64_t ldo, void* cuda_stream);
+                 int swiglu, int out_dtype, void* out, int64_t ldo, void* workspace,
+                 int64_t workspace_bytes, void* cuda_stream);
 
 /* The expert FFN: the SwiGLU product with w13 (packed [num_experts, 2 inter,
  * hidden], swiglu), its bf16 rows coded again (AFD_MX4_SCALE_FLOOR), the
@@ -727,7 +733,7 @@ int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
  * workspace: device, 256-byte aligned, at least afd_mx4_ffn_workspace bytes
  * (host only; -1 for dimensions outside the limits), else AFD_ERR_CAPACITY;
  * one call at a time may use it. */
-int64_t afd_mx4_ffn_workspace(int64_t n_rows, int inter);
+int64_t afd_mx4_ffn_workspace(int64_t n_rows, int num_experts, int hidden, int inter);
 int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
                 const int32_t* offsets, int num_experts, const void* w13, const void* wd,
                 int hidden, int inter, int out_dtype, void* out, int64_t ldo, void* workspace,

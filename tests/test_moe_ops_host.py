@@ -92,6 +92,18 @@ def test_gemm_refuses(bad):
     assert A.afd_mx4_gemm(**{**GEMM, **bad}) == A.AFD_ERR_ARG
 
 
+def test_gemm_workspace():
+    assert A.afd_mx4_gemm_workspace(96, 2, 128) == 0        # 48 rows a group: nothing needed
+    n = A.afd_mx4_gemm_workspace(400, 2, 320)
+    assert n == (3 + 2) * 3 * 1024                          # token tiles x 128-column blocks of images
+    for bad in ((-1, 2, 128), (4, 0, 128), (4, 257, 128), (4, 2, 48)):
+        assert A.afd_mx4_gemm_workspace(*bad) == -1, bad
+    big = {**GEMM, "n_rows": 400, "K": 320}
+    assert A.afd_mx4_gemm(**{**big, "workspace": P, "workspace_bytes": n - 1}) == A.AFD_ERR_CAPACITY
+    assert A.afd_mx4_gemm(**{**big, "workspace": 0, "workspace_bytes": n}) == A.AFD_ERR_ARG
+    assert A.afd_mx4_gemm(**{**big, "workspace": P + 128, "workspace_bytes": n}) == A.AFD_ERR_ARG
+
+
 def test_gemm_swiglu_is_bf16():
     assert A.afd_mx4_gemm(**{**GEMM, "swiglu": True, "out_dtype": A.AFD_DTYPE_F32}) == A.AFD_ERR_UNSUPPORTED
 
@@ -109,8 +121,9 @@ def test_ffn_refuses(bad):
 
 
 def test_ffn_workspace():
-    n = A.afd_mx4_ffn_workspace(100, 96)
+    n = A.afd_mx4_ffn_workspace(100, 2, 128, 96)
     assert n > 0 and n % 256 == 0
-    assert A.afd_mx4_ffn_workspace(0, 96) == 0
-    assert A.afd_mx4_ffn_workspace(-1, 96) == -1 and A.afd_mx4_ffn_workspace(4, 40) == -1
+    assert A.afd_mx4_ffn_workspace(0, 2, 128, 96) == 0
+    for bad in ((-1, 2, 128, 96), (4, 2, 128, 40), (4, 0, 128, 96), (4, 257, 128, 96), (4, 2, 130, 96)):
+        assert A.afd_mx4_ffn_workspace(*bad) == -1, bad
     assert A.afd_mx4_ffn(**{**FFN, "n_rows": 100, "inter": 96, "workspace_bytes": n - 1}) == A.AFD_ERR_CAPACITY

@@ -314,7 +314,7 @@ def test_streams_graphs_and_workspaces():
     src = [xa.clone(), xb.clone()]
     graphs, outs, keep = [], [], []
     for s in src:
-        ws = torch.empty(A.afd_mx4_ffn_workspace(141, 96), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(A.afd_mx4_ffn_workspace(141, 4, 256, 96), dtype=torch.uint8, device="cuda")
         gr = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gr):
             outs.append(R.mx4_ffn(R.mx4_quantize(s), off, w13, wd, workspace=ws))
