@@ -35,8 +35,7 @@ namespace {
 
 __device__ int32_t g_mx4_status;  // calls without a context
 
-constexpr int BK = 256;               // columns per stage
-constexpr int A_BYTES = 2 * kMx4BlkBytes;
+constexpr int BOX = 256;              // columns of one token box (128 bytes of codes)
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 8;          // a multiple of 4: a warp reads the TMEM lanes of its number mod 4
 constexpr int NUM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
@@ -51,15 +50,22 @@ constexpr int MAX_GROUPS = 257;       // 256 experts and the shared rows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // A stage's word for the MMA issuer, written by the copies' producer: bits
-// 0-8 the instruction's N, 9-11 the 64-column steps, then first / last stage
+// 0-8 the instruction's N, 9-12 the 64-column steps, then first / last stage
 // of its unit, and no more stages.  The issuer follows these words alone: it
 // is the one thread of control on the tensor pipe's critical path, and
 // finding its own units there cost 280 cycles a stage.
-constexpr uint32_t INFO_FIRST = 1u << 12, INFO_LAST = 1u << 13, INFO_STOP = 1u << 14;
+constexpr uint32_t INFO_FIRST = 1u << 13, INFO_LAST = 1u << 14, INFO_STOP = 1u << 15;
 
 template <int BN, int CTAS>
 struct Ring {
-  static constexpr int STAGES = CTAS == 2 ? 5 : 7;
+  // Columns per stage: 256 in seven stages, or 512 in three.  The wide form's
+  // stages are short (four MMAs of 96 cycles per 256 columns) beside what a
+  // stage costs in barriers and issue: with five of 256 columns that was 580
+  // of its cycles.
+  static constexpr int BK = CTAS == 2 ? 512 : 256;
+  static constexpr int STAGES = CTAS == 2 ? 3 : 7;
+  static constexpr int BLKS = BK / kMx4BlkCols;          // weight blocks per stage
+  static constexpr int A_BYTES = BLKS * kMx4BlkBytes;
   // Narrow: warps that fill the token scales, a stage each in turn.  No more
   // than stages: a warp that has filled stage i waits next for the release of
   // i + SF_WARPS - STAGES, and a parity wait tells a phase from the one
@@ -68,15 +74,18 @@ struct Ring {
   static_assert(SF_WARPS <= STAGES && 2 + SF_WARPS <= EPI_WARP0, "scale warps");
   static constexpr int NB = (BN + 127) / 128;            // 128-row scale images per 128 columns
   static constexpr int B_ROWS = BN / CTAS;               // token rows whose codes a CTA holds
-  static constexpr int B_BYTES = B_ROWS * (BK / 2);
-  static constexpr int S_BYTES = 2 * NB * 512;
+  static constexpr int X_BYTES = B_ROWS * (BOX / 2);     // one token box
+  static constexpr int B_BYTES = BK / BOX * X_BYTES;
+  static constexpr int S_BYTES = BLKS * NB * 512;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + S_BYTES;
-  // TMEM columns: two accumulators, then per stage the weight scales (2 x 4)
-  // and the token scales (2 x 4 NB)
-  static constexpr int SF_COLS = 8 + 8 * NB;
+  // TMEM columns: two accumulators, then slots of a stage's weight scales (4
+  // per block) and token scales (4 NB); narrow: a slot per stage, wide: two
+  // in turn, which is all that 512 columns leave room for
+  static constexpr int SF_SLOTS = CTAS == 2 ? 2 : STAGES;
+  static constexpr int SF_COLS = BLKS * (4 + 4 * NB);
   static constexpr int SF_BASE = 2 * BN;
-  static constexpr int TMEM_COLS = SF_BASE + STAGES * SF_COLS <= 256 ? 256 : 512;
-  static_assert(SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "TMEM columns");
+  static constexpr int TMEM_COLS = SF_BASE + SF_SLOTS * SF_COLS <= 256 ? 256 : 512;
+  static_assert(SF_BASE + SF_SLOTS * SF_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(STAGE_BYTES % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle alignment");
   struct Tail {
     uint64_t full[STAGES];
@@ -196,12 +205,12 @@ __device__ __forceinline__ void commit_local(uint32_t elected, uint32_t bar) {
     commit<1>(elected, bar);
 }
 // the scales of 128 columns: the weight's image, then the tokens'
-template <int CTAS, int NB>
+template <int CTAS, int NB, int BLKS>
 __device__ __forceinline__ void issue_scales(uint32_t el, int c, uint32_t sa, uint32_t ss, uint32_t sf) {
   cp_scales<CTAS>(el, sf + 4 * c, desc(kDescScales, sa + ((c * kMx4BlkBytes + kMx4BlkCodes) >> 4)));
 #pragma unroll
   for (int b = 0; b < NB; b++)
-    cp_scales<CTAS>(el, sf + 8 + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
+    cp_scales<CTAS>(el, sf + 4 * BLKS + 4 * (c * NB + b), desc(kDescScales, ss + (c * NB + b) * 32));
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int c0, int c1) {
@@ -511,30 +520,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
         const int64_t blk0 =  // the weight's blocks of this tile (past an odd edge: the last tile's again)
             ((int64_t)(t.kind ? 0 : t.group) * m_tiles + min(t.mt, m_tiles - 1)) * nk;
-        for (int kb = 0; kb * 2 < nk; kb++) {
+        for (int kb = 0; kb * R::BLKS < nk; kb++) {
           if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
           const uint32_t full = smem_u32(&tail->full[s]);
-          const int blks = min(2, nk - 2 * kb);
+          const int blks = min(R::BLKS, nk - R::BLKS * kb);
+          const int boxes = (blks + 1) / 2;  // of 256 columns; past a lone last block: zeros, or not used
           if (leader) {
-            const int left = (a.K[t.kind] - kb * BK + 63) / 64;
-            tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, 4) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
-                            (left <= 4 ? INFO_LAST : 0u);
-            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + R::B_BYTES + (CTAS == 2 ? R::S_BYTES : 0)));
+            const int left = (a.K[t.kind] - kb * R::BK + 63) / 64;
+            tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, R::BK / 64) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
+                            (left <= R::BK / 64 ? INFO_LAST : 0u);
+            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + boxes * R::X_BYTES +
+                                         (CTAS == 2 ? boxes * 2 * NB * 512 : 0)));
           }
           const uint32_t sa = smem_base + s * R::STAGE_BYTES;
+          const uint32_t sx = sa + R::A_BYTES;
           if (CTAS == 2) {
             const uint32_t full_leader = map_to_rank(full, 0);
             for (int b = 0; b < blks; b++)
-              tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW[t.kind], 0,
-                               (int)(blk0 + 2 * kb + b) * kBlkLines, full_leader);
-            tma_pair_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2),
-                             (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
-            // (a lone last block: its second half is the next tile's, copied and not used)
-            tma_pair_load_2d(sa + A_BYTES + R::B_BYTES, &a.tmS[t.kind], 0, (t.tile * nk + 2 * kb) * kImgLines,
-                             full_leader);
+              tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW[t.kind], 0, (int)(blk0 + R::BLKS * kb + b) * kBlkLines,
+                               full_leader);
+            for (int b = 0; b < boxes; b++) {
+              tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX[t.kind], (kb * (R::BK / BOX) + b) * (BOX / 2),
+                               (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
+              tma_pair_load_2d(sx + R::B_BYTES + b * 2 * NB * 512, &a.tmS[t.kind], 0,
+                               (t.tile * nk + R::BLKS * kb + 2 * b) * kImgLines, full_leader);
+            }
           } else {
-            bulk_load(sa, a.w[t.kind] + (blk0 + 2 * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
-            tma_load_2d(sa + A_BYTES, &a.tmX[t.kind], kb * (BK / 2), (int)t.row, full);
+            bulk_load(sa, a.w[t.kind] + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
+            tma_load_2d(sx, &a.tmX[t.kind], kb * (BOX / 2), (int)t.row, full);
           }
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
@@ -558,7 +571,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       // otherwise stand between the stages (about 330 of 860 cycles a stage).
       int s = 0;
       uint32_t ph = 0;
-      int acc = 0;
+      int acc = 0, slot = 0;
       uint32_t acc_ph = 0;
       bool ready = false;
       uint32_t word = 0;
@@ -581,36 +594,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const uint32_t id0 = idesc_mx4<CTAS>((int)(info & 511u), 0), id2 = id0 | idesc_mx4<CTAS>(0, 2);
         const uint32_t d = tm + (uint32_t)(acc * BN);
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
-        const uint32_t sb = sa + (A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
-        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
-        const int steps = (int)(info >> 9) & 7;
+        const uint32_t sb = sa + (R::A_BYTES >> 4), ss = sb + (R::B_BYTES >> 4);
+        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + slot * R::SF_COLS);
+        const int steps = (int)(info >> 9) & 15;
         const uint32_t more = (info & INFO_FIRST) ? 0u : 1u;
         auto scales = [&](int c) {  // of 128 columns (wide: the scale warp's part)
-          if (CTAS == 1) issue_scales<CTAS, NB>(el, c, sa, ss, sf);
+          if (CTAS == 1) issue_scales<CTAS, NB, R::BLKS>(el, c, sa, ss, sf);
         };
         auto mma = [&](int kk) {    // of 64 columns
           const int c = kk >> 1, o = kk & 1;
-          mma_mx4<CTAS>(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)), desc(kDescTokens, sb + kk * 2),
-                  o ? id2 : id0, sf + 4 * c, sf + 8 + 4 * c * NB, kk > 0 ? 1u : more);
+          mma_mx4<CTAS>(el, d, desc(kDescWeight, sa + ((c * kMx4BlkBytes + o * 32) >> 4)),
+                        desc(kDescTokens, sb + (kk >> 2) * (R::X_BYTES >> 4) + (kk & 3) * 2), o ? id2 : id0, sf + 4 * c,
+                        sf + 4 * R::BLKS + 4 * c * NB, kk > 0 ? 1u : more);
         };
-        if (steps == 4) {  // no branch between the instructions of a whole stage
-          scales(0);
-          scales(1);
+        constexpr int FULL = R::BK / 64;
+        if (steps == FULL) {  // no branch between the instructions of a whole stage
+#pragma unroll
+          for (int c = 0; c < R::BLKS; c++) scales(c);
           ready = __all_sync(0xffffffffu, test != 0);
-          mma(0);
-          mma(1);
+#pragma unroll
+          for (int kk = 0; kk < FULL / 2; kk++) mma(kk);
           word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
-          mma(2);
-          mma(3);
-        } else {           // the unit's last columns
-          scales(0);
-          if (steps > 2) scales(1);
+#pragma unroll
+          for (int kk = FULL / 2; kk < FULL; kk++) mma(kk);
+        } else {              // the unit's last columns
+#pragma unroll
+          for (int c = 0; c < R::BLKS; c++)
+            if (2 * c < steps) scales(c);
           ready = __all_sync(0xffffffffu, test != 0);
           word = *(volatile uint32_t*)&tail->info[s1];
-          mma(0);
-          if (steps > 1) mma(1);
-          if (steps > 2) mma(2);
+#pragma unroll
+          for (int kk = 0; kk < FULL - 1; kk++)
+            if (kk < steps) mma(kk);
         }
+        if (++slot == R::SF_SLOTS) slot = 0;
         commit<CTAS>(el, smem_u32(&tail->empty[s]));
         s = s1;
         ph = ph1;
@@ -632,9 +649,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     if (leader) {
       const uint32_t el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      int s = 0;
+      int s = 0, n = 0;
       uint32_t ph = 0;
-      for (;;) {
+      for (;; n++) {
         if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
         const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
         if (info & INFO_STOP) {
@@ -643,10 +660,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
         tc_fence_after();
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
-        const uint32_t ss = sa + ((A_BYTES + R::B_BYTES) >> 4);
-        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + s * R::SF_COLS);
-        issue_scales<CTAS, NB>(el, 0, sa, ss, sf);
-        if (((info >> 9) & 7u) > 2u) issue_scales<CTAS, NB>(el, 1, sa, ss, sf);
+        const uint32_t ss = sa + ((R::A_BYTES + R::B_BYTES) >> 4);
+        const uint32_t sf = tm + (uint32_t)(R::SF_BASE + (n % R::SF_SLOTS) * R::SF_COLS);
+        if (n >= R::SF_SLOTS) {  // the slot's last stage has been multiplied
+          const int m = n - R::SF_SLOTS;
+          if (!warp_wait(smem_u32(&tail->empty[m % STAGES]), (uint32_t)(m / STAGES) & 1u, abort_flag, deadline, status))
+            break;
+          tc_fence_after();
+        }
+        const int steps = (int)(info >> 9) & 15;
+#pragma unroll
+        for (int c = 0; c < R::BLKS; c++)
+          if (2 * c < steps) issue_scales<CTAS, NB, R::BLKS>(el, c, sa, ss, sf);
         commit_local<CTAS>(el, smem_u32(&tail->sfull[s]));
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
@@ -659,7 +684,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     auto advance = [&](int n) {  // n stages on
       kb += n;
       while (w.more()) {
-        const int nkb = (a.K[w.t.kind] + BK - 1) / BK;
+        const int nkb = (a.K[w.t.kind] + R::BK - 1) / R::BK;
         if (kb < nkb) break;
         kb -= nkb;
         w.next();
@@ -679,7 +704,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       bool ok = wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      uint8_t* ss = smem + (size_t)s * R::STAGE_BYTES + A_BYTES + R::B_BYTES;
+      uint8_t* ss = smem + (size_t)s * R::STAGE_BYTES + R::A_BYTES + R::B_BYTES;
 #pragma unroll
       for (int c = 0; c < 2; c++)
 #pragma unroll
@@ -828,10 +853,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
               // into the next product's scale images; zeros past inter's
               // end, so that no stray scale meets the zero columns there
               const int blk = f / 32, nk2 = mx4_kblocks(I), rt = c0 + r;
-              uint8_t* img = a.out_lo[kind] + (int64_t)t.tile * nk2 * (R::S_BYTES / 2) + (rt >> 7) * 512 +
+              uint8_t* img = a.out_lo[kind] + (int64_t)t.tile * nk2 * (NB * 512) + (rt >> 7) * 512 +
                              (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
               auto put = [&](int b, uint32_t v) {
-                if (b < nk2 * 4) img[(b >> 2) * (R::S_BYTES / 2) + (b & 3)] = (uint8_t)v;
+                if (b < nk2 * 4) img[(b >> 2) * (NB * 512) + (b & 3)] = (uint8_t)v;
               };
               put(blk, f < I ? sc : 0u);
               if (t.mt == mx4_tiles(a.M[kind], 1) - 1) put(blk + 2, 0u);
@@ -1021,7 +1046,7 @@ static int encode_box(CUtensorMap* m, CUtensorMapDataType type, int es, const vo
 
 // token rows: boxes of one stage's columns x the rows one CTA holds
 int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn) {
-  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, K / 2, rows, BK / 2, bn == kNarrow ? Ring<kNarrow, 1>::B_ROWS : Ring<kWide, 2>::B_ROWS,
+  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, K / 2, K / 2, rows, BOX / 2, bn == kNarrow ? Ring<kNarrow, 1>::B_ROWS : Ring<kWide, 2>::B_ROWS,
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // Scale images of `rows` rows in `groups` groups over K columns (wide form;
@@ -1032,7 +1057,7 @@ int64_t mx4_image_bytes(int64_t rows, int groups, int K) {
 }
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
-                    Ring<kWide, 2>::S_BYTES / 1024, CU_TENSOR_MAP_SWIZZLE_NONE);
+                    2, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
                               int groups, int K, uint8_t* image) {
