@@ -344,7 +344,7 @@ static int product(LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, u
   const int64_t units = (int64_t)mx4_tiles(M, swiglu) * ((n_rows + bn - 1) / bn + std::min<int64_t>(E, n_rows));
   if (units >= (int64_t)1 << 31 || img / 128 >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
   int rc = encode_mx4_rows(&a.tmX[0], codes, n_rows, K, bn);
-  if (!rc) rc = encode_mx4_weight(&a.tmW[0], w, mx4_weight_bytes(E, M, K, swiglu));
+  if (!rc && img) rc = encode_mx4_weight(&a.tmW[0], &a.tmW1[0], w, mx4_weight_bytes(E, M, K, swiglu));
   if (!rc && fmt == OUT_ACT) rc = encode_mx4_out(&a.tmO[0], out, n_rows, swiglu ? M / 2 : M, ldo);
   if (!rc && img) rc = encode_mx4_images(&a.tmS[0], image, img);
   if (rc) return rc;

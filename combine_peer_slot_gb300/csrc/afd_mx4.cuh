@@ -41,7 +41,7 @@ inline int64_t mx4_weight_bytes(int64_t E, int64_t M, int K, int swiglu) {
 #define OUT_MX4 3  // SwiGLU only: codes in out, scales in out_lo (ldo % 32 == 0)
 struct Mx4GemmArgs {
   CUtensorMap tmX[2];        // codes of the rows (encode_mx4_rows)
-  CUtensorMap tmW[2];        // packed weights (encode_mx4_weight); the wide form's
+  CUtensorMap tmW[2], tmW1[2];  // packed weights (encode_mx4_weight); the wide form's
   CUtensorMap tmS[2];        // their scale images (encode_mx4_images); the wide form's
   const uint8_t* xs[2];      // their scales [x_rows][K / 32]; the narrow form's
   int64_t x_rows[2];
@@ -69,7 +69,7 @@ int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
                               int groups, int K, uint8_t* image);
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo);
-int encode_mx4_weight(CUtensorMap* m, const void* packed, int64_t bytes);
+int encode_mx4_weight(CUtensorMap* stage, CUtensorMap* one, const void* packed, int64_t bytes);
 
 cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx, int64_t x_rows, int f32,
                                 const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,

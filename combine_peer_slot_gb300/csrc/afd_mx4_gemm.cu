@@ -508,9 +508,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   volatile int* abort_flag = &tail->abort_flag;
   const uint32_t smem_base = smem_u32(smem);
 
-  if (warp == 0) {
+  if (warp == 0 || (CTAS == 2 && warp == 3)) {
     if (lane == 0) {
-      // ------------------------------ copies
+      // ------------------------------ copies (wide: warp 0 the weight's, warp
+      // 3 the tokens'; one thread issuing them all was on the ring's path)
+      const bool weights = warp == 0, tokens = CTAS == 1 || warp == 3;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -525,25 +527,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           const uint32_t full = smem_u32(&tail->full[s]);
           const int blks = min(R::BLKS, nk - R::BLKS * kb);
           const int boxes = (blks + 1) / 2;  // of 256 columns; past a lone last block: zeros, or not used
-          if (leader) {
+          const uint32_t sa = smem_base + s * R::STAGE_BYTES;
+          const uint32_t sx = sa + R::A_BYTES;
+          if (weights && leader) {
             const int left = (a.K[t.kind] - kb * R::BK + 63) / 64;
             tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, R::BK / 64) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
                             (left <= R::BK / 64 ? INFO_LAST : 0u);
-            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + boxes * R::X_BYTES +
-                                         (CTAS == 2 ? boxes * 2 * NB * 512 : 0)));
+            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + boxes * R::X_BYTES + (CTAS == 2 ? R::S_BYTES : 0)));
           }
-          const uint32_t sa = smem_base + s * R::STAGE_BYTES;
-          const uint32_t sx = sa + R::A_BYTES;
           if (CTAS == 2) {
             const uint32_t full_leader = map_to_rank(full, 0);
-            for (int b = 0; b < blks; b++)
-              tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW[t.kind], 0, (int)(blk0 + R::BLKS * kb + b) * kBlkLines,
+            const int line = (int)(blk0 + R::BLKS * kb) * kBlkLines;
+            if (weights && blks == R::BLKS)
+              tma_pair_load_2d(sa, &a.tmW[t.kind], 0, line, full_leader);
+            else if (weights)
+              for (int b = 0; b < blks; b++)
+                tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW1[t.kind], 0, line + b * kBlkLines, full_leader);
+            if (tokens) {
+              for (int b = 0; b < boxes; b++)
+                tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX[t.kind], (kb * (R::BK / BOX) + b) * (BOX / 2),
+                                 (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
+              // (past the tile's last block: the next tile's images, not used)
+              tma_pair_load_2d(sx + R::B_BYTES, &a.tmS[t.kind], 0, (t.tile * nk + R::BLKS * kb) * kImgLines,
                                full_leader);
-            for (int b = 0; b < boxes; b++) {
-              tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX[t.kind], (kb * (R::BK / BOX) + b) * (BOX / 2),
-                               (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
-              tma_pair_load_2d(sx + R::B_BYTES + b * 2 * NB * 512, &a.tmS[t.kind], 0,
-                               (t.tile * nk + R::BLKS * kb + 2 * b) * kImgLines, full_leader);
             }
           } else {
             bulk_load(sa, a.w[t.kind] + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
       }
-      if (leader && ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
+      if (weights && leader && ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
         tail->info[s] = INFO_STOP;
         mbar_arrive(smem_u32(&tail->full[s]));
         if (CTAS == 1) mbar_arrive(smem_u32(&tail->full[s]));  // for the scale warp, which has no such stage
@@ -1057,7 +1063,7 @@ int64_t mx4_image_bytes(int64_t rows, int groups, int K) {
 }
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
-                    2, CU_TENSOR_MAP_SWIZZLE_NONE);
+                    Ring<kWide, 2>::BLKS, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
                               int groups, int K, uint8_t* image) {
@@ -1069,12 +1075,15 @@ int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ld
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, 2 * (int64_t)cols, 2 * ldo, rows, 128, 32,
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// packed weight: boxes of one block (the pair's copies count on the leader's
-// barrier, which only tensor copies can)
-int encode_mx4_weight(CUtensorMap* m, const void* packed, int64_t bytes) {
+// packed weight: boxes of a stage's blocks, and of one (the pair's copies
+// count on the leader's barrier, which only tensor copies can)
+int encode_mx4_weight(CUtensorMap* stage, CUtensorMap* one, const void* packed, int64_t bytes) {
   constexpr int line = kMx4BlkBytes / kBlkLines;
-  return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line, kBlkLines,
-                    CU_TENSOR_MAP_SWIZZLE_NONE);
+  const int rc = encode_box(stage, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line,
+                            Ring<kWide, 2>::BLKS * kBlkLines, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return rc ? rc
+            : encode_box(one, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line, kBlkLines,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 extern "C" int afd_mx4_poll_status(void* cuda_stream) {
