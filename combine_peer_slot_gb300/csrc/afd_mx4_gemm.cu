@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; s++) {
       mbar_init(smem_u32(&tail->full[s]), CTAS == 2 ? 1 : 2);  // the producer (the leader's), the scale warp
-      mbar_init(smem_u32(&tail->sfull[s]), 1);
+      mbar_init(smem_u32(&tail->sfull[s]), 2);  // the two scale warps
       mbar_init(smem_u32(&tail->empty[s]), 1);
     }
     for (int b = 0; b < 2; b++) {
@@ -648,9 +648,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       while (!mbar_try_wait(smem_u32(&tail->drain), 0) && globaltimer_ns() < dl) {}
       __syncwarp();
     }
-  } else if (CTAS == 2 && warp == 2) {
+  } else if (CTAS == 2 && (warp == 2 || warp == 4)) {
     // ------------------------------ wide: scales into TMEM
-    // A warp of their own issues them: six copies and four MMAs a stage from
+    // Warps of their own issue them, half of a stage's each: six copies and four MMAs a stage from
     // one warp took longer to issue than the MMAs take to run.
     if (leader) {
       const uint32_t el = elect_one();
@@ -676,8 +676,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
         const int steps = (int)(info >> 9) & 15;
 #pragma unroll
-        for (int c = 0; c < R::BLKS; c++)
+        for (int i = 0; i < R::BLKS / 2; i++) {
+          const int c = warp == 2 ? i : R::BLKS / 2 + i;
           if (2 * c < steps) issue_scales<CTAS, NB, R::BLKS>(el, c, sa, ss, sf);
+        }
         commit_local<CTAS>(el, smem_u32(&tail->sfull[s]));
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
