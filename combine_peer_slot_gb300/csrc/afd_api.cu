@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "afd_internal.cuh"
+#include "afd_mx4.cuh"
 
 size_t gemm_tc_smem_bytes();
 
@@ -31,6 +32,7 @@ struct LayerW {
   size_t T_bytes[4] = {0, 0, 0, 0};
   CUtensorMap tmA1[2];               // SwiGLU projection: routed, shared
   CUtensorMap tmA2[2];               // down projection: routed, shared
+  DevMx4Weight mx4[4];               // AFD_CFG_MX4: the packed W13, Wd, W13_s, Wd_s (in T)
 };
 
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -146,7 +148,7 @@ int validate_config(const afd_config* c) {
       c->max_layers < 1 || c->routed_cap_multiplier < 1.0f || c->wait_timeout_ns < 0)
     return AFD_ERR_ARG;
   if (c->act_dtype != AFD_DTYPE_F32 && c->act_dtype != AFD_DTYPE_BF16) return AFD_ERR_ARG;
-  if (c->flags & ~(AFD_CFG_NO_PDL | AFD_CFG_CANARY | AFD_CFG_SPLIT_GEMMS)) return AFD_ERR_ARG;
+  if (c->flags & ~(AFD_CFG_NO_PDL | AFD_CFG_CANARY | AFD_CFG_SPLIT_GEMMS | AFD_CFG_MX4)) return AFD_ERR_ARG;
   if (c->ffn_size < 0 || c->ffn_size > AFD_MAX_FFN_RANKS || c->ffn_rank < 0 ||
       c->ffn_rank >= std::max(1, c->ffn_size))
     return AFD_ERR_ARG;
@@ -158,6 +160,11 @@ int validate_config(const afd_config* c) {
   if (c->act_dtype == AFD_DTYPE_F32 && tensor) return AFD_ERR_UNSUPPORTED;
   // tensor-core engine: 16-row gate/up blocks, 32-feature epilogue quadrants
   if (tensor && (c->inter % 16 || c->shared_inter % 16 || c->hidden % 32))
+    return AFD_ERR_UNSUPPORTED;
+  // MXFP4 experts: tensor cores only, whole blocks of 32 columns
+  if ((c->flags & AFD_CFG_MX4) &&
+      (c->gemm != AFD_GEMM_TENSOR || c->hidden % 32 || c->inter % 32 || c->shared_inter % 32 || c->hidden > 65536 ||
+       c->inter > 32768 || c->shared_inter > 32768))
     return AFD_ERR_UNSUPPORTED;
   // the router keeps 16 token rows and a weight ring in shared memory
   if (router_min_smem_bytes(c->hidden, c->num_experts, c->act_dtype == AFD_DTYPE_F32) > 232448)
@@ -189,6 +196,12 @@ struct afd_ctx {
   CUtensorMap tmXp32, tmH32, tmHs32;  // 32-row boxes (small SM-pair units)
   CUtensorMap tmWin, tmWin32;         // dispatch window as [rows, hidden] (shared rows, and
                                       // the grouped form's rows from one peer, read in place)
+  struct {                            // AFD_CFG_MX4 workspace
+    uint8_t *codes, *scales;          // rows of Xp
+    uint8_t *h, *hs, *sh, *shs;       // SwiGLU rows, routed and shared: codes, scales or images
+    uint8_t *img, *simg;              // scale images of the routed and the shared rows
+    int32_t* offs;                    // {N, N + S, 0, S}
+  } m4 = {};
   std::vector<LayerW> layers;
   std::vector<uint64_t> last_seq;
   int tmax = 0;
@@ -236,6 +249,11 @@ struct afd_ctx {
       prof_head = (prof_head + 1) % kProfRing;
       prof_pending++;
     }
+  }
+
+  // a stage mark of a host-described step (layer: its weights, NULL for the device's)
+  void mark_if(const void* layer, int i) {
+    if (layer) mark(i);
   }
 
   LaunchCtx lc() { return LaunchCtx{stream, num_sms, &launches, (cfg.flags & AFD_CFG_NO_PDL) ? 0 : 1}; }
@@ -389,6 +407,13 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
   // before the one rounding to the activation type), the activation type in
   // the grouped form (the rows that go back); sized for the wider
   const int64_t yb = 4;
+  // AFD_CFG_MX4: the coded rows (routed, then shared), the coded SwiGLU rows
+  // of the routed and the shared experts, the scale images of each, and where
+  // the shared rows lie.  The images' size grows with the rows' up to the
+  // point where the wide product starts, so the largest step's is the most.
+  const bool mx4 = (cfg->flags & AFD_CFG_MX4) != 0;
+  const int64_t mrows = Tm * k + Tm;
+  auto mx = [&](int64_t bytes) { return mx4 ? bytes : (int64_t)0; };
   struct Part { int64_t bytes; } parts[] = {
       {4},                                   // status
       {(int64_t)cfg->num_peers * cfg->ring_depth * 8},  // seen
@@ -413,9 +438,14 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
       {4},                                   // go word (header check -> router)
       {AFD_MAX_PEERS * 4},                   // combine items finished per entry
       {8 * 8},                               // debug build's bounds record
-      {(Tm * k + Tm + AFD_MAX_GROUPS + AFD_MAX_PEERS) * 4}};  // token tiles' SwiGLU counters
+      {(Tm * k + Tm + AFD_MAX_GROUPS + AFD_MAX_PEERS) * 4},  // token tiles' SwiGLU counters
+      {mx(mrows * H / 2)}, {mx(mrows * H / 32)},             // MXFP4: the rows' codes and scales
+      {mx(Tm * k * I / 2)}, {mx(std::max(Tm * k * I / 32, mx4_most_image_bytes(Tm * k, (int)E, (int)I)))},
+      {mx(Tm * Is / 2)}, {mx(Is > 0 ? std::max(Tm * Is / 32, mx4_most_image_bytes(Tm, 1, (int)Is)) : 0)},
+      {mx(mx4_most_image_bytes(Tm * k, (int)E, (int)H))}, {mx(Is > 0 ? mx4_most_image_bytes(Tm, 1, (int)H) : 0)},
+      {4 * 4}};                                              // MXFP4: the shared rows' offsets
   const int nparts = sizeof(parts) / sizeof(parts[0]);
-  int64_t offs[32], total = 0;
+  int64_t offs[40], total = 0;
   for (int i = 0; i < nparts; i++) {
     offs[i] = total;
     total += round_up(parts[i].bytes > 0 ? parts[i].bytes : 1, 256);
@@ -455,6 +485,15 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
   c->ws.ret_count = reinterpret_cast<int32_t*>(b + offs[26]);
   c->ws.dbg = reinterpret_cast<int64_t*>(b + offs[27]);
   c->ws.dep = reinterpret_cast<int32_t*>(b + offs[28]);
+  c->m4.codes = b + offs[29];
+  c->m4.scales = b + offs[30];
+  c->m4.h = b + offs[31];
+  c->m4.hs = b + offs[32];
+  c->m4.sh = b + offs[33];
+  c->m4.shs = b + offs[34];
+  c->m4.img = b + offs[35];
+  c->m4.simg = b + offs[36];
+  c->m4.offs = reinterpret_cast<int32_t*>(b + offs[37]);
   c->plan1 = reinterpret_cast<GemmPlan*>(b + offs[16]);
   c->plan2 = reinterpret_cast<GemmPlan*>(b + offs[17]);
   const int ws_map[12] = {4, 5, 6, 7, 8, 9, 11, 12, 13, 14, 15, 0};
@@ -521,7 +560,40 @@ int afd_set_layer(afd_ctx* ctx, int layer, const float* Wg, const float* bias, c
   L.Wd = Wd;
   L.W13s = has_shared ? W13_s : nullptr;
   L.Wds = has_shared ? Wd_s : nullptr;
-  if (c.gemm != AFD_GEMM_SIMT) {
+  if (c.flags & AFD_CFG_MX4) {
+    // coded once (OCP scales) and packed; the caller's buffers are not read after this call returns
+    struct Src { const void* W; int E, M, K, swiglu; };
+    const Src src[4] = {{W13, c.num_experts, 2 * c.inter, c.hidden, 1},
+                        {Wd, c.num_experts, c.hidden, c.inter, 0},
+                        {W13_s, 1, 2 * c.shared_inter, c.hidden, 1},
+                        {Wd_s, 1, c.hidden, c.shared_inter, 0}};
+    for (int w = 0; w < (has_shared ? 4 : 2) && !rc; w++) {
+      const Src& q = src[w];
+      const int64_t rows = (int64_t)q.E * q.M, bytes = mx4_weight_bytes(q.E, q.M, q.K, q.swiglu);
+      if (L.T_bytes[w] != (size_t)bytes) {
+        cudaFree(L.T[w]);
+        L.T[w] = nullptr;
+        L.T_bytes[w] = 0;
+        rc = cuda_fail(cudaMalloc(&L.T[w], bytes), "weight copy");
+        if (rc) break;
+        L.T_bytes[w] = bytes;
+      }
+      uint8_t* tmp = nullptr;
+      rc = cuda_fail(cudaMalloc(&tmp, rows * q.K / 2 + rows * (q.K / 32)), "weight coding");
+      if (rc) break;
+      uint8_t* scales = tmp + rows * q.K / 2;
+      rc = cuda_fail(launch_mx4_quantize(lc, q.W, q.K, rows, 0, nullptr, 1, rows, q.K, 0, tmp, scales), "weight coding");
+      if (!rc)
+        rc = cuda_fail(launch_mx4_pack(lc, tmp, scales, q.E, q.M, q.K, q.swiglu, static_cast<uint8_t*>(L.T[w])),
+                       "weight coding");
+      if (!rc) rc = encode_mx4_weight(L.mx4[w].tm, L.T[w], bytes);
+      L.mx4[w].packed = static_cast<uint8_t*>(L.T[w]);
+      const int sync = cuda_fail(cudaStreamSynchronize(ctx->stream), "weight coding");
+      cudaFree(tmp);
+      if (!rc) rc = sync;
+    }
+    if (rc) return rc;
+  } else if (c.gemm != AFD_GEMM_SIMT) {
     // the tensor engines read tiled copies (one contiguous 16 KB block per
     // TMA box); the caller's buffers are not read after this call returns
     struct Src { const void* W; int E, M, K, swiglu, I; };
@@ -571,6 +643,7 @@ int afd_set_layer(afd_ctx* ctx, int layer, const float* Wg, const float* bias, c
   d.W13s = L.W13s;
   d.Wd = L.Wd;
   d.Wds = L.Wds;
+  for (int w = 0; w < 4; w++) d.mx4[w] = L.mx4[w];
   d.set = 1;
   rc = cuda_fail(cudaMemcpyAsync(ctx->dlayers + layer, &d, sizeof d, cudaMemcpyHostToDevice,
                                  ctx->stream),
@@ -878,6 +951,64 @@ int afd_serve_log(afd_ctx* ctx, int32_t* records, int max_records, int* n_record
   return AFD_OK;
 }
 
+// a4-a6 with AFD_CFG_MX4: the gathered rows coded, then the SwiGLU and the
+// down product of the routed experts and of the shared one.  N and S are the
+// step's rows, or the most it may carry (the device then knows its own).
+// The routed outputs keep the form that the combine or the scatter reads.
+static int experts_mx4(afd_ctx* ctx, const LayerW* L, int64_t N, int64_t S, bool grouped) {
+  const afd_config& c = ctx->cfg;
+  const DevWS& ws = ctx->ws;
+  LaunchCtx lc = ctx->lc();
+  if (N + S == 0) {
+    ctx->mark_if(L, 5);
+    return AFD_OK;
+  }
+  int rc = cuda_fail(launch_mx4_quantize_step(lc, ws.xp, c.hidden, L ? nullptr : ws.item, c.topk, (int)N, (int)S,
+                                              ctx->m4.codes, ctx->m4.scales, ctx->m4.offs),
+                     "mx4 rows");
+  if (rc) return rc;
+  // one product; wsel: 0 W13, 1 Wd, 2 W13_s, 3 Wd_s
+  auto product = [&](int wsel, const uint8_t* codes, const uint8_t* scales, uint8_t* image, int64_t x_rows,
+                     int64_t rows, const int32_t* offsets, int groups, int M, int K, int swiglu, int fmt, void* out,
+                     uint8_t* out_lo, int64_t ldo, const int32_t* shift) -> int {
+    Mx4GemmArgs a;
+    memset(&a, 0, sizeof a);
+    if (L) {
+      a.w = L->mx4[wsel].packed;
+    } else {
+      a.layers = ws.layers;
+      a.item = ws.item;
+      a.wsel = wsel;
+    }
+    a.out = out;
+    a.out_lo = out_lo;
+    a.ldo = ldo;
+    a.out_shift = shift;
+    a.fmt = fmt;
+    a.status = ws.status;
+    LaunchCtx one = lc;
+    return mx4_product(one, a, codes, scales, image, x_rows, rows, offsets, groups, M, K, swiglu);
+  };
+  const int E = c.num_experts, H = c.hidden, I = c.inter, Is = c.shared_inter;
+  if (N > 0)
+    rc = product(0, ctx->m4.codes, ctx->m4.scales, ctx->m4.img, N + S, N, ws.offsets, E, 2 * I, H, 1, OUT_MX4,
+                 ctx->m4.h, ctx->m4.hs, I, nullptr);
+  if (!rc && S > 0)
+    rc = product(2, ctx->m4.codes, ctx->m4.scales, ctx->m4.simg, N + S, S, ctx->m4.offs, 1, 2 * Is, H, 1, OUT_MX4,
+                 ctx->m4.sh, ctx->m4.shs, Is, ctx->m4.offs);
+  if (rc) return rc;
+  ctx->mark_if(L, 5);
+  // (wide products: the SwiGLU rows' scales are images already)
+  const bool wide = mx4_image_bytes(N, E, I) > 0, wide_s = S > 0 && mx4_image_bytes(S, 1, Is) > 0;
+  if (N > 0)
+    rc = product(1, ctx->m4.h, wide ? nullptr : ctx->m4.hs, ctx->m4.hs, N, N, ws.offsets, E, H, I, 0,
+                 grouped ? OUT_ACT : OUT_Y24, ws.y, ws.y_lo, H, nullptr);
+  if (!rc && S > 0)
+    rc = product(3, ctx->m4.sh, wide_s ? nullptr : ctx->m4.shs, ctx->m4.shs, S, S, ctx->m4.offs + 2, 1, H, Is, 0,
+                 OUT_F32, ws.s, nullptr, H, nullptr);
+  return rc;
+}
+
 // One FFN step.  dev == nullptr: the host describes it (f, layer).  Else a
 // step of the work-item loop over the peers in *dev: the device chooses the
 // stage and takes the layer and the counts from the headers; f then holds
@@ -894,7 +1025,8 @@ static int forward_impl(afd_ctx* ctx, int layer, FanIn& f, const PeerList* dev) 
   // the per-(peer, expert) groups would be small and each expert's weights
   // read once per peer (measured slower than gathering the peers' rows into
   // one group per expert), so those take the gather and the scatter.
-  const bool in_place = grouped && c.gemm != AFD_GEMM_SIMT && f.n_peers == 1;
+  const bool mx4 = (c.flags & AFD_CFG_MX4) != 0;  // rows are coded after the gather
+  const bool in_place = grouped && c.gemm != AFD_GEMM_SIMT && !mx4 && f.n_peers == 1;
   // routed rows: T * k partials, or the rows the peers sent already grouped
   const int64_t N = grouped ? f.rtotal : T * c.topk;
   if (!dev && (layer < 0 || layer >= c.max_layers || !ctx->layers[layer].set)) return AFD_ERR_LAYER;
@@ -912,7 +1044,7 @@ static int forward_impl(afd_ctx* ctx, int layer, FanIn& f, const PeerList* dev) 
   // each group would stream the shared weights once more, so those rows are
   // gathered.  Steps of the work-item loop (counts unknown here) gather.
   int sh_in_place = 0;
-  if (has_shared && !dev && !in_place) {
+  if (has_shared && !dev && !in_place && !mx4) {
     int64_t units_ip = 0;
     for (int i = 0; i < f.n_peers; i++) units_ip += (f.sprefix[i + 1] - f.sprefix[i] + bn - 1) / bn;
     sh_in_place = units_ip <= ((int64_t)f.stotal + bn - 1) / bn + 1;
@@ -931,7 +1063,7 @@ static int forward_impl(afd_ctx* ctx, int layer, FanIn& f, const PeerList* dev) 
   // 6.33 ms per 26 layers against 6.39 ms for 57 units from every SM forked
   // after the header check (sweep of 57-152 units x 10-152 SMs).  Steps the
   // device describes fork after the item head, whose fan-in they read.
-  const bool prefetch = c.gemm == AFD_GEMM_TENSOR && bn == 64 && N > 0;
+  const bool prefetch = c.gemm == AFD_GEMM_TENSOR && !mx4 && bn == 64 && N > 0;
   int rc = AFD_OK;
   struct Join {  // the main stream waits for the side stream on every way out
     afd_ctx* ctx;
@@ -1016,7 +1148,11 @@ static int forward_impl(afd_ctx* ctx, int layer, FanIn& f, const PeerList* dev) 
   // or the return window's rows when the outputs go there in place
   const int64_t Tcap = ctx->tmax;
   const int64_t win_rows = ctx->L.window_bytes / row_bytes;
-  if (N + T > 0) {
+  if (mx4) {
+    // (a step of the work-item loop: the most shared rows are its tokens)
+    rc = experts_mx4(ctx, L, N, !has_shared ? 0 : dev ? T : f.stotal, grouped);
+    if (rc) return rc;
+  } else if (N + T > 0) {
     if (c.gemm != AFD_GEMM_SIMT) {
       auto launch = c.gemm == AFD_GEMM_TENSOR ? launch_gemm_tc2 : launch_gemm_tc;
       GemmArgs a1;

@@ -101,6 +101,10 @@ struct PeerList {
 // chosen on the device: the TMA maps and plain pointers of every layer,
 // one entry per layer in device memory ("layer-select" operators of the
 // Async AFD RFC: the address table of every layer plus a device-side index)
+struct DevMx4Weight {  // a weight packed in MXFP4
+  CUtensorMap tm[2];      // boxes of a stage's blocks, of one block
+  const uint8_t* packed;
+};
 struct DevLayer {  // aligned as its tensor maps
   CUtensorMap tmA1[2];    // SwiGLU GEMM weights: routed experts, shared expert
   CUtensorMap tmA2[2];    // down GEMM weights
@@ -111,6 +115,7 @@ struct DevLayer {  // aligned as its tensor maps
   const void* Wd;
   const void* Wds;
   int set;
+  DevMx4Weight mx4[4];    // AFD_CFG_MX4: W13, Wd, W13s, Wds
 };
 
 // workspace words of the work-item loop

@@ -58,7 +58,7 @@ struct QuantArgs {
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const __grid_constant__ QuantArgs a) {
+__device__ __forceinline__ void quantize_chunks(const QuantArgs& a) {
   const int64_t total = a.n_rows * a.chunks;  // a multiple of 4: a block's lanes are all in or all out
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kChunks);
   const ChunkPos pos(first, a.chunks, a.magic);
@@ -112,6 +112,40 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const __grid_constant
     a.codes[i] = s == 255u ? 0u : mx4_encode8(v);
     if ((threadIdx.x & 3) == 0) a.scales[i >> 2] = (uint8_t)s;
   }
+}
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const __grid_constant__ QuantArgs a) {
+  quantize_chunks<F32>(a);
+}
+
+// ---------------------------------------------------------------------------
+// the same for a step's gathered rows: position r of Xp is row r of the
+// result.  The first thread also writes where the shared rows lie, for the
+// products that follow (a step of the work-item loop knows it on the device
+// only).  rows is the most there can be; past the step's own, the last
+// step's rows are coded again and nothing reads them.
+// ---------------------------------------------------------------------------
+struct StepArgs {
+  QuantArgs q;
+  const FanIn* item;  // NULL: the counts are n and s
+  int topk, has_shared, n, s;
+  int32_t* offs;
+};
+__global__ void __launch_bounds__(kThreads) k_mx4_quantize_step(const __grid_constant__ StepArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    int N = a.n, S = a.s;
+    if (a.item) {
+      N = a.item->grouped ? a.item->rtotal : a.item->total * a.topk;
+      S = a.has_shared ? a.item->stotal : 0;
+    }
+    a.offs[0] = N;
+    a.offs[1] = N + S;
+    a.offs[2] = 0;
+    a.offs[3] = S;
+  }
+  quantize_chunks<false>(a.q);
 }
 
 // ---------------------------------------------------------------------------
@@ -256,12 +290,64 @@ cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx,
              : launch_k(lc, k_mx4_quantize<false>, (unsigned)grid, kThreads, 0, a);
 }
 
+cudaError_t launch_mx4_quantize_step(const LaunchCtx& lc, const void* xp, int cols, const FanIn* item,
+                                     int topk, int n, int s, uint8_t* codes, uint8_t* scales, int32_t* offs) {
+  const int64_t rows = (int64_t)n + s;
+  const StepArgs a{{static_cast<const uint8_t*>(xp), (int64_t)cols * 2, rows, nullptr, 1, rows, cols / 8,
+                    0xffffffffu / (uint32_t)(cols / 8), 0, reinterpret_cast<uint32_t*>(codes), scales},
+                   item, topk, s > 0, n, s, offs};
+  const int64_t grid = std::max<int64_t>(1, chunk_grid(rows * (cols / 8)));
+  if (grid >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+  return launch_k(lc, k_mx4_quantize_step, (unsigned)grid, kThreads, 0, a);
+}
+
 cudaError_t launch_mx4_pack(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int E, int64_t M,
                             int K, int swiglu, uint8_t* packed) {
   const int tiles = mx4_tiles(M, swiglu), nkb = mx4_kblocks(K);
   return launch_k(lc, k_mx4_pack, (unsigned)((int64_t)E * tiles * nkb), kThreads, 0, codes, scales, M, K, swiglu,
                   tiles, nkb, packed);
 }
+
+int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8_t* scales, uint8_t* image,
+                int64_t x_rows, int64_t rows, const int32_t* offsets, int groups, int M, int K, int swiglu) {
+  const int bn = mx4_token_tile(rows, groups);
+  const int64_t img = mx4_image_bytes(rows, groups, K);
+  const int64_t units = (int64_t)mx4_tiles(M, swiglu) * ((rows + bn - 1) / bn + std::min<int64_t>(groups, rows));
+  if (units >= (int64_t)1 << 31 || img / 128 >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
+  int rc = encode_mx4_rows(&a.tmX, codes, x_rows, K, bn);
+  if (!rc && img && !a.layers) rc = encode_mx4_weight(a.tmW, a.w, mx4_weight_bytes(groups, M, K, swiglu));
+  if (!rc && a.fmt == OUT_ACT) rc = encode_mx4_out(&a.tmO, a.out, x_rows, swiglu ? M / 2 : M, a.ldo);
+  if (!rc && img) rc = encode_mx4_images(&a.tmS, image, img);
+  if (rc) return rc;
+  if (img && scales) {
+    rc = launched(launch_mx4_images(lc, scales, x_rows, offsets, rows, groups, K, image), "mx4 scale images");
+    if (rc) return rc;
+    lc.pdl = 1;  // the product's set-up runs while the images are written
+  }
+  a.xs = scales;
+  a.x_rows = x_rows;
+  a.M = M;
+  a.K = K;
+  a.offsets = offsets;
+  a.n_groups = groups;
+  a.swiglu = swiglu;
+  return launched(launch_mx4_gemm(lc, a, bn, units), "mx4 gemm");
+}
+
+// the products of the calls without a context
+static int product(LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, uint8_t* image, int64_t n_rows,
+                   const int32_t* offsets, int E, const void* w, int M, int K, int swiglu, int fmt, void* out,
+                   int64_t ldo, uint8_t* out_scales = nullptr) {
+  Mx4GemmArgs a;
+  memset(&a, 0, sizeof a);
+  a.w = static_cast<const uint8_t*>(w);
+  a.out = out;
+  a.out_lo = out_scales;
+  a.ldo = ldo;
+  a.fmt = fmt;
+  return mx4_product(lc, a, codes, scales, image, n_rows, n_rows, offsets, E, M, K, swiglu);
+}
+static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 extern "C" {
 
@@ -330,43 +416,6 @@ int afd_mx4_pack_weight(const uint8_t* codes, const uint8_t* scales, int num_exp
                   "mx4 pack weight");
 }
 
-static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
-
-// One product over the grouped rows.  image: the rows' scale images (wide
-// form; written here from scales unless that is NULL).  out_scales: OUT_MX4's.
-static int product(LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, uint8_t* image, int64_t n_rows,
-                   const int32_t* offsets, int E, const void* w, int M, int K, int swiglu, int fmt, void* out,
-                   int64_t ldo, uint8_t* out_scales = nullptr) {
-  Mx4GemmArgs a;
-  memset(&a, 0, sizeof a);
-  const int bn = mx4_token_tile(n_rows, E);
-  const int64_t img = mx4_image_bytes(n_rows, E, K);
-  const int64_t units = (int64_t)mx4_tiles(M, swiglu) * ((n_rows + bn - 1) / bn + std::min<int64_t>(E, n_rows));
-  if (units >= (int64_t)1 << 31 || img / 128 >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
-  int rc = encode_mx4_rows(&a.tmX[0], codes, n_rows, K, bn);
-  if (!rc && img) rc = encode_mx4_weight(&a.tmW[0], &a.tmW1[0], w, mx4_weight_bytes(E, M, K, swiglu));
-  if (!rc && fmt == OUT_ACT) rc = encode_mx4_out(&a.tmO[0], out, n_rows, swiglu ? M / 2 : M, ldo);
-  if (!rc && img) rc = encode_mx4_images(&a.tmS[0], image, img);
-  if (rc) return rc;
-  if (img && scales) {
-    rc = launched(launch_mx4_images(lc, scales, n_rows, offsets, E, K, image), "mx4 scale images");
-    if (rc) return rc;
-    lc.pdl = 1;  // the product's set-up runs while the images are written
-  }
-  a.xs[0] = scales;
-  a.x_rows[0] = n_rows;
-  a.w[0] = static_cast<const uint8_t*>(w);
-  a.out[0] = out;
-  a.out_lo[0] = out_scales;
-  a.ldo[0] = ldo;
-  a.fmt[0] = fmt;
-  a.M[0] = M;
-  a.K[0] = K;
-  a.offsets = offsets;
-  a.n_groups = E;
-  a.swiglu = swiglu;
-  return launched(launch_mx4_gemm(lc, a, bn, units), "mx4 gemm");
-}
 
 int64_t afd_mx4_gemm_workspace(int64_t n_rows, int num_experts, int K) {
   if (n_rows < 0 || n_rows > kMaxRows || num_experts < 1 || num_experts > 256 || !dims_ok(1, K) || K % kMx4Block)

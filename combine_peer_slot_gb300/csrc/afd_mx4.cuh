@@ -35,28 +35,31 @@ inline int64_t mx4_weight_bytes(int64_t E, int64_t M, int K, int swiglu) {
   return E * mx4_tiles(M, swiglu) * mx4_kblocks(K) * kMx4BlkBytes;
 }
 
-// Arguments of one grouped product.  Group g < n_groups is rows
-// [offsets[g], offsets[g + 1]) of the rows of kind 0 times weight g; with
-// shared rows, one more group: all of kind 1's rows times its weight.
+// Arguments of one grouped product: rows [offsets[g], offsets[g + 1]) times
+// weight g.
 #define OUT_MX4 3  // SwiGLU only: codes in out, scales in out_lo (ldo % 32 == 0)
 struct Mx4GemmArgs {
-  CUtensorMap tmX[2];        // codes of the rows (encode_mx4_rows)
-  CUtensorMap tmW[2], tmW1[2];  // packed weights (encode_mx4_weight); the wide form's
-  CUtensorMap tmS[2];        // their scale images (encode_mx4_images); the wide form's
-  const uint8_t* xs[2];      // their scales [x_rows][K / 32]; the narrow form's
-  int64_t x_rows[2];
-  const uint8_t* w[2];       // packed weights; the narrow form's
-  CUtensorMap tmO[2];        // bf16 outputs (encode_mx4_out)
-  void* out[2];
-  uint8_t* out_lo[2];        // OUT_Y24: the low plane; OUT_MX4: the scales (wide: their images)
-  int64_t ldo[2];            // output row pitch in elements
-  int fmt[2];                // OUT_*
-  int M[2], K[2];
+  CUtensorMap tmX;           // codes of the rows (encode_mx4_rows)
+  CUtensorMap tmW[2];        // the packed weight (encode_mx4_weight); the wide form's
+  CUtensorMap tmS;           // the rows' scale images (encode_mx4_images); the wide form's
+  CUtensorMap tmO;           // bf16 output (encode_mx4_out)
+  const uint8_t* xs;         // the rows' scales [x_rows][K / 32]; the narrow form's
+  int64_t x_rows;
+  const uint8_t* w;          // the packed weight; the narrow form's
+  void* out;
+  uint8_t* out_lo;           // OUT_Y24: the low plane; OUT_MX4: the scales (wide: their images)
+  int64_t ldo;               // output row pitch in elements
+  const int32_t* out_shift;  // device, NULL = 0: row r goes to output row r - *out_shift
+  int fmt;                   // OUT_*
+  int M, K;
   const int32_t* offsets;    // [n_groups + 1], device
   int n_groups;
-  int has_shared;
   int swiglu;
   int32_t* status;           // NULL: the file-scope status word
+  // layer chosen on the device: the weight is layers[item->layer].mx4[wsel], not tmW and w
+  const DevLayer* layers;
+  const FanIn* item;
+  int wsel;
 };
 // bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
 // output tiles, which sizes the grid
@@ -64,16 +67,28 @@ int mx4_token_tile(int64_t rows, int groups);
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units);
 int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn);
 int64_t mx4_image_bytes(int64_t rows, int groups, int K);
+int64_t mx4_most_image_bytes(int64_t rows, int groups, int K);  // over all row counts up to rows
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);
-// offsets NULL: one group of all rows
-cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
-                              int groups, int K, uint8_t* image);
+// x_rows: rows the scales hold; rows: the most the groups hold together
+cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
+                              int64_t rows, int groups, int K, uint8_t* image);
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo);
-int encode_mx4_weight(CUtensorMap* stage, CUtensorMap* one, const void* packed, int64_t bytes);
+int encode_mx4_weight(CUtensorMap* tm /* [2]: a stage's blocks, one block */, const void* packed, int64_t bytes);
 
 cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx, int64_t x_rows, int f32,
                                 const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,
                                 uint8_t* codes, uint8_t* scales);
+// The step's gathered rows (n routed, then s shared; item: the device's own
+// counts, n and s the most there can be) coded position by position, and
+// offs = {n, n + s, 0, s} for the shared rows' products
+cudaError_t launch_mx4_quantize_step(const LaunchCtx& lc, const void* xp, int cols, const FanIn* item, int topk, int n,
+                                     int s, uint8_t* codes, uint8_t* scales, int32_t* offs);
+// One product of the step or of a call.  image: the rows' scale images (wide
+// form; written from scales unless that is NULL), rows: the most rows the
+// groups hold together, x_rows: the rows that codes and scales hold.
+// a: out, out_lo, ldo, out_shift, fmt, status, and layers / item / wsel or w.
+int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8_t* scales, uint8_t* image,
+                int64_t x_rows, int64_t rows, const int32_t* offsets, int groups, int M, int K, int swiglu);
 cudaError_t launch_mx4_pack(const LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, int E, int64_t M,
                             int K, int swiglu, uint8_t* packed);
 

@@ -46,7 +46,7 @@ constexpr int EPI_BUF_BYTES = 2 * EPI_BOX_BYTES;
 // lines of 8-byte words that the pair's copies take contiguous memory as: a
 // weight block is 8 of 1088 bytes, a 128-column scale image 1 of 1024
 constexpr int kBlkLines = 8, kImgLines = 1;
-constexpr int MAX_GROUPS = 257;       // 256 experts and the shared rows
+constexpr int MAX_GROUPS = 256;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // A stage's word for the MMA issuer, written by the copies' producer: bits
@@ -97,8 +97,8 @@ struct Ring {
     uint32_t tmem_base;
     int abort_flag;
     uint32_t info[STAGES];      // what the stage holds (INFO_*)
-    int m_units[2];             // weight tiles (pairs of them) per kind, and (2^32 - 1) / m_units
-    uint32_t m_magic[2];
+    int m_units;                // weight tiles (pairs of them), and (2^32 - 1) / m_units
+    uint32_t m_magic;
     int tile0[MAX_GROUPS + 1];  // first unit of each group
     int row0[MAX_GROUPS];
     int rows[MAX_GROUPS];
@@ -324,7 +324,7 @@ __device__ __forceinline__ bool group_all(int half, bool ok) {
 }
 
 struct Unit {
-  int group, kind, mt, rows, n_mma, tile;
+  int group, mt, rows, n_mma, tile;
   int64_t row;  // first row of the token tile
 };
 
@@ -361,7 +361,6 @@ struct Walk {
       g = lo;
     }
     t.group = g;
-    t.kind = g == a.n_groups;
     const int u = unit - T->tile0[g], rows = T->rows[g];
     int nt;
     if (BN == 64) {  // the weights stream from HBM: a weight tile's token tiles side by side, for L2
@@ -369,8 +368,8 @@ struct Walk {
       t.mt = n_tiles == 1 ? u : u / n_tiles;
       nt = u - t.mt * n_tiles;
     } else {         // the units running at once share token tiles
-      const int m_units = T->m_units[t.kind];
-      nt = (int)__umulhi((uint32_t)u, T->m_magic[t.kind]);  // u / m_units, or one less
+      const int m_units = T->m_units;
+      nt = (int)__umulhi((uint32_t)u, T->m_magic);  // u / m_units, or one less
       if ((nt + 1) * m_units <= u) nt++;
       t.mt = u - nt * m_units;
       t.tile = T->nt0[g] + nt;
@@ -450,20 +449,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   grid_dep_wait();
   grid_dep_launch();
   // the groups: rows clamped to those there are, units counted
-  const int ngroups = a.n_groups + a.has_shared;
+  const int ngroups = a.n_groups;
   int mine = 0, tiles = 0;
   if (threadIdx.x < ngroups) {
     const int g = threadIdx.x;
-    const int kind = g == a.n_groups;
-    int lo = 0, hi = (int)a.x_rows[1];
-    if (!kind) {
-      lo = (int)min(max((int64_t)a.offsets[g], (int64_t)0), a.x_rows[0]);
-      hi = (int)min(max((int64_t)a.offsets[g + 1], (int64_t)lo), a.x_rows[0]);
-    }
+    const int lo = (int)min(max((int64_t)a.offsets[g], (int64_t)0), a.x_rows);
+    const int hi = (int)min(max((int64_t)a.offsets[g + 1], (int64_t)lo), a.x_rows);
     tail->row0[g] = lo;
     tail->rows[g] = hi - lo;
     tiles = (hi - lo + BN - 1) / BN;
-    mine = tiles * ((mx4_tiles(a.M[kind], a.swiglu) + CTAS - 1) / CTAS);
+    mine = tiles * ((mx4_tiles(a.M, a.swiglu) + CTAS - 1) / CTAS);
   }
   int incl = mine, tincl = tiles;
 #pragma unroll
@@ -489,15 +484,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   }
   if (threadIdx.x < ngroups) {
     tail->tile0[threadIdx.x + 1] = before + incl;
-    tail->nt0[threadIdx.x] = (int)threadIdx.x == a.n_groups ? 0 : tbefore + tincl - tiles;  // per kind
+    tail->nt0[threadIdx.x] = tbefore + tincl - tiles;
   }
   if (threadIdx.x == 0) {
     tail->tile0[0] = 0;
-    for (int k = 0; k < 2; k++) {
-      const int m = max((mx4_tiles(a.M[k], a.swiglu) + CTAS - 1) / CTAS, 1);
-      tail->m_units[k] = m;
-      tail->m_magic[k] = 0xffffffffu / (uint32_t)m;  // under 2^32 / m by at most 1: u m_magic / 2^32 > u / m - 1
-    }
+    const int m = (mx4_tiles(a.M, a.swiglu) + CTAS - 1) / CTAS;
+    tail->m_units = m;
+    tail->m_magic = 0xffffffffu / (uint32_t)m;  // under 2^32 / m by at most 1: u m_magic / 2^32 > u / m - 1
   }
   tc_fence_before();
   __syncthreads();
@@ -506,6 +499,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   const uint32_t tmem = tail->tmem_base;
   const uint64_t deadline = globaltimer_ns() + kTimeoutNs;
   volatile int* abort_flag = &tail->abort_flag;
+  // the weight: the launch's own, or that of the layer the device chose for this step
+  const DevMx4Weight* lw = a.layers ? &a.layers[a.item->layer].mx4[a.wsel] : nullptr;
+  const CUtensorMap* tmW = lw ? lw->tm : a.tmW;
+  const uint8_t* wbase = lw ? lw->packed : a.w;
   const uint32_t smem_base = smem_u32(smem);
 
   if (warp == 0 || (CTAS == 2 && warp == 3)) {
@@ -518,10 +515,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       bool ok = true;
       for (Walk<BN, CTAS> w(a, tail, ngroups, total); w.more() && ok; w.next()) {
         const Unit& t = w.t;
-        const int nk = mx4_kblocks(a.K[t.kind]);
-        const int m_tiles = mx4_tiles(a.M[t.kind], a.swiglu);
+        const int nk = mx4_kblocks(a.K);
+        const int m_tiles = mx4_tiles(a.M, a.swiglu);
         const int64_t blk0 =  // the weight's blocks of this tile (past an odd edge: the last tile's again)
-            ((int64_t)(t.kind ? 0 : t.group) * m_tiles + min(t.mt, m_tiles - 1)) * nk;
+            ((int64_t)t.group * m_tiles + min(t.mt, m_tiles - 1)) * nk;
         for (int kb = 0; kb * R::BLKS < nk; kb++) {
           if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
           const uint32_t full = smem_u32(&tail->full[s]);
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           const uint32_t sa = smem_base + s * R::STAGE_BYTES;
           const uint32_t sx = sa + R::A_BYTES;
           if (weights && leader) {
-            const int left = (a.K[t.kind] - kb * R::BK + 63) / 64;
+            const int left = (a.K - kb * R::BK + 63) / 64;
             tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, R::BK / 64) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
                             (left <= R::BK / 64 ? INFO_LAST : 0u);
             mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + boxes * R::X_BYTES + (CTAS == 2 ? R::S_BYTES : 0)));
@@ -539,21 +536,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             const uint32_t full_leader = map_to_rank(full, 0);
             const int line = (int)(blk0 + R::BLKS * kb) * kBlkLines;
             if (weights && blks == R::BLKS)
-              tma_pair_load_2d(sa, &a.tmW[t.kind], 0, line, full_leader);
+              tma_pair_load_2d(sa, tmW, 0, line, full_leader);
             else if (weights)
               for (int b = 0; b < blks; b++)
-                tma_pair_load_2d(sa + b * kMx4BlkBytes, &a.tmW1[t.kind], 0, line + b * kBlkLines, full_leader);
+                tma_pair_load_2d(sa + b * kMx4BlkBytes, tmW + 1, 0, line + b * kBlkLines, full_leader);
             if (tokens) {
               for (int b = 0; b < boxes; b++)
-                tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX[t.kind], (kb * (R::BK / BOX) + b) * (BOX / 2),
+                tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX, (kb * (R::BK / BOX) + b) * (BOX / 2),
                                  (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
               // (past the tile's last block: the next tile's images, not used)
-              tma_pair_load_2d(sx + R::B_BYTES, &a.tmS[t.kind], 0, (t.tile * nk + R::BLKS * kb) * kImgLines,
+              tma_pair_load_2d(sx + R::B_BYTES, &a.tmS, 0, (t.tile * nk + R::BLKS * kb) * kImgLines,
                                full_leader);
             }
           } else {
-            bulk_load(sa, a.w[t.kind] + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
-            tma_load_2d(sx, &a.tmX[t.kind], kb * (BOX / 2), (int)t.row, full);
+            bulk_load(sa, wbase + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
+            tma_load_2d(sx, &a.tmX, kb * (BOX / 2), (int)t.row, full);
           }
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
@@ -692,7 +689,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     auto advance = [&](int n) {  // n stages on
       kb += n;
       while (w.more()) {
-        const int nkb = (a.K[w.t.kind] + R::BK - 1) / R::BK;
+        const int nkb = (a.K + R::BK - 1) / R::BK;
         if (kb < nkb) break;
         kb -= nkb;
         w.next();
@@ -700,7 +697,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     };
     auto load = [&](uint32_t (&v)[BN / 32][2]) {
       if (w.more())
-        load_scales<BN>(a.xs[w.t.kind], a.x_rows[w.t.kind], a.K[w.t.kind] / 32, w.t.row, kb, lane, v);
+        load_scales<BN>(a.xs, a.x_rows, a.K / 32, w.t.row, kb, lane, v);
     };
     advance(warp - 2);
     uint32_t v[BN / 32][2];
@@ -745,6 +742,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     const int half = (warp - EPI_WARP0) >> 2;
     const int gt = threadIdx.x & 127;  // thread of the group
     uint8_t* ebase = smem + R::kEpiOffset + (size_t)half * 2 * EPI_BUF_BYTES;
+    const int64_t shift = a.out_shift ? (int64_t)*a.out_shift : 0;
     int buf = 0;
     int acc = 0;
     uint32_t acc_ph = 0;
@@ -754,20 +752,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       if (!group_all(half, ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      const int kind = t.kind;
-      const int64_t ldo = a.ldo[kind];
-      const int fmt = a.fmt[kind];
+      const int64_t ldo = a.ldo, row0 = t.row - shift;  // first output row
+      const int fmt = a.fmt;
       bool released = false;
       // the group's piece is in the buffer: whole ones go out by TMA
-      auto stored = [&](bool whole, int boxes, int kd, int col, int64_t row) {
+      auto stored = [&](bool whole, int boxes, int col, int64_t row) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (gt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer has been read
         group_sync(half);
         if (whole && gt == 0) {
           const uint32_t src = smem_u32(ebase + (buf ^ 1) * EPI_BUF_BYTES);
-          const int cols = a.swiglu ? a.M[kd] / 2 : a.M[kd];
+          const int cols = a.swiglu ? a.M / 2 : a.M;
           for (int b = 0; b < boxes; b++)
-            if (col + 64 * b < cols) tma_store_2d(&a.tmO[kd], src + b * EPI_BOX_BYTES, col + 64 * b, (int)row);
+            if (col + 64 * b < cols) tma_store_2d(&a.tmO, src + b * EPI_BOX_BYTES, col + 64 * b, (int)row);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       };
@@ -786,16 +783,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           tmem_ld_wait();
           if (last) release();
           const int col = t.mt * 128 + q * 32 + lane;
-          if (col < a.M[kind]) {
-            const int64_t at = (t.row + c0) * ldo + col;
+          if (col < a.M) {
+            const int64_t at = (row0 + c0) * ldo + col;
             if (fmt == OUT_F32) {
-              float* dst = reinterpret_cast<float*>(a.out[kind]) + at;
+              float* dst = reinterpret_cast<float*>(a.out) + at;
 #pragma unroll
               for (int c = 0; c < 32; c++)
                 if (c < nrows) dst[(int64_t)c * ldo] = __uint_as_float(v[c]);
             } else {
-              uint16_t* dh = reinterpret_cast<uint16_t*>(a.out[kind]) + at;
-              uint8_t* dl = a.out_lo[kind] + at;
+              uint16_t* dh = reinterpret_cast<uint16_t*>(a.out) + at;
+              uint8_t* dl = a.out_lo + at;
 #pragma unroll
               for (int c = 0; c < 32; c++)
                 if (c < nrows) {
@@ -825,8 +822,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                               (((q * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
           stmatrix_x4_trans(at, h[0], h[1], h[2], h[3]);
           stmatrix_x4_trans(at + 16 * 128, h[4], h[5], h[6], h[7]);
-          stored(nrows == 32 && fmt == OUT_ACT, 1, kind, t.mt * 64, t.row + c0);
-          const int I = a.M[kind] / 2;
+          stored(nrows == 32 && fmt == OUT_ACT, 1, t.mt * 64, row0 + c0);
+          const int I = a.M / 2;
           if (fmt == OUT_MX4) {
             // a thread codes 16 of a token's 64 features, two threads a block
             const int r = gt >> 2, f = t.mt * 64 + (gt & 3) * 16;
@@ -852,22 +849,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
               code[i] = sc == 255u ? 0u : mx4_encode8(v);
             }
             if (r < nrows && f < I) {
-              const int64_t at = (t.row + c0 + r) * ldo + f;
-              *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out[kind]) + at / 2) =
+              const int64_t at = (row0 + c0 + r) * ldo + f;
+              *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out) + at / 2) =
                   make_uint2(code[0], code[1]);
-              if (CTAS == 1 && (gt & 1) == 0) a.out_lo[kind][at / 32] = (uint8_t)sc;
+              if (CTAS == 1 && (gt & 1) == 0) a.out_lo[at / 32] = (uint8_t)sc;
             }
             if (CTAS == 2 && (gt & 1) == 0 && r < nrows) {
               // into the next product's scale images; zeros past inter's
               // end, so that no stray scale meets the zero columns there
               const int blk = f / 32, nk2 = mx4_kblocks(I), rt = c0 + r;
-              uint8_t* img = a.out_lo[kind] + (int64_t)t.tile * nk2 * (NB * 512) + (rt >> 7) * 512 +
+              uint8_t* img = a.out_lo + (int64_t)t.tile * nk2 * (NB * 512) + (rt >> 7) * 512 +
                              (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
               auto put = [&](int b, uint32_t v) {
                 if (b < nk2 * 4) img[(b >> 2) * (NB * 512) + (b & 3)] = (uint8_t)v;
               };
               put(blk, f < I ? sc : 0u);
-              if (t.mt == mx4_tiles(a.M[kind], 1) - 1) put(blk + 2, 0u);
+              if (t.mt == mx4_tiles(a.M, 1) - 1) put(blk + 2, 0u);
             }
           } else if (nrows < 32) {
             const int r0 = gt >> 3, f = t.mt * 64 + (gt & 7) * 8;
@@ -875,7 +872,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             for (int p = 0; p < 2; p++) {
               const int r = r0 + 16 * p;
               if (r < nrows && f + 8 <= I)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + f) =
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (row0 + c0 + r) * ldo + f) =
                     *reinterpret_cast<const uint4*>(ebuf + r * 128 + (((gt & 7) ^ (r & 7)) << 4));
             }
           }
@@ -889,14 +886,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                               pack_bf16(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])),
                               pack_bf16(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])),
                               pack_bf16(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])));
-          stored(nrows == 32, 2, kind, t.mt * 128, t.row + c0);
+          stored(nrows == 32, 2, t.mt * 128, row0 + c0);
           if (nrows < 32) {
             const int r0 = gt >> 4, col = t.mt * 128 + (gt & 15) * 8;
 #pragma unroll
             for (int p = 0; p < 4; p++) {
               const int r = r0 + 8 * p;
-              if (r < nrows && col + 8 <= a.M[kind])
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[kind]) + (t.row + c0 + r) * ldo + col) =
+              if (r < nrows && col + 8 <= a.M)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (row0 + c0 + r) * ldo + col) =
                     *reinterpret_cast<const uint4*>(ebuf + ((gt >> 3) & 1) * EPI_BOX_BYTES + r * 128 +
                                                     (((gt & 7) ^ (r & 7)) << 4));
             }
@@ -936,7 +933,7 @@ constexpr int kImgThreads = 256;
 struct ImageArgs {
   const uint8_t* xs;
   int64_t x_rows;
-  const int32_t* offsets;  // NULL: one group of all rows
+  const int32_t* offsets;
   int n_groups, pitch, nk;
   uint8_t* image;
 };
@@ -951,12 +948,8 @@ __global__ void __launch_bounds__(kImgThreads) k_mx4_scale_image(const __grid_co
   grid_dep_launch();
   int64_t lo = 0, hi = 0;
   if ((int)threadIdx.x < a.n_groups) {
-    if (a.offsets) {
-      lo = min(max((int64_t)a.offsets[threadIdx.x], (int64_t)0), a.x_rows);
-      hi = min(max((int64_t)a.offsets[threadIdx.x + 1], lo), a.x_rows);
-    } else {
-      hi = a.x_rows;
-    }
+    lo = min(max((int64_t)a.offsets[threadIdx.x], (int64_t)0), a.x_rows);
+    hi = min(max((int64_t)a.offsets[threadIdx.x + 1], lo), a.x_rows);
   }
   const int tiles = (int)((hi - lo + kWide - 1) / kWide);
   int incl = tiles;
@@ -1063,13 +1056,16 @@ static int64_t image_tiles(int64_t rows, int groups) { return (rows + kWide - 1)
 int64_t mx4_image_bytes(int64_t rows, int groups, int K) {
   return mx4_token_tile(rows, groups) == kWide ? image_tiles(rows, groups) * mx4_kblocks(K) * 1024 : 0;
 }
+int64_t mx4_most_image_bytes(int64_t rows, int groups, int K) {
+  return image_tiles(rows, groups) * mx4_kblocks(K) * 1024;
+}
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
                     Ring<kWide, 2>::BLKS, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
-cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t rows, const int32_t* offsets,
-                              int groups, int K, uint8_t* image) {
-  const ImageArgs a{scales, rows, offsets, groups, K / 32, mx4_kblocks(K), image};
+cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
+                              int64_t rows, int groups, int K, uint8_t* image) {
+  const ImageArgs a{scales, x_rows, offsets, groups, K / 32, mx4_kblocks(K), image};
   return launch_k(lc, k_mx4_scale_image, (unsigned)image_tiles(rows, groups), kImgThreads, 0, a);
 }
 // bf16 output rows: boxes of 64 columns x 32 rows
@@ -1079,13 +1075,13 @@ int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ld
 }
 // packed weight: boxes of a stage's blocks, and of one (the pair's copies
 // count on the leader's barrier, which only tensor copies can)
-int encode_mx4_weight(CUtensorMap* stage, CUtensorMap* one, const void* packed, int64_t bytes) {
+int encode_mx4_weight(CUtensorMap* tm, const void* packed, int64_t bytes) {
   constexpr int line = kMx4BlkBytes / kBlkLines;
-  const int rc = encode_box(stage, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line,
-                            Ring<kWide, 2>::BLKS * kBlkLines, CU_TENSOR_MAP_SWIZZLE_NONE);
-  return rc ? rc
-            : encode_box(one, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line, kBlkLines,
-                         CU_TENSOR_MAP_SWIZZLE_NONE);
+  int rc = AFD_OK;
+  for (int i = 0; i < 2 && !rc; i++)
+    rc = encode_box(tm + i, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line,
+                    (i ? 1 : Ring<kWide, 2>::BLKS) * kBlkLines, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return rc;
 }
 
 extern "C" int afd_mx4_poll_status(void* cuda_stream) {

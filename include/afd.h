@@ -128,6 +128,16 @@ extern "C" {
  * and no launch boundary separates the two.  This flag launches them as two
  * kernels instead (the stage times then split them). */
 #define AFD_CFG_SPLIT_GEMMS 4
+/* The experts (routed and shared) in MXFP4: afd_set_layer codes the weights
+ * it is given (AFD_MX4_SCALE_FLOOR; weights whose bf16 values are MXFP4
+ * values already are kept exactly), and every step codes the gathered rows
+ * and, in bf16, the SwiGLU rows the same way, multiplies the codes on the
+ * tensor cores with fp32 accumulation (afd_mx4_gemm) and leaves the rest of
+ * the step as it is.  A layer's weights take 0.53 bytes per element instead
+ * of 2.  bf16 activations, AFD_GEMM_TENSOR, hidden, inter and shared_inter
+ * multiples of 32 (else AFD_ERR_UNSUPPORTED); AFD_CFG_SPLIT_GEMMS has no
+ * meaning with it, and AFD_WS_H and AFD_WS_HS are not written. */
+#define AFD_CFG_MX4 8
 typedef struct afd_config {
   int32_t num_peers;
   int32_t ring_depth;

@@ -127,3 +127,17 @@ def test_ffn_workspace():
     for bad in ((-1, 2, 128, 96), (4, 2, 128, 40), (4, 0, 128, 96), (4, 257, 128, 96), (4, 2, 130, 96)):
         assert A.afd_mx4_ffn_workspace(*bad) == -1, bad
     assert A.afd_mx4_ffn(**{**FFN, "n_rows": 100, "inter": 96, "workspace_bytes": n - 1}) == A.AFD_ERR_CAPACITY
+
+
+def test_mx4_configuration():
+    ok = dict(num_peers=2, token_cap=64, hidden=256, num_experts=8, topk=2, inter=64, shared_inter=32,
+              flags=A.AFD_CFG_MX4)
+    assert A.afd_slot_layout(A.make_config(**ok)).window_bytes > 0
+    for bad in (dict(hidden=264), dict(inter=48), dict(shared_inter=48), dict(gemm=A.AFD_GEMM_SIMT),
+                dict(gemm=A.AFD_GEMM_TENSOR_1CTA), dict(act="f32", gemm=A.AFD_GEMM_SIMT)):
+        with pytest.raises(A.AfdError) as e:
+            A.afd_slot_layout(A.make_config(**{**ok, **bad}))
+        assert e.value.code == A.AFD_ERR_UNSUPPORTED, bad
+    with pytest.raises(A.AfdError) as e:
+        A.afd_slot_layout(A.make_config(**{**ok, "flags": 16}))
+    assert e.value.code == A.AFD_ERR_ARG
