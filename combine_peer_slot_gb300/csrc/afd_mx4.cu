@@ -13,8 +13,8 @@ namespace {
 constexpr int kThreads = 256;
 int64_t g_mx4_launches = 0;
 
-// Both coding kernels walk the matrix in chunks of eight values, a CTA
-// kChunks * 256 consecutive ones, a thread every 256th of them: a warp's
+// Both coding kernels walk the matrix in chunks of eight (or four) values, a
+// CTA kChunks * 256 consecutive ones, a thread every 256th of them: a warp's
 // loads and stores are contiguous whatever the row length, and each thread
 // has kChunks independent loads in flight.  The row of the CTA's first chunk
 // takes one 64-bit division, the rest 32-bit ones by multiplication.
@@ -150,10 +150,13 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize_step(const __grid_con
 
 // ---------------------------------------------------------------------------
 // dequantise: every value fits bf16 and fp32 exactly (three significant
-// bits, exponents within both types').  Bound by memory.
+// bits, exponents within both types').  Bound by memory.  A chunk is what
+// 16 output bytes hold, eight bf16 or four fp32 values, so that a warp's
+// stores are one run (fp32 as two stores of eight values wrote half sectors:
+// 45 MB took 14 us).
 // ---------------------------------------------------------------------------
 struct DequantArgs {
-  const uint32_t* codes;
+  const uint8_t* codes;
   const uint8_t* scales;
   int64_t n_rows;
   int chunks;
@@ -172,8 +175,10 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const __grid_consta
 #pragma unroll
   for (int u = 0; u < kChunks; u++) {
     const int64_t i = first + u * kThreads + threadIdx.x;
-    code[u] = i < total ? a.codes[i] : 0u;
-    scale[u] = i < total ? mx4_scale(a.scales[i >> 2]) : 0.0f;
+    code[u] = i >= total ? 0u
+              : F32      ? (uint32_t)reinterpret_cast<const uint16_t*>(a.codes)[i]
+                         : reinterpret_cast<const uint32_t*>(a.codes)[i];
+    scale[u] = i < total ? mx4_scale(a.scales[i >> (F32 ? 3 : 2)]) : 0.0f;
   }
 #pragma unroll
   for (int u = 0; u < kChunks; u++) {
@@ -190,15 +195,14 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const __grid_consta
         : "r"(code[u]));
     float2 v[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < (F32 ? 2 : 4); j++) {
       v[j] = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
       v[j].x *= scale[u];
       v[j].y *= scale[u];
     }
-    uint4* p = reinterpret_cast<uint4*>(a.out + r * a.ld_bytes + (int64_t)c * (F32 ? 32 : 16));
+    uint8_t* p = a.out + r * a.ld_bytes + (int64_t)c * 16;
     if (F32) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+      *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     } else {
       uint32_t b[4];
 #pragma unroll
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const __grid_consta
         const __nv_bfloat162 x = __floats2bfloat162_rn(v[j].x, v[j].y);
         b[j] = *reinterpret_cast<const uint32_t*>(&x);
       }
-      p[0] = make_uint4(b[0], b[1], b[2], b[3]);
+      *reinterpret_cast<uint4*>(p) = make_uint4(b[0], b[1], b[2], b[3]);
     }
   }
 }
@@ -387,10 +391,10 @@ int afd_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n_ro
   LaunchCtx lc;
   if (!rc) rc = make_lc(cuda_stream, &lc);
   if (rc) return rc;
-  const int chunks = cols / 8;
+  const int chunks = cols / (16 / es);
   const int64_t grid = chunk_grid(n_rows * chunks);
   if (grid >= (int64_t)1 << 31) return AFD_ERR_UNSUPPORTED;
-  const DequantArgs a{reinterpret_cast<const uint32_t*>(codes), scales, n_rows, chunks, 0xffffffffu / (uint32_t)chunks,
+  const DequantArgs a{codes, scales, n_rows, chunks, 0xffffffffu / (uint32_t)chunks,
                       static_cast<uint8_t*>(out), ldo * es};
   return launched(es == 4 ? launch_k(lc, k_mx4_dequantize<true>, (unsigned)grid, kThreads, 0, a)
                           : launch_k(lc, k_mx4_dequantize<false>, (unsigned)grid, kThreads, 0, a),

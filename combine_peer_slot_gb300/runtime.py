@@ -344,13 +344,8 @@ def _bad(what):
     raise A.AfdError(A.AFD_ERR_ARG, what)
 
 
-def _device(t):
-    """t's device and the handle of its current stream.  t has to live on the
-    current device, where the library launches (it refuses other pointers)."""
-    if not t.is_cuda:
-        raise A.AfdError(A.AFD_ERR_NOT_DEVICE, "a CUDA tensor is wanted")
-    d = t.device
-    return d, _host.raw_stream(d.index)
+def _not_cuda():
+    raise A.AfdError(A.AFD_ERR_NOT_DEVICE, "a CUDA tensor is wanted")
 
 
 def _rows_int32(h, t, n, what):
@@ -364,11 +359,11 @@ _RULES = {"floor": A.AFD_MX4_SCALE_FLOOR, "ceil": A.AFD_MX4_SCALE_CEIL}
 
 def route_select(logits, topk, bias=None, score="softmax", n_groups=1, topk_groups=1, group_top=1,
                  renorm=False, routed_scaling=1.0):
-    """afd_route_select of logits [T, E] (bf16 or fp32, any row pitch):
-    (ids int32 [T, topk], weights fp32 [T, topk])."""
+    """afd_route_select of logits [T, E] (bf16 or fp32, any row pitch; on the
+    current device): (ids int32 [T, topk], weights fp32 [T, topk])."""
     h = _host or _get()
-    code = h.code.get(logits.dtype)
-    if code is None or logits.dim() != 2 or score not in _SCORES:
+    code, kind = h.code.get(logits.dtype), _SCORES.get(score)
+    if code is None or kind is None or logits.dim() != 2:
         _bad("logits: bf16 or fp32 rows [T, E] wanted, score softmax or sigmoid")
     T, E = logits.shape
     ld, step = logits.stride()
@@ -379,12 +374,14 @@ def route_select(logits, topk, bias=None, score="softmax", n_groups=1, topk_grou
         if bias.dtype is not h.f32 or bias.shape != (E,) or not bias.is_contiguous():
             _bad("bias: contiguous fp32 [E] wanted")
         bias_ptr = bias.data_ptr()
-    dev, stream = _device(logits)
+    if not logits.is_cuda:
+        _not_cuda()
+    dev = logits.device
     ids = h.empty((T, topk), dtype=h.int32, device=dev)
     weights = h.empty((T, topk), dtype=h.f32, device=dev)
-    rc = h.select(logits.data_ptr(), ld if T > 1 else E, T, code, bias_ptr, E, topk, _SCORES[score], n_groups,
-                  topk_groups, group_top, 1 if renorm else 0, routed_scaling, ids.data_ptr(), weights.data_ptr(),
-                  stream)
+    rc = h.select(logits.data_ptr(), ld if T > 1 else E, T, code, bias_ptr, E, topk, kind, n_groups, topk_groups,
+                  group_top, 1 if renorm else 0, routed_scaling, ids.data_ptr(), weights.data_ptr(),
+                  h.raw_stream(dev.index))
     if rc:
         raise A.AfdError(rc, "afd_route_select")
     return ids, weights
@@ -418,13 +415,15 @@ def mx4_quantize(x, src_rows=None, topk=1, rule="floor"):
     if src_rows is not None:
         _rows_int32(h, src_rows, -1, "src_rows")
         n, src = src_rows.shape[0], src_rows.data_ptr()
-    dev, stream = _device(x)
+    if not x.is_cuda:
+        _not_cuda()
+    dev = x.device
     q = Mx4.__new__(Mx4)
     q.codes = codes = h.empty((n, cols // 2), dtype=h.uint8, device=dev)
     q.scales = scales = h.empty((n, cols // 32), dtype=h.uint8, device=dev)
     q.rows, q.cols = n, cols
     rc = h.quantize(x.data_ptr(), ld if n_x > 1 else cols, n_x, cols, code, src, topk, n, _RULES[rule],
-                    codes.data_ptr(), scales.data_ptr(), stream)
+                    codes.data_ptr(), scales.data_ptr(), h.raw_stream(dev.index))
     if rc:
         raise A.AfdError(rc, "afd_mx4_quantize")
     return q
@@ -436,9 +435,12 @@ def mx4_dequantize(q, dtype):
     code = h.code.get(dtype)
     if code is None:
         _bad(f"dtype {dtype}: bfloat16 or float32 wanted")
-    dev, stream = _device(q.codes)
+    if not q.codes.is_cuda:
+        _not_cuda()
+    dev = q.codes.device
     out = h.empty((q.rows, q.cols), dtype=dtype, device=dev)
-    rc = h.dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, code, out.data_ptr(), q.cols, stream)
+    rc = h.dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, code, out.data_ptr(), q.cols,
+                      h.raw_stream(dev.index))
     if rc:
         raise A.AfdError(rc, "afd_mx4_dequantize")
     return out
@@ -459,10 +461,12 @@ class Mx4Weight:
         nbytes = A.afd_mx4_weight_bytes(self.experts, self.M, self.K, self.swiglu)
         if nbytes <= 0:
             _bad(f"weight dimensions {(self.experts, self.M, self.K)}")
-        dev, stream = _device(codes)
+        if not codes.is_cuda:
+            _not_cuda()
+        dev = codes.device
         self.packed = h.empty(nbytes, dtype=h.uint8, device=dev)
         A._check(A.afd_mx4_pack_weight(codes.data_ptr(), scales.data_ptr(), self.experts, self.M, self.K,
-                                       self.swiglu, self.packed.data_ptr(), nbytes, stream),
+                                       self.swiglu, self.packed.data_ptr(), nbytes, h.raw_stream(dev.index)),
                  "afd_mx4_pack_weight")
 
 
@@ -498,12 +502,14 @@ def mx4_gemm(x, offsets, weight, out_dtype=None, out=None, workspace=None):
     _rows_int32(h, offsets, weight.experts + 1, "offsets")
     if x.cols != weight.K:
         _bad(f"rows of {x.cols} columns, weight of {weight.K}")
-    dev, stream = _device(x.codes)
+    if not x.codes.is_cuda:
+        _not_cuda()
+    dev = x.codes.device
     out, ldo, code = _output(h, x, weight.M // 2 if weight.swiglu else weight.M, out_dtype, out, dev)
     ws, ws_bytes, keep = _scratch(h, workspace, h.gemm_workspace(x.rows, weight.experts, weight.K), dev)
     rc = h.gemm(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), weight.experts,
                 weight.packed.data_ptr(), weight.M, weight.K, 1 if weight.swiglu else 0, code, out.data_ptr(), ldo,
-                ws, ws_bytes, stream)
+                ws, ws_bytes, h.raw_stream(dev.index))
     if rc:
         raise A.AfdError(rc, "afd_mx4_gemm")
     return out
@@ -518,12 +524,14 @@ def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
             or x.cols != hidden):
         _bad("w13 / wd / x dimensions do not match")
     _rows_int32(h, offsets, wd.experts + 1, "offsets")
-    dev, stream = _device(x.codes)
+    if not x.codes.is_cuda:
+        _not_cuda()
+    dev = x.codes.device
     out, ldo, code = _output(h, x, hidden, out_dtype, out, dev)
     ws, ws_bytes, keep = _scratch(h, workspace, h.ffn_workspace(x.rows, wd.experts, hidden, inter), dev)
     rc = h.ffn(x.codes.data_ptr(), x.scales.data_ptr(), x.rows, offsets.data_ptr(), wd.experts,
                w13.packed.data_ptr(), wd.packed.data_ptr(), hidden, inter, code, out.data_ptr(), ldo,
-               ws, ws_bytes, stream)
+               ws, ws_bytes, h.raw_stream(dev.index))
     if rc:
         raise A.AfdError(rc, "afd_mx4_ffn")
     return out
