@@ -341,12 +341,13 @@ int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8
 // the products of the calls without a context
 static int product(LaunchCtx& lc, const uint8_t* codes, const uint8_t* scales, uint8_t* image, int64_t n_rows,
                    const int32_t* offsets, int E, const void* w, int M, int K, int swiglu, int fmt, void* out,
-                   int64_t ldo, uint8_t* out_scales = nullptr) {
+                   int64_t ldo, uint8_t* out_scales = nullptr, int early = 0) {
   Mx4GemmArgs a;
   memset(&a, 0, sizeof a);
   a.w = static_cast<const uint8_t*>(w);
   a.out = out;
   a.out_lo = out_scales;
+  a.early = early;
   a.ldo = ldo;
   a.fmt = fmt;
   return mx4_product(lc, a, codes, scales, image, n_rows, n_rows, offsets, E, M, K, swiglu);
@@ -486,7 +487,7 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, con
   lc.pdl = 1;  // the second product's set-up runs while the first drains
   if (!rc)
     rc = product(lc, hc, wide ? nullptr : hs, hs, n_rows, offsets, num_experts, wd, hidden, inter, 0,
-                 out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo);
+                 out_dtype == AFD_DTYPE_F32 ? OUT_F32 : OUT_ACT, out, ldo, nullptr, /*early=*/1);
   return rc;
 }
 

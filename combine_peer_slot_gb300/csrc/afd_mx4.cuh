@@ -60,6 +60,8 @@ struct Mx4GemmArgs {
   const DevLayer* layers;
   const FanIn* item;
   int wsel;
+  // the kernel before writes the rows only; launched with lc.pdl
+  int early;
 };
 // bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
 // output tiles, which sizes the grid

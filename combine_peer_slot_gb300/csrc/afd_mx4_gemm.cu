@@ -22,7 +22,8 @@
 // stage of 400 tensor cycles, over the 128 bytes a cycle shared memory has;
 // the pair 31 and 28 KB.
 //
-// Warps: 0 copies, 1 MMA, from 2 scales, 8-15 epilogue.  All waits are
+// Warps: 0 weight copies, 1 MMA, from 2 scales, 3 or 7 token copies, 8-15
+// epilogue.  All waits are
 // bounded.
 #include "afd_mx4.cuh"
 
@@ -70,8 +71,9 @@ struct Ring {
   // than stages: a warp that has filled stage i waits next for the release of
   // i + SF_WARPS - STAGES, and a parity wait tells a phase from the one
   // before it only; with more warps than stages it could pass one round early.
-  static constexpr int SF_WARPS = CTAS == 2 ? 0 : 6;
-  static_assert(SF_WARPS <= STAGES && 2 + SF_WARPS <= EPI_WARP0, "scale warps");
+  static constexpr int SF_WARPS = CTAS == 2 ? 0 : 5;
+  static constexpr int TOKEN_WARP = CTAS == 2 ? 3 : 7;   // copies the tokens' codes
+  static_assert(SF_WARPS <= STAGES && 2 + SF_WARPS <= (CTAS == 2 ? EPI_WARP0 : TOKEN_WARP), "scale warps");
   static constexpr int NB = (BN + 127) / 128;            // 128-row scale images per 128 columns
   static constexpr int B_ROWS = BN / CTAS;               // token rows whose codes a CTA holds
   static constexpr int X_BYTES = B_ROWS * (BOX / 2);     // one token box
@@ -446,8 +448,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
   }
-  grid_dep_wait();
-  grid_dep_launch();
+  // a.early: the rows alone come from the kernel before; the groups and the
+  // weight are older, so this CTA's first weight copies go out while that
+  // kernel's last CTAs run, and only the roles that touch the rows wait
+  if (!a.early) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
   // the groups: rows clamped to those there are, units counted
   const int ngroups = a.n_groups;
   int mine = 0, tiles = 0;
@@ -505,11 +512,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   const uint8_t* wbase = lw ? lw->packed : a.w;
   const uint32_t smem_base = smem_u32(smem);
 
-  if (warp == 0 || (CTAS == 2 && warp == 3)) {
+  if (warp == 0 || warp == R::TOKEN_WARP) {
     if (lane == 0) {
-      // ------------------------------ copies (wide: warp 0 the weight's, warp
-      // 3 the tokens'; one thread issuing them all was on the ring's path)
-      const bool weights = warp == 0, tokens = CTAS == 1 || warp == 3;
+      // ------------------------------ copies: warp 0 the weight's, another the
+      // tokens' (one thread issuing them all was on the wide ring's path, and
+      // the weight's need not wait where the rows must)
+      const bool weights = warp == 0, tokens = !weights;
+      if (tokens && a.early) grid_dep_wait();
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -549,8 +558,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                                full_leader);
             }
           } else {
-            bulk_load(sa, wbase + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
-            tma_load_2d(sx, &a.tmX, kb * (BOX / 2), (int)t.row, full);
+            if (weights)
+              bulk_load(sa, wbase + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
+            else
+              tma_load_2d(sx, &a.tmX, kb * (BOX / 2), (int)t.row, full);
           }
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
@@ -684,6 +695,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     __syncwarp();
   } else if (CTAS == 1 && warp < 2 + R::SF_WARPS) {
     // ------------------------------ narrow: token scales, the warps take stages in turn
+    if (a.early) grid_dep_wait();
     Walk<BN, CTAS> w(a, tail, ngroups, total);
     int kb = 0;
     auto advance = [&](int n) {  // n stages on
@@ -917,6 +929,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(R::TMEM_COLS));
   }
+  // a CTA without units as well: this kernel's end says that the one before has ended
+  if (a.early) grid_dep_wait();
 }
 
 constexpr int kWide = 192, kNarrow = 64;
