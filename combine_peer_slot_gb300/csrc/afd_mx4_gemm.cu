@@ -92,7 +92,8 @@ struct Ring {
   struct Tail {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t sfull[STAGES];     // wide: the stage's scales are in TMEM
+    uint64_t sfull[2][STAGES];  // wide: the scales of the stage's first, second half are in TMEM
+    uint64_t hfree[2];          // wide: the slot's first half has been multiplied
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -424,10 +425,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; s++) {
       mbar_init(smem_u32(&tail->full[s]), CTAS == 2 ? 1 : 2);  // the producer (the leader's), the scale warp
-      mbar_init(smem_u32(&tail->sfull[s]), 2);  // the two scale warps
+      mbar_init(smem_u32(&tail->sfull[0][s]), 1);
+      mbar_init(smem_u32(&tail->sfull[1][s]), 1);
       mbar_init(smem_u32(&tail->empty[s]), 1);
     }
     for (int b = 0; b < 2; b++) {
+      mbar_init(smem_u32(&tail->hfree[b]), 1);
       mbar_init(smem_u32(&tail->tfull[b]), 1);
       mbar_init(smem_u32(&tail->tempty[b]), CTAS * EPI_WARPS);
     }
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       for (;;) {
         if (!ready) {
           if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
-          if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[s]), ph, abort_flag, deadline, status)) break;
+          if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[0][s]), ph, abort_flag, deadline, status)) break;
           word = *(volatile uint32_t*)&tail->info[s];
         }
         const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
@@ -604,7 +607,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const int s1 = s + 1 == STAGES ? 0 : s + 1;
         const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
         const uint32_t test = mbar_test_wait(smem_u32(&tail->full[s1]), ph1) &
-                              (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[s1]), ph1) : 1u);
+                              (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[0][s1]), ph1) : 1u);
+        const uint32_t test_half = CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[1][s]), ph) : 1u;
         const uint32_t id0 = idesc_mx4<CTAS>((int)(info & 511u), 0), id2 = id0 | idesc_mx4<CTAS>(0, 2);
         const uint32_t d = tm + (uint32_t)(acc * BN);
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
@@ -621,14 +625,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                         desc(kDescTokens, sb + (kk >> 2) * (R::X_BYTES >> 4) + (kk & 3) * 2), o ? id2 : id0, sf + 4 * c,
                         sf + 4 * R::BLKS + 4 * c * NB, kk > 0 ? 1u : more);
         };
+        // wide: the first half's columns of the slot are free; the second half's scales are there
+        auto half_way = [&]() {
+          if (CTAS == 1) return true;
+          commit_local<CTAS>(el, smem_u32(&tail->hfree[slot]));
+          if (!__all_sync(0xffffffffu, test_half != 0) &&
+              !warp_wait(smem_u32(&tail->sfull[1][s]), ph, abort_flag, deadline, status))
+            return false;
+          tc_fence_after();
+          return true;
+        };
         constexpr int FULL = R::BK / 64;
-        if (steps == FULL) {  // no branch between the instructions of a whole stage
+        if (steps == FULL) {  // few branches between the instructions of a whole stage
 #pragma unroll
           for (int c = 0; c < R::BLKS; c++) scales(c);
           ready = __all_sync(0xffffffffu, test != 0);
 #pragma unroll
           for (int kk = 0; kk < FULL / 2; kk++) mma(kk);
           word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
+          if (!half_way()) break;
 #pragma unroll
           for (int kk = FULL / 2; kk < FULL; kk++) mma(kk);
         } else {              // the unit's last columns
@@ -638,7 +653,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           ready = __all_sync(0xffffffffu, test != 0);
           word = *(volatile uint32_t*)&tail->info[s1];
 #pragma unroll
-          for (int kk = 0; kk < FULL - 1; kk++)
+          for (int kk = 0; kk < FULL / 2; kk++)
+            if (kk < steps) mma(kk);
+          if (!half_way()) break;
+#pragma unroll
+          for (int kk = FULL / 2; kk < FULL - 1; kk++)
             if (kk < steps) mma(kk);
         }
         if (++slot == R::SF_SLOTS) slot = 0;
@@ -669,17 +688,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
         const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
         if (info & INFO_STOP) {
-          if (lane == 0) mbar_arrive(smem_u32(&tail->sfull[s]));
+          if (lane == 0 && warp == 2) mbar_arrive(smem_u32(&tail->sfull[0][s]));
           break;
         }
         tc_fence_after();
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
         const uint32_t ss = sa + ((R::A_BYTES + R::B_BYTES) >> 4);
         const uint32_t sf = tm + (uint32_t)(R::SF_BASE + (n % R::SF_SLOTS) * R::SF_COLS);
-        if (n >= R::SF_SLOTS) {  // the slot's last stage has been multiplied
+        if (n >= R::SF_SLOTS) {  // this half of the slot's last stage has been multiplied
           const int m = n - R::SF_SLOTS;
-          if (!warp_wait(smem_u32(&tail->empty[m % STAGES]), (uint32_t)(m / STAGES) & 1u, abort_flag, deadline, status))
-            break;
+          const bool go = warp == 2 ? warp_wait(smem_u32(&tail->hfree[m % R::SF_SLOTS]), (uint32_t)(m / R::SF_SLOTS) & 1u,
+                                                abort_flag, deadline, status)
+                                    : warp_wait(smem_u32(&tail->empty[m % STAGES]), (uint32_t)(m / STAGES) & 1u,
+                                                abort_flag, deadline, status);
+          if (!go) break;
           tc_fence_after();
         }
         const int steps = (int)(info >> 9) & 15;
@@ -688,7 +710,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           const int c = warp == 2 ? i : R::BLKS / 2 + i;
           if (2 * c < steps) issue_scales<CTAS, NB, R::BLKS>(el, c, sa, ss, sf);
         }
-        commit_local<CTAS>(el, smem_u32(&tail->sfull[s]));
+        commit_local<CTAS>(el, smem_u32(&tail->sfull[warp == 2 ? 0 : 1][s]));
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
