@@ -1151,8 +1151,10 @@ static int forward_impl(afd_ctx* ctx, int layer, FanIn& f, const PeerList* dev) 
   const int64_t Tcap = ctx->tmax;
   const int64_t win_rows = ctx->L.window_bytes / row_bytes;
   if (mx4) {
-    // (a step of the work-item loop: the most shared rows are its tokens)
-    rc = experts_mx4(ctx, L, N, !has_shared ? 0 : dev ? T : f.stotal, grouped);
+    // a step of the work-item loop: the most rows its slots can bring (f's
+    // totals size the other kernels' launches, which the device's counts bound)
+    const int64_t most = std::min<int64_t>((int64_t)ctx->tmax * c.topk, (int64_t)f.n_peers * rows_cap);
+    rc = experts_mx4(ctx, L, dev && grouped ? most : N, !has_shared ? 0 : dev ? T : f.stotal, grouped);
     if (rc) return rc;
   } else if (N + T > 0) {
     if (c.gemm != AFD_GEMM_SIMT) {

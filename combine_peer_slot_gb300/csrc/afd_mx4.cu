@@ -335,6 +335,7 @@ int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8
   a.offsets = offsets;
   a.n_groups = groups;
   a.swiglu = swiglu;
+  a.tiles = (int)mx4_image_tiles(rows, groups);
   return launched(launch_mx4_gemm(lc, a, bn, units), "mx4 gemm");
 }
 

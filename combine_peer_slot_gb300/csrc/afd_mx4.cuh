@@ -62,12 +62,14 @@ struct Mx4GemmArgs {
   int wsel;
   // the kernel before writes the rows only; launched with lc.pdl
   int early;
+  int tiles;                 // token tiles the images hold (more only for offsets that overlap)
 };
 // bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
 // output tiles, which sizes the grid
 int mx4_token_tile(int64_t rows, int groups);
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units);
 int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn);
+int64_t mx4_image_tiles(int64_t rows, int groups);
 int64_t mx4_image_bytes(int64_t rows, int groups, int K);
 int64_t mx4_most_image_bytes(int64_t rows, int groups, int K);  // over all row counts up to rows
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);

@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                   make_uint2(code[0], code[1]);
               if (CTAS == 1 && (gt & 1) == 0) a.out_lo[at / 32] = (uint8_t)sc;
             }
-            if (CTAS == 2 && (gt & 1) == 0 && r < nrows) {
+            if (CTAS == 2 && (gt & 1) == 0 && r < nrows && t.tile < a.tiles) {
               // into the next product's scale images; zeros past inter's
               // end, so that no stray scale meets the zero columns there
               const int blk = f / 32, nk2 = mx4_kblocks(I), rt = c0 + r;
@@ -1088,12 +1088,14 @@ int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int 
 }
 // Scale images of `rows` rows in `groups` groups over K columns (wide form;
 // 0 bytes for the narrow one)
-static int64_t image_tiles(int64_t rows, int groups) { return (rows + kWide - 1) / kWide + std::min<int64_t>(groups, rows); }
+int64_t mx4_image_tiles(int64_t rows, int groups) {
+  return (rows + kWide - 1) / kWide + std::min<int64_t>(groups, rows);
+}
 int64_t mx4_image_bytes(int64_t rows, int groups, int K) {
-  return mx4_token_tile(rows, groups) == kWide ? image_tiles(rows, groups) * mx4_kblocks(K) * 1024 : 0;
+  return mx4_token_tile(rows, groups) == kWide ? mx4_image_tiles(rows, groups) * mx4_kblocks(K) * 1024 : 0;
 }
 int64_t mx4_most_image_bytes(int64_t rows, int groups, int K) {
-  return image_tiles(rows, groups) * mx4_kblocks(K) * 1024;
+  return mx4_image_tiles(rows, groups) * mx4_kblocks(K) * 1024;
 }
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
@@ -1102,7 +1104,7 @@ int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
                               int64_t rows, int groups, int K, uint8_t* image) {
   const ImageArgs a{scales, x_rows, offsets, groups, K / 32, mx4_kblocks(K), image};
-  return launch_k(lc, k_mx4_scale_image, (unsigned)image_tiles(rows, groups), kImgThreads, 0, a);
+  return launch_k(lc, k_mx4_scale_image, (unsigned)mx4_image_tiles(rows, groups), kImgThreads, 0, a);
 }
 // bf16 output rows: boxes of 64 columns x 32 rows
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo) {

@@ -365,7 +365,7 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
 // once; each choice is then one warp-wide integer maximum of the lanes'
 // heads, and the owner moves to its next value.
 template <typename LT, int PER>
-__global__ void __launch_bounds__(kSelWarps * 32) k_route_select(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid_constant__ SelArgs a) {
   __shared__ Contenders contenders[kSelWarps];
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kSelWarps + (threadIdx.x >> 5);

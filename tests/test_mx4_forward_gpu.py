@@ -177,6 +177,30 @@ def test_work_item_loop(graph):
     run.close()
 
 
+def test_token_level_dispatch_to_two_ranks(monkeypatch):
+    """The experts split over two FFN ranks, each with its block in MXFP4."""
+    plain = A.make_config
+    monkeypatch.setattr(A, "make_config", lambda *a, **k: plain(*a, **{**k, "flags": A.AFD_CFG_MX4}))
+    w = W.custom("fanin", seq_lens=[37, 91])
+    rs = R.RankSet(w, 2)
+    rs.route()
+    rs.dispatch_all()
+    rs.serve_all()
+    outs = rs.combine_all()
+    assert rs.poll() == (0, 0)
+    for p, n in enumerate(w.seq_lens):
+        xq = coded(rs.x[p])
+        wt = rs.weights[0]
+        want = ffn64(xq, wt["W13s"], wt["Wds"])
+        for e in range(w.num_experts):
+            t, j = (rs.ids[p][:n] == e).nonzero(as_tuple=True)
+            if t.numel():
+                want[t] += rs.wts[p][t, j].double().unsqueeze(1) * ffn64(xq[t], wt["W13"][e], wt["Wd"][e])
+        # the ranks' outputs travel in bf16: another 2^-8 of each term
+        assert float((outs[p][:n].double() - want).norm() / want.norm()) <= TOL + 2.0 ** -8
+    rs.close()
+
+
 def test_weights_that_are_mxfp4_already_are_kept():
     """bf16 weights whose values are MXFP4 values code to themselves."""
     w = torch.randn(300, 256, device="cuda").bfloat16()

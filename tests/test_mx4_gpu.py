@@ -260,6 +260,40 @@ def test_ffn_equals_its_parts(counts, hidden, inter, dtype):
     assert torch.equal(got, want)
 
 
+def test_ffn_not_finite():
+    """A NaN block of one row reaches that row's output only, as in the parts."""
+    for counts in ([30, 5], [300, 250]):
+        n = sum(counts)
+        x = torch.randn(n, 256, generator=gen(2), device="cuda").bfloat16()
+        x[7, 40] = math.nan
+        x[n - 1, 255] = math.inf
+        q = R.mx4_quantize(x)
+        off = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+        w13, wd, _, _ = ffn_weights(2, 256, 96, 4)
+        got = R.mx4_ffn(q, off, w13, wd)
+        want = R.mx4_gemm(R.mx4_quantize(R.mx4_gemm(q, off, w13)), off, wd)
+        assert same_values(got, want)
+        bad = torch.isnan(got).all(1)
+        assert bad[7] and bad[n - 1] and int(torch.isnan(got).any(1).sum()) == 2
+
+
+@pytest.mark.parametrize("offsets", [[0, 400, 0, 400], [400, 0, 400, 0], [-7, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1]])
+def test_offsets_that_overlap_stay_in_bounds(offsets):
+    """Not a valid call: its results mean nothing, but nothing outside its
+    outputs and workspace is written and the next call is right."""
+    w13, wd, _, _ = ffn_weights(3, 256, 96, 5)
+    x = R.mx4_quantize(torch.randn(400, 256, generator=gen(6), device="cuda"))
+    need = A.afd_mx4_ffn_workspace(400, 3, 256, 96)
+    ws = torch.full((need + 65536,), 171, dtype=torch.uint8, device="cuda")
+    out = torch.full((400 + 64, 256), 3.0, dtype=torch.bfloat16, device="cuda")
+    R.mx4_ffn(x, torch.tensor(offsets, device="cuda").int(), w13, wd, out=out[:400], workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 171).all() and (out[400:] == 3.0).all()
+    off = torch.tensor([0, 100, 250, 400], device="cuda").int()
+    want = R.mx4_gemm(R.mx4_quantize(R.mx4_gemm(x, off, w13)), off, wd)
+    assert torch.equal(R.mx4_ffn(x, off, w13, wd, out=out[:400], workspace=ws[:need]), want)
+
+
 # ---- together ----------------------------------------------------------------------
 def test_gate_coding_experts_and_sum_together():
     """A layer as it is used: the gate's choice, positions by expert, the
