@@ -102,7 +102,7 @@ struct PeerList {
 // one entry per layer in device memory ("layer-select" operators of the
 // Async AFD RFC: the address table of every layer plus a device-side index)
 struct DevMx4Weight {  // a weight packed in MXFP4
-  CUtensorMap tm[2];      // boxes of a stage's blocks, of one block
+  CUtensorMap tm[2];      // boxes of two blocks, of one block
   const uint8_t* packed;
 };
 struct DevLayer {  // aligned as its tensor maps

@@ -77,7 +77,7 @@ int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
                               int64_t rows, int groups, int K, uint8_t* image);
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo);
-int encode_mx4_weight(CUtensorMap* tm /* [2]: a stage's blocks, one block */, const void* packed, int64_t bytes);
+int encode_mx4_weight(CUtensorMap* tm /* [2]: a part's blocks, one block */, const void* packed, int64_t bytes);
 
 cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx, int64_t x_rows, int f32,
                                 const int32_t* src_rows, int topk, int64_t n_rows, int cols, int ceil_rule,

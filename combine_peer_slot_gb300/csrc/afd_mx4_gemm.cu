@@ -65,7 +65,12 @@ struct Ring {
   // of its cycles.
   static constexpr int BK = CTAS == 2 ? 512 : 256;
   static constexpr int STAGES = CTAS == 2 ? 3 : 7;
+  // A wide stage is filled, multiplied and freed in two parts of 256 columns,
+  // each with barriers of its own, so that a part's copies start while the
+  // other is multiplied; the issuer still goes round once per 512.
+  static constexpr int PARTS = CTAS == 2 ? 2 : 1;
   static constexpr int BLKS = BK / kMx4BlkCols;          // weight blocks per stage
+  static constexpr int PBLKS = BLKS / PARTS;             // and per part
   static constexpr int A_BYTES = BLKS * kMx4BlkBytes;
   // Narrow: warps that fill the token scales, a stage each in turn.  No more
   // than stages: a warp that has filled stage i waits next for the release of
@@ -90,16 +95,15 @@ struct Ring {
   static_assert(SF_BASE + SF_SLOTS * SF_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(STAGE_BYTES % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle alignment");
   struct Tail {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
-    uint64_t sfull[2][STAGES];  // wide: the scales of the stage's first, second half are in TMEM
-    uint64_t hfree[2];          // wide: the slot's first half has been multiplied
+    uint64_t full[PARTS][STAGES];
+    uint64_t empty[PARTS][STAGES];
+    uint64_t sfull[PARTS][STAGES];  // wide: the part's scales are in TMEM
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    uint32_t info[STAGES];      // what the stage holds (INFO_*)
+    uint32_t info[PARTS][STAGES];  // what the stage holds (INFO_*), for each part's readers
     int m_units;                // weight tiles (pairs of them), and (2^32 - 1) / m_units
     uint32_t m_magic;
     int tile0[MAX_GROUPS + 1];  // first unit of each group
@@ -424,13 +428,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   int32_t* status = a.status ? a.status : &g_mx4_status;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; s++) {
-      mbar_init(smem_u32(&tail->full[s]), CTAS == 2 ? 1 : 2);  // the producer (the leader's), the scale warp
-      mbar_init(smem_u32(&tail->sfull[0][s]), 1);
-      mbar_init(smem_u32(&tail->sfull[1][s]), 1);
-      mbar_init(smem_u32(&tail->empty[s]), 1);
+      for (int h = 0; h < R::PARTS; h++) {
+        mbar_init(smem_u32(&tail->full[h][s]), CTAS == 2 ? 1 : 2);  // the producer (the leader's), the scale warp
+        mbar_init(smem_u32(&tail->sfull[h][s]), 1);
+        mbar_init(smem_u32(&tail->empty[h][s]), 1);
+      }
     }
     for (int b = 0; b < 2; b++) {
-      mbar_init(smem_u32(&tail->hfree[b]), 1);
       mbar_init(smem_u32(&tail->tfull[b]), 1);
       mbar_init(smem_u32(&tail->tempty[b]), CTAS * EPI_WARPS);
     }
@@ -531,49 +535,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const int m_tiles = mx4_tiles(a.M, a.swiglu);
         const int64_t blk0 =  // the weight's blocks of this tile (past an odd edge: the last tile's again)
             ((int64_t)t.group * m_tiles + min(t.mt, m_tiles - 1)) * nk;
-        for (int kb = 0; kb * R::BLKS < nk; kb++) {
-          if (!wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) { ok = false; break; }
-          const uint32_t full = smem_u32(&tail->full[s]);
-          const int blks = min(R::BLKS, nk - R::BLKS * kb);
-          const int boxes = (blks + 1) / 2;  // of 256 columns; past a lone last block: zeros, or not used
-          const uint32_t sa = smem_base + s * R::STAGE_BYTES;
-          const uint32_t sx = sa + R::A_BYTES;
-          if (weights && leader) {
-            const int left = (a.K - kb * R::BK + 63) / 64;
-            tail->info[s] = (uint32_t)t.n_mma | (uint32_t)min(left, R::BK / 64) << 9 | (kb == 0 ? INFO_FIRST : 0u) |
-                            (left <= R::BK / 64 ? INFO_LAST : 0u);
-            mbar_expect_tx(full, CTAS * (blks * kMx4BlkBytes + boxes * R::X_BYTES + (CTAS == 2 ? R::S_BYTES : 0)));
-          }
-          if (CTAS == 2) {
-            const uint32_t full_leader = map_to_rank(full, 0);
-            const int line = (int)(blk0 + R::BLKS * kb) * kBlkLines;
-            if (weights && blks == R::BLKS)
-              tma_pair_load_2d(sa, tmW, 0, line, full_leader);
-            else if (weights)
-              for (int b = 0; b < blks; b++)
-                tma_pair_load_2d(sa + b * kMx4BlkBytes, tmW + 1, 0, line + b * kBlkLines, full_leader);
-            if (tokens) {
-              for (int b = 0; b < boxes; b++)
-                tma_pair_load_2d(sx + b * R::X_BYTES, &a.tmX, (kb * (R::BK / BOX) + b) * (BOX / 2),
-                                 (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
-              // (past the tile's last block: the next tile's images, not used)
-              tma_pair_load_2d(sx + R::B_BYTES, &a.tmS, 0, (t.tile * nk + R::BLKS * kb) * kImgLines,
-                               full_leader);
+        for (int kb = 0; kb * R::BLKS < nk && ok; kb++) {
+#pragma unroll
+          for (int h = 0; h < R::PARTS; h++) {
+            ok = ok && wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, deadline, status);
+            if (!ok) break;
+            const uint32_t full = smem_u32(&tail->full[h][s]);
+            const int b0 = R::BLKS * kb + R::PBLKS * h;            // the part's first block
+            const int blks = max(0, min(R::PBLKS, nk - b0));       // (a part may have none)
+            const uint32_t sa = smem_base + s * R::STAGE_BYTES + h * R::PBLKS * kMx4BlkBytes;
+            const uint32_t sx = smem_base + s * R::STAGE_BYTES + R::A_BYTES + h * R::X_BYTES;
+            if (weights && leader) {
+              const int left = (a.K - kb * R::BK + 63) / 64;
+              tail->info[h][s] = (uint32_t)t.n_mma | (uint32_t)min(left, R::BK / 64) << 9 |
+                                 (kb == 0 ? INFO_FIRST : 0u) | (left <= R::BK / 64 ? INFO_LAST : 0u);
+              mbar_expect_tx(full, blks ? CTAS * (blks * kMx4BlkBytes + R::X_BYTES + (CTAS == 2 ? R::S_BYTES / 2 : 0)) : 0);
             }
-          } else {
-            if (weights)
-              bulk_load(sa, wbase + (blk0 + R::BLKS * kb) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
-            else
-              tma_load_2d(sx, &a.tmX, kb * (BOX / 2), (int)t.row, full);
+            if (CTAS == 2) {
+              const uint32_t full_leader = map_to_rank(full, 0);
+              const int line = (int)(blk0 + b0) * kBlkLines;
+              if (weights && blks)
+                tma_pair_load_2d(sa, tmW + (blks == R::PBLKS ? 0 : 1), 0, line, full_leader);
+              if (tokens && blks) {  // (past a lone block: zeros, and the next tile's images; neither is used)
+                tma_pair_load_2d(sx, &a.tmX, b0 * (kMx4BlkCols / 2), (int)t.row + (leader ? 0 : t.n_mma / 2), full_leader);
+                tma_pair_load_2d(smem_base + s * R::STAGE_BYTES + R::A_BYTES + R::B_BYTES + h * (R::S_BYTES / 2), &a.tmS,
+                                 0, (t.tile * nk + b0) * kImgLines, full_leader);
+              }
+            } else {
+              if (weights)
+                bulk_load(sa, wbase + (blk0 + b0) * kMx4BlkBytes, blks * kMx4BlkBytes, full);
+              else
+                tma_load_2d(sx, &a.tmX, kb * (BOX / 2), (int)t.row, full);
+            }
           }
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
       }
-      if (weights && leader && ok && wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status)) {
-        tail->info[s] = INFO_STOP;
-        mbar_arrive(smem_u32(&tail->full[s]));
-        if (CTAS == 1) mbar_arrive(smem_u32(&tail->full[s]));  // for the scale warp, which has no such stage
-      }
+      if (weights && leader && ok)
+        for (int h = 0; h < R::PARTS; h++) {
+          if (!wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, deadline, status)) break;
+          tail->info[h][s] = INFO_STOP;
+          mbar_arrive(smem_u32(&tail->full[h][s]));
+          if (CTAS == 1) mbar_arrive(smem_u32(&tail->full[h][s]));  // for the scale warp, which has no such stage
+        }
       // a wait gave up: the copies in flight land before the CTA leaves
       if (!ok)
         for (int i = 0; i < 10000; i++) __nanosleep(1000);
@@ -594,9 +598,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       uint32_t word = 0;
       for (;;) {
         if (!ready) {
-          if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
+          if (!warp_wait(smem_u32(&tail->full[0][s]), ph, abort_flag, deadline, status)) break;
           if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[0][s]), ph, abort_flag, deadline, status)) break;
-          word = *(volatile uint32_t*)&tail->info[s];
+          word = *(volatile uint32_t*)&tail->info[0][s];
         }
         const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
         if (info & (INFO_STOP | INFO_FIRST)) {
@@ -606,9 +610,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         tc_fence_after();
         const int s1 = s + 1 == STAGES ? 0 : s + 1;
         const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
-        const uint32_t test = mbar_test_wait(smem_u32(&tail->full[s1]), ph1) &
+        const uint32_t test = mbar_test_wait(smem_u32(&tail->full[0][s1]), ph1) &
                               (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[0][s1]), ph1) : 1u);
-        const uint32_t test_half = CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[1][s]), ph) : 1u;
+        const uint32_t test_half = CTAS == 2 ? mbar_test_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph) &
+                                                   mbar_test_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph)
+                                             : 1u;
         const uint32_t id0 = idesc_mx4<CTAS>((int)(info & 511u), 0), id2 = id0 | idesc_mx4<CTAS>(0, 2);
         const uint32_t d = tm + (uint32_t)(acc * BN);
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
@@ -625,12 +631,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
                         desc(kDescTokens, sb + (kk >> 2) * (R::X_BYTES >> 4) + (kk & 3) * 2), o ? id2 : id0, sf + 4 * c,
                         sf + 4 * R::BLKS + 4 * c * NB, kk > 0 ? 1u : more);
         };
-        // wide: the first half's columns of the slot are free; the second half's scales are there
+        // wide: the first part is done with when these MMAs are; on to the second
         auto half_way = [&]() {
           if (CTAS == 1) return true;
-          commit_local<CTAS>(el, smem_u32(&tail->hfree[slot]));
+          commit<CTAS>(el, smem_u32(&tail->empty[0][s]));
           if (!__all_sync(0xffffffffu, test_half != 0) &&
-              !warp_wait(smem_u32(&tail->sfull[1][s]), ph, abort_flag, deadline, status))
+              (!warp_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph, abort_flag, deadline, status) ||
+               !warp_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph, abort_flag, deadline, status)))
             return false;
           tc_fence_after();
           return true;
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           ready = __all_sync(0xffffffffu, test != 0);
 #pragma unroll
           for (int kk = 0; kk < FULL / 2; kk++) mma(kk);
-          word = *(volatile uint32_t*)&tail->info[s1];  // used when ready only
+          word = *(volatile uint32_t*)&tail->info[0][s1];  // used when ready only
           if (!half_way()) break;
 #pragma unroll
           for (int kk = FULL / 2; kk < FULL; kk++) mma(kk);
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           for (int c = 0; c < R::BLKS; c++)
             if (2 * c < steps) scales(c);
           ready = __all_sync(0xffffffffu, test != 0);
-          word = *(volatile uint32_t*)&tail->info[s1];
+          word = *(volatile uint32_t*)&tail->info[0][s1];
 #pragma unroll
           for (int kk = 0; kk < FULL / 2; kk++)
             if (kk < steps) mma(kk);
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             if (kk < steps) mma(kk);
         }
         if (++slot == R::SF_SLOTS) slot = 0;
-        commit<CTAS>(el, smem_u32(&tail->empty[s]));
+        commit<CTAS>(el, smem_u32(&tail->empty[R::PARTS - 1][s]));
         s = s1;
         ph = ph1;
         if (info & INFO_LAST) {
@@ -682,35 +689,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     if (leader) {
       const uint32_t el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int h = warp == 2 ? 0 : R::PARTS - 1;
       int s = 0, n = 0;
       uint32_t ph = 0;
       for (;; n++) {
-        if (!warp_wait(smem_u32(&tail->full[s]), ph, abort_flag, deadline, status)) break;
-        const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[s], 0);
+        if (!warp_wait(smem_u32(&tail->full[h][s]), ph, abort_flag, deadline, status)) break;
+        const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[h][s], 0);
         if (info & INFO_STOP) {
-          if (lane == 0 && warp == 2) mbar_arrive(smem_u32(&tail->sfull[0][s]));
+          if (lane == 0) mbar_arrive(smem_u32(&tail->sfull[h][s]));
           break;
         }
         tc_fence_after();
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
         const uint32_t ss = sa + ((R::A_BYTES + R::B_BYTES) >> 4);
         const uint32_t sf = tm + (uint32_t)(R::SF_BASE + (n % R::SF_SLOTS) * R::SF_COLS);
-        if (n >= R::SF_SLOTS) {  // this half of the slot's last stage has been multiplied
+        if (n >= R::SF_SLOTS) {  // this part of the slot's last stage has been multiplied
           const int m = n - R::SF_SLOTS;
-          const bool go = warp == 2 ? warp_wait(smem_u32(&tail->hfree[m % R::SF_SLOTS]), (uint32_t)(m / R::SF_SLOTS) & 1u,
-                                                abort_flag, deadline, status)
-                                    : warp_wait(smem_u32(&tail->empty[m % STAGES]), (uint32_t)(m / STAGES) & 1u,
-                                                abort_flag, deadline, status);
-          if (!go) break;
+          if (!warp_wait(smem_u32(&tail->empty[h][m % STAGES]), (uint32_t)(m / STAGES) & 1u, abort_flag, deadline, status))
+            break;
           tc_fence_after();
         }
         const int steps = (int)(info >> 9) & 15;
 #pragma unroll
-        for (int i = 0; i < R::BLKS / 2; i++) {
-          const int c = warp == 2 ? i : R::BLKS / 2 + i;
+        for (int i = 0; i < R::PBLKS; i++) {
+          const int c = h * R::PBLKS + i;
           if (2 * c < steps) issue_scales<CTAS, NB, R::BLKS>(el, c, sa, ss, sf);
         }
-        commit_local<CTAS>(el, smem_u32(&tail->sfull[warp == 2 ? 0 : 1][s]));
+        commit_local<CTAS>(el, smem_u32(&tail->sfull[h][s]));
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     while (w.more()) {
       const int s = it % STAGES;
       const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
-      bool ok = wait_bar(smem_u32(&tail->empty[s]), ph ^ 1, abort_flag, deadline, status);
+      bool ok = wait_bar(smem_u32(&tail->empty[0][s]), ph ^ 1, abort_flag, deadline, status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint8_t* ss = smem + (size_t)s * R::STAGE_BYTES + R::A_BYTES + R::B_BYTES;
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive_leader<CTAS>(smem_u32(&tail->full[s]));
+      if (lane == 0) arrive_leader<CTAS>(smem_u32(&tail->full[0][s]));
       advance(R::SF_WARPS);
       load(v);
       it += R::SF_WARPS;
@@ -1099,7 +1104,7 @@ int64_t mx4_most_image_bytes(int64_t rows, int groups, int K) {
 }
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, image, 1024, 1024, bytes / 1024, 1024,
-                    Ring<kWide, 2>::BLKS, CU_TENSOR_MAP_SWIZZLE_NONE);
+                    Ring<kWide, 2>::PBLKS, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
                               int64_t rows, int groups, int K, uint8_t* image) {
@@ -1111,14 +1116,14 @@ int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ld
   return encode_box(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, out, 2 * (int64_t)cols, 2 * ldo, rows, 128, 32,
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// packed weight: boxes of a stage's blocks, and of one (the pair's copies
+// packed weight: boxes of a part's blocks, and of one (the pair's copies
 // count on the leader's barrier, which only tensor copies can)
 int encode_mx4_weight(CUtensorMap* tm, const void* packed, int64_t bytes) {
   constexpr int line = kMx4BlkBytes / kBlkLines;
   int rc = AFD_OK;
   for (int i = 0; i < 2 && !rc; i++)
     rc = encode_box(tm + i, CU_TENSOR_MAP_DATA_TYPE_UINT64, 8, packed, line, line, bytes / line, line,
-                    (i ? 1 : Ring<kWide, 2>::BLKS) * kBlkLines, CU_TENSOR_MAP_SWIZZLE_NONE);
+                    (i ? 1 : Ring<kWide, 2>::PBLKS) * kBlkLines, CU_TENSOR_MAP_SWIZZLE_NONE);
   return rc;
 }
 
