@@ -41,7 +41,8 @@ struct ChunkPos {
 // load of bf16, two of fp32).  The block's largest magnitude is an integer
 // maximum of the sign-less bits (NaN and infinity sort above every number),
 // the scale is a power of two and the division by it exact: every code is
-// the nearest e2m1 value of the exact quotient.  Bound by memory.
+// the nearest e2m1 value of the exact quotient.  Bound by memory: 13312 rows
+// of 2048 bf16 values, 69 MB, take 11.9 us (5.8 TB/s), one row 1.8 us.
 // ---------------------------------------------------------------------------
 struct QuantArgs {
   const uint8_t* x;
@@ -152,8 +153,9 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize_step(const __grid_con
 // dequantise: every value fits bf16 and fp32 exactly (three significant
 // bits, exponents within both types').  Bound by memory.  A chunk is what
 // 16 output bytes hold, eight bf16 or four fp32 values, so that a warp's
-// stores are one run (fp32 as two stores of eight values wrote half sectors:
-// 45 MB took 14 us).
+// stores are one run.  13312 x 2048 to bf16 take 10.2 us; 7996 x 1408 to
+// fp32, 45 MB, 8.1 us (14 as two stores of eight values, which wrote half
+// sectors).
 // ---------------------------------------------------------------------------
 struct DequantArgs {
   const uint8_t* codes;

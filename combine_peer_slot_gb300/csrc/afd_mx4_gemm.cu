@@ -6,13 +6,13 @@
 //
 // A unit is 128 weight rows per SM x one token tile of one group.  The weight
 // rows are the MMA's M side, the tokens its N side, so a group of few tokens
-// takes a narrow instruction and not a mostly empty 128-row one.  Per stage
-// of 256 columns a CTA takes 17 KB of weight (codes and scales together),
-// the tokens' codes by TMA (128-byte swizzle) and their scales, which
-// several warps gather from the plain rows into the image tcgen05.cp spreads
-// over the lanes (wide: a small kernel beforehand, k_mx4_scale_image): a
-// group's rows start anywhere, so the tiled image could not be laid out
-// before the groups are known.
+// takes a narrow instruction and not a mostly empty 128-row one.  Per 256
+// columns a CTA takes 17 KB of weight (codes and scales together), the
+// tokens' codes by TMA (128-byte swizzle) and their scales as the image that
+// tcgen05.cp spreads over the lanes.  A group's rows start anywhere, so that
+// image cannot be laid out before the groups are known: narrow, five warps
+// gather it from the plain rows per stage; wide, a small kernel writes it
+// beforehand (k_mx4_scale_image), or the SwiGLU product that codes the rows.
 //
 // Two forms.  Narrow (64 tokens, one SM): groups of few tokens, bound by the
 // weights' bytes; the weight's stage is one bulk copy.  Wide (192 tokens, a
@@ -22,9 +22,23 @@
 // stage of 400 tensor cycles, over the 128 bytes a cycle shared memory has;
 // the pair 31 and 28 KB.
 //
+// Measured (weights of 64 experts):
+//   narrow, 1974 rows, 2816 x 2048 with SwiGLU: 36 us, 5.6 TB/s of what it has
+//     to read (83 % of the copy rate); the weights' stream bounds it
+//   wide, 79872 rows, 2816 x 2048 with SwiGLU: 206 us, 4.5 PFLOP/s;
+//     2048 x 1408: 117 us, 3.9 PFLOP/s and 4.1 TB/s (twice the bf16 rate).  Timing
+//     copies of the second: 99 us without its stores, 90 without its loads, 81
+//     without either, 110 without the weights' loads alone.  The SMs draw 12
+//     TB/s from L2 in both; over long rows (K 8192 and more) 15 TB/s and 1166
+//     cycles a 512-column stage, 1000 without loads, of which the eight MMAs
+//     take some 620.  At that rate the board draws 1.37 of its 1.4 kW and the
+//     SMs run at 1.85 GHz.
+//   Not kept: asking L2 for a unit's first reads two units ahead (117 -> 128
+//   us: the prefetches queue before the copies); stores that L2 evicts first
+//   (no change); a third slot of scales in TMEM (2 us at best).
+//
 // Warps: 0 weight copies, 1 MMA, from 2 scales, 3 or 7 token copies, 8-15
-// epilogue.  All waits are
-// bounded.
+// epilogue.  All waits are bounded.
 #include "afd_mx4.cuh"
 
 #include <cudaTypedefs.h>
@@ -967,8 +981,8 @@ constexpr int kWide = 192, kNarrow = 64;
 // tcgen05.cp takes, [token tile][128-column block][1024 bytes] (row r's four
 // bytes at (r / 128) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4), so that a
 // stage's are one copy.  Gathering them inside the product kept six warps
-// and a proxy fence a stage busy: 20 us of a 150 us product.  One CTA per
-// token tile.
+// and a proxy fence a stage busy: 20 us of a 150 us product, where this takes
+// 4.5 us (79872 rows x 1408 columns).  One CTA per token tile.
 // ---------------------------------------------------------------------------
 constexpr int kImgThreads = 256;
 struct ImageArgs {
@@ -1052,7 +1066,10 @@ cudaError_t launch_variant(const LaunchCtx& lc, const Mx4GemmArgs& a, int64_t un
 // Token tile of a product over `rows` rows in `groups` groups: 64 rows when
 // the groups average 48 or fewer (the weights' bytes bound it: a deeper ring
 // of narrower stages), else 192 (two accumulators and the scales fill the
-// 512 TMEM columns).
+// 512 TMEM columns).  Narrow / wide in us, 64 groups of drawn sizes, 2816 x
+// 2048 with SwiGLU: average 31 36 / 41, 48 37 / 42, 56 39 / 43, 64 46 / 43, 80
+// 57 / 44; of skewed sizes (the largest five times the smallest): 48 40 /
+// 42, 56 44 / 42.  At 1248 rows a group 492 / 203.
 int mx4_token_tile(int64_t rows, int groups) { return rows <= 48 * (int64_t)groups ? kNarrow : kWide; }
 
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units) {

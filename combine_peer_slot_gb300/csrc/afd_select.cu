@@ -15,6 +15,12 @@
 // the checks); the other rows, under one in a hundred for logits of unit
 // spread, run choose_exact.  Comparing in fp64 throughout would cost the
 // fp64 pipe's rate, far below fp32's on this GPU, for every score.
+//
+// Measured: 329 rows of 64 experts 2.4 us, the time of a launch; 13312 rows of
+// 256 with sigmoid, bias and 8 groups, top 8: 22 us, where the logits' bytes
+// would take 2.  A row is about 700 integer instructions of a warp (keys,
+// sorting network, nine warp-wide maxima), which bound it, and the last rows
+// that need choose_exact add 5 us of its latency.
 #include "afd_internal.cuh"
 
 namespace {
