@@ -11,7 +11,7 @@
 namespace {
 
 constexpr int kThreads = 256;
-int64_t g_mx4_launches = 0;
+thread_local int64_t g_mx4_launches = 0;  // (calls may come from several threads)
 
 // Both coding kernels walk the matrix in chunks of eight (or four) values, a
 // CTA kChunks * 256 consecutive ones, a thread every 256th of them: a warp's

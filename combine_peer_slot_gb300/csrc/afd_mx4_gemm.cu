@@ -982,9 +982,11 @@ constexpr int kWide = 192, kNarrow = 64;
 // bytes at (r / 128) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4), so that a
 // stage's are one copy.  Gathering them inside the product kept six warps
 // and a proxy fence a stage busy: 20 us of a 150 us product, where this takes
-// 4.5 us (79872 rows x 1408 columns).  One CTA per token tile.
+// 4.5 us (79872 rows x 1408 columns).  A token tile's columns are split over
+// CTAs as long as those all run at once: with one CTA per tile a product of
+// 192 rows x 8192 columns took 23.4 us, with the split 16.9.
 // ---------------------------------------------------------------------------
-constexpr int kImgThreads = 256;
+constexpr int kImgThreads = 256, kImgDeep = 4;
 struct ImageArgs {
   const uint8_t* xs;
   int64_t x_rows;
@@ -1026,24 +1028,32 @@ __global__ void __launch_bounds__(kImgThreads) k_mx4_scale_image(const __grid_co
   if (rows == 0) return;  // past the last tile
   const uint8_t* src = a.xs + tile_row * a.pitch;
   uint8_t* dst = a.image + (int64_t)tile * a.nk * 1024;
-  // a thread: the four rows l + 32 j of one half image, 16 bytes
-  for (int i = threadIdx.x; i < a.nk * 64; i += kImgThreads) {
-    const int l = i & 31, b = (i >> 5) & 1, c = i >> 6;
-    uint32_t q[4];
+  // a thread: the four rows l + 32 j of one half image, 16 bytes; kImgDeep of them at once
+  const int n = a.nk * 64, step = (int)gridDim.y * kImgThreads;
+  for (int i0 = (int)blockIdx.y * kImgThreads + threadIdx.x; i0 < n; i0 += kImgDeep * step) {
+    uint32_t q[kImgDeep][4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int r = b * 128 + j * 32 + l;
-      q[j] = 0u;
-      if (r >= rows) continue;
-      const uint8_t* p = src + (int64_t)r * a.pitch + 4 * c;
-      if ((a.pitch & 3) == 0) {
-        q[j] = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-        for (int k = 0; k < 4; k++)
-          if (4 * c + k < a.pitch) q[j] |= (uint32_t)p[k] << (8 * k);
+    for (int u = 0; u < kImgDeep; u++) {
+      const int i = i0 + u * step, l = i & 31, b = (i >> 5) & 1, c = i >> 6;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int r = b * 128 + j * 32 + l;
+        q[u][j] = 0u;
+        if (i >= n || r >= rows) continue;
+        const uint8_t* p = src + (int64_t)r * a.pitch + 4 * c;
+        if ((a.pitch & 3) == 0) {
+          q[u][j] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+          for (int k = 0; k < 4; k++)
+            if (4 * c + k < a.pitch) q[u][j] |= (uint32_t)p[k] << (8 * k);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(dst + c * 1024 + b * 512 + l * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+#pragma unroll
+    for (int u = 0; u < kImgDeep; u++) {
+      const int i = i0 + u * step, l = i & 31, b = (i >> 5) & 1, c = i >> 6;
+      if (i < n) *reinterpret_cast<uint4*>(dst + c * 1024 + b * 512 + l * 16) = make_uint4(q[u][0], q[u][1], q[u][2], q[u][3]);
+    }
   }
 }
 
@@ -1126,7 +1136,10 @@ int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
                               int64_t rows, int groups, int K, uint8_t* image) {
   const ImageArgs a{scales, x_rows, offsets, groups, K / 32, mx4_kblocks(K), image};
-  return launch_k(lc, k_mx4_scale_image, (unsigned)mx4_image_tiles(rows, groups), kImgThreads, 0, a);
+  // a tile's columns over several CTAs while those all run at once
+  const int64_t tiles = mx4_image_tiles(rows, groups), most = ((int64_t)a.nk * 64 + kImgThreads - 1) / kImgThreads;
+  const int64_t split = std::min(most, std::max<int64_t>(1, 8 * (int64_t)lc.num_sms / std::max<int64_t>(1, tiles)));
+  return launch_k(lc, k_mx4_scale_image, dim3((unsigned)tiles, (unsigned)split), kImgThreads, 0, a);
 }
 // bf16 output rows: boxes of 64 columns x 32 rows
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo) {

@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid
   }
 }
 
-int64_t g_select_launches = 0;
+thread_local int64_t g_select_launches = 0;  // (calls may come from several threads)
 
 template <typename LT, int PER>
 cudaError_t launch_per(const LaunchCtx& lc, SelArgs a) {
