@@ -604,6 +604,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       // Each stage's barrier is tested, and its word read, while the stage
       // before it is being issued: the two round trips to shared memory would
       // otherwise stand between the stages (about 330 of 860 cycles a stage).
+      // Wide, the tests come behind a stage's MMAs, which run for longer than
+      // the tests take (before them: 2 us more of 119).
       int s = 0;
       uint32_t ph = 0;
       int acc = 0, slot = 0;
@@ -624,11 +626,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         tc_fence_after();
         const int s1 = s + 1 == STAGES ? 0 : s + 1;
         const uint32_t ph1 = s + 1 == STAGES ? ph ^ 1 : ph;
-        const uint32_t test = mbar_test_wait(smem_u32(&tail->full[0][s1]), ph1) &
-                              (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[0][s1]), ph1) : 1u);
-        const uint32_t test_half = CTAS == 2 ? mbar_test_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph) &
-                                                   mbar_test_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph)
-                                             : 1u;
+        // the next stage's barriers, tested narrow before this one is issued, wide after
+        auto look = [&]() {
+          return mbar_test_wait(smem_u32(&tail->full[0][s1]), ph1) &
+                 (CTAS == 2 ? mbar_test_wait(smem_u32(&tail->sfull[0][s1]), ph1) : 1u);
+        };
+        uint32_t test = 0;
+        if (CTAS == 1) test = look();
+        auto next_word = [&]() { word = *(volatile uint32_t*)&tail->info[0][s1]; };  // used when ready only
         const uint32_t id0 = idesc_mx4<CTAS>((int)(info & 511u), 0), id2 = id0 | idesc_mx4<CTAS>(0, 2);
         const uint32_t d = tm + (uint32_t)(acc * BN);
         const uint32_t sa = (smem_base + s * R::STAGE_BYTES) >> 4;
@@ -649,6 +654,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         auto half_way = [&]() {
           if (CTAS == 1) return true;
           commit<CTAS>(el, smem_u32(&tail->empty[0][s]));
+          const uint32_t test_half = mbar_test_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph) &
+                                     mbar_test_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph);
           if (!__all_sync(0xffffffffu, test_half != 0) &&
               (!warp_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph, abort_flag, deadline, status) ||
                !warp_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph, abort_flag, deadline, status)))
@@ -660,10 +667,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         if (steps == FULL) {  // few branches between the instructions of a whole stage
 #pragma unroll
           for (int c = 0; c < R::BLKS; c++) scales(c);
-          ready = __all_sync(0xffffffffu, test != 0);
+          if (CTAS == 1) ready = __all_sync(0xffffffffu, test != 0);
 #pragma unroll
           for (int kk = 0; kk < FULL / 2; kk++) mma(kk);
-          word = *(volatile uint32_t*)&tail->info[0][s1];  // used when ready only
+          if (CTAS == 1) next_word();
           if (!half_way()) break;
 #pragma unroll
           for (int kk = FULL / 2; kk < FULL; kk++) mma(kk);
@@ -671,8 +678,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
 #pragma unroll
           for (int c = 0; c < R::BLKS; c++)
             if (2 * c < steps) scales(c);
-          ready = __all_sync(0xffffffffu, test != 0);
-          word = *(volatile uint32_t*)&tail->info[0][s1];
+          if (CTAS == 1) {
+            ready = __all_sync(0xffffffffu, test != 0);
+            next_word();
+          }
 #pragma unroll
           for (int kk = 0; kk < FULL / 2; kk++)
             if (kk < steps) mma(kk);
@@ -683,6 +692,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         }
         if (++slot == R::SF_SLOTS) slot = 0;
         commit<CTAS>(el, smem_u32(&tail->empty[R::PARTS - 1][s]));
+        if (CTAS == 2) {
+          ready = __all_sync(0xffffffffu, look() != 0);
+          next_word();
+        }
         s = s1;
         ph = ph1;
         if (info & INFO_LAST) {
