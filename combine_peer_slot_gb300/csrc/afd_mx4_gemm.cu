@@ -25,17 +25,19 @@
 // Measured (weights of 64 experts):
 //   narrow, 1974 rows, 2816 x 2048 with SwiGLU: 36 us, 5.6 TB/s of what it has
 //     to read (83 % of the copy rate); the weights' stream bounds it
-//   wide, 79872 rows, 2816 x 2048 with SwiGLU: 206 us, 4.5 PFLOP/s;
-//     2048 x 1408: 117 us, 3.9 PFLOP/s and 4.1 TB/s (twice the bf16 rate).  Timing
-//     copies of the second: 99 us without its stores, 90 without its loads, 81
-//     without either, 110 without the weights' loads alone.  The SMs draw 12
-//     TB/s from L2 in both; over long rows (K 8192 and more) 15 TB/s and 1166
-//     cycles a 512-column stage, 1000 without loads, of which the eight MMAs
-//     take some 620.  At that rate the board draws 1.37 of its 1.4 kW and the
-//     SMs run at 1.85 GHz.
+//   wide, with its scale images, 79872 rows, 2816 x 2048 with SwiGLU: 201 us,
+//     4.6 PFLOP/s; 2048 x 1408: 119 us, 3.9 PFLOP/s and 4.1 TB/s (twice the
+//     bf16 rate).  Timing copies of the second: 103 us without its epilogue, 93
+//     without its loads, 84 without either, 112 without the weights' loads
+//     alone.  The SMs draw 12 TB/s from L2 in both; over long rows (K 8192 and
+//     more) 15 TB/s and 1166 cycles a 512-column stage, 1000 without loads, of
+//     which the eight MMAs take some 620 and their issue as much.  At that rate
+//     the board draws 1.37 of its 1.4 kW and the SMs run at 1.85 GHz.
 //   Not kept: asking L2 for a unit's first reads two units ahead (117 -> 128
 //   us: the prefetches queue before the copies); stores that L2 evicts first
-//   (no change); a third slot of scales in TMEM (2 us at best).
+//   (no change) or plain 16-byte stores (3 us slower); a third slot of scales
+//   in TMEM (2 us at best); the epilogue's next piece read from TMEM while one
+//   is coded (SwiGLU 8 us slower: more instructions beside the issuer's).
 //
 // Warps: 0 weight copies, 1 MMA, from 2 scales, 3 or 7 token copies, 8-15
 // epilogue.  All waits are bounded.
