@@ -307,7 +307,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, deadline, status));
 }
 
-__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// g / (1 + 2^(-g log2 e)).  Results under 2^-126 flush to zero: 2^x's add
+// nothing to 1, and 1 / y's belong to g under -87, where silu is under
+// 2^-119.  Six instructions a value with the product; the epilogue's share the
+// issue slots with the warp that issues the MMAs.
+__device__ __forceinline__ float silu_f(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r;
+}
 
 // TMEM lanes [l, l + 16) x 32 columns in the fragment layout: register 4 i
 // + 2 h + j holds row lane / 4 + 8 h, column 8 i + 2 (lane % 4) + j
@@ -901,7 +910,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
             const uint32_t hw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 8; i++) m = max(m, max((hw[i] << 16) & 0x7fffffffu, hw[i] & 0x7fff0000u));
+            for (int i = 0; i < 8; i++) m = __vmaxu2(m, hw[i] & 0x7fff7fffu);
+            m = max(m << 16, m & 0x7fff0000u);
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             const uint32_t sc = mx4_scale_byte(m, 0);
             const float inv = mx4_inv_scale(sc);
