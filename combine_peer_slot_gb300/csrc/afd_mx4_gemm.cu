@@ -25,8 +25,8 @@
 // Measured (weights of 64 experts):
 //   narrow, 1974 rows, 2816 x 2048 with SwiGLU: 36 us, 5.6 TB/s of what it has
 //     to read (83 % of the copy rate); the weights' stream bounds it
-//   wide, with its scale images, 79872 rows, 2816 x 2048 with SwiGLU: 201 us,
-//     4.6 PFLOP/s; 2048 x 1408: 119 us, 3.9 PFLOP/s and 4.1 TB/s (twice the
+//   wide, with its scale images, 79872 rows, 2816 x 2048 with SwiGLU: 194 us,
+//     4.7 PFLOP/s; 2048 x 1408: 119 us, 3.9 PFLOP/s and 4.1 TB/s (twice the
 //     bf16 rate).  Timing copies of the second: 103 us without its epilogue, 93
 //     without its loads, 84 without either, 112 without the weights' loads
 //     alone.  The SMs draw 12 TB/s from L2 in both; over long rows (K 8192 and
@@ -1104,7 +1104,7 @@ cudaError_t launch_variant(const LaunchCtx& lc, const Mx4GemmArgs& a, int64_t un
 // 512 TMEM columns).  Narrow / wide in us, 64 groups of drawn sizes, 2816 x
 // 2048 with SwiGLU: average 31 36 / 41, 48 37 / 42, 56 39 / 43, 64 46 / 43, 80
 // 57 / 44; of skewed sizes (the largest five times the smallest): 48 40 /
-// 42, 56 44 / 42.  At 1248 rows a group 492 / 203.
+// 42, 56 44 / 42.  At 1248 rows a group 490 / 194.
 int mx4_token_tile(int64_t rows, int groups) { return rows <= 48 * (int64_t)groups ? kNarrow : kWide; }
 
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units) {

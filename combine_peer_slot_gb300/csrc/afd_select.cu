@@ -18,9 +18,11 @@
 //
 // Measured: 329 rows of 64 experts 2.4 us, the time of a launch; 13312 rows of
 // 256 with sigmoid, bias and 8 groups, top 8: 22 us, where the logits' bytes
-// would take 2.  A row is about 700 integer instructions of a warp (keys,
-// sorting network, nine warp-wide maxima), which bound it, and the last rows
-// that need choose_exact add 5 us of its latency.
+// would take 2; without groups 18, without bias either 11.  A row is some 1200
+// instructions of a warp (scores, keys, sorting network, group ranks, nine
+// warp-wide maxima), most of them on the half-rate integer pipe, which bounds
+// it; the few rows that need choose_exact add 3 us of its latency at the end,
+// or up to 10 where one has its groups to rank as well.
 #include "afd_internal.cuh"
 
 namespace {
@@ -135,6 +137,20 @@ __device__ __forceinline__ void merge_two(float& m1, float& m2, int o) {
   m1 = fmaxf(m1, o1);
 }
 
+// Scores that rank.  exp(x) = 2^(x log2 e); both instructions flush results
+// under 2^-126 to zero, which the error bounds below, relative to the row's
+// largest score, take in.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp_fast(-x)));
+  return y;
+}
+
 // Contenders of one row: experts whose place fp32 cannot settle, with their
 // exact values.
 struct Contenders {
@@ -144,7 +160,8 @@ struct Contenders {
 
 // What two fp32 values of c may be off together, u = 2^-24: kScoreErr times
 // the largest score (1 for a sigmoid, 1 / z for a softmax) and 2 u |c| for
-// adding the bias.  __expf(x) is off by 2 + 1.173 |x| ulp, __fdividef by 2.
+// adding the bias.  exp_fast(x) is off by 2^-22 (4 u) and, from its argument's
+// two roundings, by 2 u |x|; the reciprocal by 2 u.  Taken a little larger:
 //   sigmoid: s (1 - s) times the exponential's (4 + 2.35 |l|) u, at most
 //   1.6 u, the sum 1 + e and the division 5 u: 6.6 u, twice 13.2 u
 //   softmax: the exponential's (4 + 3.35 d) u, d = top - l with its rounding,
@@ -231,7 +248,7 @@ __device__ __noinline__ void choose_exact(const SelArgs& a, int64_t row, int lan
     s[i] = 0.0f;
     c[i] = l[i];
     if (l[i] > -INFINITY) {
-      if (by_score) s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top) * smax;
+      if (by_score) s[i] = a.sigmoid ? sigmoid_fast(l[i]) : exp_fast(l[i] - top) * smax;
       if (scored) c[i] = s[i] + a.bias[e0 + i];
       if (c[i] > -INFINITY) {
         all |= 1u << i;
@@ -398,7 +415,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-      s[i] = l[i] == -INFINITY ? 0.0f : __expf(l[i] - top);
+      s[i] = l[i] == -INFINITY ? 0.0f : exp_fast(l[i] - top);
       z += s[i];
     }
 #pragma unroll
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid
     }
   } else if (by_score) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) s[i] = l[i] == -INFINITY ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+    for (int i = 0; i < PER; i++) s[i] = sigmoid_fast(l[i]);  // (-inf: 0)
   }
   uint64_t key[PER];  // high word: what is compared, 0 = not to be chosen
 #pragma unroll
