@@ -375,3 +375,41 @@ def test_repeats_give_the_same_bits():
     first = R.mx4_gemm(x, off, w)
     for _ in range(5):
         assert torch.equal(R.mx4_gemm(x, off, w), first)
+
+
+@pytest.mark.parametrize("K", [32, 128, 160, 256, 288, 384, 416, 512, 544, 768, 800, 1024, 1056])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_wide_rows_that_end_in_every_part_of_a_stage(K, swiglu):
+    """Groups large enough for the wide form; the row's end in the first or
+    the second half of a 512-column stage, or none of it in the second."""
+    check_product([150, 230, 0, 90], 272, K, torch.bfloat16, swiglu=swiglu, seed=K)
+
+
+@pytest.mark.parametrize("counts,K", [([100], 8192), ([70, 193], 4128), ([300, 5, 1000], 2080)])
+def test_wide_few_tiles_of_long_rows(counts, K):
+    """A token tile's scale image by several CTAs, in uneven shares."""
+    check_product(counts, 128, K, torch.float32, seed=K)
+
+
+def test_swiglu_at_the_ends_of_the_exponential():
+    """Gates whose exponential overflows, vanishes or is nearly 1, up = 1: the
+    exponential is off by (4 + 2 |g|) 2^-24, its sum and reciprocal by 3, and
+    results of the reciprocal under 2^-126 are zero; then one rounding to bf16."""
+    values = [s * m * 2.0 ** e for s in (1, -1) for m in (1.0, 1.5) for e in range(-20, 8)]
+    I, K = len(values), 32
+    assert I % 8 == 0
+    w = torch.zeros(2 * I, K, device="cuda")
+    w[:I, 0] = torch.tensor(values, device="cuda")
+    w[I:, 0] = 1.0
+    wq = R.mx4_quantize(w)
+    weight = R.Mx4Weight(wq.codes.view(1, 2 * I, -1), wq.scales.view(1, 2 * I, -1), swiglu=True)
+    for rows in (3, 100):
+        x = torch.zeros(rows, K, device="cuda")
+        x[:, 0] = 1.0
+        off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        out = R.mx4_gemm(R.mx4_quantize(x), off, weight).double()
+        g = torch.tensor(values, device="cuda", dtype=torch.float64)
+        want = g / (1 + torch.exp(-g))
+        bound = (2.0 ** -8 + (12 + 2 * g.abs()) * 2.0 ** -24) * want.abs() + (g.abs() + 1) * 2.0 ** -126
+        assert not torch.isnan(out).any()
+        assert ((out - want).abs() <= bound).all()
