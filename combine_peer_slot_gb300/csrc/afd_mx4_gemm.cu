@@ -927,19 +927,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
               code[i] = sc == 255u ? 0u : mx4_encode8(v);
             }
             if (r < nrows && f < I) {
-              const int64_t at = (row0 + c0 + r) * ldo + f;
-              *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out) + at / 2) =
+              const uint64_t at = (uint64_t)(row0 + c0 + r) * (uint32_t)ldo + (uint32_t)f;
+              *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out) + (at >> 1)) =
                   make_uint2(code[0], code[1]);
-              if (CTAS == 1 && (gt & 1) == 0) a.out_lo[at / 32] = (uint8_t)sc;
+              if (CTAS == 1 && (gt & 1) == 0) a.out_lo[at >> 5] = (uint8_t)sc;
             }
             if (CTAS == 2 && (gt & 1) == 0 && r < nrows && t.tile < a.tiles) {
               // into the next product's scale images; zeros past inter's
               // end, so that no stray scale meets the zero columns there
-              const int blk = f / 32, nk2 = mx4_kblocks(I), rt = c0 + r;
-              uint8_t* img = a.out_lo + (int64_t)t.tile * nk2 * (NB * 512) + (rt >> 7) * 512 +
-                             (rt & 31) * 16 + ((rt >> 5) & 3) * 4;
+              const int blk = f >> 5, nk2 = mx4_kblocks(I), rt = c0 + r;
+              uint8_t* img = a.out_lo + (uint64_t)(uint32_t)(t.tile * nk2) * (NB * 512) +
+                             (uint32_t)((rt >> 7) * 512 + (rt & 31) * 16 + ((rt >> 5) & 3) * 4);
               auto put = [&](int b, uint32_t v) {
-                if (b < nk2 * 4) img[(b >> 2) * (NB * 512) + (b & 3)] = (uint8_t)v;
+                if (b < nk2 * 4) img[(uint32_t)((b >> 2) * (NB * 512) + (b & 3))] = (uint8_t)v;
               };
               put(blk, f < I ? sc : 0u);
               if (t.mt == mx4_tiles(a.M, 1) - 1) put(blk + 2, 0u);
