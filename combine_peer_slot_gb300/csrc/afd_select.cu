@@ -563,14 +563,40 @@ __global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid
     my_s = a.sigmoid ? 1.0f / (1.0f + expf(-my_l)) : expf(my_l - top) / z;
   }
   if (scored) {
+    auto clear = [&](float v0, float v1) {
+      return v0 - v1 > score_err(a.sigmoid) * smax + 2.0f * kU * fmaxf(fabsf(v0), fabsf(v1));
+    };
     const uint32_t nk = __shfl_down_sync(0xffffffffu, my_key, 1);
     const float nl = __shfl_down_sync(0xffffffffu, my_l, 1);
     const int ni = __shfl_down_sync(0xffffffffu, my_id, 1);
-    if (lane < a.k && my_key != 0u && nk != 0u) {
-      const float v0 = unordered(my_key), v1 = unordered(nk);
-      if (!(v0 - v1 > score_err(a.sigmoid) * smax + 2.0f * kU * fmaxf(fabsf(v0), fabsf(v1))))
-        // equal logit and bias: equal values, rightly decided by index
-        close |= !(my_l == nl && a.bias[my_id] == a.bias[ni]);
+    bool twins = false;  // the last choice and the first one left out have equal logit and bias
+    if (lane < a.k && my_key != 0u && nk != 0u && !clear(unordered(my_key), unordered(nk))) {
+      // equal logit and bias: equal values, rightly decided by index
+      const bool equal = my_l == nl && a.bias[my_id] == a.bias[ni];
+      close |= !equal;
+      twins = equal && lane == a.k - 1;
+    }
+    // The index decides between the two, but a third that fp32 cannot tell from
+    // them may be larger than both: on down the order to a value clear of theirs.
+    if (__any_sync(0xffffffffu, twins)) {
+      const float kv = unordered(__shfl_sync(0xffffffffu, my_key, a.k - 1));
+      const float kl = __shfl_sync(0xffffffffu, my_l, a.k - 1);
+      const float kb = a.bias[__shfl_sync(0xffffffffu, my_id, a.k - 1)];
+      for (;;) {
+        const uint32_t v = __reduce_max_sync(0xffffffffu, head);
+        if (v == 0u || clear(kv, unordered(v))) break;
+        const int owner = __ffs((int)__ballot_sync(0xffffffffu, head == v)) - 1;
+        const int id = __shfl_sync(0xffffffffu, e0 + (int)(slots & 15u), owner);
+        if (load_logit<LT>(a.logits, row * a.ld + id) != kl || a.bias[id] != kb) {
+          close = true;
+          break;
+        }
+        if (lane == owner) {
+          at += 32;
+          head = heads[at];
+          slots >>= 4;
+        }
+      }
     }
   }
   float sum = lane < a.k ? my_s : 0.0f;
