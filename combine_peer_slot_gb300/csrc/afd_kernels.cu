@@ -1452,8 +1452,10 @@ k_router_fused(const uint8_t* win, WinGeom g, const __grid_constant__ FanIn fp, 
     for (int s = 0; s < kFrSlots; s++) mbar_expect_tx(full_bar(s), block_bytes);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     const uint32_t wbytes = (uint32_t)(((ne + 3) / 4) * hidden * 16);
-    mbar_expect_tx(wbar, wbytes);
-    bulk_load(smem_u32(fr_smem), WgQ + (int64_t)e_base * hidden, wbytes, wbar);
+    if (WgQ) {  // (none: a failed item whose layer was never set, which the skip below leaves out)
+      mbar_expect_tx(wbar, wbytes);
+      bulk_load(smem_u32(fr_smem), WgQ + (int64_t)e_base * hidden, wbytes, wbar);
+    }
   }
   for (int i = tid; i < kFrSlots * ep; i += blockDim.x) hs[i] = 0;
   __syncthreads();
@@ -1475,7 +1477,7 @@ k_router_fused(const uint8_t* win, WinGeom g, const __grid_constant__ FanIn fp, 
         __nanosleep(64);
       }
     }
-    skip_s = !ok || read_status(ws.status);
+    skip_s = !ok || !WgQ || read_status(ws.status);
   }
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every peer has started
@@ -1488,7 +1490,7 @@ k_router_fused(const uint8_t* win, WinGeom g, const __grid_constant__ FanIn fp, 
   int skip = 0;
   for (int q = 0; q < C; q++) skip |= skipv[q];
   if (skip) {  // the whole cluster leaves; nothing was exchanged
-    if (tid == 0) {  // the weight copy lands in this CTA's shared memory: wait (bounded)
+    if (tid == 0 && WgQ) {  // the weight copy lands in this CTA's shared memory: wait (bounded)
       const uint64_t dl = globaltimer_ns() + 100000000ull;
       while (!mbar_try_wait(wbar, 0) && globaltimer_ns() < dl) {}
     }
