@@ -964,7 +964,7 @@ static int experts_mx4(afd_ctx* ctx, const LayerW* L, int64_t N, int64_t S, bool
     return AFD_OK;
   }
   int rc = cuda_fail(launch_mx4_quantize_step(lc, ws.xp, c.hidden, L ? nullptr : ws.item, c.topk, (int)N, (int)S,
-                                              ctx->m4.codes, ctx->m4.scales, ctx->m4.offs),
+                                              ctx->m4.codes, ctx->m4.scales, ctx->m4.offs, ws.status),
                      "mx4 rows");
   if (rc) return rc;
   // one product; wsel: 0 W13, 1 Wd, 2 W13_s, 3 Wd_s

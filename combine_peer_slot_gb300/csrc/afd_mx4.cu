@@ -131,10 +131,12 @@ struct StepArgs {
   const FanIn* item;  // NULL: the counts are n and s
   int topk, has_shared, n, s;
   int32_t* offs;
+  const int32_t* status;
 };
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize_step(const __grid_constant__ StepArgs a) {
   grid_dep_wait();
   grid_dep_launch();
+  if (read_status(a.status)) return;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     int N = a.n, S = a.s;
     if (a.item) {
@@ -297,11 +299,12 @@ cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx,
 }
 
 cudaError_t launch_mx4_quantize_step(const LaunchCtx& lc, const void* xp, int cols, const FanIn* item,
-                                     int topk, int n, int s, uint8_t* codes, uint8_t* scales, int32_t* offs) {
+                                     int topk, int n, int s, uint8_t* codes, uint8_t* scales, int32_t* offs,
+                                     const int32_t* status) {
   const int64_t rows = (int64_t)n + s;
   const StepArgs a{{static_cast<const uint8_t*>(xp), (int64_t)cols * 2, rows, nullptr, 1, rows, cols / 8,
                     0xffffffffu / (uint32_t)(cols / 8), 0, reinterpret_cast<uint32_t*>(codes), scales},
-                   item, topk, s > 0, n, s, offs};
+                   item, topk, s > 0, n, s, offs, status};
   const int64_t grid = std::max<int64_t>(1, chunk_grid(rows * (cols / 8)));
   if (grid >= (int64_t)1 << 31) return cudaErrorInvalidValue;
   return launch_k(lc, k_mx4_quantize_step, (unsigned)grid, kThreads, 0, a);
@@ -326,7 +329,7 @@ int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8
   if (!rc && img) rc = encode_mx4_images(&a.tmS, image, img);
   if (rc) return rc;
   if (img && scales) {
-    rc = launched(launch_mx4_images(lc, scales, x_rows, offsets, rows, groups, K, image), "mx4 scale images");
+    rc = launched(launch_mx4_images(lc, scales, x_rows, offsets, rows, groups, K, image, a.status), "mx4 scale images");
     if (rc) return rc;
     lc.pdl = 1;  // the product's set-up runs while the images are written
   }

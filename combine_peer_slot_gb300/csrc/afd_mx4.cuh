@@ -55,7 +55,7 @@ struct Mx4GemmArgs {
   const int32_t* offsets;    // [n_groups + 1], device
   int n_groups;
   int swiglu;
-  int32_t* status;           // NULL: the file-scope status word
+  int32_t* status;           // the step's: no work once it is set; NULL: the file-scope word, set only
   // layer chosen on the device: the weight is layers[item->layer].mx4[wsel], not tmW and w
   const DevLayer* layers;
   const FanIn* item;
@@ -75,7 +75,7 @@ int64_t mx4_most_image_bytes(int64_t rows, int groups, int K);  // over all row 
 int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes);
 // x_rows: rows the scales hold; rows: the most the groups hold together
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
-                              int64_t rows, int groups, int K, uint8_t* image);
+                              int64_t rows, int groups, int K, uint8_t* image, const int32_t* status);
 int encode_mx4_out(CUtensorMap* m, void* out, int64_t rows, int cols, int64_t ldo);
 int encode_mx4_weight(CUtensorMap* tm /* [2]: a part's blocks, one block */, const void* packed, int64_t bytes);
 
@@ -86,7 +86,8 @@ cudaError_t launch_mx4_quantize(const LaunchCtx& lc, const void* x, int64_t ldx,
 // counts, n and s the most there can be) coded position by position, and
 // offs = {n, n + s, 0, s} for the shared rows' products
 cudaError_t launch_mx4_quantize_step(const LaunchCtx& lc, const void* xp, int cols, const FanIn* item, int topk, int n,
-                                     int s, uint8_t* codes, uint8_t* scales, int32_t* offs);
+                                     int s, uint8_t* codes, uint8_t* scales, int32_t* offs,
+                                     const int32_t* status);
 // One product of the step or of a call.  image: the rows' scale images (wide
 // form; written from scales unless that is NULL), rows: the most rows the
 // groups hold together, x_rows: the rows that codes and scales hold.

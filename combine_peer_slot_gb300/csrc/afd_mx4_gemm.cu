@@ -119,6 +119,7 @@ struct Ring {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int skip;                   // an earlier kernel of the step has failed
     uint32_t info[PARTS][STAGES];  // what the stage holds (INFO_*), for each part's readers
     int m_units;                // weight tiles (pairs of them), and (2^32 - 1) / m_units
     uint32_t m_magic;
@@ -252,6 +253,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -494,6 +500,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     grid_dep_wait();
     grid_dep_launch();
   }
+  if (threadIdx.x == 0) tail->skip = a.status ? read_status(a.status) : 0;
   // the groups: rows clamped to those there are, units counted
   const int ngroups = a.n_groups;
   int mine = 0, tiles = 0;
@@ -542,11 +549,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   __syncthreads();
   if (CTAS == 2) cluster_sync();  // both CTAs' barriers and TMEM columns are in place
   tc_fence_after();
+  // A step that has failed has no rows, and perhaps no layer: no units.  The
+  // pair decides together (each CTA's smem stays until the last cluster barrier).
+  if (tail->skip || (CTAS == 2 && a.status && ld_cluster(map_to_rank(smem_u32(&tail->skip), cluster_rank() ^ 1u)))) total = 0;
   const uint32_t tmem = tail->tmem_base;
   const uint64_t deadline = globaltimer_ns() + kTimeoutNs;
   volatile int* abort_flag = &tail->abort_flag;
   // the weight: the launch's own, or that of the layer the device chose for this step
-  const DevMx4Weight* lw = a.layers ? &a.layers[a.item->layer].mx4[a.wsel] : nullptr;
+  const DevMx4Weight* lw = a.layers && total > 0 ? &a.layers[a.item->layer].mx4[a.wsel] : nullptr;
   const CUtensorMap* tmW = lw ? lw->tm : a.tmW;
   const uint8_t* wbase = lw ? lw->packed : a.w;
   const uint32_t smem_base = smem_u32(smem);
@@ -1025,16 +1035,18 @@ struct ImageArgs {
   const int32_t* offsets;
   int n_groups, pitch, nk;
   uint8_t* image;
+  const int32_t* status;  // of the step, or NULL
 };
 __global__ void __launch_bounds__(kImgThreads) k_mx4_scale_image(const __grid_constant__ ImageArgs a) {
   __shared__ int wsum[kImgThreads / 32];
   __shared__ int64_t tile_row;
-  __shared__ int tile_rows;
+  __shared__ int tile_rows, skip;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile = (int)blockIdx.x;
   if (threadIdx.x == 0) tile_rows = 0;
   grid_dep_wait();
   grid_dep_launch();
+  if (threadIdx.x == 0) skip = a.status ? read_status(a.status) : 0;
   int64_t lo = 0, hi = 0;
   if ((int)threadIdx.x < a.n_groups) {
     lo = min(max((int64_t)a.offsets[threadIdx.x], (int64_t)0), a.x_rows);
@@ -1049,6 +1061,7 @@ __global__ void __launch_bounds__(kImgThreads) k_mx4_scale_image(const __grid_co
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
+  if (skip) return;
   for (int w = 0; w < warp; w++) incl += wsum[w];
   if (tile < incl && tile >= incl - tiles) {
     const int nt = tile - (incl - tiles);
@@ -1166,8 +1179,8 @@ int encode_mx4_images(CUtensorMap* m, const void* image, int64_t bytes) {
                     Ring<kWide, 2>::PBLKS, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 cudaError_t launch_mx4_images(const LaunchCtx& lc, const uint8_t* scales, int64_t x_rows, const int32_t* offsets,
-                              int64_t rows, int groups, int K, uint8_t* image) {
-  const ImageArgs a{scales, x_rows, offsets, groups, K / 32, mx4_kblocks(K), image};
+                              int64_t rows, int groups, int K, uint8_t* image, const int32_t* status) {
+  const ImageArgs a{scales, x_rows, offsets, groups, K / 32, mx4_kblocks(K), image, status};
   // a tile's columns over several CTAs while those all run at once
   const int64_t tiles = mx4_image_tiles(rows, groups), most = ((int64_t)a.nk * 64 + kImgThreads - 1) / kImgThreads;
   const int64_t split = std::min(most, std::max<int64_t>(1, 8 * (int64_t)lc.num_sms / std::max<int64_t>(1, tiles)));
