@@ -986,6 +986,8 @@ static int experts_mx4(afd_ctx* ctx, const LayerW* L, int64_t N, int64_t S, bool
     a.out_shift = shift;
     a.fmt = fmt;
     a.status = ws.status;
+    a.out_rows = (wsel < 2 ? (int64_t)c.topk : 1) * ctx->tmax;
+    a.dbg = ws.dbg;
     // the down products: the kernel before wrote their rows at most, never the offsets or the layer table
     a.early = lc.pdl && (wsel & 1);
     LaunchCtx one = lc;

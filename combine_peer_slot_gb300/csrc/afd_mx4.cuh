@@ -63,6 +63,8 @@ struct Mx4GemmArgs {
   // the kernel before writes the rows only; launched with lc.pdl
   int early;
   int tiles;                 // token tiles the images hold (more only for offsets that overlap)
+  int64_t out_rows;          // rows the output holds, and the workspace's record, for the
+  int64_t* dbg;              // debug build's check (NULL: not checked)
 };
 // bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
 // output tiles, which sizes the grid

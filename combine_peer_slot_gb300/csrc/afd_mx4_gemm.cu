@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       const int64_t ldo = a.ldo, row0 = t.row - shift;  // first output row
       const int fmt = a.fmt;
       bool released = false;
+      const int nstore = !a.dbg || dbg_in_range(a.dbg, status, AFD_DBG_GEMM_OUT, row0 + t.rows - 1, a.out_rows) ? t.rows : 0;
       // the group's piece is in the buffer: whole ones go out by TMA
       auto stored = [&](bool whole, int boxes, int col, int64_t row) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         if (lane == 0) arrive_leader<CTAS>(smem_u32(&tail->tempty[acc]));
         released = true;
       };
-      for (int c0 = half * 32; c0 < t.rows; c0 += 64) {
+      for (int c0 = half * 32; c0 < nstore; c0 += 64) {
         const bool last = c0 + 64 >= t.rows;
         const int nrows = min(32, t.rows - c0);
         if (!a.swiglu && fmt != OUT_ACT) {  // lane = output row: 32 neighbours per token already
