@@ -64,6 +64,8 @@ constexpr int EPI_BUF_BYTES = 2 * EPI_BOX_BYTES;
 // weight block is 8 of 1088 bytes, a 128-column scale image 1 of 1024
 constexpr int kBlkLines = 8, kImgLines = 1;
 constexpr int MAX_GROUPS = 256;
+// Bound of every wait, from its own start: a product may take longer than this
+// as a whole, none of its waits does.
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // A stage's word for the MMA issuer, written by the copies' producer: bits
@@ -283,13 +285,17 @@ __device__ __forceinline__ void tma_pair_load_2d(uint32_t dst, const CUtensorMap
 
 // (acquire at CTA scope: across the pair the barriers order copies, MMAs and
 // TMEM reads only, never the peer's plain stores)
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
-                                         int32_t* status) {
+// (A function of its own: with the loop in every role's code the expert FFN of a
+// prefill fan-in took 346 us, with the call 337.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   uint32_t spins = 0;
+  uint64_t start = 0;
   while (!mbar_try_wait(bar, parity)) {
     if ((++spins & 255u) == 0) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() > deadline) {
+      const uint64_t now = globaltimer_ns();
+      if (start == 0) start = now;
+      if (now - start > kTimeoutNs) {
         *abort_flag = 1;
         set_error(status, AFD_ERR_TIMEOUT);
         return false;
@@ -297,6 +303,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, status);
 }
 
 __device__ __forceinline__ uint32_t mbar_test_wait(uint32_t bar, uint32_t parity) {
@@ -308,9 +317,8 @@ __device__ __forceinline__ uint32_t mbar_test_wait(uint32_t bar, uint32_t parity
       : "memory");
   return ok;
 }
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline,
-                                          int32_t* status) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, deadline, status));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
 }
 
 // silu(g) * u = g / (1 + e^-g) * u.  The row is coded next, and a code moves by
@@ -495,7 +503,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   }
   // a.early: the rows alone come from the kernel before; the groups and the
   // weight are older, so this CTA's first weight copies go out while that
-  // kernel's last CTAs run, and only the roles that touch the rows wait
+  // kernel's last CTAs run; the roles wait for its end before the first of their
+  // own waits that depends on the rows, whose bound then counts this kernel only
   if (!a.early) {
     grid_dep_wait();
     grid_dep_launch();
@@ -553,7 +562,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   // pair decides together (each CTA's smem stays until the last cluster barrier).
   if (tail->skip || (CTAS == 2 && a.status && ld_cluster(map_to_rank(smem_u32(&tail->skip), cluster_rank() ^ 1u)))) total = 0;
   const uint32_t tmem = tail->tmem_base;
-  const uint64_t deadline = globaltimer_ns() + kTimeoutNs;
   volatile int* abort_flag = &tail->abort_flag;
   // the weight: the launch's own, or that of the layer the device chose for this step
   const DevMx4Weight* lw = a.layers && total > 0 ? &a.layers[a.item->layer].mx4[a.wsel] : nullptr;
@@ -568,7 +576,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       // the weight's need not wait where the rows must)
       const bool weights = warp == 0, tokens = !weights;
       if (tokens && a.early) grid_dep_wait();
-      int s = 0;
+      int s = 0, filled = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (Walk<BN, CTAS> w(a, tail, ngroups, total); w.more() && ok; w.next()) {
@@ -578,9 +586,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const int64_t blk0 =  // the weight's blocks of this tile (past an odd edge: the last tile's again)
             ((int64_t)t.group * m_tiles + min(t.mt, m_tiles - 1)) * nk;
         for (int kb = 0; kb * R::BLKS < nk && ok; kb++) {
+          // the ring is full of weights: what empties it follows the kernel before
+          if (weights && a.early && filled++ == STAGES) grid_dep_wait();
 #pragma unroll
           for (int h = 0; h < R::PARTS; h++) {
-            ok = ok && wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, deadline, status);
+            ok = ok && wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, status);
             if (!ok) break;
             const uint32_t full = smem_u32(&tail->full[h][s]);
             const int b0 = R::BLKS * kb + R::PBLKS * h;            // the part's first block
@@ -613,9 +623,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           if (++s == STAGES) { s = 0; ph ^= 1; }
         }
       }
+      if (weights && a.early) grid_dep_wait();
       if (weights && leader && ok)
         for (int h = 0; h < R::PARTS; h++) {
-          if (!wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, deadline, status)) break;
+          if (!wait_bar(smem_u32(&tail->empty[h][s]), ph ^ 1, abort_flag, status)) break;
           tail->info[h][s] = INFO_STOP;
           mbar_arrive(smem_u32(&tail->full[h][s]));
           if (CTAS == 1) mbar_arrive(smem_u32(&tail->full[h][s]));  // for the scale warp, which has no such stage
@@ -626,6 +637,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer
+    if (a.early) grid_dep_wait();
     if (leader) {
       const uint32_t el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -642,14 +654,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       uint32_t word = 0;
       for (;;) {
         if (!ready) {
-          if (!warp_wait(smem_u32(&tail->full[0][s]), ph, abort_flag, deadline, status)) break;
-          if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[0][s]), ph, abort_flag, deadline, status)) break;
+          if (!warp_wait(smem_u32(&tail->full[0][s]), ph, abort_flag, status)) break;
+          if (CTAS == 2 && !warp_wait(smem_u32(&tail->sfull[0][s]), ph, abort_flag, status)) break;
           word = *(volatile uint32_t*)&tail->info[0][s];
         }
         const uint32_t info = __shfl_sync(0xffffffffu, word, 0);
         if (info & (INFO_STOP | INFO_FIRST)) {
           if (info & INFO_STOP) break;
-          if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, deadline, status)) break;
+          if (!warp_wait(smem_u32(&tail->tempty[acc]), acc_ph ^ 1, abort_flag, status)) break;
         }
         tc_fence_after();
         const int s1 = s + 1 == STAGES ? 0 : s + 1;
@@ -685,8 +697,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           const uint32_t test_half = mbar_test_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph) &
                                      mbar_test_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph);
           if (!__all_sync(0xffffffffu, test_half != 0) &&
-              (!warp_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph, abort_flag, deadline, status) ||
-               !warp_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph, abort_flag, deadline, status)))
+              (!warp_wait(smem_u32(&tail->full[R::PARTS - 1][s]), ph, abort_flag, status) ||
+               !warp_wait(smem_u32(&tail->sfull[R::PARTS - 1][s]), ph, abort_flag, status)))
             return false;
           tc_fence_after();
           return true;
@@ -741,6 +753,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     // ------------------------------ wide: scales into TMEM
     // Warps of their own issue them, half of a stage's each: six copies and four MMAs a stage from
     // one warp took longer to issue than the MMAs take to run.
+    if (a.early) grid_dep_wait();
     if (leader) {
       const uint32_t el = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
       int s = 0, n = 0;
       uint32_t ph = 0;
       for (;; n++) {
-        if (!warp_wait(smem_u32(&tail->full[h][s]), ph, abort_flag, deadline, status)) break;
+        if (!warp_wait(smem_u32(&tail->full[h][s]), ph, abort_flag, status)) break;
         const uint32_t info = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tail->info[h][s], 0);
         if (info & INFO_STOP) {
           if (lane == 0) mbar_arrive(smem_u32(&tail->sfull[h][s]));
@@ -760,7 +773,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
         const uint32_t sf = tm + (uint32_t)(R::SF_BASE + (n % R::SF_SLOTS) * R::SF_COLS);
         if (n >= R::SF_SLOTS) {  // this part of the slot's last stage has been multiplied
           const int m = n - R::SF_SLOTS;
-          if (!warp_wait(smem_u32(&tail->empty[h][m % STAGES]), (uint32_t)(m / STAGES) & 1u, abort_flag, deadline, status))
+          if (!warp_wait(smem_u32(&tail->empty[h][m % STAGES]), (uint32_t)(m / STAGES) & 1u, abort_flag, status))
             break;
           tc_fence_after();
         }
@@ -800,7 +813,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     while (w.more()) {
       const int s = it % STAGES;
       const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
-      bool ok = wait_bar(smem_u32(&tail->empty[0][s]), ph ^ 1, abort_flag, deadline, status);
+      bool ok = wait_bar(smem_u32(&tail->empty[0][s]), ph ^ 1, abort_flag, status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       uint8_t* ss = smem + (size_t)s * R::STAGE_BYTES + R::A_BYTES + R::B_BYTES;
@@ -832,6 +845,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     // one barrier a piece: it says that this buffer is full and the other
     // one has been read.  Plain stores throughout made the epilogue, at 1750
     // cycles a piece, what bounded the wide form.
+    if (a.early) grid_dep_wait();
     const int q = warp & 3;
     const int half = (warp - EPI_WARP0) >> 2;
     const int gt = threadIdx.x & 127;  // thread of the group
@@ -842,7 +856,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
     uint32_t acc_ph = 0;
     for (Walk<BN, CTAS> w(a, tail, ngroups, total); w.more(); w.next()) {
       const Unit& t = w.t;
-      bool ok = wait_bar(smem_u32(&tail->tfull[acc]), acc_ph, abort_flag, deadline, status);
+      bool ok = wait_bar(smem_u32(&tail->tfull[acc]), acc_ph, abort_flag, status);
       if (!group_all(half, ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
