@@ -23,6 +23,7 @@ AFD_CFG_MX4 = 8
 (AFD_DBG_GATHER_INV, AFD_DBG_GATHER_PERM, AFD_DBG_GATHER_GROUPED, AFD_DBG_COMBINE_INV,
  AFD_DBG_SCATTER_INV, AFD_DBG_GEMM_OUT) = range(1, 7)
 AFD_DBG_NUM_SITES = 7
+AFD_DBG_MX4_WAIT = 7
 AFD_DIR_DISPATCH, AFD_DIR_RETURN = 0, 1
 (AFD_WS_IDS, AFD_WS_WEIGHTS, AFD_WS_COUNTS, AFD_WS_OFFSETS, AFD_WS_PERM, AFD_WS_INV, AFD_WS_XP,
  AFD_WS_H, AFD_WS_Y, AFD_WS_HS, AFD_WS_S, AFD_WS_STATUS) = range(12)

@@ -55,7 +55,7 @@ struct Mx4GemmArgs {
   const int32_t* offsets;    // [n_groups + 1], device
   int n_groups;
   int swiglu;
-  int32_t* status;           // the step's: no work once it is set; NULL: the file-scope word, set only
+  int32_t* status;           // the step's: no work once it is set; NULL: waits that give up are counted (afd_mx4_poll_status)
   // layer chosen on the device: the weight is layers[item->layer].mx4[wsel], not tmW and w
   const DevLayer* layers;
   const FanIn* item;
@@ -68,6 +68,9 @@ struct Mx4GemmArgs {
 };
 // bn: rows of a token tile (mx4_token_tile); units: an upper bound on the
 // output tiles, which sizes the grid
+#ifdef AFD_DEBUG_BOUNDS
+int mx4_plant_error();  // counts one error as a product without a context does
+#endif
 int mx4_token_tile(int64_t rows, int groups);
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units);
 int encode_mx4_rows(CUtensorMap* m, const void* codes, int64_t rows, int K, int bn);

@@ -46,11 +46,13 @@
 #include <cudaTypedefs.h>
 
 #include <cstdio>
+#include <map>
 #include <mutex>
+#include <utility>
 
 namespace {
 
-__device__ int32_t g_mx4_status;  // calls without a context
+__device__ uint32_t g_mx4_errors;  // calls without a context: waits that gave up
 
 constexpr int BOX = 256;              // columns of one token box (128 bytes of codes)
 constexpr int EPI_WARPS = 8;
@@ -297,7 +299,7 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile i
       if (start == 0) start = now;
       if (now - start > kTimeoutNs) {
         *abort_flag = 1;
-        set_error(status, AFD_ERR_TIMEOUT);
+        if (status) set_error(status, AFD_ERR_TIMEOUT); else atomicAdd(&g_mx4_errors, 1u);
         return false;
       }
     }
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
   typename R::Tail* tail = reinterpret_cast<typename R::Tail*>(smem + (size_t)STAGES * R::STAGE_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool leader = CTAS == 1 || cluster_rank() == 0;
-  int32_t* status = a.status ? a.status : &g_mx4_status;
+  int32_t* const status = a.status;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; s++) {
       for (int h = 0; h < R::PARTS; h++) {
@@ -1217,19 +1219,38 @@ int encode_mx4_weight(CUtensorMap* tm, const void* packed, int64_t bytes) {
   return rc;
 }
 
+// The errors are counted and never cleared, and a caller is told of those since
+// its own last call: with one word that the first caller cleared, a product on
+// another stream or thread could give up and its caller hear of nothing.
 extern "C" int afd_mx4_poll_status(void* cuda_stream) {
-  int32_t code = 0;
-  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(cuda_stream)) != cudaSuccess ||
-      cudaMemcpyFromSymbol(&code, g_mx4_status, sizeof code) != cudaSuccess) {
+  uint32_t n = 0;
+  int dev = 0;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&n, g_mx4_errors, sizeof n, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess) {
     cudaGetLastError();
     return AFD_ERR_CUDA;
   }
-  if (code) {
-    const int32_t zero = 0;
-    if (cudaMemcpyToSymbol(g_mx4_status, &zero, sizeof zero) != cudaSuccess) {
-      cudaGetLastError();
-      return AFD_ERR_CUDA;
-    }
+  bool more = n != 0;
+  try {
+    thread_local std::map<std::pair<int, void*>, uint32_t> told;
+    uint32_t& last = told[{dev, cuda_stream}];
+    more = n != last;
+    last = n;
+  } catch (...) {  // no memory to keep it: told again
   }
-  return code;
+  return more ? AFD_ERR_TIMEOUT : AFD_OK;
 }
+
+#ifdef AFD_DEBUG_BOUNDS
+int mx4_plant_error() {
+  uint32_t n = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&n, g_mx4_errors, sizeof n) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_mx4_errors, &(++n), sizeof n) != cudaSuccess) {
+    cudaGetLastError();
+    return AFD_ERR_CUDA;
+  }
+  return AFD_OK;
+}
+#endif

@@ -581,6 +581,9 @@ int afd_check_canaries(afd_ctx* ctx, int* window, int64_t* offset);
 #define AFD_DBG_SCATTER_INV 5    /* k_scatter_grouped: inv[r] < routed rows */
 #define AFD_DBG_GEMM_OUT 6       /* grouped GEMMs: a unit's last output row < output rows */
 #define AFD_DBG_NUM_SITES 7
+/* planted without a context (ctx NULL): one wait of an MXFP4 product that gave
+ * up, for afd_mx4_poll_status */
+#define AFD_DBG_MX4_WAIT 7
 int afd_debug_bounds(afd_ctx* ctx, int32_t* site, int64_t* index, int64_t* limit);
 int afd_debug_plant(afd_ctx* ctx, int32_t site);
 
@@ -749,9 +752,12 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
                 int hidden, int inter, int out_dtype, void* out, int64_t ldo, void* workspace,
                 int64_t workspace_bytes, void* cuda_stream);
 
-/* Synchronise the stream; return and clear the first device error of the
- * products above on the current device (AFD_ERR_TIMEOUT: a bounded wait gave
- * up and the outputs are incomplete), AFD_OK if none. */
+/* Synchronise the stream; AFD_ERR_TIMEOUT if, since this host thread's last
+ * call for this stream (since the library was loaded, for its first), a
+ * bounded wait (2 s) of any of the products above on the current device gave
+ * up and left its outputs incomplete; else AFD_OK.  The products of all
+ * streams are counted together: an error is told once to each thread and
+ * stream that polls, so that no caller takes another's. */
 int afd_mx4_poll_status(void* cuda_stream);
 
 /* Static string for a status code. */

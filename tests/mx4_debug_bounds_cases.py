@@ -1,11 +1,13 @@
 """MXFP4 steps against the bounds-checking debug build, in a process of its own
 that loads that build (AFD_LIBRARY).  Called by tests/test_mx4_debug_bounds_gpu.py;
-prints one JSON line.  Clean steps: no check fails.  Planted: every check of the
+prints one JSON line.  Status: a planted error of a product without a context is told
+once to every thread and stream that polls.  Clean steps: no check fails.  Planted: every check of the
 products' output rows fails on valid rows (the bound is taken as 0, nothing is
 stored), the step reports it, and a clean step gives the first one's bits."""
 import json
 import os
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
@@ -57,10 +59,28 @@ def case(lens, grouped):
     return out
 
 
+def told(stream):
+    return [A.afd_mx4_poll_status(stream.cuda_stream), A.afd_mx4_poll_status(stream.cuda_stream)]
+
+
+def status():
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    out = {"before": told(a) + told(b)}
+    assert A.afd_debug_plant(None, A.AFD_DBG_MX4_WAIT) == A.AFD_OK
+    out["first"], out["other_stream"] = told(a), told(b)
+    with ThreadPoolExecutor(1) as ex:
+        out["other_thread"] = ex.submit(told, a).result()
+        assert A.afd_debug_plant(None, A.AFD_DBG_MX4_WAIT) == A.AFD_OK
+        assert A.afd_debug_plant(None, A.AFD_DBG_MX4_WAIT) == A.AFD_OK
+        out["again"] = ex.submit(told, a).result() + told(a) + told(b)
+    out["new_stream"] = told(torch.cuda.Stream())
+    return out
+
+
 def main():
     A.lib()
     assert A.afd_debug_bounds(None)[0] == A.AFD_ERR_ARG, "not the debug build"
-    print(json.dumps({"narrow": case([37, 91], False), "wide": case([300, 450], False),
+    print(json.dumps({"status": status(), "narrow": case([37, 91], False), "wide": case([300, 450], False),
                       "grouped": case([60, 111], True)}))
 
 

@@ -37,3 +37,11 @@ def test_output_rows_are_checked(results, name):
     code, site, index, limit = r["planted"]
     assert (code, site, limit) == (A.AFD_ERR_BOUNDS, A.AFD_DBG_GEMM_OUT, 0) and index >= 0
     assert r["after_step"] == A.AFD_OK and r["after_bounds"] == A.AFD_OK and r["same"]
+
+
+def test_an_error_is_told_to_every_caller(results):
+    once = [A.AFD_ERR_TIMEOUT, A.AFD_OK]
+    r = results["status"]
+    assert r["before"] == [A.AFD_OK] * 4
+    assert r["first"] == r["other_stream"] == r["other_thread"] == r["new_stream"] == once
+    assert r["again"] == once * 3
