@@ -331,7 +331,9 @@ int mx4_product(LaunchCtx& lc, Mx4GemmArgs& a, const uint8_t* codes, const uint8
   if (img && scales) {
     rc = launched(launch_mx4_images(lc, scales, x_rows, offsets, rows, groups, K, image, a.status), "mx4 scale images");
     if (rc) return rc;
-    lc.pdl = 1;  // the product's set-up runs while the images are written
+    // the product's set-up runs while the images are written: in a call without
+    // a context (which has no status), in a step as its context's flags say
+    if (!a.status) lc.pdl = 1;
   }
   a.xs = scales;
   a.x_rows = x_rows;
