@@ -26,7 +26,7 @@ AFD_DBG_NUM_SITES = 7
 AFD_DBG_MX4_WAIT = 7
 AFD_DIR_DISPATCH, AFD_DIR_RETURN = 0, 1
 (AFD_WS_IDS, AFD_WS_WEIGHTS, AFD_WS_COUNTS, AFD_WS_OFFSETS, AFD_WS_PERM, AFD_WS_INV, AFD_WS_XP,
- AFD_WS_H, AFD_WS_Y, AFD_WS_HS, AFD_WS_S, AFD_WS_STATUS) = range(12)
+ AFD_WS_H, AFD_WS_Y, AFD_WS_HS, AFD_WS_S, AFD_WS_STATUS, AFD_WS_CODES) = range(13)
 AFD_HEADER_FIXED_WORDS = 12
 AFD_NOALLOC_MAX_ROUTER_WEIGHTS = 262144
 AFD_NOALLOC_MAX_LOGITS = 1048576

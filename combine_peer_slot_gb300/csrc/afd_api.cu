@@ -211,7 +211,7 @@ struct afd_ctx {
   int64_t forwards = 0;
   uint32_t go_seq = 0;               // tokens for ws.go, one per host-described routed step
   unsigned long long* canary_result = nullptr;  // AFD_CFG_CANARY: [changed words, first offset]
-  int64_t ws_cap[12];
+  int64_t ws_cap[13];
   // stage timing: one set of events per forward, in a ring, so the host
   // reads them after many forwards instead of waiting after each one
   static constexpr int kProfRing = 64;
@@ -496,8 +496,8 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
   c->m4.offs = reinterpret_cast<int32_t*>(b + offs[37]);
   c->plan1 = reinterpret_cast<GemmPlan*>(b + offs[16]);
   c->plan2 = reinterpret_cast<GemmPlan*>(b + offs[17]);
-  const int ws_map[12] = {4, 5, 6, 7, 8, 9, 11, 12, 13, 14, 15, 0};
-  for (int i = 0; i < 12; i++) c->ws_cap[i] = parts[ws_map[i]].bytes;
+  const int ws_map[13] = {4, 5, 6, 7, 8, 9, 11, 12, 13, 14, 15, 0, 29};
+  for (int i = 0; i < 13; i++) c->ws_cap[i] = parts[ws_map[i]].bytes;
   if (cfg->gemm != AFD_GEMM_SIMT) {
     rc = get_encoder();
     // token boxes: 32 rows for one CTA per tile, 128 rows (a CTA's half of a
@@ -1471,10 +1471,10 @@ int afd_get_window(afd_ctx* ctx, int direction, void** dev_ptr, int64_t* bytes) 
 }
 
 int afd_get_workspace(afd_ctx* ctx, int which, void** dev_ptr, int64_t* bytes) {
-  if (!ctx || which < 0 || which > AFD_WS_STATUS) return AFD_ERR_ARG;
-  void* ptrs[12] = {ctx->ws.ids, ctx->ws.w, ctx->ws.counts, ctx->ws.offsets, ctx->ws.perm,
+  if (!ctx || which < 0 || which > AFD_WS_CODES) return AFD_ERR_ARG;
+  void* ptrs[13] = {ctx->ws.ids, ctx->ws.w, ctx->ws.counts, ctx->ws.offsets, ctx->ws.perm,
                     ctx->ws.inv, ctx->ws.xp, ctx->ws.h, ctx->ws.y, ctx->ws.hs, ctx->ws.s,
-                    ctx->ws.status};
+                    ctx->ws.status, ctx->m4.codes};
   if (dev_ptr) *dev_ptr = ptrs[which];
   if (bytes) *bytes = ctx->ws_cap[which];
   return AFD_OK;

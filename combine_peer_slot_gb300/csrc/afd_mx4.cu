@@ -59,9 +59,10 @@ struct QuantArgs {
 };
 
 template <bool F32>
-__device__ __forceinline__ void quantize_chunks(const QuantArgs& a) {
-  const int64_t total = a.n_rows * a.chunks;  // a multiple of 4: a block's lanes are all in or all out
+__device__ __forceinline__ void quantize_chunks(const QuantArgs& a, int64_t n_rows) {
+  const int64_t total = n_rows * a.chunks;  // a multiple of 4: a block's lanes are all in or all out
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kChunks);
+  if (first >= total) return;
   const ChunkPos pos(first, a.chunks, a.magic);
   uint4 lo[kChunks], hi[kChunks];
 #pragma unroll
@@ -116,15 +117,14 @@ __device__ __forceinline__ void quantize_chunks(const QuantArgs& a) {
 }
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const __grid_constant__ QuantArgs a) {
-  quantize_chunks<F32>(a);
+  quantize_chunks<F32>(a, a.n_rows);
 }
 
 // ---------------------------------------------------------------------------
 // the same for a step's gathered rows: position r of Xp is row r of the
 // result.  The first thread also writes where the shared rows lie, for the
 // products that follow (a step of the work-item loop knows it on the device
-// only).  rows is the most there can be; past the step's own, the last
-// step's rows are coded again and nothing reads them.
+// only).  The launch's rows are the most there can be; the step's own are coded.
 // ---------------------------------------------------------------------------
 struct StepArgs {
   QuantArgs q;
@@ -137,18 +137,18 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize_step(const __grid_con
   grid_dep_wait();
   grid_dep_launch();
   if (read_status(a.status)) return;
+  int N = a.n, S = a.s;
+  if (a.item) {
+    N = a.item->grouped ? a.item->rtotal : a.item->total * a.topk;
+    S = a.has_shared ? a.item->stotal : 0;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    int N = a.n, S = a.s;
-    if (a.item) {
-      N = a.item->grouped ? a.item->rtotal : a.item->total * a.topk;
-      S = a.has_shared ? a.item->stotal : 0;
-    }
     a.offs[0] = N;
     a.offs[1] = N + S;
     a.offs[2] = 0;
     a.offs[3] = S;
   }
-  quantize_chunks<false>(a.q);
+  quantize_chunks<false>(a.q, min(a.q.n_rows, (int64_t)N + S));
 }
 
 // ---------------------------------------------------------------------------

@@ -221,6 +221,8 @@ typedef struct afd_layout {
 #define AFD_WS_HS 9         /* act [T, shared_inter] shared SwiGLU output */
 #define AFD_WS_S 10         /* fp32 [T, hidden] shared expert output */
 #define AFD_WS_STATUS 11    /* int32 device status word */
+#define AFD_WS_CODES 12     /* AFD_CFG_MX4: uint8 [T*topk + T, hidden / 2] codes of the routed rows,
+                               then of the shared ones (else 0 bytes) */
 
 typedef struct afd_ctx afd_ctx;
 
