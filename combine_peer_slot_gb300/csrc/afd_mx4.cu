@@ -464,7 +464,8 @@ static int64_t ffn_scales_bytes(int64_t n_rows, int E, int inter) {
   return up256(std::max(n_rows * inter / 32, mx4_image_bytes(n_rows, E, inter)));
 }
 int64_t afd_mx4_ffn_workspace(int64_t n_rows, int num_experts, int hidden, int inter) {
-  if (inter < kMx4Block || inter > kMaxDim || inter % kMx4Block) return -1;
+  // (2 inter rows of w13 are within the limits as well)
+  if (inter < kMx4Block || inter > kMaxDim / 2 || inter % kMx4Block) return -1;
   const int64_t img = afd_mx4_gemm_workspace(n_rows, num_experts, hidden);
   return img < 0 ? -1 : up256(n_rows * inter / 2) + ffn_scales_bytes(n_rows, num_experts, inter) + img;
 }
@@ -473,8 +474,7 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows, con
                 int num_experts, const void* w13, const void* wd, int hidden, int inter, int out_dtype, void* out,
                 int64_t ldo, void* workspace, int64_t workspace_bytes, void* cuda_stream) {
   const int64_t need = afd_mx4_ffn_workspace(n_rows, num_experts, hidden, inter);
-  if (need < 0 || afd_mx4_weight_bytes(num_experts, 2 * inter, hidden, 1) == 0 ||
-      afd_mx4_weight_bytes(num_experts, hidden, inter, 0) == 0 || ldo < hidden ||
+  if (need < 0 || ldo < hidden ||
       (out_dtype != AFD_DTYPE_F32 && out_dtype != AFD_DTYPE_BF16))
     return AFD_ERR_ARG;
   if (n_rows == 0) return AFD_OK;

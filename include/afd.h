@@ -683,7 +683,8 @@ int afd_route_select(const void* logits, int64_t ld, int n_tokens, int logits_dt
  * both without row padding.  All calls are asynchronous on cuda_stream,
  * allocate nothing, keep nothing between calls, and may be captured.
  * Errors of all: AFD_ERR_ARG (ranges, alignment, a pointer of another
- * device), AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA; n_rows == 0 does nothing.
+ * device), AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA, AFD_ERR_UNSUPPORTED (more than
+ * 2^31 blocks of work in a launch); n_rows == 0 does nothing.
  *
  * afd_mx4_quantize -- row r of the result codes row src_rows[r] / topk of x
  * (src_rows device int32 [n_rows]: positions t * topk + j as AFD_WS_PERM
@@ -743,7 +744,8 @@ int afd_mx4_gemm(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
 
 /* The expert FFN: the SwiGLU product with w13 (packed [num_experts, 2 inter,
  * hidden], swiglu), its bf16 rows coded again (AFD_MX4_SCALE_FLOOR), the
- * product with wd (packed [num_experts, hidden, inter]).  inter % 32 == 0.
+ * product with wd (packed [num_experts, hidden, inter]).  inter % 32 == 0,
+ * inter <= 32768 (w13 has 2 inter rows).
  * The same bits as afd_mx4_gemm, afd_mx4_quantize and afd_mx4_gemm in turn.
  * workspace: device, 256-byte aligned, at least afd_mx4_ffn_workspace bytes
  * (host only; -1 for dimensions outside the limits), else AFD_ERR_CAPACITY;
