@@ -487,6 +487,8 @@ def _output(h, x, cols, out_dtype, out, dev):
 def _scratch(h, workspace, need, dev):
     """(pointer, bytes, what keeps it alive until the call is enqueued)"""
     if workspace is not None:
+        if not workspace.is_contiguous():
+            _bad("workspace: a contiguous tensor wanted")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if need <= 0:
         return 0, 0, None
