@@ -353,6 +353,7 @@ def _rows_int32(h, t, n, what):
         _bad(f"{what}: contiguous int32 vector" + (f" of {n} wanted" if n >= 0 else " wanted"))
 
 
+_INT, _DIM = 2 ** 31 - 1, 65536  # the library's ints; its largest row
 _SCORES = {"softmax": A.AFD_SCORE_SOFTMAX, "sigmoid": A.AFD_SCORE_SIGMOID}
 _RULES = {"floor": A.AFD_MX4_SCALE_FLOOR, "ceil": A.AFD_MX4_SCALE_CEIL}
 
@@ -366,6 +367,10 @@ def route_select(logits, topk, bias=None, score="softmax", n_groups=1, topk_grou
     if code is None or kind is None or logits.dim() != 2:
         _bad("logits: bf16 or fp32 rows [T, E] wanted, score softmax or sigmoid")
     T, E = logits.shape
+    # (the binding passes ints and would wrap larger values)
+    if not (T <= _INT and E <= 256 and 0 < topk <= 16 and 0 < n_groups <= 32 and 0 < topk_groups <= 32
+            and 0 < group_top <= 2):
+        _bad("route_select: sizes out of range")
     ld, step = logits.stride()
     if step != 1 and E > 1:
         _bad("logits: rows of neighbouring elements wanted")
@@ -394,7 +399,7 @@ class Mx4:
     def __init__(self, codes, scales):
         h = _host or _get()
         rows, half = codes.shape if codes.dim() == 2 else _bad("codes: [rows, cols / 2] wanted")
-        if (codes.dtype is not h.uint8 or scales.dtype is not h.uint8 or half % 16
+        if (codes.dtype is not h.uint8 or scales.dtype is not h.uint8 or half % 16 or half > _DIM // 2
                 or scales.shape != (rows, half // 16) or not codes.is_contiguous() or not scales.is_contiguous()):
             _bad("MXFP4: contiguous uint8 codes [rows, cols / 2] and scales [rows, cols / 32] wanted")
         self.codes, self.scales, self.rows, self.cols = codes, scales, rows, 2 * half
@@ -409,8 +414,8 @@ def mx4_quantize(x, src_rows=None, topk=1, rule="floor"):
         _bad("x: bf16 or fp32 rows wanted, rule floor or ceil")
     n_x, cols = x.shape
     ld, step = x.stride()
-    if cols % 32 or step != 1:
-        _bad("x: rows of 32 m neighbouring elements wanted")
+    if cols % 32 or cols > _DIM or step != 1 or not 0 < topk <= _INT:
+        _bad("x: rows of 32 m neighbouring elements, up to 65536, and topk over 0 wanted")
     n, src = n_x, 0
     if src_rows is not None:
         _rows_int32(h, src_rows, -1, "src_rows")
@@ -457,6 +462,8 @@ class Mx4Weight:
                 or scales.shape != (*codes.shape[:2], codes.shape[2] // 16)):
             _bad("weight: contiguous uint8 codes [E, M, K / 2] and scales [E, M, K / 32] wanted")
         self.experts, self.M, self.K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        if self.experts > 256 or self.M > _DIM or self.K > _DIM:
+            _bad(f"weight dimensions {(self.experts, self.M, self.K)}")
         self.swiglu = bool(swiglu)
         nbytes = A.afd_mx4_weight_bytes(self.experts, self.M, self.K, self.swiglu)
         if nbytes <= 0:
