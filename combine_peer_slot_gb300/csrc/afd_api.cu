@@ -541,6 +541,32 @@ int afd_set_layer(afd_ctx* ctx, int layer, const float* Wg, const float* bias, c
   }
   LayerW& L = ctx->layers[layer];
   int rc = AFD_OK;
+  // AFD_CFG_MX4: every allocation before the first change, so that a layer whose
+  // weights are replaced keeps its old ones where there is no memory for the coding
+  struct Mx4Src { const void* W; int E, M, K, swiglu; };
+  const Mx4Src mx4_src[4] = {{W13, c.num_experts, 2 * c.inter, c.hidden, 1},
+                             {Wd, c.num_experts, c.hidden, c.inter, 0},
+                             {W13_s, 1, 2 * c.shared_inter, c.hidden, 1},
+                             {Wd_s, 1, c.hidden, c.shared_inter, 0}};
+  const int mx4_count = !(c.flags & AFD_CFG_MX4) ? 0 : has_shared ? 4 : 2;
+  struct Scratch {
+    uint8_t* p = nullptr;
+    ~Scratch() { if (p) cudaFree(p); }
+  } coded;
+  int64_t coded_bytes = 0;
+  for (int w = 0; w < mx4_count; w++) {
+    const Mx4Src& q = mx4_src[w];
+    const int64_t rows = (int64_t)q.E * q.M, bytes = mx4_weight_bytes(q.E, q.M, q.K, q.swiglu);
+    coded_bytes = std::max(coded_bytes, rows * (q.K / 2) + rows * (q.K / 32));
+    if (L.T[w]) continue;  // (sizes are the context's: the same at every call)
+    rc = cuda_fail(cudaMalloc(&L.T[w], bytes), "weight copy");
+    if (rc) return rc;
+    L.T_bytes[w] = bytes;
+  }
+  if (mx4_count) {
+    rc = cuda_fail(cudaMalloc(&coded.p, coded_bytes), "weight coding");
+    if (rc) return rc;
+  }
   // the copies below replace what a forward still in flight may read: no
   // overlap with earlier work on the stream
   LaunchCtx lc = ctx->lc();
@@ -560,38 +586,22 @@ int afd_set_layer(afd_ctx* ctx, int layer, const float* Wg, const float* bias, c
   L.Wd = Wd;
   L.W13s = has_shared ? W13_s : nullptr;
   L.Wds = has_shared ? Wd_s : nullptr;
-  if (c.flags & AFD_CFG_MX4) {
+  if (mx4_count) {
     // coded once (OCP scales) and packed; the caller's buffers are not read after this call returns
-    struct Src { const void* W; int E, M, K, swiglu; };
-    const Src src[4] = {{W13, c.num_experts, 2 * c.inter, c.hidden, 1},
-                        {Wd, c.num_experts, c.hidden, c.inter, 0},
-                        {W13_s, 1, 2 * c.shared_inter, c.hidden, 1},
-                        {Wd_s, 1, c.hidden, c.shared_inter, 0}};
-    for (int w = 0; w < (has_shared ? 4 : 2) && !rc; w++) {
-      const Src& q = src[w];
-      const int64_t rows = (int64_t)q.E * q.M, bytes = mx4_weight_bytes(q.E, q.M, q.K, q.swiglu);
-      if (L.T_bytes[w] != (size_t)bytes) {
-        cudaFree(L.T[w]);
-        L.T[w] = nullptr;
-        L.T_bytes[w] = 0;
-        rc = cuda_fail(cudaMalloc(&L.T[w], bytes), "weight copy");
-        if (rc) break;
-        L.T_bytes[w] = bytes;
-      }
-      uint8_t* tmp = nullptr;
-      rc = cuda_fail(cudaMalloc(&tmp, rows * q.K / 2 + rows * (q.K / 32)), "weight coding");
-      if (rc) break;
-      uint8_t* scales = tmp + rows * q.K / 2;
-      rc = cuda_fail(launch_mx4_quantize(lc, q.W, q.K, rows, 0, nullptr, 1, rows, q.K, 0, tmp, scales), "weight coding");
+    for (int w = 0; w < mx4_count && !rc; w++) {
+      const Mx4Src& q = mx4_src[w];
+      const int64_t rows = (int64_t)q.E * q.M;
+      uint8_t* scales = coded.p + rows * (q.K / 2);
+      rc = cuda_fail(launch_mx4_quantize(lc, q.W, q.K, rows, 0, nullptr, 1, rows, q.K, 0, coded.p, scales),
+                     "weight coding");
       if (!rc)
-        rc = cuda_fail(launch_mx4_pack(lc, tmp, scales, q.E, q.M, q.K, q.swiglu, static_cast<uint8_t*>(L.T[w])),
+        rc = cuda_fail(launch_mx4_pack(lc, coded.p, scales, q.E, q.M, q.K, q.swiglu, static_cast<uint8_t*>(L.T[w])),
                        "weight coding");
-      if (!rc) rc = encode_mx4_weight(L.mx4[w].tm, L.T[w], bytes);
+      if (!rc) rc = encode_mx4_weight(L.mx4[w].tm, L.T[w], L.T_bytes[w]);
       L.mx4[w].packed = static_cast<uint8_t*>(L.T[w]);
-      const int sync = cuda_fail(cudaStreamSynchronize(ctx->stream), "weight coding");
-      cudaFree(tmp);
-      if (!rc) rc = sync;
     }
+    const int sync = cuda_fail(cudaStreamSynchronize(ctx->stream), "weight coding");
+    if (!rc) rc = sync;
     if (rc) return rc;
   } else if (c.gemm != AFD_GEMM_SIMT) {
     // the tensor engines read tiled copies (one contiguous 16 KB block per
