@@ -424,9 +424,9 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
       {Tm * k * 4}, {Tm * k * 4},            // perm, inv
       {AFD_MAX_PEERS * E * 4},               // peer_counts
       {(Tm * k + Tm) * H * ab},              // xp (routed rows, then shared rows when gathered)
-      {Tm * k * I * ab},                     // h
+      {mx4 ? 0 : Tm * k * I * ab},           // h (MXFP4: coded, below)
       {Tm * k * H * yb},                     // y
-      {Tm * (Is > 0 ? Is : 1) * ab},         // hs
+      {mx4 ? 0 : Tm * (Is > 0 ? Is : 1) * ab},  // hs
       {Tm * H * 4},                          // s
       {(int64_t)sizeof(GemmPlan)}, {(int64_t)sizeof(GemmPlan)},
       {E * router_blocks((int)Tm) * 4}, {E * router_blocks((int)Tm) * 4},  // hist, base
@@ -504,11 +504,13 @@ int afd_create(const afd_config* cfg, void* cuda_stream, afd_ctx** out) {
     // 256-token unit) for the SM-pair engine
     const int box = cfg->gemm == AFD_GEMM_TENSOR ? 128 : 32;
     if (!rc) rc = encode_rows(&c->tmXp, c->ws.xp, Tm * k + Tm, (int)H, box);
-    if (!rc) rc = encode_rows(&c->tmH, c->ws.h, Tm * k, (int)I, box);
-    if (!rc) rc = encode_rows(&c->tmHs, c->ws.hs, Tm, (int)(Is > 0 ? Is : 64), box);
     if (!rc) rc = encode_rows(&c->tmXp32, c->ws.xp, Tm * k + Tm, (int)H, 32);
-    if (!rc) rc = encode_rows(&c->tmH32, c->ws.h, Tm * k, (int)I, 32);
-    if (!rc) rc = encode_rows(&c->tmHs32, c->ws.hs, Tm, (int)(Is > 0 ? Is : 64), 32);
+    if (!mx4) {  // (MXFP4: no such rows)
+      if (!rc) rc = encode_rows(&c->tmH, c->ws.h, Tm * k, (int)I, box);
+      if (!rc) rc = encode_rows(&c->tmHs, c->ws.hs, Tm, (int)(Is > 0 ? Is : 64), box);
+      if (!rc) rc = encode_rows(&c->tmH32, c->ws.h, Tm * k, (int)I, 32);
+      if (!rc) rc = encode_rows(&c->tmHs32, c->ws.hs, Tm, (int)(Is > 0 ? Is : 64), 32);
+    }
     const int64_t win_rows = c->L.window_bytes / (H * ab);
     if (!rc) rc = encode_rows(&c->tmWin, c->win[0], win_rows, (int)H, box);
     if (!rc) rc = encode_rows(&c->tmWin32, c->win[0], win_rows, (int)H, 32);

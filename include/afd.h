@@ -136,7 +136,7 @@ extern "C" {
  * the step as it is.  A layer's weights take 0.53 bytes per element instead
  * of 2.  bf16 activations, AFD_GEMM_TENSOR, hidden, inter and shared_inter
  * multiples of 32 (else AFD_ERR_UNSUPPORTED); AFD_CFG_SPLIT_GEMMS has no
- * meaning with it, and AFD_WS_H and AFD_WS_HS are not written. */
+ * meaning with it, and AFD_WS_H and AFD_WS_HS have 0 bytes. */
 #define AFD_CFG_MX4 8
 typedef struct afd_config {
   int32_t num_peers;

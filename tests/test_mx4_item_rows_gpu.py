@@ -61,3 +61,13 @@ def test_no_codes_without_the_flag():
     run = R.Runner(W.custom("fanin", seq_lens=[3, 4]), layers=1)
     assert A.afd_get_workspace(run.ctx, A.AFD_WS_CODES)[1] == 0
     run.close()
+
+
+def test_no_uncoded_swiglu_rows_with_the_flag():
+    """The SwiGLU rows exist as codes only: no workspace for bf16 ones."""
+    w = W.custom("fanin", seq_lens=[3, 4])
+    for flags, bytes_ in ((A.AFD_CFG_MX4, 0), (0, 2)):
+        run = R.Runner(w, layers=1, flags=flags, max_total_tokens=64)
+        assert A.afd_get_workspace(run.ctx, A.AFD_WS_H)[1] == 64 * w.topk * w.inter * bytes_
+        assert A.afd_get_workspace(run.ctx, A.AFD_WS_HS)[1] == 64 * w.shared_inter * bytes_
+        run.close()
