@@ -497,7 +497,7 @@ __host__ __device__ inline int wgq_groups(int E) { return (E + 3) / 4; }
 struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
-  int64_t* launches;
+  int64_t* launches;  // counted there; NULL: not counted
   int pdl = 0;  // 1: a launch may start while the previous kernel drains
 };
 
@@ -517,7 +517,7 @@ cudaError_t launch_k(const LaunchCtx& lc, void (*kernel)(KArgs...), dim3 grid, d
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = lc.pdl ? 1 : 0;
-  ++*lc.launches;
+  if (lc.launches) ++*lc.launches;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
@@ -539,7 +539,7 @@ cudaError_t launch_k_cluster(const LaunchCtx& lc, void (*kernel)(KArgs...), dim3
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = lc.pdl ? 2 : 1;
-  ++*lc.launches;
+  if (lc.launches) ++*lc.launches;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 #endif

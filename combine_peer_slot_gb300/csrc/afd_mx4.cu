@@ -11,7 +11,6 @@
 namespace {
 
 constexpr int kThreads = 256;
-thread_local int64_t g_mx4_launches = 0;  // (calls may come from several threads)
 
 // Both coding kernels walk the matrix in chunks of eight (or four) values, a
 // CTA kChunks * 256 consecutive ones, a thread every 256th of them: a warp's
@@ -263,7 +262,7 @@ int64_t chunk_grid(int64_t chunks) { return (chunks + kThreads * kChunks - 1) / 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 int make_lc(void* cuda_stream, LaunchCtx* lc) {
-  *lc = LaunchCtx{reinterpret_cast<cudaStream_t>(cuda_stream), 0, &g_mx4_launches};
+  *lc = LaunchCtx{reinterpret_cast<cudaStream_t>(cuda_stream), 0, nullptr};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&lc->num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {

@@ -618,8 +618,6 @@ __global__ void __launch_bounds__(kSelWarps * 32, 6) k_route_select(const __grid
   }
 }
 
-thread_local int64_t g_select_launches = 0;  // (calls may come from several threads)
-
 template <typename LT, int PER>
 cudaError_t launch_per(const LaunchCtx& lc, SelArgs a) {
   const unsigned grid = (unsigned)((a.n + kSelWarps - 1) / kSelWarps);
@@ -660,7 +658,7 @@ extern "C" int afd_route_select(const void* logits, int64_t ld, int n_tokens, in
   if (rc) return rc;
   const SelArgs a{logits, ld, bias, ids, weights, n_tokens, num_experts, topk,
                   score == AFD_SCORE_SIGMOID, n_groups, topk_groups, group_top, renorm != 0, routed_scaling, 0, 0, 0, 0};
-  const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, &g_select_launches};
+  const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, nullptr};
   const cudaError_t e = logits_dtype == AFD_DTYPE_F32 ? launch_select<float>(lc, a) : launch_select<uint16_t>(lc, a);
   if (e != cudaSuccess) {
     cudaGetLastError();
