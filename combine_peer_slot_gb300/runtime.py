@@ -196,11 +196,11 @@ class RankSet:
     """Token-level dispatch on one GPU: ffn_size FFN-rank contexts, each with
     its block of the experts (a view into the layer's expert weights, no
     copy) and the shared expert, and one Attention-peer object per peer that
-    sends to all of them.  The Attention side's gate is the library's router
+    sends to all of them; flags: AFD_CFG_* of the contexts.  The Attention side's gate is the library's router
     (afd_route_noalloc) on each peer's tokens.  Torch plumbing only."""
 
     def __init__(self, w: W.Workload, ffn_size, ring_depth=1, gemm=A.AFD_GEMM_TENSOR, layers=None,
-                 multiplier=2.0, wait_timeout_ns=0, max_total_tokens=0, device="cuda"):
+                 multiplier=2.0, wait_timeout_ns=0, max_total_tokens=0, device="cuda", flags=0):
         import torch
         self.w, self.F, self.device = w, ffn_size, device
         self.layers = w.layers if layers is None else layers
@@ -219,7 +219,7 @@ class RankSet:
                                 max_total_tokens=max_total_tokens or w.total_tokens,
                                 max_layers=self.layers, gemm=gemm,
                                 routed_cap_multiplier=multiplier,
-                                wait_timeout_ns=wait_timeout_ns, ffn_rank=r, ffn_size=ffn_size)
+                                wait_timeout_ns=wait_timeout_ns, flags=flags, ffn_rank=r, ffn_size=ffn_size)
             ctx = A.afd_create(cfg, self.stream.cuda_stream)
             for layer, wt in enumerate(self.weights):
                 W13, Wd = wt["W13"], wt["Wd"]

@@ -661,7 +661,8 @@ int afd_route_noalloc(const void* x, int n_tokens, int hidden, int act_dtype, co
  * Equal values go to the lower index (blocks and experts).  The choice is
  * that of the exact scores: values that fp32 cannot tell apart are compared
  * in fp64.  Where fewer than topk experts may be chosen, the entries left
- * get id -1 and weight 0.  A row with a NaN (or, under softmax, +inf) in
+ * get id -1 and weight 0 (afd_attn_dispatch sends rows with topk experts
+ * only: it answers an id -1 with AFD_ERR_ARG).  A row with a NaN (or, under softmax, +inf) in
  * its logits, or a NaN in the bias, gets id -1 and weight NaN throughout.
  * num_experts <= 256, topk <= 16, topk <= topk_groups * (num_experts /
  * n_groups), num_experts % n_groups == 0.  Asynchronous on cuda_stream,
