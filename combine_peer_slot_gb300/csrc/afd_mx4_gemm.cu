@@ -25,14 +25,16 @@
 // Measured (weights of 64 experts):
 //   narrow, 1974 rows, 2816 x 2048 with SwiGLU: 36 us, 5.6 TB/s of what it has
 //     to read (83 % of the copy rate); the weights' stream bounds it
-//   wide, with its scale images, 79872 rows, 2816 x 2048 with SwiGLU: 194 us,
-//     4.7 PFLOP/s; 2048 x 1408: 119 us, 3.9 PFLOP/s and 4.1 TB/s (twice the
-//     bf16 rate).  Timing copies of the second: 103 us without its epilogue, 93
-//     without its loads, 84 without either, 112 without the weights' loads
-//     alone.  The SMs draw 12 TB/s from L2 in both; over long rows (K 8192 and
-//     more) 15 TB/s and 1166 cycles a 512-column stage, 1000 without loads, of
-//     which the eight MMAs take some 620 and their issue as much.  At that rate
-//     the board draws 1.37 of its 1.4 kW and the SMs run at 1.85 GHz.
+//   wide, with its scale images, 79872 rows, 2816 x 2048 with SwiGLU: 201 us,
+//     4.6 PFLOP/s; 2048 x 1408: 116 us, 4.0 PFLOP/s and 4.2 TB/s (twice the
+//     bf16 rate).  The eight MMAs of a 512-column stage run for some 620 cycles,
+//     77 each: 11.4 PFLOP/s on 76 pairs at 1.85 GHz, at which the two would take
+//     81 and 40 us (the second's bytes 72).  A stage takes 1166 cycles over long
+//     rows (K 8192 and more; 15 TB/s from L2), 1000 without loads.  Timing copies
+//     of the second, when it took 119: 103 us without its epilogue, 93 without its
+//     loads, 84 without either, 112 without the weights' loads alone.  It is not
+//     the power: the board draws 1.37 of its 1.4 kW and reports its cap, but a
+//     pass after 20 ms of rest takes as long as one of a 3 s run (118 and 122 us).
 //   Not kept: asking L2 for a unit's first reads two units ahead (117 -> 128
 //   us: the prefetches queue before the copies); stores that L2 evicts first
 //   (no change) or plain 16-byte stores (3 us slower); a third slot of scales
@@ -330,8 +332,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // than their 64-bit values, as with the plain fp32 formula; with ex2.approx and
 // rcp.approx alone 196, and the expert FFN of a prefill fan-in lay 2.9e-4 of
 // its norm from the plain form's (now none).  14 instructions a value where
-// those took 6: 339 us for that FFN against 320; the division operator's own
-// branch made it 488.  e^88 < 2^127: 1 + e stays finite for the remainder; over
+// those took 6, 6 % of that FFN's time; the division operator's own branch
+// would be 50 %.  e^88 < 2^127: 1 + e stays finite for the remainder; over
 // 2^126, g under -87.3, its reciprocal is zero, and so is the result.
 __device__ __forceinline__ float swiglu_f(float g, float u) {
   const float y = 1.0f + expf(fminf(-g, 88.0f));
@@ -1141,7 +1143,10 @@ cudaError_t launch_variant(const LaunchCtx& lc, const Mx4GemmArgs& a, int64_t un
 // 512 TMEM columns).  Narrow / wide in us, 64 groups of drawn sizes, 2816 x
 // 2048 with SwiGLU: average 31 36 / 41, 48 37 / 42, 56 39 / 43, 64 46 / 43, 80
 // 57 / 44; of skewed sizes (the largest five times the smallest): 48 40 /
-// 42, 56 44 / 42.  At 1248 rows a group 490 / 194.
+// 42, 56 44 / 42.  At 1248 rows a group 490 / 201.  The sizes themselves are on
+// the device: groups without rows count in the average, so a few large groups
+// among many empty ones take the narrow form, and a step of the work-item loop
+// takes the form of its context's capacity.
 int mx4_token_tile(int64_t rows, int groups) { return rows <= 48 * (int64_t)groups ? kNarrow : kWide; }
 
 cudaError_t launch_mx4_gemm(const LaunchCtx& lc, const Mx4GemmArgs& a, int bn, int64_t units) {

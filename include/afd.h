@@ -135,7 +135,7 @@ extern "C" {
  * tensor cores with fp32 accumulation (afd_mx4_gemm) and leaves the rest of
  * the step as it is.  A layer's weights take 0.53 bytes per element instead
  * of 2.  bf16 activations, AFD_GEMM_TENSOR, hidden, inter and shared_inter
- * multiples of 32 (else AFD_ERR_UNSUPPORTED); AFD_CFG_SPLIT_GEMMS has no
+ * multiples of 32, up to 65536 and 32768 (else AFD_ERR_UNSUPPORTED); AFD_CFG_SPLIT_GEMMS has no
  * meaning with it, and AFD_WS_H and AFD_WS_HS have 0 bytes. */
 #define AFD_CFG_MX4 8
 typedef struct afd_config {
