@@ -331,17 +331,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // corrected by its exact remainder.  Of 23 M values 156 round to another bf16
 // than their 64-bit values, as with the plain fp32 formula; with ex2.approx and
 // rcp.approx alone 196, and the expert FFN of a prefill fan-in lay 2.9e-4 of
-// its norm from the plain form's (now none).  14 instructions a value where
+// its norm from the plain form's (now none).  15 instructions a value where
 // those took 6, 6 % of that FFN's time; the division operator's own branch
 // would be 50 %.  e^88 < 2^127: 1 + e stays finite for the remainder; over
 // 2^126, g under -87.3, its reciprocal is zero, and so is the result.  An
-// infinite g leaves no remainder (NaN); its caller puts inf * u there.
+// infinite g has inf - inf for a remainder; the minimum makes that a number.
 __device__ __forceinline__ float swiglu_f(float g, float u) {
   const float y = 1.0f + expf(fminf(-g, 88.0f));
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
   const float q = g * r;
-  return fmaf(fmaf(-q, y, g), r, q) * u;
+  return fmaf(fminf(fmaf(-q, y, g), 3e38f), r, q) * u;
 }
 
 // TMEM lanes [l, l + 16) x 32 columns in the fragment layout: register 4 i
@@ -931,14 +931,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) k_mx4_gemm(const __grid_consta
           for (int i = 0; i < 8; i++) {
             const float g0 = __uint_as_float(x[2 * i]), g1 = __uint_as_float(x[2 * i + 1]);
             h[i] = pack_bf16(swiglu_f(g0, __uint_as_float(y[2 * i])), swiglu_f(g1, __uint_as_float(y[2 * i + 1])));
-          }
-          if (fmt == OUT_ACT) {  // (coded, a block with an infinity or a NaN is the same: scale 255)
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const float g0 = __uint_as_float(x[2 * i]), g1 = __uint_as_float(x[2 * i + 1]);
-              if (g0 == INFINITY) h[i] = (h[i] & 0xffff0000u) | (pack_bf16(g0 * __uint_as_float(y[2 * i]), 0.0f) & 0xffffu);
-              if (g1 == INFINITY) h[i] = (h[i] & 0xffffu) | (pack_bf16(0.0f, g1 * __uint_as_float(y[2 * i + 1])) & 0xffff0000u);
-            }
           }
           const uint32_t at = smem_u32(ebuf) + (8 * (lane >> 4) + (lane & 7)) * 128 +
                               (((q * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
