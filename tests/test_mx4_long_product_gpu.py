@@ -1,8 +1,8 @@
 """A product that takes longer than the bound on its waits (2 s each) ends like
 any other: the bound is a wait's, not the kernel's.  The length comes from
 groups that overlap (every second one covers all rows: such a call's outputs
-are unspecified, here every writer of a row writes the same zeros) over 360 M rows
-of one scale block, 14 GB in all."""
+are unspecified, here every writer of a row writes the same zeros) over 250 M rows
+of one scale block, 10 GB in all."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -22,7 +22,7 @@ def _cuda():
 
 
 def test_longer_than_the_bound_of_a_wait():
-    n, E, M, K = 360_000_000, 256, 8, 32
+    n, E, M, K = 250_000_000, 256, 8, 32
     w = R.Mx4Weight(torch.zeros(E, M, K // 2, dtype=torch.uint8, device="cuda"),
                     torch.full((E, M, 1), 127, dtype=torch.uint8, device="cuda"))
     x = R.Mx4(torch.zeros(n, K // 2, dtype=torch.uint8, device="cuda"),
