@@ -131,6 +131,15 @@ SIGNATURES = [
     ("afd_mx4_ffn_workspace", _I64, [_I64, _I, _I, _I]),
     ("afd_mx4_ffn", _I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _I64, _P]),
     ("afd_mx4_poll_status", _I, [_P]),
+    ("afd_balance_workspace", _I64, [_I, _I, _I]),
+    ("afd_balance_loss", _I, [_P, _I64, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I64, _P]),
+    ("afd_route_backward", _I, [_P, _I64, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P, _I64, _P]),
+    ("afd_lora_plan_bytes", _I64, [_I64, _I]),
+    ("afd_lora_plan", _I, [_P, _I64, _I, _P, _I64, _P]),
+    ("afd_lora_apply", _I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _P, _I, _I, _P, _P, _I64, _I, _P, _I64, _P, _P]),
+    ("afd_lora_backward_workspace", _I64, [_I64, _I, _I, _I, _I]),
+    ("afd_lora_backward", _I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _I64, _I, _I, _P, _P, _P, _I, _P, _P, _I64, _P,
+                               _I64, _P, _P, _P, _I64, _P]),
 ]
 AFD_NUM_STAGES = 8
 STAGE_NAMES = ("header_check", "router", "plan", "gather", "gemm_swiglu", "gemm_down",
@@ -476,3 +485,50 @@ def afd_mx4_ffn(codes, scales, n_rows, offsets, num_experts, w13, wd, hidden, in
 
 def afd_mx4_poll_status(stream=0):
     return lib().afd_mx4_poll_status(stream or None)
+
+
+# ---- expert load, routing gradient, adapters (no context; pointers as ints) ------
+def afd_balance_workspace(n_tokens, num_experts, n_seqs):
+    return int(lib().afd_balance_workspace(n_tokens, num_experts, n_seqs))
+
+
+def afd_balance_loss(logits, ld, n_tokens, logits_dtype, ids, num_experts, topk, score, seq_offsets, n_seqs,
+                     loss, counts, workspace=0, workspace_bytes=0, stream=0):
+    return lib().afd_balance_loss(logits or None, ld, n_tokens, logits_dtype, ids or None, num_experts, topk,
+                                  score, seq_offsets or None, n_seqs, loss or None, counts or None,
+                                  workspace or None, workspace_bytes, stream or None)
+
+
+def afd_route_backward(logits, ld, n_tokens, logits_dtype, ids, num_experts, topk, score, renorm,
+                       routed_scaling, d_weights, seq_offsets, n_seqs, counts, d_loss, d_logits, ldd, stream=0):
+    return lib().afd_route_backward(logits or None, ld, n_tokens, logits_dtype, ids or None, num_experts, topk,
+                                    score, int(bool(renorm)), routed_scaling, d_weights or None,
+                                    seq_offsets or None, n_seqs, counts or None, d_loss or None,
+                                    d_logits or None, ldd, stream or None)
+
+
+def afd_lora_plan_bytes(n_tokens, n_adapters):
+    return int(lib().afd_lora_plan_bytes(n_tokens, n_adapters))
+
+
+def afd_lora_plan(ids, n_tokens, n_adapters, plan, plan_bytes, stream=0):
+    return lib().afd_lora_plan(ids or None, n_tokens, n_adapters, plan or None, plan_bytes, stream or None)
+
+
+def afd_lora_apply(plan, n_tokens, n_adapters, x, ldx, x_dtype, K, a, b, rank, M, scale, base, ldb, y_dtype,
+                   out, ldo, u=0, stream=0):
+    return lib().afd_lora_apply(plan or None, n_tokens, n_adapters, x or None, ldx, x_dtype, K, a or None,
+                                b or None, rank, M, scale or None, base or None, ldb, y_dtype, out or None, ldo,
+                                u or None, stream or None)
+
+
+def afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank):
+    return int(lib().afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank))
+
+
+def afd_lora_backward(plan, n_tokens, n_adapters, x, ldx, x_dtype, K, dy, ldy, y_dtype, M, u, a, b, rank, scale,
+                      d_base, ldb, dx, ldd, da, db, workspace, workspace_bytes, stream=0):
+    return lib().afd_lora_backward(plan or None, n_tokens, n_adapters, x or None, ldx, x_dtype, K, dy or None, ldy,
+                                   y_dtype, M, u or None, a or None, b or None, rank, scale or None,
+                                   d_base or None, ldb, dx or None, ldd, da or None, db or None,
+                                   workspace or None, workspace_bytes, stream or None)

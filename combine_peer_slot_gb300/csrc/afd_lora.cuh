@@ -1,0 +1,187 @@
+// afd_lora.cuh -- low-rank adapters: the plan of a batch and what the kernels
+// of its translation units share.
+#pragma once
+
+#include "afd_internal.cuh"
+
+constexpr int kLoraMaxAdapters = 1024;
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxCols = 65536;
+constexpr int64_t kLoraMaxTokens = int64_t(1) << 24;
+
+// Rows of one adapter that a tile of the products holds, and rows of one
+// piece of the weight gradients' sums.
+__host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
+__host__ __device__ inline int lora_piece(int64_t) { return 512; }
+
+// The plan, made on the device from the rows' adapter ids: the rows in adapter
+// order (stable; rows without an adapter last), cut into tiles of one adapter.
+//   head   {tiles, tiles of rows without an adapter, pieces, rows with one}
+//   tiles  {adapter (-1: none), first row in order, rows, 0}
+//   pieces {adapter, first row in order, rows, slot of its partial sums or -1}
+//   first  [adapters + 1] first partial slot; last one: slots used
+struct LoraPlan {
+  int4* head;
+  int4* tiles;
+  int4* pieces;
+  int32_t* first;   // [adapters]: first piece; [adapters + l]: pieces of l
+  int32_t* order;   // [tokens]
+  int64_t max_tiles, max_pieces, max_slots, bytes;
+};
+inline LoraPlan lora_plan_at(void* base, int64_t tokens, int64_t adapters) {
+  LoraPlan p;
+  const int64_t few = std::min(tokens, adapters);
+  p.max_tiles = tokens / lora_tile(tokens) + few + 1;
+  p.max_pieces = tokens / lora_piece(tokens) + few;
+  // an adapter of several pieces has more than one piece's rows
+  p.max_slots = 2 * (tokens / lora_piece(tokens));
+  char* at = reinterpret_cast<char*>(base);
+  auto take = [&](int64_t bytes) {
+    char* r = at;
+    at += (bytes + 15) / 16 * 16;
+    return r;
+  };
+  p.head = reinterpret_cast<int4*>(take(16));
+  p.tiles = reinterpret_cast<int4*>(take(16 * p.max_tiles));
+  p.pieces = reinterpret_cast<int4*>(take(16 * std::max<int64_t>(1, p.max_pieces)));
+  p.first = reinterpret_cast<int32_t*>(take(8 * adapters));
+  p.order = reinterpret_cast<int32_t*>(take(4 * std::max<int64_t>(1, tokens)));
+  p.bytes = at - reinterpret_cast<char*>(base);
+  return p;
+}
+
+// out[t] = base[t] + scale[l] w2[l]^T u_t, u_t = w1[l] src[t], l = the row's adapter
+struct LoraArgs {
+  LoraPlan plan;
+  const void* src;
+  int64_t lds;
+  const void* w1;      // bf16 [L][R][K]
+  const void* w2;      // bf16 [L][R][M]
+  const float* scale;  // [L] or NULL (1)
+  const void* base;    // NULL: zeros; may be out
+  int64_t ldb;
+  void* out;
+  int64_t ldo;
+  float* u;            // [T][R] or NULL
+  int64_t T;
+  int K, M, R;
+  int src_f32, out_f32;
+  int vk, vm;          // rows of src and w1 / of base, out and w2 move 16 bytes at a time
+};
+// da[l] = scale[l] sum v_t x_t^T, db[l] = scale[l] sum u_t dy_t^T
+struct LoraWgradArgs {
+  LoraPlan plan;
+  const float* p[2];   // v, u: [T][R]
+  const void* q[2];    // x, dy
+  int64_t ldq[2];
+  float* out[2];       // [L][R][N]
+  float* part[2];      // [slots][R][N]
+  int N[2];
+  int f32[2];
+  int vec[2];
+  const float* scale;
+  int64_t T;
+  int R, L;
+};
+cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);
+cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
+
+#ifdef __CUDACC__
+// D += A B on 16 x 8 x 16 bf16 values, fp32 sums: lane (g, c) = (lane / 4,
+// lane % 4) holds of A rows g, g + 8 and of B column g the k pairs 2 c, 2 c + 8;
+// of D rows g, g + 8, columns 2 c, 2 c + 1.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An fp32 value as a sum of bf16 values: the upper 8 bits of its fraction cut
+// off, then the next 8, then the rest: three parts are the value, two (the
+// second rounded) are within 2^-17 of it.  Cutting, unlike rounding, cannot
+// carry the largest finite values over to infinity; a value that is not finite
+// is all in the first part (NaN stays NaN), with zeros behind it.
+template <int PARTS>
+__device__ __forceinline__ void split_bf16(float v, uint16_t (&p)[PARTS]) {
+  const uint32_t b = __float_as_uint(v);
+  const bool fine = (b & 0x7f800000u) != 0x7f800000u;
+  p[0] = (uint16_t)(b >> 16);
+  if (!fine && (b & 0x7fffffu)) p[0] |= 0x40u;
+  float rest = fine ? v - __uint_as_float(b & 0xffff0000u) : 0.0f;
+#pragma unroll
+  for (int i = 1; i < PARTS; i++) {
+    if (i == PARTS - 1) {
+      p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
+    } else {
+      const uint32_t r = __float_as_uint(rest);
+      p[i] = (uint16_t)(r >> 16);
+      rest -= __uint_as_float(r & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T>
+struct LoraSrc;
+template <>
+struct LoraSrc<uint16_t> { static constexpr int kParts = 1; };
+template <>
+struct LoraSrc<float> { static constexpr int kParts = 3; };
+
+// Eight neighbouring values of a row from column c0 as packed bf16 parts;
+// columns from n on are zero.  vec: rows are 16-byte aligned and n % 8 == 0.
+template <typename T>
+__device__ __forceinline__ void load_eight(const T* row, int c0, int n, bool vec, uint4 (&v)[LoraSrc<T>::kParts]);
+template <>
+__device__ __forceinline__ void load_eight<uint16_t>(const uint16_t* row, int c0, int n, bool vec, uint4 (&v)[1]) {
+  v[0] = make_uint4(0u, 0u, 0u, 0u);
+  if (c0 >= n) return;
+  if (vec) {
+    v[0] = *reinterpret_cast<const uint4*>(row + c0);
+    return;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) w[i] = c0 + i < n ? (uint32_t)row[c0 + i] : 0u;
+  v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+template <>
+__device__ __forceinline__ void load_eight<float>(const float* row, int c0, int n, bool vec, uint4 (&v)[3]) {
+  float f[8];
+  if (vec && c0 < n) {
+    const float4 a = *reinterpret_cast<const float4*>(row + c0), b = *reinterpret_cast<const float4*>(row + c0 + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) f[i] = c0 + i < n ? row[c0 + i] : 0.0f;
+  }
+  uint32_t w[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    uint16_t p[3];
+    split_bf16<3>(f[i], p);
+#pragma unroll
+    for (int j = 0; j < 3; j++) w[j][i] = p[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 3; j++)
+    v[j] = make_uint4(w[j][0] | w[j][1] << 16, w[j][2] | w[j][3] << 16, w[j][4] | w[j][5] << 16, w[j][6] | w[j][7] << 16);
+}
+
+// Four rows' eight columns (rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of sixteen) to
+// B operands of eight products: in product i, column n of B is column 8 n + i
+// of the 64, so lane (g, c) needs of its own loads (columns 8 g ..) only
+__device__ __forceinline__ void pair_rows(const uint4& r0, const uint4& r1, const uint4& r2, const uint4& r3,
+                                          uint32_t (&b)[8][2]) {
+  const uint32_t x0[4] = {r0.x, r0.y, r0.z, r0.w}, x1[4] = {r1.x, r1.y, r1.z, r1.w};
+  const uint32_t x2[4] = {r2.x, r2.y, r2.z, r2.w}, x3[4] = {r3.x, r3.y, r3.z, r3.w};
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    b[2 * j][0] = __byte_perm(x0[j], x1[j], 0x5410);
+    b[2 * j][1] = __byte_perm(x2[j], x3[j], 0x5410);
+    b[2 * j + 1][0] = __byte_perm(x0[j], x1[j], 0x7632);
+    b[2 * j + 1][1] = __byte_perm(x2[j], x3[j], 0x7632);
+  }
+}
+#endif

@@ -1,0 +1,273 @@
+// afd_lora_apply.cu -- both products of the adapters in one kernel:
+//   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
+// forward with (x, A, B), backward with (dy, B, A).
+//
+// A cluster takes a tile of one adapter's rows (16 or 64, gathered by the
+// plan's order).  First its warps share the columns of src in chunks of 32,
+// each lane loading its operands of the tensor cores' products straight from
+// global memory: the k order inside a chunk is free as long as both operands
+// agree, so a lane takes 16 neighbouring bytes for its four k pairs.  The
+// sums over the warps go through shared memory, those over the CTAs through
+// distributed shared memory, always in the same order.  Then the warps share
+// the columns of out in blocks of 64.  u enters the second product as two
+// (out in bf16) or three (fp32) bf16 parts, so that it keeps 16 or 24 bits.
+#include <cooperative_groups.h>
+
+#include "afd_lora.cuh"
+
+namespace {
+
+namespace cg = cooperative_groups;
+constexpr int kWarps = 8;
+
+template <typename TO>
+struct OutParts;
+template <>
+struct OutParts<uint16_t> { static constexpr int kParts = 2; };
+template <>
+struct OutParts<float> { static constexpr int kParts = 3; };
+
+// eight neighbouring outputs: base + v, rounded once
+template <typename TO>
+__device__ __forceinline__ void add_eight(const void* base, TO* out, int c0, int n, bool vec, const float (&v)[8]) {
+  if (c0 >= n) return;
+  const TO* b = reinterpret_cast<const TO*>(base);
+  if (vec) {
+    if (sizeof(TO) == 2) {
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (b) q = *reinterpret_cast<const uint4*>(b + c0);
+      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float lo = __uint_as_float(w[i] << 16) + v[2 * i], hi = __uint_as_float(w[i] & 0xffff0000u) + v[2 * i + 1];
+        const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        w[i] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+      *reinterpret_cast<uint4*>(out + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+      if (b) {
+        p = *reinterpret_cast<const float4*>(b + c0);
+        q = *reinterpret_cast<const float4*>(b + c0 + 4);
+      }
+      *reinterpret_cast<float4*>(out + c0) = make_float4(p.x + v[0], p.y + v[1], p.z + v[2], p.w + v[3]);
+      *reinterpret_cast<float4*>(out + c0 + 4) = make_float4(q.x + v[4], q.y + v[5], q.z + v[6], q.w + v[7]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    if (c0 + i >= n) break;
+    if (sizeof(TO) == 2) {
+      const float f = (b ? __uint_as_float((uint32_t)b[c0 + i] << 16) : 0.0f) + v[i];
+      out[c0 + i] = (TO)__bfloat16_as_ushort(__float2bfloat16_rn(f));
+    } else {
+      const float f = (b ? reinterpret_cast<const float*>(base)[c0 + i] : 0.0f) + v[i];
+      reinterpret_cast<float*>(out)[c0 + i] = f;
+    }
+  }
+}
+
+template <int TT, int KC, typename TS, typename TO>
+__global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constant__ LoraArgs a) {
+  constexpr int kParts = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
+  constexpr int kRows = TT == 64 ? (KC < 2 ? KC : 2) : KC;       // rank tiles of a pass
+  constexpr int kCols = TT == 64 ? (sizeof(TS) == 4 ? 4 : 8) : TT / 8;  // token tiles of a pass
+  constexpr int kRedStride = kCols * 8 + 8;
+  extern __shared__ __align__(16) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), q = (int)cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int4 head = *a.plan.head;
+  const int64_t tile = blockIdx.x / C;
+  if (tile >= head.x + head.y) return;
+  const int4 t = a.plan.tiles[tile];
+  const int32_t* order = a.plan.order + t.y;
+  if (t.x < 0) {  // rows without an adapter: out = base
+    for (int i = warp; i < t.z; i += kWarps) {
+      const int64_t row = order[i];
+      if (a.base != a.out) {
+        const float zero[8] = {};
+        const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
+        for (int c0 = (q * 32 + lane) * 8; c0 < a.M; c0 += C * 256)
+          add_eight<TO>(b, reinterpret_cast<TO*>(a.out) + row * a.ldo, c0, a.M, a.vm, zero);
+      }
+      if (a.u && q == 0)
+        for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
+    }
+    return;
+  }
+  const int rt = (a.R + 15) / 16;                      // rank tiles
+  float* part = reinterpret_cast<float*>(smem);        // [rt * 16][TT]: this CTA's sums
+  float* red = part + rt * 16 * TT;                    // [warps][kRows * 16][kRedStride]
+  uint16_t* us = reinterpret_cast<uint16_t*>(red);     // [kU][TT][rt * 16 + 8], after the sums
+  const int ustr = rt * 16 + 8;
+  const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + (int64_t)t.x * a.R * a.K;
+  const int chunks = (a.K + 31) / 32;
+  for (int r0 = 0; r0 < rt; r0 += kRows) {
+    for (int t0 = 0; t0 < TT && t0 < t.z; t0 += kCols * 8) {
+      const TS* rows[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; j++) {
+        const int i = t0 + j * 8 + g;
+        rows[j] = i < t.z ? reinterpret_cast<const TS*>(a.src) + (int64_t)order[i] * a.lds : nullptr;
+      }
+      float acc[kRows][kCols][4];
+#pragma unroll
+      for (int i = 0; i < kRows; i++)
+#pragma unroll
+        for (int j = 0; j < kCols; j++)
+#pragma unroll
+          for (int x = 0; x < 4; x++) acc[i][j][x] = 0.0f;
+      for (int ch = q * kWarps + warp; ch < chunks; ch += C * kWarps) {
+        const int k0 = ch * 32 + c * 8;
+        uint4 w[kRows][2];
+#pragma unroll
+        for (int i = 0; i < kRows; i++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const int r = (r0 + i) * 16 + h * 8 + g;
+            uint4 v[1];
+            load_eight<uint16_t>(w1 + (int64_t)r * a.K, k0, r < a.R ? a.K : 0, a.vk, v);
+            w[i][h] = v[0];
+          }
+#pragma unroll
+        for (int j = 0; j < kCols; j++) {
+          uint4 x[kParts];
+          load_eight<TS>(rows[j], k0, rows[j] ? a.K : 0, a.vk, x);
+#pragma unroll
+          for (int p = kParts - 1; p >= 0; p--)
+#pragma unroll
+            for (int i = 0; i < kRows; i++) {
+              mma_16x8x16(acc[i][j], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, x[p].x, x[p].y);
+              mma_16x8x16(acc[i][j], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[p].z, x[p].w);
+            }
+        }
+      }
+      float* mine = red + warp * kRows * 16 * kRedStride;
+#pragma unroll
+      for (int i = 0; i < kRows; i++)
+#pragma unroll
+        for (int j = 0; j < kCols; j++) {
+          float* d = mine + (i * 16 + g) * kRedStride + j * 8 + 2 * c;
+          *reinterpret_cast<float2*>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
+          *reinterpret_cast<float2*>(d + 8 * kRedStride) = make_float2(acc[i][j][2], acc[i][j][3]);
+        }
+      __syncthreads();
+      for (int e = threadIdx.x; e < kRows * 16 * kCols * 8; e += kWarps * 32) {
+        const int r = e / (kCols * 8), i = e % (kCols * 8);
+        if (r0 + r / 16 < rt) {
+          float v = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; w++) v += red[(w * kRows * 16 + r) * kRedStride + i];
+          part[(r0 * 16 + r) * TT + t0 + i] = v;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  cluster.sync();
+  for (int e = threadIdx.x; e < rt * 16 * TT; e += kWarps * 32) {
+    const int r = e / TT, i = e % TT;
+    float v = 0.0f;
+    if (i < t.z)
+      for (int o = 0; o < C; o++) v += cluster.map_shared_rank(part, o)[e];
+    uint16_t p[kU];
+    split_bf16<kU>(v, p);
+#pragma unroll
+    for (int x = 0; x < kU; x++) us[(x * TT + i) * ustr + r] = p[x];
+    if (a.u && q == 0 && i < t.z && r < a.R) a.u[(int64_t)order[i] * a.R + r] = v;
+  }
+  cluster.sync();  // (no CTA's sums are read after this)
+  const float scale = a.scale ? a.scale[t.x] : 1.0f;
+  const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
+  const int sub = (t.z + 15) / 16, items = (a.M + 63) / 64 * sub, all = C * kWarps;
+  const int per = (items + all - 1) / all, first = (q * kWarps + warp) * per, groups = (rt + KC - 1) / KC;
+  uint32_t b[KC][8][2];
+  int held = -1;
+  for (int it = first; it < min(first + per, items); it++) {
+    const int m0 = it / sub * 64, s0 = it % sub * 16;
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int x = 0; x < 4; x++) acc[i][x] = 0.0f;
+    for (int gr = 0; gr < groups; gr++) {
+      if (groups > 1 || held != m0) {
+        held = m0;
+#pragma unroll
+        for (int kc = 0; kc < KC; kc++) {
+          uint4 v[4][1];
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
+            load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, a.vm, v[x]);
+          }
+          pair_rows(v[0][0], v[1][0], v[2][0], v[3][0], b[kc]);
+        }
+      }
+#pragma unroll
+      for (int kc = 0; kc < KC; kc++) {
+        if (gr * KC + kc >= rt) break;
+#pragma unroll
+        for (int p = kU - 1; p >= 0; p--) {
+          const uint16_t* u0 = us + (p * TT + s0 + g) * ustr + (gr * KC + kc) * 16 + 2 * c;
+          const uint16_t* u1 = u0 + 8 * ustr;
+          const uint32_t a0 = *reinterpret_cast<const uint32_t*>(u0), a1 = *reinterpret_cast<const uint32_t*>(u1);
+          const uint32_t a2 = *reinterpret_cast<const uint32_t*>(u0 + 8), a3 = *reinterpret_cast<const uint32_t*>(u1 + 8);
+#pragma unroll
+          for (int i = 0; i < 8; i++) mma_16x8x16(acc[i], a0, a1, a2, a3, b[kc][i][0], b[kc][i][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int i = s0 + g + h * 8;
+      if (i >= t.z) continue;
+      const int64_t row = order[i];
+      const TO* br = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
+#pragma unroll
+      for (int s = 0; s < 2; s++) {
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; x++) v[x] = scale * acc[x][2 * h + s];
+        add_eight<TO>(br, reinterpret_cast<TO*>(a.out) + row * a.ldo, m0 + c * 16 + s * 8, a.M, a.vm, v);
+      }
+    }
+  }
+}
+
+template <int TT, int KC, typename TS, typename TO>
+cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
+  constexpr int kRows = TT == 64 ? (KC < 2 ? KC : 2) : KC, kCols = TT == 64 ? (sizeof(TS) == 4 ? 4 : 8) : TT / 8;
+  const int rt = (a.R + 15) / 16;
+  const int part = rt * 16 * TT * 4, red = kWarps * kRows * 16 * (kCols * 8 + 8) * 4;
+  const int us = OutParts<TO>::kParts * TT * (rt * 16 + 8) * 2;
+  const int bytes = part + std::max(red, us);
+  static std::atomic<int> done[kMaxCachedDevices];
+  constexpr int kMost = kLoraMaxRank * TT * 4 +
+                        (kWarps * kRows * 16 * (kCols * 8 + 8) * 4 > 3 * TT * (kLoraMaxRank + 8) * 2
+                             ? kWarps * kRows * 16 * (kCols * 8 + 8) * 4
+                             : 3 * TT * (kLoraMaxRank + 8) * 2);
+  cudaError_t e = smem_attr_once(k_lora_apply<TT, KC, TS, TO>, kMost, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = a.plan.max_tiles;
+  unsigned C = 8;
+  while (C > 1 && (tiles * C > 608 || (int64_t)C * kWarps > 2 * std::max((a.K + 31) / 32, (a.M + 63) / 64 * (TT / 16)))) C /= 2;
+  return launch_k_cluster(lc, k_lora_apply<TT, KC, TS, TO>, (unsigned)(tiles * C), kWarps * 32, (size_t)bytes, C, a);
+}
+template <int TT, typename TS, typename TO>
+cudaError_t by_rank(const LaunchCtx& lc, const LoraArgs& a) {
+  return a.R <= 16 ? run<TT, 1, TS, TO>(lc, a) : a.R <= 32 ? run<TT, 2, TS, TO>(lc, a) : run<TT, 4, TS, TO>(lc, a);
+}
+template <int TT>
+cudaError_t by_type(const LaunchCtx& lc, const LoraArgs& a) {
+  if (a.src_f32) return a.out_f32 ? by_rank<TT, float, float>(lc, a) : by_rank<TT, float, uint16_t>(lc, a);
+  return a.out_f32 ? by_rank<TT, uint16_t, float>(lc, a) : by_rank<TT, uint16_t, uint16_t>(lc, a);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a) {
+  return lora_tile(a.T) == 16 ? by_type<16>(lc, a) : by_type<64>(lc, a);
+}

@@ -328,6 +328,10 @@ class _Host:
         self.select, self.quantize, self.dequantize = L.afd_route_select, L.afd_mx4_quantize, L.afd_mx4_dequantize
         self.gemm, self.gemm_workspace = L.afd_mx4_gemm, L.afd_mx4_gemm_workspace
         self.ffn, self.ffn_workspace = L.afd_mx4_ffn, L.afd_mx4_ffn_workspace
+        self.balance, self.balance_workspace = L.afd_balance_loss, L.afd_balance_workspace
+        self.route_backward = L.afd_route_backward
+        self.lora_apply = L.afd_lora_apply
+        self.lora_backward, self.lora_backward_workspace = L.afd_lora_backward, L.afd_lora_backward_workspace
 
 
 _host = None
@@ -544,3 +548,196 @@ def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
     if rc:
         raise A.AfdError(rc, "afd_mx4_ffn")
     return out
+
+
+# ---- expert load, routing gradient, adapters on torch tensors --------------------
+def _gate_inputs(h, logits, ids, score, seq_offsets):
+    """(T, E, topk, dtype code, score code, row pitch, offsets' pointer, sequences)"""
+    code, kind = h.code.get(logits.dtype), _SCORES.get(score)
+    if code is None or kind is None or logits.dim() != 2:
+        _bad("logits: bf16 or fp32 rows [T, E] wanted, score softmax or sigmoid")
+    T, E = logits.shape
+    ld, step = logits.stride()
+    if T > _INT or not 0 < E <= 256 or (step != 1 and E > 1):
+        _bad("logits: rows of up to 256 neighbouring elements wanted")
+    topk = 1
+    if ids is not None:
+        if ids.dtype is not h.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+            _bad("ids: contiguous int32 [T, topk] wanted")
+        topk = ids.shape[1]
+    off, seqs = 0, 1
+    if seq_offsets is not None:
+        _rows_int32(h, seq_offsets, -1, "seq_offsets")
+        off, seqs = seq_offsets.data_ptr(), seq_offsets.shape[0] - 1
+    if not (0 < topk <= 16 and 0 < seqs <= 65535):
+        _bad("ids of 1 to 16 columns, 1 to 65535 sequences wanted")
+    if not logits.is_cuda:
+        _not_cuda()
+    return T, E, topk, code, kind, ld if T > 1 else E, off, seqs
+
+
+def balance_loss(logits, ids, score="softmax", seq_offsets=None, workspace=None):
+    """afd_balance_loss of the choice ids int32 [T, topk] on logits [T, E]:
+    (loss fp32 [S], counts int32 [S, E]); seq_offsets int32 [S + 1], or one
+    sequence of all rows."""
+    h = _host or _get()
+    if ids is None:
+        _bad("ids: contiguous int32 [T, topk] wanted")
+    T, E, topk, code, kind, ld, off, seqs = _gate_inputs(h, logits, ids, score, seq_offsets)
+    dev = logits.device
+    loss = h.empty((seqs,), dtype=h.f32, device=dev)
+    counts = h.empty((seqs, E), dtype=h.int32, device=dev)
+    ws, ws_bytes, keep = _scratch(h, workspace, h.balance_workspace(T, E, seqs), dev)
+    rc = h.balance(logits.data_ptr(), ld, T, code, ids.data_ptr(), E, topk, kind, off, seqs, loss.data_ptr(),
+                   counts.data_ptr(), ws, ws_bytes, h.raw_stream(dev.index))
+    if rc:
+        raise A.AfdError(rc, "afd_balance_loss")
+    return loss, counts
+
+
+def _rows_f32(h, t, shape, what):
+    if t.dtype is not h.f32 or t.shape != shape or not t.is_contiguous():
+        _bad(f"{what}: contiguous fp32 {list(shape)} wanted")
+    return t.data_ptr()
+
+
+def route_backward(logits, ids, d_weights=None, score="softmax", renorm=False, routed_scaling=1.0, counts=None,
+                   d_loss=None, seq_offsets=None, out=None):
+    """afd_route_backward: the gradient of logits [T, E] (in their dtype) from
+    that of route_select's weights (d_weights fp32 [T, topk]) and that of
+    balance_loss's loss (d_loss fp32 [S], with its counts); either may be
+    left out."""
+    h = _host or _get()
+    if ids is None and d_weights is not None:
+        _bad("d_weights without ids")
+    if (counts is None) != (d_loss is None):
+        _bad("counts and d_loss: both or neither")
+    T, E, topk, code, kind, ld, off, seqs = _gate_inputs(h, logits, ids, score, seq_offsets)
+    pw = pc = pl = 0
+    if d_weights is not None:
+        pw = _rows_f32(h, d_weights, (T, topk), "d_weights")
+    if d_loss is not None:
+        pl = _rows_f32(h, d_loss, (seqs,), "d_loss")
+        if counts.dtype is not h.int32 or counts.shape != (seqs, E) or not counts.is_contiguous():
+            _bad("counts: contiguous int32 [S, E] wanted")
+        pc = counts.data_ptr()
+    if ids is None:
+        topk = 1
+    dev = logits.device
+    if out is None:
+        out, ldd = h.empty((T, E), dtype=logits.dtype, device=dev), E
+    else:
+        if out.dtype is not logits.dtype or out.shape != (T, E) or (out.stride(1) != 1 and E > 1):
+            _bad("out: rows like logits' wanted")
+        ldd = out.stride(0) if T > 1 else E
+    rc = h.route_backward(logits.data_ptr(), ld, T, code, ids.data_ptr() if ids is not None else 0, E, topk, kind,
+                          1 if renorm else 0, routed_scaling, pw, off, seqs, pc, pl, out.data_ptr(), ldd,
+                          h.raw_stream(dev.index))
+    if rc:
+        raise A.AfdError(rc, "afd_route_backward")
+    return out
+
+
+class LoraBatch:
+    """Rows sorted by adapter (afd_lora_plan): ids int32 [T], -1 = none, of
+    `adapters` adapters.  Made once for a batch, for all its projections; ids
+    is not kept."""
+    __slots__ = ("plan", "rows", "adapters")
+
+    def __init__(self, ids, adapters):
+        h = _host or _get()
+        _rows_int32(h, ids, -1, "ids")
+        n = ids.shape[0]
+        if n > 1 << 24 or not 0 < adapters <= 1024:
+            _bad("up to 2^24 rows and 1 to 1024 adapters wanted")
+        if not ids.is_cuda:
+            _not_cuda()
+        dev = ids.device
+        nbytes = A.afd_lora_plan_bytes(n, adapters)
+        self.plan = h.empty(nbytes, dtype=h.uint8, device=dev)
+        self.rows, self.adapters = n, adapters
+        A._check(A.afd_lora_plan(ids.data_ptr(), n, adapters, self.plan.data_ptr(), nbytes,
+                                 h.raw_stream(dev.index)), "afd_lora_plan")
+
+
+def _lora_weights(h, batch, a, b):
+    """(rank, K, M)"""
+    if (a.dtype is not h.bf16 or b.dtype is not h.bf16 or a.dim() != 3 or b.dim() != 3 or a.shape[0] != batch.adapters
+            or b.shape[:2] != a.shape[:2] or not a.is_contiguous() or not b.is_contiguous()):
+        _bad("a, b: contiguous bf16 [adapters, rank, K] and [adapters, rank, M] wanted")
+    rank, K, M = a.shape[1], a.shape[2], b.shape[2]
+    if not (0 < rank <= 128 and 0 < K <= _DIM and 0 < M <= _DIM):
+        _bad("rank 1 to 128, K and M 1 to 65536 wanted")
+    return rank, K, M
+
+
+def _lora_rows(h, t, shape, what, dtype=None):
+    """(row pitch, dtype code) of rows of neighbouring elements"""
+    code = h.code.get(t.dtype)
+    if code is None or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1) or dtype not in (None, t.dtype):
+        _bad(f"{what}: rows {list(shape)} of bf16 or fp32 wanted, alike where they meet")
+    return t.stride(0) if shape[0] > 1 else shape[1], code
+
+
+def lora_apply(batch, x, a, b, base=None, scale=None, out=None, out_dtype=None, keep=False):
+    """afd_lora_apply of the rows x [T, K] of batch (LoraBatch) with adapters
+    a bf16 [L, rank, K] and b bf16 [L, rank, M]: base + scale[l] b[l]^T a[l] x
+    as [T, M].  base: the shared projection's rows or None (zeros); out may be
+    base.  keep: also u fp32 [T, rank] = a[l] x, for lora_backward."""
+    h = _host or _get()
+    rank, K, M = _lora_weights(h, batch, a, b)
+    T = batch.rows
+    ldx, xc = _lora_rows(h, x, (T, K), "x")
+    if not x.is_cuda:
+        _not_cuda()
+    dev = x.device
+    if out is None:
+        out = h.empty((T, M), dtype=out_dtype or (base.dtype if base is not None else x.dtype), device=dev)
+    ldo, yc = _lora_rows(h, out, (T, M), "out", out_dtype)
+    pb = ldb = 0
+    if base is not None:
+        ldb, _ = _lora_rows(h, base, (T, M), "base", out.dtype)
+        pb = base.data_ptr()
+    ps = _rows_f32(h, scale, (batch.adapters,), "scale") if scale is not None else 0
+    u = h.empty((T, rank), dtype=h.f32, device=dev) if keep else None
+    rc = h.lora_apply(batch.plan.data_ptr(), T, batch.adapters, x.data_ptr(), ldx, xc, K, a.data_ptr(), b.data_ptr(),
+                      rank, M, ps, pb, ldb, yc, out.data_ptr(), ldo, u.data_ptr() if keep else 0,
+                      h.raw_stream(dev.index))
+    if rc:
+        raise A.AfdError(rc, "afd_lora_apply")
+    return (out, u) if keep else out
+
+
+def lora_backward(batch, x, dy, u, a, b, d_base=None, scale=None, dx=None, da=None, db=None, workspace=None):
+    """afd_lora_backward: (dx like x, da fp32 like a, db fp32 like b) of dy
+    [T, M] and lora_apply's u; d_base [T, K]: the shared projection's own
+    gradient, or None (zeros); dx may be d_base."""
+    h = _host or _get()
+    rank, K, M = _lora_weights(h, batch, a, b)
+    T, L = batch.rows, batch.adapters
+    ldx, xc = _lora_rows(h, x, (T, K), "x")
+    ldy, yc = _lora_rows(h, dy, (T, M), "dy")
+    if not x.is_cuda:
+        _not_cuda()
+    dev = x.device
+    if dx is None:
+        dx = h.empty((T, K), dtype=x.dtype, device=dev)
+    ldd, _ = _lora_rows(h, dx, (T, K), "dx", x.dtype)
+    pb = ldb = 0
+    if d_base is not None:
+        ldb, _ = _lora_rows(h, d_base, (T, K), "d_base", x.dtype)
+        pb = d_base.data_ptr()
+    if da is None:
+        da = h.empty((L, rank, K), dtype=h.f32, device=dev)
+    if db is None:
+        db = h.empty((L, rank, M), dtype=h.f32, device=dev)
+    pda, pdb = _rows_f32(h, da, (L, rank, K), "da"), _rows_f32(h, db, (L, rank, M), "db")
+    pu = _rows_f32(h, u, (T, rank), "u")
+    ps = _rows_f32(h, scale, (L,), "scale") if scale is not None else 0
+    ws, ws_bytes, keep = _scratch(h, workspace, h.lora_backward_workspace(T, L, K, M, rank), dev)
+    rc = h.lora_backward(batch.plan.data_ptr(), T, L, x.data_ptr(), ldx, xc, K, dy.data_ptr(), ldy, yc, M, pu,
+                         a.data_ptr(), b.data_ptr(), rank, ps, pb, ldb, dx.data_ptr(), ldd, pda, pdb, ws, ws_bytes,
+                         h.raw_stream(dev.index))
+    if rc:
+        raise A.AfdError(rc, "afd_lora_backward")
+    return dx, da, db

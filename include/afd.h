@@ -765,6 +765,110 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
  * stream that polls, so that no caller takes another's. */
 int afd_mx4_poll_status(void* cuda_stream);
 
+/* ---- load of the experts, gradient of the routing choice --------------------
+ * What a gate that is trained needs next to afd_route_select: how many rows
+ * each expert got, how uneven that is, and the gradient of both the balance
+ * loss and the chosen weights.
+ *   logits, ld, n_tokens, logits_dtype, num_experts, topk, score: as
+ *            afd_route_select's
+ *   ids      device int32 [n_tokens, topk], as afd_route_select writes them;
+ *            entries outside [0, num_experts) are no choice.  One that stands
+ *            twice in a row counts twice
+ *   seq_offsets  device int32 [n_seqs + 1], ascending: sequence s is the rows
+ *            [seq_offsets[s], seq_offsets[s + 1]), clamped to [0, n_tokens];
+ *            NULL: one sequence of all rows (n_seqs 1).  n_seqs <= 65535
+ * With p_te the softmax of row t, or s_te / sum_e s_te of its sigmoids (0
+ * throughout a row whose logits are all -inf), n_s the rows of sequence s:
+ *   counts   device int32 [n_seqs, num_experts] out: the choices of e in s
+ *   loss     device fp32 [n_seqs] out: num_experts / (topk n_s^2) *
+ *            sum_e counts[s, e] * sum_{t in s} p_te: 1 for an even gate, 0
+ *            for a sequence without rows, NaN where a row of it has a NaN
+ * The sums do not depend on timing.  workspace: device, 256-byte aligned, at
+ * least afd_balance_workspace bytes (host only; 0 for few rows, -1 for sizes
+ * outside the limits), else AFD_ERR_CAPACITY; one call at a time may use it.
+ * Asynchronous on cuda_stream, allocates nothing, keeps nothing; may be
+ * captured.  Errors: AFD_ERR_ARG, AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA. */
+int64_t afd_balance_workspace(int n_tokens, int num_experts, int n_seqs);
+int afd_balance_loss(const void* logits, int64_t ld, int n_tokens, int logits_dtype,
+                     const int32_t* ids, int num_experts, int topk, int score,
+                     const int32_t* seq_offsets, int n_seqs, float* loss, int32_t* counts,
+                     void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
+/* d_logits [n_tokens, num_experts] of logits_dtype, row pitch ldd, written
+ * whole: the sum of two gradients, each left out where its inputs are NULL.
+ *   d_weights  device fp32 [n_tokens, topk]: the gradient with respect to the
+ *              weights that afd_route_select returned for these logits, ids,
+ *              score, renorm and routed_scaling (ids may be NULL without it)
+ *   counts, d_loss  both or neither: afd_balance_loss's counts and the
+ *              gradient with respect to its loss [n_seqs], with the same
+ *              seq_offsets; rows outside every sequence get none
+ * The counts and the choice are constants of the gradient.  A row with a NaN
+ * (or, under softmax, +inf) in its logits gets NaN throughout.  d_logits may
+ * be logits itself (same pitch).  Errors, capture: as afd_balance_loss. */
+int afd_route_backward(const void* logits, int64_t ld, int n_tokens, int logits_dtype,
+                       const int32_t* ids, int num_experts, int topk, int score, int renorm,
+                       float routed_scaling, const float* d_weights, const int32_t* seq_offsets,
+                       int n_seqs, const int32_t* counts, const float* d_loss, void* d_logits,
+                       int64_t ldd, void* cuda_stream);
+
+/* ---- low-rank adapters beside a shared projection ----------------------------
+ * The rows of a fan-in belong to many requests; each may bring an adapter of
+ * its own to a projection whose weight they share.  Beside that projection's
+ * product (base, of any origin: a gate's logits, afd_mx4_gemm's rows):
+ *   u_t = A[l] x_t,  out_t = base_t + scale[l] B[l]^T u_t,  l = ids[t]
+ * A bf16 [n_adapters, rank, K], B bf16 [n_adapters, rank, M], both rank-major
+ * and without padding (smaller adapters: zero rows); u is held in fp32 and
+ * enters the second product with 16 (out bf16) or 24 (fp32) bits; sums in
+ * fp32; out is rounded once.  A row with a NaN or an infinity in it, or an
+ * adapter with one, gives values that are not finite in its own rows only.
+ * Limits: n_tokens <= 2^24, n_adapters <= 1024, rank <= 128, K and M <= 65536.
+ *
+ * afd_lora_plan -- sorts the rows by adapter, once for all projections that
+ * the rows meet.  ids: device int32 [n_tokens]; an entry outside
+ * [0, n_adapters) is a row without an adapter.  plan: device, 256-byte
+ * aligned, at least afd_lora_plan_bytes (host only; -1 for sizes outside the
+ * limits), else AFD_ERR_CAPACITY; the calls that read it are given the same
+ * n_tokens and n_adapters, and any number of them may at a time. */
+int64_t afd_lora_plan_bytes(int64_t n_tokens, int n_adapters);
+int afd_lora_plan(const int32_t* ids, int64_t n_tokens, int n_adapters, void* plan,
+                  int64_t plan_bytes, void* cuda_stream);
+
+/*   x        device, x_dtype [n_tokens, K], row pitch ldx elements
+ *   scale    device fp32 [n_adapters], or NULL: 1
+ *   base     device, y_dtype [n_tokens, M], row pitch ldb: the shared
+ *            projection's rows; NULL: zeros; may be out itself (same pitch),
+ *            whose rows without an adapter are then left as they are
+ *   out      device, y_dtype [n_tokens, M], row pitch ldo
+ *   u        device fp32 [n_tokens, rank] out, or NULL: kept for
+ *            afd_lora_backward; 0 for rows without an adapter
+ * Any pitch and element alignment; rows of whole 16 bytes with K % 8 == 0 and
+ * M % 8 == 0 are moved 16 bytes at a time.  The calls are asynchronous on
+ * cuda_stream, allocate nothing, keep nothing, and may be captured.  Errors:
+ * AFD_ERR_ARG, AFD_ERR_NOT_DEVICE, AFD_ERR_CUDA; n_tokens == 0 does nothing. */
+int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters, const void* x, int64_t ldx,
+                   int x_dtype, int K, const void* A, const void* B, int rank, int M,
+                   const float* scale, const void* base, int64_t ldb, int y_dtype, void* out,
+                   int64_t ldo, float* u, void* cuda_stream);
+
+/* The gradients, with v_t = B[l] dy_t:
+ *   dx_t = d_base_t + scale[l] A[l]^T v_t     x_dtype [n_tokens, K], pitch ldd
+ *   dA[l] = scale[l] sum_t v_t x_t^T          fp32 [n_adapters, rank, K]
+ *   dB[l] = scale[l] sum_t u_t dy_t^T         fp32 [n_adapters, rank, M]
+ * dy: y_dtype [n_tokens, M], row pitch ldy; u: afd_lora_apply's; d_base: the
+ * shared projection's gradient, NULL or dx itself as base above.  dA and dB
+ * (16-byte aligned) are written whole, zeros for adapters without rows (also
+ * with n_tokens 0).  The sums' order does not depend on timing.  workspace:
+ * device, 256-byte aligned, at least afd_lora_backward_workspace bytes (host
+ * only; -1 outside the limits), else AFD_ERR_CAPACITY; one call at a time may
+ * use it. */
+int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank);
+int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const void* x,
+                      int64_t ldx, int x_dtype, int K, const void* dy, int64_t ldy, int y_dtype,
+                      int M, const float* u, const void* A, const void* B, int rank,
+                      const float* scale, const void* d_base, int64_t ldb, void* dx, int64_t ldd,
+                      float* dA, float* dB, void* workspace, int64_t workspace_bytes,
+                      void* cuda_stream);
+
 /* Static string for a status code. */
 const char* afd_strerror(int code);
 
