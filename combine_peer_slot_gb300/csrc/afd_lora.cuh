@@ -12,7 +12,7 @@ constexpr int64_t kLoraMaxTokens = int64_t(1) << 24;
 // Rows of one adapter that a tile of the products holds, and rows of one
 // piece of the weight gradients' sums.
 __host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
-__host__ __device__ inline int lora_piece(int64_t) { return 512; }
+__host__ __device__ inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : 1024; }
 
 // The plan, made on the device from the rows' adapter ids: the rows in adapter
 // order (stable; rows without an adapter last), cut into tiles of one adapter.
@@ -66,7 +66,8 @@ struct LoraArgs {
   int64_t T;
   int K, M, R;
   int src_f32, out_f32;
-  int vk, vm;          // rows of src and w1 / of base, out and w2 move 16 bytes at a time
+  // how rows can be moved: 2 = 16 bytes at a time, 1 = 4, 0 = by elements
+  int how_src, how_w1, how_w2, how_base, how_out;
 };
 // da[l] = scale[l] sum v_t x_t^T, db[l] = scale[l] sum u_t dy_t^T
 struct LoraWgradArgs {
@@ -78,12 +79,13 @@ struct LoraWgradArgs {
   float* part[2];      // [slots][R][N]
   int N[2];
   int f32[2];
-  int vec[2];
+  int how[2];          // as LoraArgs::how_src
   const float* scale;
   int64_t T;
   int R, L;
 };
-cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);
+cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 16
+cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 64
 cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
 
 #ifdef __CUDACC__
@@ -121,12 +123,30 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&p)[PARTS]) {
   }
 }
 
+// two neighbouring fp32 values to packed bf16 parts
+template <int PARTS>
+__device__ __forceinline__ void split_pair(float2 v, uint32_t (&p)[PARTS]) {
+  uint16_t a[PARTS], b[PARTS];
+  split_bf16<PARTS>(v.x, a);
+  split_bf16<PARTS>(v.y, b);
+#pragma unroll
+  for (int i = 0; i < PARTS; i++) p[i] = (uint32_t)a[i] | (uint32_t)b[i] << 16;
+}
+
 template <typename T>
 struct LoraSrc;
 template <>
 struct LoraSrc<uint16_t> { static constexpr int kParts = 1; };
 template <>
 struct LoraSrc<float> { static constexpr int kParts = 3; };
+
+// parts of u beside an output of this type
+template <typename TO>
+struct OutParts;
+template <>
+struct OutParts<uint16_t> { static constexpr int kParts = 2; };
+template <>
+struct OutParts<float> { static constexpr int kParts = 3; };
 
 // Eight neighbouring values of a row from column c0 as packed bf16 parts;
 // columns from n on are zero.  vec: rows are 16-byte aligned and n % 8 == 0.
@@ -184,4 +204,57 @@ __device__ __forceinline__ void pair_rows(const uint4& r0, const uint4& r1, cons
     b[2 * j + 1][1] = __byte_perm(x2[j], x3[j], 0x7632);
   }
 }
+
+// ---- tiles in shared memory: rows of 128 bytes ----
+constexpr int kLoraRowBytes = 128;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// 16-byte chunk c of row r of a tile: chunks are swapped within a row so that
+// eight rows' same chunk lie in different banks
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
+  return tile + r * kLoraRowBytes + ((c ^ (r & 7)) << 4);
+}
+
+// One chunk of a row from element c0 (n in the row; NULL: no row), zeros past
+// its end.  how: 2 = 16 bytes at a time, 1 = 4 (even sizes), 0 = elements,
+// through registers.
+template <typename T>
+__device__ __forceinline__ void load_chunk(uint32_t dst, const T* row, int c0, int n, int how, const void* any) {
+  constexpr int E = 16 / (int)sizeof(T);
+  if (how == 2) {
+    const bool in = row && c0 < n;
+    copy16(dst, in ? (const void*)(row + c0) : any, in);
+  } else if (how == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int c = c0 + i * (E / 4);
+      const bool in = row && c < n;
+      copy4(dst + 4 * i, in ? (const void*)(row + c) : any, in);
+    }
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (row)
+#pragma unroll
+      for (int i = 0; i < E; i++)
+        if (c0 + i < n) w[i * (int)sizeof(T) / 4] |= (uint32_t)(*reinterpret_cast<const uint16_t*>(row + c0 + i)) << (i % 2 * 16);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+  }
+}
+
 #endif

@@ -2,8 +2,8 @@
 //   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
 // forward with (x, A, B), backward with (dy, B, A).
 //
-// A cluster takes a tile of one adapter's rows (16 or 64, gathered by the
-// plan's order).  First its warps share the columns of src in chunks of 32,
+// for batches of few rows (afd_lora_tiles.cu has the form for many).  A cluster
+// takes a tile of up to 16 rows of one adapter, gathered by the plan's order.  First its warps share the columns of src in chunks of 32,
 // each lane loading its operands of the tensor cores' products straight from
 // global memory: the k order inside a chunk is free as long as both operands
 // agree, so a lane takes 16 neighbouring bytes for its four k pairs.  The
@@ -18,14 +18,7 @@
 namespace {
 
 namespace cg = cooperative_groups;
-constexpr int kWarps = 8;
-
-template <typename TO>
-struct OutParts;
-template <>
-struct OutParts<uint16_t> { static constexpr int kParts = 2; };
-template <>
-struct OutParts<float> { static constexpr int kParts = 3; };
+constexpr int kWarps = 8, TT = 16, kRedStride = TT + 8;
 
 // eight neighbouring outputs: base + v, rounded once
 template <typename TO>
@@ -68,12 +61,13 @@ __device__ __forceinline__ void add_eight(const void* base, TO* out, int c0, int
   }
 }
 
-template <int TT, int KC, typename TS, typename TO>
+template <int KC, typename TS, typename TO>
 __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constant__ LoraArgs a) {
   constexpr int kParts = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
-  constexpr int kRows = TT == 64 ? (KC < 2 ? KC : 2) : KC;       // rank tiles of a pass
-  constexpr int kCols = TT == 64 ? (sizeof(TS) == 4 ? 4 : 8) : TT / 8;  // token tiles of a pass
-  constexpr int kRedStride = kCols * 8 + 8;
+  constexpr int kRows = KC;                 // rank tiles of a pass
+  constexpr int kCols = TT / 8;             // row tiles
+  const bool vk = a.how_src == 2 && a.how_w1 == 2;
+  const bool vm = a.how_w2 == 2 && a.how_out == 2 && (!a.base || a.how_base == 2);
   extern __shared__ __align__(16) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), q = (int)cluster.block_rank();
@@ -90,7 +84,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
         const float zero[8] = {};
         const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
         for (int c0 = (q * 32 + lane) * 8; c0 < a.M; c0 += C * 256)
-          add_eight<TO>(b, reinterpret_cast<TO*>(a.out) + row * a.ldo, c0, a.M, a.vm, zero);
+          add_eight<TO>(b, reinterpret_cast<TO*>(a.out) + row * a.ldo, c0, a.M, vm, zero);
       }
       if (a.u && q == 0)
         for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
@@ -104,67 +98,65 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   const int ustr = rt * 16 + 8;
   const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + (int64_t)t.x * a.R * a.K;
   const int chunks = (a.K + 31) / 32;
+  const TS* rows[kCols];
+#pragma unroll
+  for (int j = 0; j < kCols; j++) {
+    const int i = j * 8 + g;
+    rows[j] = i < t.z ? reinterpret_cast<const TS*>(a.src) + (int64_t)order[i] * a.lds : nullptr;
+  }
   for (int r0 = 0; r0 < rt; r0 += kRows) {
-    for (int t0 = 0; t0 < TT && t0 < t.z; t0 += kCols * 8) {
-      const TS* rows[kCols];
+    float acc[kRows][kCols][4];
+#pragma unroll
+    for (int i = 0; i < kRows; i++)
+#pragma unroll
+      for (int j = 0; j < kCols; j++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) acc[i][j][x] = 0.0f;
+    for (int ch = q * kWarps + warp; ch < chunks; ch += C * kWarps) {
+      const int k0 = ch * 32 + c * 8;
+      uint4 w[kRows][2];
+#pragma unroll
+      for (int i = 0; i < kRows; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int r = (r0 + i) * 16 + h * 8 + g;
+          uint4 v[1];
+          load_eight<uint16_t>(w1 + (int64_t)r * a.K, k0, r < a.R ? a.K : 0, vk, v);
+          w[i][h] = v[0];
+        }
 #pragma unroll
       for (int j = 0; j < kCols; j++) {
-        const int i = t0 + j * 8 + g;
-        rows[j] = i < t.z ? reinterpret_cast<const TS*>(a.src) + (int64_t)order[i] * a.lds : nullptr;
-      }
-      float acc[kRows][kCols][4];
+        uint4 x[kParts];
+        load_eight<TS>(rows[j], k0, rows[j] ? a.K : 0, vk, x);
 #pragma unroll
-      for (int i = 0; i < kRows; i++)
+        for (int p = kParts - 1; p >= 0; p--)
 #pragma unroll
-        for (int j = 0; j < kCols; j++)
-#pragma unroll
-          for (int x = 0; x < 4; x++) acc[i][j][x] = 0.0f;
-      for (int ch = q * kWarps + warp; ch < chunks; ch += C * kWarps) {
-        const int k0 = ch * 32 + c * 8;
-        uint4 w[kRows][2];
-#pragma unroll
-        for (int i = 0; i < kRows; i++)
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const int r = (r0 + i) * 16 + h * 8 + g;
-            uint4 v[1];
-            load_eight<uint16_t>(w1 + (int64_t)r * a.K, k0, r < a.R ? a.K : 0, a.vk, v);
-            w[i][h] = v[0];
+          for (int i = 0; i < kRows; i++) {
+            mma_16x8x16(acc[i][j], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, x[p].x, x[p].y);
+            mma_16x8x16(acc[i][j], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[p].z, x[p].w);
           }
-#pragma unroll
-        for (int j = 0; j < kCols; j++) {
-          uint4 x[kParts];
-          load_eight<TS>(rows[j], k0, rows[j] ? a.K : 0, a.vk, x);
-#pragma unroll
-          for (int p = kParts - 1; p >= 0; p--)
-#pragma unroll
-            for (int i = 0; i < kRows; i++) {
-              mma_16x8x16(acc[i][j], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, x[p].x, x[p].y);
-              mma_16x8x16(acc[i][j], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[p].z, x[p].w);
-            }
-        }
       }
-      float* mine = red + warp * kRows * 16 * kRedStride;
-#pragma unroll
-      for (int i = 0; i < kRows; i++)
-#pragma unroll
-        for (int j = 0; j < kCols; j++) {
-          float* d = mine + (i * 16 + g) * kRedStride + j * 8 + 2 * c;
-          *reinterpret_cast<float2*>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
-          *reinterpret_cast<float2*>(d + 8 * kRedStride) = make_float2(acc[i][j][2], acc[i][j][3]);
-        }
-      __syncthreads();
-      for (int e = threadIdx.x; e < kRows * 16 * kCols * 8; e += kWarps * 32) {
-        const int r = e / (kCols * 8), i = e % (kCols * 8);
-        if (r0 + r / 16 < rt) {
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; w++) v += red[(w * kRows * 16 + r) * kRedStride + i];
-          part[(r0 * 16 + r) * TT + t0 + i] = v;
-        }
-      }
-      __syncthreads();
     }
+    float* mine = red + warp * kRows * 16 * kRedStride;
+#pragma unroll
+    for (int i = 0; i < kRows; i++)
+#pragma unroll
+      for (int j = 0; j < kCols; j++) {
+        float* d = mine + (i * 16 + g) * kRedStride + j * 8 + 2 * c;
+        *reinterpret_cast<float2*>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
+        *reinterpret_cast<float2*>(d + 8 * kRedStride) = make_float2(acc[i][j][2], acc[i][j][3]);
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRows * 16 * kCols * 8; e += kWarps * 32) {
+      const int r = e / (kCols * 8), i = e % (kCols * 8);
+      if (r0 + r / 16 < rt) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) v += red[(w * kRows * 16 + r) * kRedStride + i];
+        part[(r0 * 16 + r) * TT + i] = v;
+      }
+    }
+    __syncthreads();
   }
   cluster.sync();
   for (int e = threadIdx.x; e < rt * 16 * TT; e += kWarps * 32) {
@@ -201,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
 #pragma unroll
           for (int x = 0; x < 4; x++) {
             const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
-            load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, a.vm, v[x]);
+            load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, vm, v[x]);
           }
           pair_rows(v[0][0], v[1][0], v[2][0], v[3][0], b[kc]);
         }
@@ -231,43 +223,34 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
         float v[8];
 #pragma unroll
         for (int x = 0; x < 8; x++) v[x] = scale * acc[x][2 * h + s];
-        add_eight<TO>(br, reinterpret_cast<TO*>(a.out) + row * a.ldo, m0 + c * 16 + s * 8, a.M, a.vm, v);
+        add_eight<TO>(br, reinterpret_cast<TO*>(a.out) + row * a.ldo, m0 + c * 16 + s * 8, a.M, vm, v);
       }
     }
   }
 }
 
-template <int TT, int KC, typename TS, typename TO>
+template <int KC, typename TS, typename TO>
 cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
-  constexpr int kRows = TT == 64 ? (KC < 2 ? KC : 2) : KC, kCols = TT == 64 ? (sizeof(TS) == 4 ? 4 : 8) : TT / 8;
   const int rt = (a.R + 15) / 16;
-  const int part = rt * 16 * TT * 4, red = kWarps * kRows * 16 * (kCols * 8 + 8) * 4;
-  const int us = OutParts<TO>::kParts * TT * (rt * 16 + 8) * 2;
-  const int bytes = part + std::max(red, us);
+  constexpr int kRed = kWarps * KC * 16 * kRedStride * 4;
+  const int bytes = rt * 16 * TT * 4 + std::max(kRed, OutParts<TO>::kParts * TT * (rt * 16 + 8) * 2);
+  constexpr int kU = OutParts<TO>::kParts * TT * (kLoraMaxRank + 8) * 2;
   static std::atomic<int> done[kMaxCachedDevices];
-  constexpr int kMost = kLoraMaxRank * TT * 4 +
-                        (kWarps * kRows * 16 * (kCols * 8 + 8) * 4 > 3 * TT * (kLoraMaxRank + 8) * 2
-                             ? kWarps * kRows * 16 * (kCols * 8 + 8) * 4
-                             : 3 * TT * (kLoraMaxRank + 8) * 2);
-  cudaError_t e = smem_attr_once(k_lora_apply<TT, KC, TS, TO>, kMost, done);
+  cudaError_t e = smem_attr_once(k_lora_apply<KC, TS, TO>, kLoraMaxRank * TT * 4 + (kRed > kU ? kRed : kU), done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.plan.max_tiles;
   unsigned C = 8;
-  while (C > 1 && (tiles * C > 608 || (int64_t)C * kWarps > 2 * std::max((a.K + 31) / 32, (a.M + 63) / 64 * (TT / 16)))) C /= 2;
-  return launch_k_cluster(lc, k_lora_apply<TT, KC, TS, TO>, (unsigned)(tiles * C), kWarps * 32, (size_t)bytes, C, a);
+  while (C > 1 && (tiles * C > 608 || (int64_t)C * kWarps > 2 * std::max((a.K + 31) / 32, (a.M + 63) / 64))) C /= 2;
+  return launch_k_cluster(lc, k_lora_apply<KC, TS, TO>, (unsigned)(tiles * C), kWarps * 32, (size_t)bytes, C, a);
 }
-template <int TT, typename TS, typename TO>
+template <typename TS, typename TO>
 cudaError_t by_rank(const LaunchCtx& lc, const LoraArgs& a) {
-  return a.R <= 16 ? run<TT, 1, TS, TO>(lc, a) : a.R <= 32 ? run<TT, 2, TS, TO>(lc, a) : run<TT, 4, TS, TO>(lc, a);
-}
-template <int TT>
-cudaError_t by_type(const LaunchCtx& lc, const LoraArgs& a) {
-  if (a.src_f32) return a.out_f32 ? by_rank<TT, float, float>(lc, a) : by_rank<TT, float, uint16_t>(lc, a);
-  return a.out_f32 ? by_rank<TT, uint16_t, float>(lc, a) : by_rank<TT, uint16_t, uint16_t>(lc, a);
+  return a.R <= 16 ? run<1, TS, TO>(lc, a) : a.R <= 32 ? run<2, TS, TO>(lc, a) : run<4, TS, TO>(lc, a);
 }
 
 }  // namespace
 
 cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a) {
-  return lora_tile(a.T) == 16 ? by_type<16>(lc, a) : by_type<64>(lc, a);
+  if (a.src_f32) return a.out_f32 ? by_rank<float, float>(lc, a) : by_rank<float, uint16_t>(lc, a);
+  return a.out_f32 ? by_rank<uint16_t, float>(lc, a) : by_rank<uint16_t, uint16_t>(lc, a);
 }

@@ -1,0 +1,323 @@
+// afd_lora_tiles.cu -- both products of the adapters for batches of many rows
+// (tiles of 64; afd_lora_apply.cu has the form for few):
+//   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
+//
+// Bound by memory: src and base in, out out, at rank operations a byte.  So
+// everything that comes from memory goes through one ring of shared memory
+// stages filled by asynchronous copies, several stages ahead and from the
+// first product's last ones straight into the second's first: a stage is 128
+// bytes of each of the tile's 64 rows (of src, then of base) and the weight's
+// matching columns.  The second product adds into base's stage where it lies,
+// and each warp stores its 16 rows' 64 bytes whole.  Copies gather rows by
+// the plan's order, so no row is moved beforehand.
+//
+// A cluster of C CTAs splits src's columns for the first product (the sums
+// meet through distributed shared memory, in order) and out's for the second.
+// The tensor cores' fp32 sums cut where they should round, so every four
+// stages the sums move to registers that add with rounding.
+#include <cooperative_groups.h>
+
+#include "afd_lora.cuh"
+
+namespace {
+
+namespace cg = cooperative_groups;
+constexpr int TT = 64;
+constexpr int kThreads = 256;
+constexpr int kRowBytes = kLoraRowBytes;      // of a stage's row, of either operand
+constexpr int kTileBytes = TT * kRowBytes;
+constexpr int kFlush = 4;                     // stages between two moves of the sums
+
+// stages, and CTAs an SM holds
+template <int KC>
+struct Form {
+  static constexpr int kStages = KC == 1 ? 6 : KC == 2 ? 5 : KC == 4 ? 3 : 4;
+  static constexpr int kCtas = KC <= 4 ? 3 : 1;
+  static constexpr int kStageBytes = kTileBytes + KC * 16 * kRowBytes;
+  static constexpr int kUStride = KC * 16 + 4;
+  static constexpr int kBytes = kStages * kStageBytes + TT * kUStride * 4;
+};
+
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+template <int KC, typename TS, typename TO>
+__global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const __grid_constant__ LoraArgs a) {
+  typedef Form<KC> F;
+  constexpr int kS = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts, S = F::kStages;
+  constexpr int KB = kRowBytes / (int)sizeof(TS), CB = kRowBytes / (int)sizeof(TO);  // columns of a stage
+  constexpr int NT = CB / 16;                                                          // a warp's column tiles
+  constexpr bool kHold = KC * kU <= 8;                                                 // u's operands stay in registers
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int32_t rows[TT];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), q = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int wt = warp & 3, half = warp >> 2;  // 16 rows; first product: half of the ranks, second: of the columns
+  const int4 head = *a.plan.head;
+  const int64_t tile = blockIdx.x / C;
+  if (tile >= head.x + head.y) return;
+  const int4 t = a.plan.tiles[tile];
+  if (tid < TT) rows[tid] = tid < t.z ? a.plan.order[t.y + tid] : -1;
+  __syncthreads();
+  if (t.x < 0) {  // rows without an adapter: out = base
+    for (int i = warp; i < t.z; i += kThreads / 32) {
+      const int64_t row = rows[i];
+      if (a.base != a.out) {
+        const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
+        TO* o = reinterpret_cast<TO*>(a.out) + row * a.ldo;
+        if (a.how_out == 2 && (!b || a.how_base == 2)) {
+          for (int c0 = (q * 32 + lane) * (CB / 8); c0 < a.M; c0 += C * 32 * (CB / 8))
+            *reinterpret_cast<uint4*>(o + c0) = b ? *reinterpret_cast<const uint4*>(b + c0) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          for (int c0 = q * 32 + lane; c0 < a.M; c0 += C * 32) o[c0] = b ? b[c0] : (TO)0;
+        }
+      }
+      if (a.u && q == 0)
+        for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
+    }
+    return;
+  }
+  const uint32_t ring = smem_u32(smem);
+  float* part = reinterpret_cast<float*>(smem + S * F::kStageBytes);  // [TT][kUStride]
+  const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + (int64_t)t.x * a.R * a.K;
+  const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
+  const int all1 = (a.K + KB - 1) / KB, all2 = (a.M + CB - 1) / CB;
+  const int k0 = all1 * q / C, n1 = all1 * (q + 1) / C - k0, m0 = all2 * q / C, n2 = all2 * (q + 1) / C - m0;
+  const int n = n1 + n2;
+  // this thread's chunk of rows tid / 8 and tid / 8 + 32 of a tile
+  const int ch = tid & 7, r0 = tid >> 3;
+  const int64_t row0 = rows[r0], row1 = rows[r0 + 32];
+
+  auto fill = [&](int i) {
+    if (i < n) {
+      const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
+      if (i < n1) {
+        const int c0 = (k0 + i) * KB;
+        const TS* s = reinterpret_cast<const TS*>(a.src);
+        load_chunk<TS>(chunk_at(st, r0, ch), row0 >= 0 ? s + row0 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
+        load_chunk<TS>(chunk_at(st, r0 + 32, ch), row1 >= 0 ? s + row1 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
+        for (int e = tid; e < KC * 16 * (KB / 8); e += kThreads) {
+          const int r = e / (KB / 8), cc = e % (KB / 8);
+          load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w1 + (int64_t)r * a.K : nullptr, c0 + cc * 8, a.K, a.how_w1, a.plan.head);
+        }
+      } else {
+        const int c0 = (m0 + i - n1) * CB;
+        const TO* b = reinterpret_cast<const TO*>(a.base);
+        load_chunk<TO>(chunk_at(st, r0, ch), b && row0 >= 0 ? b + row0 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+        load_chunk<TO>(chunk_at(st, r0 + 32, ch), b && row1 >= 0 ? b + row1 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+        for (int e = tid; e < KC * 16 * (CB / 8); e += kThreads) {
+          const int r = e / (CB / 8), cc = e % (CB / 8);
+          load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w2 + (int64_t)r * a.M : nullptr, c0 + cc * 8, a.M, a.how_w2, a.plan.head);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto ready = [&]() {  // the oldest stage is here, for all threads; the one before it is free
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    __syncthreads();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; i++) fill(i);
+
+  // ---- u: the warp's 16 rows x KC * 8 ranks ----
+  float acc[KC][4], sum[KC][4];
+#pragma unroll
+  for (int i = 0; i < KC; i++)
+#pragma unroll
+    for (int x = 0; x < 4; x++) acc[i][x] = sum[i][x] = 0.0f;
+  for (int i = 0; i < n1; i++) {
+    ready();
+    fill(i + S - 1);
+    const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
+#pragma unroll
+    for (int ks = 0; ks < KB / 16; ks++) {
+      uint32_t x[kS][4];
+      if (kS == 1) {
+        ldsm4(chunk_at(st, wt * 16 + (lane & 15), ks * 2 + (lane >> 4)), x[0]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int col = ks * 16 + 2 * c + (j >> 1) * 8;
+          uint32_t p[kS];
+          split_pair<kS>(lds_f2(chunk_at(st, wt * 16 + g + (j & 1) * 8, col >> 2) + (col & 3) * 4), p);
+#pragma unroll
+          for (int y = 0; y < kS; y++) x[y][j] = p[y];
+        }
+      }
+      if (KC == 1) {
+        uint32_t b0, b1;
+        ldsm2(chunk_at(wst, half * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), b0, b1);
+#pragma unroll
+        for (int y = kS - 1; y >= 0; y--) mma_16x8x16(acc[0], x[y][0], x[y][1], x[y][2], x[y][3], b0, b1);
+      } else {
+#pragma unroll
+        for (int j = 0; j < KC / 2; j++) {
+          uint32_t b[4];
+          ldsm4(chunk_at(wst, half * KC * 8 + j * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), b);
+#pragma unroll
+          for (int y = kS - 1; y >= 0; y--) {
+            mma_16x8x16(acc[2 * j], x[y][0], x[y][1], x[y][2], x[y][3], b[0], b[1]);
+            mma_16x8x16(acc[(2 * j + 1) % KC], x[y][0], x[y][1], x[y][2], x[y][3], b[2], b[3]);
+          }
+        }
+      }
+    }
+    if (i % kFlush == kFlush - 1) {
+#pragma unroll
+      for (int j = 0; j < KC; j++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          sum[j][x] += acc[j][x];
+          acc[j][x] = 0.0f;
+        }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < KC; j++) {
+    float* d = part + (wt * 16 + g) * F::kUStride + (half * KC + j) * 8 + 2 * c;
+    *reinterpret_cast<float2*>(d) = make_float2(sum[j][0] + acc[j][0], sum[j][1] + acc[j][1]);
+    *reinterpret_cast<float2*>(d + 8 * F::kUStride) = make_float2(sum[j][2] + acc[j][2], sum[j][3] + acc[j][3]);
+  }
+  if (C > 1) {
+    // each thread the sums over the CTAs of its values, held until every CTA has read
+    constexpr int kMine = TT * KC * 16 / kThreads;
+    float v[kMine];
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int e = tid + i * kThreads, at = e / (KC * 16) * F::kUStride + e % (KC * 16);
+      v[i] = 0.0f;
+      for (int o = 0; o < C; o++) v[i] += cluster.map_shared_rank(part, o)[at];
+    }
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int e = tid + i * kThreads;
+      part[e / (KC * 16) * F::kUStride + e % (KC * 16)] = v[i];
+    }
+  }
+  __syncthreads();
+  if (a.u && q == 0) {
+    for (int e = tid; e < TT * KC * 16; e += kThreads) {
+      const int i = e / (KC * 16), r = e % (KC * 16);
+      if (i < t.z && r < a.R) a.u[(int64_t)rows[i] * a.R + r] = part[i * F::kUStride + r];
+    }
+  }
+  // ---- out: the warp's 16 rows x CB / 2 columns of each block ----
+  const float scale = a.scale ? a.scale[t.x] : 1.0f;
+  auto operand = [&](int ks, uint32_t (&p)[kU][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint32_t w[kU];
+      split_pair<kU>(*reinterpret_cast<const float2*>(part + (wt * 16 + g + (j & 1) * 8) * F::kUStride + ks * 16 + 2 * c + (j >> 1) * 8), w);
+#pragma unroll
+      for (int y = 0; y < kU; y++) p[y][j] = w[y];
+    }
+  };
+  uint32_t held[kHold ? KC : 1][kU][4];
+  if (kHold)
+#pragma unroll
+    for (int ks = 0; ks < KC; ks++) operand(ks, held[kHold ? ks : 0]);
+  const int steps = (a.R + 15) / 16;
+  for (int i = n1; i < n; i++) {
+    ready();
+    fill(i + S - 1);
+    const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
+    float d[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int x = 0; x < 4; x++) d[j][x] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KC; ks++) {
+      if (ks >= steps) break;
+      if (!kHold) operand(ks, held[0]);
+      uint32_t(&u)[kU][4] = held[kHold ? ks : 0];
+#pragma unroll
+      for (int j = 0; j < NT / 2; j++) {
+        uint32_t b[4];
+        ldsm4t(chunk_at(wst, ks * 16 + (lane & 15), half * NT + 2 * j + (lane >> 4)), b);
+#pragma unroll
+        for (int y = kU - 1; y >= 0; y--) {
+          mma_16x8x16(d[2 * j], u[y][0], u[y][1], u[y][2], u[y][3], b[0], b[1]);
+          mma_16x8x16(d[2 * j + 1], u[y][0], u[y][1], u[y][2], u[y][3], b[2], b[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int r = wt * 16 + g + h * 8;
+        if (sizeof(TO) == 2) {
+          const uint32_t at = chunk_at(st, r, half * NT + j) + 4 * c;
+          uint32_t w;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+          const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(w << 16) + scale * d[j][2 * h],
+                                                         __uint_as_float(w & 0xffff0000u) + scale * d[j][2 * h + 1]);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&v)) : "memory");
+        } else {
+          const int col = (half * NT + j) * 8 + 2 * c;
+          const uint32_t at = chunk_at(st, r, col >> 2) + (col & 3) * 4;
+          const float2 w = lds_f2(at);
+          sts_f2(at, w.x + scale * d[j][2 * h], w.y + scale * d[j][2 * h + 1]);
+        }
+      }
+    __syncwarp();
+    const int c0 = (m0 + i - n1) * CB;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int r = wt * 16 + h * 8 + g, cc = half * 4 + c, col = c0 + cc * (CB / 8);
+      const int64_t row = rows[r];
+      if (row >= 0 && col < a.M) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(chunk_at(st, r, cc)) : "memory");
+        TO* o = reinterpret_cast<TO*>(a.out) + row * a.ldo + col;
+        if (a.how_out == 2) {
+          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (sizeof(TO) == 2) {
+#pragma unroll
+          for (int x = 0; x < 8; x++)
+            if (col + x < a.M) reinterpret_cast<uint16_t*>(o)[x] = (uint16_t)(w[x / 2] >> (x % 2 * 16));
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+            if (col + x < a.M) reinterpret_cast<uint32_t*>(o)[x] = w[x];
+        }
+      }
+    }
+  }
+}
+
+template <int KC, typename TS, typename TO>
+cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
+  typedef Form<KC> F;
+  static std::atomic<int> done[kMaxCachedDevices];
+  cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO>, F::kBytes, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = a.plan.max_tiles;
+  unsigned C = 8;
+  while (C > 1 && tiles * C > 152 * F::kCtas) C /= 2;
+  return launch_k_cluster(lc, k_lora_tiles<KC, TS, TO>, (unsigned)(tiles * C), kThreads, (size_t)F::kBytes, C, a);
+}
+template <typename TS, typename TO>
+cudaError_t by_rank(const LaunchCtx& lc, const LoraArgs& a) {
+  return a.R <= 16 ? run<1, TS, TO>(lc, a) : a.R <= 32 ? run<2, TS, TO>(lc, a)
+       : a.R <= 64 ? run<4, TS, TO>(lc, a) : run<8, TS, TO>(lc, a);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a) {
+  if (a.src_f32) return a.out_f32 ? by_rank<float, float>(lc, a) : by_rank<float, uint16_t>(lc, a);
+  return a.out_f32 ? by_rank<uint16_t, float>(lc, a) : by_rank<uint16_t, uint16_t>(lc, a);
+}

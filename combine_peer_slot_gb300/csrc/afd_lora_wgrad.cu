@@ -1,0 +1,266 @@
+// afd_lora_wgrad.cu -- the adapters' weight gradients:
+//   da[l] = scale[l] sum_t v_t x_t^T,  db[l] = scale[l] sum_t u_t dy_t^T
+// over the rows t of adapter l: [rank x columns] sums of outer products.
+//
+// A CTA takes one piece of an adapter's rows and a slab of columns of x or dy.
+// Rows stream through a ring of shared memory stages of 32, gathered by
+// asynchronous copies; u or v (fp32) is split once a stage into three bf16
+// parts, so that the products on the tensor cores keep its 24 bits.  A warp
+// holds 16 ranks x 64 columns.  The tensor cores' fp32 sums cut where they
+// should round, so every other stage they move to registers that add with
+// rounding.  Adapters of several pieces leave partial sums, added in order by
+// a second kernel, which also clears the gradients of adapters without rows.
+#include "afd_lora.cuh"
+
+namespace {
+
+constexpr int kRows = 32;  // of a stage
+
+// rank groups of 16 x column groups of 64: one warp each
+template <int RG>
+struct Wg {
+  static constexpr int kCg = RG == 1 ? 8 : RG <= 4 ? 4 : 2;
+  static constexpr int kThreads = RG * kCg * 32;
+  static constexpr int kSlab = kCg * 64;
+  static constexpr int kStageBytes = kRows * kSlab * 2;
+  static constexpr int kStages = RG == 1 ? 3 : 6;
+  static constexpr int kPStride = RG * 16 + 8;                 // bf16 of a row's parts
+  static constexpr int kPartBytes = 3 * kRows * kPStride * 2;  // one stage's
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kBytes = kRing + 2 * kPartBytes;
+  static constexpr int kCtas = kThreads == 256 ? 2 : 1;
+};
+constexpr int kMaxPiece = 1024;
+
+template <int RG>
+__device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, const int4& pc, int rg, int m0, int lane,
+                                           const float (&sum)[8][4]) {
+  const int N = a.N[which], g = lane >> 2, c = lane & 3;
+  const float scale = a.scale ? a.scale[pc.x] : 1.0f;
+  float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * a.R * N : a.part[which] + (int64_t)pc.w * a.R * N;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int r = rg * 16 + h * 8 + g;
+    if (r >= a.R) continue;
+    float* d = out + (int64_t)r * N;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const int col = m0 + j * 8 + 2 * c;
+      const float v0 = scale * sum[j][2 * h], v1 = scale * sum[j][2 * h + 1];
+      if (N % 2 == 0) {
+        if (col < N) *reinterpret_cast<float2*>(d + col) = make_float2(v0, v1);
+      } else {
+        if (col < N) d[col] = v0;
+        if (col + 1 < N) d[col + 1] = v1;
+      }
+    }
+  }
+}
+
+template <int RG, typename TQ>
+__device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int slab, const int4& pc, uint8_t* smem,
+                                      const int32_t* rows) {
+  typedef Wg<RG> W;
+  constexpr int kQ = LoraSrc<TQ>::kParts, S = W::kStages;
+  constexpr int kRowsQ = kQ == 1 ? kRows : kRows / 2;         // fp32: a stage holds half the rows
+  constexpr int kCB = kLoraRowBytes / (int)sizeof(TQ);        // columns of a 128-byte row
+  constexpr int kChunks = W::kSlab * (int)sizeof(TQ) / 16;    // of a row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int rg = warp % RG, cg = warp / RG;
+  const int N = a.N[which], m0 = slab * W::kSlab + cg * 64;
+  const uint32_t ring = smem_u32(smem), parts = ring + W::kRing;
+  const TQ* Q = reinterpret_cast<const TQ*>(a.q[which]);
+  const float* P = a.p[which];
+  const int how = a.how[which];
+  const int n = (pc.z + kRowsQ - 1) / kRowsQ;
+
+  auto fill = [&](int i) {
+    if (i < n) {
+      const uint32_t st = ring + (i % S) * W::kStageBytes;
+#pragma unroll
+      for (int e = tid; e < kRowsQ * kChunks; e += W::kThreads) {
+        const int r = e / kChunks, ch = e % kChunks, row = rows[min(i * kRowsQ + r, kMaxPiece - 1)];
+        const bool in = i * kRowsQ + r < pc.z;
+        load_chunk<TQ>(chunk_at(st + (ch >> 3) * (kRowsQ * kLoraRowBytes), r, ch & 7),
+                       in ? Q + (int64_t)row * a.ldq[which] : nullptr,
+                       slab * W::kSlab + ch * (16 / (int)sizeof(TQ)), N, how, a.plan.head);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // u or v of a stage: to registers, then as parts to shared memory
+  constexpr int kMine = kRowsQ * RG * 16 / W::kThreads > 0 ? kRowsQ * RG * 16 / W::kThreads : 1;
+  static_assert(kRowsQ * RG * 16 % W::kThreads == 0, "values of a stage");
+  float pv[kMine];
+  auto take = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < kMine; j++) {
+      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = i * kRowsQ + e / (RG * 16);
+      pv[j] = t < pc.z && r < a.R ? P[(int64_t)rows[t] * a.R + r] : 0.0f;
+    }
+  };
+  auto put = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < kMine; j++) {
+      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = e / (RG * 16);
+      uint16_t p[3];
+      split_bf16<3>(pv[j], p);
+#pragma unroll
+      for (int x = 0; x < 3; x++)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(parts + (i & 1) * W::kPartBytes + ((x * kRows + t) * W::kPStride + r) * 2),
+                     "h"(p[x]) : "memory");
+    }
+  };
+  float acc[8][4], sum[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+#pragma unroll
+    for (int x = 0; x < 4; x++) acc[j][x] = sum[j][x] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < S - 1; i++) fill(i);
+  take(0);
+  put(0);
+  for (int i = 0; i < n; i++) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    __syncthreads();
+    fill(i + S - 1);
+    if (i + 1 < n) take(i + 1);
+    const uint32_t st = ring + (i % S) * W::kStageBytes, ps = parts + (i & 1) * W::kPartBytes;
+    if (m0 < N) {
+#pragma unroll
+      for (int ks = 0; ks < kRowsQ / 16; ks++) {
+        uint32_t p[3][4];
+#pragma unroll
+        for (int x = 0; x < 3; x++)
+          ldsm4t(ps + ((x * kRows + ks * 16 + (lane & 7) + (lane >> 4) * 8) * W::kPStride + rg * 16 + ((lane >> 3) & 1) * 8) * 2, p[x]);
+        if (kQ == 1) {
+          const uint32_t t = st + cg * (kRowsQ * kLoraRowBytes);
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            uint32_t b[4];
+            ldsm4t(chunk_at(t, ks * 16 + (lane & 15), 2 * j + (lane >> 4)), b);
+#pragma unroll
+            for (int x = 2; x >= 0; x--) {
+              mma_16x8x16(acc[2 * j], p[x][0], p[x][1], p[x][2], p[x][3], b[0], b[1]);
+              mma_16x8x16(acc[2 * j + 1], p[x][0], p[x][1], p[x][2], p[x][3], b[2], b[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const int col = cg * 64 + j * 8 + g;
+            const uint32_t t = st + col / kCB * (kRowsQ * kLoraRowBytes);
+            uint32_t b[kQ][2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              float2 v;
+              const int r = ks * 16 + h * 8 + 2 * c, cc = col % kCB;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.x) : "r"(chunk_at(t, r, cc >> 2) + (cc & 3) * 4) : "memory");
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.y) : "r"(chunk_at(t, r + 1, cc >> 2) + (cc & 3) * 4) : "memory");
+              uint32_t w[kQ];
+              split_pair<kQ>(v, w);
+#pragma unroll
+              for (int y = 0; y < kQ; y++) b[y][h] = w[y];
+            }
+#pragma unroll
+            for (int y = kQ - 1; y >= 0; y--)
+#pragma unroll
+              for (int x = 2 - y; x >= 0; x--)  // products under 2^-24 of the largest are left out
+                mma_16x8x16(acc[j], p[x][0], p[x][1], p[x][2], p[x][3], b[y][0], b[y][1]);
+          }
+        }
+      }
+      if (i & 1) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            sum[j][x] += acc[j][x];
+            acc[j][x] = 0.0f;
+          }
+      }
+    }
+    if (i + 1 < n) put(i + 1);
+  }
+  if (m0 < N) {
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+#pragma unroll
+      for (int x = 0; x < 4; x++) sum[j][x] += acc[j][x];
+    store_sums<RG>(a, which, pc, rg, m0, lane, sum);
+  }
+}
+
+template <int RG, typename TX, typename TY>
+__global__ void __launch_bounds__(Wg<RG>::kThreads, Wg<RG>::kCtas) k_lora_wgrad(const __grid_constant__ LoraWgradArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int32_t rows[kMaxPiece];
+  const int4 head = *a.plan.head;
+  if ((int)blockIdx.y >= head.z) return;
+  const int4 pc = a.plan.pieces[blockIdx.y];
+  for (int i = threadIdx.x; i < kMaxPiece; i += Wg<RG>::kThreads) rows[i] = i < pc.z ? a.plan.order[pc.y + i] : 0;
+  __syncthreads();
+  const int nx = (a.N[0] + Wg<RG>::kSlab - 1) / Wg<RG>::kSlab;
+  if ((int)blockIdx.x < nx)
+    wgrad<RG, TX>(a, 0, blockIdx.x, pc, smem, rows);
+  else
+    wgrad<RG, TY>(a, 1, blockIdx.x - nx, pc, smem, rows);
+}
+
+// Adapters of several pieces: their partial sums in order.  Those without
+// rows: zeros.  (One piece: already written.)  V values a thread at a time.
+template <int V>
+__global__ void __launch_bounds__(256) k_lora_wgrad_sum(const __grid_constant__ LoraWgradArgs a) {
+  const int l = blockIdx.y;
+  const int pieces = a.plan.first[a.L + l];
+  if (pieces == 1) return;
+  const int64_t slot = a.plan.first[l];
+  const int64_t n0 = (int64_t)a.R * a.N[0], all = n0 + (int64_t)a.R * a.N[1];
+  for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; e < all; e += (int64_t)gridDim.x * 256 * V) {
+    const int w = e >= n0;
+    const int64_t i = w ? e - n0 : e, size = w ? all - n0 : n0;
+    const float* p = a.part[w] + slot * size + i;
+    float* o = a.out[w] + l * size + i;
+    if (V == 4) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int s = 0; s < pieces; s++) {
+        const float4 x = *reinterpret_cast<const float4*>(p + s * size);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      }
+      *reinterpret_cast<float4*>(o) = v;
+    } else {
+      float v = 0.0f;
+#pragma unroll 4
+      for (int s = 0; s < pieces; s++) v += p[s * size];
+      *o = v;
+    }
+  }
+}
+
+template <int RG, typename TX, typename TY>
+cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
+  typedef Wg<RG> W;
+  static std::atomic<int> done[kMaxCachedDevices];
+  cudaError_t e = smem_attr_once(k_lora_wgrad<RG, TX, TY>, W::kBytes, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.N[0] + W::kSlab - 1) / W::kSlab + (a.N[1] + W::kSlab - 1) / W::kSlab, (unsigned)a.plan.max_pieces);
+  e = launch_k(lc, k_lora_wgrad<RG, TX, TY>, grid, W::kThreads, W::kBytes, a);
+  if (e != cudaSuccess) return e;
+  const int64_t all = (int64_t)a.R * (a.N[0] + a.N[1]);
+  const bool four = (int64_t)a.R * a.N[0] % 4 == 0 && (int64_t)a.R * a.N[1] % 4 == 0;
+  const dim3 sums((unsigned)std::min<int64_t>((all + (four ? 1023 : 255)) / (four ? 1024 : 256), 1024), a.L);
+  return four ? launch_k(lc, k_lora_wgrad_sum<4>, sums, 256, 0, a) : launch_k(lc, k_lora_wgrad_sum<1>, sums, 256, 0, a);
+}
+template <typename TX, typename TY>
+cudaError_t by_rank(const LaunchCtx& lc, const LoraWgradArgs& a) {
+  return a.R <= 16 ? run<1, TX, TY>(lc, a) : a.R <= 32 ? run<2, TX, TY>(lc, a)
+       : a.R <= 64 ? run<4, TX, TY>(lc, a) : run<8, TX, TY>(lc, a);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a) {
+  if (a.f32[0]) return a.f32[1] ? by_rank<float, float>(lc, a) : by_rank<float, uint16_t>(lc, a);
+  return a.f32[1] ? by_rank<uint16_t, float>(lc, a) : by_rank<uint16_t, uint16_t>(lc, a);
+}
