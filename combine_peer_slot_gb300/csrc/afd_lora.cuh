@@ -12,7 +12,8 @@ constexpr int64_t kLoraMaxTokens = int64_t(1) << 24;
 // Rows of one adapter that a tile of the products holds, and rows of one
 // piece of the weight gradients' sums.
 __host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
-__host__ __device__ inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : 1024; }
+constexpr int kLoraMaxPiece = 512;
+__host__ __device__ inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : kLoraMaxPiece; }
 
 // The plan, made on the device from the rows' adapter ids: the rows in adapter
 // order (stable; rows without an adapter last), cut into tiles of one adapter.
@@ -83,10 +84,13 @@ struct LoraWgradArgs {
   const float* scale;
   int64_t T;
   int R, L;
+  int pairs;           // neighbouring ranks of u and v can be read together
 };
 cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 16
 cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 64
 cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
+cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, LoraWgradArgs a);  // the matrices of bf16 rows
+cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);          // waits that gave up, once the stream is there
 
 #ifdef __CUDACC__
 // D += A B on 16 x 8 x 16 bf16 values, fp32 sums: lane (g, c) = (lane / 4,

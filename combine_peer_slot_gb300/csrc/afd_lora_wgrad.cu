@@ -1,12 +1,13 @@
-// afd_lora_wgrad.cu -- the adapters' weight gradients:
+// afd_lora_wgrad.cu -- the adapters' weight gradients from fp32 rows
+// (afd_lora_wgrad_tc.cu: from bf16 ones), and the sum over an adapter's pieces:
 //   da[l] = scale[l] sum_t v_t x_t^T,  db[l] = scale[l] sum_t u_t dy_t^T
 // over the rows t of adapter l: [rank x columns] sums of outer products.
 //
 // A CTA takes one piece of an adapter's rows and a slab of columns of x or dy.
-// Rows stream through a ring of shared memory stages of 32, gathered by
-// asynchronous copies; u or v (fp32) is split once a stage into three bf16
-// parts, so that the products on the tensor cores keep its 24 bits.  A warp
-// holds 16 ranks x 64 columns.  The tensor cores' fp32 sums cut where they
+// Rows stream through a ring of shared memory stages of 16, gathered by
+// asynchronous copies; they and u or v are split into three bf16 parts each,
+// so that the products on the tensor cores keep 24 bits.  A warp holds 16
+// ranks x 64 columns.  The tensor cores' fp32 sums cut where they
 // should round, so every other stage they move to registers that add with
 // rounding.  Adapters of several pieces leave partial sums, added in order by
 // a second kernel, which also clears the gradients of adapters without rows.
@@ -14,7 +15,7 @@
 
 namespace {
 
-constexpr int kRows = 32;  // of a stage
+constexpr int kRows = 16;  // of a stage
 
 // rank groups of 16 x column groups of 64: one warp each
 template <int RG>
@@ -22,7 +23,7 @@ struct Wg {
   static constexpr int kCg = RG == 1 ? 8 : RG <= 4 ? 4 : 2;
   static constexpr int kThreads = RG * kCg * 32;
   static constexpr int kSlab = kCg * 64;
-  static constexpr int kStageBytes = kRows * kSlab * 2;
+  static constexpr int kStageBytes = kRows * kSlab * 4;
   static constexpr int kStages = RG == 1 ? 3 : 6;
   static constexpr int kPStride = RG * 16 + 8;                 // bf16 of a row's parts
   static constexpr int kPartBytes = 3 * kRows * kPStride * 2;  // one stage's
@@ -30,7 +31,6 @@ struct Wg {
   static constexpr int kBytes = kRing + 2 * kPartBytes;
   static constexpr int kCtas = kThreads == 256 ? 2 : 1;
 };
-constexpr int kMaxPiece = 1024;
 
 template <int RG>
 __device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, const int4& pc, int rg, int m0, int lane,
@@ -57,45 +57,44 @@ __device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, co
   }
 }
 
-template <int RG, typename TQ>
+template <int RG>
 __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int slab, const int4& pc, uint8_t* smem,
                                       const int32_t* rows) {
   typedef Wg<RG> W;
-  constexpr int kQ = LoraSrc<TQ>::kParts, S = W::kStages;
-  constexpr int kRowsQ = kQ == 1 ? kRows : kRows / 2;         // fp32: a stage holds half the rows
-  constexpr int kCB = kLoraRowBytes / (int)sizeof(TQ);        // columns of a 128-byte row
-  constexpr int kChunks = W::kSlab * (int)sizeof(TQ) / 16;    // of a row
+  constexpr int kQ = LoraSrc<float>::kParts, S = W::kStages;
+  constexpr int kCB = kLoraRowBytes / 4;     // columns of a 128-byte row
+  constexpr int kChunks = W::kSlab / 4;      // of a row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int rg = warp % RG, cg = warp / RG;
   const int N = a.N[which], m0 = slab * W::kSlab + cg * 64;
   const uint32_t ring = smem_u32(smem), parts = ring + W::kRing;
-  const TQ* Q = reinterpret_cast<const TQ*>(a.q[which]);
+  const float* Q = reinterpret_cast<const float*>(a.q[which]);
   const float* P = a.p[which];
   const int how = a.how[which];
-  const int n = (pc.z + kRowsQ - 1) / kRowsQ;
+  const int n = (pc.z + kRows - 1) / kRows;
 
   auto fill = [&](int i) {
     if (i < n) {
       const uint32_t st = ring + (i % S) * W::kStageBytes;
 #pragma unroll
-      for (int e = tid; e < kRowsQ * kChunks; e += W::kThreads) {
-        const int r = e / kChunks, ch = e % kChunks, row = rows[min(i * kRowsQ + r, kMaxPiece - 1)];
-        const bool in = i * kRowsQ + r < pc.z;
-        load_chunk<TQ>(chunk_at(st + (ch >> 3) * (kRowsQ * kLoraRowBytes), r, ch & 7),
+      for (int e = tid; e < kRows * kChunks; e += W::kThreads) {
+        const int r = e / kChunks, ch = e % kChunks, row = rows[min(i * kRows + r, kLoraMaxPiece - 1)];
+        const bool in = i * kRows + r < pc.z;
+        load_chunk<float>(chunk_at(st + (ch >> 3) * (kRows * kLoraRowBytes), r, ch & 7),
                        in ? Q + (int64_t)row * a.ldq[which] : nullptr,
-                       slab * W::kSlab + ch * (16 / (int)sizeof(TQ)), N, how, a.plan.head);
+                       slab * W::kSlab + ch * 4, N, how, a.plan.head);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // u or v of a stage: to registers, then as parts to shared memory
-  constexpr int kMine = kRowsQ * RG * 16 / W::kThreads > 0 ? kRowsQ * RG * 16 / W::kThreads : 1;
-  static_assert(kRowsQ * RG * 16 % W::kThreads == 0, "values of a stage");
+  constexpr int kMine = kRows * RG * 16 / W::kThreads;
+  static_assert(kRows * RG * 16 % W::kThreads == 0, "values of a stage");
   float pv[kMine];
   auto take = [&](int i) {
 #pragma unroll
     for (int j = 0; j < kMine; j++) {
-      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = i * kRowsQ + e / (RG * 16);
+      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = i * kRows + e / (RG * 16);
       pv[j] = t < pc.z && r < a.R ? P[(int64_t)rows[t] * a.R + r] : 0.0f;
     }
   };
@@ -128,46 +127,32 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
     const uint32_t st = ring + (i % S) * W::kStageBytes, ps = parts + (i & 1) * W::kPartBytes;
     if (m0 < N) {
 #pragma unroll
-      for (int ks = 0; ks < kRowsQ / 16; ks++) {
+      for (int ks = 0; ks < kRows / 16; ks++) {
         uint32_t p[3][4];
 #pragma unroll
         for (int x = 0; x < 3; x++)
           ldsm4t(ps + ((x * kRows + ks * 16 + (lane & 7) + (lane >> 4) * 8) * W::kPStride + rg * 16 + ((lane >> 3) & 1) * 8) * 2, p[x]);
-        if (kQ == 1) {
-          const uint32_t t = st + cg * (kRowsQ * kLoraRowBytes);
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            uint32_t b[4];
-            ldsm4t(chunk_at(t, ks * 16 + (lane & 15), 2 * j + (lane >> 4)), b);
+        for (int j = 0; j < 8; j++) {
+          const int col = cg * 64 + j * 8 + g;
+          const uint32_t t = st + col / kCB * (kRows * kLoraRowBytes);
+          uint32_t b[kQ][2];
 #pragma unroll
-            for (int x = 2; x >= 0; x--) {
-              mma_16x8x16(acc[2 * j], p[x][0], p[x][1], p[x][2], p[x][3], b[0], b[1]);
-              mma_16x8x16(acc[2 * j + 1], p[x][0], p[x][1], p[x][2], p[x][3], b[2], b[3]);
-            }
+          for (int h = 0; h < 2; h++) {
+            float2 v;
+            const int r = ks * 16 + h * 8 + 2 * c, cc = col % kCB;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.x) : "r"(chunk_at(t, r, cc >> 2) + (cc & 3) * 4) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.y) : "r"(chunk_at(t, r + 1, cc >> 2) + (cc & 3) * 4) : "memory");
+            uint32_t w[kQ];
+            split_pair<kQ>(v, w);
+#pragma unroll
+            for (int y = 0; y < kQ; y++) b[y][h] = w[y];
           }
-        } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const int col = cg * 64 + j * 8 + g;
-            const uint32_t t = st + col / kCB * (kRowsQ * kLoraRowBytes);
-            uint32_t b[kQ][2];
+          for (int y = kQ - 1; y >= 0; y--)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              float2 v;
-              const int r = ks * 16 + h * 8 + 2 * c, cc = col % kCB;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.x) : "r"(chunk_at(t, r, cc >> 2) + (cc & 3) * 4) : "memory");
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.y) : "r"(chunk_at(t, r + 1, cc >> 2) + (cc & 3) * 4) : "memory");
-              uint32_t w[kQ];
-              split_pair<kQ>(v, w);
-#pragma unroll
-              for (int y = 0; y < kQ; y++) b[y][h] = w[y];
-            }
-#pragma unroll
-            for (int y = kQ - 1; y >= 0; y--)
-#pragma unroll
-              for (int x = 2 - y; x >= 0; x--)  // products under 2^-24 of the largest are left out
-                mma_16x8x16(acc[j], p[x][0], p[x][1], p[x][2], p[x][3], b[y][0], b[y][1]);
-          }
+            for (int x = 2 - y; x >= 0; x--)  // products under 2^-24 of the largest are left out
+              mma_16x8x16(acc[j], p[x][0], p[x][1], p[x][2], p[x][3], b[y][0], b[y][1]);
         }
       }
       if (i & 1) {
@@ -191,20 +176,18 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
   }
 }
 
-template <int RG, typename TX, typename TY>
+template <int RG>
 __global__ void __launch_bounds__(Wg<RG>::kThreads, Wg<RG>::kCtas) k_lora_wgrad(const __grid_constant__ LoraWgradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int32_t rows[kMaxPiece];
+  __shared__ int32_t rows[kLoraMaxPiece];
   const int4 head = *a.plan.head;
   if ((int)blockIdx.y >= head.z) return;
   const int4 pc = a.plan.pieces[blockIdx.y];
-  for (int i = threadIdx.x; i < kMaxPiece; i += Wg<RG>::kThreads) rows[i] = i < pc.z ? a.plan.order[pc.y + i] : 0;
+  for (int i = threadIdx.x; i < kLoraMaxPiece; i += Wg<RG>::kThreads) rows[i] = i < pc.z ? a.plan.order[pc.y + i] : 0;
   __syncthreads();
-  const int nx = (a.N[0] + Wg<RG>::kSlab - 1) / Wg<RG>::kSlab;
-  if ((int)blockIdx.x < nx)
-    wgrad<RG, TX>(a, 0, blockIdx.x, pc, smem, rows);
-  else
-    wgrad<RG, TY>(a, 1, blockIdx.x - nx, pc, smem, rows);
+  const int nx = a.f32[0] ? (a.N[0] + Wg<RG>::kSlab - 1) / Wg<RG>::kSlab : 0;
+  const int which = (int)blockIdx.x >= nx;
+  wgrad<RG>(a, which, (int)blockIdx.x - (which ? nx : 0), pc, smem, rows);
 }
 
 // Adapters of several pieces: their partial sums in order.  Those without
@@ -238,29 +221,30 @@ __global__ void __launch_bounds__(256) k_lora_wgrad_sum(const __grid_constant__ 
   }
 }
 
-template <int RG, typename TX, typename TY>
+template <int RG>
 cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
   typedef Wg<RG> W;
   static std::atomic<int> done[kMaxCachedDevices];
-  cudaError_t e = smem_attr_once(k_lora_wgrad<RG, TX, TY>, W::kBytes, done);
+  cudaError_t e = smem_attr_once(k_lora_wgrad<RG>, W::kBytes, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.N[0] + W::kSlab - 1) / W::kSlab + (a.N[1] + W::kSlab - 1) / W::kSlab, (unsigned)a.plan.max_pieces);
-  e = launch_k(lc, k_lora_wgrad<RG, TX, TY>, grid, W::kThreads, W::kBytes, a);
-  if (e != cudaSuccess) return e;
-  const int64_t all = (int64_t)a.R * (a.N[0] + a.N[1]);
-  const bool four = (int64_t)a.R * a.N[0] % 4 == 0 && (int64_t)a.R * a.N[1] % 4 == 0;
-  const dim3 sums((unsigned)std::min<int64_t>((all + (four ? 1023 : 255)) / (four ? 1024 : 256), 1024), a.L);
-  return four ? launch_k(lc, k_lora_wgrad_sum<4>, sums, 256, 0, a) : launch_k(lc, k_lora_wgrad_sum<1>, sums, 256, 0, a);
+  int slabs = 0;
+  for (int w = 0; w < 2; w++)
+    if (a.f32[w]) slabs += (a.N[w] + W::kSlab - 1) / W::kSlab;
+  return launch_k(lc, k_lora_wgrad<RG>, dim3(slabs, (unsigned)a.plan.max_pieces), W::kThreads, W::kBytes, a);
 }
-template <typename TX, typename TY>
 cudaError_t by_rank(const LaunchCtx& lc, const LoraWgradArgs& a) {
-  return a.R <= 16 ? run<1, TX, TY>(lc, a) : a.R <= 32 ? run<2, TX, TY>(lc, a)
-       : a.R <= 64 ? run<4, TX, TY>(lc, a) : run<8, TX, TY>(lc, a);
+  return a.R <= 16 ? run<1>(lc, a) : a.R <= 32 ? run<2>(lc, a) : a.R <= 64 ? run<4>(lc, a) : run<8>(lc, a);
 }
 
 }  // namespace
 
 cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a) {
-  if (a.f32[0]) return a.f32[1] ? by_rank<float, float>(lc, a) : by_rank<float, uint16_t>(lc, a);
-  return a.f32[1] ? by_rank<uint16_t, float>(lc, a) : by_rank<uint16_t, uint16_t>(lc, a);
+  cudaError_t e = cudaSuccess;
+  if (!a.f32[0] || !a.f32[1]) e = launch_lora_wgrad_tc(lc, a);
+  if (e == cudaSuccess && (a.f32[0] || a.f32[1])) e = by_rank(lc, a);
+  if (e != cudaSuccess) return e;
+  const int64_t all = (int64_t)a.R * (a.N[0] + a.N[1]);
+  const bool four = (int64_t)a.R * a.N[0] % 4 == 0 && (int64_t)a.R * a.N[1] % 4 == 0;
+  const dim3 sums((unsigned)std::min<int64_t>((all + (four ? 1023 : 255)) / (four ? 1024 : 256), 1024), a.L);
+  return four ? launch_k(lc, k_lora_wgrad_sum<4>, sums, 256, 0, a) : launch_k(lc, k_lora_wgrad_sum<1>, sums, 256, 0, a);
 }

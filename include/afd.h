@@ -759,8 +759,8 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
 
 /* Synchronise the stream; AFD_ERR_TIMEOUT if, since this host thread's last
  * call for this stream (since the library was loaded, for its first), a
- * bounded wait (2 s) of any of the products above on the current device gave
- * up and left its outputs incomplete; else AFD_OK.  The products of all
+ * bounded wait (2 s) of any of the products above, or of afd_lora_backward, on
+ * the current device gave up and left its outputs incomplete; else AFD_OK.  The products of all
  * streams are counted together: an error is told once to each thread and
  * stream that polls, so that no caller takes another's. */
 int afd_mx4_poll_status(void* cuda_stream);
