@@ -215,7 +215,8 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 extern "C" int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank) {
   if (!batch_ok(n_tokens, n_adapters) || !dims_ok(K, M, rank)) return -1;
   const LoraPlan p = lora_plan_at(nullptr, n_tokens, n_adapters);
-  return up256(n_tokens * rank * 4) + up256(p.max_slots * rank * K * 4) + up256(p.max_slots * rank * M * 4);
+  return up256(n_tokens * rank * 4) + 2 * up256(n_tokens * 3 * lora_padded(rank) * 2) + up256(p.max_slots * rank * K * 4) +
+         up256(p.max_slots * rank * M * 4);
 }
 
 extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const void* x, int64_t ldx,
@@ -248,23 +249,44 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
   }
   const int rc = check_device_ptrs({plan, x, dy, u, a, b, scale, d_base, dx, da, db, workspace});
   if (rc) return rc;
-  float* v = reinterpret_cast<float*>(workspace);
+  // workspace: v, the parts of v and of u, the partial sums of da and db
+  char* at = reinterpret_cast<char*>(workspace);
+  auto take = [&](int64_t bytes) {
+    char* r = at;
+    at += up256(bytes);
+    return r;
+  };
+  float* v = reinterpret_cast<float*>(take(n_tokens * rank * 4));
+  uint16_t* v_parts = reinterpret_cast<uint16_t*>(take(n_tokens * 3 * lora_padded(rank) * 2));
+  uint16_t* u_parts = reinterpret_cast<uint16_t*>(take(n_tokens * 3 * lora_padded(rank) * 2));
   LoraArgs g{};
   g.plan = lora_plan_at(const_cast<void*>(plan), n_tokens, n_adapters);
   g.src = dy; g.lds = ldy; g.w1 = b; g.w2 = a; g.scale = scale;
-  g.base = d_base; g.ldb = ldb; g.out = dx; g.ldo = ldd; g.u = v;
+  g.base = d_base; g.ldb = ldb; g.out = dx; g.ldo = ldd;
   g.T = n_tokens; g.K = M; g.M = K; g.R = rank;
   g.src_f32 = y_dtype == AFD_DTYPE_F32; g.out_f32 = x_dtype == AFD_DTYPE_F32;
   LoraWgradArgs w{};
   w.plan = g.plan;
   w.p[0] = v; w.p[1] = u; w.q[0] = x; w.q[1] = dy; w.ldq[0] = ldx; w.ldq[1] = ldy;
   w.out[0] = da; w.out[1] = db; w.N[0] = K; w.N[1] = M;
-  w.part[0] = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + up256(n_tokens * rank * 4));
-  w.part[1] = reinterpret_cast<float*>(reinterpret_cast<char*>(w.part[0]) + up256(g.plan.max_slots * rank * K * 4));
+  w.part[0] = reinterpret_cast<float*>(take(g.plan.max_slots * rank * K * 4));
+  w.part[1] = reinterpret_cast<float*>(take(g.plan.max_slots * rank * M * 4));
   w.f32[0] = g.out_f32; w.f32[1] = g.src_f32;
   w.how[0] = how_rows(x, ldx, K, x_dtype);
   w.how[1] = how_rows(dy, ldy, M, y_dtype);
   w.scale = scale; w.T = n_tokens; w.R = rank; w.L = n_adapters;
+  // what each gradient reads beside its rows: fp32 values, or parts
+  if (w.f32[0]) {
+    g.u = v;
+  } else {
+    g.u_parts = v_parts;
+    w.parts[0] = v_parts;
+  }
+  if (!w.f32[1]) {
+    g.other = u;
+    g.other_parts = u_parts;
+    w.parts[1] = u_parts;
+  }
   const LaunchCtx lc{stream, 0, nullptr};
   cudaError_t e = launch_products(lc, g);
   if (e == cudaSuccess) e = launch_lora_wgrad(lc, w);

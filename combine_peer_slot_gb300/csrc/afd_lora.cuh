@@ -64,6 +64,11 @@ struct LoraArgs {
   void* out;
   int64_t ldo;
   float* u;            // [T][R] or NULL
+  // for the weight gradients, or NULL: rows in the plan's order as three bf16
+  // parts of `padded` ranks each, of u as computed here and of `other` [T][R]
+  uint16_t* u_parts;
+  const float* other;
+  uint16_t* other_parts;
   int64_t T;
   int K, M, R;
   int src_f32, out_f32;
@@ -73,7 +78,8 @@ struct LoraArgs {
 // da[l] = scale[l] sum v_t x_t^T, db[l] = scale[l] sum u_t dy_t^T
 struct LoraWgradArgs {
   LoraPlan plan;
-  const float* p[2];   // v, u: [T][R]
+  const float* p[2];   // v, u: [T][R], beside fp32 rows
+  const uint16_t* parts[2];  // and as LoraArgs::u_parts, beside bf16 ones
   const void* q[2];    // x, dy
   int64_t ldq[2];
   float* out[2];       // [L][R][N]
@@ -84,12 +90,13 @@ struct LoraWgradArgs {
   const float* scale;
   int64_t T;
   int R, L;
-  int pairs;           // neighbouring ranks of u and v can be read together
 };
+// ranks of one part
+__host__ __device__ inline int lora_padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 16
 cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 64
 cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
-cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, LoraWgradArgs a);  // the matrices of bf16 rows
+cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, const LoraWgradArgs& a);  // the matrices of bf16 rows
 cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);          // waits that gave up, once the stream is there
 
 #ifdef __CUDACC__

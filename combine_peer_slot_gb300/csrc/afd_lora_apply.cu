@@ -61,6 +61,14 @@ __device__ __forceinline__ void add_eight(const void* base, TO* out, int c0, int
   }
 }
 
+// one value's parts, of row i in the plan's order
+__device__ __forceinline__ void store_parts(uint16_t* to, int padded, int64_t i, int r, float v) {
+  uint16_t p[3];
+  split_bf16<3>(v, p);
+#pragma unroll
+  for (int x = 0; x < 3; x++) to[(i * 3 + x) * padded + r] = p[x];
+}
+
 template <int KC, typename TS, typename TO>
 __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constant__ LoraArgs a) {
   constexpr int kParts = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
     }
     return;
   }
-  const int rt = (a.R + 15) / 16;                      // rank tiles
+  const int rt = (a.R + 15) / 16, padded = lora_padded(a.R);  // rank tiles
   float* part = reinterpret_cast<float*>(smem);        // [rt * 16][TT]: this CTA's sums
   float* red = part + rt * 16 * TT;                    // [warps][kRows * 16][kRedStride]
   uint16_t* us = reinterpret_cast<uint16_t*>(red);     // [kU][TT][rt * 16 + 8], after the sums
@@ -169,6 +177,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
 #pragma unroll
     for (int x = 0; x < kU; x++) us[(x * TT + i) * ustr + r] = p[x];
     if (a.u && q == 0 && i < t.z && r < a.R) a.u[(int64_t)order[i] * a.R + r] = v;
+    if (a.u_parts && q == 0 && i < t.z) store_parts(a.u_parts, padded, t.y + i, r, v);
+  }
+  if (q == C - 1) {
+    for (int e = threadIdx.x; a.u_parts && e < t.z * (padded - rt * 16); e += kWarps * 32)
+      store_parts(a.u_parts, padded, t.y + e % t.z, rt * 16 + e / t.z, 0.0f);
+    for (int e = threadIdx.x; a.other_parts && e < t.z * padded; e += kWarps * 32) {
+      const int r = e % padded, i = e / padded;
+      store_parts(a.other_parts, padded, t.y + i, r, r < a.R ? a.other[(int64_t)order[i] * a.R + r] : 0.0f);
+    }
   }
   cluster.sync();  // (no CTA's sums are read after this)
   const float scale = a.scale ? a.scale[t.x] : 1.0f;

@@ -47,6 +47,32 @@ __device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
+// A stage's copies where some rows cannot be moved 16 bytes at a time.
+template <int KC, typename TS, typename TO>
+__device__ __noinline__ void slow_fill(const LoraArgs& a, uint32_t st, bool first, int c0, int64_t row0, int64_t row1,
+                                       const uint16_t* w1, const uint16_t* w2) {
+  constexpr int KB = kRowBytes / (int)sizeof(TS), CB = kRowBytes / (int)sizeof(TO);
+  const int ch = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const uint32_t wst = st + kTileBytes;
+  if (first) {
+    const TS* s = reinterpret_cast<const TS*>(a.src);
+    load_chunk<TS>(chunk_at(st, r0, ch), row0 >= 0 ? s + row0 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
+    load_chunk<TS>(chunk_at(st, r0 + 32, ch), row1 >= 0 ? s + row1 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
+    for (int e = threadIdx.x; e < KC * 16 * (KB / 8); e += kThreads) {
+      const int r = e / (KB / 8), cc = e % (KB / 8);
+      load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w1 + (int64_t)r * a.K : nullptr, c0 + cc * 8, a.K, a.how_w1, a.plan.head);
+    }
+  } else {
+    const TO* b = reinterpret_cast<const TO*>(a.base);
+    load_chunk<TO>(chunk_at(st, r0, ch), b && row0 >= 0 ? b + row0 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+    load_chunk<TO>(chunk_at(st, r0 + 32, ch), b && row1 >= 0 ? b + row1 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+    for (int e = threadIdx.x; e < KC * 16 * (CB / 8); e += kThreads) {
+      const int r = e / (CB / 8), cc = e % (CB / 8);
+      load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w2 + (int64_t)r * a.M : nullptr, c0 + cc * 8, a.M, a.how_w2, a.plan.head);
+    }
+  }
+}
+
 template <int KC, typename TS, typename TO>
 __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const __grid_constant__ LoraArgs a) {
   typedef Form<KC> F;
@@ -91,31 +117,50 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   const int all1 = (a.K + KB - 1) / KB, all2 = (a.M + CB - 1) / CB;
   const int k0 = all1 * q / C, n1 = all1 * (q + 1) / C - k0, m0 = all2 * q / C, n2 = all2 * (q + 1) / C - m0;
   const int n = n1 + n2;
-  // this thread's chunk of rows tid / 8 and tid / 8 + 32 of a tile
+  // This thread's chunk of rows tid / 8 and tid / 8 + 32 of a tile, and of the
+  // weight's rows tid / kWc + i kWr: addresses that move on by a stage's columns.
   const int ch = tid & 7, r0 = tid >> 3;
-  const int64_t row0 = rows[r0], row1 = rows[r0 + 32];
-
+  const bool fast = a.how_src == 2 && a.how_w1 == 2 && a.how_w2 == 2 && a.how_base == 2;
+  const char *p0 = nullptr, *p1 = nullptr, *pw = nullptr;
+  int left = 0, wleft = 0;  // columns from the chunk on; <= 0: none
+  auto start = [&](const void* rows_at, int64_t ld, int size, int first, int cols, int chunk_cols, const uint16_t* w, int wide) {
+    const char* b = reinterpret_cast<const char*>(rows_at);
+    const int c0 = first * (kRowBytes / size) + ch * (16 / size);
+    const int64_t row0 = rows[r0], row1 = rows[r0 + 32];
+    p0 = b && row0 >= 0 ? b + (row0 * ld + c0) * size : nullptr;
+    p1 = b && row1 >= 0 ? b + (row1 * ld + c0) * size : nullptr;
+    left = cols - c0;
+    const int wc = first * chunk_cols + tid % (chunk_cols / 8) * 8;
+    pw = reinterpret_cast<const char*>(w + (int64_t)(tid / (chunk_cols / 8)) * wide + wc);
+    wleft = cols - wc;
+  };
   auto fill = [&](int i) {
     if (i < n) {
       const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
-      if (i < n1) {
-        const int c0 = (k0 + i) * KB;
-        const TS* s = reinterpret_cast<const TS*>(a.src);
-        load_chunk<TS>(chunk_at(st, r0, ch), row0 >= 0 ? s + row0 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
-        load_chunk<TS>(chunk_at(st, r0 + 32, ch), row1 >= 0 ? s + row1 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
-        for (int e = tid; e < KC * 16 * (KB / 8); e += kThreads) {
-          const int r = e / (KB / 8), cc = e % (KB / 8);
-          load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w1 + (int64_t)r * a.K : nullptr, c0 + cc * 8, a.K, a.how_w1, a.plan.head);
+      if (fast) {
+        if (i == 0 && n1 > 0) start(a.src, a.lds, sizeof(TS), k0, a.K, KB, w1, a.K);
+        if (i == n1) start(a.base, a.ldb, sizeof(TO), m0, a.M, CB, w2, a.M);
+        copy16(chunk_at(st, r0, ch), p0 ? p0 : (const char*)a.plan.head, p0 && left > 0);
+        copy16(chunk_at(st, r0 + 32, ch), p1 ? p1 : (const char*)a.plan.head, p1 && left > 0);
+        if (p0) p0 += kRowBytes;
+        if (p1) p1 += kRowBytes;
+        const bool one = i < n1;
+        const int cols = one ? KB : CB, wide = one ? a.K : a.M;
+        left -= cols;
+        const int per = cols / 8, wr = kThreads / per;  // chunks of a weight row; rows filled at a time
+        const int r = tid / per, cc = tid % per;
+#pragma unroll
+        for (int x = 0; x < (KC * 16 * 8 + kThreads - 1) / kThreads; x++) {
+          const int rr = r + x * wr;
+          if (rr < KC * 16) {
+            const bool in = rr < a.R && wleft > 0;
+            copy16(chunk_at(wst, rr, cc), in ? pw + (int64_t)x * wr * wide * 2 : (const char*)a.plan.head, in);
+          }
         }
+        pw += cols * 2;
+        wleft -= cols;
       } else {
-        const int c0 = (m0 + i - n1) * CB;
-        const TO* b = reinterpret_cast<const TO*>(a.base);
-        load_chunk<TO>(chunk_at(st, r0, ch), b && row0 >= 0 ? b + row0 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
-        load_chunk<TO>(chunk_at(st, r0 + 32, ch), b && row1 >= 0 ? b + row1 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
-        for (int e = tid; e < KC * 16 * (CB / 8); e += kThreads) {
-          const int r = e / (CB / 8), cc = e % (CB / 8);
-          load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w2 + (int64_t)r * a.M : nullptr, c0 + cc * 8, a.M, a.how_w2, a.plan.head);
-        }
+        slow_fill<KC, TS, TO>(a, st, i < n1, i < n1 ? (k0 + i) * KB : (m0 + i - n1) * CB, rows[r0], rows[r0 + 32], w1, w2);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -211,6 +256,24 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
       if (i < t.z && r < a.R) a.u[(int64_t)rows[i] * a.R + r] = part[i * F::kUStride + r];
     }
   }
+  if (a.u_parts || a.other_parts) {  // rows t.y + i of the plan's order, KC * 16 ranks a part
+    for (int e = tid + q * kThreads; e < t.z * KC * 8; e += C * kThreads) {
+      const int i = e / (KC * 8), r = e % (KC * 8) * 2;
+      const int64_t to = (int64_t)(t.y + i) * 3 * (KC * 16) + r;
+      uint32_t p[3];
+      if (a.u_parts) {
+        split_pair<3>(*reinterpret_cast<const float2*>(part + i * F::kUStride + r), p);
+#pragma unroll
+        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(a.u_parts + to + x * (KC * 16)) = p[x];
+      }
+      if (a.other_parts) {
+        const float* o = a.other + (int64_t)rows[i] * a.R + r;
+        split_pair<3>(make_float2(r < a.R ? o[0] : 0.0f, r + 1 < a.R ? o[1] : 0.0f), p);
+#pragma unroll
+        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(a.other_parts + to + x * (KC * 16)) = p[x];
+      }
+    }
+  }
   // ---- out: the warp's 16 rows x CB / 2 columns of each block ----
   const float scale = a.scale ? a.scale[t.x] : 1.0f;
   auto operand = [&](int ks, uint32_t (&p)[kU][4]) {
@@ -227,6 +290,13 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
 #pragma unroll
     for (int ks = 0; ks < KC; ks++) operand(ks, held[kHold ? ks : 0]);
   const int steps = (a.R + 15) / 16;
+  // this lane's 16 bytes of rows g and g + 8 of the warp's
+  TO* o[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int64_t row = rows[wt * 16 + h * 8 + g];
+    o[h] = row >= 0 ? reinterpret_cast<TO*>(a.out) + row * a.ldo + m0 * CB + (half * 4 + c) * (CB / 8) : nullptr;
+  }
   for (int i = n1; i < n; i++) {
     ready();
     fill(i + S - 1);
@@ -272,27 +342,25 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
         }
       }
     __syncwarp();
-    const int c0 = (m0 + i - n1) * CB;
+    const int cc = half * 4 + c, col = (m0 + i - n1) * CB + cc * (CB / 8);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const int r = wt * 16 + h * 8 + g, cc = half * 4 + c, col = c0 + cc * (CB / 8);
-      const int64_t row = rows[r];
-      if (row >= 0 && col < a.M) {
+      if (o[h] && col < a.M) {
         uint32_t w[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(chunk_at(st, r, cc)) : "memory");
-        TO* o = reinterpret_cast<TO*>(a.out) + row * a.ldo + col;
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(chunk_at(st, wt * 16 + h * 8 + g, cc)) : "memory");
         if (a.how_out == 2) {
-          *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(o[h]) = make_uint4(w[0], w[1], w[2], w[3]);
         } else if (sizeof(TO) == 2) {
 #pragma unroll
           for (int x = 0; x < 8; x++)
-            if (col + x < a.M) reinterpret_cast<uint16_t*>(o)[x] = (uint16_t)(w[x / 2] >> (x % 2 * 16));
+            if (col + x < a.M) reinterpret_cast<uint16_t*>(o[h])[x] = (uint16_t)(w[x / 2] >> (x % 2 * 16));
         } else {
 #pragma unroll
           for (int x = 0; x < 4; x++)
-            if (col + x < a.M) reinterpret_cast<uint32_t*>(o)[x] = w[x];
+            if (col + x < a.M) reinterpret_cast<uint32_t*>(o[h])[x] = w[x];
         }
+        o[h] += CB;
       }
     }
   }

@@ -6,10 +6,12 @@
 // product's k runs over the rows, so both operands are used as they lie in
 // memory, rows of neighbouring elements (MN-major), 64 of them to a 128-byte
 // swizzled row: asynchronous copies gather x or dy by the plan's order
-// straight into the layout the tensor cores read.  u or v (fp32) is split into
-// three bf16 parts, which keep its 24 bits; the parts of up to 42 ranks stand
-// side by side in the 128 rows of one MMA and are added at the end, those of
-// more take two or three MMAs.
+// straight into the layout the tensor cores read.  u or v comes as three bf16
+// parts, which keep its 24 bits, written in the plan's order by the kernel of
+// the products: splitting fp32 values here, once for each 128 columns, was more
+// than half of the instructions (98 us where this takes 63).  The parts of up
+// to 32 ranks stand side by side in the 128 rows of one MMA and are added at
+// the end, those of more take two or three MMAs.
 //
 // Sums in TMEM may cut where they should round, so they move to registers
 // every four stages (128 rows) and start anew in the other accumulator, while
@@ -26,7 +28,6 @@ __device__ uint32_t g_lora_errors;  // waits that gave up
 
 constexpr int kThreads = 256, kRows = 32, kSlab = 128;
 constexpr int kAtom = kRows * kLoraRowBytes;     // 64 columns or ranks of a stage
-constexpr int kStageBytes = 2 * kAtom;
 constexpr int kFlush = 4;                        // stages between two moves of the sums
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kOutStride = 65;                   // floats, of the output's staging
@@ -35,20 +36,22 @@ constexpr int kOutStride = 65;                   // floats, of the output's stag
 template <int MP>
 struct Tc {
   static constexpr int kMmas = MP <= 32 ? 1 : MP == 64 ? 2 : 3;  // a 16-row step
-  static constexpr int kPartBytes = kMmas * 2 * kAtom;
-  static constexpr int kStages = MP == 128 ? 6 : 7;
+  static constexpr int kAtoms = (3 * MP + 63) / 64;              // of the parts
+  static constexpr int kChunks = 3 * MP / 8;                     // 16-byte chunks of a row's parts
+  static constexpr int kStageBytes = (2 + kAtoms) * kAtom;
+  static constexpr int kStages = MP == 16 ? 7 : MP == 32 ? 6 : MP == 64 ? 4 : 3;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kBytes = kRing + 2 * kPartBytes;
+  static constexpr int kBytes = kRing + kAtom;                   // and an atom of zeros: MMA rows of no part
   // accumulator rows of a rank: this many, this far apart (MP 64: the first
   // and third part share theirs)
   static constexpr int kSums = MP <= 32 ? 3 : MP == 64 ? 2 : 1;
   static_assert(128 * kOutStride * 4 <= kRing, "the output is staged in the ring");
 };
 
-// MN-major operand, 128-byte swizzle: 64-element atoms kAtom apart, 8-row
-// groups 1024 bytes apart
-__device__ __forceinline__ uint64_t operand(uint32_t addr) {
-  return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | (uint32_t)(kAtom >> 4) << 16 | ((addr & 0x3ffffu) >> 4);
+// MN-major operand, 128-byte swizzle: two atoms of 64 elements `apart` bytes
+// apart, 8-row groups 1024
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t apart) {
+  return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | apart >> 4 << 16 | ((addr & 0x3ffffu) >> 4);
 }
 // bf16 x bf16 -> fp32, both operands MN-major, M = N = 128
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(kSlab >> 3) << 17 | (128u >> 4) << 24;
@@ -79,14 +82,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
   const int nx = a.f32[0] ? 0 : (a.N[0] + kSlab - 1) / kSlab;
   const int which = (int)blockIdx.x >= nx, m0 = ((int)blockIdx.x - (which ? nx : 0)) * kSlab;
   const int N = a.N[which], how = a.how[which], R = a.R;
+  const uint16_t* P = a.parts[which] + (int64_t)pc.y * (3 * MP);
   const uint16_t* Q = reinterpret_cast<const uint16_t*>(a.q[which]);
   const int64_t ldq = a.ldq[which];
-  const float* P = a.p[which];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = smem_u32(smem), parts = ring + W::kRing, bar = smem_u32(bars);
+  const uint32_t ring = smem_u32(smem), zero = ring + W::kRing, bar = smem_u32(bars);
   for (int i = tid; i < pc.z; i += kThreads) rows[i] = a.plan.order[pc.y + i];
-  for (int i = tid; i < 2 * W::kPartBytes / 16; i += kThreads)  // places of no part stay zero
-    *reinterpret_cast<uint4*>(smem + W::kRing + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+  *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
+  if (W::kChunks % 8)  // chunks of the last atom that no part fills stay zero
+    for (int e = tid; e < S * kRows * (8 - W::kChunks % 8); e += kThreads) {
+      const int c = W::kChunks % 8 + e % (8 - W::kChunks % 8), r = e / (8 - W::kChunks % 8);
+      const uint32_t at = chunk_at(ring + r / kRows * W::kStageBytes + (1 + W::kAtoms) * kAtom, r % kRows, c);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+    }
   if (tid == 0) {
     mbar_init(bar, 1);
     mbar_init(bar + 8, 1);
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
 
   auto fill = [&](int i) {
     if (i < n) {
-      const uint32_t st = ring + (i % S) * kStageBytes;
+      const uint32_t st = ring + (i % S) * W::kStageBytes;
       const int ch = tid & 15;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
@@ -112,40 +120,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
         load_chunk<uint16_t>(chunk_at(st + (ch >> 3) * kAtom, r, ch & 7), t < pc.z ? Q + (int64_t)rows[t] * ldq : nullptr,
                              m0 + ch * 8, N, how, a.plan.head);
       }
+#pragma unroll
+      for (int j = 0; j < (kRows * W::kChunks + kThreads - 1) / kThreads; j++) {
+        const int e = tid + j * kThreads, r = e / W::kChunks, c = e % W::kChunks, t = i * kRows + r;
+        if (e < kRows * W::kChunks)
+          copy16(chunk_at(st + (2 + (c >> 3)) * kAtom, r, c & 7), P + (t < pc.z ? t : 0) * (3 * MP) + c * 8, t < pc.z);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  constexpr int kPairs = kRows * MP / 2 / kThreads;  // of a thread, neighbouring ranks
-  float2 pv[kPairs];
-  auto take = [&](int i) {
-#pragma unroll
-    for (int j = 0; j < kPairs; j++) {
-      const int e = tid + j * kThreads, r = e % (MP / 2) * 2, t = i * kRows + e / (MP / 2);
-      pv[j] = make_float2(0.0f, 0.0f);
-      if (t < pc.z && r < R) {
-        const float* p = P + (int64_t)rows[t] * R + r;
-        if (a.pairs) {
-          pv[j] = *reinterpret_cast<const float2*>(p);
-        } else {
-          pv[j].x = p[0];
-          if (r + 1 < R) pv[j].y = p[1];
-        }
-      }
-    }
-  };
-  auto put = [&](int i) {
-    const uint32_t base = parts + (i & 1) * W::kPartBytes;
-#pragma unroll
-    for (int j = 0; j < kPairs; j++) {
-      const int e = tid + j * kThreads, r = e % (MP / 2) * 2, t = e / (MP / 2);
-      uint32_t p[3];
-      split_pair<3>(pv[j], p);
-#pragma unroll
-      for (int x = 0; x < 3; x++) {
-        const int m = x * MP + r;
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(chunk_at(base + m / 64 * kAtom, t, m % 64 / 8) + m % 8 * 2), "r"(p[x]) : "memory");
-      }
-    }
   };
   // accumulator row 32 (warp % 4) + lane, columns 64 (warp / 4) ..
   float sum[64];
@@ -167,33 +149,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
   };
 #pragma unroll
   for (int i = 0; i < S - 1; i++) fill(i);
-  take(0);
-  put(0);
   bool good = true;
   int i = 0;
   for (; i < n; i++) {
-    if (i + 1 < n) take(i + 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (__syncthreads_or(!good)) break;
     if (tid == 0) {
       tc_fence_after();
       const uint32_t d = tmem + (i / kFlush & 1) * kSlab;
-      const uint32_t qa = ring + (i % S) * kStageBytes, pa = parts + (i & 1) * W::kPartBytes;
+      const uint32_t qa = ring + (i % S) * W::kStageBytes, pa = qa + 2 * kAtom;
 #pragma unroll
       for (int ks = 0; ks < kRows / 16; ks++)
 #pragma unroll
         for (int x = W::kMmas - 1; x >= 0; x--)
-          tc_mma_f16(d, operand(pa + x * 2 * kAtom + ks * 2048), operand(qa + ks * 2048), kIdesc,
-                     i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+          tc_mma_f16(d, operand(pa + x * 2 * kAtom + ks * 2048, 2 * x + 1 < W::kAtoms ? kAtom : zero - (pa + x * 2 * kAtom)),
+                     operand(qa + ks * 2048, kAtom), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
       tc_commit(bar + 8 * (i & 1));
     }
-    if (i > 0) {  // the stage before: its ring slot and parts are free, and its sums complete
+    if (i > 0) {  // the stage before: its ring slot is free, its sums complete
       good = wait_mma(bar + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
       if (i % kFlush == 0) flush(i / kFlush - 1);
     }
     fill(i + S - 1);
-    if (i + 1 < n) put(i + 1);
   }
   if (i == n && n > 0) {
     good = wait_mma(bar + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
@@ -244,8 +222,7 @@ cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
 
 }  // namespace
 
-cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, LoraWgradArgs a) {
-  a.pairs = a.R % 2 == 0 && reinterpret_cast<uintptr_t>(a.p[0]) % 8 == 0 && reinterpret_cast<uintptr_t>(a.p[1]) % 8 == 0;
+cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, const LoraWgradArgs& a) {
   return a.R <= 16 ? run<16>(lc, a) : a.R <= 32 ? run<32>(lc, a) : a.R <= 64 ? run<64>(lc, a) : run<128>(lc, a);
 }
 
