@@ -7,7 +7,8 @@
 // Rows stream through a ring of shared memory stages of 16, gathered by
 // asynchronous copies; they and u or v are split into three bf16 parts each,
 // so that the products on the tensor cores keep 24 bits.  A warp holds 16
-// ranks x 64 columns.  The tensor cores' fp32 sums cut where they
+// ranks x 16 columns: splitting takes it longer than multiplying, and gates'
+// logits have few columns (60 of them, 2000 rows: 25 us with 64 a warp, 9 with 16).  The tensor cores' fp32 sums cut where they
 // should round, so every other stage they move to registers that add with
 // rounding.  Adapters of several pieces leave partial sums, added in order by
 // a second kernel, which also clears the gradients of adapters without rows.
@@ -16,25 +17,26 @@
 namespace {
 
 constexpr int kRows = 16;  // of a stage
+constexpr int kCols = 16, kTiles = kCols / 8;  // of a warp
 
-// rank groups of 16 x column groups of 64: one warp each
+// rank groups of 16 x column groups of 16: one warp each
 template <int RG>
 struct Wg {
   static constexpr int kCg = RG == 1 ? 8 : RG <= 4 ? 4 : 2;
   static constexpr int kThreads = RG * kCg * 32;
-  static constexpr int kSlab = kCg * 64;
+  static constexpr int kSlab = kCg * kCols;
   static constexpr int kStageBytes = kRows * kSlab * 4;
-  static constexpr int kStages = RG == 1 ? 3 : 6;
+  static constexpr int kStages = 6;
   static constexpr int kPStride = RG * 16 + 8;                 // bf16 of a row's parts
   static constexpr int kPartBytes = 3 * kRows * kPStride * 2;  // one stage's
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kBytes = kRing + 2 * kPartBytes;
-  static constexpr int kCtas = kThreads == 256 ? 2 : 1;
+  static constexpr int kCtas = kThreads == 256 ? 3 : 1;
 };
 
 template <int RG>
 __device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, const int4& pc, int rg, int m0, int lane,
-                                           const float (&sum)[8][4]) {
+                                           const float (&sum)[kTiles][4]) {
   const int N = a.N[which], g = lane >> 2, c = lane & 3;
   const float scale = a.scale ? a.scale[pc.x] : 1.0f;
   float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * a.R * N : a.part[which] + (int64_t)pc.w * a.R * N;
@@ -44,7 +46,7 @@ __device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, co
     if (r >= a.R) continue;
     float* d = out + (int64_t)r * N;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
+    for (int j = 0; j < kTiles; j++) {
       const int col = m0 + j * 8 + 2 * c;
       const float v0 = scale * sum[j][2 * h], v1 = scale * sum[j][2 * h + 1];
       if (N % 2 == 0) {
@@ -66,7 +68,7 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
   constexpr int kChunks = W::kSlab / 4;      // of a row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int rg = warp % RG, cg = warp / RG;
-  const int N = a.N[which], m0 = slab * W::kSlab + cg * 64;
+  const int N = a.N[which], m0 = slab * W::kSlab + cg * kCols;
   const uint32_t ring = smem_u32(smem), parts = ring + W::kRing;
   const float* Q = reinterpret_cast<const float*>(a.q[which]);
   const float* P = a.p[which];
@@ -110,9 +112,9 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
                      "h"(p[x]) : "memory");
     }
   };
-  float acc[8][4], sum[8][4];
+  float acc[kTiles][4], sum[kTiles][4];
 #pragma unroll
-  for (int j = 0; j < 8; j++)
+  for (int j = 0; j < kTiles; j++)
 #pragma unroll
     for (int x = 0; x < 4; x++) acc[j][x] = sum[j][x] = 0.0f;
 #pragma unroll
@@ -133,8 +135,8 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
         for (int x = 0; x < 3; x++)
           ldsm4t(ps + ((x * kRows + ks * 16 + (lane & 7) + (lane >> 4) * 8) * W::kPStride + rg * 16 + ((lane >> 3) & 1) * 8) * 2, p[x]);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          const int col = cg * 64 + j * 8 + g;
+        for (int j = 0; j < kTiles; j++) {
+          const int col = cg * kCols + j * 8 + g;
           const uint32_t t = st + col / kCB * (kRows * kLoraRowBytes);
           uint32_t b[kQ][2];
 #pragma unroll
@@ -157,7 +159,7 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
       }
       if (i & 1) {
 #pragma unroll
-        for (int j = 0; j < 8; j++)
+        for (int j = 0; j < kTiles; j++)
 #pragma unroll
           for (int x = 0; x < 4; x++) {
             sum[j][x] += acc[j][x];
@@ -169,7 +171,7 @@ __device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int sla
   }
   if (m0 < N) {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
+    for (int j = 0; j < kTiles; j++)
 #pragma unroll
       for (int x = 0; x < 4; x++) sum[j][x] += acc[j][x];
     store_sums<RG>(a, which, pc, rg, m0, lane, sum);
