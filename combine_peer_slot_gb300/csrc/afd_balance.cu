@@ -6,7 +6,11 @@
 //   p_te = softmax(l_t)_e, or s_te / sum_e s_te with s = 1 / (1 + exp(-l))
 //   loss_s = E / (k n_s^2) sum_e counts_se sum_{t in s} p_te
 //
-// A warp takes a row: lane l holds the experts [l PER, (l + 1) PER).
+// A row is LANES lanes of eight neighbouring experts: 8, 16 or 32 lanes for up
+// to 64, 128 or 256 experts, so a warp holds 4, 2 or 1 rows and a row's sums
+// take 3 to 5 exchanges for four rows at a time (with a warp to a row of 64 the
+// exchanges were most of the instructions).  Each pass loads the next row's
+// logits before it computes with the present one's: bound by memory latency.
 #include <cooperative_groups.h>
 
 #include "afd_internal.cuh"
@@ -15,7 +19,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kFinal = 8;  // CTAs that finish one sequence: 32 experts each
+constexpr int kPer = 8;     // experts of a lane
+constexpr int kFinal = 8;   // most CTAs that finish one sequence: 32 experts each
+constexpr int kWarps = 16;  // of a block of k_balance
+constexpr int kMaxChunks = 320;
 
 struct GateArgs {
   const void* logits;
@@ -23,7 +30,7 @@ struct GateArgs {
   const int32_t* ids;
   const int32_t* off;  // [S + 1], or NULL: one sequence of all rows
   int n, E, k, S, sigmoid;
-  int vec;             // a lane's run of logits can be loaded whole
+  int vec;             // rows of logits can be loaded 16 bytes at a time
   // forward
   float* loss;
   int32_t* counts;     // backward: read
@@ -51,34 +58,24 @@ __device__ __forceinline__ float load_one<uint16_t>(const void* p, int64_t i) {
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
 }
 
-template <int BYTES>
-struct Run;
-template <>
-struct Run<4> { typedef uint32_t T; };
-template <>
-struct Run<8> { typedef uint2 T; };
-template <>
-struct Run<16> { typedef uint4 T; };
-
-// PER neighbouring logits of a row; experts past the last one read as -inf
-template <typename LT, int PER>
-__device__ __forceinline__ void load_row(const void* p, int64_t i0, int have, int vec, float (&v)[PER]) {
-  if (vec && have >= PER) {
-    constexpr int kBytes = PER * (int)sizeof(LT) < 16 ? PER * (int)sizeof(LT) : 16;
-    typedef typename Run<kBytes>::T V;
+// a lane's eight logits of a row; experts past the last one read as -inf
+template <typename LT>
+__device__ __forceinline__ void load_row(const void* p, int64_t i0, int have, int vec, float (&v)[kPer]) {
+  if (vec && have >= kPer) {
+    constexpr int kQ = kPer * (int)sizeof(LT) / 16;
     union {
-      V q[PER * sizeof(LT) / kBytes];
-      LT e[PER];
+      uint4 q[kQ];
+      LT e[kPer];
     } u;
-    const V* s = reinterpret_cast<const V*>(reinterpret_cast<const LT*>(p) + i0);
+    const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const LT*>(p) + i0);
 #pragma unroll
-    for (int i = 0; i < (int)(PER * sizeof(LT) / kBytes); i++) u.q[i] = s[i];
+    for (int i = 0; i < kQ; i++) u.q[i] = s[i];
 #pragma unroll
-    for (int i = 0; i < PER; i++) v[i] = load_one<LT>(u.e, i);
+    for (int i = 0; i < kPer; i++) v[i] = load_one<LT>(u.e, i);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < PER; i++) v[i] = i < have ? load_one<LT>(p, i0 + i) : -INFINITY;
+  for (int i = 0; i < kPer; i++) v[i] = i < have ? load_one<LT>(p, i0 + i) : -INFINITY;
 }
 
 template <typename LT>
@@ -90,41 +87,45 @@ __device__ __forceinline__ uint16_t rounded<uint16_t>(float v) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-template <typename LT, int PER>
-__device__ __forceinline__ void store_row(void* p, int64_t i0, int have, int vec, const float (&v)[PER]) {
+template <typename LT>
+__device__ __forceinline__ void store_row(void* p, int64_t i0, int have, int vec, const float (&v)[kPer]) {
   LT* d = reinterpret_cast<LT*>(p) + i0;
-  if (vec && have >= PER) {
-    constexpr int kBytes = PER * (int)sizeof(LT) < 16 ? PER * (int)sizeof(LT) : 16;
-    typedef typename Run<kBytes>::T V;
+  if (vec && have >= kPer) {
+    constexpr int kQ = kPer * (int)sizeof(LT) / 16;
     union {
-      V q[PER * sizeof(LT) / kBytes];
-      LT e[PER];
+      uint4 q[kQ];
+      LT e[kPer];
     } u;
 #pragma unroll
-    for (int i = 0; i < PER; i++) u.e[i] = rounded<LT>(v[i]);
+    for (int i = 0; i < kPer; i++) u.e[i] = rounded<LT>(v[i]);
 #pragma unroll
-    for (int i = 0; i < (int)(PER * sizeof(LT) / kBytes); i++) reinterpret_cast<V*>(d)[i] = u.q[i];
+    for (int i = 0; i < kQ; i++) reinterpret_cast<uint4*>(d)[i] = u.q[i];
     return;
   }
 #pragma unroll
-  for (int i = 0; i < PER; i++)
+  for (int i = 0; i < kPer; i++)
     if (i < have) d[i] = rounded<LT>(v[i]);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// over the lanes of a row
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int LANES>
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-// s = 1 / (1 + exp(-l)) and 1 - s, each to fp32's precision of itself
+// s = 1 / (1 + exp(-l)) and 1 - s, each to fp32's precision of itself; the
+// denominator is between 1 and 2, where the quotient's short form is within an
+// ulp (the full one is a third of the row's instructions)
 __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
-  const float e = expf(-fabsf(l)), r = 1.0f / (1.0f + e), q = e * r;
+  const float e = expf(-fabsf(l)), r = __fdividef(1.0f, 1.0f + e), q = e * r;
   s = l >= 0.0f ? r : q;  // (NaN: q, which is NaN)
   rest = l >= 0.0f ? q : r;
 }
@@ -137,37 +138,45 @@ struct RowSum {
 // p of a row from its logits.  sigmoid: rest = 1 - s as well.  A row of -inf
 // has p = 0.  Scores whose sum nears fp32's smallest number come from logits
 // under -60, where s = exp(l) (1 - 1e-26): their shares are the softmax's.
-template <int PER>
-__device__ __forceinline__ RowSum shares(const float (&l)[PER], int sigmoid, float (&p)[PER], float (&rest)[PER]) {
+template <int LANES>
+__device__ __forceinline__ RowSum shares(const float (&l)[kPer], int sigmoid, float (&p)[kPer], float (&rest)[kPer]) {
   RowSum r{0.0f, 0.0f};
+  bool small = true;
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
+    for (int i = 0; i < kPer; i++) {
       sigmoid_pair(l[i], p[i], rest[i]);
       r.z += p[i];
     }
-    r.z = warp_sum(r.z);
-    if (!(r.z < 1e-30f)) {
+    r.z = row_sum<LANES>(r.z);
+    small = r.z < 1e-30f;
+    if (!__any_sync(0xffffffffu, small)) {
       const float inv = 1.0f / r.z;
 #pragma unroll
-      for (int i = 0; i < PER; i++) p[i] *= inv;
+      for (int i = 0; i < kPer; i++) p[i] *= inv;
       return r;
     }
   }
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; i++) top = fmaxf(top, l[i]);
-  r.top = warp_max(top);
-  r.z = 0.0f;
+  for (int i = 0; i < kPer; i++) top = fmaxf(top, l[i]);
+  top = row_max<LANES>(top);
+  float z = 0.0f, x[kPer];
 #pragma unroll
-  for (int i = 0; i < PER; i++) {
-    p[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - r.top);
-    r.z += p[i];
+  for (int i = 0; i < kPer; i++) {
+    x[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
+    z += x[i];
   }
-  r.z = warp_sum(r.z);
+  z = row_sum<LANES>(z);
+  if (small) {  // (the warp's other rows keep their sigmoids)
+    r.top = top;
+    r.z = z;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) p[i] = x[i];
+  }
   const float inv = r.z == 0.0f ? 0.0f : 1.0f / r.z;
 #pragma unroll
-  for (int i = 0; i < PER; i++) p[i] *= inv;
+  for (int i = 0; i < kPer; i++) p[i] *= inv;
   return r;
 }
 
@@ -181,46 +190,72 @@ __device__ __forceinline__ void sequence(const GateArgs& a, int s, int& lo, int&
   }
 }
 
-// E / (k n^2) sum_e counts p, over the 32 WARPS' values of one block
+// E / (k n^2) sum_e counts p
 __device__ __forceinline__ float loss_of(const GateArgs& a, int rows, double dot) {
   return rows ? (float)(dot * (double)a.E / ((double)a.k * (double)rows * (double)rows)) : 0.0f;
 }
 
-// Block (c, s): the rows lo + c, lo + c + chunks, .. of sequence s, a warp
-// each.  One chunk: the sequence's loss at once; else its share of the sums.
-// Sums of p: at most rows / (warps chunks) terms in a lane's fp32 chain, then
-// the warps' in order.  Counts are whole numbers, so their order is free.
-template <typename LT, int PER, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) k_balance(const __grid_constant__ GateArgs a) {
-  __shared__ float sums[WARPS][32 * PER];
-  __shared__ int32_t cnt[32 * PER];
-  __shared__ double dots[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER, have = a.E - e0;
-  const int s = blockIdx.y, c = blockIdx.x;
-  for (int e = threadIdx.x; e < 32 * PER; e += WARPS * 32) cnt[e] = 0;
+// A sequence's rows are shared by `chunks` blocks of kWarps warps.  One chunk:
+// its loss at once; else a block's share of the sums.  Sums of p: a lane's fp32
+// chain over its rows, then the warp's rows and the warps in order.  Counts
+// are whole numbers, so their order is free.
+template <typename LT, int LANES>
+__global__ void __launch_bounds__(kWarps * 32) k_balance(const __grid_constant__ GateArgs a) {
+  constexpr int kE = LANES * kPer, kAtOnce = 32 / LANES, kIds = LANES < 16 ? 2 : 1;
+  __shared__ float sums[kWarps][kE];
+  __shared__ int32_t cnt[kE];
+  __shared__ double dots[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
+  const int e0 = sub * kPer, have = a.E - e0, s = blockIdx.y, c = blockIdx.x;
+  for (int e = threadIdx.x; e < kE; e += kWarps * 32) cnt[e] = 0;
+  if (a.chunks > 1) cudaTriggerProgrammaticLaunchCompletion();  // (the second kernel waits for this one's end)
   int lo, hi;
   sequence(a, s, lo, hi);
   __syncthreads();
-  float acc[PER];
+  float acc[kPer];
 #pragma unroll
-  for (int i = 0; i < PER; i++) acc[i] = 0.0f;
-  for (int64_t row = (int64_t)lo + c * WARPS + warp; row < hi; row += (int64_t)a.chunks * WARPS) {
-    float l[PER], p[PER], rest[PER];
-    load_row<LT, PER>(a.logits, row * a.ld + e0, have, a.vec, l);
-    const int id = lane < a.k ? a.ids[row * a.k + lane] : -1;
-    shares<PER>(l, a.sigmoid, p, rest);
+  for (int i = 0; i < kPer; i++) acc[i] = 0.0f;
+  const int64_t step = (int64_t)a.chunks * kWarps * kAtOnce;
+  int64_t row = (int64_t)lo + (c * kWarps + warp) * kAtOnce + lane / LANES;
+  float next[kPer];
+  int nid[kIds];
+  auto load = [&](int64_t at) {
+    const bool in = at < hi;
+    load_row<LT>(a.logits, in ? at * a.ld + e0 : 0, in ? have : 0, a.vec, next);
 #pragma unroll
-    for (int i = 0; i < PER; i++) acc[i] += p[i];
-    if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1);
+    for (int j = 0; j < kIds; j++) nid[j] = in && sub + j * LANES < a.k ? a.ids[at * a.k + sub + j * LANES] : -1;
+  };
+  // (the same passes for all rows of the warp: the first one's)
+  const int64_t passes = max((int64_t)0, ((int64_t)hi - (row - lane / LANES) + step - 1) / step);
+  if (passes) load(row);
+  for (int64_t i = 0; i < passes; i++) {
+    float l[kPer], p[kPer], rest[kPer];
+    int id[kIds];
+#pragma unroll
+    for (int x = 0; x < kPer; x++) l[x] = next[x];
+#pragma unroll
+    for (int j = 0; j < kIds; j++) id[j] = nid[j];
+    row += step;
+    if (i + 1 < passes) load(row);
+    shares<LANES>(l, a.sigmoid, p, rest);
+#pragma unroll
+    for (int x = 0; x < kPer; x++) acc[x] += p[x];
+#pragma unroll
+    for (int j = 0; j < kIds; j++)
+      if (id[j] >= 0 && id[j] < a.E) atomicAdd(&cnt[id[j]], 1);
   }
 #pragma unroll
-  for (int i = 0; i < PER; i++) sums[warp][e0 + i] = acc[i];
+  for (int x = 0; x < kPer; x++) {
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], o);
+    if (lane < LANES) sums[warp][e0 + x] = acc[x];
+  }
   __syncthreads();
   double dot = 0.0;
-  for (int e = threadIdx.x; e < a.E; e += WARPS * 32) {
+  for (int e = threadIdx.x; e < a.E; e += kWarps * 32) {
     float v = 0.0f;
-#pragma unroll 8
-    for (int w = 0; w < WARPS; w++) v += sums[w][e];
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) v += sums[w][e];
     if (a.chunks > 1) {
       const int64_t at = ((int64_t)s * a.chunks + c) * a.E + e;
       a.part[at] = v;
@@ -237,43 +272,50 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance(const __grid_constant__ 
   __syncthreads();
   if (threadIdx.x == 0) {
     double v = 0.0;
-    for (int w = 0; w < WARPS; w++) v += dots[w];
+    for (int w = 0; w < (a.E + 31) / 32; w++) v += dots[w];
     a.loss[s] = loss_of(a, hi - lo, v);
   }
 }
 
 // The chunks' sums to counts and loss: a cluster per sequence, CTA q the
-// experts [32 q, 32 q + 32), lane = expert, warps stride the chunks; sums in
-// 64 bits, in a fixed order.
-__global__ void __cluster_dims__(kFinal, 1, 1) __launch_bounds__(256) k_balance_finish(const __grid_constant__ GateArgs a) {
-  __shared__ double sums[8][32];
-  __shared__ int32_t cnts[8][32];
+// experts [32 q, 32 q + 32), lane = expert, warps stride the chunks, all in a
+// fixed order: fp32 over the chunks (at most 10 terms a warp and 32 warps),
+// 64 bits over the experts.
+__global__ void __launch_bounds__(1024) k_balance_finish(const __grid_constant__ GateArgs a) {
+  __shared__ float sums[32][32];
+  __shared__ int32_t cnts[32][33];
   __shared__ double dot_of[kFinal];
   cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = blockIdx.x, s = blockIdx.y;
   const int e = q * 32 + lane;
   cudaGridDependencySynchronize();
-  double v = 0.0;
+  float v = 0.0f;
   int32_t n = 0;
   if (e < a.E) {
     const float* p = a.part + (int64_t)s * a.chunks * a.E + e;
-    const int32_t* m = reinterpret_cast<const int32_t*>(a.part) + (int64_t)a.S * a.chunks * a.E + (int64_t)s * a.chunks * a.E + e;
-#pragma unroll 4
-    for (int c = warp; c < a.chunks; c += 8) {
-      v += (double)p[(int64_t)c * a.E];
-      n += m[(int64_t)c * a.E];
+    const int32_t* m = reinterpret_cast<const int32_t*>(a.part) + (int64_t)(a.S + s) * a.chunks * a.E + e;
+#pragma unroll
+    for (int i = 0; i < kMaxChunks / 32; i++) {
+      const int c = warp + i * 32;
+      if (c < a.chunks) {
+        v += p[(int64_t)c * a.E];
+        n += m[(int64_t)c * a.E];
+      }
     }
   }
   sums[warp][lane] = v;
   cnts[warp][lane] = n;
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < 8; w++) {
+    v = 0.0f;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < 32; w++) {
       v += sums[w][lane];
       n += cnts[w][lane];
     }
     if (e < a.E) a.counts[(int64_t)s * a.E + e] = n;
-    double dot = v * (double)n;
+    double dot = (double)v * (double)n;
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) *cluster.map_shared_rank(&dot_of[q], 0) = dot;
@@ -281,7 +323,7 @@ __global__ void __cluster_dims__(kFinal, 1, 1) __launch_bounds__(256) k_balance_
   cluster.sync();
   if (q == 0 && threadIdx.x == 0) {
     double d = 0.0;
-    for (int i = 0; i < kFinal; i++) d += dot_of[i];
+    for (int i = 0; i < (int)gridDim.x; i++) d += dot_of[i];
     int lo, hi;
     sequence(a, s, lo, hi);
     a.loss[s] = loss_of(a, hi - lo, d);
@@ -296,167 +338,227 @@ __global__ void __cluster_dims__(kFinal, 1, 1) __launch_bounds__(256) k_balance_
 //   w_j = c s_j / sum s_i:  share_j (d w_j - sum share d w) c, through log s
 // Chosen shares come from their own logits, so that a row whose chosen scores
 // are all tiny keeps its precision.
-template <typename LT, int PER>
-__global__ void __launch_bounds__(256) k_route_backward(const __grid_constant__ GateArgs a) {
-  __shared__ float added[8][32 * PER];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER, have = a.E - e0;
-  float* add = added[warp];
+template <typename LT, int LANES>
+__global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant__ GateArgs a) {
+  constexpr int kE = LANES * kPer, kAtOnce = 32 / LANES, kIds = LANES < 16 ? 2 : 1;
+  __shared__ float added[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
+  const int e0 = sub * kPer, have = a.E - e0;
+  float* add = added[warp] + lane / LANES * kE;
 #pragma unroll
-  for (int i = 0; i < PER; i++) add[e0 + i] = 0.0f;
+  for (int i = 0; i < kPer; i++) add[e0 + i] = 0.0f;
   __syncwarp();
   const int64_t first = (int64_t)blockIdx.x * a.per_block;
   const int64_t last = min((int64_t)a.n, first + a.per_block);
   int seq = -1, lo = 0, hi = 0;  // the sequence of g
-  int next = 0;                  // the first sequence that may hold the row
-  float g[PER];
+  int search = 0;                // the first sequence that may hold the row
+  float g[kPer];
 #pragma unroll
-  for (int i = 0; i < PER; i++) g[i] = 0.0f;
-  if (a.dloss && a.off) {  // the last sequence that starts at or before the first row
-    int b = 0, e = a.S;
-    while (e - b > 1) {
-      const int m = (b + e) / 2;
-      if (a.off[m] <= first) b = m; else e = m;
-    }
-    next = b;
-  }
-  for (int64_t row = first + warp; row < last; row += 8) {
-    float l[PER], p[PER], rest[PER];
-    load_row<LT, PER>(a.logits, row * a.ld + e0, have, a.vec, l);
-    int id = -1;
-    float dw = 0.0f, my_l = -INFINITY;
-    if (a.dw && lane < a.k) {
-      id = a.ids[row * a.k + lane];
-      if (id < 0 || id >= a.E) id = -1;
-      if (id >= 0) {
-        dw = a.dw[row * a.k + lane] * a.scale;
-        my_l = load_one<LT>(a.logits, row * a.ld + id);
+  for (int i = 0; i < kPer; i++) g[i] = 0.0f;
+  float next[kPer], ndw[kIds], nl[kIds];
+  int nid[kIds];
+  auto load = [&](int64_t at) {
+    const bool in = at < last;
+    load_row<LT>(a.logits, in ? at * a.ld + e0 : 0, in ? have : 0, a.vec, next);
+#pragma unroll
+    for (int j = 0; j < kIds; j++) {
+      int id = -1;
+      if (a.dw && in && sub + j * LANES < a.k) {
+        id = a.ids[at * a.k + sub + j * LANES];
+        if (id < 0 || id >= a.E) id = -1;
       }
+      nid[j] = id;
+      ndw[j] = id >= 0 ? a.dw[at * a.k + sub + j * LANES] * a.scale : 0.0f;
+      nl[j] = id >= 0 ? load_one<LT>(a.logits, at * a.ld + id) : -INFINITY;
     }
-    if (a.dloss && !(seq >= 0 && row >= lo && row < hi)) {
+  };
+  int64_t row = first + warp * kAtOnce + lane / LANES;
+  load(row);
+  if (a.dloss && a.off) {  // the last sequence that starts at or before the first row
+    if (a.S <= 32) {
+      search = __popc(__ballot_sync(0xffffffffu, lane > 0 && lane < a.S && a.off[lane] <= first));
+    } else {
+      int b = 0, e = a.S;
+      while (e - b > 1) {
+        const int m = (b + e) / 2;
+        if (a.off[m] <= first) b = m; else e = m;
+      }
+      search = b;
+    }
+  }
+  for (int64_t base = first + warp * kAtOnce; base < last; base += 8 * kAtOnce, row += 8 * kAtOnce) {
+    float l[kPer], p[kPer], rest[kPer], dw[kIds], my_l[kIds];
+    int id[kIds];
+#pragma unroll
+    for (int i = 0; i < kPer; i++) l[i] = next[i];
+#pragma unroll
+    for (int j = 0; j < kIds; j++) {
+      id[j] = nid[j];
+      dw[j] = ndw[j];
+      my_l[j] = nl[j];
+    }
+    load(row + 8 * kAtOnce);
+    const bool in = row < last;
+    if (a.dloss && __any_sync(0xffffffffu, in && !(seq >= 0 && row >= lo && row < hi))) {
       int found = -1;
-      for (; next < a.S; next++) {
-        sequence(a, next, lo, hi);
+      for (; in && search < a.S; search++) {
+        sequence(a, search, lo, hi);
         if (row < lo) break;
         if (row < hi) {
-          found = next;
+          found = search;
           break;
         }
       }
       seq = found;
-      if (seq >= 0) {
-        int32_t n[PER];
-        int64_t total = 0;
+      int32_t n[kPer];
+      int64_t all = 0;
 #pragma unroll
-        for (int i = 0; i < PER; i++) {
-          n[i] = i < have ? a.counts[(int64_t)seq * a.E + e0 + i] : 0;
-          total += n[i];
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        const float rows = (float)(hi - lo), f = a.dloss[seq] / ((float)a.k * rows) / rows;
-#pragma unroll
-        for (int i = 0; i < PER; i++) g[i] = (float)((int64_t)n[i] * a.E - total) * f;
-      } else {
-#pragma unroll
-        for (int i = 0; i < PER; i++) g[i] = 0.0f;
+      for (int i = 0; i < kPer; i++) {
+        n[i] = seq >= 0 && i < have ? a.counts[(int64_t)seq * a.E + e0 + i] : 0;
+        all += n[i];
       }
+#pragma unroll
+      for (int o = LANES / 2; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      const float rows = (float)(hi - lo), f = seq >= 0 ? a.dloss[seq] / ((float)a.k * rows) / rows : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; i++) g[i] = seq >= 0 ? (float)((int64_t)n[i] * a.E - all) * f : 0.0f;
     }
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < PER; i++) bad |= l[i] != l[i] || (!a.sigmoid && l[i] == INFINITY);
-    const RowSum r = shares<PER>(l, a.sigmoid, p, rest);
+    for (int i = 0; i < kPer; i++) bad |= l[i] != l[i] || (!a.sigmoid && l[i] == INFINITY);
+    const uint32_t bad_lanes = __ballot_sync(0xffffffffu, bad);
+    const RowSum r = shares<LANES>(l, a.sigmoid, p, rest);
     float inner = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; i++) inner += p[i] * g[i];
-    inner = warp_sum(inner);
-    float part = 0.0f;
+    for (int i = 0; i < kPer; i++) inner += p[i] * g[i];
+    inner = row_sum<LANES>(inner);
     if (a.dw) {
-      float s = 0.0f, my_rest = 1.0f;
-      if (a.sigmoid) sigmoid_pair(my_l, s, my_rest);
+      float s[kIds], my_rest[kIds], part[kIds];
+#pragma unroll
+      for (int j = 0; j < kIds; j++) {
+        s[j] = 0.0f;
+        my_rest[j] = 1.0f;
+        if (a.sigmoid) sigmoid_pair(my_l[j], s[j], my_rest[j]);
+      }
       if (a.renorm) {
-        float total = a.sigmoid ? warp_sum(s) : 0.0f;
-        if (!a.sigmoid || total < 1e-30f) {
-          const float top = warp_max(my_l);
-          // (under -745 the scores are 0 in fp64 too, and so are the weights)
-          s = my_l == -INFINITY || (!a.sigmoid && top - r.top < -745.0f) ? 0.0f : expf(my_l - top);
-          total = warp_sum(s);
+        float total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kIds; j++) total += s[j];
+        total = a.sigmoid ? row_sum<LANES>(total) : 0.0f;
+        const bool small = !a.sigmoid || total < 1e-30f;
+        if (__any_sync(0xffffffffu, small)) {
+          float top = my_l[0], z = 0.0f, x[kIds];
+          if (kIds == 2) top = fmaxf(top, my_l[kIds - 1]);
+          top = row_max<LANES>(top);
+#pragma unroll
+          for (int j = 0; j < kIds; j++) {
+            // (under -745 the scores are 0 in fp64 too, and so are the weights)
+            x[j] = my_l[j] == -INFINITY || (!a.sigmoid && top - r.top < -745.0f) ? 0.0f : expf(my_l[j] - top);
+            z += x[j];
+          }
+          z = row_sum<LANES>(z);
+          if (small) {
+            total = z;
+#pragma unroll
+            for (int j = 0; j < kIds; j++) s[j] = x[j];
+          }
         }
-        const float share = total == 0.0f ? 0.0f : s / total;
-        part = share * (dw - warp_sum(share * dw));
-        if (a.sigmoid) part *= my_rest;
+        float mean = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kIds; j++) {
+          s[j] = total == 0.0f ? 0.0f : s[j] / total;
+          mean += s[j] * dw[j];
+        }
+        mean = row_sum<LANES>(mean);
+#pragma unroll
+        for (int j = 0; j < kIds; j++) part[j] = s[j] * (dw[j] - mean) * my_rest[j];
       } else if (a.sigmoid) {
-        part = s * my_rest * dw;
+#pragma unroll
+        for (int j = 0; j < kIds; j++) part[j] = s[j] * my_rest[j] * dw[j];
       } else {
-        s = my_l == -INFINITY ? 0.0f : expf(my_l - r.top) / r.z;
-        part = s * dw;
-        inner += warp_sum(part);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kIds; j++) {
+          part[j] = my_l[j] == -INFINITY ? 0.0f : expf(my_l[j] - r.top) / r.z * dw[j];
+          sum += part[j];
+        }
+        inner += row_sum<LANES>(sum);
       }
       // to the experts' lanes; an id that stands twice in a row is added twice
-      const uint32_t same = __match_any_sync(0xffffffffu, id >= 0 ? id : ~lane);
-      if (__any_sync(0xffffffffu, (same & (same - 1)) != 0u)) {
-        for (int j = 0; j < a.k; j++) {
-          if (lane == j && id >= 0) add[id] += part;
-          __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kIds; j++) {
+        const uint32_t same = __match_any_sync(0xffffffffu, id[j] >= 0 ? lane / LANES * 256 + id[j] : ~lane);
+        if (__any_sync(0xffffffffu, (same & (same - 1)) != 0u)) {
+          for (int x = 0; x < LANES; x++) {
+            if (sub == x && id[j] >= 0) add[id[j]] += part[j];
+            __syncwarp();
+          }
+        } else if (id[j] >= 0) {
+          add[id[j]] += part[j];
         }
-      } else if (id >= 0) {
-        add[id] = part;
+        __syncwarp();
       }
-      __syncwarp();
     }
     const float nan = __int_as_float(0x7fc00000);
-    bad = __any_sync(0xffffffffu, bad);
-    float d[PER];
+    bad = (bad_lanes >> (lane / LANES * LANES) & (LANES == 32 ? 0xffffffffu : (1u << (LANES & 31)) - 1u)) != 0u;
+    float d[kPer];
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
+    for (int i = 0; i < kPer; i++) {
       d[i] = p[i] * (g[i] - inner);
       if (a.sigmoid) d[i] *= rest[i];
       if (a.dw) d[i] += add[e0 + i];
       if (bad) d[i] = nan;
     }
-    store_row<LT, PER>(a.d, row * a.ldd + e0, have, a.dvec, d);
+    if (in) store_row<LT>(a.d, row * a.ldd + e0, have, a.dvec, d);
     if (a.dw) {
       __syncwarp();
-      if (id >= 0) add[id] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kIds; j++)
+        if (id[j] >= 0) add[id[j]] = 0.0f;
       __syncwarp();
     }
   }
 }
 
-// A lane's run of PER elements of LT can be moved whole from this matrix.
-template <typename LT, int PER>
-int whole(const void* p, int64_t ld) {
-  const uintptr_t run = std::min<uintptr_t>(16, PER * sizeof(LT));
-  return reinterpret_cast<uintptr_t>(p) % run == 0 && ld * (int64_t)sizeof(LT) % (int64_t)run == 0;
+// rows can be moved 16 bytes at a time, eight elements a lane
+int whole(const void* p, int64_t ld, int size) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
 
+// Blocks that share a sequence.  Up to 512 rows one block each finishes at
+// once; more rows take the second kernel, with one pass over its warps' rows to
+// each block and at most kMaxChunks shares (two blocks an SM) to add.
 constexpr int kOneBlockRows = 512;
-int balance_chunks(int64_t n, int S) {
+int balance_chunks(int64_t n, int E, int S) {
   if (n <= kOneBlockRows) return 1;
-  const int64_t most = (n + 15) / 16;  // two rows a warp at least
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (304 + S - 1) / S));
+  const int at_once = kWarps * (E <= 64 ? 4 : E <= 128 ? 2 : 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>((n + at_once - 1) / at_once, kMaxChunks / S));
 }
 
-template <typename LT, int PER>
+template <typename LT, int LANES>
 cudaError_t run_balance(LaunchCtx lc, GateArgs a) {
-  a.vec = whole<LT, PER>(a.logits, a.ld);
-  if (a.chunks == 1) return launch_k(lc, k_balance<LT, PER, 16>, dim3(1, a.S), 16 * 32, 0, a);
-  cudaError_t e = launch_k(lc, k_balance<LT, PER, 8>, dim3(a.chunks, a.S), 8 * 32, 0, a);
-  if (e != cudaSuccess) return e;
+  a.vec = whole(a.logits, a.ld, sizeof(LT));
+  const cudaError_t e = launch_k(lc, k_balance<LT, LANES>, dim3(a.chunks, a.S), kWarps * 32, 0, a);
+  if (e != cudaSuccess || a.chunks == 1) return e;
   lc.pdl = 1;
-  return launch_k(lc, k_balance_finish, dim3(kFinal, a.S), 256, 0, a);
+  const unsigned ctas = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : 8;
+  return launch_k_cluster(lc, k_balance_finish, dim3(ctas, a.S), 1024, 0, ctas, a);
 }
-template <typename LT, int PER>
+template <typename LT, int LANES>
 cudaError_t run_backward(const LaunchCtx& lc, GateArgs a) {
-  a.vec = whole<LT, PER>(a.logits, a.ld);
-  a.dvec = whole<LT, PER>(a.d, a.ldd);
-  a.per_block = 8;
-  return launch_k(lc, k_route_backward<LT, PER>, (unsigned)((a.n + a.per_block - 1) / a.per_block), 256, 0, a);
+  a.vec = whole(a.logits, a.ld, sizeof(LT));
+  a.dvec = whole(a.d, a.ldd, sizeof(LT));
+  // passes of 8 warps' rows a block: one, and more from where the 456 blocks
+  // that run at a time (three an SM) have one each
+  const int64_t at_once = 8 * 32 / LANES;
+  a.per_block = (int)(at_once * std::max<int64_t>(1, (a.n + 456 * at_once - 1) / (456 * at_once)));
+  return launch_k(lc, k_route_backward<LT, LANES>, (unsigned)((a.n + a.per_block - 1) / a.per_block), 256, 0, a);
 }
 template <typename LT>
 cudaError_t run_gate(const LaunchCtx& lc, const GateArgs& a, bool forward) {
-  if (a.E <= 64) return forward ? run_balance<LT, 2>(lc, a) : run_backward<LT, 2>(lc, a);
-  if (a.E <= 128) return forward ? run_balance<LT, 4>(lc, a) : run_backward<LT, 4>(lc, a);
-  return forward ? run_balance<LT, 8>(lc, a) : run_backward<LT, 8>(lc, a);
+  if (a.E <= 64) return forward ? run_balance<LT, 8>(lc, a) : run_backward<LT, 8>(lc, a);
+  if (a.E <= 128) return forward ? run_balance<LT, 16>(lc, a) : run_backward<LT, 16>(lc, a);
+  return forward ? run_balance<LT, 32>(lc, a) : run_backward<LT, 32>(lc, a);
 }
 
 bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
@@ -472,7 +574,7 @@ bool gate_args_ok(int64_t ld, int n, int dtype, int E, int k, int score, int S, 
 
 extern "C" int64_t afd_balance_workspace(int n_tokens, int num_experts, int n_seqs) {
   if (n_tokens < 0 || num_experts < 1 || num_experts > 256 || n_seqs < 1 || n_seqs > 65535) return -1;
-  const int c = balance_chunks(n_tokens, n_seqs);
+  const int c = balance_chunks(n_tokens, num_experts, n_seqs);
   return c == 1 ? 0 : (int64_t)n_seqs * c * num_experts * 8;
 }
 
@@ -494,7 +596,7 @@ extern "C" int afd_balance_loss(const void* logits, int64_t ld, int n_tokens, in
   a.logits = logits; a.ld = ld; a.ids = ids; a.off = seq_offsets;
   a.n = n_tokens; a.E = num_experts; a.k = topk; a.S = n_seqs; a.sigmoid = score == AFD_SCORE_SIGMOID;
   a.loss = loss; a.counts = counts; a.part = reinterpret_cast<float*>(workspace);
-  a.chunks = balance_chunks(n_tokens, n_seqs);
+  a.chunks = balance_chunks(n_tokens, num_experts, n_seqs);
   const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, nullptr};
   if ((logits_dtype == AFD_DTYPE_F32 ? run_gate<float>(lc, a, true) : run_gate<uint16_t>(lc, a, true)) != cudaSuccess) {
     cudaGetLastError();
