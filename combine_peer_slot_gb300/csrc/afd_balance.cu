@@ -121,6 +121,26 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
+// two sums, two largest values of a row in the time of one
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& v, float& w) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v, o), y = __shfl_xor_sync(0xffffffffu, w, o);
+    v += x;
+    w += y;
+  }
+}
+template <int LANES>
+__device__ __forceinline__ void row_maxima(float& v, float& w) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v, o), y = __shfl_xor_sync(0xffffffffu, w, o);
+    v = fmaxf(v, x);
+    w = fmaxf(w, y);
+  }
+}
+
 // s = 1 / (1 + exp(-l)) and 1 - s, each to fp32's precision of itself; the
 // denominator is between 1 and 2, where the quotient's short form is within an
 // ulp (the full one is a third of the row's instructions)
@@ -130,54 +150,84 @@ __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
   rest = l >= 0.0f ? q : r;
 }
 
-// What one row's sums of exponentials are.
-struct RowSum {
-  float top, z;  // largest logit, sum of exp(l - top)
-};
-
-// p of a row from its logits.  sigmoid: rest = 1 - s as well.  A row of -inf
-// has p = 0.  Scores whose sum nears fp32's smallest number come from logits
-// under -60, where s = exp(l) (1 - 1e-26): their shares are the softmax's.
-template <int LANES>
-__device__ __forceinline__ RowSum shares(const float (&l)[kPer], int sigmoid, float (&p)[kPer], float (&rest)[kPer]) {
-  RowSum r{0.0f, 0.0f};
-  bool small = true;
-  if (sigmoid) {
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-      sigmoid_pair(l[i], p[i], rest[i]);
-      r.z += p[i];
-    }
-    r.z = row_sum<LANES>(r.z);
-    small = r.z < 1e-30f;
-    if (!__any_sync(0xffffffffu, small)) {
-      const float inv = 1.0f / r.z;
-#pragma unroll
-      for (int i = 0; i < kPer; i++) p[i] *= inv;
-      return r;
-    }
-  }
-  float top = -INFINITY;
+// The exponentials of a row's logits and of its chosen ones (KIDS a lane), each
+// relative to their own largest, and their sums: 0 throughout where all are
+// -inf.  top: the row's largest; chosen far enough below it that their scores
+// are 0 in fp64 too (and route_select's weights with them) count as none.
+template <int LANES, int KIDS>
+__device__ __forceinline__ void exponentials(const float (&l)[kPer], const float (&cl)[KIDS], bool far_is_none,
+                                             float (&x)[kPer], float& z, float (&cx)[KIDS], float& cz, float& top) {
+  float ctop = -INFINITY;
+  top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kPer; i++) top = fmaxf(top, l[i]);
-  top = row_max<LANES>(top);
-  float z = 0.0f, x[kPer];
+#pragma unroll
+  for (int j = 0; j < KIDS; j++) ctop = fmaxf(ctop, cl[j]);
+  row_maxima<LANES>(top, ctop);
+  z = cz = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
     x[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
     z += x[i];
   }
-  z = row_sum<LANES>(z);
-  if (small) {  // (the warp's other rows keep their sigmoids)
-    r.top = top;
-    r.z = z;
+  const bool none = far_is_none && ctop - top < -745.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) p[i] = x[i];
+  for (int j = 0; j < KIDS; j++) {
+    cx[j] = cl[j] == -INFINITY || none ? 0.0f : expf(cl[j] - ctop);
+    cz += cx[j];
   }
-  const float inv = r.z == 0.0f ? 0.0f : 1.0f / r.z;
+  row_sums<LANES>(z, cz);
+}
+
+// A row's shares p, and of its chosen logits cl the scores' shares of the
+// chosen (cs; renorm) or the scores; under sigmoid the 1 - s of both as well.
+// Scores whose sum nears fp32's smallest number come from logits under -60,
+// where s = exp(l) (1 - 1e-26): their shares are the softmax's.
+template <int LANES, int KIDS>
+__device__ __forceinline__ void shares(const float (&l)[kPer], const float (&cl)[KIDS], int sigmoid, bool renorm,
+                                       float (&p)[kPer], float (&rest)[kPer], float (&cs)[KIDS], float (&crest)[KIDS]) {
+  float z = 0.0f, cz = 0.0f;
+  bool small = false, csmall = false;
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      sigmoid_pair(l[i], p[i], rest[i]);
+      z += p[i];
+    }
+#pragma unroll
+    for (int j = 0; j < KIDS; j++) {
+      sigmoid_pair(cl[j], cs[j], crest[j]);
+      cz += cs[j];
+    }
+    row_sums<LANES>(z, cz);
+    small = z < 1e-30f;
+    csmall = renorm && cz < 1e-30f;
+  }
+  if (!sigmoid || __any_sync(0xffffffffu, small || csmall)) {
+    float x[kPer], cx[KIDS], xz, cxz, top;
+    exponentials<LANES, KIDS>(l, cl, !sigmoid, x, xz, cx, cxz, top);
+    if (!sigmoid || small) {  // (the warp's other rows keep their sigmoids)
+      z = xz;
+#pragma unroll
+      for (int i = 0; i < kPer; i++) p[i] = x[i];
+    }
+    if (!sigmoid || csmall) {
+      cz = cxz;
+#pragma unroll
+      for (int j = 0; j < KIDS; j++) {
+        cs[j] = cx[j];
+        if (!sigmoid && !renorm) cs[j] = cl[j] == -INFINITY ? 0.0f : expf(cl[j] - top) / xz;
+      }
+    }
+  }
+  const float inv = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
   for (int i = 0; i < kPer; i++) p[i] *= inv;
-  return r;
+  if (renorm) {
+    const float cinv = cz == 0.0f ? 0.0f : 1.0f / cz;
+#pragma unroll
+    for (int j = 0; j < KIDS; j++) cs[j] *= cinv;
+  }
 }
 
 // rows [lo, hi) of sequence s, inside [0, n]
@@ -237,7 +287,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance(const __grid_constant__
     for (int j = 0; j < kIds; j++) id[j] = nid[j];
     row += step;
     if (i + 1 < passes) load(row);
-    shares<LANES>(l, a.sigmoid, p, rest);
+    const float none[1] = {-INFINITY};
+    float cs[1], crest[1];
+    shares<LANES, 1>(l, none, a.sigmoid, false, p, rest, cs, crest);
 #pragma unroll
     for (int x = 0; x < kPer; x++) acc[x] += p[x];
 #pragma unroll
@@ -338,16 +390,19 @@ __global__ void __launch_bounds__(1024) k_balance_finish(const __grid_constant__
 //   w_j = c s_j / sum s_i:  share_j (d w_j - sum share d w) c, through log s
 // Chosen shares come from their own logits, so that a row whose chosen scores
 // are all tiny keeps its precision.
-template <typename LT, int LANES>
+// DW: with the weights' gradient.
+template <typename LT, int LANES, bool DW>
 __global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant__ GateArgs a) {
   constexpr int kE = LANES * kPer, kAtOnce = 32 / LANES, kIds = LANES < 16 ? 2 : 1;
-  __shared__ float added[8][256];
+  __shared__ __align__(16) float added[DW ? 8 : 1][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
   const int e0 = sub * kPer, have = a.E - e0;
-  float* add = added[warp] + lane / LANES * kE;
-#pragma unroll
-  for (int i = 0; i < kPer; i++) add[e0 + i] = 0.0f;
-  __syncwarp();
+  float* add = added[DW ? warp : 0] + lane / LANES * kE;
+  float4* mine = reinterpret_cast<float4*>(add + e0);  // (by fours: by ones, lanes would meet in eight banks)
+  if (DW) {
+    mine[0] = mine[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncwarp();
+  }
   const int64_t first = (int64_t)blockIdx.x * a.per_block;
   const int64_t last = min((int64_t)a.n, first + a.per_block);
   int seq = -1, lo = 0, hi = 0;  // the sequence of g
@@ -363,7 +418,7 @@ __global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant
 #pragma unroll
     for (int j = 0; j < kIds; j++) {
       int id = -1;
-      if (a.dw && in && sub + j * LANES < a.k) {
+      if (DW && in && sub + j * LANES < a.k) {
         id = a.ids[at * a.k + sub + j * LANES];
         if (id < 0 || id >= a.E) id = -1;
       }
@@ -427,63 +482,22 @@ __global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kPer; i++) bad |= l[i] != l[i] || (!a.sigmoid && l[i] == INFINITY);
     const uint32_t bad_lanes = __ballot_sync(0xffffffffu, bad);
-    const RowSum r = shares<LANES>(l, a.sigmoid, p, rest);
-    float inner = 0.0f;
+    float cs[kIds], crest[kIds];
+    shares<LANES, kIds>(l, my_l, a.sigmoid, DW && a.renorm, p, rest, cs, crest);
+    float inner = 0.0f, mean = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; i++) inner += p[i] * g[i];
-    inner = row_sum<LANES>(inner);
-    if (a.dw) {
-      float s[kIds], my_rest[kIds], part[kIds];
+    if (DW) {
+#pragma unroll
+      for (int j = 0; j < kIds; j++) mean += cs[j] * dw[j];
+      row_sums<LANES>(inner, mean);
+      float part[kIds];
 #pragma unroll
       for (int j = 0; j < kIds; j++) {
-        s[j] = 0.0f;
-        my_rest[j] = 1.0f;
-        if (a.sigmoid) sigmoid_pair(my_l[j], s[j], my_rest[j]);
+        part[j] = cs[j] * (a.renorm ? dw[j] - mean : dw[j]);
+        if (a.sigmoid) part[j] *= crest[j];
       }
-      if (a.renorm) {
-        float total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kIds; j++) total += s[j];
-        total = a.sigmoid ? row_sum<LANES>(total) : 0.0f;
-        const bool small = !a.sigmoid || total < 1e-30f;
-        if (__any_sync(0xffffffffu, small)) {
-          float top = my_l[0], z = 0.0f, x[kIds];
-          if (kIds == 2) top = fmaxf(top, my_l[kIds - 1]);
-          top = row_max<LANES>(top);
-#pragma unroll
-          for (int j = 0; j < kIds; j++) {
-            // (under -745 the scores are 0 in fp64 too, and so are the weights)
-            x[j] = my_l[j] == -INFINITY || (!a.sigmoid && top - r.top < -745.0f) ? 0.0f : expf(my_l[j] - top);
-            z += x[j];
-          }
-          z = row_sum<LANES>(z);
-          if (small) {
-            total = z;
-#pragma unroll
-            for (int j = 0; j < kIds; j++) s[j] = x[j];
-          }
-        }
-        float mean = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kIds; j++) {
-          s[j] = total == 0.0f ? 0.0f : s[j] / total;
-          mean += s[j] * dw[j];
-        }
-        mean = row_sum<LANES>(mean);
-#pragma unroll
-        for (int j = 0; j < kIds; j++) part[j] = s[j] * (dw[j] - mean) * my_rest[j];
-      } else if (a.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < kIds; j++) part[j] = s[j] * my_rest[j] * dw[j];
-      } else {
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kIds; j++) {
-          part[j] = my_l[j] == -INFINITY ? 0.0f : expf(my_l[j] - r.top) / r.z * dw[j];
-          sum += part[j];
-        }
-        inner += row_sum<LANES>(sum);
-      }
+      if (!a.sigmoid && !a.renorm) inner += mean;
       // to the experts' lanes; an id that stands twice in a row is added twice
 #pragma unroll
       for (int j = 0; j < kIds; j++) {
@@ -498,6 +512,8 @@ __global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant
         }
         __syncwarp();
       }
+    } else {
+      inner = row_sum<LANES>(inner);
     }
     const float nan = __int_as_float(0x7fc00000);
     bad = (bad_lanes >> (lane / LANES * LANES) & (LANES == 32 ? 0xffffffffu : (1u << (LANES & 31)) - 1u)) != 0u;
@@ -506,15 +522,20 @@ __global__ void __launch_bounds__(256, 3) k_route_backward(const __grid_constant
     for (int i = 0; i < kPer; i++) {
       d[i] = p[i] * (g[i] - inner);
       if (a.sigmoid) d[i] *= rest[i];
-      if (a.dw) d[i] += add[e0 + i];
-      if (bad) d[i] = nan;
+    }
+    if (DW) {
+      const float4 u = mine[0], v = mine[1];
+      d[0] += u.x; d[1] += u.y; d[2] += u.z; d[3] += u.w;
+      d[4] += v.x; d[5] += v.y; d[6] += v.z; d[7] += v.w;
+    }
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < kPer; i++) d[i] = nan;
     }
     if (in) store_row<LT>(a.d, row * a.ldd + e0, have, a.dvec, d);
-    if (a.dw) {
+    if (DW) {
       __syncwarp();
-#pragma unroll
-      for (int j = 0; j < kIds; j++)
-        if (id[j] >= 0) add[id[j]] = 0.0f;
+      mine[0] = mine[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       __syncwarp();
     }
   }
@@ -552,7 +573,9 @@ cudaError_t run_backward(const LaunchCtx& lc, GateArgs a) {
   // that run at a time (three an SM) have one each
   const int64_t at_once = 8 * 32 / LANES;
   a.per_block = (int)(at_once * std::max<int64_t>(1, (a.n + 456 * at_once - 1) / (456 * at_once)));
-  return launch_k(lc, k_route_backward<LT, LANES>, (unsigned)((a.n + a.per_block - 1) / a.per_block), 256, 0, a);
+  const unsigned grid = (unsigned)((a.n + a.per_block - 1) / a.per_block);
+  return a.dw ? launch_k(lc, k_route_backward<LT, LANES, true>, grid, 256, 0, a)
+              : launch_k(lc, k_route_backward<LT, LANES, false>, grid, 256, 0, a);
 }
 template <typename LT>
 cudaError_t run_gate(const LaunchCtx& lc, const GateArgs& a, bool forward) {

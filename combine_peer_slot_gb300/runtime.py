@@ -554,21 +554,25 @@ def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
 def _gate_inputs(h, logits, ids, score, seq_offsets):
     """(T, E, topk, dtype code, score code, row pitch, offsets' pointer, sequences)"""
     code, kind = h.code.get(logits.dtype), _SCORES.get(score)
-    if code is None or kind is None or logits.dim() != 2:
+    shape = logits.shape
+    if code is None or kind is None or len(shape) != 2:
         _bad("logits: bf16 or fp32 rows [T, E] wanted, score softmax or sigmoid")
-    T, E = logits.shape
+    T, E = shape
     ld, step = logits.stride()
     if T > _INT or not 0 < E <= 256 or (step != 1 and E > 1):
         _bad("logits: rows of up to 256 neighbouring elements wanted")
     topk = 1
     if ids is not None:
-        if ids.dtype is not h.int32 or ids.dim() != 2 or ids.shape[0] != T or not ids.is_contiguous():
+        shape = ids.shape
+        if ids.dtype is not h.int32 or len(shape) != 2 or shape[0] != T or not ids.is_contiguous():
             _bad("ids: contiguous int32 [T, topk] wanted")
-        topk = ids.shape[1]
+        topk = shape[1]
     off, seqs = 0, 1
     if seq_offsets is not None:
-        _rows_int32(h, seq_offsets, -1, "seq_offsets")
-        off, seqs = seq_offsets.data_ptr(), seq_offsets.shape[0] - 1
+        shape = seq_offsets.shape
+        if seq_offsets.dtype is not h.int32 or len(shape) != 1 or not seq_offsets.is_contiguous():
+            _bad("seq_offsets: contiguous int32 vector wanted")
+        off, seqs = seq_offsets.data_ptr(), shape[0] - 1
     if not (0 < topk <= 16 and 0 < seqs <= 65535):
         _bad("ids of 1 to 16 columns, 1 to 65535 sequences wanted")
     if not logits.is_cuda:
@@ -662,10 +666,12 @@ class LoraBatch:
 
 def _lora_weights(h, batch, a, b):
     """(rank, K, M)"""
-    if (a.dtype is not h.bf16 or b.dtype is not h.bf16 or a.dim() != 3 or b.dim() != 3 or a.shape[0] != batch.adapters
-            or b.shape[:2] != a.shape[:2] or not a.is_contiguous() or not b.is_contiguous()):
+    sa, sb = a.shape, b.shape
+    if (a.dtype is not h.bf16 or b.dtype is not h.bf16 or len(sa) != 3 or len(sb) != 3 or sa[0] != batch.adapters
+            or sb[0] != sa[0] or sb[1] != sa[1] or not a.is_contiguous() or not b.is_contiguous()):
         _bad("a, b: contiguous bf16 [adapters, rank, K] and [adapters, rank, M] wanted")
-    rank, K, M = a.shape[1], a.shape[2], b.shape[2]
+    _, rank, K = sa
+    M = sb[2]
     if not (0 < rank <= 128 and 0 < K <= _DIM and 0 < M <= _DIM):
         _bad("rank 1 to 128, K and M 1 to 65536 wanted")
     return rank, K, M
@@ -673,10 +679,14 @@ def _lora_weights(h, batch, a, b):
 
 def _lora_rows(h, t, shape, what, dtype=None):
     """(row pitch, dtype code) of rows of neighbouring elements"""
-    code = h.code.get(t.dtype)
-    if code is None or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1) or dtype not in (None, t.dtype):
+    kind = t.dtype
+    code = h.code.get(kind)
+    if code is None or t.shape != shape or (dtype is not None and dtype is not kind):
         _bad(f"{what}: rows {list(shape)} of bf16 or fp32 wanted, alike where they meet")
-    return t.stride(0) if shape[0] > 1 else shape[1], code
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        _bad(f"{what}: rows of neighbouring elements wanted")
+    return ld if shape[0] > 1 else shape[1], code
 
 
 def lora_apply(batch, x, a, b, base=None, scale=None, out=None, out_dtype=None, keep=False):
