@@ -14,8 +14,8 @@ constexpr int kPlanWarps = 32;
 __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t* ids, int n, int L, LoraPlan p, int tile, int piece) {
   extern __shared__ int32_t cnt[];  // [warps][L + 1]
   __shared__ int32_t total[kLoraMaxAdapters + 1], rows0[kLoraMaxAdapters + 2], tile0[kLoraMaxAdapters + 2],
-      piece0[kLoraMaxAdapters + 2], slot0[kLoraMaxAdapters + 2];
-  __shared__ int32_t sums[4][kPlanWarps];
+      piece0[kLoraMaxAdapters + 2], slot0[kLoraMaxAdapters + 2], block0[kLoraMaxAdapters + 2];
+  __shared__ int32_t sums[5][kPlanWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, keys = L + 1;
   for (int i = threadIdx.x; i < kPlanWarps * keys; i += kPlanWarps * 32) cnt[i] = 0;
   __syncthreads();
@@ -58,23 +58,23 @@ __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t*
       total[k] = v;
     }
     __syncthreads();
-    // rows, tiles, pieces and partial slots before each adapter: two
+    // rows, tiles, pieces, partial slots and blocks before each adapter: two
     // neighbouring adapters a thread (L + 1 <= 1025; the last one apart)
-    int v[2][4], s[4] = {0, 0, 0, 0};
+    int v[2][5], s[5] = {0, 0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       const int k = threadIdx.x * 2 + i, c = k < keys ? total[k] : 0;
       const int pieces = k < L ? (c + piece - 1) / piece : 0;
-      const int add[4] = {c, (c + tile - 1) / tile, pieces, pieces > 1 ? pieces : 0};
+      const int add[5] = {c, (c + tile - 1) / tile, pieces, pieces > 1 ? pieces : 0, (c + kLoraBlockRows - 1) / kLoraBlockRows};
 #pragma unroll
-      for (int x = 0; x < 4; x++) {
+      for (int x = 0; x < 5; x++) {
         v[i][x] = s[x];
         s[x] += add[x];
       }
     }
-    int incl[4];
+    int incl[5];
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
+    for (int x = 0; x < 5; x++) {
       incl[x] = s[x];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -85,10 +85,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t*
     }
     __syncthreads();
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
+    for (int x = 0; x < 5; x++) {
       int before = incl[x] - s[x];
       for (int w = 0; w < warp; w++) before += sums[x][w];
-      int32_t* to = x == 0 ? rows0 : x == 1 ? tile0 : x == 2 ? piece0 : slot0;
+      int32_t* to = x == 0 ? rows0 : x == 1 ? tile0 : x == 2 ? piece0 : x == 3 ? slot0 : block0;
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         const int k = threadIdx.x * 2 + i;
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t*
     for (int k = threadIdx.x; k < L; k += kPlanWarps * 32) {
       p.first[k] = slot0[k];
       p.first[L + k] = piece0[k + 1] - piece0[k];
+      p.shift[k] = block0[k] * kLoraBlockRows - rows0[k];
     }
     // tile i: of the last adapter whose tiles start at or before it
     for (int i = threadIdx.x; i < tile0[keys]; i += kPlanWarps * 32) {
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t*
         if (tile0[m] <= i) a = m; else b = m;
       }
       const int at = (i - tile0[a]) * tile;
-      p.tiles[i] = make_int4(a < L ? a : -1, rows0[a] + at, min(tile, total[a] - at), 0);
+      p.tiles[i] = make_int4(a < L ? a : -1, rows0[a] + at, min(tile, total[a] - at),
+                              a < L && at + tile >= total[a] ? (kLoraBlockRows - total[a] % kLoraBlockRows) % kLoraBlockRows : 0);
     }
     for (int i = threadIdx.x; i < piece0[L]; i += kPlanWarps * 32) {
       int a = 0, b = L;
@@ -150,7 +152,8 @@ cudaError_t launch_products(const LaunchCtx& lc, LoraArgs& g) {
   g.how_w2 = how_rows(g.w2, g.M, g.M, AFD_DTYPE_BF16);
   g.how_base = how_rows(g.base, g.ldb, g.M, to);
   g.how_out = how_rows(g.out, g.ldo, g.M, to);
-  return lora_tile(g.T) == 16 ? launch_lora_apply(lc, g) : launch_lora_tiles(lc, g);
+  if (lora_tile(g.T) == 16) return launch_lora_apply(lc, g);
+  return lora_tc_takes(g) ? launch_lora_tc(lc, g) : launch_lora_tiles(lc, g);
 }
 }  // namespace
 
@@ -198,7 +201,7 @@ extern "C" int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters
   g.plan = lora_plan_at(const_cast<void*>(plan), n_tokens, n_adapters);
   g.src = x; g.lds = ldx; g.w1 = a; g.w2 = b; g.scale = scale;
   g.base = base; g.ldb = ldb; g.out = out; g.ldo = ldo; g.u = u;
-  g.T = n_tokens; g.K = K; g.M = M; g.R = rank;
+  g.T = n_tokens; g.K = K; g.M = M; g.R = rank; g.L = n_adapters;
   g.src_f32 = x_dtype == AFD_DTYPE_F32; g.out_f32 = y_dtype == AFD_DTYPE_F32;
   const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, nullptr};
   if (launch_products(lc, g) != cudaSuccess) {
@@ -215,7 +218,7 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 extern "C" int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank) {
   if (!batch_ok(n_tokens, n_adapters) || !dims_ok(K, M, rank)) return -1;
   const LoraPlan p = lora_plan_at(nullptr, n_tokens, n_adapters);
-  return up256(n_tokens * rank * 4) + 2 * up256(n_tokens * 3 * lora_padded(rank) * 2) + up256(p.max_slots * rank * K * 4) +
+  return up256(n_tokens * rank * 4) + 2 * up256(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))) + up256(p.max_slots * rank * K * 4) +
          up256(p.max_slots * rank * M * 4);
 }
 
@@ -257,13 +260,13 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
     return r;
   };
   float* v = reinterpret_cast<float*>(take(n_tokens * rank * 4));
-  uint16_t* v_parts = reinterpret_cast<uint16_t*>(take(n_tokens * 3 * lora_padded(rank) * 2));
-  uint16_t* u_parts = reinterpret_cast<uint16_t*>(take(n_tokens * 3 * lora_padded(rank) * 2));
+  uint16_t* v_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
+  uint16_t* u_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
   LoraArgs g{};
   g.plan = lora_plan_at(const_cast<void*>(plan), n_tokens, n_adapters);
   g.src = dy; g.lds = ldy; g.w1 = b; g.w2 = a; g.scale = scale;
   g.base = d_base; g.ldb = ldb; g.out = dx; g.ldo = ldd;
-  g.T = n_tokens; g.K = M; g.M = K; g.R = rank;
+  g.T = n_tokens; g.K = M; g.M = K; g.R = rank; g.L = n_adapters;
   g.src_f32 = y_dtype == AFD_DTYPE_F32; g.out_f32 = x_dtype == AFD_DTYPE_F32;
   LoraWgradArgs w{};
   w.plan = g.plan;

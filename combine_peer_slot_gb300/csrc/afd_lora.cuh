@@ -11,21 +11,26 @@ constexpr int64_t kLoraMaxTokens = int64_t(1) << 24;
 
 // Rows of one adapter that a tile of the products holds, and rows of one
 // piece of the weight gradients' sums.
-__host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
+constexpr int kLoraSms = 152;
+inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 128; }
 constexpr int kLoraMaxPiece = 512;
 __host__ __device__ inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : kLoraMaxPiece; }
 
 // The plan, made on the device from the rows' adapter ids: the rows in adapter
 // order (stable; rows without an adapter last), cut into tiles of one adapter.
 //   head   {tiles, tiles of rows without an adapter, pieces, rows with one}
-//   tiles  {adapter (-1: none), first row in order, rows, 0}
+//   tiles  {adapter (-1: none), first row in order, rows, rows that an
+//          adapter's last tile lacks to a whole block of 32}
 //   pieces {adapter, first row in order, rows, slot of its partial sums or -1}
-//   first  [adapters + 1] first partial slot; last one: slots used
+//   first  [adapters] first partial slot, then [adapters] pieces
+//   shift  [adapters] from a row's place in order to its place among u_parts,
+//          where each adapter begins with a block of 32 rows
 struct LoraPlan {
   int4* head;
   int4* tiles;
   int4* pieces;
-  int32_t* first;   // [adapters]: first piece; [adapters + l]: pieces of l
+  int32_t* first;
+  int32_t* shift;
   int32_t* order;   // [tokens]
   int64_t max_tiles, max_pieces, max_slots, bytes;
 };
@@ -46,6 +51,7 @@ inline LoraPlan lora_plan_at(void* base, int64_t tokens, int64_t adapters) {
   p.tiles = reinterpret_cast<int4*>(take(16 * p.max_tiles));
   p.pieces = reinterpret_cast<int4*>(take(16 * std::max<int64_t>(1, p.max_pieces)));
   p.first = reinterpret_cast<int32_t*>(take(8 * adapters));
+  p.shift = reinterpret_cast<int32_t*>(take(4 * adapters));
   p.order = reinterpret_cast<int32_t*>(take(4 * std::max<int64_t>(1, tokens)));
   p.bytes = at - reinterpret_cast<char*>(base);
   return p;
@@ -64,13 +70,13 @@ struct LoraArgs {
   void* out;
   int64_t ldo;
   float* u;            // [T][R] or NULL
-  // for the weight gradients, or NULL: rows in the plan's order as three bf16
-  // parts of `padded` ranks each, of u as computed here and of `other` [T][R]
+  // for the weight gradients, or NULL: three bf16 parts of u as computed here
+  // and of `other` [T][R], as their kernel copies them (parts_at)
   uint16_t* u_parts;
   const float* other;
   uint16_t* other_parts;
   int64_t T;
-  int K, M, R;
+  int K, M, R, L;
   int src_f32, out_f32;
   // how rows can be moved: 2 = 16 bytes at a time, 1 = 4, 0 = by elements
   int how_src, how_w1, how_w2, how_base, how_out;
@@ -91,10 +97,22 @@ struct LoraWgradArgs {
   int64_t T;
   int R, L;
 };
+// Parts of u for the weight gradients: blocks of 32 rows (each adapter's first
+// row begins one, the last is filled up with zeros), each the shared memory
+// image of an MN-major operand with the 128-byte swizzle: atoms of 64 of a row's
+// 3 MP values.  Values past those are never read into a sum.
+constexpr int kLoraBlockRows = 32;
+__host__ __device__ constexpr int lora_atoms(int MP) { return (3 * MP + 63) / 64; }
+inline int64_t lora_parts_bytes(int64_t tokens, int64_t adapters, int MP) {
+  return ((tokens + 31) / 32 + std::min(tokens, adapters)) * lora_atoms(MP) * 4096;
+}
 // ranks of one part
 __host__ __device__ inline int lora_padded(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 cudaError_t launch_lora_apply(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 16
-cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 64
+cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles of 128, 64 at a time
+bool lora_tc_takes(const LoraArgs& a);                                  // the next one's sizes and alignment
+cudaError_t launch_lora_tc(const LaunchCtx& lc, const LoraArgs& a);     // tiles of 128
+cudaError_t lora_tc_error_count(uint32_t* n, cudaStream_t stream);
 cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
 cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, const LoraWgradArgs& a);  // the matrices of bf16 rows
 cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);          // waits that gave up, once the stream is there
@@ -142,6 +160,13 @@ __device__ __forceinline__ void split_pair(float2 v, uint32_t (&p)[PARTS]) {
   split_bf16<PARTS>(v.y, b);
 #pragma unroll
   for (int i = 0; i < PARTS; i++) p[i] = (uint32_t)a[i] | (uint32_t)b[i] << 16;
+}
+
+// value m of a row's parts: part m / MP, rank m % MP
+template <int MP>
+__device__ __forceinline__ uint16_t* parts_at(uint16_t* to, int64_t row, int m) {
+  const int r = (int)(row & 31);
+  return to + (row >> 5) * (lora_atoms(MP) * 2048) + (m >> 6) * 2048 + r * 64 + (((m >> 3 & 7) ^ (r & 7)) << 3) + (m & 7);
 }
 
 template <typename T>
@@ -268,4 +293,33 @@ __device__ __forceinline__ void load_chunk(uint32_t dst, const T* row, int c0, i
   }
 }
 
+
+// ---- tcgen05, one CTA: issued by the elected lane of a warp that runs its loop
+// as a whole.  Under a branch on the lane the operands would leave the uniform
+// registers that these instructions take them from: four MMAs and a commit
+// then took 740 cycles. ----
+__device__ __forceinline__ uint32_t lora_elect() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+// descriptors: the layout's upper word, address (16-byte units) and, of MN-major
+// operands of two atoms, their distance in the lower
+__device__ __forceinline__ uint64_t lora_desc(uint32_t addr16, uint32_t apart16) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | apart16 << 16), "r"((1024u >> 4) | 1u << 14 | 2u << 29));
+  return d;
+}
+__device__ __forceinline__ void lora_mma(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void lora_commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(elected)
+      : "memory");
+}
 #endif

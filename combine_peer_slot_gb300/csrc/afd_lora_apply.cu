@@ -61,12 +61,16 @@ __device__ __forceinline__ void add_eight(const void* base, TO* out, int c0, int
   }
 }
 
-// one value's parts, of row i in the plan's order
+// one value's parts, of row i among them
 __device__ __forceinline__ void store_parts(uint16_t* to, int padded, int64_t i, int r, float v) {
   uint16_t p[3];
   split_bf16<3>(v, p);
 #pragma unroll
-  for (int x = 0; x < 3; x++) to[(i * 3 + x) * padded + r] = p[x];
+  for (int x = 0; x < 3; x++)
+    *(padded == 16   ? parts_at<16>(to, i, x * 16 + r)
+      : padded == 32 ? parts_at<32>(to, i, x * 32 + r)
+      : padded == 64 ? parts_at<64>(to, i, x * 64 + r)
+                     : parts_at<128>(to, i, x * 128 + r)) = p[x];
 }
 
 template <int KC, typename TS, typename TO>
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   const int ustr = rt * 16 + 8;
   const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + (int64_t)t.x * a.R * a.K;
   const int chunks = (a.K + 31) / 32;
+  const int64_t part_row = t.y + (a.u_parts || a.other_parts ? a.plan.shift[t.x] : 0);
   const TS* rows[kCols];
 #pragma unroll
   for (int j = 0; j < kCols; j++) {
@@ -177,14 +182,17 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
 #pragma unroll
     for (int x = 0; x < kU; x++) us[(x * TT + i) * ustr + r] = p[x];
     if (a.u && q == 0 && i < t.z && r < a.R) a.u[(int64_t)order[i] * a.R + r] = v;
-    if (a.u_parts && q == 0 && i < t.z) store_parts(a.u_parts, padded, t.y + i, r, v);
+    if (a.u_parts && q == 0 && i < t.z) store_parts(a.u_parts, padded, part_row + i, r, v);
   }
-  if (q == C - 1) {
-    for (int e = threadIdx.x; a.u_parts && e < t.z * (padded - rt * 16); e += kWarps * 32)
-      store_parts(a.u_parts, padded, t.y + e % t.z, rt * 16 + e / t.z, 0.0f);
-    for (int e = threadIdx.x; a.other_parts && e < t.z * padded; e += kWarps * 32) {
+  if (q == C - 1) {  // (ranks past the last, and rows to a whole block: zeros)
+    const int all = t.z + t.w, more = padded - rt * 16;
+    for (int e = threadIdx.x; a.u_parts && e < all * padded; e += kWarps * 32) {
       const int r = e % padded, i = e / padded;
-      store_parts(a.other_parts, padded, t.y + i, r, r < a.R ? a.other[(int64_t)order[i] * a.R + r] : 0.0f);
+      if (i >= t.z || r >= padded - more) store_parts(a.u_parts, padded, part_row + i, r, 0.0f);
+    }
+    for (int e = threadIdx.x; a.other_parts && e < all * padded; e += kWarps * 32) {
+      const int r = e % padded, i = e / padded;
+      store_parts(a.other_parts, padded, part_row + i, r, r < a.R && i < t.z ? a.other[(int64_t)order[i] * a.R + r] : 0.0f);
     }
   }
   cluster.sync();  // (no CTA's sums are read after this)

@@ -1,5 +1,6 @@
-// afd_lora_tiles.cu -- both products of the adapters for batches of many rows
-// (tiles of 64; afd_lora_apply.cu has the form for few):
+// afd_lora_tiles.cu -- both products of the adapters for batches of many rows,
+// of any type, alignment and rank (afd_lora_apply.cu: few rows, afd_lora_tc.cu:
+// bf16 rows of whole 16 bytes, ranks up to 64), 64 rows a tile:
 //   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
 //
 // Bound by memory: src and base in, out out, at rank operations a byte.  So
@@ -87,9 +88,15 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int wt = warp & 3, half = warp >> 2;  // 16 rows; first product: half of the ranks, second: of the columns
   const int4 head = *a.plan.head;
-  const int64_t tile = blockIdx.x / C;
+  const int64_t tile = blockIdx.x / C / 2;  // half of one of the plan's tiles
   if (tile >= head.x + head.y) return;
-  const int4 t = a.plan.tiles[tile];
+  int4 t = a.plan.tiles[tile];
+  const int skip = blockIdx.x / C % 2 * TT;
+  if (t.z <= skip) return;
+  t.y += skip;
+  t.z -= skip;
+  if (t.z > TT) t.w = 0;
+  t.z = min(t.z, TT);
   if (tid < TT) rows[tid] = tid < t.z ? a.plan.order[t.y + tid] : -1;
   __syncthreads();
   if (t.x < 0) {  // rows without an adapter: out = base
@@ -256,21 +263,22 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
       if (i < t.z && r < a.R) a.u[(int64_t)rows[i] * a.R + r] = part[i * F::kUStride + r];
     }
   }
-  if (a.u_parts || a.other_parts) {  // rows t.y + i of the plan's order, KC * 16 ranks a part
-    for (int e = tid + q * kThreads; e < t.z * KC * 8; e += C * kThreads) {
+  if (a.u_parts || a.other_parts) {  // (rows to a whole block: zeros)
+    const int64_t part_row = t.y + a.plan.shift[t.x];
+    for (int e = tid + q * kThreads; e < (t.z + t.w) * KC * 8; e += C * kThreads) {
       const int i = e / (KC * 8), r = e % (KC * 8) * 2;
-      const int64_t to = (int64_t)(t.y + i) * 3 * (KC * 16) + r;
+      const bool real = i < t.z;
       uint32_t p[3];
       if (a.u_parts) {
-        split_pair<3>(*reinterpret_cast<const float2*>(part + i * F::kUStride + r), p);
+        split_pair<3>(real ? *reinterpret_cast<const float2*>(part + i * F::kUStride + r) : make_float2(0.0f, 0.0f), p);
 #pragma unroll
-        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(a.u_parts + to + x * (KC * 16)) = p[x];
+        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(parts_at<KC * 16>(a.u_parts, part_row + i, x * KC * 16 + r)) = p[x];
       }
       if (a.other_parts) {
-        const float* o = a.other + (int64_t)rows[i] * a.R + r;
-        split_pair<3>(make_float2(r < a.R ? o[0] : 0.0f, r + 1 < a.R ? o[1] : 0.0f), p);
+        const float* o = a.other + (int64_t)rows[real ? i : 0] * a.R + r;
+        split_pair<3>(make_float2(real && r < a.R ? o[0] : 0.0f, real && r + 1 < a.R ? o[1] : 0.0f), p);
 #pragma unroll
-        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(a.other_parts + to + x * (KC * 16)) = p[x];
+        for (int x = 0; x < 3; x++) *reinterpret_cast<uint32_t*>(parts_at<KC * 16>(a.other_parts, part_row + i, x * KC * 16 + r)) = p[x];
       }
     }
   }
@@ -372,7 +380,7 @@ cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
   static std::atomic<int> done[kMaxCachedDevices];
   cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO>, F::kBytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = a.plan.max_tiles;
+  const int64_t tiles = 2 * a.plan.max_tiles;
   unsigned C = 8;
   while (C > 1 && tiles * C > 152 * F::kCtas) C /= 2;
   return launch_k_cluster(lc, k_lora_tiles<KC, TS, TO>, (unsigned)(tiles * C), kThreads, (size_t)F::kBytes, C, a);

@@ -7,9 +7,11 @@
 // memory, rows of neighbouring elements (MN-major), 64 of them to a 128-byte
 // swizzled row: asynchronous copies gather x or dy by the plan's order
 // straight into the layout the tensor cores read.  u or v comes as three bf16
-// parts, which keep its 24 bits, written in the plan's order by the kernel of
-// the products: splitting fp32 values here, once for each 128 columns, was more
-// than half of the instructions (98 us where this takes 63).  The parts of up
+// parts, which keep its 24 bits, written by the kernel of the products as the
+// stages hold them, so that one bulk copy brings a stage's: splitting fp32
+// values here, once for each 128 columns, was more than half of the
+// instructions (98 us where this takes @@), and by 16-byte copies of the threads
+// they took more of the copies' rate than x and dy (61).  The parts of up
 // to 32 ranks stand side by side in the 128 rows of one MMA and are added at
 // the end, those of more take two or three MMAs.
 //
@@ -18,7 +20,7 @@
 // the next MMAs run.  Bound by memory: 2 rank operations a byte (times three
 // parts) are a fifth of what the tensor cores do in the time.
 //
-// Every wait is for MMAs already issued, and bounded; one that gives up is
+// Every wait is for MMAs or copies already issued, and bounded; one that gives up is
 // counted (afd_mx4_poll_status).
 #include "afd_lora.cuh"
 
@@ -36,10 +38,9 @@ constexpr int kOutStride = 65;                   // floats, of the output's stag
 template <int MP>
 struct Tc {
   static constexpr int kMmas = MP <= 32 ? 1 : MP == 64 ? 2 : 3;  // a 16-row step
-  static constexpr int kAtoms = (3 * MP + 63) / 64;              // of the parts
-  static constexpr int kChunks = 3 * MP / 8;                     // 16-byte chunks of a row's parts
+  static constexpr int kAtoms = lora_atoms(MP);                  // of the parts
   static constexpr int kStageBytes = (2 + kAtoms) * kAtom;
-  static constexpr int kStages = MP == 16 ? 7 : MP == 32 ? 6 : MP == 64 ? 4 : 3;
+  static constexpr int kStages = MP == 16 ? 7 : MP == 32 ? 6 : MP == 64 ? 5 : 3;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kBytes = kRing + kAtom;                   // and an atom of zeros: MMA rows of no part
   // accumulator rows of a rank: this many, this far apart (MP 64: the first
@@ -48,11 +49,6 @@ struct Tc {
   static_assert(128 * kOutStride * 4 <= kRing, "the output is staged in the ring");
 };
 
-// MN-major operand, 128-byte swizzle: two atoms of 64 elements `apart` bytes
-// apart, 8-row groups 1024
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t apart) {
-  return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | apart >> 4 << 16 | ((addr & 0x3ffffu) >> 4);
-}
 // bf16 x bf16 -> fp32, both operands MN-major, M = N = 128
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(kSlab >> 3) << 17 | (128u >> 4) << 24;
 
@@ -74,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
   constexpr int S = W::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int32_t rows[kLoraMaxPiece];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t bars[2], there[S];  // MMAs of a stage done; its parts there
   __shared__ uint32_t tmem_base;
   const int4 head = *a.plan.head;
   if ((int)blockIdx.y >= head.z) return;
@@ -82,22 +78,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
   const int nx = a.f32[0] ? 0 : (a.N[0] + kSlab - 1) / kSlab;
   const int which = (int)blockIdx.x >= nx, m0 = ((int)blockIdx.x - (which ? nx : 0)) * kSlab;
   const int N = a.N[which], how = a.how[which], R = a.R;
-  const uint16_t* P = a.parts[which] + (int64_t)pc.y * (3 * MP);
+  // blocks of the parts, as the stages hold them
+  const uint16_t* P = a.parts[which] + (int64_t)(pc.y + a.plan.shift[pc.x]) / kLoraBlockRows * (W::kAtoms * kAtom / 2);
   const uint16_t* Q = reinterpret_cast<const uint16_t*>(a.q[which]);
   const int64_t ldq = a.ldq[which];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = smem_u32(smem), zero = ring + W::kRing, bar = smem_u32(bars);
   for (int i = tid; i < pc.z; i += kThreads) rows[i] = a.plan.order[pc.y + i];
   *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
-  if (W::kChunks % 8)  // chunks of the last atom that no part fills stay zero
-    for (int e = tid; e < S * kRows * (8 - W::kChunks % 8); e += kThreads) {
-      const int c = W::kChunks % 8 + e % (8 - W::kChunks % 8), r = e / (8 - W::kChunks % 8);
-      const uint32_t at = chunk_at(ring + r / kRows * W::kStageBytes + (1 + W::kAtoms) * kAtom, r % kRows, c);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
-    }
   if (tid == 0) {
     mbar_init(bar, 1);
     mbar_init(bar + 8, 1);
+    for (int i = 0; i < S; i++) mbar_init(smem_u32(&there[i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -120,11 +112,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
         load_chunk<uint16_t>(chunk_at(st + (ch >> 3) * kAtom, r, ch & 7), t < pc.z ? Q + (int64_t)rows[t] * ldq : nullptr,
                              m0 + ch * 8, N, how, a.plan.head);
       }
-#pragma unroll
-      for (int j = 0; j < (kRows * W::kChunks + kThreads - 1) / kThreads; j++) {
-        const int e = tid + j * kThreads, r = e / W::kChunks, c = e % W::kChunks, t = i * kRows + r;
-        if (e < kRows * W::kChunks)
-          copy16(chunk_at(st + (2 + (c >> 3)) * kAtom, r, c & 7), P + (t < pc.z ? t : 0) * (3 * MP) + c * 8, t < pc.z);
+      if (tid == 0) {
+        const uint32_t b = smem_u32(&there[i % S]);
+        mbar_expect_tx(b, W::kAtoms * kAtom);
+        bulk_load(st + 2 * kAtom, P + (int64_t)i * (W::kAtoms * kAtom / 2), W::kAtoms * kAtom, b);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -155,32 +146,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (__syncthreads_or(!good)) break;
-    if (tid == 0) {
+    if (warp == 0) {
+      good = __all_sync(0xffffffffu, wait_mma(smem_u32(&there[i % S]), i / S & 1));
       tc_fence_after();
-      const uint32_t d = tmem + (i / kFlush & 1) * kSlab;
-      const uint32_t qa = ring + (i % S) * W::kStageBytes, pa = qa + 2 * kAtom;
+      const uint32_t el = lora_elect(), d = tmem + (i / kFlush & 1) * kSlab;
+      // two atoms of 64 elements each, 8-row groups 1024 bytes apart
+      const uint32_t qa = (ring + (i % S) * W::kStageBytes) >> 4, pa = qa + (2 * kAtom >> 4);
 #pragma unroll
       for (int ks = 0; ks < kRows / 16; ks++)
 #pragma unroll
         for (int x = W::kMmas - 1; x >= 0; x--)
-          tc_mma_f16(d, operand(pa + x * 2 * kAtom + ks * 2048, 2 * x + 1 < W::kAtoms ? kAtom : zero - (pa + x * 2 * kAtom)),
-                     operand(qa + ks * 2048, kAtom), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
-      tc_commit(bar + 8 * (i & 1));
+          lora_mma(el, d, lora_desc(pa + (x * 2 * kAtom + ks * 2048 >> 4), 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - (pa + (x * 2 * kAtom >> 4))),
+                   lora_desc(qa + ks * 128, kAtom >> 4), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+      lora_commit(el, bar + 8 * (i & 1));
     }
     if (i > 0) {  // the stage before: its ring slot is free, its sums complete
-      good = wait_mma(bar + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
+      good &= wait_mma(bar + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
       if (i % kFlush == 0) flush(i / kFlush - 1);
     }
     fill(i + S - 1);
   }
   if (i == n && n > 0) {
-    good = wait_mma(bar + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
+    good &= wait_mma(bar + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
     flush((n - 1) / kFlush);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   const bool bad = __syncthreads_or(!good);
   if (bad) {
-    if (tid == 0) atomicAdd(&g_lora_errors, 1u);
+    if (tid == 0) {
+      atomicAdd(&g_lora_errors, 1u);
+      for (int x = max(0, i - 1); x < min(n, i + S - 1); x++) wait_mma(smem_u32(&there[x % S]), x / S & 1);  // copies under way
+    }
+    __syncthreads();
   } else {
     const float scale = a.scale ? a.scale[pc.x] : 1.0f;
     float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * R * N : a.part[which] + (int64_t)pc.w * R * N;

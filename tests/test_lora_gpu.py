@@ -49,7 +49,7 @@ def near(got, want, tol, what):
     assert bool((over <= 0).all()), (what, float(over.max()), int((over > 0).sum()))
 
 
-def check_apply(d, base="other", scale=True):
+def check_apply(d, base="other", scale=True, out=None):
     T = d["x"].shape[0]
     batch = R.LoraBatch(d["ids"], d["a"].shape[0])
     s = d["scale"] if scale else None
@@ -61,7 +61,7 @@ def check_apply(d, base="other", scale=True):
         assert got is y
     else:
         got, gu = R.lora_apply(batch, d["x"], d["a"], d["b"], d["base"] if base == "other" else None, scale=s,
-                               out_dtype=yt, keep=True)
+                               out=out, out_dtype=yt, keep=True)
     assert got.dtype == yt and gu.dtype == F
     near(gu, u, eu, "u")
     tol = eo + PARTS[yt] * size
@@ -75,9 +75,9 @@ def check_apply(d, base="other", scale=True):
     return batch, got, gu
 
 
-def check_backward(d, batch, u, base="other", scale=True):
+def check_backward(d, batch, u, base="other", scale=True, dx=None):
     s = d["scale"] if scale else None
-    xt = d["x"].dtype
+    xt, to = d["x"].dtype, dx
     dx, da, db, eo, size, ea, eb = ref.adapter_grads(d["ids"], d["x"], d["dy"], u, d["a"], d["b"], s,
                                                      None if base == "none" else d["d_base"])
     if base == "same":
@@ -85,7 +85,7 @@ def check_backward(d, batch, u, base="other", scale=True):
         gx, ga, gb = R.lora_backward(batch, d["x"], d["dy"], u, d["a"], d["b"], d_base=t, scale=s, dx=t)
     else:
         gx, ga, gb = R.lora_backward(batch, d["x"], d["dy"], u, d["a"], d["b"],
-                                     d_base=d["d_base"] if base == "other" else None, scale=s)
+                                     d_base=d["d_base"] if base == "other" else None, scale=s, dx=to)
     tol = eo + PARTS[xt] * size
     near(gx, dx, tol + ref.HALF[xt] * (dx.abs() + tol), "dx")
     near(ga, da, ea + U * (da.abs() + ea), "da")
@@ -141,18 +141,11 @@ def test_pitches(xt, yt, T):
             v = w[:, first:first + d[n].shape[1]]
             v.copy_(d[n])
             d[n] = v
-        batch = R.LoraBatch(d["ids"], 3)
-        y0, u0 = R.lora_apply(batch, d["x"].contiguous(), d["a"], d["b"], d["base"].contiguous(), scale=d["scale"], keep=True)
         o = wide(d["base"])
-        y, u = R.lora_apply(batch, d["x"], d["a"], d["b"], d["base"], scale=d["scale"], out=o[:, first:first + 96], keep=True)
-        assert torch.equal(y, y0) and torch.equal(u, u0)
+        batch, _, u = check_apply(d, out=o[:, first:first + 96])
         assert (o[:, :first] == 7).all() and (o[:, first + 96:] == 7).all()
-        g0 = R.lora_backward(batch, d["x"].contiguous(), d["dy"].contiguous(), u, d["a"], d["b"],
-                             d_base=d["d_base"].contiguous(), scale=d["scale"])
         o = wide(d["d_base"])
-        g = R.lora_backward(batch, d["x"], d["dy"], u, d["a"], d["b"], d_base=d["d_base"], scale=d["scale"],
-                            dx=o[:, first:first + 160])
-        assert all(torch.equal(p, q) for p, q in zip(g, g0))
+        check_backward(d, batch, u, dx=o[:, first:first + 160])
         assert (o[:, :first] == 7).all() and (o[:, first + 160:] == 7).all()
 
 
