@@ -2,94 +2,134 @@
 // tcgen05 (fp32 rows: afd_lora_wgrad.cu):
 //   da[l] = scale[l] sum_t v_t x_t^T,  db[l] = scale[l] sum_t u_t dy_t^T
 //
-// A CTA takes one piece of an adapter's rows and 128 columns of x or dy.  The
-// product's k runs over the rows, so both operands are used as they lie in
+// The product's k runs over the rows, so both operands are used as they lie in
 // memory, rows of neighbouring elements (MN-major), 64 of them to a 128-byte
 // swizzled row: asynchronous copies gather x or dy by the plan's order
 // straight into the layout the tensor cores read.  u or v comes as three bf16
 // parts, which keep its 24 bits, written by the kernel of the products as the
-// stages hold them, so that one bulk copy brings a stage's: splitting fp32
-// values here, once for each 128 columns, was more than half of the
-// instructions (98 us where this takes @@), and by 16-byte copies of the threads
-// they took more of the copies' rate than x and dy (61).  The parts of up
-// to 32 ranks stand side by side in the 128 rows of one MMA and are added at
-// the end, those of more take two or three MMAs.
+// stages hold them: one bulk copy brings a stage's.  The parts of up to 32
+// ranks stand side by side in the 128 rows of one MMA and are added at the
+// end, those of more take two or three MMAs.
 //
 // Sums in TMEM may cut where they should round, so they move to registers
 // every four stages (128 rows) and start anew in the other accumulator, while
-// the next MMAs run.  Bound by memory: 2 rank operations a byte (times three
-// parts) are a fifth of what the tensor cores do in the time.
+// the next MMAs run.
 //
-// Every wait is for MMAs or copies already issued, and bounded; one that gives up is
-// counted (afd_mx4_poll_status).
+// Bound by memory: one CTA an SM runs through items (a piece of an adapter's
+// rows, 256 columns of x or dy) with its warps apart: three copy, one issues the
+// MMAs, sixteen sum and store, and the copies run on into the next item while
+// the last is stored.  With all warps together, two CTAs of 128 columns an SM,
+// a stage of 32 rows took 1150 to 1800 cycles of barrier, issue, wait and
+// copying one after the other, and an item 9000 before and behind its stages
+// (rank 64, 13312 rows: 62 us where this takes 47).
+//
+// All waits are bounded; one that gives up is counted (afd_mx4_poll_status).
 #include "afd_lora.cuh"
 
 namespace {
 
 __device__ uint32_t g_lora_errors;  // waits that gave up
 
-constexpr int kThreads = 256, kRows = 32, kSlab = 128;
+constexpr int kSumWarps = 16, kCopyWarps = 3;  // (and one more: five warps a scheduler leave 96 registers a thread)
+constexpr int kThreads = (kSumWarps + kCopyWarps + 1) * 32;
+constexpr int kRows = kLoraBlockRows, kSlab = 256;
 constexpr int kAtom = kRows * kLoraRowBytes;     // 64 columns or ranks of a stage
 constexpr int kFlush = 4;                        // stages between two moves of the sums
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kOutStride = 65;                   // floats, of the output's staging
+constexpr int kOutStride = 68;                   // floats, of the output's staging
 
 // MP: ranks of a part, padded: the parts stand MP rows apart
 template <int MP>
 struct Tc {
   static constexpr int kMmas = MP <= 32 ? 1 : MP == 64 ? 2 : 3;  // a 16-row step
   static constexpr int kAtoms = lora_atoms(MP);                  // of the parts
-  static constexpr int kStageBytes = (2 + kAtoms) * kAtom;
-  static constexpr int kStages = MP == 16 ? 7 : MP == 32 ? 6 : MP == 64 ? 5 : 3;
-  static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kBytes = kRing + kAtom;                   // and an atom of zeros: MMA rows of no part
-  // accumulator rows of a rank: this many, this far apart (MP 64: the first
-  // and third part share theirs)
+  static constexpr int kStageBytes = (kSlab / 64 + kAtoms) * kAtom;
+  // accumulator rows of a rank: this many, MP apart (MP 64: the first and
+  // third part share theirs), which meet in shared memory
   static constexpr int kSums = MP <= 32 ? 3 : MP == 64 ? 2 : 1;
-  static_assert(128 * kOutStride * 4 <= kRing, "the output is staged in the ring");
+  static constexpr int kOutBytes = kSums > 1 ? 4 * 64 * kOutStride * 4 : 0;
+  static constexpr int kStages = (224 * 1024 - kAtom - kOutBytes) / kStageBytes;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kBytes = kRing + kAtom + kOutBytes;       // with an atom of zeros: MMA rows of no part
 };
 
-// bf16 x bf16 -> fp32, both operands MN-major, M = N = 128
+// bf16 x bf16 -> fp32, both operands MN-major, M 128, N 256
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(kSlab >> 3) << 17 | (128u >> 4) << 24;
 
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+// false: the wait, or another one of the CTA, has given up
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t start = globaltimer_ns();
   uint32_t spins = 0;
   while (!mbar_try_wait(bar, parity)) {
-    if ((++spins & 255u) == 0 && globaltimer_ns() - start > kTimeoutNs) return false;
+    if ((++spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - start > kTimeoutNs) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
   }
   return true;
 }
-__device__ __forceinline__ bool wait_mma(uint32_t bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || wait_long(bar, parity);
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag));
+}
+
+// of the 128 threads at a barrier: whether all say yes
+__device__ __forceinline__ bool all_of(int id, bool yes) {
+  uint32_t r;
+  asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %2, 0; bar.red.and.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
+               : "=r"(r) : "r"(id), "r"((uint32_t)yes) : "memory");
+  return r != 0;
+}
+
+// scaled values of a row from column c on
+__device__ __forceinline__ void store_four(float* row, int c, int N, float scale, const float* v) {
+  if (N % 4 == 0) {
+    if (c < N) *reinterpret_cast<float4*>(row + c) = make_float4(scale * v[0], scale * v[1], scale * v[2], scale * v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (c + j < N) row[c + j] = scale * v[j];
+  }
+}
+template <int COLS>
+__device__ __forceinline__ void store_row(float* row, int c, int N, float scale, const float (&v)[COLS]) {
+#pragma unroll
+  for (int j = 0; j < COLS; j += 4) store_four(row, c + j, N, scale, v + j);
+}
+
+// A stage's rows where they cannot be moved 16 bytes at a time.
+__device__ __noinline__ void slow_rows(uint32_t st, const uint16_t* Q, int64_t ldq, int my_row, int have, int col, int N, int how, const void* any) {
+  const int lane = threadIdx.x & 31;
+  for (int j = 0; j < kRows; j++) {
+    const int64_t row = __shfl_sync(0xffffffffu, my_row, j);
+    load_chunk<uint16_t>(chunk_at(st + (lane >> 3) * kAtom, j, lane & 7), j < have ? Q + row * ldq : nullptr, col, N, how, any);
+  }
 }
 
 template <int MP>
-__global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_constant__ LoraWgradArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_lora_wgrad_tc(const __grid_constant__ LoraWgradArgs a) {
   typedef Tc<MP> W;
   constexpr int S = W::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int32_t rows[kLoraMaxPiece];
-  __shared__ uint64_t bars[2], there[S];  // MMAs of a stage done; its parts there
+  // of each stage: full, free again; sums of a group of stages: complete, taken
+  __shared__ uint64_t full[S], empty[S], dfull[2], dempty[2];
   __shared__ uint32_t tmem_base;
-  const int4 head = *a.plan.head;
-  if ((int)blockIdx.y >= head.z) return;
-  const int4 pc = a.plan.pieces[blockIdx.y];
-  const int nx = a.f32[0] ? 0 : (a.N[0] + kSlab - 1) / kSlab;
-  const int which = (int)blockIdx.x >= nx, m0 = ((int)blockIdx.x - (which ? nx : 0)) * kSlab;
-  const int N = a.N[which], how = a.how[which], R = a.R;
-  // blocks of the parts, as the stages hold them
-  const uint16_t* P = a.parts[which] + (int64_t)(pc.y + a.plan.shift[pc.x]) / kLoraBlockRows * (W::kAtoms * kAtom / 2);
-  const uint16_t* Q = reinterpret_cast<const uint16_t*>(a.q[which]);
-  const int64_t ldq = a.ldq[which];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = smem_u32(smem), zero = ring + W::kRing, bar = smem_u32(bars);
-  for (int i = tid; i < pc.z; i += kThreads) rows[i] = a.plan.order[pc.y + i];
-  *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
-  if (tid == 0) {
-    mbar_init(bar, 1);
-    mbar_init(bar + 8, 1);
-    for (int i = 0; i < S; i++) mbar_init(smem_u32(&there[i]), 1);
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.R;
+  const int nx = a.f32[0] ? 0 : (a.N[0] + kSlab - 1) / kSlab, slabs = nx + (a.f32[1] ? 0 : (a.N[1] + kSlab - 1) / kSlab);
+  const int items = a.plan.head->z * slabs;
+  const uint32_t ring = smem_u32(smem), zero = ring + W::kRing;
+  if (tid < kAtom / 16) *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < S) {
+    mbar_init(smem_u32(&full[tid]), 33);  // a copying warp's lanes, and its bulk copy
+    mbar_init(smem_u32(&empty[tid]), 1);
+    if (tid < 2) {
+      mbar_init(smem_u32(&dfull[tid]), 1);
+      mbar_init(smem_u32(&dempty[tid]), kSumWarps);
+    }
+    if (tid == 0) abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -97,110 +137,165 @@ __global__ void __launch_bounds__(kThreads, 2) k_lora_wgrad_tc(const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int n = (pc.z + kRows - 1) / kRows;
-
-  auto fill = [&](int i) {
-    if (i < n) {
-      const uint32_t st = ring + (i % S) * W::kStageBytes;
-      const int ch = tid & 15;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int r = (tid >> 4) + h * 16, t = i * kRows + r;
-        load_chunk<uint16_t>(chunk_at(st + (ch >> 3) * kAtom, r, ch & 7), t < pc.z ? Q + (int64_t)rows[t] * ldq : nullptr,
-                             m0 + ch * 8, N, how, a.plan.head);
-      }
-      if (tid == 0) {
-        const uint32_t b = smem_u32(&there[i % S]);
-        mbar_expect_tx(b, W::kAtoms * kAtom);
-        bulk_load(st + 2 * kAtom, P + (int64_t)i * (W::kAtoms * kAtom / 2), W::kAtoms * kAtom, b);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // accumulator row 32 (warp % 4) + lane, columns 64 (warp / 4) ..
-  float sum[64];
-#pragma unroll
-  for (int j = 0; j < 64; j++) sum[j] = 0.0f;
-  const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * 64;
-  auto flush = [&](int group) {
-    tc_fence_after();
-    const uint32_t d = mine + (group & 1) * kSlab;
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(d + h * 32, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; j++) sum[h * 32 + j] += __uint_as_float(v[j]);
-    }
-    tc_fence_before();
-  };
-#pragma unroll
-  for (int i = 0; i < S - 1; i++) fill(i);
+  volatile int* const gave_up = &abort_flag;
   bool good = true;
-  int i = 0;
-  for (; i < n; i++) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (__syncthreads_or(!good)) break;
-    if (warp == 0) {
-      good = __all_sync(0xffffffffu, wait_mma(smem_u32(&there[i % S]), i / S & 1));
-      tc_fence_after();
-      const uint32_t el = lora_elect(), d = tmem + (i / kFlush & 1) * kSlab;
-      // two atoms of 64 elements each, 8-row groups 1024 bytes apart
-      const uint32_t qa = (ring + (i % S) * W::kStageBytes) >> 4, pa = qa + (2 * kAtom >> 4);
-#pragma unroll
-      for (int ks = 0; ks < kRows / 16; ks++)
-#pragma unroll
-        for (int x = W::kMmas - 1; x >= 0; x--)
-          lora_mma(el, d, lora_desc(pa + (x * 2 * kAtom + ks * 2048 >> 4), 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - (pa + (x * 2 * kAtom >> 4))),
-                   lora_desc(qa + ks * 128, kAtom >> 4), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
-      lora_commit(el, bar + 8 * (i & 1));
+  int slot = 0, stage = 0;  // of the ring, over all items
+  uint32_t turn = 0;
+  auto next = [&]() {
+    stage++;
+    if (++slot == S) {
+      slot = 0;
+      turn++;
     }
-    if (i > 0) {  // the stage before: its ring slot is free, its sums complete
-      good &= wait_mma(bar + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1);
-      if (i % kFlush == 0) flush(i / kFlush - 1);
-    }
-    fill(i + S - 1);
-  }
-  if (i == n && n > 0) {
-    good &= wait_mma(bar + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
-    flush((n - 1) / kFlush);
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  const bool bad = __syncthreads_or(!good);
-  if (bad) {
-    if (tid == 0) {
-      atomicAdd(&g_lora_errors, 1u);
-      for (int x = max(0, i - 1); x < min(n, i + S - 1); x++) wait_mma(smem_u32(&there[x % S]), x / S & 1);  // copies under way
-    }
-    __syncthreads();
-  } else {
-    const float scale = a.scale ? a.scale[pc.x] : 1.0f;
-    float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * R * N : a.part[which] + (int64_t)pc.w * R * N;
-    float* stage = reinterpret_cast<float*>(smem);  // [128][kOutStride]
-    for (int p = 0; p < 2; p++) {  // 64 columns at a time
-      if (warp >> 2 == p) {
-        float* s = stage + ((warp & 3) * 32 + lane) * kOutStride;
+  };
+
+  if (warp >= kSumWarps && warp < kSumWarps + kCopyWarps) {  // ---- copies: every kCopyWarps-th stage ----
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int4 pc = a.plan.pieces[item / slabs];
+      const int slab = item % slabs, which = slab >= nx, m0 = (slab - (which ? nx : 0)) * kSlab;
+      const int N = a.N[which], col = m0 + lane * 8, n = (pc.z + kRows - 1) / kRows;
+      const uint16_t* Q = reinterpret_cast<const uint16_t*>(a.q[which]);
+      const uint16_t* P = a.parts[which] + (int64_t)(pc.y + a.plan.shift[pc.x]) / kRows * (W::kAtoms * kAtom / 2);
+      const int64_t ldq = a.ldq[which];
+      const bool fast = a.how[which] == 2, in = col < N;
+      for (int i = 0; i < n; i++, next()) {
+        if (stage % kCopyWarps != warp - kSumWarps) continue;
+        if (turn) {
+          good = warp_wait(smem_u32(&empty[slot]), (turn - 1) & 1, gave_up);
+          if (!good) break;
+        }
+        const uint32_t st = ring + slot * W::kStageBytes, bar = smem_u32(&full[slot]);
+        const int have = min(kRows, pc.z - i * kRows);  // rows of the piece; the others zero
+        const int my_row = lane < have ? a.plan.order[pc.y + i * kRows + lane] : 0;
+        if (lane == 0) {
+          mbar_expect_tx(bar, W::kAtoms * kAtom);
+          bulk_load(st + kSlab / 64 * kAtom, P + (int64_t)i * (W::kAtoms * kAtom / 2), W::kAtoms * kAtom, bar);
+        }
+        if (fast) {
+          const char* p = in ? reinterpret_cast<const char*>(Q + col) : reinterpret_cast<const char*>(a.plan.head);
+          const int64_t pitch = in ? ldq * 2 : 0;
+          const uint32_t to = st + (lane >> 3) * kAtom, ch = (lane & 7) << 4;
 #pragma unroll
-        for (int j = 0; j < 64; j++) s[j] = sum[j];
-      }
-      __syncthreads();
-      for (int e = tid; e < R * 64; e += kThreads) {
-        const int r = e >> 6, col = m0 + p * 64 + (e & 63);
-        if (col < N) {
-          float v = stage[r * kOutStride + (e & 63)];
-#pragma unroll
-          for (int x = 1; x < W::kSums; x++) v += stage[(x * MP + r) * kOutStride + (e & 63)];
-          out[(int64_t)r * N + col] = scale * v;
+          for (int j = 0; j < kRows; j++) {
+            const int row = __shfl_sync(0xffffffffu, my_row, j);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * kLoraRowBytes + (ch ^ (j & 7) << 4)),
+                         "l"(p + row * pitch), "r"(in && j < have ? 16 : 0)
+                         : "memory");
+          }
+          // each lane arrives when its copies have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        } else {
+          slow_rows(st, Q, ldq, my_row, have, col, N, a.how[which], a.plan.head);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          mbar_arrive(bar);
         }
       }
-      __syncthreads();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kSumWarps + kCopyWarps) {  // ---- products ----
+    const uint32_t el = lora_elect();
+    uint32_t group = 0;
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int n = (a.plan.pieces[item / slabs].z + kRows - 1) / kRows;
+      for (int i = 0; i < n; i++, next()) {
+        good = warp_wait(smem_u32(&full[slot]), turn & 1, gave_up);
+        if (good && i % kFlush == 0 && group >= 2) good = warp_wait(smem_u32(&dempty[group & 1]), (group / 2 - 1) & 1, gave_up);
+        if (!good) break;
+        // the copies' writes, seen through the barrier, before the products'
+        // reads, which go another way
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_after();
+        const uint32_t d = tmem + (group & 1) * kSlab;
+        // atoms of 64 elements, 8-row groups 1024 bytes apart
+        const uint32_t qa = (ring + slot * W::kStageBytes) >> 4, pa = qa + (kSlab / 64 * kAtom >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kRows / 16; ks++)
+#pragma unroll
+          for (int x = W::kMmas - 1; x >= 0; x--)
+            lora_mma(el, d, lora_desc(pa + (x * 2 * kAtom + ks * 2048 >> 4), 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - (pa + (x * 2 * kAtom >> 4))),
+                     lora_desc(qa + ks * 128, kAtom >> 4), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+        lora_commit(el, smem_u32(&empty[slot]));
+        if (i % kFlush == kFlush - 1 || i == n - 1) lora_commit(el, smem_u32(&dfull[group++ & 1]));
+      }
+    }
+    if (!good) {  // (a wait has given up: time for bulk copies under way to land)
+      const uint64_t start = globaltimer_ns();
+      while (globaltimer_ns() - start < 1000000ull) {}
+    }
+  } else {  // ---- sums: accumulator row 32 (warp % 4) + lane, columns 64 (warp / 4) .. ----
+    const int m = (warp & 3) * 32 + lane, cg = warp >> 2;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + cg * 64;
+    float* out_stage = reinterpret_cast<float*>(smem + W::kRing + kAtom) + cg * 64 * kOutStride;  // [64][kOutStride]
+    uint32_t group = 0;
+    auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + cg) : "memory"); };  // the four warps of these columns
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int4 pc = a.plan.pieces[item / slabs];
+      const int slab = item % slabs, which = slab >= nx, m0 = (slab - (which ? nx : 0)) * kSlab + cg * 64;
+      const int N = a.N[which], n = (pc.z + kRows - 1) / kRows;
+      float sum[64];
+#pragma unroll
+      for (int j = 0; j < 64; j++) sum[j] = 0.0f;
+      for (int i = 0; i < n; i += kFlush, group++) {
+        good = warp_wait(smem_u32(&dfull[group & 1]), group / 2 & 1, gave_up);
+        if (!good) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t v[16];
+          tmem_ld_16(mine + (group & 1) * kSlab + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty[group & 1]));
+      }
+      if (!all_of(1 + cg, good)) {  // (the four warps leave together: none waits for one that has left)
+        good = false;
+        break;
+      }
+      const float scale = a.scale ? a.scale[pc.x] : 1.0f;
+      float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * R * N : a.part[which] + (int64_t)pc.w * R * N;
+      if (W::kSums == 1) {
+        if (m < R) store_row<64>(out + (int64_t)m * N, m0, N, scale, sum);
+        continue;
+      }
+      // the parts' sums meet, and go to memory a row's 64 columns at a time
+      float* mine_out = out_stage + (m < MP ? m : m - MP) * kOutStride;
+      if (m >= MP && m < W::kSums * MP) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) *reinterpret_cast<float4*>(mine_out + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+      }
+      meet();
+      if (m < MP) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+#pragma unroll
+          for (int x = 0; x < W::kSums - 1; x++) {
+            const float4 v = *reinterpret_cast<const float4*>(mine_out + x * MP * kOutStride + j);
+            sum[j] += v.x; sum[j + 1] += v.y; sum[j + 2] += v.z; sum[j + 3] += v.w;
+          }
+          *reinterpret_cast<float4*>(mine_out + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+        }
+      }
+      meet();
+      for (int r = (warp & 3) * 8 + (lane >> 2); r < R; r += 32) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) v[j] = out_stage[r * kOutStride + (lane & 3) * 4 + j / 4 * 16 + j % 4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) store_four(out + (int64_t)r * N, m0 + (lane & 3) * 4 + j * 16, N, scale, v + 4 * j);
+      }
+      meet();
     }
   }
+  __syncthreads();
+  if (tid == 0 && abort_flag) atomicAdd(&g_lora_errors, 1u);
   tc_fence_after();
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kSlab));
 }
@@ -209,12 +304,9 @@ template <int MP>
 cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
   typedef Tc<MP> W;
   static std::atomic<int> done[kMaxCachedDevices];
-  cudaError_t e = smem_attr_once(k_lora_wgrad_tc<MP>, W::kBytes, done);
+  const cudaError_t e = smem_attr_once(k_lora_wgrad_tc<MP>, W::kBytes, done);
   if (e != cudaSuccess) return e;
-  int slabs = 0;
-  for (int w = 0; w < 2; w++)
-    if (!a.f32[w]) slabs += (a.N[w] + kSlab - 1) / kSlab;
-  return launch_k(lc, k_lora_wgrad_tc<MP>, dim3(slabs, (unsigned)a.plan.max_pieces), kThreads, W::kBytes, a);
+  return launch_k(lc, k_lora_wgrad_tc<MP>, kLoraSms, kThreads, W::kBytes, a);
 }
 
 }  // namespace
