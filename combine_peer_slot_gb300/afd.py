@@ -140,6 +140,7 @@ SIGNATURES = [
     ("afd_lora_backward_workspace", _I64, [_I64, _I, _I, _I, _I]),
     ("afd_lora_backward", _I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _I64, _I, _I, _P, _P, _P, _I, _P, _P, _I64, _P,
                                _I64, _P, _P, _P, _I64, _P]),
+    ("afd_lora_poll_status", _I, [_P]),
 ]
 AFD_NUM_STAGES = 8
 STAGE_NAMES = ("header_check", "router", "plan", "gather", "gemm_swiglu", "gemm_down",
@@ -532,3 +533,7 @@ def afd_lora_backward(plan, n_tokens, n_adapters, x, ldx, x_dtype, K, dy, ldy, y
                                    y_dtype, M, u or None, a or None, b or None, rank, scale or None,
                                    d_base or None, ldb, dx or None, ldd, da or None, db or None,
                                    workspace or None, workspace_bytes, stream or None)
+
+
+def afd_lora_poll_status(stream=0):
+    return lib().afd_lora_poll_status(stream or None)

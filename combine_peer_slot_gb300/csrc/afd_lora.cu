@@ -3,6 +3,8 @@
 // entry points.  The products themselves are in afd_lora_apply.cu.
 #include "afd_lora.cuh"
 
+#include <map>
+
 namespace {
 
 constexpr int kPlanWarps = 32;
@@ -193,7 +195,7 @@ extern "C" int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters
   if (n_tokens == 0) return AFD_OK;
   if (!plan || off_by(plan, 256) || !x || !a || !b || !out || off_by(x, size_of(x_dtype)) || off_by(a, 2) ||
       off_by(b, 2) || off_by(scale, 4) || off_by(base, size_of(y_dtype)) || off_by(out, size_of(y_dtype)) ||
-      off_by(u, 4) || (base == out && ldb != ldo))
+      off_by(u, 4) || (base == out && ldb != ldo) || x == out)
     return AFD_ERR_ARG;
   const int rc = check_device_ptrs({plan, x, a, b, scale, base, out, u});
   if (rc) return rc;
@@ -236,7 +238,7 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
       (!plan || off_by(plan, 256) || !x || !dy || !u || !a || !b || !dx || !workspace || off_by(workspace, 256) ||
        off_by(x, size_of(x_dtype)) || off_by(dy, size_of(y_dtype)) || off_by(u, 4) || off_by(a, 2) || off_by(b, 2) ||
        off_by(scale, 4) || off_by(d_base, size_of(x_dtype)) || off_by(dx, size_of(x_dtype)) ||
-       (d_base == dx && ldb != ldd)))
+       (d_base == dx && ldb != ldd) || x == dx || dy == dx))
     return AFD_ERR_ARG;
   if (workspace_bytes < need) return AFD_ERR_CAPACITY;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
@@ -298,4 +300,27 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
     return AFD_ERR_CUDA;
   }
   return AFD_OK;
+}
+
+// The errors are counted and never cleared, and a caller is told of those since
+// its own last call, so that no caller takes another's.
+extern "C" int afd_lora_poll_status(void* cuda_stream) {
+  uint32_t n[2] = {0, 0};
+  int dev = 0;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
+  if (cudaGetDevice(&dev) != cudaSuccess || lora_error_count(&n[0], stream) != cudaSuccess ||
+      lora_tc_error_count(&n[1], stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess) {
+    cudaGetLastError();
+    return AFD_ERR_CUDA;
+  }
+  const uint32_t all = n[0] + n[1];
+  bool more = all != 0;
+  try {
+    thread_local std::map<std::pair<int, void*>, uint32_t> told;
+    uint32_t& last = told[{dev, cuda_stream}];
+    more = all != last;
+    last = all;
+  } catch (...) {  // no memory to keep it: told again
+  }
+  return more ? AFD_ERR_TIMEOUT : AFD_OK;
 }

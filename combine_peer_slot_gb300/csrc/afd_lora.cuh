@@ -113,7 +113,7 @@ cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles
 bool lora_tc_takes(const LoraArgs& a);                                  // the next one's sizes and alignment
 cudaError_t launch_lora_tc(const LaunchCtx& lc, const LoraArgs& a);     // tiles of 128
 cudaError_t lora_tc_error_count(uint32_t* n, cudaStream_t stream);
-cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a);
+cudaError_t launch_lora_wgrad(LaunchCtx lc, const LoraWgradArgs& a);
 cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, const LoraWgradArgs& a);  // the matrices of bf16 rows
 cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);          // waits that gave up, once the stream is there
 

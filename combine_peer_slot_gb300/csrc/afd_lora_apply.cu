@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int4 head = *a.plan.head;
   const int64_t tile = blockIdx.x / C;
+  const int4 t = a.plan.tiles[tile];  // (read beside head; past its tiles there is room for more)
   if (tile >= head.x + head.y) return;
-  const int4 t = a.plan.tiles[tile];
   const int32_t* order = a.plan.order + t.y;
   if (t.x < 0) {  // rows without an adapter: out = base
     for (int i = warp; i < t.z; i += kWarps) {
@@ -171,12 +171,32 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
     }
     __syncthreads();
   }
+  // the second product's share of this warp; its first columns' weight, which
+  // does not depend on u, is asked for while the CTAs meet
+  const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
+  const int sub = (t.z + 15) / 16, items = (a.M + 63) / 64 * sub, all = C * kWarps;
+  const int per = (items + all - 1) / all, first = (q * kWarps + warp) * per, groups = (rt + KC - 1) / KC;
+  uint4 early[4][1];
+  const bool ahead = KC == 1 && first < items;
+  if (ahead) {
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+      const int r = 2 * c + (x >> 1) * 8 + (x & 1);
+      load_eight<uint16_t>(w2 + (int64_t)r * a.M, first / sub * 64 + g * 8, r < a.R ? a.M : 0, vm, early[x]);
+    }
+    const int i = first % sub * 16 + lane / 2;  // and the rows of base
+    if (a.base && i < t.z)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TO*>(a.base) + (int64_t)order[i] * a.ldb +
+                                                    min(first / sub * 64 + (lane & 1) * 32, a.M - 1)));
+  }
   cluster.sync();
   for (int e = threadIdx.x; e < rt * 16 * TT; e += kWarps * 32) {
     const int r = e / TT, i = e % TT;
-    float v = 0.0f;
-    if (i < t.z)
-      for (int o = 0; o < C; o++) v += cluster.map_shared_rank(part, o)[e];
+    float w[8], v = 0.0f;  // (at most eight CTAs: all asked for, then added in order)
+#pragma unroll
+    for (int o = 0; o < 8; o++) w[o] = i < t.z && o < C ? cluster.map_shared_rank(part, o)[e] : 0.0f;
+#pragma unroll
+    for (int o = 0; o < 8; o++) v += w[o];
     uint16_t p[kU];
     split_bf16<kU>(v, p);
 #pragma unroll
@@ -197,9 +217,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   }
   cluster.sync();  // (no CTA's sums are read after this)
   const float scale = a.scale ? a.scale[t.x] : 1.0f;
-  const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
-  const int sub = (t.z + 15) / 16, items = (a.M + 63) / 64 * sub, all = C * kWarps;
-  const int per = (items + all - 1) / all, first = (q * kWarps + warp) * per, groups = (rt + KC - 1) / KC;
   uint32_t b[KC][8][2];
   int held = -1;
   for (int it = first; it < min(first + per, items); it++) {
@@ -215,10 +232,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
 #pragma unroll
         for (int kc = 0; kc < KC; kc++) {
           uint4 v[4][1];
+          if (KC == 1 && it == first) {
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
-            load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, vm, v[x]);
+            for (int x = 0; x < 4; x++) v[x][0] = early[x][0];
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
+              load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, vm, v[x]);
+            }
           }
           pair_rows(v[0][0], v[1][0], v[2][0], v[3][0], b[kc]);
         }

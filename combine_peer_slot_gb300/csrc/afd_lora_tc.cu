@@ -15,7 +15,7 @@
 // u goes into the second product as two bf16 parts, 16 of its bits.  The sums of the first product move from TMEM to registers every eight
 // stages, since the tensor cores' fp32 sums cut where they should round.
 //
-// All waits are bounded; one that gives up is counted (afd_mx4_poll_status).
+// All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"
 
 namespace {

@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   const int wt = warp & 3, half = warp >> 2;  // 16 rows; first product: half of the ranks, second: of the columns
   const int4 head = *a.plan.head;
   const int64_t tile = blockIdx.x / C / 2;  // half of one of the plan's tiles
+  int4 t = a.plan.tiles[tile];  // (read beside head; past its tiles there is room for more)
   if (tile >= head.x + head.y) return;
-  int4 t = a.plan.tiles[tile];
   const int skip = blockIdx.x / C % 2 * TT;
   if (t.z <= skip) return;
   t.y += skip;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   // This thread's chunk of rows tid / 8 and tid / 8 + 32 of a tile, and of the
   // weight's rows tid / kWc + i kWr: addresses that move on by a stage's columns.
   const int ch = tid & 7, r0 = tid >> 3;
-  const bool fast = a.how_src == 2 && a.how_w1 == 2 && a.how_w2 == 2 && a.how_base == 2;
+  const bool fast1 = a.how_src == 2 && a.how_w1 == 2, fast2 = a.how_w2 == 2 && a.how_base == 2;
   const char *p0 = nullptr, *p1 = nullptr, *pw = nullptr;
   int left = 0, wleft = 0;  // columns from the chunk on; <= 0: none
   auto start = [&](const void* rows_at, int64_t ld, int size, int first, int cols, int chunk_cols, const uint16_t* w, int wide) {
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   auto fill = [&](int i) {
     if (i < n) {
       const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
-      if (fast) {
+      if (i < n1 ? fast1 : fast2) {
         if (i == 0 && n1 > 0) start(a.src, a.lds, sizeof(TS), k0, a.K, KB, w1, a.K);
         if (i == n1) start(a.base, a.ldb, sizeof(TO), m0, a.M, CB, w2, a.M);
         copy16(chunk_at(st, r0, ch), p0 ? p0 : (const char*)a.plan.head, p0 && left > 0);
@@ -246,8 +246,12 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
 #pragma unroll
     for (int i = 0; i < kMine; i++) {
       const int e = tid + i * kThreads, at = e / (KC * 16) * F::kUStride + e % (KC * 16);
+      float w[8];  // (at most eight CTAs: all asked for, then added in order)
+#pragma unroll
+      for (int o = 0; o < 8; o++) w[o] = o < C ? cluster.map_shared_rank(part, o)[at] : 0.0f;
       v[i] = 0.0f;
-      for (int o = 0; o < C; o++) v[i] += cluster.map_shared_rank(part, o)[at];
+#pragma unroll
+      for (int o = 0; o < 8; o++) v[i] += w[o];
     }
     cluster.sync();
 #pragma unroll

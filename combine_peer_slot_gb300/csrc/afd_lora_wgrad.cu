@@ -182,6 +182,7 @@ template <int RG>
 __global__ void __launch_bounds__(Wg<RG>::kThreads, Wg<RG>::kCtas) k_lora_wgrad(const __grid_constant__ LoraWgradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int32_t rows[kLoraMaxPiece];
+  grid_dep_wait();
   const int4 head = *a.plan.head;
   if ((int)blockIdx.y >= head.z) return;
   const int4 pc = a.plan.pieces[blockIdx.y];
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(Wg<RG>::kThreads, Wg<RG>::kCtas) k_lora_wgrad(
 // rows: zeros.  (One piece: already written.)  V values a thread at a time.
 template <int V>
 __global__ void __launch_bounds__(256) k_lora_wgrad_sum(const __grid_constant__ LoraWgradArgs a) {
+  grid_dep_wait();
   const int l = blockIdx.y;
   const int pieces = a.plan.first[a.L + l];
   if (pieces == 1) return;
@@ -240,7 +242,11 @@ cudaError_t by_rank(const LaunchCtx& lc, const LoraWgradArgs& a) {
 
 }  // namespace
 
-cudaError_t launch_lora_wgrad(const LaunchCtx& lc, const LoraWgradArgs& a) {
+// Each kernel may start while the one before it ends, and waits for its end
+// before all else (a block that left without waiting would let the next one
+// start too early).
+cudaError_t launch_lora_wgrad(LaunchCtx lc, const LoraWgradArgs& a) {
+  lc.pdl = 1;
   cudaError_t e = cudaSuccess;
   if (!a.f32[0] || !a.f32[1]) e = launch_lora_wgrad_tc(lc, a);
   if (e == cudaSuccess && (a.f32[0] || a.f32[1])) e = by_rank(lc, a);

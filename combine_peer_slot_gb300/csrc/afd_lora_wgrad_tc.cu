@@ -23,7 +23,7 @@
 // copying one after the other, and an item 9000 before and behind its stages
 // (rank 64, 13312 rows: 62 us where this takes 47).
 //
-// All waits are bounded; one that gives up is counted (afd_mx4_poll_status).
+// All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"
 
 namespace {
@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_wgrad_tc(const __grid_cons
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.R;
   const int nx = a.f32[0] ? 0 : (a.N[0] + kSlab - 1) / kSlab, slabs = nx + (a.f32[1] ? 0 : (a.N[1] + kSlab - 1) / kSlab);
-  const int items = a.plan.head->z * slabs;
   const uint32_t ring = smem_u32(smem), zero = ring + W::kRing;
   if (tid < kAtom / 16) *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
   if (tid < S) {
@@ -140,7 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_wgrad_tc(const __grid_cons
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   tc_fence_after();
+  grid_dep_wait();  // the products' kernel
   const uint32_t tmem = tmem_base;
+  const int items = a.plan.head->z * slabs;
   volatile int* const gave_up = &abort_flag;
   bool good = true;
   int slot = 0, stage = 0;  // of the ring, over all items

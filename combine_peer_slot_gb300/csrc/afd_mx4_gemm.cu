@@ -43,7 +43,6 @@
 //
 // Warps: 0 weight copies, 1 MMA, from 2 scales, 3 or 7 token copies, 8-15
 // epilogue.  All waits are bounded.
-#include "afd_lora.cuh"
 #include "afd_mx4.cuh"
 
 #include <cudaTypedefs.h>
@@ -1230,17 +1229,15 @@ int encode_mx4_weight(CUtensorMap* tm, const void* packed, int64_t bytes) {
 // its own last call: with one word that the first caller cleared, a product on
 // another stream or thread could give up and its caller hear of nothing.
 extern "C" int afd_mx4_poll_status(void* cuda_stream) {
-  uint32_t n = 0, lora = 0, lora_tc = 0;
+  uint32_t n = 0;
   int dev = 0;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaMemcpyFromSymbolAsync(&n, g_mx4_errors, sizeof n, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-      lora_error_count(&lora, stream) != cudaSuccess || lora_tc_error_count(&lora_tc, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess) {
     cudaGetLastError();
     return AFD_ERR_CUDA;
   }
-  n += lora + lora_tc;
   bool more = n != 0;
   try {
     thread_local std::map<std::pair<int, void*>, uint32_t> told;

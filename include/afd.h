@@ -759,8 +759,8 @@ int afd_mx4_ffn(const uint8_t* codes, const uint8_t* scales, int64_t n_rows,
 
 /* Synchronise the stream; AFD_ERR_TIMEOUT if, since this host thread's last
  * call for this stream (since the library was loaded, for its first), a
- * bounded wait (2 s) of any of the products above, or of afd_lora_backward, on
- * the current device gave up and left its outputs incomplete; else AFD_OK.  The products of all
+ * bounded wait (2 s) of any of the products above on the current device gave
+ * up and left its outputs incomplete; else AFD_OK.  The products of all
  * streams are counted together: an error is told once to each thread and
  * stream that polls, so that no caller takes another's. */
 int afd_mx4_poll_status(void* cuda_stream);
@@ -838,7 +838,8 @@ int afd_lora_plan(const int32_t* ids, int64_t n_tokens, int n_adapters, void* pl
  *   base     device, y_dtype [n_tokens, M], row pitch ldb: the shared
  *            projection's rows; NULL: zeros; may be out itself (same pitch),
  *            whose rows without an adapter are then left as they are
- *   out      device, y_dtype [n_tokens, M], row pitch ldo
+ *   out      device, y_dtype [n_tokens, M], row pitch ldo; no other overlap
+ *            of what is written with what is read
  *   u        device fp32 [n_tokens, rank] out, or NULL: kept for
  *            afd_lora_backward; 0 for rows without an adapter
  * Any pitch and element alignment; rows of whole 16 bytes with K % 8 == 0 and
@@ -855,7 +856,8 @@ int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters, const voi
  *   dA[l] = scale[l] sum_t v_t x_t^T          fp32 [n_adapters, rank, K]
  *   dB[l] = scale[l] sum_t u_t dy_t^T         fp32 [n_adapters, rank, M]
  * dy: y_dtype [n_tokens, M], row pitch ldy; u: afd_lora_apply's; d_base: the
- * shared projection's gradient, NULL or dx itself as base above.  dA and dB
+ * shared projection's gradient, NULL or dx itself as base above, and no other
+ * overlap.  dA and dB
  * (16-byte aligned) are written whole, zeros for adapters without rows (also
  * with n_tokens 0).  The sums' order does not depend on timing.  workspace:
  * device, 256-byte aligned, at least afd_lora_backward_workspace bytes (host
@@ -868,6 +870,11 @@ int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const 
                       const float* scale, const void* d_base, int64_t ldb, void* dx, int64_t ldd,
                       float* dA, float* dB, void* workspace, int64_t workspace_bytes,
                       void* cuda_stream);
+
+/* afd_mx4_poll_status of the adapters' calls: AFD_ERR_TIMEOUT if a bounded wait
+ * (2 s) of afd_lora_apply or afd_lora_backward gave up since this thread's last
+ * call for this stream. */
+int afd_lora_poll_status(void* cuda_stream);
 
 /* Static string for a status code. */
 const char* afd_strerror(int code);

@@ -189,6 +189,25 @@ def test_strides(dtype):
         assert torch.equal(R.route_backward(view, ids, out=view, **kw), d)
 
 
+def test_offsets_over_32_bits():
+    T, pitch = 700, (5 * 2 ** 29) // 700 // 8 * 8
+    l = torch.empty(T * pitch, dtype=torch.bfloat16, device="cuda").view(T, pitch)[:, :64]
+    l.copy_(draw(T, 64, 6, 1, torch.bfloat16)[0])
+    ids = R.route_select(l, 6)[0]
+    _, counts = check_balance(l, ids, "softmax")
+    check_grad(l, ids, "softmax", counts=counts, d_loss=torch.ones(1, device="cuda"))
+
+
+def test_many_sequences():
+    """As many sequences as rows, more, and more than there are shares of the sums."""
+    for T, S in ((600, 600), (2000, 3000), (900, 400)):
+        l, ids, g = draw(T, 32, 4, S)
+        cut = torch.randint(0, T + 1, (S - 1,), generator=g, device="cuda").sort().values.int()
+        off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), T)])
+        _, counts = check_balance(l, ids, "sigmoid", off)
+        check_grad(l, ids, "sigmoid", counts=counts, d_loss=torch.randn(S, generator=g, device="cuda"), seq_offsets=off)
+
+
 def test_no_rows():
     l = torch.zeros(0, 8, device="cuda")
     ids = torch.zeros(0, 2, dtype=torch.int32, device="cuda")

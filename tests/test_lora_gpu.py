@@ -97,7 +97,8 @@ SIZES = [(1, 64, 64, 8, 1), (1, 2048, 2816, 16, 8), (5, 16, 24, 1, 3), (17, 40, 
          (64, 33, 17, 7, 2), (200, 256, 512, 32, 7), (329, 512, 704, 16, 64), (1024, 72, 64, 4, 2),
          (1025, 128, 64, 8, 3), (1500, 200, 136, 40, 6), (2100, 64, 1000, 64, 1), (1300, 96, 72, 100, 4),
          (1100, 48, 40, 128, 2), (3000, 136, 60, 9, 300), (90, 1, 1, 1, 1000), (4000, 61, 1030, 24, 2),
-         (50, 3000, 24, 33, 3), (1200, 24, 4100, 17, 5)]
+         (50, 3000, 24, 33, 3), (1200, 24, 4100, 17, 5),
+         (1030, 520, 264, 64, 3), (2600, 72, 72, 33, 9), (5000, 128, 200, 48, 40)]
 
 
 @pytest.mark.parametrize("T,K,M,rank,L", SIZES)
@@ -217,6 +218,7 @@ def test_repeats_streams_and_graphs(T):
                 got.append(both(batch))
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for o in got for p, q in zip(o, first))
+    assert A.afd_lora_poll_status(torch.cuda.current_stream().cuda_stream) == A.AFD_OK
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         inner = R.LoraBatch(d["ids"], 5)
@@ -227,6 +229,28 @@ def test_repeats_streams_and_graphs(T):
     graph.replay()
     again = both(R.LoraBatch(d["ids"], 5))
     assert all(torch.equal(p, q) for p, q in zip(held, again)) and not torch.equal(again[0], first[0])
+
+
+@pytest.mark.parametrize("T,rank", [(40, 16), (1200, 8), (1200, 48)])
+def test_offsets_over_32_bits(T, rank):
+    """Rows whose elements lie past 2^31 elements and 2^32 bytes from the first."""
+    K, M = 64, 96
+    d = make(T, K, M, rank, 3, BF, BF, "mixed", 9)
+    pitch = (5 * 2 ** 29) // T // 8 * 8
+    big = torch.empty(T * pitch, dtype=BF, device="cuda").view(T, pitch)
+    for n, first in (("x", 0), ("base", 64), ("dy", 160), ("d_base", 256)):
+        v = big[:, first:first + d[n].shape[1]]
+        v.copy_(d[n])
+        d[n] = v
+    batch, _, u = check_apply(d, out=big[:, 320:320 + M])
+    check_backward(d, batch, u, dx=big[:, 416:416 + K])
+
+
+def test_many_rows_and_adapters():
+    """200000 rows of all 1024 adapters: every tile, piece and block of the plan."""
+    d = make(200000, 16, 24, 4, 1024, BF, BF, "mixed", 13)
+    batch, y, u = check_apply(d)
+    check_backward(d, batch, u)
 
 
 def test_gradients_against_differences():

@@ -79,7 +79,7 @@ APPLY = dict(plan=P, n_tokens=4, n_adapters=2, x=P, ldx=64, x_dtype=A.AFD_DTYPE_
     dict(K=65537, ldx=65537), dict(M=0), dict(M=65537, ldb=65537, ldo=65537), dict(rank=0), dict(rank=129),
     dict(x_dtype=2), dict(y_dtype=-1), dict(ldx=63), dict(ldb=31), dict(ldo=31), dict(plan=0), dict(plan=P + 16),
     dict(x=0), dict(a=0), dict(b=0), dict(out=0), dict(x=P + 1), dict(a=P + 1), dict(b=P + 1), dict(out=P + 2),
-    dict(base=P + 2), dict(scale=P + 2), dict(u=P + 2), dict(base=P, out=P, ldb=40)])
+    dict(base=P + 2), dict(scale=P + 2), dict(u=P + 2), dict(base=P, out=P, ldb=40), dict(out=P)])
 def test_apply_refuses(bad):
     assert A.afd_lora_apply(**{**APPLY, **bad}) == A.AFD_ERR_ARG
 
@@ -94,13 +94,13 @@ GRAD = dict(plan=P, n_tokens=4, n_adapters=2, x=P, ldx=64, x_dtype=A.AFD_DTYPE_B
     dict(y_dtype=2), dict(ldx=63), dict(ldy=31), dict(ldd=63), dict(ldb=63), dict(plan=0), dict(x=0), dict(dy=0),
     dict(u=0), dict(a=0), dict(b=0), dict(dx=0), dict(da=0), dict(db=0), dict(workspace=0), dict(workspace=P + 64),
     dict(x=P + 1), dict(dy=P + 2), dict(u=P + 2), dict(da=P + 8), dict(db=P + 4), dict(dx=P + 1), dict(d_base=P + 1),
-    dict(scale=P + 2), dict(d_base=P, dx=P, ldb=72)])
+    dict(scale=P + 2), dict(d_base=P, dx=P, ldb=72), dict(dx=P)])
 def test_backward_refuses(bad):
     assert A.afd_lora_backward(**{**GRAD, **bad}) == A.AFD_ERR_ARG
 
 
 def test_backward_workspace():
-    n = A.afd_lora_backward_workspace(2000, 8, 64, 32, 8)
+    n = A.afd_lora_backward_workspace(2000, 2, 64, 32, 8)
     assert n > 0 and n % 256 == 0
     for bad in ((-1, 8, 64, 32, 8), (4, 0, 64, 32, 8), (4, 8, 0, 32, 8), (4, 8, 64, 65537, 8), (4, 8, 64, 32, 129)):
         assert A.afd_lora_backward_workspace(*bad) == -1
