@@ -137,7 +137,7 @@ SIGNATURES = [
     ("afd_lora_plan_bytes", _I64, [_I64, _I]),
     ("afd_lora_plan", _I, [_P, _I64, _I, _P, _I64, _P]),
     ("afd_lora_apply", _I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _P, _I, _I, _P, _P, _I64, _I, _P, _I64, _P, _P]),
-    ("afd_lora_backward_workspace", _I64, [_I64, _I, _I, _I, _I]),
+    ("afd_lora_backward_workspace", _I64, [_I64, _I, _I, _I, _I, _I, _I]),
     ("afd_lora_backward", _I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _I64, _I, _I, _P, _P, _P, _I, _P, _P, _I64, _P,
                                _I64, _P, _P, _P, _I64, _P]),
     ("afd_lora_poll_status", _I, [_P]),
@@ -523,8 +523,8 @@ def afd_lora_apply(plan, n_tokens, n_adapters, x, ldx, x_dtype, K, a, b, rank, M
                                 u or None, stream or None)
 
 
-def afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank):
-    return int(lib().afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank))
+def afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank, x_dtype, y_dtype):
+    return int(lib().afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank, x_dtype, y_dtype))
 
 
 def afd_lora_backward(plan, n_tokens, n_adapters, x, ldx, x_dtype, K, dy, ldy, y_dtype, M, u, a, b, rank, scale,

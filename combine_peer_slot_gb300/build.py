@@ -23,8 +23,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 SOURCES = ["afd_api.cu", "afd_kernels.cu", "afd_gemm_tc.cu", "afd_gemm_tc2.cu", "afd_noalloc.cu",
            "afd_attn.cu", "afd_select.cu", "afd_mx4.cu", "afd_mx4_gemm.cu", "afd_balance.cu",
-           "afd_lora.cu", "afd_lora_apply.cu", "afd_lora_tiles.cu", "afd_lora_wgrad.cu",
-           "afd_lora_wgrad_tc.cu", "afd_lora_tc.cu"]
+           "afd_lora.cu", "afd_lora_apply.cu", "afd_lora_tiles.cu", "afd_lora_wgrad.cu", "afd_lora_tc.cu"]
 
 
 def _compile(src, verbose, debug=False):

@@ -217,11 +217,19 @@ namespace {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
-extern "C" int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank) {
-  if (!batch_ok(n_tokens, n_adapters) || !dims_ok(K, M, rank)) return -1;
-  const LoraPlan p = lora_plan_at(nullptr, n_tokens, n_adapters);
-  return up256(n_tokens * rank * 4) + 2 * up256(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))) + up256(p.max_slots * rank * K * 4) +
-         up256(p.max_slots * rank * M * 4);
+// The workspace: parts of v and of u, the partial sums of da and db, and the
+// planes of x and dy where the rows themselves cannot be copied to the tensor
+// cores' operands (the pitches are not known when its size is asked for, so
+// bf16 rows count with one plane unless their columns are whole).
+static int64_t lora_workspace(int64_t T, int L, int K, int M, int R, int x_f32, int y_f32) {
+  const LoraPlan p = lora_plan_at(nullptr, T, L);
+  return 2 * up256(lora_parts_bytes(T, L, lora_padded(R))) + up256(p.max_slots * R * K * 4) + up256(p.max_slots * R * M * 4) +
+         up256(T * lora_plane_pitch(K) * 2 * (x_f32 ? 3 : 1)) + up256(T * lora_plane_pitch(M) * 2 * (y_f32 ? 3 : 1));
+}
+
+extern "C" int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank, int x_dtype, int y_dtype) {
+  if (!batch_ok(n_tokens, n_adapters) || !dims_ok(K, M, rank) || !dtype_ok(x_dtype) || !dtype_ok(y_dtype)) return -1;
+  return lora_workspace(n_tokens, n_adapters, K, M, rank, x_dtype == AFD_DTYPE_F32, y_dtype == AFD_DTYPE_F32);
 }
 
 extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const void* x, int64_t ldx,
@@ -232,7 +240,7 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
   if (!batch_ok(n_tokens, n_adapters) || !dims_ok(K, M, rank) || !dtype_ok(x_dtype) || !dtype_ok(y_dtype) || ldx < K ||
       ldy < M || ldd < K || (d_base && ldb < K))
     return AFD_ERR_ARG;
-  const int64_t need = afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank);
+  const int64_t need = afd_lora_backward_workspace(n_tokens, n_adapters, K, M, rank, x_dtype, y_dtype);
   if (!da || !db || off_by(da, 16) || off_by(db, 16)) return AFD_ERR_ARG;
   if (n_tokens &&
       (!plan || off_by(plan, 256) || !x || !dy || !u || !a || !b || !dx || !workspace || off_by(workspace, 256) ||
@@ -254,46 +262,48 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
   }
   const int rc = check_device_ptrs({plan, x, dy, u, a, b, scale, d_base, dx, da, db, workspace});
   if (rc) return rc;
-  // workspace: v, the parts of v and of u, the partial sums of da and db
   char* at = reinterpret_cast<char*>(workspace);
   auto take = [&](int64_t bytes) {
     char* r = at;
     at += up256(bytes);
     return r;
   };
-  float* v = reinterpret_cast<float*>(take(n_tokens * rank * 4));
-  uint16_t* v_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
-  uint16_t* u_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
   LoraArgs g{};
   g.plan = lora_plan_at(const_cast<void*>(plan), n_tokens, n_adapters);
   g.src = dy; g.lds = ldy; g.w1 = b; g.w2 = a; g.scale = scale;
   g.base = d_base; g.ldb = ldb; g.out = dx; g.ldo = ldd;
   g.T = n_tokens; g.K = M; g.M = K; g.R = rank; g.L = n_adapters;
   g.src_f32 = y_dtype == AFD_DTYPE_F32; g.out_f32 = x_dtype == AFD_DTYPE_F32;
+  g.u_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
+  g.other_parts = reinterpret_cast<uint16_t*>(take(lora_parts_bytes(n_tokens, n_adapters, lora_padded(rank))));
+  g.other = u;
   LoraWgradArgs w{};
   w.plan = g.plan;
-  w.p[0] = v; w.p[1] = u; w.q[0] = x; w.q[1] = dy; w.ldq[0] = ldx; w.ldq[1] = ldy;
+  w.parts[0] = g.u_parts; w.parts[1] = g.other_parts;
   w.out[0] = da; w.out[1] = db; w.N[0] = K; w.N[1] = M;
   w.part[0] = reinterpret_cast<float*>(take(g.plan.max_slots * rank * K * 4));
   w.part[1] = reinterpret_cast<float*>(take(g.plan.max_slots * rank * M * 4));
-  w.f32[0] = g.out_f32; w.f32[1] = g.src_f32;
-  w.how[0] = how_rows(x, ldx, K, x_dtype);
-  w.how[1] = how_rows(dy, ldy, M, y_dtype);
-  w.scale = scale; w.T = n_tokens; w.R = rank; w.L = n_adapters;
-  // what each gradient reads beside its rows: fp32 values, or parts
-  if (w.f32[0]) {
-    g.u = v;
-  } else {
-    g.u_parts = v_parts;
-    w.parts[0] = v_parts;
-  }
-  if (!w.f32[1]) {
-    g.other = u;
-    g.other_parts = u_parts;
-    w.parts[1] = u_parts;
-  }
+  w.scale = scale; w.R = rank; w.L = n_adapters;
   const LaunchCtx lc{stream, 0, nullptr};
-  cudaError_t e = launch_products(lc, g);
+  const void* rows[2] = {x, dy};
+  const int64_t ld[2] = {ldx, ldy};
+  const int dtype[2] = {x_dtype, y_dtype};
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 2 && e == cudaSuccess; i++) {
+    const int f32 = dtype[i] == AFD_DTYPE_F32, how = how_rows(rows[i], ld[i], w.N[i], dtype[i]);
+    w.planes[i] = f32 ? 3 : 1;
+    w.q[i] = rows[i];
+    w.ldq[i] = ld[i];
+    if (f32 || how != 2) {
+      uint16_t* to = reinterpret_cast<uint16_t*>(take(n_tokens * lora_plane_pitch(w.N[i]) * 2 * w.planes[i]));
+      e = launch_lora_planes(lc, g.plan, n_tokens, rows[i], ld[i], w.N[i], f32, how == 2 && w.N[i] % 8 == 0, to);
+      w.q[i] = to;
+      w.ldq[i] = lora_plane_pitch(w.N[i]);
+      w.plane[i] = n_tokens * w.ldq[i];
+      w.ordered[i] = 1;
+    }
+  }
+  if (e == cudaSuccess) e = launch_products(lc, g);
   if (e == cudaSuccess) e = launch_lora_wgrad(lc, w);
   if (e != cudaSuccess) {
     cudaGetLastError();

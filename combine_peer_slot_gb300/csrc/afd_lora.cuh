@@ -84,19 +84,19 @@ struct LoraArgs {
 // da[l] = scale[l] sum v_t x_t^T, db[l] = scale[l] sum u_t dy_t^T
 struct LoraWgradArgs {
   LoraPlan plan;
-  const float* p[2];   // v, u: [T][R], beside fp32 rows
-  const uint16_t* parts[2];  // and as LoraArgs::u_parts, beside bf16 ones
-  const void* q[2];    // x, dy
-  int64_t ldq[2];
-  float* out[2];       // [L][R][N]
-  float* part[2];      // [slots][R][N]
+  const uint16_t* parts[2];  // of v, of u (LoraArgs::u_parts)
+  // rows x, dy: bf16, of whole 16 bytes; gathered by the plan's order or laid
+  // out in it, one plane or three, `plane` elements apart
+  const void* q[2];
+  int64_t ldq[2], plane[2];
+  int planes[2], ordered[2];
+  float* out[2];             // [L][R][N]
+  float* part[2];            // [slots][R][N]
   int N[2];
-  int f32[2];
-  int how[2];          // as LoraArgs::how_src
   const float* scale;
-  int64_t T;
   int R, L;
 };
+inline int64_t lora_plane_pitch(int N) { return ((int64_t)N + 7) / 8 * 8; }
 // Parts of u for the weight gradients: blocks of 32 rows (each adapter's first
 // row begins one, the last is filled up with zeros), each the shared memory
 // image of an MN-major operand with the 128-byte swizzle: atoms of 64 of a row's
@@ -113,9 +113,10 @@ cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a);  // tiles
 bool lora_tc_takes(const LoraArgs& a);                                  // the next one's sizes and alignment
 cudaError_t launch_lora_tc(const LaunchCtx& lc, const LoraArgs& a);     // tiles of 128
 cudaError_t lora_tc_error_count(uint32_t* n, cudaStream_t stream);
+cudaError_t launch_lora_planes(const LaunchCtx& lc, const LoraPlan& plan, int64_t tokens, const void* q, int64_t ldq, int N,
+                               int f32, int vec, uint16_t* to);
 cudaError_t launch_lora_wgrad(LaunchCtx lc, const LoraWgradArgs& a);
-cudaError_t launch_lora_wgrad_tc(const LaunchCtx& lc, const LoraWgradArgs& a);  // the matrices of bf16 rows
-cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);          // waits that gave up, once the stream is there
+cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream);  // waits that gave up, once the stream is there
 
 #ifdef __CUDACC__
 // D += A B on 16 x 8 x 16 bf16 values, fp32 sums: lane (g, c) = (lane / 4,
@@ -293,6 +294,50 @@ __device__ __forceinline__ void load_chunk(uint32_t dst, const T* row, int c0, i
   }
 }
 
+
+// Up to 128 rows without an adapter: out = base (nothing where they are the
+// same), u = 0; by threads first, first + step, ..  Eight loads stand before
+// their stores (one at a time, decode's few such rows took as long as all its
+// products).
+template <typename TO>
+__device__ __forceinline__ void copy_bare(const LoraArgs& a, const int32_t* order, int rows, int first, int step) {
+  constexpr int E = 16 / (int)sizeof(TO), kBatch = 8;
+  const TO* base = reinterpret_cast<const TO*>(a.base);
+  TO* out = reinterpret_cast<TO*>(a.out);
+  if (a.base != a.out) {
+    const bool vec = a.how_out == 2 && (!base || a.how_base == 2);
+    const uint32_t per_row = vec ? a.M / E : a.M, all = rows * per_row;
+    for (uint32_t i0 = first; i0 < all; i0 += kBatch * step) {
+      uint4 v[kBatch];
+      int64_t at[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        const uint32_t i = i0 + k * step;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        at[k] = -1;
+        if (i < all) {
+          const int64_t row = order[i / per_row];
+          const uint32_t c = i % per_row * (vec ? E : 1);
+          at[k] = row * a.ldo + c;
+          if (base) {
+            if (vec) v[k] = *reinterpret_cast<const uint4*>(base + row * a.ldb + c);
+            else if (sizeof(TO) == 2) v[k].x = reinterpret_cast<const uint16_t*>(base)[row * a.ldb + c];
+            else v[k].x = reinterpret_cast<const uint32_t*>(base)[row * a.ldb + c];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; k++)
+        if (at[k] >= 0) {
+          if (vec) *reinterpret_cast<uint4*>(out + at[k]) = v[k];
+          else if (sizeof(TO) == 2) reinterpret_cast<uint16_t*>(out)[at[k]] = (uint16_t)v[k].x;
+          else reinterpret_cast<uint32_t*>(out)[at[k]] = v[k].x;
+        }
+    }
+  }
+  if (a.u)
+    for (uint32_t i = first; i < (uint32_t)(rows * a.R); i += step) a.u[(int64_t)order[i / a.R] * a.R + i % a.R] = 0.0f;
+}
 
 // ---- tcgen05, one CTA: issued by the elected lane of a warp that runs its loop
 // as a whole.  Under a branch on the lane the operands would leave the uniform

@@ -89,18 +89,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   const int4 t = a.plan.tiles[tile];  // (read beside head; past its tiles there is room for more)
   if (tile >= head.x + head.y) return;
   const int32_t* order = a.plan.order + t.y;
-  if (t.x < 0) {  // rows without an adapter: out = base
-    for (int i = warp; i < t.z; i += kWarps) {
-      const int64_t row = order[i];
-      if (a.base != a.out) {
-        const float zero[8] = {};
-        const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
-        for (int c0 = (q * 32 + lane) * 8; c0 < a.M; c0 += C * 256)
-          add_eight<TO>(b, reinterpret_cast<TO*>(a.out) + row * a.ldo, c0, a.M, vm, zero);
-      }
-      if (a.u && q == 0)
-        for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
-    }
+  if (t.x < 0) {
+    copy_bare<TO>(a, order, t.z, q * kWarps * 32 + threadIdx.x, C * kWarps * 32);
     return;
   }
   const int rt = (a.R + 15) / 16, padded = lora_padded(a.R);  // rank tiles

@@ -411,21 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
   if (tid == 0 && abort_flag) atomicAdd(&g_errors, 1u);
   tc_fence_after();
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
-  // rows without an adapter: out = base
-  constexpr int E = 16 / (int)sizeof(TO);
-  const int64_t bare0 = head.w;
-  for (int i = blockIdx.x * (kThreads / 32) + warp; bare0 + i < a.T; i += gridDim.x * (kThreads / 32)) {
-    const int64_t row = a.plan.order[bare0 + i];
-    if (a.base != a.out) {
-      const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
-      TO* o = reinterpret_cast<TO*>(a.out) + row * a.ldo;
-#pragma unroll 4
-      for (int c0 = lane * E; c0 < a.M; c0 += 32 * E)
-        *reinterpret_cast<uint4*>(o + c0) = b ? *reinterpret_cast<const uint4*>(b + c0) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (a.u)
-      for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
-  }
+  for (int64_t i = head.w + (int64_t)blockIdx.x * 32; i < a.T; i += (int64_t)gridDim.x * 32)
+    copy_bare<TO>(a, a.plan.order + i, (int)min((int64_t)32, a.T - i), tid, kThreads);
 }
 
 }  // namespace

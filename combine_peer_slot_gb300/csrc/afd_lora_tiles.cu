@@ -99,22 +99,8 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   t.z = min(t.z, TT);
   if (tid < TT) rows[tid] = tid < t.z ? a.plan.order[t.y + tid] : -1;
   __syncthreads();
-  if (t.x < 0) {  // rows without an adapter: out = base
-    for (int i = warp; i < t.z; i += kThreads / 32) {
-      const int64_t row = rows[i];
-      if (a.base != a.out) {
-        const TO* b = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
-        TO* o = reinterpret_cast<TO*>(a.out) + row * a.ldo;
-        if (a.how_out == 2 && (!b || a.how_base == 2)) {
-          for (int c0 = (q * 32 + lane) * (CB / 8); c0 < a.M; c0 += C * 32 * (CB / 8))
-            *reinterpret_cast<uint4*>(o + c0) = b ? *reinterpret_cast<const uint4*>(b + c0) : make_uint4(0u, 0u, 0u, 0u);
-        } else {
-          for (int c0 = q * 32 + lane; c0 < a.M; c0 += C * 32) o[c0] = b ? b[c0] : (TO)0;
-        }
-      }
-      if (a.u && q == 0)
-        for (int r = lane; r < a.R; r += 32) a.u[row * a.R + r] = 0.0f;
-    }
+  if (t.x < 0) {
+    copy_bare<TO>(a, rows, t.z, q * kThreads + tid, C * kThreads);
     return;
   }
   const uint32_t ring = smem_u32(smem);
@@ -384,9 +370,13 @@ cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
   static std::atomic<int> done[kMaxCachedDevices];
   cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO>, F::kBytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = 2 * a.plan.max_tiles;
-  unsigned C = 8;
-  while (C > 1 && tiles * C > 152 * F::kCtas) C /= 2;
+  // As many CTAs a tile as fill the SMs; halves of tiles that hold rows, at most
+  // (some of those of many adapters' last tiles do not: a third more is room).
+  // Ranks over 32 have four times the sums to exchange: four CTAs at most (4399
+  // rows of 1160 fp32 columns, rank 64: 68 us with four, 94 with eight).
+  const int64_t tiles = 2 * a.plan.max_tiles, held = a.T / TT + std::min<int64_t>(a.T, a.L) + 1;
+  unsigned C = KC >= 4 ? 4 : 8;
+  while (C > 1 && held * C > kLoraSms * F::kCtas * 4 / 3) C /= 2;
   return launch_k_cluster(lc, k_lora_tiles<KC, TS, TO>, (unsigned)(tiles * C), kThreads, (size_t)F::kBytes, C, a);
 }
 template <typename TS, typename TO>

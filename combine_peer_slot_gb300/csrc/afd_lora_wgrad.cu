@@ -1,196 +1,294 @@
-// afd_lora_wgrad.cu -- the adapters' weight gradients from fp32 rows
-// (afd_lora_wgrad_tc.cu: from bf16 ones), and the sum over an adapter's pieces:
+// afd_lora_wgrad.cu -- the adapters' weight gradients, on tcgen05:
 //   da[l] = scale[l] sum_t v_t x_t^T,  db[l] = scale[l] sum_t u_t dy_t^T
-// over the rows t of adapter l: [rank x columns] sums of outer products.
 //
-// A CTA takes one piece of an adapter's rows and a slab of columns of x or dy.
-// Rows stream through a ring of shared memory stages of 16, gathered by
-// asynchronous copies; they and u or v are split into three bf16 parts each,
-// so that the products on the tensor cores keep 24 bits.  A warp holds 16
-// ranks x 16 columns: splitting takes it longer than multiplying, and gates'
-// logits have few columns (60 of them, 2000 rows: 25 us with 64 a warp, 9 with 16).  The tensor cores' fp32 sums cut where they
-// should round, so every other stage they move to registers that add with
-// rounding.  Adapters of several pieces leave partial sums, added in order by
-// a second kernel, which also clears the gradients of adapters without rows.
+// The product's k runs over the rows, so both operands are used as they lie in
+// memory, rows of neighbouring elements (MN-major), 64 of them to a 128-byte
+// swizzled row: asynchronous copies gather x or dy by the plan's order
+// straight into the layout the tensor cores read.  u or v comes as three bf16
+// parts, which keep its 24 bits, written by the kernel of the products as the
+// stages hold them: one bulk copy brings a stage's.  Rows of fp32, or not of
+// whole 16 bytes, are first laid out in the plan's order as one or three bf16
+// planes (k_lora_planes): 24 bits again, a stage for each plane (split by the
+// threads that multiply, the gradients of 12000 fp32 rows of 3649 columns, rank
+// 64, took 200 us more).  The parts of up to 32 ranks stand side by side in the 128 rows of one MMA and are added at the
+// end, those of more take two or three MMAs.
+//
+// Sums in TMEM may cut where they should round, so they move to registers
+// every four stages (128 rows) and start anew in the other accumulator, while
+// the next MMAs run.
+//
+// Bound by memory: one CTA an SM runs through items (a piece of an adapter's
+// rows, 256 columns of x or dy) with its warps apart: three copy, one issues the
+// MMAs, sixteen sum and store, and the copies run on into the next item while
+// the last is stored.  With all warps together, two CTAs of 128 columns an SM,
+// a stage of 32 rows took 1150 to 1800 cycles of barrier, issue, wait and
+// copying one after the other, and an item 9000 before and behind its stages
+// (rank 64, 13312 rows: 62 us where this takes 47).
+//
+// All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"
 
 namespace {
 
-constexpr int kRows = 16;  // of a stage
-constexpr int kCols = 16, kTiles = kCols / 8;  // of a warp
+__device__ uint32_t g_lora_errors;  // waits that gave up
 
-// rank groups of 16 x column groups of 16: one warp each
-template <int RG>
-struct Wg {
-  static constexpr int kCg = RG == 1 ? 8 : RG <= 4 ? 4 : 2;
-  static constexpr int kThreads = RG * kCg * 32;
-  static constexpr int kSlab = kCg * kCols;
-  static constexpr int kStageBytes = kRows * kSlab * 4;
-  static constexpr int kStages = 6;
-  static constexpr int kPStride = RG * 16 + 8;                 // bf16 of a row's parts
-  static constexpr int kPartBytes = 3 * kRows * kPStride * 2;  // one stage's
+constexpr int kSumWarps = 16, kCopyWarps = 3;  // (and one more: five warps a scheduler leave 96 registers a thread)
+constexpr int kThreads = (kSumWarps + kCopyWarps + 1) * 32;
+constexpr int kRows = kLoraBlockRows, kSlab = 256;
+constexpr int kAtom = kRows * kLoraRowBytes;     // 64 columns or ranks of a stage
+constexpr int kFlush = 4;                        // stages between two moves of the sums
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kOutStride = 68;                   // floats, of the output's staging
+
+// MP: ranks of a part, padded: the parts stand MP rows apart
+template <int MP>
+struct Tc {
+  static constexpr int kMmas = MP <= 32 ? 1 : MP == 64 ? 2 : 3;  // a 16-row step
+  static constexpr int kAtoms = lora_atoms(MP);                  // of the parts
+  static constexpr int kStageBytes = (kSlab / 64 + kAtoms) * kAtom;
+  // accumulator rows of a rank: this many, MP apart (MP 64: the first and
+  // third part share theirs), which meet in shared memory
+  static constexpr int kSums = MP <= 32 ? 3 : MP == 64 ? 2 : 1;
+  static constexpr int kOutBytes = kSums > 1 ? 4 * 64 * kOutStride * 4 : 0;
+  static constexpr int kStages = (224 * 1024 - kAtom - kOutBytes) / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kBytes = kRing + 2 * kPartBytes;
-  static constexpr int kCtas = kThreads == 256 ? 3 : 1;
+  static constexpr int kBytes = kRing + kAtom + kOutBytes;       // with an atom of zeros: MMA rows of no part
 };
 
-template <int RG>
-__device__ __forceinline__ void store_sums(const LoraWgradArgs& a, int which, const int4& pc, int rg, int m0, int lane,
-                                           const float (&sum)[kTiles][4]) {
-  const int N = a.N[which], g = lane >> 2, c = lane & 3;
-  const float scale = a.scale ? a.scale[pc.x] : 1.0f;
-  float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * a.R * N : a.part[which] + (int64_t)pc.w * a.R * N;
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const int r = rg * 16 + h * 8 + g;
-    if (r >= a.R) continue;
-    float* d = out + (int64_t)r * N;
-#pragma unroll
-    for (int j = 0; j < kTiles; j++) {
-      const int col = m0 + j * 8 + 2 * c;
-      const float v0 = scale * sum[j][2 * h], v1 = scale * sum[j][2 * h + 1];
-      if (N % 2 == 0) {
-        if (col < N) *reinterpret_cast<float2*>(d + col) = make_float2(v0, v1);
-      } else {
-        if (col < N) d[col] = v0;
-        if (col + 1 < N) d[col + 1] = v1;
+// bf16 x bf16 -> fp32, both operands MN-major, M 128, N 256
+constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(kSlab >> 3) << 17 | (128u >> 4) << 24;
+
+// false: the wait, or another one of the CTA, has given up
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t start = globaltimer_ns();
+  uint32_t spins = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - start > kTimeoutNs) {
+        *abort_flag = 1;
+        return false;
       }
     }
   }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag));
 }
 
-template <int RG>
-__device__ __forceinline__ void wgrad(const LoraWgradArgs& a, int which, int slab, const int4& pc, uint8_t* smem,
-                                      const int32_t* rows) {
-  typedef Wg<RG> W;
-  constexpr int kQ = LoraSrc<float>::kParts, S = W::kStages;
-  constexpr int kCB = kLoraRowBytes / 4;     // columns of a 128-byte row
-  constexpr int kChunks = W::kSlab / 4;      // of a row
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int rg = warp % RG, cg = warp / RG;
-  const int N = a.N[which], m0 = slab * W::kSlab + cg * kCols;
-  const uint32_t ring = smem_u32(smem), parts = ring + W::kRing;
-  const float* Q = reinterpret_cast<const float*>(a.q[which]);
-  const float* P = a.p[which];
-  const int how = a.how[which];
-  const int n = (pc.z + kRows - 1) / kRows;
+// of the 128 threads at a barrier: whether all say yes
+__device__ __forceinline__ bool all_of(int id, bool yes) {
+  uint32_t r;
+  asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %2, 0; bar.red.and.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
+               : "=r"(r) : "r"(id), "r"((uint32_t)yes) : "memory");
+  return r != 0;
+}
 
-  auto fill = [&](int i) {
-    if (i < n) {
-      const uint32_t st = ring + (i % S) * W::kStageBytes;
+// scaled values of a row from column c on
+__device__ __forceinline__ void store_four(float* row, int c, int N, float scale, const float* v) {
+  if (N % 4 == 0) {
+    if (c < N) *reinterpret_cast<float4*>(row + c) = make_float4(scale * v[0], scale * v[1], scale * v[2], scale * v[3]);
+  } else {
 #pragma unroll
-      for (int e = tid; e < kRows * kChunks; e += W::kThreads) {
-        const int r = e / kChunks, ch = e % kChunks, row = rows[min(i * kRows + r, kLoraMaxPiece - 1)];
-        const bool in = i * kRows + r < pc.z;
-        load_chunk<float>(chunk_at(st + (ch >> 3) * (kRows * kLoraRowBytes), r, ch & 7),
-                       in ? Q + (int64_t)row * a.ldq[which] : nullptr,
-                       slab * W::kSlab + ch * 4, N, how, a.plan.head);
+    for (int j = 0; j < 4; j++)
+      if (c + j < N) row[c + j] = scale * v[j];
+  }
+}
+template <int COLS>
+__device__ __forceinline__ void store_row(float* row, int c, int N, float scale, const float (&v)[COLS]) {
+#pragma unroll
+  for (int j = 0; j < COLS; j += 4) store_four(row, c + j, N, scale, v + j);
+}
+
+// a piece's stages: every 32 rows, once for each plane
+__device__ __forceinline__ int stages_of(const int4& pc, int planes) { return (pc.z + kRows - 1) / kRows * planes; }
+
+template <int MP>
+__global__ void __launch_bounds__(kThreads, 1) k_lora_wgrad(const __grid_constant__ LoraWgradArgs a) {
+  typedef Tc<MP> W;
+  constexpr int S = W::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // of each stage: full, free again; sums of a group of stages: complete, taken
+  __shared__ uint64_t full[S], empty[S], dfull[2], dempty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.R;
+  const int nx = (a.N[0] + kSlab - 1) / kSlab, slabs = nx + (a.N[1] + kSlab - 1) / kSlab;
+  const uint32_t ring = smem_u32(smem), zero = ring + W::kRing;
+  if (tid < kAtom / 16) *reinterpret_cast<uint4*>(smem + W::kRing + 16 * tid) = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < S) {
+    mbar_init(smem_u32(&full[tid]), 33);  // a copying warp's lanes, and its bulk copy
+    mbar_init(smem_u32(&empty[tid]), 1);
+    if (tid < 2) {
+      mbar_init(smem_u32(&dfull[tid]), 1);
+      mbar_init(smem_u32(&dempty[tid]), kSumWarps);
+    }
+    if (tid == 0) abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "r"(2 * kSlab));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_wait();  // the products' kernel
+  const uint32_t tmem = tmem_base;
+  const int items = a.plan.head->z * slabs;
+  volatile int* const gave_up = &abort_flag;
+  bool good = true;
+  int slot = 0, stage = 0;  // of the ring, over all items
+  uint32_t turn = 0;
+  auto next = [&]() {
+    stage++;
+    if (++slot == S) {
+      slot = 0;
+      turn++;
+    }
+  };
+
+  if (warp >= kSumWarps && warp < kSumWarps + kCopyWarps) {  // ---- copies: every kCopyWarps-th stage ----
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int4 pc = a.plan.pieces[item / slabs];
+      const int slab = item % slabs, which = slab >= nx, m0 = (slab - (which ? nx : 0)) * kSlab;
+      const int N = a.N[which], col = m0 + lane * 8, planes = a.planes[which], n = stages_of(pc, planes);
+      const uint16_t* P = a.parts[which] + (int64_t)(pc.y + a.plan.shift[pc.x]) / kRows * (W::kAtoms * kAtom / 2);
+      const bool in = col < N;
+      const int64_t pitch = in ? a.ldq[which] * 2 : 0;
+      int plane = 0, block = 0;
+      for (int i = 0; i < n; i++, next(), plane = plane + 1 < planes ? plane + 1 : (block++, 0)) {
+        if (stage % kCopyWarps != warp - kSumWarps) continue;
+        if (turn) {
+          good = warp_wait(smem_u32(&empty[slot]), (turn - 1) & 1, gave_up);
+          if (!good) break;
+        }
+        const uint32_t st = ring + slot * W::kStageBytes, bar = smem_u32(&full[slot]);
+        const int t0 = block * kRows, have = min(kRows, pc.z - t0);  // rows of the piece; the others zero
+        const int my_row = lane >= have ? 0 : a.ordered[which] ? pc.y + t0 + lane : a.plan.order[pc.y + t0 + lane];
+        if (lane == 0) {
+          mbar_expect_tx(bar, W::kAtoms * kAtom);
+          bulk_load(st + kSlab / 64 * kAtom, P + (int64_t)block * (W::kAtoms * kAtom / 2), W::kAtoms * kAtom, bar);
+        }
+        const char* p = in ? reinterpret_cast<const char*>(a.q[which]) + (plane * a.plane[which] + col) * 2
+                           : reinterpret_cast<const char*>(a.plan.head);
+        const uint32_t to = st + (lane >> 3) * kAtom, ch = (lane & 7) << 4;
+#pragma unroll
+        for (int j = 0; j < kRows; j++) {
+          const int row = __shfl_sync(0xffffffffu, my_row, j);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * kLoraRowBytes + (ch ^ (j & 7) << 4)),
+                       "l"(p + row * pitch), "r"(in && j < have ? 16 : 0)
+                       : "memory");
+        }
+        // each lane arrives when its copies have landed
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // u or v of a stage: to registers, then as parts to shared memory
-  constexpr int kMine = kRows * RG * 16 / W::kThreads;
-  static_assert(kRows * RG * 16 % W::kThreads == 0, "values of a stage");
-  float pv[kMine];
-  auto take = [&](int i) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kSumWarps + kCopyWarps) {  // ---- products ----
+    const uint32_t el = lora_elect();
+    uint32_t group = 0;
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int n = stages_of(a.plan.pieces[item / slabs], a.planes[item % slabs >= nx]);
+      for (int i = 0; i < n; i++, next()) {
+        good = warp_wait(smem_u32(&full[slot]), turn & 1, gave_up);
+        if (good && i % kFlush == 0 && group >= 2) good = warp_wait(smem_u32(&dempty[group & 1]), (group / 2 - 1) & 1, gave_up);
+        if (!good) break;
+        // the copies' writes, seen through the barrier, before the products'
+        // reads, which go another way
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_after();
+        const uint32_t d = tmem + (group & 1) * kSlab;
+        // atoms of 64 elements, 8-row groups 1024 bytes apart
+        const uint32_t qa = (ring + slot * W::kStageBytes) >> 4, pa = qa + (kSlab / 64 * kAtom >> 4);
 #pragma unroll
-    for (int j = 0; j < kMine; j++) {
-      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = i * kRows + e / (RG * 16);
-      pv[j] = t < pc.z && r < a.R ? P[(int64_t)rows[t] * a.R + r] : 0.0f;
+        for (int ks = 0; ks < kRows / 16; ks++)
+#pragma unroll
+          for (int x = W::kMmas - 1; x >= 0; x--)
+            lora_mma(el, d, lora_desc(pa + (x * 2 * kAtom + ks * 2048 >> 4), 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - (pa + (x * 2 * kAtom >> 4))),
+                     lora_desc(qa + ks * 128, kAtom >> 4), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+        lora_commit(el, smem_u32(&empty[slot]));
+        if (i % kFlush == kFlush - 1 || i == n - 1) lora_commit(el, smem_u32(&dfull[group++ & 1]));
+      }
     }
-  };
-  auto put = [&](int i) {
-#pragma unroll
-    for (int j = 0; j < kMine; j++) {
-      const int e = tid + j * W::kThreads, r = e % (RG * 16), t = e / (RG * 16);
-      uint16_t p[3];
-      split_bf16<3>(pv[j], p);
-#pragma unroll
-      for (int x = 0; x < 3; x++)
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(parts + (i & 1) * W::kPartBytes + ((x * kRows + t) * W::kPStride + r) * 2),
-                     "h"(p[x]) : "memory");
+    if (!good) {  // (a wait has given up: time for bulk copies under way to land)
+      const uint64_t start = globaltimer_ns();
+      while (globaltimer_ns() - start < 1000000ull) {}
     }
-  };
-  float acc[kTiles][4], sum[kTiles][4];
+  } else {  // ---- sums: accumulator row 32 (warp % 4) + lane, columns 64 (warp / 4) .. ----
+    const int m = (warp & 3) * 32 + lane, cg = warp >> 2;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + cg * 64;
+    float* out_stage = reinterpret_cast<float*>(smem + W::kRing + kAtom) + cg * 64 * kOutStride;  // [64][kOutStride]
+    uint32_t group = 0;
+    auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + cg) : "memory"); };  // the four warps of these columns
+    for (int item = blockIdx.x; item < items && good; item += gridDim.x) {
+      const int4 pc = a.plan.pieces[item / slabs];
+      const int slab = item % slabs, which = slab >= nx, m0 = (slab - (which ? nx : 0)) * kSlab + cg * 64;
+      const int N = a.N[which], n = stages_of(pc, a.planes[which]);
+      float sum[64];
 #pragma unroll
-  for (int j = 0; j < kTiles; j++)
+      for (int j = 0; j < 64; j++) sum[j] = 0.0f;
+      for (int i = 0; i < n; i += kFlush, group++) {
+        good = warp_wait(smem_u32(&dfull[group & 1]), group / 2 & 1, gave_up);
+        if (!good) break;
+        tc_fence_after();
 #pragma unroll
-    for (int x = 0; x < 4; x++) acc[j][x] = sum[j][x] = 0.0f;
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t v[16];
+          tmem_ld_16(mine + (group & 1) * kSlab + c, v);
+          tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < S - 1; i++) fill(i);
-  take(0);
-  put(0);
-  for (int i = 0; i < n; i++) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-    __syncthreads();
-    fill(i + S - 1);
-    if (i + 1 < n) take(i + 1);
-    const uint32_t st = ring + (i % S) * W::kStageBytes, ps = parts + (i & 1) * W::kPartBytes;
-    if (m0 < N) {
+          for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty[group & 1]));
+      }
+      if (!all_of(1 + cg, good)) {  // (the four warps leave together: none waits for one that has left)
+        good = false;
+        break;
+      }
+      const float scale = a.scale ? a.scale[pc.x] : 1.0f;
+      float* out = pc.w < 0 ? a.out[which] + (int64_t)pc.x * R * N : a.part[which] + (int64_t)pc.w * R * N;
+      if (W::kSums == 1) {
+        if (m < R) store_row<64>(out + (int64_t)m * N, m0, N, scale, sum);
+        continue;
+      }
+      // the parts' sums meet, and go to memory a row's 64 columns at a time
+      float* mine_out = out_stage + (m < MP ? m : m - MP) * kOutStride;
+      if (m >= MP && m < W::kSums * MP) {
 #pragma unroll
-      for (int ks = 0; ks < kRows / 16; ks++) {
-        uint32_t p[3][4];
+        for (int j = 0; j < 64; j += 4) *reinterpret_cast<float4*>(mine_out + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+      }
+      meet();
+      if (m < MP) {
 #pragma unroll
-        for (int x = 0; x < 3; x++)
-          ldsm4t(ps + ((x * kRows + ks * 16 + (lane & 7) + (lane >> 4) * 8) * W::kPStride + rg * 16 + ((lane >> 3) & 1) * 8) * 2, p[x]);
+        for (int j = 0; j < 64; j += 4) {
 #pragma unroll
-        for (int j = 0; j < kTiles; j++) {
-          const int col = cg * kCols + j * 8 + g;
-          const uint32_t t = st + col / kCB * (kRows * kLoraRowBytes);
-          uint32_t b[kQ][2];
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            float2 v;
-            const int r = ks * 16 + h * 8 + 2 * c, cc = col % kCB;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.x) : "r"(chunk_at(t, r, cc >> 2) + (cc & 3) * 4) : "memory");
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.y) : "r"(chunk_at(t, r + 1, cc >> 2) + (cc & 3) * 4) : "memory");
-            uint32_t w[kQ];
-            split_pair<kQ>(v, w);
-#pragma unroll
-            for (int y = 0; y < kQ; y++) b[y][h] = w[y];
+          for (int x = 0; x < W::kSums - 1; x++) {
+            const float4 v = *reinterpret_cast<const float4*>(mine_out + x * MP * kOutStride + j);
+            sum[j] += v.x; sum[j + 1] += v.y; sum[j + 2] += v.z; sum[j + 3] += v.w;
           }
-#pragma unroll
-          for (int y = kQ - 1; y >= 0; y--)
-#pragma unroll
-            for (int x = 2 - y; x >= 0; x--)  // products under 2^-24 of the largest are left out
-              mma_16x8x16(acc[j], p[x][0], p[x][1], p[x][2], p[x][3], b[y][0], b[y][1]);
+          *reinterpret_cast<float4*>(mine_out + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
         }
       }
-      if (i & 1) {
+      meet();
+      for (int r = (warp & 3) * 8 + (lane >> 2); r < R; r += 32) {
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < kTiles; j++)
+        for (int j = 0; j < 16; j++) v[j] = out_stage[r * kOutStride + (lane & 3) * 4 + j / 4 * 16 + j % 4];
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            sum[j][x] += acc[j][x];
-            acc[j][x] = 0.0f;
-          }
+        for (int j = 0; j < 4; j++) store_four(out + (int64_t)r * N, m0 + (lane & 3) * 4 + j * 16, N, scale, v + 4 * j);
       }
+      meet();
     }
-    if (i + 1 < n) put(i + 1);
   }
-  if (m0 < N) {
-#pragma unroll
-    for (int j = 0; j < kTiles; j++)
-#pragma unroll
-      for (int x = 0; x < 4; x++) sum[j][x] += acc[j][x];
-    store_sums<RG>(a, which, pc, rg, m0, lane, sum);
-  }
-}
-
-template <int RG>
-__global__ void __launch_bounds__(Wg<RG>::kThreads, Wg<RG>::kCtas) k_lora_wgrad(const __grid_constant__ LoraWgradArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int32_t rows[kLoraMaxPiece];
-  grid_dep_wait();
-  const int4 head = *a.plan.head;
-  if ((int)blockIdx.y >= head.z) return;
-  const int4 pc = a.plan.pieces[blockIdx.y];
-  for (int i = threadIdx.x; i < kLoraMaxPiece; i += Wg<RG>::kThreads) rows[i] = i < pc.z ? a.plan.order[pc.y + i] : 0;
   __syncthreads();
-  const int nx = a.f32[0] ? (a.N[0] + Wg<RG>::kSlab - 1) / Wg<RG>::kSlab : 0;
-  const int which = (int)blockIdx.x >= nx;
-  wgrad<RG>(a, which, (int)blockIdx.x - (which ? nx : 0), pc, smem, rows);
+  if (tid == 0 && abort_flag) atomicAdd(&g_lora_errors, 1u);
+  tc_fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kSlab));
 }
 
 // Adapters of several pieces: their partial sums in order.  Those without
@@ -225,34 +323,61 @@ __global__ void __launch_bounds__(256) k_lora_wgrad_sum(const __grid_constant__ 
   }
 }
 
-template <int RG>
-cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
-  typedef Wg<RG> W;
-  static std::atomic<int> done[kMaxCachedDevices];
-  cudaError_t e = smem_attr_once(k_lora_wgrad<RG>, W::kBytes, done);
-  if (e != cudaSuccess) return e;
-  int slabs = 0;
-  for (int w = 0; w < 2; w++)
-    if (a.f32[w]) slabs += (a.N[w] + W::kSlab - 1) / W::kSlab;
-  return launch_k(lc, k_lora_wgrad<RG>, dim3(slabs, (unsigned)a.plan.max_pieces), W::kThreads, W::kBytes, a);
+// Rows in the plan's order as bf16 planes, a warp a row: three of an fp32 row
+// (its parts), one of a bf16 row.
+template <typename T>
+__global__ void __launch_bounds__(256) k_lora_planes(const LoraPlan plan, const T* q, int64_t ldq, int N, int vec, uint16_t* to,
+                                                     int64_t pitch, int64_t plane) {
+  constexpr int kP = LoraSrc<T>::kParts;
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = plan.head->w, step = (int64_t)gridDim.x * 8;
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
+    const T* from = q + (int64_t)plan.order[i] * ldq;
+#pragma unroll 2
+    for (int c = lane * 8; c < N; c += 256) {
+      uint4 v[kP];
+      load_eight<T>(from, c, N, vec, v);
+#pragma unroll
+      for (int x = 0; x < kP; x++) *reinterpret_cast<uint4*>(to + x * plane + i * pitch + c) = v[x];
+    }
+  }
 }
-cudaError_t by_rank(const LaunchCtx& lc, const LoraWgradArgs& a) {
-  return a.R <= 16 ? run<1>(lc, a) : a.R <= 32 ? run<2>(lc, a) : a.R <= 64 ? run<4>(lc, a) : run<8>(lc, a);
+
+template <int MP>
+cudaError_t run(const LaunchCtx& lc, const LoraWgradArgs& a) {
+  typedef Tc<MP> W;
+  static std::atomic<int> done[kMaxCachedDevices];
+  const cudaError_t e = smem_attr_once(k_lora_wgrad<MP>, W::kBytes, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(lc, k_lora_wgrad<MP>, kLoraSms, kThreads, W::kBytes, a);
 }
 
 }  // namespace
+
+cudaError_t launch_lora_planes(const LaunchCtx& lc, const LoraPlan& plan, int64_t tokens, const void* q, int64_t ldq, int N,
+                               int f32, int vec, uint16_t* to) {
+  const int64_t pitch = lora_plane_pitch(N), plane = tokens * pitch;
+  const unsigned grid = (unsigned)std::min<int64_t>((tokens + 7) / 8, 8 * kLoraSms);
+  return f32 ? launch_k(lc, k_lora_planes<float>, grid, 256, 0, plan, reinterpret_cast<const float*>(q), ldq, N, vec, to, pitch, plane)
+             : launch_k(lc, k_lora_planes<uint16_t>, grid, 256, 0, plan, reinterpret_cast<const uint16_t*>(q), ldq, N, vec, to, pitch, plane);
+}
 
 // Each kernel may start while the one before it ends, and waits for its end
 // before all else (a block that left without waiting would let the next one
 // start too early).
 cudaError_t launch_lora_wgrad(LaunchCtx lc, const LoraWgradArgs& a) {
   lc.pdl = 1;
-  cudaError_t e = cudaSuccess;
-  if (!a.f32[0] || !a.f32[1]) e = launch_lora_wgrad_tc(lc, a);
-  if (e == cudaSuccess && (a.f32[0] || a.f32[1])) e = by_rank(lc, a);
+  const cudaError_t e = a.R <= 16   ? run<16>(lc, a)
+                        : a.R <= 32 ? run<32>(lc, a)
+                        : a.R <= 64 ? run<64>(lc, a)
+                                    : run<128>(lc, a);
   if (e != cudaSuccess) return e;
   const int64_t all = (int64_t)a.R * (a.N[0] + a.N[1]);
   const bool four = (int64_t)a.R * a.N[0] % 4 == 0 && (int64_t)a.R * a.N[1] % 4 == 0;
   const dim3 sums((unsigned)std::min<int64_t>((all + (four ? 1023 : 255)) / (four ? 1024 : 256), 1024), a.L);
   return four ? launch_k(lc, k_lora_wgrad_sum<4>, sums, 256, 0, a) : launch_k(lc, k_lora_wgrad_sum<1>, sums, 256, 0, a);
+}
+
+cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream) {
+  return cudaMemcpyFromSymbolAsync(n, g_lora_errors, sizeof *n, 0, cudaMemcpyDeviceToHost, stream);
 }

@@ -744,7 +744,7 @@ def lora_backward(batch, x, dy, u, a, b, d_base=None, scale=None, dx=None, da=No
     pda, pdb = _rows_f32(h, da, (L, rank, K), "da"), _rows_f32(h, db, (L, rank, M), "db")
     pu = _rows_f32(h, u, (T, rank), "u")
     ps = _rows_f32(h, scale, (L,), "scale") if scale is not None else 0
-    ws, ws_bytes, keep = _scratch(h, workspace, h.lora_backward_workspace(T, L, K, M, rank), dev)
+    ws, ws_bytes, keep = _scratch(h, workspace, h.lora_backward_workspace(T, L, K, M, rank, xc, yc), dev)
     rc = h.lora_backward(batch.plan.data_ptr(), T, L, x.data_ptr(), ldx, xc, K, dy.data_ptr(), ldy, yc, M, pu,
                          a.data_ptr(), b.data_ptr(), rank, ps, pb, ldb, dx.data_ptr(), ldd, pda, pdb, ws, ws_bytes,
                          h.raw_stream(dev.index))

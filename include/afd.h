@@ -863,7 +863,8 @@ int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters, const voi
  * device, 256-byte aligned, at least afd_lora_backward_workspace bytes (host
  * only; -1 outside the limits), else AFD_ERR_CAPACITY; one call at a time may
  * use it. */
-int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank);
+int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank,
+                                    int x_dtype, int y_dtype);
 int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const void* x,
                       int64_t ldx, int x_dtype, int K, const void* dy, int64_t ldy, int y_dtype,
                       int M, const float* u, const void* A, const void* B, int rank,

@@ -100,9 +100,10 @@ def test_backward_refuses(bad):
 
 
 def test_backward_workspace():
-    n = A.afd_lora_backward_workspace(2000, 2, 64, 32, 8)
+    n = A.afd_lora_backward_workspace(2000, 2, 64, 32, 8, A.AFD_DTYPE_BF16, A.AFD_DTYPE_F32)
     assert n > 0 and n % 256 == 0
-    for bad in ((-1, 8, 64, 32, 8), (4, 0, 64, 32, 8), (4, 8, 0, 32, 8), (4, 8, 64, 65537, 8), (4, 8, 64, 32, 129)):
+    for bad in ((-1, 8, 64, 32, 8, 0, 0), (4, 0, 64, 32, 8, 0, 0), (4, 8, 0, 32, 8, 0, 0), (4, 8, 64, 65537, 8, 0, 0),
+                (4, 8, 64, 32, 129, 0, 0), (4, 8, 64, 32, 8, 2, 0), (4, 8, 64, 32, 8, 0, -1)):
         assert A.afd_lora_backward_workspace(*bad) == -1
     assert A.afd_lora_backward(**{**GRAD, "n_tokens": 2000, "workspace_bytes": n - 1}) == A.AFD_ERR_CAPACITY
 
