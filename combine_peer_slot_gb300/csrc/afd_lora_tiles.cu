@@ -28,15 +28,22 @@ constexpr int kThreads = 256;
 constexpr int kRowBytes = kLoraRowBytes;      // of a stage's row, of either operand
 constexpr int kTileBytes = TT * kRowBytes;
 constexpr int kFlush = 4;                     // stages between two moves of the sums
+constexpr int kXStride = 80;                  // bytes, of a row's 32 values of one part
 
 // stages, and CTAs an SM holds
-template <int KC>
+template <int KC, int KS, int KU>
 struct Form {
   static constexpr int kStages = KC == 1 ? 6 : KC == 2 ? 5 : KC == 4 ? 3 : 4;
   static constexpr int kCtas = KC <= 4 ? 3 : 1;
   static constexpr int kStageBytes = kTileBytes + KC * 16 * kRowBytes;
   static constexpr int kUStride = KC * 16 + 4;
-  static constexpr int kBytes = kStages * kStageBytes + TT * kUStride * 4;
+  // u's sums; its parts take their place where a warp cannot hold them
+  static constexpr bool kHold = KC * KU <= 8;
+  static constexpr int kPStride = KC * 16 + 8;
+  static constexpr int kUBytes = kHold || TT * kUStride * 4 > KU * TT * kPStride * 2 ? TT * kUStride * 4 : KU * TT * kPStride * 2;
+  // an fp32 stage's rows as bf16 parts
+  static constexpr int kXBytes = KS > 1 ? KS * TT * kXStride : 0;
+  static constexpr int kBytes = kStages * kStageBytes + kUBytes + kXBytes;
 };
 
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
@@ -46,6 +53,16 @@ __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
 }
 __device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+// eight fp32 values, from two chunks, to their parts
+template <int PARTS>
+__device__ __forceinline__ void split_eight_at(uint32_t a, uint32_t b, uint4 (&to)[PARTS]) {
+  uint32_t w[4][PARTS];
+#pragma unroll
+  for (int j = 0; j < 4; j++) split_pair<PARTS>(lds_f2((j < 2 ? a : b) + (j & 1) * 8), w[j]);
+#pragma unroll
+  for (int x = 0; x < PARTS; x++) to[x] = make_uint4(w[0][x], w[1][x], w[2][x], w[3][x]);
 }
 
 // A stage's copies where some rows cannot be moved 16 bytes at a time.
@@ -75,12 +92,13 @@ __device__ __noinline__ void slow_fill(const LoraArgs& a, uint32_t st, bool firs
 }
 
 template <int KC, typename TS, typename TO>
-__global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const __grid_constant__ LoraArgs a) {
-  typedef Form<KC> F;
-  constexpr int kS = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts, S = F::kStages;
+__global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const __grid_constant__ LoraArgs a) {
+  constexpr int kS = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
+  typedef Form<KC, kS, kU> F;
+  constexpr int S = F::kStages;
   constexpr int KB = kRowBytes / (int)sizeof(TS), CB = kRowBytes / (int)sizeof(TO);  // columns of a stage
   constexpr int NT = CB / 16;                                                          // a warp's column tiles
-  constexpr bool kHold = KC * kU <= 8;                                                 // u's operands stay in registers
+  constexpr bool kHold = F::kHold;                                                     // u's operands stay in registers
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int32_t rows[TT];
   cg::cluster_group cluster = cg::this_cluster();
@@ -105,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
   }
   const uint32_t ring = smem_u32(smem);
   float* part = reinterpret_cast<float*>(smem + S * F::kStageBytes);  // [TT][kUStride]
+  const uint32_t us = ring + S * F::kStageBytes, xs = us + F::kUBytes;
   const uint16_t* w1 = reinterpret_cast<const uint16_t*>(a.w1) + (int64_t)t.x * a.R * a.K;
   const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
   const int all1 = (a.K + KB - 1) / KB, all2 = (a.M + CB - 1) / CB;
@@ -175,6 +194,16 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
     ready();
     fill(i + S - 1);
     const uint32_t st = ring + (i % S) * F::kStageBytes, wst = st + kTileBytes;
+    if (kS > 1) {  // the rows' parts, split once for all warps that multiply them
+      const int r = tid >> 2, c8 = (tid & 3) * 8;
+      uint4 v[kS];
+      split_eight_at<kS>(chunk_at(st, r, c8 >> 2), chunk_at(st, r, (c8 >> 2) + 1), v);
+#pragma unroll
+      for (int y = 0; y < kS; y++)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(xs + (y * TT + r) * kXStride + c8 * 2), "r"(v[y].x), "r"(v[y].y),
+                     "r"(v[y].z), "r"(v[y].w) : "memory");
+      __syncthreads();
+    }
 #pragma unroll
     for (int ks = 0; ks < KB / 16; ks++) {
       uint32_t x[kS][4];
@@ -182,13 +211,7 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
         ldsm4(chunk_at(st, wt * 16 + (lane & 15), ks * 2 + (lane >> 4)), x[0]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const int col = ks * 16 + 2 * c + (j >> 1) * 8;
-          uint32_t p[kS];
-          split_pair<kS>(lds_f2(chunk_at(st, wt * 16 + g + (j & 1) * 8, col >> 2) + (col & 3) * 4), p);
-#pragma unroll
-          for (int y = 0; y < kS; y++) x[y][j] = p[y];
-        }
+        for (int y = 0; y < kS; y++) ldsm4(xs + (y * TT + wt * 16 + (lane & 15)) * kXStride + (ks * 2 + (lane >> 4)) * 16, x[y]);
       }
       if (KC == 1) {
         uint32_t b0, b1;
@@ -284,9 +307,28 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
     }
   };
   uint32_t held[kHold ? KC : 1][kU][4];
-  if (kHold)
+  if (kHold) {
 #pragma unroll
     for (int ks = 0; ks < KC; ks++) operand(ks, held[kHold ? ks : 0]);
+  } else {  // as parts [kU][TT][kPStride], in the sums' place
+    constexpr int kMine = TT * KC * 8 / kThreads;
+    float2 v[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int e = tid + i * kThreads;
+      v[i] = *reinterpret_cast<const float2*>(part + e / (KC * 8) * F::kUStride + e % (KC * 8) * 2);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+      const int e = tid + i * kThreads;
+      uint32_t p[kU];
+      split_pair<kU>(v[i], p);
+#pragma unroll
+      for (int y = 0; y < kU; y++)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(us + ((y * TT + e / (KC * 8)) * F::kPStride + e % (KC * 8) * 2) * 2), "r"(p[y]) : "memory");
+    }
+  }
   const int steps = (a.R + 15) / 16;
   // this lane's 16 bytes of rows g and g + 8 of the warp's
   TO* o[2];
@@ -307,7 +349,10 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
 #pragma unroll
     for (int ks = 0; ks < KC; ks++) {
       if (ks >= steps) break;
-      if (!kHold) operand(ks, held[0]);
+      if (!kHold) {
+#pragma unroll
+        for (int y = 0; y < kU; y++) ldsm4(us + ((y * TT + wt * 16 + (lane & 15)) * F::kPStride + ks * 16 + (lane >> 4) * 8) * 2, held[0][y]);
+      }
       uint32_t(&u)[kU][4] = held[kHold ? ks : 0];
 #pragma unroll
       for (int j = 0; j < NT / 2; j++) {
@@ -366,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, Form<KC>::kCtas) k_lora_tiles(const 
 
 template <int KC, typename TS, typename TO>
 cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
-  typedef Form<KC> F;
+  typedef Form<KC, LoraSrc<TS>::kParts, OutParts<TO>::kParts> F;
   static std::atomic<int> done[kMaxCachedDevices];
   cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO>, F::kBytes, done);
   if (e != cudaSuccess) return e;
