@@ -1,6 +1,7 @@
 // afd_lora.cu -- low-rank adapters of many requests beside a shared
-// projection: the plan of a batch, the adapters' weight gradients and the C
-// entry points.  The products themselves are in afd_lora_apply.cu.
+// projection: the plan of a batch and the C entry points.  The products are in
+// afd_lora_apply.cu (few rows), afd_lora_tiles.cu and afd_lora_tc.cu (many), the
+// weight gradients in afd_lora_wgrad.cu.
 #include "afd_lora.cuh"
 
 #include <map>
@@ -11,8 +12,9 @@ constexpr int kPlanWarps = 32;
 
 // One CTA: a stable counting sort of the rows by adapter.  Each warp counts a
 // run of the rows (lanes of one adapter find each other, so no two add to one
-// counter at a time and no order depends on timing), the counts are summed over warps and adapters, and
-// each warp places its run.
+// counter at a time and no order depends on timing), the counts are summed over
+// warps and adapters, and each warp places its run.  Made once for a batch:
+// 329 rows 10 us, 13312 rows of 8 adapters 12 to 19, of 1024 up to 44.
 __global__ void __launch_bounds__(kPlanWarps * 32, 1) k_lora_plan(const int32_t* ids, int n, int L, LoraPlan p, int tile, int piece) {
   extern __shared__ int32_t cnt[];  // [warps][L + 1]
   __shared__ int32_t total[kLoraMaxAdapters + 1], rows0[kLoraMaxAdapters + 2], tile0[kLoraMaxAdapters + 2],

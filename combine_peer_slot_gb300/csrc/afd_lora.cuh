@@ -9,12 +9,15 @@ constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxCols = 65536;
 constexpr int64_t kLoraMaxTokens = int64_t(1) << 24;
 
-// Rows of one adapter that a tile of the products holds, and rows of one
-// piece of the weight gradients' sums.
-constexpr int kLoraSms = 152;
+constexpr int kLoraSms = 152;  // CTAs of the kernels that hold one an SM
+// Rows of one adapter that a tile of the products holds.  A decode step's rows
+// bring many adapters of a few rows each; over a thousand rows the adapters'
+// runs are longer.
 inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 128; }
-constexpr int kLoraMaxPiece = 512;
-__host__ __device__ inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : kLoraMaxPiece; }
+// Rows of one piece of the weight gradients' sums: enough pieces for all SMs,
+// and few enough that their partial sums stay small (13312 rows of 8 adapters,
+// rank 64: 512 and 1024 rows 112 us, 2048 121).
+inline int lora_piece(int64_t tokens) { return tokens <= 4096 ? 128 : 512; }
 
 // The plan, made on the device from the rows' adapter ids: the rows in adapter
 // order (stable; rows without an adapter last), cut into tiles of one adapter.

@@ -1,16 +1,21 @@
-// afd_lora_apply.cu -- both products of the adapters in one kernel:
+// afd_lora_apply.cu -- both products of the adapters in one kernel, for batches
+// of few rows (afd_lora_tiles.cu has the form for many):
 //   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
 // forward with (x, A, B), backward with (dy, B, A).
 //
-// for batches of few rows (afd_lora_tiles.cu has the form for many).  A cluster
-// takes a tile of up to 16 rows of one adapter, gathered by the plan's order.  First its warps share the columns of src in chunks of 32,
-// each lane loading its operands of the tensor cores' products straight from
+// A cluster takes a tile of up to 16 rows of one adapter, gathered by the plan's
+// order.  First its warps share the columns of src in chunks of 32, each lane
+// loading its operands of the tensor cores' products straight from
 // global memory: the k order inside a chunk is free as long as both operands
 // agree, so a lane takes 16 neighbouring bytes for its four k pairs.  The
 // sums over the warps go through shared memory, those over the CTAs through
 // distributed shared memory, always in the same order.  Then the warps share
 // the columns of out in blocks of 64.  u enters the second product as two
 // (out in bf16) or three (fp32) bf16 parts, so that it keeps 16 or 24 bits.
+//
+// Measured (2048 to 2816 columns, rank 16): one row 4.6 us, 329 rows of 64
+// adapters 8.5 us, where their bytes would take 2.2: a chain of reads that
+// depend on each other (plan, order, rows and A, the CTAs' sums, B and base).
 #include <cooperative_groups.h>
 
 #include "afd_lora.cuh"

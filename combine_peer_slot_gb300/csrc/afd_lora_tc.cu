@@ -7,13 +7,24 @@
 // warps do not wait for each other: four gather rows by the plan's order
 // (asynchronous copies, a stage each in turn), one issues the MMAs, eight turn
 // u into the second product's operand and add to base.  An item is a tile of
-// up to 128 rows of one adapter and a share of the output columns; a stage is 128 bytes of each row, of src and then of base,
-// with the weight's 64 columns, and the ring runs on from product to product
-// and from item to item.  Each share of a tile computes u anew, from L2 but for
+// up to 128 rows of one adapter and a share of the output columns; a stage is
+// 128 bytes of each row, of src and then of base, with the weight's 64 columns,
+// and the ring runs on from product to product and from item to item.  Each share of a tile computes u anew, from L2 but for
 // the first one's reads, which costs less than meeting.
 //
-// u goes into the second product as two bf16 parts, 16 of its bits.  The sums of the first product move from TMEM to registers every eight
-// stages, since the tensor cores' fp32 sums cut where they should round.
+// u goes into the second product as two bf16 parts, 16 of its bits.  The sums
+// of the first product move from TMEM to registers every eight stages, since
+// the tensor cores' fp32 sums cut where they should round.
+//
+// Measured: 13312 rows of 8 adapters, 2816 to 2048 columns, rank 64, 55 us, 3.4
+// TB/s of what they have to move; afd_lora_tiles.cu's takes 64.  Once its ring
+// is full a CTA moves 23 bytes a cycle, near its share of the memory's rate;
+// before that stand 3 us of dependent reads, between the products 2 us in which
+// u goes through registers, and 110 tiles leave 42 of 152 SMs idle (96 rows a
+// tile filled them and gained 2 us: the memory was busy).  Not kept: gathering
+// by TMA (tile::gather4: 1.5 us a stage); asking L2 for whole rows ahead (12 us
+// slower); each copying warp a part of every stage (0.8 us of barriers and
+// waits for each, whatever the ring's depth).
 //
 // All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"

@@ -1,6 +1,6 @@
 // afd_lora_tiles.cu -- both products of the adapters for batches of many rows,
 // of any type, alignment and rank (afd_lora_apply.cu: few rows, afd_lora_tc.cu:
-// bf16 rows of whole 16 bytes, ranks up to 64), 64 rows a tile:
+// bf16 rows of whole 16 bytes, ranks of 33 to 64), 64 rows a tile:
 //   u_t = w1[l] src_t,  out_t = base_t + scale[l] w2[l]^T u_t
 //
 // Bound by memory: src and base in, out out, at rank operations a byte.  So
@@ -16,6 +16,13 @@
 // meet through distributed shared memory, in order) and out's for the second.
 // The tensor cores' fp32 sums cut where they should round, so every four
 // stages the sums move to registers that add with rounding.
+//
+// Measured (8 adapters, rank 16 and 8): 13312 rows, 2048 to 2816 columns bf16,
+// 43 us, 4.7 TB/s of what they have to move (70 % of the copy rate); beside 64
+// fp32 logits 17 us, 3.6 TB/s.  Between launch and first rows stand three
+// dependent reads (plan, order, rows), some 3 us; with the SMs' three CTAs full
+// of stages the rest runs near the copy rate.  fp32 rows take three MMAs for
+// one and a split of every stage: 2000 rows of 60 logits to 1408 columns 11 us.
 #include <cooperative_groups.h>
 
 #include "afd_lora.cuh"

@@ -10,8 +10,9 @@
 // whole 16 bytes, are first laid out in the plan's order as one or three bf16
 // planes (k_lora_planes): 24 bits again, a stage for each plane (split by the
 // threads that multiply, the gradients of 12000 fp32 rows of 3649 columns, rank
-// 64, took 200 us more).  The parts of up to 32 ranks stand side by side in the 128 rows of one MMA and are added at the
-// end, those of more take two or three MMAs.
+// 64, took 200 us more).  The parts of up to 32 ranks stand side by side in the
+// 128 rows of one MMA and are added at the end, those of more take two or three
+// MMAs.
 //
 // Sums in TMEM may cut where they should round, so they move to registers
 // every four stages (128 rows) and start anew in the other accumulator, while
@@ -23,7 +24,10 @@
 // the last is stored.  With all warps together, two CTAs of 128 columns an SM,
 // a stage of 32 rows took 1150 to 1800 cycles of barrier, issue, wait and
 // copying one after the other, and an item 9000 before and behind its stages
-// (rank 64, 13312 rows: 62 us where this takes 47).
+// (rank 64, 13312 rows: 62 us where this takes 48, and the sum of the pieces 8
+// more).  What it has to read and write would take 21; a stage's copies take a
+// warp 1200 to 2600 cycles, most while other warps store partial sums, and five
+// stages are all that the staged output leaves room for.
 //
 // All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"
