@@ -222,7 +222,7 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // The workspace: parts of v and of u, the partial sums of da and db, and the
 // planes of x and dy where the rows themselves cannot be copied to the tensor
 // cores' operands (the pitches are not known when its size is asked for, so
-// bf16 rows count with one plane unless their columns are whole).
+// bf16 rows always count with one).
 static int64_t lora_workspace(int64_t T, int L, int K, int M, int R, int x_f32, int y_f32) {
   const LoraPlan p = lora_plan_at(nullptr, T, L);
   return 2 * up256(lora_parts_bytes(T, L, lora_padded(R))) + up256(p.max_slots * R * K * 4) + up256(p.max_slots * R * M * 4) +

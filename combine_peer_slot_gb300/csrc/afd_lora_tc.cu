@@ -9,8 +9,9 @@
 // u into the second product's operand and add to base.  An item is a tile of
 // up to 128 rows of one adapter and a share of the output columns; a stage is
 // 128 bytes of each row, of src and then of base, with the weight's 64 columns,
-// and the ring runs on from product to product and from item to item.  Each share of a tile computes u anew, from L2 but for
-// the first one's reads, which costs less than meeting.
+// and the ring runs on from product to product and from item to item.  Each
+// share of a tile computes u anew, from L2 but for the first one's reads, which
+// costs less than meeting.
 //
 // u goes into the second product as two bf16 parts, 16 of its bits.  The sums
 // of the first product move from TMEM to registers every eight stages, since
@@ -35,8 +36,7 @@ __device__ uint32_t g_errors;  // waits that gave up
 
 constexpr int TT = 128;
 constexpr int kSumWarps = 8, kCopyWarps = 4;
-constexpr int kSumThreads = kSumWarps * 32, kCopyThreads = kCopyWarps * 32;
-constexpr int kThreads = kSumThreads + kCopyThreads + 32;
+constexpr int kThreads = (kSumWarps + kCopyWarps + 1) * 32;
 constexpr int kCopyRows = 4, kCopies = TT / kCopyRows;  // rows of a warp's copy, copies of a stage
 constexpr int kRowsBytes = TT * kLoraRowBytes;  // a stage's rows
 constexpr int kFlush = 8;                       // stages between two moves of u's sums
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
           if (a.u_parts) {
             split_eight<3>(u + 8 * c, p);
 #pragma unroll
-            for (int x = 0; x < 3; x++) *reinterpret_cast<uint4*>(parts_at<RP>(a.u_parts, part_row + row, x * RP + rank0 + c * 8)) = p[x];
+            for (int x = 0; x < 3; x++)
+              *reinterpret_cast<uint4*>(parts_at<RP>(a.u_parts, part_row + row, x * RP + rank0 + c * 8)) = p[x];
           }
           if (a.other_parts) {
             const float* o = a.other + out_row * a.R;
@@ -355,14 +356,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
             for (int r = 0; r < 8; r++) v[r] = rank0 + c * 8 + r < a.R ? o[rank0 + c * 8 + r] : 0.0f;
             split_eight<3>(v, p);
 #pragma unroll
-            for (int x = 0; x < 3; x++) *reinterpret_cast<uint4*>(parts_at<RP>(a.other_parts, part_row + row, x * RP + rank0 + c * 8)) = p[x];
+            for (int x = 0; x < 3; x++)
+              *reinterpret_cast<uint4*>(parts_at<RP>(a.other_parts, part_row + row, x * RP + rank0 + c * 8)) = p[x];
           }
         }
       }
       if (share == 0 && (a.u_parts || a.other_parts) && row < t.w) {  // to a whole block: zeros
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
         for (int c = half; c < 3 * RP / 8; c += 2) {
-          if (a.u_parts) *reinterpret_cast<uint4*>(parts_at<RP>(a.u_parts, part_row + t.z + row, c * 8)) = make_uint4(0u, 0u, 0u, 0u);
-          if (a.other_parts) *reinterpret_cast<uint4*>(parts_at<RP>(a.other_parts, part_row + t.z + row, c * 8)) = make_uint4(0u, 0u, 0u, 0u);
+          if (a.u_parts) *reinterpret_cast<uint4*>(parts_at<RP>(a.u_parts, part_row + t.z + row, c * 8)) = none;
+          if (a.other_parts) *reinterpret_cast<uint4*>(parts_at<RP>(a.other_parts, part_row + t.z + row, c * 8)) = none;
         }
       }
       // this lane's 16 bytes of rows 4 h + lane / 8 of the warp's, as they are stored

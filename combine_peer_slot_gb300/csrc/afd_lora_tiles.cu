@@ -89,8 +89,9 @@ __device__ __noinline__ void slow_fill(const LoraArgs& a, uint32_t st, bool firs
     }
   } else {
     const TO* b = reinterpret_cast<const TO*>(a.base);
-    load_chunk<TO>(chunk_at(st, r0, ch), b && row0 >= 0 ? b + row0 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
-    load_chunk<TO>(chunk_at(st, r0 + 32, ch), b && row1 >= 0 ? b + row1 * a.ldb : nullptr, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+    const TO *b0 = b && row0 >= 0 ? b + row0 * a.ldb : nullptr, *b1 = b && row1 >= 0 ? b + row1 * a.ldb : nullptr;
+    load_chunk<TO>(chunk_at(st, r0, ch), b0, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
+    load_chunk<TO>(chunk_at(st, r0 + 32, ch), b1, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
     for (int e = threadIdx.x; e < KC * 16 * (CB / 8); e += kThreads) {
       const int r = e / (CB / 8), cc = e % (CB / 8);
       load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w2 + (int64_t)r * a.M : nullptr, c0 + cc * 8, a.M, a.how_w2, a.plan.head);
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       uint32_t w[kU];
-      split_pair<kU>(*reinterpret_cast<const float2*>(part + (wt * 16 + g + (j & 1) * 8) * F::kUStride + ks * 16 + 2 * c + (j >> 1) * 8), w);
+      const float* v = part + (wt * 16 + g + (j & 1) * 8) * F::kUStride + ks * 16 + 2 * c + (j >> 1) * 8;
+      split_pair<kU>(*reinterpret_cast<const float2*>(v), w);
 #pragma unroll
       for (int y = 0; y < kU; y++) p[y][j] = w[y];
     }
@@ -332,8 +334,10 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
       uint32_t p[kU];
       split_pair<kU>(v[i], p);
 #pragma unroll
-      for (int y = 0; y < kU; y++)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(us + ((y * TT + e / (KC * 8)) * F::kPStride + e % (KC * 8) * 2) * 2), "r"(p[y]) : "memory");
+      for (int y = 0; y < kU; y++) {
+        const uint32_t to = us + ((y * TT + e / (KC * 8)) * F::kPStride + e % (KC * 8) * 2) * 2;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(p[y]) : "memory");
+      }
     }
   }
   const int steps = (a.R + 15) / 16;
@@ -358,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
       if (ks >= steps) break;
       if (!kHold) {
 #pragma unroll
-        for (int y = 0; y < kU; y++) ldsm4(us + ((y * TT + wt * 16 + (lane & 15)) * F::kPStride + ks * 16 + (lane >> 4) * 8) * 2, held[0][y]);
+        for (int y = 0; y < kU; y++)
+          ldsm4(us + ((y * TT + wt * 16 + (lane & 15)) * F::kPStride + ks * 16 + (lane >> 4) * 8) * 2, held[0][y]);
       }
       uint32_t(&u)[kU][4] = held[kHold ? ks : 0];
 #pragma unroll

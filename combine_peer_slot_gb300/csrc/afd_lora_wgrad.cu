@@ -210,9 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_wgrad(const __grid_constan
 #pragma unroll
         for (int ks = 0; ks < kRows / 16; ks++)
 #pragma unroll
-          for (int x = W::kMmas - 1; x >= 0; x--)
-            lora_mma(el, d, lora_desc(pa + (x * 2 * kAtom + ks * 2048 >> 4), 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - (pa + (x * 2 * kAtom >> 4))),
-                     lora_desc(qa + ks * 128, kAtom >> 4), kIdesc, i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+          for (int x = W::kMmas - 1; x >= 0; x--) {
+            const uint32_t at = pa + (x * 2 * kAtom >> 4), apart = 2 * x + 1 < W::kAtoms ? kAtom >> 4 : (zero >> 4) - at;
+            lora_mma(el, d, lora_desc(at + (ks * 2048 >> 4), apart), lora_desc(qa + ks * 128, kAtom >> 4), kIdesc,
+                     i % kFlush != 0 || ks != 0 || x != W::kMmas - 1);
+          }
         lora_commit(el, smem_u32(&empty[slot]));
         if (i % kFlush == kFlush - 1 || i == n - 1) lora_commit(el, smem_u32(&dfull[group++ & 1]));
       }
@@ -362,8 +364,8 @@ cudaError_t launch_lora_planes(const LaunchCtx& lc, const LoraPlan& plan, int64_
                                int f32, int vec, uint16_t* to) {
   const int64_t pitch = lora_plane_pitch(N), plane = tokens * pitch;
   const unsigned grid = (unsigned)std::min<int64_t>((tokens + 7) / 8, 8 * kLoraSms);
-  return f32 ? launch_k(lc, k_lora_planes<float>, grid, 256, 0, plan, reinterpret_cast<const float*>(q), ldq, N, vec, to, pitch, plane)
-             : launch_k(lc, k_lora_planes<uint16_t>, grid, 256, 0, plan, reinterpret_cast<const uint16_t*>(q), ldq, N, vec, to, pitch, plane);
+  if (f32) return launch_k(lc, k_lora_planes<float>, grid, 256, 0, plan, (const float*)q, ldq, N, vec, to, pitch, plane);
+  return launch_k(lc, k_lora_planes<uint16_t>, grid, 256, 0, plan, (const uint16_t*)q, ldq, N, vec, to, pitch, plane);
 }
 
 // Each kernel may start while the one before it ends, and waits for its end
