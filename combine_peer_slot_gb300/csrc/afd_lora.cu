@@ -145,8 +145,8 @@ bool dims_ok(int K, int M, int R) {
 }
 // how rows of n elements can be moved (LoraArgs)
 int how_rows(const void* p, int64_t ld, int n, int dtype) {
-  for (int b = 16; b >= 4; b /= 4)
-    if (!off_by(p, b) && ld * size_of(dtype) % b == 0 && n * size_of(dtype) % b == 0) return b == 16 ? 2 : 1;
+  for (int b = 16; b >= 4; b /= 2)
+    if (!off_by(p, b) && ld * size_of(dtype) % b == 0 && n * size_of(dtype) % b == 0) return b;
   return 0;
 }
 cudaError_t launch_products(const LaunchCtx& lc, LoraArgs& g) {
@@ -296,9 +296,9 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
     w.planes[i] = f32 ? 3 : 1;
     w.q[i] = rows[i];
     w.ldq[i] = ld[i];
-    if (f32 || how != 2) {
+    if (f32 || how != 16) {
       uint16_t* to = reinterpret_cast<uint16_t*>(take(n_tokens * lora_plane_pitch(w.N[i]) * 2 * w.planes[i]));
-      e = launch_lora_planes(lc, g.plan, n_tokens, rows[i], ld[i], w.N[i], f32, how == 2 && w.N[i] % 8 == 0, to);
+      e = launch_lora_planes(lc, g.plan, n_tokens, rows[i], ld[i], w.N[i], f32, how == 16 && w.N[i] % 8 == 0, to);
       w.q[i] = to;
       w.ldq[i] = lora_plane_pitch(w.N[i]);
       w.plane[i] = n_tokens * w.ldq[i];

@@ -81,7 +81,7 @@ struct LoraArgs {
   int64_t T;
   int K, M, R, L;
   int src_f32, out_f32;
-  // how rows can be moved: 2 = 16 bytes at a time, 1 = 4, 0 = by elements
+  // how rows can be moved: 16, 8 or 4 bytes at a time, 0 = by elements (bf16)
   int how_src, how_w1, how_w2, how_base, how_out;
 };
 // da[l] = scale[l] sum v_t x_t^T, db[l] = scale[l] sum u_t dy_t^T
@@ -188,6 +188,28 @@ struct OutParts<uint16_t> { static constexpr int kParts = 2; };
 template <>
 struct OutParts<float> { static constexpr int kParts = 3; };
 
+// Eight bf16 values of a row of any alignment from column c0, zeros from column
+// n on: by the words that hold one of them at least (so nothing is read past
+// the 4-byte word of the row's first or last value), shifted into place.
+__device__ __forceinline__ uint4 load_words(const uint16_t* row, int c0, int n) {
+  const int have = min(n - c0, 8);
+  if (have <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c0);
+  const int odd = (int)(at >> 1 & 1);
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(at - 2 * odd);
+  uint32_t w[5];
+#pragma unroll
+  for (int i = 0; i < 5; i++) w[i] = 2 * i < have + odd ? from[i] : 0u;
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[i] = __funnelshift_r(w[i], w[i + 1], 16 * odd);
+    if (2 * i >= have) v[i] = 0u;
+    else if (2 * i + 1 >= have) v[i] &= 0xffffu;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Eight neighbouring values of a row from column c0 as packed bf16 parts;
 // columns from n on are zero.  vec: rows are 16-byte aligned and n % 8 == 0.
 template <typename T>
@@ -200,7 +222,7 @@ __device__ __forceinline__ void load_eight<uint16_t>(const uint16_t* row, int c0
     v[0] = *reinterpret_cast<const uint4*>(row + c0);
     return;
   }
-  uint32_t w[8];
+  uint32_t w[8];  // (load_words' longer code costs the rows that do not take it 5 % in afd_lora_apply.cu)
 #pragma unroll
   for (int i = 0; i < 8; i++) w[i] = c0 + i < n ? (uint32_t)row[c0 + i] : 0u;
   v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
@@ -250,8 +272,9 @@ constexpr int kLoraRowBytes = 128;
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_few(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? BYTES : 0), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -271,32 +294,22 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
   return tile + r * kLoraRowBytes + ((c ^ (r & 7)) << 4);
 }
 
-// One chunk of a row from element c0 (n in the row; NULL: no row), zeros past
-// its end.  how: 2 = 16 bytes at a time, 1 = 4 (even sizes), 0 = elements,
-// through registers.
+// The asynchronous copy of one chunk of a row from element c0 (n in the row;
+// NULL: no row), zeros past its end; how: 16, 8 or 4 bytes at a time.
 template <typename T>
-__device__ __forceinline__ void load_chunk(uint32_t dst, const T* row, int c0, int n, int how, const void* any) {
-  constexpr int E = 16 / (int)sizeof(T);
-  if (how == 2) {
-    const bool in = row && c0 < n;
-    copy16(dst, in ? (const void*)(row + c0) : any, in);
-  } else if (how == 1) {
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const T* row, int c0, int n, int how, const void* any) {
+  const char* from = reinterpret_cast<const char*>(row + c0);
+  const int left = row ? (n - c0) * (int)sizeof(T) : 0;  // bytes
+  if (how == 16) {
+    copy16(dst, left > 0 ? from : any, left > 0);
+  } else if (how == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int c = c0 + i * (E / 4);
-      const bool in = row && c < n;
-      copy4(dst + 4 * i, in ? (const void*)(row + c) : any, in);
-    }
+    for (int i = 0; i < 16; i += 8) copy_few<8>(dst + i, left > i ? from + i : any, left > i);
   } else {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (row)
 #pragma unroll
-      for (int i = 0; i < E; i++)
-        if (c0 + i < n) w[i * (int)sizeof(T) / 4] |= (uint32_t)(*reinterpret_cast<const uint16_t*>(row + c0 + i)) << (i % 2 * 16);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    for (int i = 0; i < 16; i += 4) copy_few<4>(dst + i, left > i ? from + i : any, left > i);
   }
 }
-
 
 // Up to 128 rows without an adapter: out = base (nothing where they are the
 // same), u = 0; by threads first, first + step, ..  Eight loads stand before
@@ -308,7 +321,7 @@ __device__ __forceinline__ void copy_bare(const LoraArgs& a, const int32_t* orde
   const TO* base = reinterpret_cast<const TO*>(a.base);
   TO* out = reinterpret_cast<TO*>(a.out);
   if (a.base != a.out) {
-    const bool vec = a.how_out == 2 && (!base || a.how_base == 2);
+    const bool vec = a.how_out == 16 && (!base || a.how_base == 16);
     const uint32_t per_row = vec ? a.M / E : a.M, all = rows * per_row;
     for (uint32_t i0 = first; i0 < all; i0 += kBatch * step) {
       uint4 v[kBatch];

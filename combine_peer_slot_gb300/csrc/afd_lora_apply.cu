@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   constexpr int kParts = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
   constexpr int kRows = KC;                 // rank tiles of a pass
   constexpr int kCols = TT / 8;             // row tiles
-  const bool vk = a.how_src == 2 && a.how_w1 == 2;
-  const bool vm = a.how_w2 == 2 && a.how_out == 2 && (!a.base || a.how_base == 2);
+  const bool vk = a.how_src == 16 && a.how_w1 == 16;
+  const bool vm = a.how_w2 == 16 && a.how_out == 16 && (!a.base || a.how_base == 16);
   extern __shared__ __align__(16) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), q = (int)cluster.block_rank();

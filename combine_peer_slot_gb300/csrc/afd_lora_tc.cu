@@ -437,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
 // 1100 23 / 16, 4000 25 / 23, 13312 47 / 47.  fp32 outputs, which are logits of
 // few columns, gained nothing from it either.
 bool lora_tc_takes(const LoraArgs& a) {
-  return !a.src_f32 && !a.out_f32 && a.R > 32 && a.R <= 64 && a.how_src == 2 && a.how_w1 == 2 && a.how_w2 == 2 &&
-         a.how_out == 2 && (!a.base || a.how_base == 2) && a.lds < (int64_t(1) << 31) &&
+  return !a.src_f32 && !a.out_f32 && a.R > 32 && a.R <= 64 && a.how_src == 16 && a.how_w1 == 16 && a.how_w2 == 16 &&
+         a.how_out == 16 && (!a.base || a.how_base == 16) && a.lds < (int64_t(1) << 31) &&
          (!a.base || a.ldb < (int64_t(1) << 31));
 }
 

@@ -18,7 +18,7 @@
 // stages the sums move to registers that add with rounding.
 //
 // Measured (8 adapters, rank 16 and 8): 13312 rows, 2048 to 2816 columns bf16,
-// 43 us, 4.7 TB/s of what they have to move (70 % of the copy rate); beside 64
+// 42 us, 4.9 TB/s of what they have to move (73 % of the copy rate); beside 64
 // fp32 logits 17 us, 3.6 TB/s.  Between launch and first rows stand three
 // dependent reads (plan, order, rows), some 3 us; with the SMs' three CTAs full
 // of stages the rest runs near the copy rate.  fp32 rows take three MMAs for
@@ -58,6 +58,19 @@ __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ void sts_f2(uint32_t addr, float x, float y) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
@@ -72,34 +85,77 @@ __device__ __forceinline__ void split_eight_at(uint32_t a, uint32_t b, uint4 (&t
   for (int x = 0; x < PARTS; x++) to[x] = make_uint4(w[0][x], w[1][x], w[2][x], w[3][x]);
 }
 
-// A stage's copies where some rows cannot be moved 16 bytes at a time.
-template <int KC, typename TS, typename TO>
-__device__ __noinline__ void slow_fill(const LoraArgs& a, uint32_t st, bool first, int c0, int64_t row0, int64_t row1,
-                                       const uint16_t* w1, const uint16_t* w2) {
-  constexpr int KB = kRowBytes / (int)sizeof(TS), CB = kRowBytes / (int)sizeof(TO);
-  const int ch = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+// A stage's rows and weights where some cannot be moved 16 bytes at a time:
+// this thread's chunk of two rows and its share of the weight's.  Those that
+// come through registers (bf16 rows of odd places) are all asked for before the
+// first is stored.
+template <int KC, typename T>
+__device__ __noinline__ void slow_fill(uint32_t st, const T* row0, const T* row1, int c0, int cols, int how, const uint16_t* w,
+                                       int ranks, int how_w, const void* any) {
+  constexpr int E = 16 / (int)sizeof(T);  // elements of a row's chunk; chunks of a weight's row
+  constexpr int kMine = (KC * 16 * E + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x, ch = tid & 7, r0 = tid >> 3;
   const uint32_t wst = st + kTileBytes;
-  if (first) {
-    const TS* s = reinterpret_cast<const TS*>(a.src);
-    load_chunk<TS>(chunk_at(st, r0, ch), row0 >= 0 ? s + row0 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
-    load_chunk<TS>(chunk_at(st, r0 + 32, ch), row1 >= 0 ? s + row1 * a.lds : nullptr, c0 + ch * (KB / 8), a.K, a.how_src, a.plan.head);
-    for (int e = threadIdx.x; e < KC * 16 * (KB / 8); e += kThreads) {
-      const int r = e / (KB / 8), cc = e % (KB / 8);
-      load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w1 + (int64_t)r * a.K : nullptr, c0 + cc * 8, a.K, a.how_w1, a.plan.head);
-    }
+  uint4 v[2], m[kMine];
+  const bool bare = sizeof(T) == 2 && how == 0;  // (fp32 rows are of whole words)
+  if (bare) {
+    v[0] = load_words(reinterpret_cast<const uint16_t*>(row0), c0 + ch * E, row0 ? cols : 0);
+    v[1] = load_words(reinterpret_cast<const uint16_t*>(row1), c0 + ch * E, row1 ? cols : 0);
   } else {
-    const TO* b = reinterpret_cast<const TO*>(a.base);
-    const TO *b0 = b && row0 >= 0 ? b + row0 * a.ldb : nullptr, *b1 = b && row1 >= 0 ? b + row1 * a.ldb : nullptr;
-    load_chunk<TO>(chunk_at(st, r0, ch), b0, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
-    load_chunk<TO>(chunk_at(st, r0 + 32, ch), b1, c0 + ch * (CB / 8), a.M, a.how_base, a.plan.head);
-    for (int e = threadIdx.x; e < KC * 16 * (CB / 8); e += kThreads) {
-      const int r = e / (CB / 8), cc = e % (CB / 8);
-      load_chunk<uint16_t>(chunk_at(wst, r, cc), r < a.R ? w2 + (int64_t)r * a.M : nullptr, c0 + cc * 8, a.M, a.how_w2, a.plan.head);
+    copy_chunk<T>(chunk_at(st, r0, ch), row0, c0 + ch * E, cols, how, any);
+    copy_chunk<T>(chunk_at(st, r0 + 32, ch), row1, c0 + ch * E, cols, how, any);
+  }
+#pragma unroll
+  for (int x = 0; x < kMine; x++) {
+    const int e = tid + x * kThreads, r = e / E, c = c0 + e % E * 8;
+    const uint16_t* p = r < ranks ? w + (int64_t)r * cols : nullptr;
+    if (how_w == 0) m[x] = load_words(p, c, p ? cols : 0);
+    else if (r < KC * 16) copy_chunk<uint16_t>(chunk_at(wst, r, e % E), p, c, cols, how_w, any);
+  }
+  if (bare) {
+    sts16(chunk_at(st, r0, ch), v[0]);
+    sts16(chunk_at(st, r0 + 32, ch), v[1]);
+  }
+#pragma unroll
+  for (int x = 0; x < kMine; x++) {
+    const int e = tid + x * kThreads, r = e / E;
+    if (how_w == 0 && r < KC * 16) sts16(chunk_at(wst, r, e % E), m[x]);
+  }
+}
+
+// A warp's 16 rows of a block, 64 bytes each, from column `first`, where they
+// cannot be stored 16 bytes at a time: neighbouring lanes neighbouring values
+// (each lane its own 16 bytes' values one by one: four times the sectors, 78 us
+// for 7956 rows of 1181 to 1031 columns that take 43).
+template <typename TO>
+__device__ __forceinline__ void slow_store(const LoraArgs& a, uint32_t st, const int32_t* rows, int first) {
+  const int lane = threadIdx.x & 31, wt = threadIdx.x >> 5 & 3, half = threadIdx.x >> 7;
+  if (sizeof(TO) == 4 || a.how_out) {  // two rows' 16 words at a time
+    const int word = lane & 15, col = first + word * (4 / (int)sizeof(TO));
+#pragma unroll
+    for (int h = 0; h < 8; h++) {
+      const int r = wt * 16 + 2 * h + (lane >> 4);
+      const int64_t row = rows[r];
+      if (row >= 0 && col < a.M)
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<TO*>(a.out) + row * a.ldo + col) =
+            lds4(chunk_at(st, r, half * 4 + (word >> 2)) + (word & 3) * 4);
+    }
+  } else {  // a row's 32 values
+#pragma unroll
+    for (int h = 0; h < 16; h++) {
+      const int r = wt * 16 + h;
+      const int64_t row = rows[r];
+      if (row >= 0 && first + lane < a.M)
+        reinterpret_cast<uint16_t*>(a.out)[row * a.ldo + first + lane] =
+            (uint16_t)(lds4(chunk_at(st, r, half * 4 + (lane >> 3)) + (lane >> 1 & 3) * 4) >> (lane & 1) * 16);
     }
   }
 }
 
-template <int KC, typename TS, typename TO>
+// WHOLE: all rows can be moved 16 bytes at a time, and no code for others is
+// there (13312 rows of 2048 to 2816 columns 41.6 us, with it 42.8; 7956 rows of
+// 1184 to 1032 columns 18.7 and 21.4; of 1181 to 1031 columns 43).
+template <int KC, typename TS, typename TO, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const __grid_constant__ LoraArgs a) {
   constexpr int kS = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
   typedef Form<KC, kS, kU> F;
@@ -140,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
   // This thread's chunk of rows tid / 8 and tid / 8 + 32 of a tile, and of the
   // weight's rows tid / kWc + i kWr: addresses that move on by a stage's columns.
   const int ch = tid & 7, r0 = tid >> 3;
-  const bool fast1 = a.how_src == 2 && a.how_w1 == 2, fast2 = a.how_w2 == 2 && a.how_base == 2;
+  const bool fast1 = WHOLE || (a.how_src == 16 && a.how_w1 == 16), fast2 = WHOLE || (a.how_w2 == 16 && a.how_base == 16);
   const char *p0 = nullptr, *p1 = nullptr, *pw = nullptr;
   int left = 0, wleft = 0;  // columns from the chunk on; <= 0: none
   auto start = [&](const void* rows_at, int64_t ld, int size, int first, int cols, int chunk_cols, const uint16_t* w, int wide) {
@@ -180,7 +236,16 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
         pw += cols * 2;
         wleft -= cols;
       } else {
-        slow_fill<KC, TS, TO>(a, st, i < n1, i < n1 ? (k0 + i) * KB : (m0 + i - n1) * CB, rows[r0], rows[r0 + 32], w1, w2);
+        const int64_t row0 = rows[r0], row1 = rows[r0 + 32];
+        if (i < n1) {
+          const TS* p = reinterpret_cast<const TS*>(a.src);
+          slow_fill<KC, TS>(st, row0 >= 0 ? p + row0 * a.lds : nullptr, row1 >= 0 ? p + row1 * a.lds : nullptr, (k0 + i) * KB, a.K,
+                            a.how_src, w1, a.R, a.how_w1, a.plan.head);
+        } else {
+          const TO* p = reinterpret_cast<const TO*>(a.base);
+          slow_fill<KC, TO>(st, p && row0 >= 0 ? p + row0 * a.ldb : nullptr, p && row1 >= 0 ? p + row1 * a.ldb : nullptr,
+                            (m0 + i - n1) * CB, a.M, a.how_base, w2, a.R, a.how_w2, a.plan.head);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -208,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
       split_eight_at<kS>(chunk_at(st, r, c8 >> 2), chunk_at(st, r, (c8 >> 2) + 1), v);
 #pragma unroll
       for (int y = 0; y < kS; y++)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(xs + (y * TT + r) * kXStride + c8 * 2), "r"(v[y].x), "r"(v[y].y),
-                     "r"(v[y].z), "r"(v[y].w) : "memory");
+        sts16(xs + (y * TT + r) * kXStride + c8 * 2, v[y]);
       __syncthreads();
     }
 #pragma unroll
@@ -384,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
         const int r = wt * 16 + g + h * 8;
         if (sizeof(TO) == 2) {
           const uint32_t at = chunk_at(st, r, half * NT + j) + 4 * c;
-          uint32_t w;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+          const uint32_t w = lds4(at);
           const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(w << 16) + scale * d[j][2 * h],
                                                          __uint_as_float(w & 0xffff0000u) + scale * d[j][2 * h + 1]);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&v)) : "memory");
@@ -397,35 +460,26 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
         }
       }
     __syncwarp();
-    const int cc = half * 4 + c, col = (m0 + i - n1) * CB + cc * (CB / 8);
+    const int first = (m0 + i - n1) * CB + half * (CB / 2);  // the half's first column
+    if (WHOLE || a.how_out == 16) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      if (o[h] && col < a.M) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(chunk_at(st, wt * 16 + h * 8 + g, cc)) : "memory");
-        if (a.how_out == 2) {
-          *reinterpret_cast<uint4*>(o[h]) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (sizeof(TO) == 2) {
-#pragma unroll
-          for (int x = 0; x < 8; x++)
-            if (col + x < a.M) reinterpret_cast<uint16_t*>(o[h])[x] = (uint16_t)(w[x / 2] >> (x % 2 * 16));
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; x++)
-            if (col + x < a.M) reinterpret_cast<uint32_t*>(o[h])[x] = w[x];
+      for (int h = 0; h < 2; h++) {
+        if (o[h] && first + c * (CB / 8) < a.M) {
+          *reinterpret_cast<uint4*>(o[h]) = lds16(chunk_at(st, wt * 16 + h * 8 + g, half * 4 + c));
+          o[h] += CB;
         }
-        o[h] += CB;
       }
+    } else {
+      slow_store<TO>(a, st, rows, first);
     }
   }
 }
 
-template <int KC, typename TS, typename TO>
+template <int KC, typename TS, typename TO, bool WHOLE>
 cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
   typedef Form<KC, LoraSrc<TS>::kParts, OutParts<TO>::kParts> F;
   static std::atomic<int> done[kMaxCachedDevices];
-  cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO>, F::kBytes, done);
+  cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO, WHOLE>, F::kBytes, done);
   if (e != cudaSuccess) return e;
   // As many CTAs a tile as fill the SMs; halves of tiles that hold rows, at most
   // (some of those of many adapters' last tiles do not: a third more is room).
@@ -434,17 +488,22 @@ cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
   const int64_t tiles = 2 * a.plan.max_tiles, held = a.T / TT + std::min<int64_t>(a.T, a.L) + 1;
   unsigned C = KC >= 4 ? 4 : 8;
   while (C > 1 && held * C > kLoraSms * F::kCtas * 4 / 3) C /= 2;
-  return launch_k_cluster(lc, k_lora_tiles<KC, TS, TO>, (unsigned)(tiles * C), kThreads, (size_t)F::kBytes, C, a);
+  return launch_k_cluster(lc, k_lora_tiles<KC, TS, TO, WHOLE>, (unsigned)(tiles * C), kThreads, (size_t)F::kBytes, C, a);
+}
+template <typename TS, typename TO, bool WHOLE>
+cudaError_t by_rank(const LaunchCtx& lc, const LoraArgs& a) {
+  return a.R <= 16 ? run<1, TS, TO, WHOLE>(lc, a) : a.R <= 32 ? run<2, TS, TO, WHOLE>(lc, a)
+       : a.R <= 64 ? run<4, TS, TO, WHOLE>(lc, a) : run<8, TS, TO, WHOLE>(lc, a);
 }
 template <typename TS, typename TO>
-cudaError_t by_rank(const LaunchCtx& lc, const LoraArgs& a) {
-  return a.R <= 16 ? run<1, TS, TO>(lc, a) : a.R <= 32 ? run<2, TS, TO>(lc, a)
-       : a.R <= 64 ? run<4, TS, TO>(lc, a) : run<8, TS, TO>(lc, a);
+cudaError_t by_rows(const LaunchCtx& lc, const LoraArgs& a) {
+  const bool whole = a.how_src == 16 && a.how_w1 == 16 && a.how_w2 == 16 && a.how_out == 16 && (!a.base || a.how_base == 16);
+  return whole ? by_rank<TS, TO, true>(lc, a) : by_rank<TS, TO, false>(lc, a);
 }
 
 }  // namespace
 
 cudaError_t launch_lora_tiles(const LaunchCtx& lc, const LoraArgs& a) {
-  if (a.src_f32) return a.out_f32 ? by_rank<float, float>(lc, a) : by_rank<float, uint16_t>(lc, a);
-  return a.out_f32 ? by_rank<uint16_t, float>(lc, a) : by_rank<uint16_t, uint16_t>(lc, a);
+  if (a.src_f32) return a.out_f32 ? by_rows<float, float>(lc, a) : by_rows<float, uint16_t>(lc, a);
+  return a.out_f32 ? by_rows<uint16_t, float>(lc, a) : by_rows<uint16_t, uint16_t>(lc, a);
 }

@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(256) k_lora_planes(const LoraPlan plan, const 
 #pragma unroll 2
     for (int c = lane * 8; c < N; c += 256) {
       uint4 v[kP];
-      load_eight<T>(from, c, N, vec, v);
+      if (sizeof(T) == 2 && !vec) v[0] = load_words(reinterpret_cast<const uint16_t*>(from), c, N);
+      else load_eight<T>(from, c, N, vec, v);
 #pragma unroll
       for (int x = 0; x < kP; x++) *reinterpret_cast<uint4*>(to + x * plane + i * pitch + c) = v[x];
     }
