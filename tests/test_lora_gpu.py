@@ -150,6 +150,25 @@ def test_pitches(xt, yt, T):
         assert (o[:, :first] == 7).all() and (o[:, first + 160:] == 7).all()
 
 
+@pytest.mark.parametrize("xt,yt", [(BF, BF), (BF, F), (F, F), (F, BF)])
+@pytest.mark.parametrize("T,rank", [(30, 16), (1100, 16), (1100, 48), (1100, 100)])
+def test_ragged_columns(xt, yt, T, rank):
+    """Columns that end inside a word, 8 and 16 bytes, from rows that begin at
+    any element; nothing beside the outputs' rows is written."""
+    for K, M, pitch, first in ((161, 97, 203, 3), (162, 98, 206, 2), (164, 100, 208, 4), (67, 257, 265, 5)):
+        d = make(T, K, M, rank, 3, xt, yt, "mixed", 11)
+        for n in ("x", "base", "dy", "d_base"):
+            v = torch.full((T, pitch), math.nan, dtype=d[n].dtype, device="cuda")[:, first:first + d[n].shape[1]]
+            v.copy_(d[n])
+            d[n] = v
+        o = torch.full((T, pitch), 7.0, dtype=yt, device="cuda")
+        batch, _, u = check_apply(d, out=o[:, first:first + M])
+        assert (o[:, :first] == 7).all() and (o[:, first + M:] == 7).all()
+        o = torch.full((T, pitch), 7.0, dtype=xt, device="cuda")
+        check_backward(d, batch, u, dx=o[:, first:first + K])
+        assert (o[:, :first] == 7).all() and (o[:, first + K:] == 7).all()
+
+
 @pytest.mark.parametrize("T", [48, 1300])
 @pytest.mark.parametrize("xt", [BF, F])
 def test_not_finite_rows(T, xt):
