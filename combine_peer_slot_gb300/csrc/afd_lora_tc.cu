@@ -17,7 +17,7 @@
 // of the first product move from TMEM to registers every eight stages, since
 // the tensor cores' fp32 sums cut where they should round.
 //
-// Measured: 13312 rows of 8 adapters, 2816 to 2048 columns, rank 64, 55 us, 3.4
+// Measured: 13312 rows of 8 adapters, 2816 to 2048 columns, rank 64, 53 us, 3.6
 // TB/s of what they have to move; afd_lora_tiles.cu's takes 64.  Once its ring
 // is full a CTA moves 23 bytes a cycle, near its share of the memory's rate;
 // before that stand 3 us of dependent reads, between the products 2 us in which
@@ -25,7 +25,9 @@
 // tile filled them and gained 2 us: the memory was busy).  Not kept: gathering
 // by TMA (tile::gather4: 1.5 us a stage); asking L2 for whole rows ahead (12 us
 // slower); each copying warp a part of every stage (0.8 us of barriers and
-// waits for each, whatever the ring's depth).
+// waits for each, whatever the ring's depth); a warp that waits for its last
+// stage's copies and then says so (55 us; each lane's arrival by its copies'
+// end 53; six copying warps, not four, half a microsecond less).
 //
 // All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"
@@ -47,9 +49,7 @@ constexpr int kStageBytes = kRowsBytes + RP * kLoraRowBytes;
 constexpr int kUBytes = KU * kRowsBytes;        // u's parts, rows of 128 bytes
 constexpr int S = (224 * 1024 - kUBytes) / kStageBytes;  // stages
 constexpr int kBytes = S * kStageBytes + kUBytes;
-// (a copying warp says that a stage is there after it has begun its next one,
-// kCopyWarps stages on, for which that one's slot must be another)
-static_assert(S > kCopyWarps + 1, "stages ahead");
+static_assert(S >= kCopyWarps, "each copying warp has a stage");
 
 // Operands have the 128-byte swizzle: K-major (8-row groups 1024 bytes apart),
 // or MN-major of one 64-element atom (8-k groups 1024 bytes apart).
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
   const int shares = shares_of(head.x, gridDim.x, n1, blocks, lane), items = head.x * shares;
   const uint32_t ring = smem_u32(smem), us = ring + S * kStageBytes;
   if (tid < S) {
-    mbar_init(smem_u32(&full[tid]), 1);
+    mbar_init(smem_u32(&full[tid]), 32);
     mbar_init(smem_u32(&empty1[tid]), 1);
     mbar_init(smem_u32(&empty2[tid]), kSumWarps / 2);
     if (tid < 2) {
@@ -175,7 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
     // its copies (two barriers, the wait) then passes while others copy.
     const int ch = lane & 7, r0 = lane >> 3;  // this lane's 16 bytes of rows r0 + 4 j
     int stage = 0, slot = 0;                  // of the ring, all warps'
-    int open = -1;                            // slot of this warp's stage under way
     // by slot: its last use was for the second product; the uses for the
     // first, for the second so far, modulo 2
     uint32_t second = 0, odd1 = 0, odd2 = 0;
@@ -214,21 +213,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
             const bool with = r0 + kCopyRows * j < a.R;
             copy16_if(true, (j & 1 ? at1 : at0) + kRowsBytes + j * 512, with ? w + (uint64_t)j * wpitch : nowhere, with ? bytes : 0);
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (open >= 0) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[open]));
-          }
-          open = slot;
+          // each lane arrives when its copies have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
         }
         second = one ? second & ~bit : second | bit;
         if (one) odd1 ^= bit; else odd2 ^= bit;
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
-    if (good && open >= 0 && lane == 0) mbar_arrive(smem_u32(&full[open]));
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
   } else if (warp == kSumWarps + kCopyWarps) {  // ---- products ----
     const uint32_t el = lora_elect(), d1 = idesc(RP, false), d2 = idesc(64, true);
     const int steps = (a.R + 15) / 16;
@@ -433,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
 
 // Ranks of 33 to 64 only: microseconds for 2048 to 2816 columns, 8 adapters, this
 // kernel and afd_lora_tiles.cu's, by rows: rank 64: 1100 25 / 28, 4000 31 / 35,
-// 13312 55 / 70; rank 32: 1100 23 / 18, 4000 27 / 25, 13312 49 / 52; rank 16:
+// 13312 53 / 70; rank 32: 1100 23 / 18, 4000 27 / 25, 13312 49 / 52; rank 16:
 // 1100 23 / 16, 4000 25 / 23, 13312 47 / 47.  fp32 outputs, which are logits of
 // few columns, gained nothing from it either.
 bool lora_tc_takes(const LoraArgs& a) {
