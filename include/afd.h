@@ -857,12 +857,11 @@ int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters, const voi
  *   dB[l] = scale[l] sum_t u_t dy_t^T         fp32 [n_adapters, rank, M]
  * dy: y_dtype [n_tokens, M], row pitch ldy; u: afd_lora_apply's; d_base: the
  * shared projection's gradient, NULL or dx itself as base above, and no other
- * overlap.  dA and dB
- * (16-byte aligned) are written whole, zeros for adapters without rows (also
- * with n_tokens 0).  The sums' order does not depend on timing.  workspace:
- * device, 256-byte aligned, at least afd_lora_backward_workspace bytes (host
- * only; -1 outside the limits), else AFD_ERR_CAPACITY; one call at a time may
- * use it. */
+ * overlap.  dA and dB (16-byte aligned) are written whole, zeros for adapters
+ * without rows (also with n_tokens 0).  The sums' order does not depend on
+ * timing.  workspace: device, 256-byte aligned, at least
+ * afd_lora_backward_workspace bytes (host only; -1 outside the limits), else
+ * AFD_ERR_CAPACITY; one call at a time may use it. */
 int64_t afd_lora_backward_workspace(int64_t n_tokens, int n_adapters, int K, int M, int rank,
                                     int x_dtype, int y_dtype);
 int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const void* x,
