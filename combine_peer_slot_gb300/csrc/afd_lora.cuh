@@ -133,8 +133,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
 }
 
 // An fp32 value as a sum of bf16 values: the upper 8 bits of its fraction cut
-// off, then the next 8, then the rest: three parts are the value, two (the
-// second rounded) are within 2^-17 of it.  Cutting, unlike rounding, cannot
+// off, then the next 8, then the rest: three parts are the value.  Cutting, unlike rounding, cannot
 // carry the largest finite values over to infinity; a value that is not finite
 // is all in the first part (NaN stays NaN), with zeros behind it.
 template <int PARTS>
@@ -180,13 +179,12 @@ struct LoraSrc<uint16_t> { static constexpr int kParts = 1; };
 template <>
 struct LoraSrc<float> { static constexpr int kParts = 3; };
 
-// parts of u beside an output of this type
-template <typename TO>
-struct OutParts;
-template <>
-struct OutParts<uint16_t> { static constexpr int kParts = 2; };
-template <>
-struct OutParts<float> { static constexpr int kParts = 3; };
+// Parts of u in the second product: all of fp32's bits, beside bf16 outputs too,
+// since base or another rank may cancel what the upper ones make (two parts left
+// bf16 outputs 1.1e-4 of their norm from those of an fp32 u, three 3 to 5e-5, and
+// a third MMA takes 2 us of 45 over a prefill fan-in of rank 16, 2 of 112 in the
+// gradients of rank 64).
+constexpr int kLoraUParts = 3;
 
 // Eight bf16 values of a row of any alignment from column c0, zeros from column
 // n on: by the words that hold one of them at least (so nothing is read past

@@ -10,8 +10,8 @@
 // agree, so a lane takes 16 neighbouring bytes for its four k pairs.  The
 // sums over the warps go through shared memory, those over the CTAs through
 // distributed shared memory, always in the same order.  Then the warps share
-// the columns of out in blocks of 64.  u enters the second product as two
-// (out in bf16) or three (fp32) bf16 parts, so that it keeps 16 or 24 bits.
+// the columns of out in blocks of 64.  u enters the second product as
+// three bf16 parts, which keep its 24 bits.
 //
 // Measured (2048 to 2816 columns, rank 16): one row 4.6 us, 329 rows of 64
 // adapters 8.5 us, where their bytes would take 2.2: a chain of reads that
@@ -80,7 +80,7 @@ __device__ __forceinline__ void store_parts(uint16_t* to, int padded, int64_t i,
 
 template <int KC, typename TS, typename TO>
 __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constant__ LoraArgs a) {
-  constexpr int kParts = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
+  constexpr int kParts = LoraSrc<TS>::kParts, kU = kLoraUParts;
   constexpr int kRows = KC;                 // rank tiles of a pass
   constexpr int kCols = TT / 8;             // row tiles
   const bool vk = a.how_src == 16 && a.how_w1 == 16;
@@ -275,8 +275,8 @@ template <int KC, typename TS, typename TO>
 cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
   const int rt = (a.R + 15) / 16;
   constexpr int kRed = kWarps * KC * 16 * kRedStride * 4;
-  const int bytes = rt * 16 * TT * 4 + std::max(kRed, OutParts<TO>::kParts * TT * (rt * 16 + 8) * 2);
-  constexpr int kU = OutParts<TO>::kParts * TT * (kLoraMaxRank + 8) * 2;
+  const int bytes = rt * 16 * TT * 4 + std::max(kRed, kLoraUParts * TT * (rt * 16 + 8) * 2);
+  constexpr int kU = kLoraUParts * TT * (kLoraMaxRank + 8) * 2;
   static std::atomic<int> done[kMaxCachedDevices];
   cudaError_t e = smem_attr_once(k_lora_apply<KC, TS, TO>, kLoraMaxRank * TT * 4 + (kRed > kU ? kRed : kU), done);
   if (e != cudaSuccess) return e;

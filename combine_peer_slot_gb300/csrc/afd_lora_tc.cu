@@ -13,7 +13,7 @@
 // share of a tile computes u anew, from L2 but for the first one's reads, which
 // costs less than meeting.
 //
-// u goes into the second product as two bf16 parts, 16 of its bits.  The sums
+// u goes into the second product as three bf16 parts, all of its bits.  The sums
 // of the first product move from TMEM to registers every eight stages, since
 // the tensor cores' fp32 sums cut where they should round.
 //
@@ -46,7 +46,7 @@ constexpr int kRowsBytes = TT * kLoraRowBytes;  // a stage's rows
 constexpr int kFlush = 8;                       // stages between two moves of u's sums
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-constexpr int RP = 64, KU = OutParts<uint16_t>::kParts;  // ranks of a part, padded; parts
+constexpr int RP = 64, KU = kLoraUParts;  // ranks of a part, padded; parts
 constexpr int kStageBytes = kRowsBytes + RP * kLoraRowBytes;
 constexpr int kUBytes = KU * kRowsBytes;        // u's parts, rows of 128 bytes
 constexpr int S = (224 * 1024 - kUBytes) / kStageBytes;  // stages

@@ -38,13 +38,14 @@ constexpr int kFlush = 4;                     // stages between two moves of the
 constexpr int kXStride = 80;                  // bytes, of a row's 32 values of one part
 
 // stages, and CTAs an SM holds
-template <int KC, int KS, int KU>
+template <int KC, int KS>
 struct Form {
   static constexpr int kStages = KC == 1 ? 6 : KC == 2 ? 5 : KC == 4 ? 3 : 4;
   static constexpr int kCtas = KC <= 4 ? 3 : 1;
   static constexpr int kStageBytes = kTileBytes + KC * 16 * kRowBytes;
   static constexpr int kUStride = KC * 16 + 4;
   // u's sums; its parts take their place where a warp cannot hold them
+  static constexpr int KU = kLoraUParts;
   static constexpr bool kHold = KC * KU <= 8;
   static constexpr int kPStride = KC * 16 + 8;
   static constexpr int kUBytes = kHold || TT * kUStride * 4 > KU * TT * kPStride * 2 ? TT * kUStride * 4 : KU * TT * kPStride * 2;
@@ -157,8 +158,8 @@ __device__ __forceinline__ void slow_store(const LoraArgs& a, uint32_t st, const
 // 1184 to 1032 columns 18.7 and 21.4; of 1181 to 1031 columns 43).
 template <int KC, typename TS, typename TO, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const __grid_constant__ LoraArgs a) {
-  constexpr int kS = LoraSrc<TS>::kParts, kU = OutParts<TO>::kParts;
-  typedef Form<KC, kS, kU> F;
+  constexpr int kS = LoraSrc<TS>::kParts, kU = kLoraUParts;
+  typedef Form<KC, kS> F;
   constexpr int S = F::kStages;
   constexpr int KB = kRowBytes / (int)sizeof(TS), CB = kRowBytes / (int)sizeof(TO);  // columns of a stage
   constexpr int NT = CB / 16;                                                          // a warp's column tiles
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
 
 template <int KC, typename TS, typename TO, bool WHOLE>
 cudaError_t run(const LaunchCtx& lc, const LoraArgs& a) {
-  typedef Form<KC, LoraSrc<TS>::kParts, OutParts<TO>::kParts> F;
+  typedef Form<KC, LoraSrc<TS>::kParts> F;
   static std::atomic<int> done[kMaxCachedDevices];
   cudaError_t e = smem_attr_once(k_lora_tiles<KC, TS, TO, WHOLE>, F::kBytes, done);
   if (e != cudaSuccess) return e;

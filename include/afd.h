@@ -818,8 +818,8 @@ int afd_route_backward(const void* logits, int64_t ld, int n_tokens, int logits_
  *   u_t = A[l] x_t,  out_t = base_t + scale[l] B[l]^T u_t,  l = ids[t]
  * A bf16 [n_adapters, rank, K], B bf16 [n_adapters, rank, M], both rank-major
  * and without padding (smaller adapters: zero rows); u is held in fp32 and
- * enters the second product with 16 (out bf16) or 24 (fp32) bits; sums in
- * fp32; out is rounded once.  A row with a NaN or an infinity in it, or an
+ * enters the second product with all its bits; sums in fp32; out is rounded
+ * once.  A row with a NaN or an infinity in it, or an
  * adapter with one, gives values that are not finite in its own rows only.
  * Limits: n_tokens <= 2^24, n_adapters <= 1024, rank <= 128, K and M <= 65536.
  *

@@ -1,0 +1,61 @@
+"""The adapters' calls where their arithmetic and their pipelines reach furthest,
+against 64-bit forms."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from combine_peer_slot_gb300 import afd as A
+from combine_peer_slot_gb300 import runtime as R
+
+U = 2.0 ** -24
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    A.lib()
+
+
+def digits(T, cols, g):
+    """Rows whose first three values h, m, l add up to 24 bits, 8 of them each."""
+    x = torch.zeros(T, cols, device="cuda")
+    for i in range(3):
+        x[:, i] = torch.randint(128, 256, (T,), generator=g, device="cuda").float() / 128 * 2.0 ** (-8 * i)
+    return x
+
+
+def pairs(rank, src, out):
+    """Weights for which even ranks hold h + m + l, odd ones h + m, and each output is one even rank less the next odd one."""
+    w1, w2 = torch.zeros(2, rank, src, device="cuda"), torch.zeros(2, rank, out, device="cuda")
+    w1[:, :, :2] = 1
+    w1[:, ::2, 2] = 1
+    p = 2 * (torch.arange(out, device="cuda") % (rank // 2))
+    w2[:, p, torch.arange(out, device="cuda")] = 1
+    w2[:, p + 1, torch.arange(out, device="cuda")] = -1
+    return w1.to(BF), w2.to(BF)
+
+
+@pytest.mark.parametrize("T,rank", [(40, 8), (40, 60), (1600, 16), (1600, 32), (1600, 48), (1600, 64), (1600, 100)])
+@pytest.mark.parametrize("pitch", [64, 63])
+def test_u_keeps_its_bits(T, rank, pitch):
+    """Beside bf16 outputs u enters the second product with all of fp32's bits: the
+    difference of two of its values that differ in the last eight comes out.  Off by
+    at most: the first product's one step, 2 U of terms up to 2.02, for both; the
+    second's three, 2 U of their 4.04 each: under 33 U.  The output's rounding, half
+    a step of under 2^-15: 2^-23."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + rank)
+    ids = torch.randint(0, 2, (T,), generator=g, device="cuda").int()
+    x = torch.zeros(T, pitch, dtype=BF, device="cuda")[:, :56]
+    x.copy_(digits(T, 56, g))
+    low = x[:, 2:3].double()
+    tol = 33 * U + 2.0 ** -23
+    batch = R.LoraBatch(ids, 2)
+    w1, w2 = pairs(rank, 56, 48)
+    y, u = R.lora_apply(batch, x, w1, w2, keep=True)
+    assert y.dtype == BF and ((y.double() - low).abs() <= tol).all()
+    dx = R.lora_backward(batch, torch.zeros(T, 48, dtype=BF, device="cuda"), x, u, w2, w1)[0]
+    assert dx.dtype == BF and ((dx.double() - low).abs() <= tol).all()
