@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(1024) k_balance_finish(const __grid_constant__
   cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = blockIdx.x, s = blockIdx.y;
   const int e = q * 32 + lane;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
   cudaGridDependencySynchronize();
   float v = 0.0f;
   int32_t n = 0;
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(1024) k_balance_finish(const __grid_constant__
   sums[warp][lane] = v;
   cnts[warp][lane] = n;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the CTA that is written to has, too
   if (warp == 0) {
     v = 0.0f;
     n = 0;
