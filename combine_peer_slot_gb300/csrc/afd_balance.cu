@@ -159,10 +159,12 @@ __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
 
 // The exponentials of a row's logits and of its chosen ones (KIDS a lane), each
 // relative to their own largest, and their sums: 0 throughout where all are
-// -inf.  top: the row's largest; chosen far enough below it that their scores
-// are 0 in fp64 too (and route_select's weights with them) count as none.
+// -inf.  top: the row's largest.  Scores that are 0 in fp64 too (and
+// route_select's weights with them) are none: under softmax those of chosen far
+// enough below top, under sigmoid those of logits whose exp(-l) leaves fp64.
+constexpr float kSigmoidNone = -709.78271484375f;  // the largest such fp32 value
 template <int LANES, int KIDS>
-__device__ __forceinline__ void exponentials(const float (&l)[kPer], const float (&cl)[KIDS], bool far_is_none,
+__device__ __forceinline__ void exponentials(const float (&l)[kPer], const float (&cl)[KIDS], int sigmoid,
                                              float (&x)[kPer], float& z, float (&cx)[KIDS], float& cz, float& top) {
   float ctop = -INFINITY;
   top = -INFINITY;
@@ -172,15 +174,16 @@ __device__ __forceinline__ void exponentials(const float (&l)[kPer], const float
   for (int j = 0; j < KIDS; j++) ctop = fmaxf(ctop, cl[j]);
   row_maxima<LANES>(top, ctop);
   z = cz = 0.0f;
+  const float least = sigmoid ? kSigmoidNone : -INFINITY;  // (NaN is above it, and stays)
 #pragma unroll
   for (int i = 0; i < kPer; i++) {
-    x[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
+    x[i] = l[i] <= least ? 0.0f : expf(l[i] - top);
     z += x[i];
   }
-  const bool none = far_is_none && ctop - top < -745.0f;
+  const bool none = !sigmoid && ctop - top < -745.0f;
 #pragma unroll
   for (int j = 0; j < KIDS; j++) {
-    cx[j] = cl[j] == -INFINITY || none ? 0.0f : expf(cl[j] - ctop);
+    cx[j] = cl[j] <= least || none ? 0.0f : expf(cl[j] - ctop);
     cz += cx[j];
   }
   row_sums<LANES>(z, cz);
@@ -189,7 +192,8 @@ __device__ __forceinline__ void exponentials(const float (&l)[kPer], const float
 // A row's shares p, and of its chosen logits cl the scores' shares of the
 // chosen (cs; renorm) or the scores; under sigmoid the 1 - s of both as well.
 // Scores whose sum nears fp32's smallest number come from logits under -60,
-// where s = exp(l) (1 - 1e-26): their shares are the softmax's.
+// where s = exp(l) (1 - 1e-26): their shares are the softmax's, of those that
+// fp64 holds.
 template <int LANES, int KIDS>
 __device__ __forceinline__ void shares(const float (&l)[kPer], const float (&cl)[KIDS], int sigmoid, bool renorm,
                                        float (&p)[kPer], float (&rest)[kPer], float (&cs)[KIDS], float (&crest)[KIDS]) {
@@ -212,7 +216,7 @@ __device__ __forceinline__ void shares(const float (&l)[kPer], const float (&cl)
   }
   if (!sigmoid || __any_sync(0xffffffffu, small || csmall)) {
     float x[kPer], cx[KIDS], xz, cxz, top;
-    exponentials<LANES, KIDS>(l, cl, !sigmoid, x, xz, cx, cxz, top);
+    exponentials<LANES, KIDS>(l, cl, sigmoid, x, xz, cx, cxz, top);
     if (!sigmoid || small) {  // (the warp's other rows keep their sigmoids)
       z = xz;
 #pragma unroll

@@ -778,7 +778,8 @@ int afd_mx4_poll_status(void* cuda_stream);
  *            [seq_offsets[s], seq_offsets[s + 1]), clamped to [0, n_tokens];
  *            NULL: one sequence of all rows (n_seqs 1).  n_seqs <= 65535
  * With p_te the softmax of row t, or s_te / sum_e s_te of its sigmoids (0
- * throughout a row whose logits are all -inf), n_s the rows of sequence s:
+ * throughout a row whose logits are all -inf, or whose sigmoids are 0 in fp64:
+ * logits under -709.78, as in afd_route_select), n_s the rows of sequence s:
  *   counts   device int32 [n_seqs, num_experts] out: the choices of e in s
  *   loss     device fp32 [n_seqs] out: num_experts / (topk n_s^2) *
  *            sum_e counts[s, e] * sum_{t in s} p_te: 1 for an even gate, 0

@@ -19,6 +19,46 @@ def _cuda():
     A.lib()
 
 
+def test_sigmoids_below_64_bits():
+    """Where exp(-l) leaves fp64, from -709.79 on, a sigmoid is 0, as in route_select:
+    no share, no weight, no gradient; logits above that keep theirs beside it."""
+    E, k = 48, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    l = torch.randn(24, E, generator=g, device="cuda")
+    lowest = torch.finfo(torch.float32).min
+    far = [-1e30, lowest, -709.8, -720.0, -760.0, -1e4]
+    for i, v in enumerate(far):
+        l[i] = v
+        l[6 + i, ::3] = v                       # some
+        l[12 + i] = v
+        l[12 + i, 7] = -650.0                   # all but one, which is far down itself
+        l[18 + i] = -709.7 + 0.05 * l[18 + i]   # around the border
+        l[18 + i, 5:9] = v
+    off = torch.arange(25, device="cuda").int()
+    for same in (False, True):  # the choice, and one of the far entries alone
+        ids, w = R.route_select(l, k, score="sigmoid", renorm=True)
+        if same:
+            ids = (torch.arange(k, device="cuda").int() + 5).repeat(24, 1)
+            w = ref.weights(l.double(), ids, "sigmoid", True, 1.0)
+        loss, counts = R.balance_loss(l, ids, score="sigmoid", seq_offsets=off)
+        want, _ = ref.balance(l, ids, "sigmoid", off.tolist())
+        assert ((loss.double() - want).abs() <= 100 * U * want).all()
+        assert (loss[:6] == 0).all()
+        dw = torch.randn(24, k, generator=g, device="cuda")
+        d_loss = torch.randn(24, generator=g, device="cuda")
+        for renorm in (False, True):
+            for kw in (dict(d_weights=dw), dict(counts=counts, d_loss=d_loss), dict(d_weights=dw, counts=counts, d_loss=d_loss)):
+                d = R.route_backward(l, ids, score="sigmoid", renorm=renorm, **kw, **({"seq_offsets": off} if "counts" in kw else {}))
+                r, size = ref.route_grad(l, ids, "sigmoid", renorm=renorm, **kw, **({"offsets": off.tolist()} if "counts" in kw else {}))
+                # (|l - top| up to 70 where it is not none)
+                assert ((d.double() - r).abs() <= 300 * U * size + 1e-38).all()
+        none = (w == 0).all(1)
+        assert bool(none[:6].all())
+        d = R.route_backward(l, ids, d_weights=dw, score="sigmoid", renorm=True)
+        assert (d[none] == 0).all()
+
+
 @pytest.mark.parametrize("E", [33, 64, 100, 129, 256])
 def test_many_rows_from_several_streams(E):
     """Losses of many rows, whose sums clusters of blocks finish, asked for again and
