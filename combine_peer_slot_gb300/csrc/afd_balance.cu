@@ -257,13 +257,18 @@ __device__ __forceinline__ float loss_of(const GateArgs& a, int rows, double dot
 }
 
 // A sequence's rows are shared by `chunks` blocks of kWarps warps.  One chunk:
-// its loss at once; else a block's share of the sums.  Sums of p: a lane's fp32
-// chain over its rows, then the warp's rows and the warps in order.  Counts
-// are whole numbers, so their order is free.
+// its loss at once; else a block's share of the sums.  Sums of p: a lane's rows
+// kRun at a time in fp32, the runs in fp64 (one fp32 chain over all rows of a
+// sequence that many others leave one block was 1e-4 off), then the warp's rows
+// and the warps in order.  Counts are whole numbers, so their order is free.
+// (The runs' sums stay in shared memory: as registers they halve the blocks an SM
+// holds, or spill 100 bytes a thread.)
+constexpr int kRun = 64;
 template <typename LT, int LANES>
 __global__ void __launch_bounds__(kWarps * 32) k_balance(const __grid_constant__ GateArgs a) {
   constexpr int kE = LANES * kPer, kAtOnce = 32 / LANES, kIds = LANES < 16 ? 2 : 1;
-  __shared__ float sums[kWarps][kE];
+  __shared__ double runs[kPer][kWarps * 32];                     // each thread's own
+  float(*sums)[kE] = reinterpret_cast<float(*)[kE]>(&runs[0][0]);  // [kWarps], in their place afterwards
   __shared__ int32_t cnt[kE];
   __shared__ double dots[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
@@ -306,7 +311,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < kIds; j++)
       if (id[j] >= 0 && id[j] < a.E) atomicAdd(&cnt[id[j]], 1);
+    if (i % kRun == kRun - 1) {
+#pragma unroll
+      for (int x = 0; x < kPer; x++) {
+        runs[x][threadIdx.x] = (i == kRun - 1 ? 0.0 : runs[x][threadIdx.x]) + (double)acc[x];
+        acc[x] = 0.0f;
+      }
+    }
   }
+  if (passes >= kRun) {
+#pragma unroll
+    for (int x = 0; x < kPer; x++) acc[x] = (float)(runs[x][threadIdx.x] + (double)acc[x]);
+  }
+  __syncthreads();
 #pragma unroll
   for (int x = 0; x < kPer; x++) {
 #pragma unroll

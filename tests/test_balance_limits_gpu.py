@@ -59,6 +59,28 @@ def test_sigmoids_below_64_bits():
         assert (d[none] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,T", [(256, 400000), (60, 700000)])
+def test_one_long_sequence_among_many(score, E, T):
+    """Nearly all rows in one of 400 sequences: however many rows a block adds up, its
+    sums are off by at most 64 U of a row's shares (the exponential and its quotient), 64
+    terms in fp32, and what warps and lanes add: 21."""
+    S = 400
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E)
+    row = torch.randn(1, E, generator=g, device="cuda")
+    l = row.repeat(T, 1)  # (equal rows: roundings of one sign, as an even gate's)
+    ids = torch.full((T, 1), 3, dtype=torch.int32, device="cuda")
+    off = torch.cat([torch.arange(200), torch.arange(T - 200, T + 1)]).int().cuda()
+    assert off.numel() == S + 1
+    loss, counts = R.balance_loss(l, ids, score=score, seq_offsets=off)
+    _, p = ref.shares(row.double(), score)
+    want = E * p[0, 3]  # of every sequence: E / n^2 n n p
+    assert int(counts.sum()) == T and int(counts[199, 3]) == T - 399
+    worst = float(((loss.double() - want) / want).abs().max())
+    assert worst <= (64 + 64 + 21) * U, worst / U
+
+
 @pytest.mark.parametrize("E", [33, 64, 100, 129, 256])
 def test_many_rows_from_several_streams(E):
     """Losses of many rows, whose sums clusters of blocks finish, asked for again and
