@@ -8,7 +8,8 @@
 // loading its operands of the tensor cores' products straight from
 // global memory: the k order inside a chunk is free as long as both operands
 // agree, so a lane takes 16 neighbouring bytes for its four k pairs.  The
-// sums over the warps go through shared memory, those over the CTAs through
+// sums over the warps go through shared memory (65536 fp32 columns by one warp in
+// one chain of MMAs left u 1440 half steps off), those over the CTAs through
 // distributed shared memory, always in the same order.  Then the warps share
 // the columns of out in blocks of 64.  u enters the second product as
 // three bf16 parts, which keep its 24 bits.
@@ -24,6 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 constexpr int kWarps = 8, TT = 16, kRedStride = TT + 8;
+constexpr int kMove = 8;  // chunks between two moves of the sums
 
 // eight neighbouring outputs: base + v, rounded once
 template <typename TO>
@@ -120,6 +122,26 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
       for (int j = 0; j < kCols; j++)
 #pragma unroll
         for (int x = 0; x < 4; x++) acc[i][j][x] = 0.0f;
+    // The tensor cores' sums cut where they should round: every kMove chunks they
+    // move to this warp's place in shared memory, each lane its own.
+    float* mine = red + warp * kRows * 16 * kRedStride;
+    bool moved = false;
+    auto move = [&]() {
+#pragma unroll
+      for (int i = 0; i < kRows; i++)
+#pragma unroll
+        for (int j = 0; j < kCols; j++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            float2* d = reinterpret_cast<float2*>(mine + (i * 16 + h * 8 + g) * kRedStride + j * 8 + 2 * c);
+            float2 v = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+            if (moved) v = make_float2(d->x + v.x, d->y + v.y);
+            *d = v;
+            acc[i][j][2 * h] = acc[i][j][2 * h + 1] = 0.0f;
+          }
+      moved = true;
+    };
+    int held = 0;
     for (int ch = q * kWarps + warp; ch < chunks; ch += C * kWarps) {
       const int k0 = ch * 32 + c * 8;
       uint4 w[kRows][2];
@@ -144,16 +166,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
             mma_16x8x16(acc[i][j], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, x[p].z, x[p].w);
           }
       }
-    }
-    float* mine = red + warp * kRows * 16 * kRedStride;
-#pragma unroll
-    for (int i = 0; i < kRows; i++)
-#pragma unroll
-      for (int j = 0; j < kCols; j++) {
-        float* d = mine + (i * 16 + g) * kRedStride + j * 8 + 2 * c;
-        *reinterpret_cast<float2*>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(d + 8 * kRedStride) = make_float2(acc[i][j][2], acc[i][j][3]);
+      if (++held == kMove) {
+        move();
+        held = 0;
       }
+    }
+    move();
     __syncthreads();
     for (int e = threadIdx.x; e < kRows * 16 * kCols * 8; e += kWarps * 32) {
       const int r = e / (kCols * 8), i = e % (kCols * 8);
