@@ -642,6 +642,10 @@ extern "C" int afd_balance_loss(const void* logits, int64_t ld, int n_tokens, in
       misaligned(loss, 4) || misaligned(counts, 4) || (need && (!workspace || misaligned(workspace, 256))))
     return AFD_ERR_ARG;
   if (need > workspace_bytes) return AFD_ERR_CAPACITY;
+  const int64_t T = n_tokens, E = num_experts;
+  if (!apart({run_of(loss, n_seqs * 4), run_of(counts, n_seqs * E * 4), run_of(workspace, need)},
+             {{logits, ld * (int64_t)esz, E * (int64_t)esz, T}, run_of(ids, T * topk * 4), run_of(seq_offsets, (n_seqs + 1) * 4)}))
+    return AFD_ERR_ARG;
   const int rc = check_device_ptrs({n_tokens ? logits : nullptr, n_tokens ? ids : nullptr, seq_offsets, loss, counts,
                                     need ? workspace : nullptr});
   if (rc) return rc;
@@ -670,6 +674,13 @@ extern "C" int afd_route_backward(const void* logits, int64_t ld, int n_tokens, 
   const uintptr_t esz = logits_dtype == AFD_DTYPE_F32 ? 4 : 2;
   if (!logits || !d_logits || (d_weights && !ids) || misaligned(logits, esz) || misaligned(d_logits, esz) ||
       misaligned(ids, 4) || misaligned(d_weights, 4) || misaligned(counts, 4) || misaligned(d_loss, 4))
+    return AFD_ERR_ARG;
+  const int64_t T = n_tokens, width = num_experts * (int64_t)esz;
+  const bool in_place = d_logits == logits && (ldd == ld || T == 1);
+  if (!apart({{d_logits, ldd * (int64_t)esz, width, T}},
+             {{in_place ? nullptr : logits, ld * (int64_t)esz, width, T}, run_of(d_weights ? ids : nullptr, T * topk * 4),
+              run_of(d_weights, T * topk * 4), run_of(seq_offsets, (n_seqs + 1) * 4),
+              run_of(counts, (int64_t)n_seqs * num_experts * 4), run_of(d_loss, n_seqs * 4)}))
     return AFD_ERR_ARG;
   const int rc = check_device_ptrs({logits, ids, d_weights, seq_offsets, counts, d_loss, d_logits});
   if (rc) return rc;

@@ -37,6 +37,49 @@ inline int check_device_ptrs(std::initializer_list<const void*> ptrs) {
   return AFD_OK;
 }
 
+// Rows of a buffer in bytes: n of `width`, `pitch` apart (a run: one row).
+struct RowSpan {
+  const void* at;
+  int64_t pitch, width, n;
+};
+inline RowSpan run_of(const void* p, int64_t bytes) { return {p, bytes, bytes, bytes ? 1 : 0}; }
+// whether two buffers (NULL: none) share a byte; rows of one may lie between the other's
+inline bool rows_meet(const RowSpan& a, const RowSpan& b) {
+  if (!a.at || !b.at || a.n <= 0 || b.n <= 0) return false;
+  const int64_t off = (int64_t)((intptr_t)b.at - (intptr_t)a.at);  // b's first row from a's
+  if (off >= (a.n - 1) * a.pitch + a.width || -off >= (b.n - 1) * b.pitch + b.width) return false;
+  if (a.n == 1 && b.n == 1) return true;
+  if (a.pitch == b.pitch) {
+    // rows i of a, j of b meet where off - a.width < (i - j) pitch < off + b.width
+    int64_t m = (off - a.width) / a.pitch;
+    while (m * a.pitch <= off - a.width) m++;
+    while ((m - 1) * a.pitch > off - a.width) m--;
+    m = std::max(m, 1 - b.n);
+    return m < a.n && m * a.pitch < off + b.width;
+  }
+  // (pitches differ only for rows of two buffers that a caller has interleaved by hand)
+  const RowSpan &few = a.n <= b.n ? a : b, &many = a.n <= b.n ? b : a;
+  const int64_t lead = &few == &a ? off : -off;  // many's first row from few's
+  for (int64_t i = 0; i < few.n; i++) {
+    const int64_t lo = i * few.pitch - lead, hi = lo + few.width;  // row i from many's first row
+    if (hi <= 0) continue;
+    const int64_t j = std::max<int64_t>(0, (lo - many.width) / many.pitch);
+    for (int64_t k = j; k < many.n && k * many.pitch < hi; k++)
+      if (k * many.pitch + many.width > lo) return true;
+  }
+  return false;
+}
+// what is written shares no byte with what is read, nor with what else is written
+inline bool apart(std::initializer_list<RowSpan> written, std::initializer_list<RowSpan> read) {
+  for (const RowSpan* w = written.begin(); w != written.end(); w++) {
+    for (const RowSpan* o = w + 1; o != written.end(); o++)
+      if (rows_meet(*w, *o)) return false;
+    for (const RowSpan& r : read)
+      if (rows_meet(*w, r)) return false;
+  }
+  return true;
+}
+
 // Launch settings the launchers cache (a kernel's shared-memory attribute,
 // occupancy figures) are per device: a process may hold contexts on several.
 constexpr int kMaxCachedDevices = 64;

@@ -172,6 +172,7 @@ extern "C" int afd_lora_plan(const int32_t* ids, int64_t n_tokens, int n_adapter
     return AFD_ERR_ARG;
   const LoraPlan p = lora_plan_at(plan, n_tokens, n_adapters);
   if (plan_bytes < p.bytes) return AFD_ERR_CAPACITY;
+  if (!apart({run_of(plan, p.bytes)}, {run_of(ids, n_tokens * 4)})) return AFD_ERR_ARG;
   const int rc = check_device_ptrs({n_tokens ? ids : nullptr, plan});
   if (rc) return rc;
   const LaunchCtx lc{reinterpret_cast<cudaStream_t>(cuda_stream), 0, nullptr};
@@ -197,7 +198,12 @@ extern "C" int afd_lora_apply(const void* plan, int64_t n_tokens, int n_adapters
   if (n_tokens == 0) return AFD_OK;
   if (!plan || off_by(plan, 256) || !x || !a || !b || !out || off_by(x, size_of(x_dtype)) || off_by(a, 2) ||
       off_by(b, 2) || off_by(scale, 4) || off_by(base, size_of(y_dtype)) || off_by(out, size_of(y_dtype)) ||
-      off_by(u, 4) || (base == out && ldb != ldo) || x == out)
+      off_by(u, 4) || (base == out && ldb != ldo))
+    return AFD_ERR_ARG;
+  const int64_t xs = size_of(x_dtype), ys = size_of(y_dtype), T = n_tokens, L = n_adapters;
+  if (!apart({{out, ldo * ys, M * ys, T}, run_of(u, T * rank * 4)},
+             {run_of(plan, afd_lora_plan_bytes(T, n_adapters)), {x, ldx * xs, K * xs, T}, run_of(a, L * rank * K * 2),
+              run_of(b, L * rank * M * 2), run_of(scale, L * 4), {base == out ? nullptr : base, ldb * ys, M * ys, T}}))
     return AFD_ERR_ARG;
   const int rc = check_device_ptrs({plan, x, a, b, scale, base, out, u});
   if (rc) return rc;
@@ -248,9 +254,15 @@ extern "C" int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapt
       (!plan || off_by(plan, 256) || !x || !dy || !u || !a || !b || !dx || !workspace || off_by(workspace, 256) ||
        off_by(x, size_of(x_dtype)) || off_by(dy, size_of(y_dtype)) || off_by(u, 4) || off_by(a, 2) || off_by(b, 2) ||
        off_by(scale, 4) || off_by(d_base, size_of(x_dtype)) || off_by(dx, size_of(x_dtype)) ||
-       (d_base == dx && ldb != ldd) || x == dx || dy == dx))
+       (d_base == dx && ldb != ldd)))
     return AFD_ERR_ARG;
   if (workspace_bytes < need) return AFD_ERR_CAPACITY;
+  const int64_t xs = size_of(x_dtype), ys = size_of(y_dtype), T = n_tokens, L = n_adapters;
+  if (!apart({{dx, ldd * xs, K * xs, T}, run_of(da, L * rank * K * 4), run_of(db, L * rank * M * 4), run_of(workspace, T ? need : 0)},
+             {run_of(plan, T ? afd_lora_plan_bytes(T, n_adapters) : 0), {x, ldx * xs, K * xs, T}, {dy, ldy * ys, M * ys, T},
+              run_of(u, T * rank * 4), run_of(a, T ? L * rank * K * 2 : 0), run_of(b, T ? L * rank * M * 2 : 0),
+              run_of(scale, T ? L * 4 : 0), {d_base == dx ? nullptr : d_base, ldb * xs, K * xs, T}}))
+    return AFD_ERR_ARG;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(cuda_stream);
   if (n_tokens == 0) {  // no rows: no gradient
     const int rc = check_device_ptrs({da, db});

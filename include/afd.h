@@ -805,7 +805,9 @@ int afd_balance_loss(const void* logits, int64_t ld, int n_tokens, int logits_dt
  *              seq_offsets; rows outside every sequence get none
  * The counts and the choice are constants of the gradient.  A row with a NaN
  * (or, under softmax, +inf) in its logits gets NaN throughout.  d_logits may
- * be logits itself (same pitch).  Errors, capture: as afd_balance_loss. */
+ * be logits itself (same pitch); any other overlap with an input, as any of
+ * afd_balance_loss's outputs or workspace, is AFD_ERR_ARG.  Errors, capture: as
+ * afd_balance_loss. */
 int afd_route_backward(const void* logits, int64_t ld, int n_tokens, int logits_dtype,
                        const int32_t* ids, int num_experts, int topk, int score, int renorm,
                        float routed_scaling, const float* d_weights, const int32_t* seq_offsets,
@@ -839,8 +841,9 @@ int afd_lora_plan(const int32_t* ids, int64_t n_tokens, int n_adapters, void* pl
  *   base     device, y_dtype [n_tokens, M], row pitch ldb: the shared
  *            projection's rows; NULL: zeros; may be out itself (same pitch),
  *            whose rows without an adapter are then left as they are
- *   out      device, y_dtype [n_tokens, M], row pitch ldo; no other overlap
- *            of what is written with what is read
+ *   out      device, y_dtype [n_tokens, M], row pitch ldo; what is written
+ *            shares no other byte with what is read or written, else
+ *            AFD_ERR_ARG (rows may lie between another buffer's)
  *   u        device fp32 [n_tokens, rank] out, or NULL: kept for
  *            afd_lora_backward; 0 for rows without an adapter
  * Any pitch and element alignment; rows of whole 16 bytes with K % 8 == 0 and
