@@ -1536,6 +1536,8 @@ int afd_debug_bounds(afd_ctx* ctx, int32_t* site, int64_t* index, int64_t* limit
 int afd_debug_plant(afd_ctx* ctx, int32_t site) {
 #ifdef AFD_DEBUG_BOUNDS
   if (!ctx && site == AFD_DBG_MX4_WAIT) return mx4_plant_error();
+  if (!ctx && site == AFD_DBG_LORA_WAIT) return lora_tc_plant_error();
+  if (!ctx && site == AFD_DBG_LORA_WGRAD_WAIT) return lora_plant_error();
   if (!ctx || site < 0 || site >= AFD_DBG_NUM_SITES) return AFD_ERR_ARG;
   const int64_t rec[5] = {0, 0, 0, 0, site};
   if (cuda_fail(cudaStreamSynchronize(ctx->stream), "stream sync") ||

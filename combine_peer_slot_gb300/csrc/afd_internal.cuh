@@ -80,6 +80,13 @@ inline bool apart(std::initializer_list<RowSpan> written, std::initializer_list<
   return true;
 }
 
+#ifdef AFD_DEBUG_BOUNDS
+// each counts one wait that gave up as the adapters' products (afd_lora_tc.cu)
+// and their weight gradients (afd_lora_wgrad.cu) do
+int lora_tc_plant_error();
+int lora_plant_error();
+#endif
+
 // Launch settings the launchers cache (a kernel's shared-memory attribute,
 // occupancy figures) are per device: a process may hold contexts on several.
 constexpr int kMaxCachedDevices = 64;

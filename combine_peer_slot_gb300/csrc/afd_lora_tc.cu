@@ -446,3 +446,15 @@ cudaError_t launch_lora_tc(const LaunchCtx& lc, const LoraArgs& a) {
 cudaError_t lora_tc_error_count(uint32_t* n, cudaStream_t stream) {
   return cudaMemcpyFromSymbolAsync(n, g_errors, sizeof *n, 0, cudaMemcpyDeviceToHost, stream);
 }
+
+#ifdef AFD_DEBUG_BOUNDS
+int lora_tc_plant_error() {
+  uint32_t n = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&n, g_errors, sizeof n) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_errors, &(++n), sizeof n) != cudaSuccess) {
+    cudaGetLastError();
+    return AFD_ERR_CUDA;
+  }
+  return AFD_OK;
+}
+#endif

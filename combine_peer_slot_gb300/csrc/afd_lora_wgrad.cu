@@ -388,3 +388,15 @@ cudaError_t launch_lora_wgrad(LaunchCtx lc, const LoraWgradArgs& a) {
 cudaError_t lora_error_count(uint32_t* n, cudaStream_t stream) {
   return cudaMemcpyFromSymbolAsync(n, g_lora_errors, sizeof *n, 0, cudaMemcpyDeviceToHost, stream);
 }
+
+#ifdef AFD_DEBUG_BOUNDS
+int lora_plant_error() {
+  uint32_t n = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&n, g_lora_errors, sizeof n) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_lora_errors, &(++n), sizeof n) != cudaSuccess) {
+    cudaGetLastError();
+    return AFD_ERR_CUDA;
+  }
+  return AFD_OK;
+}
+#endif

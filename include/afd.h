@@ -567,7 +567,9 @@ int afd_check_canaries(afd_ctx* ctx, int* window, int64_t* offset);
  * replaced by 0), sets the step's status to AFD_ERR_BOUNDS and records the
  * first failure: site, index and the bound it broke.  The release build
  * compiles the checks out.  (Expert ids and the slot header's counts and
- * shared indices are checked in both builds.)
+ * shared indices are checked in both builds.)  Calls without a context have no
+ * such checks: what they read is the caller's, and the adapters' plan has to be
+ * afd_lora_plan's for the same n_tokens and n_adapters.
  * afd_debug_bounds synchronises the stream and returns AFD_OK when nothing
  * failed since the context was created or last planted, else AFD_ERR_BOUNDS
  * with *site, *index and *limit (each may be NULL).  afd_debug_plant clears
@@ -583,9 +585,12 @@ int afd_check_canaries(afd_ctx* ctx, int* window, int64_t* offset);
 #define AFD_DBG_SCATTER_INV 5    /* k_scatter_grouped: inv[r] < routed rows */
 #define AFD_DBG_GEMM_OUT 6       /* grouped GEMMs: a unit's last output row < output rows */
 #define AFD_DBG_NUM_SITES 7
-/* planted without a context (ctx NULL): one wait of an MXFP4 product that gave
- * up, for afd_mx4_poll_status */
+/* planted without a context (ctx NULL): one wait that gave up of an MXFP4
+ * product, for afd_mx4_poll_status, of the adapters' products or of their
+ * weight gradients, for afd_lora_poll_status */
 #define AFD_DBG_MX4_WAIT 7
+#define AFD_DBG_LORA_WAIT 8
+#define AFD_DBG_LORA_WGRAD_WAIT 9
 int afd_debug_bounds(afd_ctx* ctx, int32_t* site, int64_t* index, int64_t* limit);
 int afd_debug_plant(afd_ctx* ctx, int32_t site);
 
@@ -877,7 +882,8 @@ int afd_lora_backward(const void* plan, int64_t n_tokens, int n_adapters, const 
 
 /* afd_mx4_poll_status of the adapters' calls: AFD_ERR_TIMEOUT if a bounded wait
  * (2 s) of afd_lora_apply or afd_lora_backward gave up since this thread's last
- * call for this stream. */
+ * call for this stream; their outputs are then incomplete, and the calls
+ * themselves, which do not wait for the device, have returned AFD_OK. */
 int afd_lora_poll_status(void* cuda_stream);
 
 /* Static string for a status code. */
