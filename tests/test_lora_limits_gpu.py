@@ -7,6 +7,7 @@ pytestmark = pytest.mark.gpu
 
 from combine_peer_slot_gb300 import afd as A
 from combine_peer_slot_gb300 import runtime as R
+from tests import test_lora_gpu as form
 
 U = 2.0 ** -24
 BF, F = torch.bfloat16, torch.float32
@@ -59,3 +60,51 @@ def test_u_keeps_its_bits(T, rank, pitch):
     assert y.dtype == BF and ((y.double() - low).abs() <= tol).all()
     dx = R.lora_backward(batch, torch.zeros(T, 48, dtype=BF, device="cuda"), x, u, w2, w1)[0]
     assert dx.dtype == BF and ((dx.double() - low).abs() <= tol).all()
+
+
+# Over 152 tiles, so that a persistent CTA goes from item to item (over 304: twice), over
+# 1024 columns of both products, so that its ring wraps within each and every barrier
+# is waited for; pieces times slabs of the weight gradients likewise, in each of its forms.
+MANY = [(24000, 1096, 1160, 48, 200, "mixed"), (24000, 1160, 1096, 64, 400, "mixed"), (45000, 1096, 600, 64, 4, "runs"),
+        (9000, 520, 2100, 100, 40, "mixed"), (9000, 2100, 520, 128, 12, "mixed"), (20000, 1032, 1096, 16, 300, "mixed"),
+        (20000, 1096, 1032, 32, 90, "mixed")]
+
+
+@pytest.mark.parametrize("T,K,M,rank,L,how", MANY)
+def test_many_items_a_block(T, K, M, rank, L, how):
+    d = form.make(T, K, M, rank, L, BF, BF, how, T + rank)
+    batch, _, u = form.check_apply(d)
+    form.check_backward(d, batch, u)
+    assert A.afd_lora_poll_status(torch.cuda.current_stream().cuda_stream) == A.AFD_OK
+
+
+@pytest.mark.parametrize("T,rank,L", [(12000, 48, 160), (30000, 64, 9), (5000, 100, 60)])
+def test_many_items_repeat(T, rank, L):
+    """Equal bits from call to call, from two streams at a time with one plan, and from a
+    replayed graph."""
+    d = form.make(T, 1032, 712, rank, L, BF, BF, "mixed", rank)
+    batch = R.LoraBatch(d["ids"], L)
+
+    def both():
+        y, u = R.lora_apply(batch, d["x"], d["a"], d["b"], d["base"], scale=d["scale"], keep=True)
+        return (y, u) + R.lora_backward(batch, d["x"], d["dy"], u, d["a"], d["b"], d_base=d["d_base"], scale=d["scale"])
+
+    first = both()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(both())
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for o in got for p, q in zip(o, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(held, first))
+    assert A.afd_lora_poll_status(torch.cuda.current_stream().cuda_stream) == A.AFD_OK
