@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   // the second product's share of this warp; its first columns' weight, which
   // does not depend on u, is asked for while the CTAs meet
   const uint16_t* w2 = reinterpret_cast<const uint16_t*>(a.w2) + (int64_t)t.x * a.R * a.M;
-  const int sub = (t.z + 15) / 16, items = (a.M + 63) / 64 * sub, all = C * kWarps;
+  const int items = (a.M + 63) / 64, all = C * kWarps;
   const int per = (items + all - 1) / all, first = (q * kWarps + warp) * per, groups = (rt + KC - 1) / KC;
   uint4 early[4][1];
   const bool ahead = KC == 1 && first < items;
@@ -195,12 +195,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
 #pragma unroll
     for (int x = 0; x < 4; x++) {
       const int r = 2 * c + (x >> 1) * 8 + (x & 1);
-      load_eight<uint16_t>(w2 + (int64_t)r * a.M, first / sub * 64 + g * 8, r < a.R ? a.M : 0, vm, early[x]);
+      load_eight<uint16_t>(w2 + (int64_t)r * a.M, first * 64 + g * 8, r < a.R ? a.M : 0, vm, early[x]);
     }
-    const int i = first % sub * 16 + lane / 2;  // and the rows of base
+    const int i = lane / 2;  // and the rows of base
     if (a.base && i < t.z)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TO*>(a.base) + (int64_t)order[i] * a.ldb +
-                                                    min(first / sub * 64 + (lane & 1) * 32, a.M - 1)));
+                                                    min(first * 64 + (lane & 1) * 32, a.M - 1)));
   }
   cluster.sync();
   for (int e = threadIdx.x; e < rt * 16 * TT; e += kWarps * 32) {
@@ -231,39 +231,35 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
   cluster.sync();  // (no CTA's sums are read after this)
   const float scale = a.scale ? a.scale[t.x] : 1.0f;
   uint32_t b[KC][8][2];
-  int held = -1;
   for (int it = first; it < min(first + per, items); it++) {
-    const int m0 = it / sub * 64, s0 = it % sub * 16;
+    const int m0 = it * 64;
     float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
       for (int x = 0; x < 4; x++) acc[i][x] = 0.0f;
     for (int gr = 0; gr < groups; gr++) {
-      if (groups > 1 || held != m0) {
-        held = m0;
 #pragma unroll
-        for (int kc = 0; kc < KC; kc++) {
-          uint4 v[4][1];
-          if (KC == 1 && it == first) {
+      for (int kc = 0; kc < KC; kc++) {
+        uint4 v[4][1];
+        if (KC == 1 && it == first) {
 #pragma unroll
-            for (int x = 0; x < 4; x++) v[x][0] = early[x][0];
-          } else {
+          for (int x = 0; x < 4; x++) v[x][0] = early[x][0];
+        } else {
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
-              const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
-              load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, vm, v[x]);
-            }
+          for (int x = 0; x < 4; x++) {
+            const int r = (gr * KC + kc) * 16 + 2 * c + (x >> 1) * 8 + (x & 1);
+            load_eight<uint16_t>(w2 + (int64_t)r * a.M, m0 + g * 8, r < a.R ? a.M : 0, vm, v[x]);
           }
-          pair_rows(v[0][0], v[1][0], v[2][0], v[3][0], b[kc]);
         }
+        pair_rows(v[0][0], v[1][0], v[2][0], v[3][0], b[kc]);
       }
 #pragma unroll
       for (int kc = 0; kc < KC; kc++) {
         if (gr * KC + kc >= rt) break;
 #pragma unroll
         for (int p = kU - 1; p >= 0; p--) {
-          const uint16_t* u0 = us + (p * TT + s0 + g) * ustr + (gr * KC + kc) * 16 + 2 * c;
+          const uint16_t* u0 = us + (p * TT + g) * ustr + (gr * KC + kc) * 16 + 2 * c;
           const uint16_t* u1 = u0 + 8 * ustr;
           const uint32_t a0 = *reinterpret_cast<const uint32_t*>(u0), a1 = *reinterpret_cast<const uint32_t*>(u1);
           const uint32_t a2 = *reinterpret_cast<const uint32_t*>(u0 + 8), a3 = *reinterpret_cast<const uint32_t*>(u1 + 8);
@@ -274,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_lora_apply(const __grid_constan
     }
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const int i = s0 + g + h * 8;
+      const int i = g + h * 8;
       if (i >= t.z) continue;
       const int64_t row = order[i];
       const TO* br = a.base ? reinterpret_cast<const TO*>(a.base) + row * a.ldb : nullptr;
