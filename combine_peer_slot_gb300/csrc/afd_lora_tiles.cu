@@ -41,17 +41,23 @@ constexpr int kXStride = 80;                  // bytes, of a row's 32 values of 
 template <int KC, int KS>
 struct Form {
   static constexpr int kStages = KC == 1 ? 6 : KC == 2 ? 5 : KC == 4 ? 3 : 4;
-  static constexpr int kCtas = KC <= 4 ? 3 : 1;
   static constexpr int kStageBytes = kTileBytes + KC * 16 * kRowBytes;
   static constexpr int kUStride = KC * 16 + 4;
   // u's sums; its parts take their place where a warp cannot hold them
   static constexpr int KU = kLoraUParts;
   static constexpr bool kHold = KC * KU <= 8;
-  static constexpr int kPStride = KC * 16 + 8;
-  static constexpr int kUBytes = kHold || TT * kUStride * 4 > KU * TT * kPStride * 2 ? TT * kUStride * 4 : KU * TT * kPStride * 2;
+  // Of a row's part, its 16-byte chunks swapped as in chunk_at: padded instead,
+  // ranks of 33 to 64 left two CTAs an SM (13312 rows of 2048 to 2816 fp32 outputs
+  // 140 us, now 110; bf16 rows of 2049 to 2817 elements' pitch 207, now 127).
+  static constexpr int kPBytes = KC * 32;
+  static constexpr int kUBytes = kHold || TT * kUStride * 4 > KU * TT * kPBytes ? TT * kUStride * 4 : KU * TT * kPBytes;
   // an fp32 stage's rows as bf16 parts
   static constexpr int kXBytes = KS > 1 ? KS * TT * kXStride : 0;
   static constexpr int kBytes = kStages * kStageBytes + kUBytes + kXBytes;
+  // An SM has 228 KB, of which a CTA takes 2 besides (fp32 rows: two CTAs; taken
+  // for three in the clusters' size, 4000 rows of 2048 to 2816 fp32 columns took 49
+  // us at rank 16 and 60 at 32, where they take 39 and 45).
+  static constexpr int kCtas = KC <= 4 ? std::min(3, 228 * 1024 / (kBytes + 2048)) : 1;
 };
 
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
   if (kHold) {
 #pragma unroll
     for (int ks = 0; ks < KC; ks++) operand(ks, held[kHold ? ks : 0]);
-  } else {  // as parts [kU][TT][kPStride], in the sums' place
+  } else {  // as parts [kU][TT] of kPBytes, in the sums' place
     constexpr int kMine = TT * KC * 8 / kThreads;
     float2 v[kMine];
 #pragma unroll
@@ -400,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
       split_pair<kU>(v[i], p);
 #pragma unroll
       for (int y = 0; y < kU; y++) {
-        const uint32_t to = us + ((y * TT + e / (KC * 8)) * F::kPStride + e % (KC * 8) * 2) * 2;
+        const int r = e / (KC * 8), col = e % (KC * 8) * 2;
+        const uint32_t to = us + (y * TT + r) * F::kPBytes + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2;
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(p[y]) : "memory");
       }
     }
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const 
       if (!kHold) {
 #pragma unroll
         for (int y = 0; y < kU; y++)
-          ldsm4(us + ((y * TT + wt * 16 + (lane & 15)) * F::kPStride + ks * 16 + (lane >> 4) * 8) * 2, held[0][y]);
+          ldsm4(us + (y * TT + wt * 16 + (lane & 15)) * F::kPBytes + (((ks * 2 + (lane >> 4)) ^ (lane & 7)) << 4), held[0][y]);
       }
       uint32_t(&u)[kU][4] = held[kHold ? ks : 0];
 #pragma unroll
