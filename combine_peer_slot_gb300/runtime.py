@@ -610,10 +610,10 @@ def route_backward(logits, ids, d_weights=None, score="softmax", renorm=False, r
     """afd_route_backward: the gradient of logits [T, E] (in their dtype) from
     that of route_select's weights (d_weights fp32 [T, topk]) and that of
     balance_loss's loss (d_loss fp32 [S], with its counts); either may be
-    left out."""
+    left out, ids (None) where both are."""
     h = _host or _get()
-    if ids is None and d_weights is not None:
-        _bad("d_weights without ids")
+    if ids is None and (d_weights is not None or counts is not None):
+        _bad("d_weights or counts without ids (whose columns are the loss's topk)")
     if (counts is None) != (d_loss is None):
         _bad("counts and d_loss: both or neither")
     T, E, topk, code, kind, ld, off, seqs = _gate_inputs(h, logits, ids, score, seq_offsets)

@@ -804,7 +804,8 @@ int afd_balance_loss(const void* logits, int64_t ld, int n_tokens, int logits_dt
  * whole: the sum of two gradients, each left out where its inputs are NULL.
  *   d_weights  device fp32 [n_tokens, topk]: the gradient with respect to the
  *              weights that afd_route_select returned for these logits, ids,
- *              score, renorm and routed_scaling (ids may be NULL without it)
+ *              score, renorm and routed_scaling (ids may be NULL without it;
+ *              topk is the loss's all the same)
  *   counts, d_loss  both or neither: afd_balance_loss's counts and the
  *              gradient with respect to its loss [n_seqs], with the same
  *              seq_offsets; rows outside every sequence get none
