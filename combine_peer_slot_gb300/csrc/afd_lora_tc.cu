@@ -425,11 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_lora_tc(const __grid_constant__
 
 }  // namespace
 
-// Ranks of 33 to 64 only: microseconds for 2048 to 2816 columns, 8 adapters, this
-// kernel and afd_lora_tiles.cu's, by rows: rank 64: 1100 25 / 28, 4000 31 / 35,
-// 13312 53 / 70; rank 32: 1100 23 / 18, 4000 27 / 25, 13312 49 / 52; rank 16:
-// 1100 23 / 16, 4000 25 / 23, 13312 47 / 47.  fp32 outputs, which are logits of
-// few columns, gained nothing from it either.
+// Ranks of 33 to 64 only.  Microseconds, this kernel / afd_lora_tiles.cu's, two
+// batches in turn (so that rows come from memory): 2048 to 2816 columns, 8
+// adapters, rank 64: 1100 rows 25 / 23, 4000 31 / 35, 13312 57 / 76; 300 adapters:
+// 4000 31 / 61, 400: 13312 61 / 96.  Narrow: 13312 rows of 64 columns 12 / 18, of
+// 512 20 / 32; 4000 of 64 to 512 12 / 15; the other way, by 1 to 2 us, up to a few
+// thousand rows of some hundred columns (1100 of 256, 4000 of 128).  Rank 32, 8
+// adapters: 1100 25 / 20, 4000 29 / 44, 13312 51 / 55; rank 16: 25 / 14, 29 / 35, 49 /
+// 47: ranks of 17 to 32 would need their parts for the weight gradients in a layout
+// of their own here, and lose their small batches.  fp32 outputs, which are logits
+// of few columns, gained nothing from it either.
 bool lora_tc_takes(const LoraArgs& a) {
   return !a.src_f32 && !a.out_f32 && a.R > 32 && a.R <= 64 && a.how_src == 16 && a.how_w1 == 16 && a.how_w2 == 16 &&
          a.how_out == 16 && (!a.base || a.how_base == 16) && a.lds < (int64_t(1) << 31) &&

@@ -551,6 +551,11 @@ def mx4_ffn(x, offsets, w13, wd, out_dtype=None, out=None, workspace=None):
 
 
 # ---- expert load, routing gradient, adapters on torch tensors --------------------
+# Values in, values out: autograd records none of these calls, also where a tensor
+# given to them asks for gradients; the gradients are calls of their own
+# (route_backward, lora_backward), for a user's backward pass to make.
+# They return before the device is done: whether a bounded wait of the adapters'
+# kernels gave up is asked of afd.afd_lora_poll_status.
 def _gate_inputs(h, logits, ids, score, seq_offsets):
     """(T, E, topk, dtype code, score code, row pitch, offsets' pointer, sequences)"""
     code, kind = h.code.get(logits.dtype), _SCORES.get(score)

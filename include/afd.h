@@ -788,7 +788,8 @@ int afd_mx4_poll_status(void* cuda_stream);
  *   counts   device int32 [n_seqs, num_experts] out: the choices of e in s
  *   loss     device fp32 [n_seqs] out: num_experts / (topk n_s^2) *
  *            sum_e counts[s, e] * sum_{t in s} p_te: 1 for an even gate, 0
- *            for a sequence without rows, NaN where a row of it has a NaN
+ *            for a sequence without rows, NaN where a row of it has a NaN (or,
+ *            under softmax, +inf)
  * The sums do not depend on timing.  workspace: device, 256-byte aligned, at
  * least afd_balance_workspace bytes (host only; 0 for few rows, -1 for sizes
  * outside the limits), else AFD_ERR_CAPACITY; one call at a time may use it.

@@ -108,3 +108,18 @@ def test_many_items_repeat(T, rank, L):
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(held, first))
     assert A.afd_lora_poll_status(torch.cuda.current_stream().cuda_stream) == A.AFD_OK
+
+
+def test_tensors_that_ask_for_gradients():
+    """Taken as values: equal bits, outputs without a graph, whose gradients are calls of their own."""
+    d = form.make(40, 64, 96, 8, 3, BF, BF, "mixed", 2)
+    batch = R.LoraBatch(d["ids"], 3)
+
+    def both(x, a, b):
+        y, u = R.lora_apply(batch, x, a, b, d["base"], keep=True)
+        return (y, u) + R.lora_backward(batch, x, d["dy"], u, a, b)
+
+    asked = [d[n].clone().requires_grad_() for n in ("x", "a", "b")]
+    got = both(*asked)
+    assert not any(t.requires_grad for t in got)
+    assert all(torch.equal(p, q) for p, q in zip(got, both(d["x"], d["a"], d["b"])))
