@@ -17,19 +17,20 @@
 // of the first product move from TMEM to registers every eight stages, since
 // the tensor cores' fp32 sums cut where they should round.
 //
-// Measured: 13312 rows of 8 adapters, 2816 to 2048 columns, rank 64, 53 us, 3.6
-// TB/s of what they have to move; afd_lora_tiles.cu's takes 64.  A CTA's first
+// Measured: 13312 rows of 8 adapters, 2816 to 2048 columns, rank 64, 56 us, 3.4
+// TB/s of what they have to move; afd_lora_tiles.cu's takes 75.  A CTA's first
 // product takes 800 cycles a stage (31 bytes a cycle), half of them waiting for
-// copies; the second 1700, waiting for the sums of earlier blocks to be stored:
-// base in and out out at 2.2 TB/s each over the 110 SMs that have a tile.
-// Before them stand 3 us of dependent reads, between them 2 us in which u goes
-// through registers (96 rows a tile filled all 152 SMs and gained 2 us).  Not
-// kept: sixteen summing warps with four accumulators (no change); gathering by
-// TMA (tile::gather4: 1.5 us a stage); asking L2 for whole rows ahead (12 us
-// slower); each copying warp a part of every stage (0.8 us of barriers and
-// waits for each, whatever the ring's depth); a warp that waits for its last
-// stage's copies and then says so (55 us; each lane's arrival by its copies'
-// end 53; six copying warps, not four, half a microsecond less).
+// copies; the second 1700 (with two parts of u, the third is 3 us of the whole),
+// waiting for the sums of earlier blocks to be stored: base in and out out at 2.2
+// TB/s each over the 110 SMs that have a tile.  Before them stand 3 us of dependent
+// reads, between them 2 us in which u goes through registers (96 rows a tile
+// filled all 152 SMs and gained 2 us).  Not kept, at 53 us with two parts: sixteen
+// summing warps with four accumulators (no change); gathering by TMA
+// (tile::gather4: 1.5 us a stage); asking L2 for whole rows ahead (12 us slower);
+// each copying warp a part of every stage (0.8 us of barriers and waits for each,
+// whatever the ring's depth); a warp that waits for its last stage's copies and
+// then says so (55 us; each lane's arrival by its copies' end 53; six copying
+// warps, not four, half a microsecond less).
 //
 // All waits are bounded; one that gives up is counted (afd_lora_poll_status).
 #include "afd_lora.cuh"

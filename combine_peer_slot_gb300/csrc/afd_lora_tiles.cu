@@ -18,11 +18,11 @@
 // stages the sums move to registers that add with rounding.
 //
 // Measured (8 adapters, rank 16 and 8): 13312 rows, 2048 to 2816 columns bf16,
-// 42 us, 4.9 TB/s of what they have to move (73 % of the copy rate); beside 64
-// fp32 logits 17 us, 3.6 TB/s.  Between launch and first rows stand three
+// 44 us, 4.7 TB/s of what they have to move (70 % of the copy rate); beside 64
+// fp32 logits 17 us, 3.7 TB/s.  Between launch and first rows stand three
 // dependent reads (plan, order, rows), some 3 us; with the SMs' three CTAs full
 // of stages the rest runs near the copy rate.  fp32 rows take three MMAs for
-// one and a split of every stage: 2000 rows of 60 logits to 1408 columns 11 us.
+// one and a split of every stage: 2000 rows of 60 logits to 1408 columns 12 us.
 #include <cooperative_groups.h>
 
 #include "afd_lora.cuh"
@@ -160,8 +160,8 @@ __device__ __forceinline__ void slow_store(const LoraArgs& a, uint32_t st, const
 }
 
 // WHOLE: all rows can be moved 16 bytes at a time, and no code for others is
-// there (13312 rows of 2048 to 2816 columns 41.6 us, with it 42.8; 7956 rows of
-// 1184 to 1032 columns 18.7 and 21.4; of 1181 to 1031 columns 43).
+// there (with two parts of u, 13312 rows of 2048 to 2816 columns 41.6 us, with
+// that code 42.8; 7956 rows of 1184 to 1032 columns 18.7 and 21.4).
 template <int KC, typename TS, typename TO, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, KC <= 4 ? 3 : 1) k_lora_tiles(const __grid_constant__ LoraArgs a) {
   constexpr int kS = LoraSrc<TS>::kParts, kU = kLoraUParts;
