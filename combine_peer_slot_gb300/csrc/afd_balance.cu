@@ -14,10 +14,10 @@
 //
 // Measured: 13312 rows of 64 experts, 4 sequences: counts and loss 5 and 4 us
 // (sums; their finish, which begins as the sums end), gradient 5.4; of 256 experts
-// 8, 6 and 10, with the chosen weights' gradient 14, where the bytes would take 2, 4 and 4.  Bound by
-// instructions and the latency of a row's exchanges: some 500 a row of 256 (an
-// exponential, a quotient and the products of each expert), at half the issue
-// rate with 24 warps an SM.
+// 8, 6 and 10, with the chosen weights' gradient 14, where the bytes would take 2,
+// 4 and 4.  Bound by instructions and the latency of a row's exchanges: some 500 a
+// row of 256 (an exponential, a quotient and the products of each expert), at half
+// the issue rate with 24 warps an SM.
 #include <cooperative_groups.h>
 
 #include "afd_internal.cuh"
